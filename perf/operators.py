@@ -282,7 +282,8 @@ def _plain_append(s):
         amax.scatter_reduce_(0, block[:, None].expand(-1, x.shape[1]), x.abs().amax(-1), "amax")
         want = _power_scale(amax)
         before = scale[first]                                                 # [seqs, hkv]
-        grown = torch.where((held > 0)[:, None], torch.maximum(before, want[first]), want[first])
+        more = torch.where(amax[first] > 0, torch.maximum(before, want[first]), before)
+        grown = torch.where((held > 0)[:, None], more, want[first])
         scale[block] = want[block]
         scale[first] = grown
         there = codes[first].view(torch.float8_e4m3fn).float() * (before / grown)[:, :, None, None]
@@ -430,7 +431,8 @@ def _exact_append(s, case):
             x = x.view(hkv, b1 - b0, BLOCK, d).transpose(0, 1)
             want = _scale_of(x)
             if lo:
-                want[0] = torch.maximum(want[0], scale[ids[0]])
+                old = scale[ids[0]]
+                want[0] = torch.where((x[0] != 0).any((-1, -2)), torch.maximum(want[0], old), old)
             y = _round(x / want[:, :, None, None])
             z = codes[ids].clone()
             if lo:
