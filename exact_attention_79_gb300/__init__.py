@@ -8,6 +8,7 @@ the device is not sm_103, the calls raise.
 """
 import ctypes
 import os
+from typing import NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfa_gb300.so")
@@ -47,6 +48,10 @@ SIGNATURES = {
     "fa_fp8_quantize_v": (_I, [_VP, _VP, _VP, _I, _I, _I, _VP]),
     "fa_fwd_fp8": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _F, _VP]),
     "fa_fwd_fp8_kv": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _I, _F, _VP]),
+    "fa_cache8_append": (_I, [_VP, _LL, _LL, _VP, _LL, _LL, _VP, _VP, _I, _I, _VP, _VP, _I, _VP]),
+    "fa_fwd_cache8_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "fa_fwd_cache8": (_I, [_VP, _VP, _VP, _I, _VP, _VP, _VP, _VP, _SZ, _I, _I, _I, _I, _F, _I, _F, _VP]),
+    "fa_cache8_evict": (_I, [_VP, _VP, _I, _VP, _I, _I, _I, _VP, _I, _VP, _VP, _VP]),
     "fa_ex2_throughput": (_I, [ctypes.POINTER(ctypes.c_double), _VP]),
     "fa_sm_clock_mhz": (_I, [ctypes.POINTER(ctypes.c_double), _VP]),
     "fa_device_status": (_I, [_VP]),
@@ -287,6 +292,165 @@ def bwd(q, k, v, o, lse, do, causal=False, scale=None, workspace=None, dq=None, 
                                     _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(),
                                     B, Hq, Hkv, N, d, int(bool(causal)), float(scale), _stream(q)))
     return dq, dk, dv
+
+
+CACHE8_BLOCK = 64       # tokens per cache block (FA_CACHE8_BLOCK)
+
+
+class Cache8(NamedTuple):
+    """An 8-bit cache of keys and values (fa_cache8): a pool of blocks of 64 tokens, shared by sequences whose block
+    tables (int32 [B, max_blocks]) say which blocks they have. k, v: uint8 e4m3 codes [num_blocks, Hkv, 64, d];
+    k_scale, v_scale: fp32 [num_blocks, Hkv]; weight: fp32 [num_blocks, Hkv, 64] accumulated attention weight, or
+    None. Contiguous CUDA tensors on one device; nothing else is kept."""
+    k: "torch.Tensor"           # noqa: F821
+    v: "torch.Tensor"           # noqa: F821
+    k_scale: "torch.Tensor"     # noqa: F821
+    v_scale: "torch.Tensor"     # noqa: F821
+    weight: "torch.Tensor" = None   # noqa: F821
+
+
+class _Cache8(ctypes.Structure):
+    _fields_ = [("k", _VP), ("v", _VP), ("k_scale", _VP), ("v_scale", _VP), ("weight", _VP),
+                ("num_blocks", _I), ("Hkv", _I), ("d", _I)]
+
+
+def new_cache8(num_blocks, Hkv, d, device="cuda", weight=False):
+    """An empty Cache8 on `device`, with accumulated weights or without."""
+    import torch
+    codes = [torch.zeros(num_blocks, Hkv, CACHE8_BLOCK, d, dtype=torch.uint8, device=device) for _ in range(2)]
+    scales = [torch.ones(num_blocks, Hkv, dtype=torch.float32, device=device) for _ in range(2)]
+    w = torch.zeros(num_blocks, Hkv, CACHE8_BLOCK, dtype=torch.float32, device=device) if weight else None
+    return Cache8(*codes, *scales, w)
+
+
+def _cache8_specs(cache):
+    """The cache's tensors as _require takes them, its C form and (num_blocks, Hkv, d)."""
+    import torch
+    if cache.k.dim() != 4 or cache.k.shape[2] != CACHE8_BLOCK:
+        raise ValueError(f"cache.k must be [num_blocks, Hkv, {CACHE8_BLOCK}, d]")
+    nb, Hkv, _, d = cache.k.shape
+    f32, u8 = torch.float32, torch.uint8
+    specs = [(cache.k, "cache.k", u8, (nb, Hkv, CACHE8_BLOCK, d)), (cache.v, "cache.v", u8, (nb, Hkv, CACHE8_BLOCK, d)),
+             (cache.k_scale, "cache.k_scale", f32, (nb, Hkv)), (cache.v_scale, "cache.v_scale", f32, (nb, Hkv))]
+    if cache.weight is not None:
+        specs.append((cache.weight, "cache.weight", f32, (nb, Hkv, CACHE8_BLOCK)))
+    c = _Cache8(cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(),
+                cache.weight.data_ptr() if cache.weight is not None else None, nb, Hkv, d)
+    return specs, c, (nb, Hkv, d)
+
+
+def _table_spec(block_table, name="block_table", B=None):
+    import torch
+    if block_table.dim() != 2 or (B is not None and block_table.shape[0] != B):
+        raise ValueError(f"{name} must be [B, max_blocks]")
+    return block_table, name, torch.int32, tuple(block_table.shape)
+
+
+def _call_on(device, name, *args):
+    """A library call on `device`'s current stream, with that device current."""
+    import torch
+    fn = getattr(load(), name)
+    stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    if device.index == torch.cuda.current_device():
+        code = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, stream)
+    _check(name, code)
+
+
+def _heads_strides(t, name, H, T, d):
+    """Strides (between heads, between tokens) of a bf16 [H, T, d] tensor whose rows of d values are contiguous
+    and 16-byte aligned: [H, T, d] itself, or [T, H, d].transpose(0, 1). A dimension of size 1 gets a stride that
+    nothing reads through."""
+    import torch
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != (H, T, d):
+        raise ValueError(f"{name}: expected {torch.bfloat16} of shape {(H, T, d)}, got {t.dtype} of shape {tuple(t.shape)}")
+    sh, st, sd = t.stride()
+    sh, st = (sh if H > 1 else d), (st if T > 1 else d)
+    if (sd != 1 and d > 1) or sh % 8 or st % 8:
+        raise ValueError(f"{name}: the last dimension must be contiguous and the other strides multiples of 8")
+    return sh, st
+
+
+def _placed(device, *named):
+    for t, name in named:
+        if not t.is_cuda or t.device != device:
+            raise ValueError(f"{name} must be a CUDA tensor on {device}")
+
+
+def cache8_append(cache, k, v, cu_seqlens, block_table, start):
+    """Append tokens to the sequences of an 8-bit cache (fa_cache8_append), in place on the current stream.
+
+    k, v: bf16 [Hkv, T, d] (strided: [T, Hkv, d].transpose(0, 1) as well), the new tokens of all sequences one behind
+    the other; sequence b's are cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32 [B + 1]) and become its positions from
+    start[b] (int32 [B]) on. One token each: cu_seqlens = 0, 1, ..., B."""
+    import torch
+    specs, c, (_, Hkv, d) = _cache8_specs(cache)
+    if k.dim() != 3:
+        raise ValueError("k must be [Hkv, T, d]")
+    T, dev = k.shape[1], k.device
+    B = block_table.shape[0]
+    i32 = torch.int32
+    ks, vs = _heads_strides(k, "k", Hkv, T, d), _heads_strides(v, "v", Hkv, T, d)
+    _require(dev, *specs, (cu_seqlens, "cu_seqlens", i32, (B + 1,)), _table_spec(block_table), (start, "start", i32, (B,)))
+    _placed(dev, (k, "k"), (v, "v"))
+    if T == 0:
+        return
+    _call_on(dev, "fa_cache8_append", _ptr(k), *ks, _ptr(v), *vs, _ptr(cu_seqlens), _ptr(start), B, T, ctypes.byref(c),
+             _ptr(block_table), block_table.shape[1])
+
+
+def fwd_cache8(q, cache, block_table, lengths, causal=True, scale=None, out=None, lse=None, workspace=None,
+               weight_decay=None):
+    """O, LSE of the last Nq positions of each sequence over an 8-bit cache (fa_fwd_cache8), on the current stream.
+
+    q: bf16 [B, Hq, Nq, d]; lengths: int32 [B], tokens held with the Nq new ones among them; (Hq / Hkv) * Nq <= 128.
+    weight_decay (a number): cache.weight = weight_decay * cache.weight + each token's summed probabilities as well.
+    Returns (o like q, lse fp32 [B, Hq, Nq])."""
+    import torch
+    lib = load()
+    if q.dim() != 4:
+        raise ValueError("q must be [B, Hq, Nq, d]")
+    specs, c, (_, Hkv, d) = _cache8_specs(cache)
+    B, Hq, Nq, _ = q.shape
+    dev, bf16 = q.device, torch.bfloat16
+    if weight_decay is not None and cache.weight is None:
+        raise ValueError("weight_decay needs a cache with weights")
+    if scale is None:
+        scale = d ** -0.5
+    o = torch.empty((B, Hq, Nq, d), dtype=bf16, device=dev) if out is None else out
+    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev) if lse is None else lse
+    table = _table_spec(block_table, B=B)
+    if workspace is None:
+        n = lib.fa_fwd_cache8_workspace_bytes(B, Hq, Hkv, Nq, d, block_table.shape[1])
+        workspace = torch.empty(int(n), dtype=torch.uint8, device=dev)
+    _require(dev, (q, "q", bf16, (B, Hq, Nq, d)), *specs, table, (lengths, "lengths", torch.int32, (B,)),
+             (o, "out", bf16, (B, Hq, Nq, d)), (lse, "lse", torch.float32, (B, Hq, Nq)),
+             (workspace, "workspace", torch.uint8, (workspace.numel(),)))
+    _call_on(dev, "fa_fwd_cache8", _ptr(q), ctypes.byref(c), _ptr(block_table), block_table.shape[1], _ptr(lengths),
+             _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel(), B, Hq, Nq, int(bool(causal)), float(scale),
+             int(weight_decay is not None), float(weight_decay or 0.0))
+    return o, lse
+
+
+def cache8_evict(cache, block_table, lengths, keep, recent, to_table, new_lengths=None, kept=None):
+    """Cut sequences of an 8-bit cache to at most `keep` tokens per KV head (fa_cache8_evict), on the current stream:
+    the last `recent` and, of the others, those with the largest accumulated weight. They go, in their order, to the
+    blocks of to_table (int32 [B, to_blocks], 64 * to_blocks >= keep), none of which the sequences may hold already.
+    Returns (new_lengths int32 [B], kept int32 [B, Hkv, keep]: positions before, -1 past the new length)."""
+    import torch
+    specs, c, (_, Hkv, d) = _cache8_specs(cache)
+    if cache.weight is None:
+        raise ValueError("eviction needs a cache with weights")
+    B, dev, i32 = block_table.shape[0], cache.k.device, torch.int32
+    new_lengths = torch.empty(B, dtype=i32, device=dev) if new_lengths is None else new_lengths
+    kept = torch.empty((B, Hkv, keep), dtype=i32, device=dev) if kept is None else kept
+    _require(dev, *specs, _table_spec(block_table), _table_spec(to_table, "to_table", B), (lengths, "lengths", i32, (B,)),
+             (new_lengths, "new_lengths", i32, (B,)), (kept, "kept", i32, (B, Hkv, keep)))
+    _call_on(dev, "fa_cache8_evict", ctypes.byref(c), _ptr(block_table), block_table.shape[1], _ptr(lengths), B, keep,
+             recent, _ptr(to_table), to_table.shape[1], _ptr(kept), _ptr(new_lengths))
+    return new_lengths, kept
 
 
 def ex2_throughput(stream=None):

@@ -592,6 +592,144 @@ fa_status fa_fwd_fp8_kv(const void* q, const float* q_scale, const void* k, cons
   return fwd_fp8_common(q, q_scale, k, k_scale, vt, v_scale, o, lse, B, Hq, Hkv, Nq, Nk, d, causal, scale, stream);
 }
 
+}  // extern "C"
+
+namespace {
+// The cache's own rules, and its arrays as the kernels take them.
+fa_status cache8_pools(const fa_cache8* c, int B, int max_blocks, const void* block_table, bool need_weight,
+                       fa::Cache8Pools* out) {
+  if (!c || !block_table) return FA_ERR_INVALID_ARG;
+  const void* ptrs[] = {c->k, c->v, c->k_scale, c->v_scale};
+  for (const void* ptr : ptrs)
+    if (!ptr || !aligned16(ptr)) return FA_ERR_INVALID_ARG;
+  if (!aligned16(c->weight) || (need_weight && !c->weight)) return FA_ERR_INVALID_ARG;
+  if (c->num_blocks < 1 || c->Hkv < 1 || c->Hkv > 65535 || c->d < 1 || B < 1 || B > 65535 || max_blocks < 1 ||
+      max_blocks > (1 << 24))
+    return FA_ERR_INVALID_ARG;
+  if (!fp8_dim(c->d)) return FA_ERR_UNSUPPORTED;
+  *out = fa::Cache8Pools{c->k, c->v, c->k_scale, c->v_scale, c->weight, c->num_blocks, c->Hkv, c->d};
+  return FA_OK;
+}
+
+// Bytes of the partial results of fa_fwd_cache8; off_s: where the statistics start.
+size_t cache8_workspace(int parts, int cols, int d, size_t* off_s) {
+  const size_t D = d <= 64 ? 64 : d <= 128 ? 128 : 256;
+  const size_t rows = 2 * static_cast<size_t>(parts) * cols;
+  *off_s = align256(rows * D * 4);
+  return *off_s + align256(rows * 3 * 4);
+}
+
+fa_status cache8_rows(int B, int Hq, int Hkv, int Nq, int d, int max_blocks) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Nq < 1 || Hq % Hkv != 0 || d < 1 || max_blocks < 1) return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(Hq / Hkv) * Nq > fa::kCache8MaxRows || !fp8_dim(d)) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+}  // namespace
+
+extern "C" {
+
+fa_status fa_cache8_append(const void* k, long long k_stride_h, long long k_stride_t, const void* v,
+                           long long v_stride_h, long long v_stride_t, const int* cu_seqlens, const int* start, int B,
+                           int T, const fa_cache8* cache, const int* block_table, int max_blocks, void* stream) {
+  if (!k || !v || !cu_seqlens || !start || !aligned16(k) || !aligned16(v)) return FA_ERR_INVALID_ARG;
+  const long long strides[] = {k_stride_h, k_stride_t, v_stride_h, v_stride_t};
+  for (long long s : strides)
+    if (s < 0 || s % 8 != 0) return FA_ERR_INVALID_ARG;
+  if (T < 1) return FA_ERR_INVALID_ARG;
+  fa::Cache8AppendParams p{};
+  fa_status st = cache8_pools(cache, B, max_blocks, block_table, false, &p.c);
+  if (st != FA_OK) return st;
+  unsigned* status = nullptr;
+  st = device_state(stream, &status);
+  if (st != FA_OK) return st;
+  p.k = k;
+  p.v = v;
+  p.k_sh = k_stride_h;
+  p.k_st = k_stride_t;
+  p.v_sh = v_stride_h;
+  p.v_st = v_stride_t;
+  p.cu = cu_seqlens;
+  p.start = start;
+  p.table = block_table;
+  p.B = B;
+  p.T = T;
+  p.max_blocks = max_blocks;
+  return fa::launch_cache8_append(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_fwd_cache8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int max_blocks) {
+  if (cache8_rows(B, Hq, Hkv, Nq, d, max_blocks) != FA_OK) return 0;
+  const int R = Hq / Hkv * Nq, cols = fa::cache8_columns(d, R);
+  size_t off_s;
+  return cache8_workspace(fa::cache8_parts(B, Hkv, (R + cols - 1) / cols, max_blocks), cols, d, &off_s);
+}
+
+fa_status fa_fwd_cache8(const void* q, const fa_cache8* cache, const int* block_table, int max_blocks,
+                        const int* lengths, void* o, float* lse, void* workspace, size_t workspace_bytes, int B, int Hq,
+                        int Nq, int causal, float scale, int add_weights, float weight_decay, void* stream) {
+  if (!q || !o || !lse || !lengths || !aligned16(q) || !aligned16(o) || !aligned16(lse)) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
+  if (add_weights && (!std::isfinite(weight_decay) || !(weight_decay >= 0.f))) return FA_ERR_INVALID_ARG;
+  fa::Cache8Params p{};
+  fa_status st = cache8_pools(cache, B, max_blocks, block_table, add_weights != 0, &p.c);
+  if (st == FA_OK) st = cache8_rows(B, Hq, p.c.Hkv, Nq, p.c.d, max_blocks);
+  if (st != FA_OK) return st;
+  p.G = Hq / p.c.Hkv;
+  p.R = p.G * Nq;
+  const int cols = fa::cache8_columns(p.c.d, p.R);
+  p.chunks = (p.R + cols - 1) / cols;
+  size_t off_s;
+  const size_t need = cache8_workspace(fa::cache8_parts(B, p.c.Hkv, p.chunks, max_blocks), cols, p.c.d, &off_s);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < need)
+    return FA_ERR_WORKSPACE;
+  unsigned* status = nullptr;
+  st = device_state(stream, &status);
+  if (st != FA_OK) return st;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.table = block_table;
+  p.lengths = lengths;
+  p.B = B;
+  p.max_blocks = max_blocks;
+  p.Hq = Hq;
+  p.Nq = Nq;
+  p.causal = causal ? 1 : 0;
+  p.add_weights = add_weights ? 1 : 0;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.decay = weight_decay;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_s = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + off_s);
+  return fa::launch_cache8_fwd(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_cache8_evict(const fa_cache8* cache, const int* block_table, int max_blocks, const int* lengths, int B,
+                          int keep, int recent, const int* to_table, int to_blocks, int* kept, int* new_lengths,
+                          void* stream) {
+  if (!lengths || !to_table || !kept || !new_lengths) return FA_ERR_INVALID_ARG;
+  if (keep < 1 || recent < 0 || recent > keep || to_blocks < 1 ||
+      static_cast<long long>(to_blocks) * FA_CACHE8_BLOCK < keep)
+    return FA_ERR_INVALID_ARG;
+  fa::Cache8EvictParams p{};
+  fa_status st = cache8_pools(cache, B, max_blocks, block_table, true, &p.c);
+  if (st != FA_OK) return st;
+  if (static_cast<long long>(B) * to_blocks >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
+  unsigned* status = nullptr;
+  st = device_state(stream, &status);
+  if (st != FA_OK) return st;
+  p.table = block_table;
+  p.lengths = lengths;
+  p.to_table = to_table;
+  p.kept = kept;
+  p.new_lengths = new_lengths;
+  p.B = B;
+  p.max_blocks = max_blocks;
+  p.to_blocks = to_blocks;
+  p.keep = keep;
+  p.recent = recent;
+  return fa::launch_cache8_evict(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 fa_status fa_ex2_throughput(double* per_sm_per_cycle, void* stream) {
   if (!per_sm_per_cycle) return FA_ERR_INVALID_ARG;
   unsigned* status = nullptr;

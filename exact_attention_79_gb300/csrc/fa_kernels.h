@@ -3,6 +3,7 @@
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <cuda_bf16.h>
 
 namespace fa {
 
@@ -120,5 +121,57 @@ cudaError_t launch_bwd_wide(const BwdMaps& m, const BwdMaps& m64, const BwdParam
 // Deterministic backward after launch_bwd_pre: the dK/dV pass and the dQ pass
 // (two launches on `stream`); reads only the LSE and D parts of the workspace.
 cudaError_t launch_bwd_deterministic(int d, const BwdMaps& m, const BwdParams& p, cudaStream_t stream);
+
+// ---- the 8-bit block cache (fa_cache8*.cu): pools of blocks of 64 tokens, codes
+// [num_blocks, Hkv, 64, d], scales [num_blocks, Hkv], weights [num_blocks, Hkv, 64]
+struct Cache8Pools {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  float* weight;                   // may be null where it is not needed
+  int num_blocks, Hkv, d;
+};
+struct Cache8AppendParams {
+  Cache8Pools c;
+  const void* k;                   // bf16 new tokens, [Hkv, T, d] with strides in elements
+  const void* v;
+  long long k_sh, k_st, v_sh, v_st;
+  const int* cu;                   // [B + 1] where each sequence's new tokens begin
+  const int* start;                // [B] tokens held before
+  const int* table;                // [B, max_blocks]
+  int B, T, max_blocks;
+};
+struct Cache8Params {
+  Cache8Pools c;
+  const __nv_bfloat16* q;          // [B, Hq, Nq, d]
+  __nv_bfloat16* o;
+  float* lse;                      // [B, Hq, Nq]
+  const int* table;
+  const int* lengths;              // [B]
+  int B, max_blocks, Hq, Nq;
+  int G, R;                        // query heads per KV head; rows of a KV head's group, G * Nq
+  int chunks;                      // row chunks of cache8_columns() rows
+  int causal, add_weights;
+  float scale_log2, decay;
+  float* part_o;                   // partial results: [2 parts][columns][D] and [2 parts][columns][3]
+  float* part_s;
+};
+struct Cache8EvictParams {
+  Cache8Pools c;
+  const int* table;
+  const int* lengths;
+  const int* to_table;             // [B, to_blocks]
+  int* kept;                       // [B, Hkv, keep]
+  int* new_lengths;                // [B]
+  int B, max_blocks, to_blocks, keep, recent;
+};
+constexpr int kCache8MaxRows = 128;   // G * Nq of one call
+constexpr int kCache8Parts = 304;     // CTAs of the attention: parts the work is cut into at most
+int cache8_columns(int d, int R);     // query rows a CTA takes at once
+int cache8_parts(int B, int Hkv, int chunks, int max_blocks);
+cudaError_t launch_cache8_append(const Cache8AppendParams& p, cudaStream_t stream);
+cudaError_t launch_cache8_fwd(const Cache8Params& p, cudaStream_t stream);
+cudaError_t launch_cache8_evict(const Cache8EvictParams& p, cudaStream_t stream);
 
 }  // namespace fa

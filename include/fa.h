@@ -287,6 +287,95 @@ fa_status fa_bwd_noalloc(const void* q, const void* k, const void* v, const void
                          const void* dO, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int N, int d,
                          int causal, float scale, void* stream);
 
+/* ---- Serving: an 8-bit cache of keys and values.
+ *
+ * fa_cache8: a pool of blocks of FA_CACHE8_BLOCK = 64 tokens. Block p, KV head
+ * h, slot s holds one token's K and V as e4m3 codes (the format of fa_fwd_fp8)
+ * with one fp32 scale per block and KV head each; a value is code * scale.
+ * All five arrays are dense device memory, 16-byte aligned, owned by the
+ * caller, who also decides which blocks a sequence has: block_table
+ * [B, max_blocks] int32 (device), entry j the block with the sequence's tokens
+ * 64 j .. 64 j + 63. Blocks may be shared by sequences that only read them. A
+ * table entry outside [0, num_blocks) is never followed: tokens that would lie
+ * there are not written, and are absent to whoever reads.
+ *   k, v     codes [num_blocks, Hkv, 64, d]
+ *   k_scale, v_scale  fp32 [num_blocks, Hkv], finite and >= 0
+ *   weight   fp32 [num_blocks, Hkv, 64], accumulated attention weight, or NULL
+ *            in a cache that keeps none
+ * d a multiple of 16 from 16 to 256, Hkv 1 to 65535, num_blocks >= 1,
+ * max_blocks 1 to 2^24, B 1 to 65535. Contents of unused slots and blocks are
+ * never looked at (they may hold anything). Streams, graphs, errors and devices
+ * as for the other calls; FA_ERR_UNSUPPORTED for another d.
+ * Source: block-wise scales from the largest magnitude ("Flash Attention
+ * V3技术解析", section 3.2); the cache itself has no counterpart on the pages. */
+#define FA_CACHE8_BLOCK 64
+typedef struct {
+  unsigned char* k;
+  unsigned char* v;
+  float* k_scale;
+  float* v_scale;
+  float* weight;
+  int num_blocks;
+  int Hkv;
+  int d;
+} fa_cache8;
+
+/* Append bf16 tokens of B sequences. k, v: [Hkv, T, d] with strides (in
+ * elements, multiples of 8) between heads and tokens and the d values of a
+ * token contiguous, so a [T, Hkv, d] projection needs no copy. Tokens
+ * cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (device int32 [B + 1], not
+ * decreasing, within 0 .. T) become positions start[b], start[b] + 1, ...
+ * (device int32 [B]) of sequence b; a sequence may get none. A block's scale is
+ * the smallest power of two s >= 2^-126 with max|x| <= 448 s (1 for zeros);
+ * code = e4m3(x / s), to nearest even. A block that held tokens keeps its scale
+ * unless a new one needs a larger, and then the codes there are multiplied by
+ * old / new and rounded again (only codes that become subnormal change value).
+ * Slots behind the last new token are left as they were. New tokens' weights
+ * become 0. An infinity is held at 448 s and takes no part in s; a NaN stays.
+ * Positions behind the table's end are not written. One call must not name a
+ * block twice among the blocks it writes. T >= 1. */
+fa_status fa_cache8_append(const void* k, long long k_stride_h, long long k_stride_t, const void* v,
+                           long long v_stride_h, long long v_stride_t, const int* cu_seqlens, const int* start,
+                           int B, int T, const fa_cache8* cache, const int* block_table, int max_blocks,
+                           void* stream);
+
+/* Attention over the cache for the last Nq positions of each sequence: q, o
+ * bf16 [B, Hq, Nq, d], lse fp32 [B, Hq, Nq], lengths int32 [B] (device): tokens
+ * held, the Nq new ones included (taken within 0 .. 64 max_blocks). As
+ * fa_fwd_kv on the values of the cache: key j is visible to query i iff
+ * j < lengths[b] and, when causal, j <= i + lengths[b] - Nq; a row that sees
+ * none gets O = 0, lse = -inf. Hq % Hkv == 0 and (Hq / Hkv) * Nq <= 128
+ * (FA_ERR_UNSUPPORTED above). The products take the codes as they are, Q to
+ * the bit (within 2^-39 of a row's largest value) and P rounded to 11 bits;
+ * sums are fp32. A NaN among a sequence's V values reaches every query of the
+ * call on that sequence and head.
+ * add_weights: also weight_j = weight_decay * weight_j + sum of the
+ * probabilities of key j over the Hq / Hkv heads and Nq queries, for every
+ * key j < lengths[b] (weight_decay finite, >= 0; 0 overwrites). It needs
+ * cache->weight, and no two sequences of the call may then share a block.
+ * workspace: fa_fwd_cache8_workspace_bytes(B, Hq, Hkv, Nq, d, max_blocks)
+ * bytes, 256-byte aligned, contents before and after of no meaning; calls
+ * that may overlap on the GPU need one each. */
+size_t fa_fwd_cache8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int max_blocks);
+fa_status fa_fwd_cache8(const void* q, const fa_cache8* cache, const int* block_table, int max_blocks,
+                        const int* lengths, void* o, float* lse, void* workspace, size_t workspace_bytes, int B,
+                        int Hq, int Nq, int causal, float scale, int add_weights, float weight_decay, void* stream);
+
+/* Evict: of each sequence's tokens, per KV head, keep at most `keep`: the last
+ * `recent` (0 <= recent <= keep) and of the others those with the largest
+ * weight (a NaN counts as the largest; ties go to the earlier token), in their
+ * order. Their codes go to the blocks of to_table [B, to_blocks] (device
+ * int32, 64 * to_blocks >= keep), with scales from their own values as
+ * fa_cache8_append takes them, and their weights with them; slots behind them
+ * are left as they were. kept int32 [B, Hkv, keep]: the tokens' positions
+ * before, -1 past the sequence's new length; new_lengths int32 [B]:
+ * min(lengths, keep). Heads keep different tokens but equally many. A block of
+ * to_table must be neither a source of this call nor named twice in it; the
+ * sources are left as they were. keep >= 1; cache->weight is needed. */
+fa_status fa_cache8_evict(const fa_cache8* cache, const int* block_table, int max_blocks, const int* lengths, int B,
+                          int keep, int recent, const int* to_table, int to_blocks, int* kept, int* new_lengths,
+                          void* stream);
+
 /* Synchronises `stream`, then returns and clears the status word of that
  * stream: FA_OK, FA_ERR_TIMEOUT (a bounded wait inside a kernel ran out; that
  * call's outputs are invalid), FA_ERR_DEVICE (a kernel found the device's
