@@ -48,6 +48,8 @@ SIGNATURES = {
     "fa_fp8_quantize_v": (_I, [_VP, _VP, _VP, _I, _I, _I, _VP]),
     "fa_fwd_fp8": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _F, _VP]),
     "fa_fwd_fp8_kv": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _I, _F, _VP]),
+    "fa_fwd_packed": (_I, [_VP, _LL, _LL, _VP, _LL, _LL, _VP, _LL, _LL, _VP, _LL, _LL, _VP, _VP,
+                           _I, _I, _I, _I, _I, _I, _F, _VP]),
     "fa_cache8_append": (_I, [_VP, _LL, _LL, _VP, _LL, _LL, _VP, _VP, _I, _I, _VP, _VP, _I, _VP]),
     "fa_fwd_cache8_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "fa_fwd_cache8": (_I, [_VP, _VP, _VP, _I, _VP, _VP, _VP, _VP, _SZ, _I, _I, _I, _I, _F, _I, _F, _VP]),
@@ -377,6 +379,35 @@ def _placed(device, *named):
     for t, name in named:
         if not t.is_cuda or t.device != device:
             raise ValueError(f"{name} must be a CUDA tensor on {device}")
+
+
+def fwd_packed(q, k, v, cu_seqlens, causal=True, scale=None, out=None, lse=None):
+    """O, LSE of S packed sequences of different lengths, each attending to itself (fa_fwd_packed), on the current
+    stream.
+
+    q: bf16 [Hq, T, d]; k, v: [Hkv, T, d]; each [H, T, d] or a [T, H, d] tensor's .transpose(0, 1). cu_seqlens: int32
+    [S + 1] on the device; sequence s has rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1. Returns (o with q's layout, lse
+    fp32 [Hq, T]); rows of no sequence are left as they were (unset in new tensors)."""
+    import torch
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be 3-D: [H, T, d]")
+    Hq, T, d = q.shape
+    Hkv, dev = k.shape[0], q.device
+    if scale is None:
+        scale = d ** -0.5
+    o = torch.empty_like(q) if out is None else out
+    lse = torch.empty((Hq, T), dtype=torch.float32, device=dev) if lse is None else lse
+    strides = [(t, _heads_strides(t, n, H, T, d)) for t, n, H in ((q, "q", Hq), (k, "k", Hkv), (v, "v", Hkv), (o, "out", Hq))]
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must be [S + 1]")
+    S = cu_seqlens.shape[0] - 1
+    _require(dev, (cu_seqlens, "cu_seqlens", torch.int32, (S + 1,)), (lse, "lse", torch.float32, (Hq, T)))
+    _placed(dev, (k, "k"), (v, "v"), (o, "out"))
+    if T == 0 or S == 0:
+        return o, lse
+    args = [x for t, (sh, st) in strides for x in (_ptr(t), sh, st)]
+    _call_on(dev, "fa_fwd_packed", *args, _ptr(lse), _ptr(cu_seqlens), S, T, Hq, Hkv, d, int(bool(causal)), float(scale))
+    return o, lse
 
 
 def cache8_append(cache, k, v, cu_seqlens, block_table, start):

@@ -120,15 +120,15 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // read as zeros and never stored.
 bool fp8_dim(int d) { return d >= 16 && d <= 256 && d % 16 == 0; }
 
-// 3-D map over a dense [BH, N, d] tensor: dims (d, N, BH), one box = 128 rows
-// by 128 bytes with 128-byte swizzle. Rows past N read as zero and are not
-// written by stores.
-bool make_map(CUtensorMap* m, const void* ptr, int elt_bytes, int d, int N, long long BH, int box_rows = 128) {
+// 3-D map over a [BH, N, d] tensor: dims (d, N, BH), one box = 128 rows by 128
+// bytes with 128-byte swizzle. Rows past N read as zero and are not written by
+// stores. row, head: distances between rows and between heads in elements.
+bool make_map_strided(CUtensorMap* m, const void* ptr, int elt_bytes, int d, int N, long long BH, long long row,
+                      long long head, int box_rows) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(BH)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * elt_bytes,
-                                 static_cast<cuuint64_t>(d) * N * elt_bytes};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row) * elt_bytes, static_cast<cuuint64_t>(head) * elt_bytes};
   const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / elt_bytes), static_cast<cuuint32_t>(box_rows), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUtensorMapDataType dt = elt_bytes == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
@@ -139,6 +139,11 @@ bool make_map(CUtensorMap* m, const void* ptr, int elt_bytes, int d, int N, long
                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+// The same over a dense tensor.
+bool make_map(CUtensorMap* m, const void* ptr, int elt_bytes, int d, int N, long long BH, int box_rows = 128) {
+  return make_map_strided(m, ptr, elt_bytes, d, N, BH, d, static_cast<long long>(d) * N, box_rows);
 }
 
 fa_status check_sizes(int B, int Hq, int Hkv, int N, int d, float scale) {
@@ -485,6 +490,54 @@ fa_status fa_fwd_kv(const void* q, const void* k, const void* v, void* o, float*
                     int Nk, int d, int causal, float scale, void* stream) {
   if (Nk < 1) return FA_ERR_INVALID_ARG;
   return fwd_common(2, q, k, v, o, lse, B, Hq, Hkv, Nq, d, causal, scale, stream, nullptr, 0, 0, Nk);
+}
+
+fa_status fa_fwd_packed(const void* q, long long q_stride_h, long long q_stride_t, const void* k, long long k_stride_h,
+                        long long k_stride_t, const void* v, long long v_stride_h, long long v_stride_t, void* o,
+                        long long o_stride_h, long long o_stride_t, float* lse, const int* cu_seqlens, int S, int T,
+                        int Hq, int Hkv, int d, int causal, float scale, void* stream) {
+  if (!q || !k || !v || !o || !lse || !cu_seqlens) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse)) return FA_ERR_INVALID_ARG;
+  fa_status st = check_sizes(1, Hq, Hkv, T, d, scale);
+  if (st != FA_OK) return st;
+  if (S < 1) return FA_ERR_INVALID_ARG;
+  // rows and heads apart (no broadcast), 16-byte rows, within a tensor map's strides
+  const long long strides[] = {q_stride_h, q_stride_t, k_stride_h, k_stride_t,
+                               v_stride_h, v_stride_t, o_stride_h, o_stride_t};
+  for (long long s : strides)
+    if (s < d || s % 8 != 0 || s >= (1LL << 39)) return FA_ERR_INVALID_ARG;
+  if (d > 128) return FA_ERR_UNSUPPORTED;
+  if ((T + 255LL * S) / 256 * Hq >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
+  unsigned* status = nullptr;
+  unsigned long long* clock_acc = nullptr;
+  st = device_state(stream, &status, nullptr, &clock_acc);
+  if (st != FA_OK) return st;
+  CUtensorMap mq, mk, mv, mo;
+  if (!make_map_strided(&mq, q, 2, d, T, Hq, q_stride_t, q_stride_h, 128) ||
+      !make_map_strided(&mk, k, 2, d, T, Hkv, k_stride_t, k_stride_h, 128) ||
+      !make_map_strided(&mv, v, 2, d, T, Hkv, v_stride_t, v_stride_h, 128) ||
+      !make_map_strided(&mo, o, 2, d, T, Hq, o_stride_t, o_stride_h, 128))
+    return FA_ERR_CUDA;
+  fa::FwdParams p{};
+  p.lse = lse;
+  p.status = status;
+  p.clock_acc = clock_acc;
+  p.N = p.Nk = p.T = T;
+  p.S = S;
+  p.cu = cu_seqlens;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.o_sh = o_stride_h;
+  p.o_st = o_stride_t;
+  p.head_dim = d;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.BH = Hq;
+  p.causal = causal ? 1 : 0;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.timeout_ns = wait_limit_ns();
+  p.test_stall = test_stall();
+  return fa::launch_fwd_packed(d, mq, mk, mv, mo, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK
+                                                                                                        : FA_ERR_CUDA;
 }
 
 fa_status fa_fwd_pair(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv,

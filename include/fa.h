@@ -98,6 +98,24 @@ fa_status fa_fwd(const void* q, const void* k, const void* v, void* o, float* ls
 fa_status fa_fwd_kv(const void* q, const void* k, const void* v, void* o, float* lse,
                     int B, int Hq, int Hkv, int Nq, int Nk, int d, int causal, float scale, void* stream);
 
+/* Forward over packed sequences, bf16: S sequences of different lengths one
+ * behind the other, each attending to itself alone. q, o [Hq, T, d], k, v
+ * [Hkv, T, d] with strides in elements between heads and between rows (multiples
+ * of 8, at least d, so no broadcast; the d values of a row contiguous): a
+ * [T, H, d] projection needs no copy. cu_seqlens: device int32 [S + 1], not
+ * decreasing, within 0 .. T; sequence s has rows cu_seqlens[s] ..
+ * cu_seqlens[s + 1] - 1 and may be empty. lse [Hq, T]. Row i of a sequence sees
+ * its rows j (j <= i when causal) and nothing of the others, whatever they hold.
+ * Rows of no sequence (before the first, behind the last) are left as they
+ * were, in o and in lse. Values outside the rules for cu_seqlens are taken
+ * within 0 .. T, and some rows may then not be written. d <= 128
+ * (FA_ERR_UNSUPPORTED above). One launch; nothing is read on the host. */
+fa_status fa_fwd_packed(const void* q, long long q_stride_h, long long q_stride_t, const void* k,
+                        long long k_stride_h, long long k_stride_t, const void* v, long long v_stride_h,
+                        long long v_stride_t, void* o, long long o_stride_h, long long o_stride_t, float* lse,
+                        const int* cu_seqlens, int S, int T, int Hq, int Hkv, int d, int causal, float scale,
+                        void* stream);
+
 /* fa_fwd_kv computed by clusters of two CTAs whose matrix products run as
  * tcgen05 cta_group::2 pairs (M = 256 over two SMs; each CTA loads half of
  * every K and V tile). Same arguments, layouts, masking and results as
