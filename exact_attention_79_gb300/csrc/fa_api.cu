@@ -507,16 +507,16 @@ fa_status fa_fwd_packed(const void* q, long long q_stride_h, long long q_stride_
   for (long long s : strides)
     if (s < d || s % 8 != 0 || s >= (1LL << 39)) return FA_ERR_INVALID_ARG;
   if (d > 128) return FA_ERR_UNSUPPORTED;
-  if ((T + 255LL * S) / 256 * Hq >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
   unsigned* status = nullptr;
   unsigned long long* clock_acc = nullptr;
-  st = device_state(stream, &status, nullptr, &clock_acc);
+  int num_sms = 0;
+  st = device_state(stream, &status, &num_sms, &clock_acc);
   if (st != FA_OK) return st;
   CUtensorMap mq, mk, mv, mo;
   if (!make_map_strided(&mq, q, 2, d, T, Hq, q_stride_t, q_stride_h, 128) ||
       !make_map_strided(&mk, k, 2, d, T, Hkv, k_stride_t, k_stride_h, 128) ||
       !make_map_strided(&mv, v, 2, d, T, Hkv, v_stride_t, v_stride_h, 128) ||
-      !make_map_strided(&mo, o, 2, d, T, Hq, o_stride_t, o_stride_h, 128))
+      !make_map_strided(&mo, o, 2, d, T, Hq, o_stride_t, o_stride_h, 32))
     return FA_ERR_CUDA;
   fa::FwdParams p{};
   p.lse = lse;
@@ -531,13 +531,12 @@ fa_status fa_fwd_packed(const void* q, long long q_stride_h, long long q_stride_
   p.head_dim = d;
   p.Hq = Hq;
   p.Hkv = Hkv;
-  p.BH = Hq;
   p.causal = causal ? 1 : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.timeout_ns = wait_limit_ns();
   p.test_stall = test_stall();
-  return fa::launch_fwd_packed(d, mq, mk, mv, mo, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK
-                                                                                                        : FA_ERR_CUDA;
+  return fa::launch_fwd_packed(d, mq, mk, mv, mo, p, num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK : FA_ERR_CUDA;
 }
 
 fa_status fa_fwd_pair(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv,

@@ -149,57 +149,7 @@ __device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint3
   }
 }
 
-// Packed sequences: the r-th (sequence, query-tile pair) in the order of the
-// pair's index, largest first (causal: the pairs with the most key tiles
-// first), sequences in their order among equals. C(w) = sum_s max(0, pairs_s - w)
-// counts the pairs of index w or more; the index of the r-th is the largest w
-// with C(w) > r. Every warp looks it up by itself (no work list to build, no
-// second launch); one lane per sequence. False: fewer pairs than r + 1.
-struct PackedItem {
-  int start, len, pair;
-};
-__device__ __forceinline__ void packed_sequence(const FwdParams& p, int s, int& start, int& len) {
-  start = max(0, min(p.cu[s], p.T));
-  len = max(0, min(p.cu[s + 1], p.T) - start);
-}
-__device__ __forceinline__ bool packed_item(const FwdParams& p, int r, int lane, PackedItem& it) {
-  auto pairs = [&](int s) {
-    int start, len;
-    packed_sequence(p, s, start, len);
-    return (len + 2 * kBM - 1) / (2 * kBM);
-  };
-  const int first = lane < p.S ? pairs(lane) : 0;          // the sequence of this lane; more than 32 are read again
-  auto count = [&](int w) {
-    int c = max(0, first - w);
-    for (int s = lane + 32; s < p.S; s += 32) c += max(0, pairs(s) - w);
-    return __reduce_add_sync(0xffffffffu, c);
-  };
-  int top = first;
-  for (int s = lane + 32; s < p.S; s += 32) top = max(top, pairs(s));
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (count(0) <= r) return false;
-  int lo = 0, hi = top;                                    // C(lo) > r >= C(hi)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (count(mid) > r) lo = mid;
-    else hi = mid;
-  }
-  int k = r - count(lo + 1);                               // the k-th sequence with more than lo pairs
-  for (int s0 = 0; s0 < p.S; s0 += 32) {
-    const int np = s0 == 0 ? first : s0 + lane < p.S ? pairs(s0 + lane) : 0;
-    const unsigned hit = __ballot_sync(0xffffffffu, np > lo);
-    if (k < __popc(hit)) {
-      const int s = s0 + static_cast<int>(__fns(hit, 0, k + 1));
-      packed_sequence(p, s, it.start, it.len);
-      it.pair = lo;
-      return true;
-    }
-    k -= __popc(hit);
-  }
-  return false;
-}
-
-template <typename T, int D, bool kSparse, bool kPacked>
+template <typename T, int D, bool kSparse>
 __global__ void __launch_bounds__(FwdCfg<T, D>::kThreads, 1)
 fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
            const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
@@ -232,9 +182,6 @@ fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
   // barriers; entry = tile | (visible to tile 0) << 14 | (visible to tile 1) << 15
   int* const list_count = reinterpret_cast<int*>(gbars + 480);       // [0] all, [1] group 0's prefix
   const uint32_t bar_stall = bars + 472;                             // nothing arrives (timeout test)
-  // packed: the sequence's first row and length, parked here so that the
-  // softmax warps hold no register for what only their epilogue needs
-  volatile int* const parked = reinterpret_cast<volatile int*>(gbars + 488);   // [2]
   unsigned long long* const clock_start = reinterpret_cast<unsigned long long*>(gbars + 456);   // [2]
   static_assert(80 + 16 * C::kStages <= 456, "barrier area");
   uint16_t* const tile_list = reinterpret_cast<uint16_t*>(gbars + C::kBarBytes);
@@ -244,26 +191,18 @@ fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
 
   // ---- work item: (query-tile pair, batch*head), heaviest causal pairs first
   const int lin = blockIdx.x;
-  PackedItem item{0, 0, 0};
-  if constexpr (kPacked) {
-    if (!packed_item(p, lin / p.BH, lane, item)) return;     // the whole CTA: every warp finds the same
-  }
-  const int pair = kPacked ? item.pair : p.num_pairs - 1 - lin / p.BH;
+  const int pair = p.num_pairs - 1 - lin / p.BH;
   const int bh = lin % p.BH;
   const int b = bh / p.Hq, h = bh % p.Hq;
   const int bh_kv = b * p.Hkv + h / (p.Hq / p.Hkv);
-  // query and key positions; packed: the sequence's, whose rows begin at row0
-  const int N = kPacked ? item.len : p.N, Nk = kPacked ? item.len : p.Nk;
-  const int row0 = kPacked ? item.start : 0;
-  const int causal_off = kPacked ? 0 : p.causal_off;
-  const int nq = (N + kBM - 1) / kBM;
-  const int nk = (Nk + kBN - 1) / kBN;
+  const int nq = (p.N + kBM - 1) / kBM;
+  const int nk = (p.Nk + kBN - 1) / kBN;
   const int qt[2] = {C::kTilesPerCta * pair, C::kTilesPerCta * pair + 1};
   // key tiles a query tile reaches: causal, up to the one holding key
   // (last row + Nk - N), none if that is negative
   auto reach = [&](int t) {
     if (!p.causal) return nk;
-    const int last = t * kBM + kBM - 1 + causal_off;
+    const int last = t * kBM + kBM - 1 + p.causal_off;
     return last < 0 ? 0 : min(nk, last / kBN + 1);
   };
   int nkv[2];
@@ -274,10 +213,6 @@ fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
   if (threadIdx.x == 0) {
     clock_mark(clock_start);
     *abort_flag = 0;
-    if constexpr (kPacked) {
-      parked[0] = item.start;
-      parked[1] = item.len;
-    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar_q_full(i), 1);
       mbar_init(bar_s_full(i), 1);
@@ -348,7 +283,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
         if (nkv[i] == 0) continue;
         mbar_arrive_expect_tx(bar_q_full(i), C::kTileBytes);
         for (int bx = 0; bx < C::kNBox; ++bx)
-          tma_load_3d(s_q[i] + bx * kBoxBytes, &map_q, bar_q_full(i), bx * C::kChunk, row0 + qt[i] * kBM, bh);
+          tma_load_3d(s_q[i] + bx * kBoxBytes, &map_q, bar_q_full(i), bx * C::kChunk, qt[i] * kBM, bh);
       }
       for (int c = 0; c < 2 * nmax; ++c) {
         const int slot = c % kSt;
@@ -358,7 +293,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
         const CUtensorMap* m = (c & 1) ? &map_v : &map_k;
         const uint32_t dst = s_kv + slot * C::kTileBytes;
         for (int bx = 0; bx < C::kNBox; ++bx)
-          tma_load_3d(dst + bx * kBoxBytes, m, bar_kv_full(slot), bx * C::kChunk, row0 + kv_tile(c >> 1) * kBN, bh_kv);
+          tma_load_3d(dst + bx * kBoxBytes, m, bar_kv_full(slot), bx * C::kChunk, kv_tile(c >> 1) * kBN, bh_kv);
       }
     }
     __syncwarp();
@@ -436,19 +371,13 @@ fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
   } else if (C::kPingPong && warp >= 10) {
     // ------------------------------------------------------------ ring watcher (bf16; warp 11 idle)
     setmaxnreg_dec<C::kRegsOther>();
-    // packed: the rows of V behind the sequence's end belong to the next one
-    // and may hold anything; P is 0 there, but 0 x inf is not, so the watcher
-    // clears them before it lets the product read the tile (the last of the
-    // sequence, hence of this CTA)
-    const bool ragged = kPacked && nmax == nk && Nk % kBN != 0;
-    bool ok = true;
     if (warp == 10 && lane == 0) {
       // L: the group whose S MMAs are issued last in each step (group 1 unless absent)
       const int L = (nkv[1] == nmax) ? 1 : 0;
       // parity waits only tell phase k from phase k-1: observe every phase of
       // every slot in order, starting with K_0 (load 0), which only the
       // issuer needs
-      ok = nmax == 0 || mbar_wait(bar_kv_full(0), 0, abort_flag, deadline);
+      bool ok = nmax == 0 || mbar_wait(bar_kv_full(0), 0, abort_flag, deadline);
       auto hand_p = [&](int i, int j) {
         // arrive for phase j only once phase j-1 has completed
         if (j > 0) ok = mbar_wait(bar_p_ready(i), (j - 1) & 1, abort_flag, deadline);
@@ -462,7 +391,6 @@ fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
           const int ck = 2 * j + 2;
           ok = mbar_wait(bar_kv_full(ck % kSt), (ck / kSt) & 1, abort_flag, deadline);
         }
-        if (kPacked && ragged && j == nmax - 1) break;       // with the whole warp, below
         if (ok && L == 1 && j < nkv[0]) hand_p(0, j);
         // S_L(j) done: it was issued after every MMA that reads K_j or V_{j-1},
         // and the tensor core completes one thread's MMAs in order. Waited for
@@ -477,31 +405,6 @@ fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
       }
     }
     __syncwarp();
-    if constexpr (kPacked) {
-      if (warp == 10 && ragged && __shfl_sync(0xffffffffu, static_cast<int>(ok), 0)) {
-        const int j = nmax - 1, cv = 2 * j + 1;
-        ok = mbar_wait(bar_kv_full(cv % kSt), (cv / kSt) & 1, abort_flag, deadline);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
-          const uint32_t first = s_kv + (cv % kSt) * C::kTileBytes + (Nk % kBN) * 128;
-          const int units = (kBN - Nk % kBN) * 8;            // 16 bytes each, in every box
-          for (int i = lane; i < units * C::kNBox; i += 32)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};"
-                         :: "r"(first + (i / units) * kBoxBytes + (i % units) * 16), "r"(0) : "memory");
-          fence_proxy_async_smem();
-        }
-        __syncwarp();
-        // the last step's arrivals (no slot goes back: nothing is loaded any more)
-        if (ok && lane == 0) {
-          for (int i = 0; i < 2 && ok; ++i) {
-            if (nkv[i] != nmax) continue;
-            if (j > 0) ok = mbar_wait(bar_p_ready(i), (j - 1) & 1, abort_flag, deadline);
-            if (ok) mbar_arrive(bar_p_ready(i));
-          }
-        }
-        __syncwarp();
-      }
-    }
   } else {
     // ------------------------------------------------------------ softmax groups
     if constexpr (C::kPingPong) setmaxnreg_inc<C::kRegsSoftmax>();
@@ -550,8 +453,8 @@ fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
       int lim = kBN;
       const int kvt = kv_tile(j);
       const int kv0 = kvt * kBN;
-      if (p.causal) lim = min(lim, q_row + causal_off - kv0 + 1);   // bottom-right: key <= row + Nk - N
-      if (kv0 + kBN > Nk) lim = min(lim, Nk - kv0);
+      if (p.causal) lim = min(lim, q_row + p.causal_off - kv0 + 1);   // bottom-right: key <= row + Nk - N
+      if (kv0 + kBN > p.Nk) lim = min(lim, p.Nk - kv0);
       if (kSparse && !((tile_list[j] >> (14 + g)) & 1)) lim = 0;   // tile visible to the other query tile only
       if (lim < kBN) {
 #pragma unroll
@@ -665,7 +568,6 @@ fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
     // than keys under the causal rule) skips the loop and writes O = 0,
     // LSE = -inf; so does any row that saw no key (l = 0).
     const bool empty = has_tile[g] && n_kv == 0;
-    const int seq_row = kPacked ? parked[0] : 0, rows_all = kPacked ? parked[1] : p.N;
     if (ok) {
       ok = mbar_wait(bar_o_final(g), 0, abort_flag, deadline);
       ok = __all_sync(0xffffffffu, ok);
@@ -709,36 +611,17 @@ fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
         }
       }
       fence_proxy_async_smem();
-      if (q_row < rows_all) p.lse[static_cast<size_t>(bh) * (kPacked ? p.T : p.N) + seq_row + q_row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      if (q_row < p.N) p.lse[static_cast<size_t>(bh) * p.N + q_row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
     // every warp of the group meets here whether or not its waits succeeded,
     // so a timeout in one warp cannot leave the others stuck on the barrier;
     // a warp that gave up has raised the abort flag, and then nothing is stored
     named_bar_sync(1 + g, 128);
-    const bool whole = !kPacked || (qt[g] + 1) * kBM <= rows_all;
-    if (has_tile[g] && whole && !*abort_flag && warp == C::kSm0 + 4 * g && lane == 0) {
+    if (has_tile[g] && !*abort_flag && warp == C::kSm0 + 4 * g && lane == 0) {
       for (int bx = 0; bx < C::kNBox; ++bx)
-        tma_store_3d(&map_o, s_q[g] + bx * kBoxBytes, bx * C::kChunk, seq_row + qt[g] * kBM, bh);
+        tma_store_3d(&map_o, s_q[g] + bx * kBoxBytes, bx * C::kChunk, qt[g] * kBM, bh);
       tma_store_commit();
       tma_store_wait_all0();
-    }
-    if constexpr (kPacked) {
-      // the sequence ends inside the tile: its rows one by one, 16 bytes per
-      // lane, since the rows behind them are another sequence's
-      if (has_tile[g] && !whole && !*abort_flag) {
-        constexpr int kUnits = D / 8;
-        const int rows = min(32, rows_all - qt[g] * kBM - quarter * 32);
-        for (int i = lane; i < rows * kUnits; i += 32) {
-          const int r = quarter * 32 + i / kUnits, u = i % kUnits;
-          if (u * 8 < p.head_dim) {
-            uint4 x;
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                         : "r"(swz128(s_q[g] + (u / 8) * kBoxBytes, r, u % 8)) : "memory");
-            *reinterpret_cast<uint4*>(p.o + static_cast<long long>(bh) * p.o_sh +
-                                      static_cast<long long>(seq_row + qt[g] * kBM + r) * p.o_st + u * 8) = x;
-          }
-        }
-      }
     }
   }
 
@@ -754,7 +637,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
   if (threadIdx.x == 0) clock_record(p.clock_acc, clock_start);
 }
 
-template <typename T, int D, bool kSparse, bool kPacked = false>
+template <typename T, int D, bool kSparse>
 static cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
                           const FwdParams& p, int grid, cudaStream_t stream) {
   using C = FwdCfg<T, D>;
@@ -763,10 +646,10 @@ static cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CU
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   static PerDeviceOnce attr;
   const cudaError_t e = attr.run([] {
-    return cudaFuncSetAttribute(fwd_kernel<T, D, kSparse, kPacked>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    return cudaFuncSetAttribute(fwd_kernel<T, D, kSparse>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   });
   if (e != cudaSuccess) return e;
-  fwd_kernel<T, D, kSparse, kPacked><<<grid, C::kThreads, kSmem, stream>>>(mq, mk, mv, mo, p);
+  fwd_kernel<T, D, kSparse><<<grid, C::kThreads, kSmem, stream>>>(mq, mk, mv, mo, p);
   return cudaGetLastError();
 }
 
@@ -786,17 +669,6 @@ cudaError_t launch_fwd(int dtype_bytes, int d, const CUtensorMap& mq, const CUte
     return sparse ? launch<__nv_bfloat16, 64, true>(mq, mk, mv, mo, p, grid, stream)
                   : launch<__nv_bfloat16, 64, false>(mq, mk, mv, mo, p, grid, stream);
   if (dtype_bytes == 4 && d == 64) return launch<float, 64, false>(mq, mk, mv, mo, p, grid, stream);
-  return cudaErrorInvalidValue;
-}
-
-cudaError_t launch_fwd_packed(int d, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                              const CUtensorMap& mo, const FwdParams& p, cudaStream_t stream) {
-  // at most (n + 255) / 256 pairs of query tiles per sequence
-  const long long pairs = (p.T + 255LL * p.S) / (2 * kBM);
-  if (pairs * p.BH >= (1LL << 31)) return cudaErrorInvalidValue;
-  const int grid = static_cast<int>(pairs * p.BH);
-  if (d > 64 && d <= 128) return launch<__nv_bfloat16, 128, false, true>(mq, mk, mv, mo, p, grid, stream);
-  if (d <= 64) return launch<__nv_bfloat16, 64, false, true>(mq, mk, mv, mo, p, grid, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -32,7 +32,7 @@ struct FwdParams {
   int head_dim;                    // FP8 forward: d (64 runs in the d = 128 kernel, columns past d zero)
   unsigned long long* clock_acc;   // [2] SM cycles and ns of every CTA's lifetime, summed (fwd_kernel); may be null
   // packed sequences (launch_fwd_packed): sequence s has rows cu[s] .. cu[s + 1] - 1
-  // of the T rows of every head; O as ordinary memory for tiles that end inside a sequence
+  // of the T rows of every head; O by address
   const int* cu;
   int S, T;
   __nv_bfloat16* o;
@@ -44,10 +44,11 @@ constexpr int kMaskMaxTiles = 1024;  // block-mask rows up to 1024 tiles (N <= 1
 cudaError_t launch_fwd(int dtype_bytes, int d, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                        const CUtensorMap& mo, FwdParams p, cudaStream_t stream);
 
-// bf16, d <= 128, packed sequences: maps over [heads, T, d] (any strides), p.cu, p.S,
-// p.T, p.o and p.head_dim set, p.BH = Hq.
+// bf16, d <= 128, packed sequences: maps over [heads, T, d] (any strides; O's with
+// 32-row boxes), p.cu, p.S,
+// p.T, p.o and p.head_dim set. One CTA per SM.
 cudaError_t launch_fwd_packed(int d, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                              const CUtensorMap& mo, const FwdParams& p, cudaStream_t stream);
+                              const CUtensorMap& mo, FwdParams p, int num_sms, cudaStream_t stream);
 
 // bf16, d in (64, 128], no block mask: clusters of two CTAs (four query tiles)
 // whose MMAs run as cta_group::2 pairs; mk64 is the K map with 64-row boxes
