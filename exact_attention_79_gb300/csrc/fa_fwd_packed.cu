@@ -21,9 +21,9 @@
 //
 // Warps: 0-3 and 4-7 the two softmax groups (one thread per query row), 8 TMA
 // producer, 9 tensor-core issuer, 10 ring watcher, 11 scheduler. Barriers and
-// parities run on across items; everything else is as in fa_fwd.cu, but O has
-// staging of its own, 4 KB per softmax warp, so that the next item's Q can
-// be loaded over this one's while O leaves.
+// parities run on across items; the steps within an item are as in fa_fwd.cu, but
+// O has staging of its own, 4 KB per softmax warp, so that the next item's Q
+// can be loaded over this one's while O leaves.
 #include "fa_common.cuh"
 #include "fa_kernels.h"
 
@@ -180,16 +180,15 @@ fwd_packed_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
   const uint32_t s_out = s_kv + kSt * C::kTileBytes;
   const uint32_t bars = s_out + C::kOutBytes;
   uint8_t* const gbars = gbase + (bars - base);
-  auto bar_q_full = [&](int i) { return bars + 8u * i; };
-  auto bar_q_empty = [&](int i) { return bars + 16u + 8u * i; };
-  auto bar_s_full = [&](int i) { return bars + 32u + 8u * i; };
-  auto bar_p_ready = [&](int i) { return bars + 48u + 8u * i; };
-  auto bar_o_final = [&](int i) { return bars + 64u + 8u * i; };
-  auto bar_item_full = [&](int i) { return bars + 80u + 8u * i; };
-  auto bar_item_empty = [&](int i) { return bars + 80u + 8u * (kItems + i); };
-  auto bar_kv_full = [&](int s) { return bars + 144u + 8u * s; };
-  auto bar_kv_empty = [&](int s) { return bars + 144u + 8u * (kSt + s); };
-  static_assert(144 + 16 * kSt <= 352, "barrier area");
+  auto bar_q_empty = [&](int i) { return bars + 8u * i; };
+  auto bar_s_full = [&](int i) { return bars + 16u + 8u * i; };
+  auto bar_p_ready = [&](int i) { return bars + 32u + 8u * i; };
+  auto bar_o_final = [&](int i) { return bars + 48u + 8u * i; };
+  auto bar_item_full = [&](int i) { return bars + 112u + 8u * i; };
+  auto bar_item_empty = [&](int i) { return bars + 112u + 8u * (kItems + i); };
+  auto bar_kv_full = [&](int s) { return bars + 176u + 8u * s; };
+  auto bar_kv_empty = [&](int s) { return bars + 176u + 8u * (kSt + s); };
+  static_assert(176 + 16 * kSt <= 352, "barrier area");
   const uint32_t bar_stall = bars + 352;                             // nothing arrives (timeout test)
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbars + 360);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(gbars + 364);
@@ -205,7 +204,6 @@ fwd_packed_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
     clock_mark(clock_start);
     *abort_flag = 0;
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar_q_full(i), 1);
       mbar_init(bar_q_empty(i), 1);
       mbar_init(bar_s_full(i), 1);
       mbar_init(bar_p_ready(i), 129);                    // + the ring watcher
@@ -272,26 +270,33 @@ fwd_packed_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
       bool ok = true;
       for (int n = 0; ok && take(n, w); ++n) {
         release(n);
+        // The Q tiles can be loaded only when the last item's last S is done, and
+        // come from device memory: into L2 with them meanwhile.
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (w.nkv[i] > 0)
+            for (int bx = 0; bx < C::kNBox; ++bx)
+              tma_prefetch_l2_3d(&map_q, bx * 64, w.row0 + w.qt[i] * kBM, w.head[i]);
         for (int x = 0; x < 2 * w.nmax && ok; ++x, ++c) {
           const int slot = c % kSt;
           ok = wait(bar_kv_empty(slot), ((c / kSt) & 1) ^ 1, abort_flag, p.timeout_ns);
           if (!ok) break;
-          mbar_arrive_expect_tx(bar_kv_full(slot), C::kTileBytes);
+          // K_0's barrier stands for the item's Q tiles too: one wait before its first S
+          const int tiles = x > 0 ? 1 : 1 + (w.nkv[0] > 0) + (w.nkv[1] > 0);
+          mbar_arrive_expect_tx(bar_kv_full(slot), tiles * C::kTileBytes);
           const CUtensorMap* m = (x & 1) ? &map_v : &map_k;
           for (int bx = 0; bx < C::kNBox; ++bx)
             tma_load_3d(s_kv + slot * C::kTileBytes + bx * kBoxBytes, m, bar_kv_full(slot), bx * 64,
                         w.row0 + (x >> 1) * kBN, w.kv_head);
           if (x > 0) continue;
-          // the Q tiles behind K_0, which may find its slot free earlier
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (!ok || w.nkv[i] == 0) continue;
             ok = wait(bar_q_empty(i), (nq[i] & 1) ^ 1, abort_flag, p.timeout_ns);
             if (!ok) continue;
             ++nq[i];
-            mbar_arrive_expect_tx(bar_q_full(i), C::kTileBytes);
             for (int bx = 0; bx < C::kNBox; ++bx)
-              tma_load_3d(s_q(i) + bx * kBoxBytes, &map_q, bar_q_full(i), bx * 64, w.row0 + w.qt[i] * kBM, w.head[i]);
+              tma_load_3d(s_q(i) + bx * kBoxBytes, &map_q, bar_kv_full(slot), bx * 64, w.row0 + w.qt[i] * kBM, w.head[i]);
           }
         }
       }
@@ -317,100 +322,93 @@ fwd_packed_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
           round ^= 1;
         }
       };
-      uint32_t np0 = 0, np1 = 0, nq0 = 0, nq1 = 0;       // parities: P-ready, Q tiles of each group
-      Work w{};
+      uint32_t np0 = 0, np1 = 0;                         // P-ready parity of each group
       bool ok = !p.test_stall || wait(bar_stall, 0, abort_flag, p.timeout_ns);   // runs out by design
-      // S_i(0) of the item in w
-      auto first_scores = [&]() {
-        const uint64_t k0 = kd + slot * kSlotDesc;
+      auto scores0 = [&]() {
+        issue_qk<D>(tbase + C::col_s(0), qd0, kd + slot * kSlotDesc, idesc_qk);
+        mma_commit(bar_s_full(0));
+      };
+      auto scores1 = [&]() {
+        issue_qk<D>(tbase + C::col_s(1), qd1, kd + slot * kSlotDesc, idesc_qk);
+        mma_commit(bar_s_full(1));
+      };
+      // S_i(0) of an item whose group i has n_i key tiles; early: S_0(0) is out already
+      auto first_scores = [&](int n0, int n1, bool early) {
         ok = wait(bar_kv_full(slot), round, abort_flag, p.timeout_ns);
-        if (ok && w.nkv[0] > 0) {
-          ok = wait(bar_q_full(0), nq0, abort_flag, p.timeout_ns);
-          nq0 ^= 1;
-          tc_fence_after();
-          if (ok) issue_qk<D>(tbase + C::col_s(0), qd0, k0, idesc_qk);
-          mma_commit(bar_s_full(0));
-        }
-        if (ok && w.nkv[1] > 0) {
-          ok = wait(bar_q_full(1), nq1, abort_flag, p.timeout_ns);
-          nq1 ^= 1;
-          tc_fence_after();
-          if (ok) issue_qk<D>(tbase + C::col_s(1), qd1, k0, idesc_qk);
-          mma_commit(bar_s_full(1));
-        }
+        if (!ok) return;
+        tc_fence_after();
+        if (n0 > 0 && !early) scores0();
+        if (n1 > 0) scores1();
         step_slot(1);
       };
+      Work nx;
       int n = 0;
-      bool have = ok && take(0, w);
+      bool have = ok && take(0, nx);
       if (have) {
         release(0);
-        first_scores();
+        first_scores(nx.nkv[0], nx.nkv[1], false);
       }
       while (have && ok) {
+        const int nkv0 = nx.nkv[0], nkv1 = nx.nkv[1], nmax = nx.nmax;
+        ++n;
+        have = take(n, nx);                              // the next one, while the softmax is at this one's first tile
+        if (have) release(n);
         // V_j and K_{j+1} are there when P-ready is (the watcher's arrival). P-ready
         // of j = 0 also says that the group has read the last item's O.
         auto edge_step = [&](int j) {
           const uint64_t v0 = vd + slot * kSlotDesc;
           step_slot(1);
-          const uint64_t k0 = kd + slot * kSlotDesc;
-          if (j + 1 < w.nmax) step_slot(1);
-          if (j < w.nkv[0]) {
+          if (j < nkv0) {
             ok = wait(bar_p_ready(0), np0, abort_flag, p.timeout_ns);
             if (!ok) return;
             np0 ^= 1;
             tc_fence_after();
             issue_pv(tbase + C::col_o(0), tbase + C::col_s(0), v0, idesc_pv, j > 0);
-            if (j + 1 < w.nkv[0]) {
-              issue_qk<D>(tbase + C::col_s(0), qd0, k0, idesc_qk);
-              mma_commit(bar_s_full(0));
-            } else {
-              mma_commit(bar_o_final(0));
-            }
+            if (j + 1 < nkv0) scores0();
+            else mma_commit(bar_o_final(0));
           }
-          if (j < w.nkv[1]) {
+          // The next item's S_0(0) already here, if its tiles are: group 0
+          // is at it while group 1 finishes. (Not if the next item has no group 1:
+          // then its first S would stand for this item's last P V towards the watcher.)
+          bool early = false;
+          if (j + 1 == nmax && have && nx.nkv[1] > 0 && mbar_try_wait(bar_kv_full(slot), round)) {
+            early = true;
+            tc_fence_after();
+            scores0();
+          }
+          if (j < nkv1) {
             ok = wait(bar_p_ready(1), np1, abort_flag, p.timeout_ns);
             if (!ok) return;
             np1 ^= 1;
             tc_fence_after();
             issue_pv(tbase + C::col_o(1), tbase + C::col_s(1), v0, idesc_pv, j > 0);
-            if (j + 1 < w.nkv[1]) {
-              issue_qk<D>(tbase + C::col_s(1), qd1, k0, idesc_qk);
-              mma_commit(bar_s_full(1));
-            } else {
-              mma_commit(bar_o_final(1));
-            }
+            if (j + 1 < nkv1) scores1();
+            else mma_commit(bar_o_final(1));
           }
+          if (j + 1 < nmax) step_slot(1);
+          else if (have) first_scores(nx.nkv[0], nx.nkv[1], early);
         };
         edge_step(0);
         int j = 1;
-        const int inner = min(w.nkv[0], w.nkv[1]) - 1;   // both groups have a next step
+        const int inner = min(nkv0, nkv1) - 1;           // both groups have a next step
         for (; j < inner && ok; ++j) {
           const uint64_t v0 = vd + slot * kSlotDesc;
-          step_slot(1);
-          const uint64_t k0 = kd + slot * kSlotDesc;
           step_slot(1);
           ok = wait(bar_p_ready(0), np0, abort_flag, p.timeout_ns);
           if (!ok) break;
           tc_fence_after();
           issue_pv(tbase + C::col_o(0), tbase + C::col_s(0), v0, idesc_pv, true);
-          issue_qk<D>(tbase + C::col_s(0), qd0, k0, idesc_qk);
-          mma_commit(bar_s_full(0));
+          scores0();
           ok = wait(bar_p_ready(1), np1, abort_flag, p.timeout_ns);
           if (!ok) break;
           tc_fence_after();
           issue_pv(tbase + C::col_o(1), tbase + C::col_s(1), v0, idesc_pv, true);
-          issue_qk<D>(tbase + C::col_s(1), qd1, k0, idesc_qk);
-          mma_commit(bar_s_full(1));
+          scores1();
+          step_slot(1);
           np0 ^= 1;
           np1 ^= 1;
         }
-        for (; j < w.nmax && ok; ++j) edge_step(j);
-        ++n;
-        have = ok && take(n, w);
-        if (have) {
-          release(n);
-          first_scores();
-        }
+        for (; j < nmax && ok; ++j) edge_step(j);
       }
     }
     __syncwarp();
@@ -453,9 +451,11 @@ fwd_packed_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
             const int from = w.len % kBN;
             const uint32_t dst = s_kv + (cv % kSt) * C::kTileBytes + from * 128;
             const int units = (kBN - from) * 8;          // 16 bytes each, in every box
-            for (int i = lane; i < units * C::kNBox; i += 32)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};"
-                           :: "r"(dst + (i / units) * kBoxBytes + (i % units) * 16), "r"(0) : "memory");
+#pragma unroll
+            for (int bx = 0; bx < C::kNBox; ++bx)
+              for (int i = lane; i < units; i += 32)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" :: "r"(dst + bx * kBoxBytes + i * 16), "r"(0)
+                             : "memory");
             fence_proxy_async_smem();
           }
           __syncwarp();
@@ -467,6 +467,10 @@ fwd_packed_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
           if (ok) {
             mbar_arrive(bar_kv_empty((cv - 1) % kSt));
             if (cv > 1) mbar_arrive(bar_kv_empty((cv - 2) % kSt));
+            if (j + 1 == w.nmax) {                       // every S of the item is done: its Q tiles too
+              if (w.nkv[0] > 0) mbar_arrive(bar_q_empty(0));
+              if (w.nkv[1] > 0) mbar_arrive(bar_q_empty(1));
+            }
           }
           if (ok && L == 1) hand(1, np1);
           else if (ok) hand(0, np0);
@@ -512,7 +516,8 @@ fwd_packed_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
     const uint32_t t_s = tbase + lane_off + C::col_s(g);
     const uint32_t t_o = tbase + lane_off + C::col_o(g);
     const float sl2 = p.scale_log2;
-    uint32_t ns = 0, no = 0;                             // parities: S, O final of this group
+    const uint32_t stage = s_out + warp * 4096;
+    uint32_t ns = 0, no = 0;                             // parities: S, O final
     for (int n = 0;; ++n) {
       Work w;
       const bool have = take(n, w);
@@ -595,71 +600,62 @@ fwd_packed_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
         tc_fence_before();
         mbar_arrive(bar_p_ready(g));
       }
-      // every S that reads this Q tile is done
-      if (ok && quarter == 0 && lane == 0) mbar_arrive(bar_q_empty(g));
       // ---------------------------------------------------------- epilogue
-      if (ok) {
-        ok = wait(bar_o_final(g), no, abort_flag, p.timeout_ns);
-        ok = __all_sync(0xffffffffu, ok);
-      }
-      if (!ok) break;
-      tc_fence_after();
-      no ^= 1;
+      // what it needs before O is final
       const float inv_l = l > 0.f ? 1.0f / l : 0.f;
-      // the item once more: the loop above holds no register for what only
-      // this needs
-      volatile int* const it = items + 4 * (n % kItems);
-      const int q_row = (two_heads ? it[2] : 2 * it[2] + g) * kBM + row;   // within the sequence
+      volatile int* const it = items + 4 * (n % kItems);   // once more: the loop above holds no register for it
       const int head = two_heads ? 2 * it[3] + g : it[3];
-      const int at = it[0] + q_row;
-      const int it1 = it[1];
-      const bool mine = q_row < it1;
+      const int first = (two_heads ? it[2] : 2 * it[2] + g) * kBM + quarter * 32;   // this warp's rows in the sequence
+      const int valid = min(32, it[1] - first);            // of them inside it, may be <= 0
+      const int at = it[0] + first;
       __syncwarp();
       if (lane == 0) release(n);
-      const uint32_t stage = s_out + warp * 4096;
-      const int valid = min(32, it1 - (q_row - lane));     // rows of this warp inside the sequence, may be <= 0
+      if (ok && lane < valid)
+        p.lse[static_cast<long long>(head) * p.T + at + lane] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      if (ok) ok = wait(bar_o_final(g), no, abort_flag, p.timeout_ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      no ^= 1;
+      tc_fence_after();
+      uint32_t o[D / 32][32], r[D / 2];
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x) tmem_ld_32x32b_x32(t_o + 32 * x, o[x]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x) {
+        reg_fence_x32(o[x]);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          r[16 * x + e] = pack_bf16x2(__uint_as_float(o[x][2 * e]) * inv_l, __uint_as_float(o[x][2 * e + 1]) * inv_l);
+      }
 #pragma unroll
       for (int x0 = 0; x0 < D; x0 += 64) {
         if (lane == 0) tma_store_wait_read0();           // the warp's last store has left its buffer
         __syncwarp();
 #pragma unroll
-        for (int x1 = 0; x1 < 64; x1 += 32) {
-          uint32_t o[32];
-          tmem_ld_32x32b_x32(t_o + x0 + x1, o);
-          tmem_wait_ld();
-          reg_fence_x32(o);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t r[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              r[e] = pack_bf16x2(__uint_as_float(o[8 * u + 2 * e]) * inv_l, __uint_as_float(o[8 * u + 2 * e + 1]) * inv_l);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(swz128(stage, lane, x1 / 8 + u)), "r"(r[0]),
-                         "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
-          }
-        }
+        for (int u = 0; u < 8; ++u)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(swz128(stage, lane, u)), "r"(r[x0 / 2 + 4 * u]),
+                       "r"(r[x0 / 2 + 4 * u + 1]), "r"(r[x0 / 2 + 4 * u + 2]), "r"(r[x0 / 2 + 4 * u + 3]) : "memory");
         if (valid == 32) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_3d(&map_o, stage, x0, at - lane, head);
+            tma_store_3d(&map_o, stage, x0, at, head);
             tma_store_commit();
           }
         } else {
           // the sequence ends among the warp's rows: the rows behind are another's
           __syncwarp();
           for (int i = lane; i < valid * 8; i += 32) {
-            const int r = i >> 3, u = i & 7;
+            const int rr = i >> 3, u = i & 7;
             if (x0 + 8 * u < p.head_dim) {
               uint4 y;
               asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
-                           : "r"(swz128(stage, r, u)) : "memory");
-              *reinterpret_cast<uint4*>(p.o + head * p.o_sh + (at - lane + r) * p.o_st + x0 + 8 * u) = y;
+                           : "r"(swz128(stage, rr, u)) : "memory");
+              *reinterpret_cast<uint4*>(p.o + head * p.o_sh + (at + rr) * p.o_st + x0 + 8 * u) = y;
             }
           }
         }
       }
-      if (mine) p.lse[static_cast<long long>(head) * p.T + at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
     if (lane == 0) tma_store_wait_all0();
     __syncwarp();
