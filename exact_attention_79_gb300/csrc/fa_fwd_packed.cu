@@ -184,6 +184,7 @@ fwd_packed_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
   auto bar_s_full = [&](int i) { return bars + 16u + 8u * i; };
   auto bar_p_ready = [&](int i) { return bars + 32u + 8u * i; };
   auto bar_o_final = [&](int i) { return bars + 48u + 8u * i; };
+  const uint32_t bar_q1_full = bars + 64u;               // Q of group 1 (group 0's lands on K_0's barrier)
   auto bar_item_full = [&](int i) { return bars + 112u + 8u * i; };
   auto bar_item_empty = [&](int i) { return bars + 112u + 8u * (kItems + i); };
   auto bar_kv_full = [&](int s) { return bars + 176u + 8u * s; };
@@ -217,6 +218,7 @@ fwd_packed_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
       mbar_init(bar_kv_full(s), 1);
       mbar_init(bar_kv_empty(s), 1);
     }
+    mbar_init(bar_q1_full, 1);
     mbar_init(bar_stall, 1);
     fence_mbar_init();
   }
@@ -281,9 +283,9 @@ fwd_packed_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
           const int slot = c % kSt;
           ok = wait(bar_kv_empty(slot), ((c / kSt) & 1) ^ 1, abort_flag, p.timeout_ns);
           if (!ok) break;
-          // K_0's barrier stands for the item's Q tiles too: one wait before its first S
-          const int tiles = x > 0 ? 1 : 1 + (w.nkv[0] > 0) + (w.nkv[1] > 0);
-          mbar_arrive_expect_tx(bar_kv_full(slot), tiles * C::kTileBytes);
+          // K_0's barrier stands for group 0's Q tile too (the group always has one):
+          // one wait before the item's first S
+          mbar_arrive_expect_tx(bar_kv_full(slot), (x > 0 ? 1 : 2) * C::kTileBytes);
           const CUtensorMap* m = (x & 1) ? &map_v : &map_k;
           for (int bx = 0; bx < C::kNBox; ++bx)
             tma_load_3d(s_kv + slot * C::kTileBytes + bx * kBoxBytes, m, bar_kv_full(slot), bx * 64,
@@ -295,8 +297,10 @@ fwd_packed_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
             ok = wait(bar_q_empty(i), (nq[i] & 1) ^ 1, abort_flag, p.timeout_ns);
             if (!ok) continue;
             ++nq[i];
+            const uint32_t bar = i ? bar_q1_full : bar_kv_full(slot);
+            if (i) mbar_arrive_expect_tx(bar, C::kTileBytes);
             for (int bx = 0; bx < C::kNBox; ++bx)
-              tma_load_3d(s_q(i) + bx * kBoxBytes, &map_q, bar_kv_full(slot), bx * 64, w.row0 + w.qt[i] * kBM, w.head[i]);
+              tma_load_3d(s_q(i) + bx * kBoxBytes, &map_q, bar, bx * 64, w.row0 + w.qt[i] * kBM, w.head[i]);
           }
         }
       }
@@ -322,7 +326,7 @@ fwd_packed_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
           round ^= 1;
         }
       };
-      uint32_t np0 = 0, np1 = 0;                         // P-ready parity of each group
+      uint32_t np0 = 0, np1 = 0, nq1 = 0;                // parities: P-ready of each group, Q of group 1
       bool ok = !p.test_stall || wait(bar_stall, 0, abort_flag, p.timeout_ns);   // runs out by design
       auto scores0 = [&]() {
         issue_qk<D>(tbase + C::col_s(0), qd0, kd + slot * kSlotDesc, idesc_qk);
@@ -334,11 +338,19 @@ fwd_packed_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
       };
       // S_i(0) of an item whose group i has n_i key tiles; early: S_0(0) is out already
       auto first_scores = [&](int n0, int n1, bool early) {
-        ok = wait(bar_kv_full(slot), round, abort_flag, p.timeout_ns);
-        if (!ok) return;
-        tc_fence_after();
-        if (n0 > 0 && !early) scores0();
-        if (n1 > 0) scores1();
+        if (!early) {
+          ok = wait(bar_kv_full(slot), round, abort_flag, p.timeout_ns);
+          if (!ok) return;
+          tc_fence_after();
+          scores0();
+        }
+        if (n1 > 0) {
+          ok = wait(bar_q1_full, nq1, abort_flag, p.timeout_ns);
+          if (!ok) return;
+          nq1 ^= 1;
+          tc_fence_after();
+          scores1();
+        }
         step_slot(1);
       };
       Work nx;
@@ -364,8 +376,11 @@ fwd_packed_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
             np0 ^= 1;
             tc_fence_after();
             issue_pv(tbase + C::col_o(0), tbase + C::col_s(0), v0, idesc_pv, j > 0);
-            if (j + 1 < nkv0) scores0();
-            else mma_commit(bar_o_final(0));
+            if (j + 1 < nkv0) {
+              scores0();
+            } else {
+              mma_commit(bar_o_final(0));
+            }
           }
           // The next item's S_0(0) already here, if its tiles are: group 0
           // is at it while group 1 finishes. (Not if the next item has no group 1:
@@ -382,15 +397,18 @@ fwd_packed_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
             np1 ^= 1;
             tc_fence_after();
             issue_pv(tbase + C::col_o(1), tbase + C::col_s(1), v0, idesc_pv, j > 0);
-            if (j + 1 < nkv1) scores1();
-            else mma_commit(bar_o_final(1));
+            if (j + 1 < nkv1) {
+              scores1();
+            } else {
+              mma_commit(bar_o_final(1));
+            }
           }
           if (j + 1 < nmax) step_slot(1);
           else if (have) first_scores(nx.nkv[0], nx.nkv[1], early);
         };
         edge_step(0);
         int j = 1;
-        const int inner = min(nkv0, nkv1) - 1;           // both groups have a next step
+        const int inner = min(nkv0, nkv1) - 1;           // both groups have two more steps
         for (; j < inner && ok; ++j) {
           const uint64_t v0 = vd + slot * kSlotDesc;
           step_slot(1);
@@ -467,10 +485,10 @@ fwd_packed_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
           if (ok) {
             mbar_arrive(bar_kv_empty((cv - 1) % kSt));
             if (cv > 1) mbar_arrive(bar_kv_empty((cv - 2) % kSt));
-            if (j + 1 == w.nmax) {                       // every S of the item is done: its Q tiles too
-              if (w.nkv[0] > 0) mbar_arrive(bar_q_empty(0));
-              if (w.nkv[1] > 0) mbar_arrive(bar_q_empty(1));
-            }
+          }
+          if (ok && j + 1 == w.nmax) {                   // every S of the item is done: its Q tiles too
+            if (w.nkv[0] > 0) mbar_arrive(bar_q_empty(0));
+            if (w.nkv[1] > 0) mbar_arrive(bar_q_empty(1));
           }
           if (ok && L == 1) hand(1, np1);
           else if (ok) hand(0, np0);
@@ -518,17 +536,23 @@ fwd_packed_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
     const float sl2 = p.scale_log2;
     const uint32_t stage = s_out + warp * 4096;
     uint32_t ns = 0, no = 0;                             // parities: S, O final
-    for (int n = 0;; ++n) {
-      Work w;
-      const bool have = take(n, w);
-      if (!__all_sync(0xffffffffu, have)) break;
-      const int n_kv = g ? w.nkv[1] : w.nkv[0];
-      if (n_kv == 0) {
+    // The group's next item with a tile for it, from n on: its key tiles and the
+    // keys this row sees (causal), or that there are. -1: no more.
+    int n = 0, n_kv, seen;
+    auto next = [&]() {
+      for (;; ++n) {
+        Work w;
+        const bool have = take(n, w);
+        n_kv = -1;
+        if (!__all_sync(0xffffffffu, have)) return;
+        n_kv = g ? w.nkv[1] : w.nkv[0];
+        seen = p.causal ? min(w.len, (g ? w.qt[1] : w.qt[0]) * kBM + row + 1) : w.len;
+        if (n_kv > 0) return;
         if (lane == 0) release(n);
-        continue;
       }
-      // keys this row sees (causal), or that there are
-      const int seen = p.causal ? min(w.len, (g ? w.qt[1] : w.qt[0]) * kBM + row + 1) : w.len;
+    };
+    next();
+    while (n_kv > 0) {
       float m = -INFINITY;                               // running max, log2 units of scale*s
       float l = 0.f;                                     // running sum relative to m
       bool ok = true;
@@ -612,6 +636,8 @@ fwd_packed_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
       if (lane == 0) release(n);
       if (ok && lane < valid)
         p.lse[static_cast<long long>(head) * p.T + at + lane] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      ++n;
+      next();                                              // while the last P V runs
       if (ok) ok = wait(bar_o_final(g), no, abort_flag, p.timeout_ns);
       if (!__all_sync(0xffffffffu, ok)) break;
       no ^= 1;
