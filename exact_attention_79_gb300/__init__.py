@@ -51,7 +51,7 @@ SIGNATURES = {
     "fa_fwd_packed": (_I, [_VP, _LL, _LL, _VP, _LL, _LL, _VP, _LL, _LL, _VP, _LL, _LL, _VP, _VP,
                            _I, _I, _I, _I, _I, _I, _F, _VP]),
     "fa_cache8_append": (_I, [_VP, _LL, _LL, _VP, _LL, _LL, _VP, _VP, _I, _I, _VP, _VP, _I, _VP]),
-    "fa_fwd_cache8_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "fa_fwd_cache8_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
     "fa_fwd_cache8": (_I, [_VP, _VP, _VP, _I, _VP, _VP, _VP, _VP, _SZ, _I, _I, _I, _I, _F, _I, _F, _VP]),
     "fa_cache8_evict": (_I, [_VP, _VP, _I, _VP, _I, _I, _I, _VP, _I, _VP, _VP, _VP]),
     "fa_ex2_throughput": (_I, [ctypes.POINTER(ctypes.c_double), _VP]),
@@ -454,7 +454,7 @@ def fwd_cache8(q, cache, block_table, lengths, causal=True, scale=None, out=None
     lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev) if lse is None else lse
     table = _table_spec(block_table, B=B)
     if workspace is None:
-        n = lib.fa_fwd_cache8_workspace_bytes(B, Hq, Hkv, Nq, d, block_table.shape[1])
+        n = lib.fa_fwd_cache8_workspace_bytes(B, Hq, Hkv, Nq, d, block_table.shape[1], int(weight_decay is not None))
         workspace = torch.empty(int(n), dtype=torch.uint8, device=dev)
     _require(dev, (q, "q", bf16, (B, Hq, Nq, d)), *specs, table, (lengths, "lengths", torch.int32, (B,)),
              (o, "out", bf16, (B, Hq, Nq, d)), (lse, "lse", torch.float32, (B, Hq, Nq)),

@@ -658,22 +658,34 @@ fa_status cache8_pools(const fa_cache8* c, int B, int max_blocks, const void* bl
   if (c->num_blocks < 1 || c->Hkv < 1 || c->Hkv > 65535 || c->d < 1 || B < 1 || B > 65535 || max_blocks < 1 ||
       max_blocks > (1 << 24))
     return FA_ERR_INVALID_ARG;
-  if (!fp8_dim(c->d)) return FA_ERR_UNSUPPORTED;
+  if (!fp8_dim(c->d) || static_cast<long long>(c->num_blocks) * c->Hkv >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
   *out = fa::Cache8Pools{c->k, c->v, c->k_scale, c->v_scale, c->weight, c->num_blocks, c->Hkv, c->d};
   return FA_OK;
 }
 
-// Bytes of the partial results of fa_fwd_cache8; off_s: where the statistics start.
-size_t cache8_workspace(int parts, int cols, int d, size_t* off_s) {
-  const size_t D = d <= 64 ? 64 : d <= 128 ? 128 : 256;
-  const size_t rows = 2 * static_cast<size_t>(parts) * cols;
-  *off_s = align256(rows * D * 4);
-  return *off_s + align256(rows * 3 * 4);
+// Bytes of fa_fwd_cache8's workspace: partial results, their statistics (off_s)
+// and, with weights, the scores of every token and row (off_x).
+struct Cache8Workspace {
+  size_t off_s, off_x, total;
+};
+Cache8Workspace cache8_workspace(int B, int Hkv, int R, int d, int max_blocks, bool weights) {
+  const int cols = fa::cache8_columns(d, R), chunks = (R + cols - 1) / cols;
+  const size_t D = d <= 128 ? 128 : 256;
+  const size_t rows = 2 * static_cast<size_t>(fa::cache8_parts(B, Hkv, d, R, max_blocks)) * cols;
+  const size_t units = static_cast<size_t>(B) * Hkv * chunks * max_blocks;
+  Cache8Workspace w;
+  w.off_s = align256(rows * D * 4);
+  w.off_x = w.off_s + align256(rows * 3 * 4);
+  w.total = w.off_x + (weights ? units * FA_CACHE8_BLOCK * cols * 4 : 0);
+  return w;
 }
 
 fa_status cache8_rows(int B, int Hq, int Hkv, int Nq, int d, int max_blocks) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Nq < 1 || Hq % Hkv != 0 || d < 1 || max_blocks < 1) return FA_ERR_INVALID_ARG;
   if (static_cast<long long>(Hq / Hkv) * Nq > fa::kCache8MaxRows || !fp8_dim(d)) return FA_ERR_UNSUPPORTED;
+  // units of work (row groups x blocks) are counted in 32 bits
+  const int R = Hq / Hkv * Nq, cols = fa::cache8_columns(d, R), chunks = (R + cols - 1) / cols;
+  if (static_cast<double>(B) * Hkv * chunks * max_blocks >= 2147483648.0) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
 }  // namespace
@@ -709,11 +721,9 @@ fa_status fa_cache8_append(const void* k, long long k_stride_h, long long k_stri
   return fa::launch_cache8_append(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-size_t fa_fwd_cache8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int max_blocks) {
+size_t fa_fwd_cache8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int max_blocks, int add_weights) {
   if (cache8_rows(B, Hq, Hkv, Nq, d, max_blocks) != FA_OK) return 0;
-  const int R = Hq / Hkv * Nq, cols = fa::cache8_columns(d, R);
-  size_t off_s;
-  return cache8_workspace(fa::cache8_parts(B, Hkv, (R + cols - 1) / cols, max_blocks), cols, d, &off_s);
+  return cache8_workspace(B, Hkv, Hq / Hkv * Nq, d, max_blocks, add_weights != 0).total;
 }
 
 fa_status fa_fwd_cache8(const void* q, const fa_cache8* cache, const int* block_table, int max_blocks,
@@ -730,9 +740,8 @@ fa_status fa_fwd_cache8(const void* q, const fa_cache8* cache, const int* block_
   p.R = p.G * Nq;
   const int cols = fa::cache8_columns(p.c.d, p.R);
   p.chunks = (p.R + cols - 1) / cols;
-  size_t off_s;
-  const size_t need = cache8_workspace(fa::cache8_parts(B, p.c.Hkv, p.chunks, max_blocks), cols, p.c.d, &off_s);
-  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < need)
+  const Cache8Workspace w = cache8_workspace(B, p.c.Hkv, p.R, p.c.d, max_blocks, add_weights != 0);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < w.total)
     return FA_ERR_WORKSPACE;
   unsigned* status = nullptr;
   st = device_state(stream, &status);
@@ -751,8 +760,16 @@ fa_status fa_fwd_cache8(const void* q, const fa_cache8* cache, const int* block_
   p.scale_log2 = scale * 1.4426950408889634f;
   p.decay = weight_decay;
   p.part_o = static_cast<float*>(workspace);
-  p.part_s = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + off_s);
-  return fa::launch_cache8_fwd(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  p.part_s = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.off_s);
+  p.scores = add_weights ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.off_x) : nullptr;
+  p.status = status;
+  p.timeout_ns = wait_limit_ns();
+  p.test_stall = test_stall();
+  CUtensorMap mk, mv;
+  const long long rows = static_cast<long long>(p.c.num_blocks) * p.c.Hkv;
+  if (!make_map(&mk, p.c.k, 1, p.c.d, FA_CACHE8_BLOCK, rows, 64) || !make_map(&mv, p.c.v, 1, p.c.d, FA_CACHE8_BLOCK, rows, 64))
+    return FA_ERR_CUDA;
+  return fa::launch_cache8_fwd(mk, mv, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 fa_status fa_cache8_evict(const fa_cache8* cache, const int* block_table, int max_blocks, const int* lengths, int B,

@@ -1,198 +1,129 @@
-// Attention of a few new queries per sequence over the 8-bit block cache.
+// Attention of a few new queries per sequence over the 8-bit block cache, on
+// the tensor cores with the cache's codes as they are.
 //
 // For sequence b, KV head h the R = (Hq / Hkv) * Nq query rows that share the
-// head are the columns of two tensor-core products per 16 keys:
-//   S^T [16 keys x R] = K [16 x d] Q^T,   O^T [d x R] += V^T [d x 16] P^T,
-// so K and V, read once, fill the M side of mma.m16n8k16 and the few rows
-// cost N = 8 columns at a time. e4m3 codes become halves exactly; the block's
-// K scale multiplies the logits, its V scale is folded into P's exponent. Q is
-// brought to [2^14, 2^15) by a power of two per row, where every bf16 value
-// down to 2^-29 of the row's largest is an exact half.
+// head are columns of two e4m3 products (tcgen05 kind::f8f6f4) per tile of 128
+// tokens, two blocks of the cache:
+//   S^T [128 tokens x R] = K [128 x d] Q^T      O^T [d x R] += V^T [d x 128] P^T
+// K and V go from memory to shared memory (TMA, 128-byte swizzle) and from
+// there into the products; no thread ever touches them. What the threads make
+// small enough for e4m3 are Q and P, as sums of e4m3 terms in columns of their own:
+//   Q, times a power of two per row that brings it to [128, 256): q = q0 + q1 / 16, which
+//      is exact for every bf16 value down to 2^-10 (2^-17 of the row's largest);
+//   P, y = 2^(s - reference + 4) <= 256: y = y0 + y1 / 16 + y2 / 256, each term the rounding
+//      of what the one before left, 2^-12 relative and 2^-18 absolute.
+// fp32 accumulators in TMEM: S^T twice (the next tile's is computed while this one's
+// softmax runs), O^T with three columns per row.
 //
-// Each warp keeps its own online softmax over the 16-key slices it takes (two
-// references per column: ml for the sum of probabilities, mo for O, whose
-// terms carry the V scales; both trail the true maximum by at most 2^8, and
-// are only looked up across lanes when one would trail further). P is rounded
-// to half relative to mo (2^-11 relative), O and the sums are fp32.
+// One thread per token. A block's K scale multiplies its logits; its V scale is
+// folded into P's exponent. Hence two references per row: ml for the sum of
+// probabilities, mo for O. Both are common to the CTA and may trail the true
+// maximum by up to 2^4; when a token exceeds that (told by the barrier that the
+// softmax warps pass once a tile), all look up the maximum and rescale O in TMEM.
 //
 // HBM-bound: 2 d bytes per cached token and KV head, against which Q and O
 // are small. The work is a line of units, one per (sequence, KV head, chunk of
-// rows, block of 64 tokens), cut into equal parts for the CTAs whatever the
+// rows, block of 64 tokens), cut into equal parts for the CTAs (two per SM, so
+// that one's row changes hide behind the other's stream) whatever the
 // sequences' lengths; a row whose units fall to several CTAs is joined from
 // their partial results by a second kernel.
-#include <cuda_fp16.h>
-
+//
+// Warps: 0-3 softmax, 4 producer (block table, scales, TMA), 5 tensor-core issuer, 6
+// Q (reads, splits and lays out the next row group's queries).
 #include "fa_cache8.cuh"
 
 namespace fa {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr float kShift = 6.f;             // P is taken times 2^6: at most 2^14 as a half, normal down to 2^-20
+constexpr int kThreads = 224;
+constexpr float kTrail = 4.f;             // log2 of how far a reference may trail
+constexpr float kShift = 4.f;             // y = 2^(x - reference + kShift) <= 2^8
+constexpr int kInfo = 8;                  // tiles whose scales wait in shared memory
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// Whether `mine` holds for any of the softmax warps' 128 threads, which meet here.
+__device__ __forceinline__ bool meet_or(bool mine) {
+  int any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "selp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(any) : "r"(static_cast<int>(mine)) : "memory");
+  return any != 0;
 }
-// Transpose of an 8 x 8 matrix of halves spread over the warp.
-__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-  return r;
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(taddr));
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
+// Makes the registers depend on the tcgen05.wait::ld before.
+__device__ __forceinline__ void reg_fence_x16(uint32_t (&r)[16]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]) :: "memory");
 }
-
-// The codes of one 16-key slice as a lane (g = lane / 4, t = lane % 4) feeds
-// them to the products. K: rows g and g + 8, bytes 64 c + 16 t .. + 15 of each
-// 64-byte piece c; word w of a piece is the operand of product step 4 c + w
-// (which columns of d a step covers is free as long as Q agrees). V: tokens
-// 2t, 2t+1, 2t+8, 2t+9, a lane's D / 8 columns of d as words.
-template <int D>
-struct Slice {
-  uint4 k[2][D / 64];
-  uint32_t v[4][D / 32];
-};
-
-// column of d that word w, byte e of a lane's V words holds
-template <int D>
-__device__ __forceinline__ int v_column(int g, int w) {
-  if constexpr (D == 64) return 8 * g + 4 * w;
-  else return 128 * (w >> 2) + 16 * g + 4 * (w & 3);
+__device__ __forceinline__ void store_byte(uint32_t addr, uint32_t x) {
+  asm volatile("st.shared.b8 [%0], %1;" :: "r"(addr), "r"(x) : "memory");
 }
-
-template <int D>
-__device__ __forceinline__ void load_slice(Slice<D>& s, const uint8_t* k, const uint8_t* v, int d, int tokens, int lane) {
-  const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-  for (int r = 0; r < 2; ++r)
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) {
-      const int row = g + 8 * r, col = 64 * c + 16 * t;
-      s.k[r][c] = (row < tokens && col < d) ? __ldg(reinterpret_cast<const uint4*>(k + row * d + col)) : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = 2 * t + (i & 1) + 8 * (i >> 1);
-    if constexpr (D == 64) {
-      const int col = 8 * g;
-      const uint2 x = (row < tokens && col < d) ? __ldg(reinterpret_cast<const uint2*>(v + row * d + col)) : make_uint2(0, 0);
-      s.v[i][0] = x.x;
-      s.v[i][1] = x.y;
-    } else {
-#pragma unroll
-      for (int c = 0; c < D / 128; ++c) {
-        const int col = 128 * c + 16 * g;
-        const uint4 x = (row < tokens && col < d) ? __ldg(reinterpret_cast<const uint4*>(v + row * d + col)) : make_uint4(0, 0, 0, 0);
-        s.v[i][4 * c] = x.x;
-        s.v[i][4 * c + 1] = x.y;
-        s.v[i][4 * c + 2] = x.z;
-        s.v[i][4 * c + 3] = x.w;
+// Bounded wait whose limit starts at its own first look at the timer.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned long long limit_ns) {
+  uint32_t polls = 0;
+  uint64_t until = 0;
+  while (!mbar_try_wait(bar, parity)) {
+    if ((++polls & 255u) == 0) {
+      if (*abort_flag) return false;
+      const uint64_t now = global_timer_ns();
+      if (until == 0) until = now + limit_ns;
+      if (now > until) {
+        *abort_flag = 1;
+        return false;
       }
     }
   }
+  return true;
 }
 
-// The query rows [row0, row0 + ncols) of the group as product operands in
-// shared memory: for column n, step j and lane l the two registers at
-// sq[((n / 8) * (D / 16) + j) * 32 + l]; rows past R and columns past d are 0.
-// qs[n]: the power of two by which the row was divided.
-template <int D>
-__device__ __forceinline__ void stage_queries(uint2* sq, float* qs, const __nv_bfloat16* q, int R, int row0, int ncols,
-                                              int d, int warp, int lane) {
-  for (int n = warp; n < ncols; n += kWarps) {
-    const int row = row0 + n;
-    float x[D / 128 < 1 ? 1 : D / 128][4];
-    float amax = 0.f;
-#pragma unroll
-    for (int c = 0; c < (D + 127) / 128; ++c) {
-      const int col = 128 * c + 4 * lane;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[c][e] = 0.f;
-      if (row < R && col < d) {
-        const uint2 u = *reinterpret_cast<const uint2*>(q + static_cast<size_t>(row) * d + col);
-        x[c][0] = __uint_as_float(u.x << 16);
-        x[c][1] = __uint_as_float(u.x & 0xFFFF0000u);
-        x[c][2] = __uint_as_float(u.y << 16);
-        x[c][3] = __uint_as_float(u.y & 0xFFFF0000u);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(x[c][e]));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    // exponent that brings the largest to [2^14, 2^15); bounded so that both powers are normal
-    const int e2 = amax > 0.f ? max(-100, min(100, static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14)) : 0;
-    const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
-    if (lane == 0) qs[n] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
-#pragma unroll
-    for (int c = 0; c < (D + 127) / 128; ++c) {
-      const int col = 128 * c + 4 * lane;
-      if (col < D) {
-        const int j = 4 * (col / 64) + (col % 16) / 4, t = (col % 64) / 16;
-        sq[((n >> 3) * (D / 16) + j) * 32 + (n & 7) * 4 + t] =
-            make_uint2(pack_f16x2(x[c][0] * down, x[c][1] * down), pack_f16x2(x[c][2] * down, x[c][3] * down));
-      }
-    }
-  }
+// The line of units: for sequence after sequence, row group (KV head, chunk)
+// after row group, its blocks. A sequence has at least one block of units, so
+// that rows without keys are written too.
+__device__ __forceinline__ int line_blocks(const Cache8Params& p, int b) {
+  return max(1, (cache_length(p.lengths, b, p.max_blocks) + kCacheBlock - 1) / kCacheBlock);
+}
+// All units; by a whole warp.
+__device__ __forceinline__ int line_total(const Cache8Params& p, int lane) {
+  int sum = 0;
+  for (int b = lane; b < p.B; b += 32) sum += line_blocks(p, b);
+  return __reduce_add_sync(0xffffffffu, sum) * p.c.Hkv * p.chunks;
+}
+// Parts the line is cut into by a grid of `ctas`: none of them empty, so that
+// every part between a row's first and last has a partial result of it.
+__device__ __forceinline__ int line_parts(int total, int ctas) { return min(ctas, total); }
+__device__ __forceinline__ int part_begin(int total, int i, int parts) {
+  return static_cast<int>(static_cast<long long>(total) * i / parts);
+}
+// the part that unit u belongs to
+__device__ __forceinline__ int part_of(int total, int u, int parts) {
+  return static_cast<int>(((u + 1LL) * parts - 1) / total);
 }
 
-// S^T of one slice for NT column tiles (before any scale).
-template <int D, int NT>
-__device__ __forceinline__ void scores(float (&s)[NT][4], const uint4 (&k)[2][D / 64], const uint2* sq, int lane) {
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
-#pragma unroll
-  for (int j = 0; j < D / 16; ++j) {
-    const uint4 x = k[0][j / 4], y = k[1][j / 4];
-    const uint32_t wx = j % 4 == 0 ? x.x : j % 4 == 1 ? x.y : j % 4 == 2 ? x.z : x.w;
-    const uint32_t wy = j % 4 == 0 ? y.x : j % 4 == 1 ? y.y : j % 4 == 2 ? y.z : y.w;
-    const uint32_t a0 = e4m3x2_to_f16x2(wx), a1 = e4m3x2_to_f16x2(wy);
-    const uint32_t a2 = e4m3x2_to_f16x2(wx >> 16), a3 = e4m3x2_to_f16x2(wy >> 16);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const uint2 b = sq[(n * (D / 16) + j) * 32 + lane];
-      mma_f16(s[n], a0, a1, a2, a3, b.x, b.y);
-    }
+// A place on the line.
+struct Place {
+  int b, before;             // sequence, units before it
+  int nblk, len;             // its blocks of units and tokens
+  __device__ __forceinline__ void load(const Cache8Params& p) {
+    nblk = line_blocks(p, b);
+    len = cache_length(p.lengths, b, p.max_blocks);
   }
-}
-
-// Where a unit of the line lies, and the whole line's length. A sequence has
-// at least one block of units, so that rows without keys are written too.
-struct Line {
-  long long total;
-  __device__ __forceinline__ static int blocks(const Cache8Params& p, int b) {
-    return max(1, (cache_length(p.lengths, b, p.max_blocks) + kCacheBlock - 1) / kCacheBlock);
-  }
-  // all lanes of a warp together
-  __device__ __forceinline__ Line(const Cache8Params& p, int per_block, int lane) {
-    long long sum = 0;
-    for (int b = lane; b < p.B; b += 32) sum += blocks(p, b);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    total = sum * per_block;
-  }
-  // parts it is cut into by a grid of `ctas`: none of them empty, so that
-  // every part between a row's first and last has a partial result of it
-  __device__ __forceinline__ long long parts(long long ctas) const { return min(ctas, total); }
-  // sequence of unit u, and the units before that sequence
-  __device__ __forceinline__ static void find(const Cache8Params& p, int per_block, long long u, int lane, int& b,
-                                              long long& before) {
-    long long base = 0;
+  // to the sequence of unit u, by a whole warp
+  __device__ __forceinline__ void find(const Cache8Params& p, int u, int lane) {
+    const int per_block = p.c.Hkv * p.chunks;
+    int base = 0;
+    b = p.B - 1;
+    before = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const int cnt = b0 + lane < p.B ? blocks(p, b0 + lane) : 0;
-      long long incl = cnt;
+      const int cnt = b0 + lane < p.B ? line_blocks(p, b0 + lane) : 0;
+      int incl = cnt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
       }
       const unsigned hit = __ballot_sync(0xffffffffu, u < (base + incl) * per_block);
@@ -200,427 +131,755 @@ struct Line {
         const int src = __ffs(hit) - 1;
         b = b0 + src;
         before = (base + __shfl_sync(0xffffffffu, incl - cnt, src)) * per_block;
-        return;
+        break;
       }
       base += __shfl_sync(0xffffffffu, incl, 31);
     }
-    b = p.B - 1;
-    before = 0;
+    load(p);
+  }
+  // onwards to the sequence of unit u (one that exists)
+  __device__ __forceinline__ void go(const Cache8Params& p, int u) {
+    const int per_block = p.c.Hkv * p.chunks;
+    while (u - before >= nblk * per_block) {
+      before += nblk * per_block;
+      ++b;
+      load(p);
+    }
   }
 };
-__device__ __forceinline__ long long part_begin(long long total, long long i, long long parts) { return total * i / parts; }
-// the part that unit u belongs to
-__device__ __forceinline__ long long part_of(long long total, long long u, long long parts) {
-  return ((u + 1) * parts - 1) / total;
-}
 
-template <int D, int NT>
+template <int D, int R>
 struct Cfg {
-  static constexpr int kCols = 8 * NT;
-  static constexpr int kQBytes = NT * (D / 16) * 32 * 8;
-  static constexpr int kRedBytes = kWarps * kCols * D * 4;
-  static constexpr int kStatBytes = (3 * kWarps + 4) * kCols * 4;
-  static constexpr int kSmem = kQBytes + kRedBytes + kStatBytes;
+  static constexpr int kChunks = D / 128;                  // 128-byte columns of K and V
+  static constexpr int kNS = 2 * R;                        // S^T columns: two terms of Q
+  static constexpr int kNP = (3 * R + 15) / 16 * 16;       // O^T columns: three terms of P
+  static constexpr int kPerSm = D == 256 && R > 8 ? 1 : 2;
+  static constexpr int kTile = 16384 * kChunks;            // K or V of a tile
+  static constexpr int kQBufs = D == 256 ? 1 : 2;
+  static constexpr int kQBytes = kNS * 128 * kChunks;
+  static constexpr int kPBytes = kNP * 128;
+  // references and their changes (4 R), the warps' maxima and sums (8 R), 1 / scale of Q per buffer
+  static constexpr int kStatFloats = 4 * R + 8 * R + 2 * R;
+  static constexpr int kFixed = kQBufs * kQBytes + 2 * kPBytes + kStatFloats * 4 + kInfo * 32 + 512;
+  static constexpr int kBudget = (kPerSm == 2 ? 113 : 227) * 1024;
+  static constexpr int kFit = (kBudget - kFixed) / kTile;
+  static constexpr int kRing = kFit < 8 ? kFit : 8;        // tiles of K or V
+  static constexpr int kLayout = kRing * kTile + kFixed;
+  static constexpr int kSmem = kLayout + 1024 <= kBudget ? kLayout + 1024 : kBudget;   // + what the base's alignment may take
+  static constexpr uint32_t kColO = 2 * kNS;
+  static constexpr int kCols = 2 * kNS + kNP * kChunks;
+  static constexpr uint32_t kTmem = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+  static_assert(kRing >= 3 && kTmem * kPerSm <= 512, "shared memory or TMEM budget");
 };
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads) cache8_fwd_kernel(const Cache8Params p) {
-  using C = Cfg<D, NT>;
-  extern __shared__ __align__(16) uint8_t smem[];
-  uint2* const sq = reinterpret_cast<uint2*>(smem);
-  float* const red = reinterpret_cast<float*>(smem + C::kQBytes);                 // [warp][column][D]
-  float* const st_ml = reinterpret_cast<float*>(smem + C::kQBytes + C::kRedBytes);  // [warp][column]
-  float* const st_l = st_ml + kWarps * C::kCols;
-  float* const st_mo = st_l + kWarps * C::kCols;
-  float* const f_ml = st_mo + kWarps * C::kCols;                                  // [column]
-  float* const f_l = f_ml + C::kCols;
-  float* const f_mo = f_l + C::kCols;
-  float* const qs = f_mo + C::kCols;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int per_block = p.c.Hkv * p.chunks;
+// A row group's share of a part: blocks [blk0, blk1) of (b, h, chunk).
+struct Segment {
+  int b, h, chunk, blk0, blk1, nblk, len, tiles;
+  __device__ __forceinline__ Segment(const Cache8Params& p, Place& at, int u, int u1) {
+    at.go(p, u);
+    b = at.b;
+    nblk = at.nblk;
+    len = at.len;
+    const int row = (u - at.before) / nblk;              // head * chunks + chunk
+    blk0 = u - at.before - row * nblk;
+    blk1 = min(nblk, blk0 + (u1 - u));
+    h = row / p.chunks;
+    chunk = row - h * p.chunks;
+    tiles = (blk1 - blk0 + 1) / 2;
+  }
+};
 
-  const Line line(p, per_block, lane);
-  const long long parts = line.parts(gridDim.x);
-  if (blockIdx.x >= parts) return;
-  const long long u0 = part_begin(line.total, blockIdx.x, parts), u1 = part_begin(line.total, blockIdx.x + 1, parts);
-  int b;
-  long long before;
-  Line::find(p, per_block, u0, lane, b, before);
-  for (long long u = u0; u < u1;) {
-    // ---- segment: blocks [blk0, blk1) of row group (b, h, chunk)
-    const int nblk = Line::blocks(p, b);
-    const int len = cache_length(p.lengths, b, p.max_blocks);
-    const int row = static_cast<int>((u - before) / nblk);                        // head * chunks + chunk
-    const int blk0 = static_cast<int>((u - before) - static_cast<long long>(row) * nblk);
-    const int blk1 = static_cast<int>(min(static_cast<long long>(nblk), blk0 + (u1 - u)));
-    const int h = row / p.chunks, chunk = row - h * p.chunks;
-    const int row0 = chunk * C::kCols;
-    const size_t qrow = (static_cast<size_t>(b) * p.Hq + static_cast<size_t>(h) * p.G) * p.Nq;   // first of the R rows
-    __syncthreads();                                     // the previous segment's shared memory is free
-    stage_queries<D>(sq, qs, p.q + qrow * p.c.d, p.R, row0, C::kCols, p.c.d, warp, lane);
-    __syncthreads();
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads, Cfg<D, R>::kPerSm)
+cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Cache8Params p) {
+  using C = Cfg<D, R>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const gbase = smem_raw + (base - raw);
+  if ((base - raw) + C::kLayout > static_cast<uint32_t>(C::kSmem)) {
+    // the layout needs the dynamic window to start near a 1 KB boundary
+    if (threadIdx.x == 0) atomicOr(p.status, kDevLayout);
+    return;
+  }
+  const uint32_t s_q = base + C::kRing * C::kTile, s_p = s_q + C::kQBufs * C::kQBytes;
+  auto s_kv = [&](int i) { return base + i * C::kTile; };
+  constexpr int kOffStat = C::kRing * C::kTile + C::kQBufs * C::kQBytes + 2 * C::kPBytes;
+  float* const ref_l = reinterpret_cast<float*>(gbase + kOffStat);     // [R] ml, then mo
+  float* const ref_o = ref_l + R;
+  float* const change_l = ref_o + R;                                   // [R] factors of the last change
+  float* const change_o = change_l + R;
+  float* const warp_l = change_o + R;                                  // [4][R] maxima of the warps (ml, mo); sums
+  float* const warp_o = warp_l + 4 * R;
+  float* const q_scale = warp_o + 4 * R;                               // [2][R] power of two the row was divided by
+  volatile float* const info = reinterpret_cast<volatile float*>(q_scale + 2 * R);   // [kInfo][8]: per half K scale, V scale, there
+  const uint32_t bars = base + kOffStat + C::kStatFloats * 4 + kInfo * 32;
+  uint8_t* const gbars = gbase + (bars - base);
+  auto bar_kv_full = [&](int i) { return bars + 8u * i; };             // 8
+  auto bar_kv_empty = [&](int i) { return bars + 64u + 8u * i; };      // 8
+  auto bar_info = [&](int i) { return bars + 128u + 8u * i; };         // kInfo
+  auto bar_s_full = [&](int i) { return bars + 192u + 8u * i; };
+  auto bar_s_free = [&](int i) { return bars + 208u + 8u * i; };
+  auto bar_p_ready = [&](int i) { return bars + 224u + 8u * i; };
+  auto bar_p_empty = [&](int i) { return bars + 240u + 8u * i; };      // P V done
+  auto bar_q_full = [&](int i) { return bars + 256u + 8u * i; };
+  auto bar_q_empty = [&](int i) { return bars + 272u + 8u * i; };
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbars + 296);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(gbars + 300);
+  const uint32_t bar_stall = bars + 304;                               // nothing arrives (timeout test)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    float o[NT][D / 16][4];
-    float ml[NT][2], mo[NT][2], l[NT][2], qsc[NT][2];
-    int lim[NT][2];                                      // keys visible to the column
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[n][j][e] = 0.f;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int col = 8 * n + 2 * t + e;
-        ml[n][e] = mo[n][e] = -INFINITY;
-        l[n][e] = 0.f;
-        qsc[n][e] = qs[col] * p.scale_log2;
-        lim[n][e] = p.causal ? min(len, max(0, len - p.Nq + (row0 + col) % p.Nq + 1)) : len;
-      }
+  // the second kernel may be set up meanwhile; it waits for this one's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int total = line_total(p, lane);
+  const int parts = line_parts(total, gridDim.x);
+  if (static_cast<int>(blockIdx.x) >= parts) return;
+  const int u0 = part_begin(total, blockIdx.x, parts), u1 = part_begin(total, blockIdx.x + 1, parts);
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < C::kRing; ++i) {
+      mbar_init(bar_kv_full(i), 1);
+      mbar_init(bar_kv_empty(i), 1);
     }
-    const int all = p.causal ? max(0, len - p.Nq + 1) : len;     // keys below it are visible to every column
-    const int* const table = p.table + static_cast<long long>(b) * p.max_blocks;
+    for (int i = 0; i < kInfo; ++i) mbar_init(bar_info(i), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_s_full(i), 1);
+      mbar_init(bar_s_free(i), 4);
+      mbar_init(bar_p_ready(i), 128);
+      mbar_init(bar_p_empty(i), 1);
+      mbar_init(bar_q_full(i), 1);
+      mbar_init(bar_q_empty(i), 2);                      // its products done, its scales read
+    }
+    mbar_init(bar_stall, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(tmem_slot), C::kTmem);
+    tmem_relinquish();
+  }
+  Place at;
+  at.find(p, u0, lane);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
 
-    for (int s = blk0 * 4 + warp; s < blk1 * 4; s += kWarps) {
-      const int blk = s >> 2;
-      const int key0 = s * 16;
-      if (key0 >= len) break;
-      const int page = table[blk];
-      if (page < 0 || page >= p.c.num_blocks) continue;          // no such block: its tokens are absent
-      const size_t ph = static_cast<size_t>(page) * p.c.Hkv + h;
-      const size_t off = (ph * kCacheBlock + (s & 3) * 16) * p.c.d;
-      Slice<D> sl;
-      load_slice<D>(sl, p.c.k + off, p.c.v + off, p.c.d, len - key0, lane);
-      const float ks = __ldg(p.c.k_scale + ph), vs = __ldg(p.c.v_scale + ph);
-      const float lvs = log2f(vs);
-      float x[NT][4];
-      scores<D, NT>(x, sl.k, sq, lane);
-      bool grow = false;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[n][e] *= ks * qsc[n][e & 1];
-          if (key0 + 16 > all && key0 + g + 8 * (e >> 1) >= lim[n][e & 1]) x[n][e] = -INFINITY;
-          grow |= x[n][e] > ml[n][e & 1] + 8.f || x[n][e] + lvs > mo[n][e & 1] + 8.f;
-        }
-      }
-      if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(x[n][e], x[n][e + 2]);
-#pragma unroll
-            for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
-            if (mx > ml[n][e]) {
-              l[n][e] *= ex2_approx(ml[n][e] - mx);
-              ml[n][e] = mx;
-            }
-            if (mx + lvs > mo[n][e]) {
-              const float alpha = ex2_approx(mo[n][e] - (mx + lvs));
-              mo[n][e] = mx + lvs;
-#pragma unroll
-              for (int j = 0; j < D / 16; ++j) {
-                o[n][j][e] *= alpha;
-                o[n][j][e + 2] *= alpha;
+  if (warp == 4) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      tma_prefetch_map(&map_k);
+      tma_prefetch_map(&map_v);
+    }
+    int c = 0, tile = 0;                                 // loads and tiles so far
+    bool ok = true;
+    for (int u = u0; u < u1 && ok;) {
+      const Segment s(p, at, u, u1);
+      const int* const table = p.table + static_cast<long long>(s.b) * p.max_blocks;
+      const int held = (s.len + kCacheBlock - 1) / kCacheBlock;        // blocks with tokens (nblk but for an empty sequence)
+      for (int blk = s.blk0; blk < s.blk1 && ok; blk += 32) {
+        // 32 blocks at a time, one per lane
+        const int mine = blk + lane;
+        int page = mine < s.blk1 && mine < held ? table[mine] : -1;
+        if (page >= p.c.num_blocks) page = -1;
+        const long long ph = page >= 0 ? static_cast<long long>(page) * p.c.Hkv + s.h : -1;
+        const float ks = page >= 0 ? __ldg(p.c.k_scale + ph) : 0.f, vs = page >= 0 ? __ldg(p.c.v_scale + ph) : 0.f;
+        const int z = static_cast<int>(ph);
+        for (int i = 0; i < 32 && blk + i < s.blk1 && ok; i += 2, ++tile) {
+          const int za = __shfl_sync(0xffffffffu, z, i), zb = __shfl_sync(0xffffffffu, z, i + 1);
+          const int there = (za >= 0) + (zb >= 0);
+          if (lane == i || lane == i + 1) {
+            volatile float* const dst = info + (tile % kInfo) * 8 + (lane - i) * 4;
+            dst[0] = ks;
+            dst[1] = vs;
+            dst[2] = page >= 0 ? 1.f : 0.f;
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar_info(tile % kInfo));
+            for (int kv = 0; kv < 2 && ok; ++kv, ++c) {
+              const int slot = c % C::kRing;
+              ok = wait(bar_kv_empty(slot), ((c / C::kRing) & 1) ^ 1, abort_flag, p.timeout_ns);
+              if (!ok) break;
+              mbar_arrive_expect_tx(bar_kv_full(slot), there * 8192 * C::kChunks);
+              const CUtensorMap* const m = kv ? &map_v : &map_k;
+              for (int ch = 0; ch < C::kChunks; ++ch) {
+                if (za >= 0) tma_load_3d(s_kv(slot) + ch * 16384, m, bar_kv_full(slot), ch * 128, 0, za);
+                if (zb >= 0) tma_load_3d(s_kv(slot) + ch * 16384 + 8192, m, bar_kv_full(slot), ch * 128, 0, zb);
               }
             }
           }
-      }
-      uint32_t pb[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float po[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float a = ml[n][e & 1], c = mo[n][e & 1];
-          l[n][e & 1] += ex2_approx(x[n][e] - (a == -INFINITY ? 0.f : a));
-          po[e] = ex2_approx(x[n][e] + (lvs - (c == -INFINITY ? 0.f : c) + kShift));
+          ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
         }
-        pb[n][0] = movmatrix(pack_f16x2(po[0], po[1]));
-        pb[n][1] = movmatrix(pack_f16x2(po[2], po[3]));
       }
-#pragma unroll
-      for (int w = 0; w < D / 32; ++w)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t sel = half ? 0x7362u : 0x5140u;
-          const uint32_t x01 = __byte_perm(sl.v[0][w], sl.v[1][w], sel), x89 = __byte_perm(sl.v[2][w], sl.v[3][w], sel);
-          const uint32_t a0 = e4m3x2_to_f16x2(x01), a1 = e4m3x2_to_f16x2(x01 >> 16);
-          const uint32_t a2 = e4m3x2_to_f16x2(x89), a3 = e4m3x2_to_f16x2(x89 >> 16);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16(o[n][2 * w + half], a0, a1, a2, a3, pb[n][0], pb[n][1]);
-        }
+      u += s.blk1 - s.blk0;
     }
-
-    // ---- join the warps
+    __syncwarp();
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ tensor-core issuer
+    if (lane == 0) {
+      const uint32_t id_s = make_idesc(0, 128, C::kNS, 0, 0);          // K tile and Q: both K-major
+      const uint32_t id_o = make_idesc(0, 128, C::kNP, 1, 0);          // V tile: d contiguous, hence MN-major
+      const int steps = (p.c.d + 31) / 32;                             // products over d that are not all zeros
+      int tile = 0, seg = 0;
+      bool ok = !p.test_stall || wait(bar_stall, 0, abort_flag, p.timeout_ns);   // runs out by design
+      // S^T of tile `t`, whose K is load 2 t, with the queries of segment `g`
+      auto scores = [&](int t, int g) {
+        const int slot = (2 * t) % C::kRing;
+        ok = wait(bar_kv_full(slot), ((2 * t) / C::kRing) & 1, abort_flag, p.timeout_ns) &&
+             wait(bar_s_free(t & 1), ((t >> 1) & 1) ^ 1, abort_flag, p.timeout_ns);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t kd = smem_desc_sw128(s_kv(slot), 16, 1024);
+        const uint64_t qd = smem_desc_sw128(s_q + (g % C::kQBufs) * C::kQBytes, 16, 1024);
+        for (int k = 0; k < steps; ++k)
+          mma_fp8_ss(tbase + (t & 1) * C::kNS, desc_add(kd, (k >> 2) * 16384 + (k & 3) * 32),
+                     desc_add(qd, (k >> 2) * (C::kNS * 128) + (k & 3) * 32), id_s, k > 0);
+        mma_commit(bar_s_full(t & 1));
+        mma_commit(bar_kv_empty(slot));
+      };
+      for (int u = u0; u < u1 && ok; ++seg) {
+        const Segment s(p, at, u, u1);
+        ok = wait(bar_q_full(seg % C::kQBufs), (seg / C::kQBufs) & 1, abort_flag, p.timeout_ns);
+        if (!ok) break;
+        scores(tile, seg);
+        for (int j = 0; j < s.tiles && ok; ++j, ++tile) {
+          if (j + 1 < s.tiles) scores(tile + 1, seg);
+          else mma_commit(bar_q_empty(seg % C::kQBufs));
+          if (!ok) break;
+          const int slot = (2 * tile + 1) % C::kRing;
+          ok = wait(bar_kv_full(slot), ((2 * tile + 1) / C::kRing) & 1, abort_flag, p.timeout_ns) &&
+               wait(bar_p_ready(tile & 1), (tile >> 1) & 1, abort_flag, p.timeout_ns);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t pd = smem_desc_sw128(s_p + (tile & 1) * C::kPBytes, 16, 1024);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+          for (int mb = 0; mb < C::kChunks; ++mb) {
+            if (128 * mb >= p.c.d) continue;
+            const uint64_t vd = smem_desc_sw128(s_kv(slot) + mb * 16384, 16384, 1024);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float sum = l[n][e];
-#pragma unroll
-        for (int sh = 4; sh < 32; sh <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, sh);
-        const int col = 8 * n + 2 * t + e;
-        if (g == 0) {
-          st_ml[warp * C::kCols + col] = ml[n][e];
-          st_mo[warp * C::kCols + col] = mo[n][e];
-          st_l[warp * C::kCols + col] = sum;
+            for (int k = 0; k < 4; ++k)
+              mma_fp8_ss(tbase + C::kColO + mb * C::kNP, desc_add(vd, k * 4096), desc_add(pd, k * 32), id_o, j > 0 || k > 0);
+          }
+          mma_commit(bar_p_empty(tile & 1));
+          mma_commit(bar_kv_empty(slot));
         }
-        float* const dst = red + (warp * C::kCols + col) * D;
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w)
-          *reinterpret_cast<float4*>(dst + v_column<D>(g, w)) =
-              make_float4(o[n][2 * w][e], o[n][2 * w][e + 2], o[n][2 * w + 1][e], o[n][2 * w + 1][e + 2]);
-      }
-    __syncthreads();
-    if (tid < C::kCols) {
-      float a = -INFINITY, c = -INFINITY, sum = 0.f;
-      for (int w = 0; w < kWarps; ++w) {
-        a = fmaxf(a, st_ml[w * C::kCols + tid]);
-        c = fmaxf(c, st_mo[w * C::kCols + tid]);
-      }
-      for (int w = 0; w < kWarps; ++w) {
-        const float m = st_ml[w * C::kCols + tid];
-        const float lw = st_l[w * C::kCols + tid];
-        sum += m == -INFINITY ? lw : lw * ex2_approx(m - a);    // (a NaN stays)
-        const float mw = st_mo[w * C::kCols + tid];
-        st_mo[w * C::kCols + tid] = mw == -INFINITY ? 1.f : ex2_approx(mw - c);
-      }
-      f_ml[tid] = a;
-      f_l[tid] = sum;
-      f_mo[tid] = c - kShift;
-    }
-    __syncthreads();
-    const bool whole = blk0 == 0 && blk1 == nblk;
-    const long long slot = (2LL * blockIdx.x + (u == u0 ? 0 : 1)) * C::kCols;
-    for (int i = tid; i < C::kCols * (D / 4); i += kThreads) {
-      const int col = i / (D / 4), c4 = (i - col * (D / 4)) * 4;
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = st_mo[w * C::kCols + col];
-        const float4 y = *reinterpret_cast<const float4*>(red + (w * C::kCols + col) * D + c4);
-        a.x = fmaf(f, y.x, a.x);
-        a.y = fmaf(f, y.y, a.y);
-        a.z = fmaf(f, y.z, a.z);
-        a.w = fmaf(f, y.w, a.w);
-      }
-      if (whole) {
-        if (row0 + col < p.R && c4 < p.c.d) {
-          const float sum = f_l[col];
-          const float f = sum == 0.f ? 0.f : ex2_approx(f_mo[col] - f_ml[col]) / sum;
-          *reinterpret_cast<uint2*>(p.o + (qrow + row0 + col) * p.c.d + c4) =
-              make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
-        }
-      } else {
-        *reinterpret_cast<float4*>(p.part_o + (slot + col) * D + c4) = a;
+        u += s.blk1 - s.blk0;
       }
     }
-    if (tid < C::kCols) {
-      if (whole) {
-        if (row0 + tid < p.R) p.lse[qrow + row0 + tid] = f_l[tid] == 0.f ? -INFINITY : (f_ml[tid] + log2f(f_l[tid])) * kLn2;
-      } else {
-        float* const s3 = p.part_s + (slot + tid) * 3;
-        s3[0] = f_ml[tid];
-        s3[1] = f_l[tid];
-        s3[2] = f_mo[tid];
+    __syncwarp();
+  } else if (warp == 6) {
+    // ------------------------------------------------------------ queries
+    bool ok = true;
+    int seg = 0;
+    for (int u = u0; u < u1 && ok; ++seg) {
+      const Segment s(p, at, u, u1);
+      const int buf = seg % C::kQBufs;
+      const size_t qrow = (static_cast<size_t>(s.b) * p.Hq + static_cast<size_t>(s.h) * p.G) * p.Nq + s.chunk * R;
+      const int rows = min(R, p.R - s.chunk * R);
+      ok = wait(bar_q_empty(buf), ((seg / C::kQBufs) & 1) ^ 1, abort_flag, p.timeout_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t dst = s_q + buf * C::kQBytes;
+      for (int q = 0; q < R; ++q) {
+        float x[C::kChunks][4];
+        float amax = 0.f;
+#pragma unroll
+        for (int ch = 0; ch < C::kChunks; ++ch) {
+          const int col = 128 * ch + 4 * lane;
+          uint2 v = make_uint2(0, 0);
+          if (q < rows && col < p.c.d) v = *reinterpret_cast<const uint2*>(p.q + (qrow + q) * p.c.d + col);
+          x[ch][0] = __uint_as_float(v.x << 16);
+          x[ch][1] = __uint_as_float(v.x & 0xFFFF0000u);
+          x[ch][2] = __uint_as_float(v.y << 16);
+          x[ch][3] = __uint_as_float(v.y & 0xFFFF0000u);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(x[ch][e]));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        // exponent that brings the largest to [128, 256); bounded so that both powers are normal.
+        // An infinity among them becomes NaN, as its logits are.
+        const int e2 = amax > 0.f ? max(-100, min(100, static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 7)) : 0;
+        const float down = amax < INFINITY ? __uint_as_float(static_cast<uint32_t>(127 - e2) << 23) : NAN;
+        if (lane == 0) q_scale[buf * R + q] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+#pragma unroll
+        for (int ch = 0; ch < C::kChunks; ++ch) {
+          uint32_t hi = 0, lo = 0;
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const float a = x[ch][e] * down, b = x[ch][e + 1] * down;
+            const uint32_t c0 = pack_e4m3x2(a, b);
+            const float2 f = e4m3x2_to_float2(c0);
+            hi |= c0 << (8 * e);
+            lo |= pack_e4m3x2((a - f.x) * 16.f, (b - f.y) * 16.f) << (8 * e);
+          }
+          // row q (first terms) and row R + q (second) of the operand, bytes 4 lane .. + 3
+          const uint32_t box = dst + ch * (C::kNS * 128);
+          asm volatile("st.shared.b32 [%0], %1;" :: "r"(swz128(box, q, lane >> 2) + (lane & 3) * 4), "r"(hi) : "memory");
+          asm volatile("st.shared.b32 [%0], %1;" :: "r"(swz128(box, R + q, lane >> 2) + (lane & 3) * 4), "r"(lo) : "memory");
+        }
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_q_full(buf));
+      u += s.blk1 - s.blk0;
     }
-    u += blk1 - blk0;
-    if (u - before >= static_cast<long long>(nblk) * per_block) {                 // the next sequence
-      before += static_cast<long long>(nblk) * per_block;
-      ++b;
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int row = threadIdx.x;                         // token of the tile; column of d in the epilogue
+    const int half = row >> 6;
+    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    bool ok = true;
+    int tile = 0, seg = 0;
+    for (int u = u0; u < u1; ++seg) {
+      const Segment s(p, at, u, u1);
+      const int row0 = s.chunk * R;
+      const int all = p.causal ? max(0, s.len - p.Nq + 1) : s.len;     // keys below it are visible to every row
+      float l[R];
+#pragma unroll
+      for (int q = 0; q < R; ++q) l[q] = 0.f;
+      if (row < R) ref_l[row] = ref_o[row] = -INFINITY;
+      named_bar_sync(1, 128);
+      // the queries' scales are there when their operand is
+      if (ok) ok = wait(bar_q_full(seg % C::kQBufs), (seg / C::kQBufs) & 1, abort_flag, p.timeout_ns);
+      const float* const qs = q_scale + (seg % C::kQBufs) * R;
+      for (int j = 0; j < s.tiles; ++j, ++tile) {
+        const int buf = tile & 1;
+        if (ok)
+          ok = wait(bar_info(tile % kInfo), (tile / kInfo) & 1, abort_flag, p.timeout_ns) &&
+               wait(bar_s_full(buf), (tile >> 1) & 1, abort_flag, p.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        const float ks = info[(tile % kInfo) * 8 + half * 4] * p.scale_log2;
+        const float vs = info[(tile % kInfo) * 8 + half * 4 + 1];
+        const int blk = s.blk0 + 2 * j + half;
+        const int key = blk * kCacheBlock + (row & 63);
+        // tokens past the length, of no block, or of another CTA's block are absent
+        const bool there = blk < s.blk1 && key < s.len && info[(tile % kInfo) * 8 + half * 4 + 2] != 0.f;
+        const float lvs = log2f(vs);
+        float x[R];
+        bool grow = !ok;
+        if (ok) {
+          tc_fence_after();
+#pragma unroll
+          for (int q0 = 0; q0 < R; q0 += 8) {
+            // columns q0 .. + 7 of both terms
+            uint32_t hi[16], lo[16];
+            if constexpr (R == 8) {
+              tmem_ld_x16(tbase + lane_off + buf * C::kNS, hi);
+              tmem_wait_ld();
+              reg_fence_x16(hi);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) lo[e] = hi[8 + e];
+            } else if (q0 % 16 == 0) {
+              tmem_ld_x16(tbase + lane_off + buf * C::kNS + q0, hi);
+              tmem_ld_x16(tbase + lane_off + buf * C::kNS + R + q0, lo);
+              tmem_wait_ld();
+              reg_fence_x16(hi);
+              reg_fence_x16(lo);
+#pragma unroll
+              for (int e = 8; e < 16; ++e)
+                x[(q0 + e) % R] = fmaf(__uint_as_float(lo[e]), 0.0625f, __uint_as_float(hi[e])) * (ks * qs[(q0 + e) % R]);
+            } else {
+              continue;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              x[q0 + e] = fmaf(__uint_as_float(lo[e]), 0.0625f, __uint_as_float(hi[e])) * (ks * qs[q0 + e]);
+          }
+          tc_fence_before();
+          if (!there || key >= all) {
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+              // row row0 + q is query (row0 + q) % Nq of its head, and sees the keys up to its own position
+              const bool seen = there && (!p.causal || key <= s.len - p.Nq + (row0 + q) % p.Nq);
+              x[q] = seen ? x[q] : -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < R; ++q) grow |= x[q] > ref_l[q] + kTrail || x[q] + lvs > ref_o[q] + kTrail;
+        }
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(bar_s_free(buf));
+        if (meet_or(grow)) {
+          if (meet_or(!ok)) {                            // a wait ran out somewhere: all leave together
+            ok = false;
+            break;
+          }
+          // the tile's maxima, as integers of the floats' order
+#pragma unroll
+          for (int q = 0; q < R; ++q) {
+            auto most = [&](float v) {
+              const uint32_t b = __float_as_uint(v);
+              // (a NaN takes no part: it would raise the reference for good)
+              const uint32_t key_of = v != v ? 0u : (b & 0x80000000u) ? ~b : b | 0x80000000u;
+              const uint32_t top = __reduce_max_sync(0xffffffffu, key_of);
+              return top == 0u ? -INFINITY : __uint_as_float((top & 0x80000000u) ? top & 0x7FFFFFFFu : ~top);
+            };
+            const float a = most(x[q]), b = most(x[q] + lvs);
+            if (lane == 0) {
+              warp_l[warp * R + q] = a;
+              warp_o[warp * R + q] = b;
+            }
+          }
+          named_bar_sync(1, 128);
+          if (row < R) {
+            auto raise = [&](float* ref, const float* w, float* change) {
+              const float old = ref[row];
+              const float now = fmaxf(old, fmaxf(fmaxf(w[row], w[R + row]), fmaxf(w[2 * R + row], w[3 * R + row])));
+              ref[row] = now;
+              change[row] = now > old ? ex2_approx(old - now) : 1.f;
+            };
+            raise(ref_l, warp_l, change_l);
+            raise(ref_o, warp_o, change_o);
+          }
+          named_bar_sync(1, 128);
+#pragma unroll
+          for (int q = 0; q < R; ++q) l[q] *= change_l[q];
+          if (j > 0) {
+            // O <- O * change, once the P V before has completed
+            ok = wait(bar_p_empty(buf ^ 1), ((tile - 1) >> 1) & 1, abort_flag, p.timeout_ns);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+              tc_fence_after();
+#pragma unroll
+              for (int mb = 0; mb < C::kChunks; ++mb)
+#pragma unroll
+                for (int c0 = 0; c0 < 3 * R; c0 += 8) {
+                  uint32_t o[8];
+                  const uint32_t col = tbase + lane_off + C::kColO + mb * C::kNP + c0;
+                  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                               : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]) : "r"(col));
+                  tmem_wait_ld();
+                  asm volatile("" : "+r"(o[0]), "+r"(o[1]), "+r"(o[2]), "+r"(o[3]), "+r"(o[4]), "+r"(o[5]), "+r"(o[6]), "+r"(o[7]) :: "memory");
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * change_o[(c0 + e) % R]);
+                  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                               :: "r"(col), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]) : "memory");
+                }
+              tmem_wait_st();
+              tc_fence_before();
+            }
+          }
+        }
+        if (p.scores != nullptr && blk < s.blk1) {
+          // for the weights: this token's scores, -inf where hidden or absent
+          float4* const keep = reinterpret_cast<float4*>(p.scores + (static_cast<size_t>(u + 2 * j + half) * kCacheBlock + (row & 63)) * R);
+#pragma unroll
+          for (int q = 0; q < R; q += 4)
+            if (row0 + q < p.R) keep[q / 4] = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
+        }
+        // the P V that read this buffer two tiles ago has completed
+        if (ok) ok = wait(bar_p_empty(buf), ((tile >> 1) & 1) ^ 1, abort_flag, p.timeout_ns);
+        const uint32_t dst = s_p + buf * C::kPBytes + (row & 15);
+        const int unit = row >> 4;
+#pragma unroll
+        for (int q = 0; q < R; q += 2) {
+          float y[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float a = ref_l[q + e], c = ref_o[q + e];
+            l[q + e] += ex2_approx(x[q + e] - (a == -INFINITY ? 0.f : a));
+            y[e] = ex2_approx(x[q + e] + (lvs - (c == -INFINITY ? 0.f : c) + kShift));
+          }
+          if (!there) y[0] = y[1] = 0.f;                 // (no block: no scale either)
+          const uint32_t c0 = pack_e4m3x2(y[0], y[1]);
+          const float2 f0 = e4m3x2_to_float2(c0);
+          const float r0 = (y[0] - f0.x) * 16.f, r1 = (y[1] - f0.y) * 16.f;
+          const uint32_t c1 = pack_e4m3x2(r0, r1);
+          const float2 f1 = e4m3x2_to_float2(c1);
+          const uint32_t c2 = pack_e4m3x2((r0 - f1.x) * 16.f, (r1 - f1.y) * 16.f);
+          const uint32_t codes[3] = {c0, c1, c2};
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            // rows k R + q and k R + q + 1 of the operand (R a multiple of 8), byte `row`
+            store_byte(dst + (k * R + q) * 128 + ((unit ^ (q & 7)) << 4), codes[k]);
+            store_byte(dst + (k * R + q + 1) * 128 + ((unit ^ ((q + 1) & 7)) << 4), codes[k] >> 8);
+          }
+        }
+        if (!there) {
+          // this token's V may be anything; P is 0, but 0 x NaN is not: clear it
+          const int slot = (2 * tile + 1) % C::kRing;
+          if (ok) ok = wait(bar_kv_full(slot), ((2 * tile + 1) / C::kRing) & 1, abort_flag, p.timeout_ns);
+#pragma unroll
+          for (int ch = 0; ch < C::kChunks; ++ch)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (ok)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" :: "r"(s_kv(slot) + ch * 16384 + row * 128 + i * 16), "r"(0) : "memory");
+        }
+        fence_proxy_async_smem();
+        if (ok) mbar_arrive(bar_p_ready(buf));
+      }
+      // ---------------------------------------------------------- the row group's result
+      if (meet_or(!ok)) break;
+      const int last = tile - 1;
+      ok = wait(bar_p_empty(last & 1), (last >> 1) & 1, abort_flag, p.timeout_ns);
+      // the sums over the tile's 128 tokens
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        float sum = l[q];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) warp_l[warp * R + q] = sum;
+      }
+      if (meet_or(!ok)) break;
+      tc_fence_after();
+      const bool whole = s.blk0 == 0 && s.blk1 == s.nblk;
+      const long long slot0 = (2LL * blockIdx.x + (u == u0 ? 0 : 1)) * R;
+      const size_t qrow = (static_cast<size_t>(s.b) * p.Hq + static_cast<size_t>(s.h) * p.G) * p.Nq + row0;
+      const int rows = min(R, p.R - row0);
+#pragma unroll
+      for (int mb = 0; mb < C::kChunks; ++mb)
+#pragma unroll
+        for (int q0 = 0; q0 < R; q0 += 8) {
+          uint32_t o[3][8];
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                         : "=r"(o[k][0]), "=r"(o[k][1]), "=r"(o[k][2]), "=r"(o[k][3]), "=r"(o[k][4]), "=r"(o[k][5]), "=r"(o[k][6]), "=r"(o[k][7])
+                         : "r"(tbase + lane_off + C::kColO + mb * C::kNP + k * R + q0));
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            asm volatile("" : "+r"(o[k][0]), "+r"(o[k][1]), "+r"(o[k][2]), "+r"(o[k][3]), "+r"(o[k][4]), "+r"(o[k][5]), "+r"(o[k][6]), "+r"(o[k][7]) :: "memory");
+          const int col = 128 * mb + row;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int q = q0 + e;
+            const float v = __uint_as_float(o[0][e]) + (__uint_as_float(o[1][e]) + __uint_as_float(o[2][e]) * 0.0625f) * 0.0625f;
+            if (whole) {
+              const float sum = warp_l[q] + warp_l[R + q] + warp_l[2 * R + q] + warp_l[3 * R + q];
+              const float f = sum == 0.f ? 0.f : ex2_approx(ref_o[q] - kShift - ref_l[q]) / sum;
+              if (q < rows && col < p.c.d) p.o[(qrow + q) * p.c.d + col] = __float2bfloat16_rn(sum == 0.f ? 0.f : v * f);
+            } else {
+              p.part_o[(slot0 + q) * D + col] = v;
+            }
+          }
+        }
+      tc_fence_before();
+      if (row < R) {
+        const float sum = warp_l[row] + warp_l[R + row] + warp_l[2 * R + row] + warp_l[3 * R + row];
+        if (whole) {
+          if (row < rows) p.lse[qrow + row] = sum == 0.f ? -INFINITY : (ref_l[row] + log2f(sum)) * kLn2;
+        } else {
+          float* const s3 = p.part_s + (slot0 + row) * 3;
+          s3[0] = ref_l[row];
+          s3[1] = sum;
+          s3[2] = ref_o[row] - kShift;
+        }
+      }
+      named_bar_sync(1, 128);                            // references and sums are free for the next row group
+      if (row == 0) mbar_arrive(bar_q_empty(seg % C::kQBufs));
+      u += s.blk1 - s.blk0;
     }
   }
+
+  // ---------------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {
+    if (threadIdx.x == 0) atomicOr(p.status, kDevTimeout);
+    abort_grace_period();
+  }
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tbase, C::kTmem);
 }
 
-// Joins the rows whose units went to several CTAs: one CTA per row.
+// ------------------------------------------------------------------ second kernel
+// Joins the rows whose units went to several parts (one warp per row), and adds
+// the weights: weight_j = decay weight_j + sum over the group's rows of
+// 2^(s_rj - LSE_r), from the scores that the first kernel kept (the
+// probabilities need the whole row's LSE; reading K again instead costs d
+// bytes per token and head against 8 per row, mostly from L2).
+constexpr int kFinishWarps = 4;
+constexpr int kWeightCtas = 2432;        // 16 per SM: all its threads, waiting for memory most of the time
+
+// Where a row's partial results lie.
+struct RowParts {
+  int c0, c1, first, cols, r;                            // parts c0 .. c1; in c0 it is that part's first row or not
+  __device__ __forceinline__ RowParts(int total, int parts, int ua, int nblk, int cols_, int r_) : cols(cols_), r(r_) {
+    c0 = part_of(total, ua, parts);
+    c1 = part_of(total, ua + nblk - 1, parts);
+    first = part_begin(total, c0, parts) == ua ? 0 : 1;
+  }
+  __device__ __forceinline__ long long slot(int c) const { return (2LL * c + (c == c0 ? first : 0)) * cols + r; }
+};
+
 template <int D>
-__global__ void __launch_bounds__(D / 4 < 32 ? 32 : D / 4) cache8_join_kernel(const Cache8Params p, int cols, int ctas) {
-  const int lane = threadIdx.x & 31;
-  const int b = blockIdx.y, h = blockIdx.x / p.R, r = blockIdx.x - h * p.R;
+__global__ void __launch_bounds__(kFinishWarps * 32) cache8_finish_kernel(const Cache8Params p, int cols, int ctas, int join_ctas) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int total = line_total(p, lane);
+  const int parts = line_parts(total, ctas);
   const int per_block = p.c.Hkv * p.chunks;
-  const Line line(p, per_block, lane);
-  const long long parts = line.parts(ctas);
-  long long before = 0;
-  for (int i = lane; i < b; i += 32) before += Line::blocks(p, i);
+  if (static_cast<int>(blockIdx.x) < join_ctas) {
+    // ---- join: row R0 of the B * Hkv * R
+    const long long row = static_cast<long long>(blockIdx.x) * kFinishWarps + warp;
+    const int per_seq = p.c.Hkv * p.R;
+    if (row >= static_cast<long long>(p.B) * per_seq) return;
+    const int b = static_cast<int>(row / per_seq), hr = static_cast<int>(row - static_cast<long long>(b) * per_seq);
+    const int h = hr / p.R, r = hr - h * p.R;
+    int before = 0;
+    for (int i = lane; i < b; i += 32) before += line_blocks(p, i);
+    before = __reduce_add_sync(0xffffffffu, before) * per_block;
+    const int nblk = line_blocks(p, b);
+    const RowParts rp(total, parts, before + (h * p.chunks + r / cols) * nblk, nblk, cols, r % cols);
+    if (rp.c0 == rp.c1) return;                          // written whole
+    float ml = -INFINITY, mo = -INFINITY;
+    for (int c = rp.c0 + lane; c <= rp.c1; c += 32) {
+      const float* const s3 = p.part_s + rp.slot(c) * 3;
+      ml = fmaxf(ml, s3[0]);
+      mo = fmaxf(mo, s3[2]);
+    }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-  const int nblk = Line::blocks(p, b), chunk = r / cols;
-  const long long ua = before * per_block + static_cast<long long>(h * p.chunks + chunk) * nblk;
-  const long long c0 = part_of(line.total, ua, parts), c1 = part_of(line.total, ua + nblk - 1, parts);
-  if (c0 == c1) return;                                       // written whole
-  const int first = part_begin(line.total, c0, parts) == ua ? 0 : 1;
-  float ml = -INFINITY, mo = -INFINITY;
-  for (long long c = c0; c <= c1; ++c) {
-    const float* const s3 = p.part_s + ((2 * c + (c == c0 ? first : 0)) * cols + r % cols) * 3;
-    ml = fmaxf(ml, s3[0]);
-    mo = fmaxf(mo, s3[2]);
-  }
-  float sum = 0.f;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int c4 = threadIdx.x * 4;
-  for (long long c = c0; c <= c1; ++c) {
-    const long long slot = (2 * c + (c == c0 ? first : 0)) * cols + r % cols;
-    const float* const s3 = p.part_s + slot * 3;
-    sum += s3[0] == -INFINITY ? s3[1] : s3[1] * ex2_approx(s3[0] - ml);
-    const float f = s3[2] == -INFINITY ? 1.f : ex2_approx(s3[2] - mo);   // (no term yet: O is 0, or a NaN that stays)
-    if (c4 < D) {
-      const float4 y = *reinterpret_cast<const float4*>(p.part_o + slot * D + c4);
-      a.x = fmaf(f, y.x, a.x);
-      a.y = fmaf(f, y.y, a.y);
-      a.z = fmaf(f, y.z, a.z);
-      a.w = fmaf(f, y.w, a.w);
+    for (int o = 16; o > 0; o >>= 1) {
+      ml = fmaxf(ml, __shfl_xor_sync(0xffffffffu, ml, o));
+      mo = fmaxf(mo, __shfl_xor_sync(0xffffffffu, mo, o));
     }
+    constexpr int kPer = D / 128;                        // float4 per lane
+    float sum = 0.f;
+    float4 a[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int c = rp.c0; c <= rp.c1; ++c) {
+      const long long slot = rp.slot(c);
+      const float* const s3 = p.part_s + slot * 3;
+      sum += s3[0] == -INFINITY ? s3[1] : s3[1] * ex2_approx(s3[0] - ml);
+      const float f = s3[2] == -INFINITY ? 1.f : ex2_approx(s3[2] - mo);   // (no term yet: O is 0, or a NaN that stays)
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        {
+          const float4 y = *reinterpret_cast<const float4*>(p.part_o + slot * D + 128 * i + 4 * lane);
+          a[i].x = fmaf(f, y.x, a[i].x);
+          a[i].y = fmaf(f, y.y, a[i].y);
+          a[i].z = fmaf(f, y.z, a[i].z);
+          a[i].w = fmaf(f, y.w, a[i].w);
+        }
+    }
+    const size_t at = (static_cast<size_t>(b) * p.Hq + static_cast<size_t>(h) * p.G) * p.Nq + r;
+    const float f = sum == 0.f ? 0.f : ex2_approx(mo - ml) / sum;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (128 * i + 4 * lane < p.c.d)
+        *reinterpret_cast<uint2*>(p.o + at * p.c.d + 128 * i + 4 * lane) =
+            make_uint2(pack_bf16x2(a[i].x * f, a[i].y * f), pack_bf16x2(a[i].z * f, a[i].w * f));
+    if (lane == 0) p.lse[at] = sum == 0.f ? -INFINITY : (ml + log2f(sum)) * kLn2;
+    return;
   }
-  const size_t row = (static_cast<size_t>(b) * p.Hq + static_cast<size_t>(h) * p.G) * p.Nq + r;
-  const float f = sum == 0.f ? 0.f : ex2_approx(mo - ml) / sum;
-  if (c4 < p.c.d)
-    *reinterpret_cast<uint2*>(p.o + row * p.c.d + c4) = make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
-  if (threadIdx.x == 0) p.lse[row] = sum == 0.f ? -INFINITY : (ml + log2f(sum)) * kLn2;
-}
-
-// ------------------------------------------------------------------ weights
-// weight_j = decay weight_j + sum over the group's rows of exp(s_rj - LSE_r):
-// the scores once more from K (the probabilities need the whole row's LSE).
-// Units are (sequence, KV head, block).
-template <int D>
-__global__ void __launch_bounds__(kThreads) cache8_weight_kernel(const Cache8Params p) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  const int ntiles = (p.R + 7) / 8;
-  uint2* const sq = reinterpret_cast<uint2*>(smem);
-  float* const qs = reinterpret_cast<float*>(smem + ntiles * (D / 16) * 32 * 8);   // [columns]
-  float* const lse2 = qs + ntiles * 8;                                             // [columns], +inf past R
-  int* const lim = reinterpret_cast<int*>(lse2 + ntiles * 8);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int per_block = p.c.Hkv;
-  const Line line(p, per_block, lane);
-  const long long parts = line.parts(gridDim.x);
-  if (blockIdx.x >= parts) return;
-  const long long u0 = part_begin(line.total, blockIdx.x, parts), u1 = part_begin(line.total, blockIdx.x + 1, parts);
-  int b;
-  long long before;
-  Line::find(p, per_block, u0, lane, b, before);
-  for (long long u = u0; u < u1;) {
-    const int nblk = Line::blocks(p, b);
-    const int len = cache_length(p.lengths, b, p.max_blocks);
-    const int h = static_cast<int>((u - before) / nblk);
-    const int blk0 = static_cast<int>((u - before) - static_cast<long long>(h) * nblk);
-    const int blk1 = static_cast<int>(min(static_cast<long long>(nblk), blk0 + (u1 - u)));
-    const size_t qrow = (static_cast<size_t>(b) * p.Hq + static_cast<size_t>(h) * p.G) * p.Nq;
+  // ---- weights: an equal share of the (sequence, KV head, block), two at a time,
+  // one thread per token
+  __shared__ float lse2[kCache8MaxRows];
+  const int all = total / p.chunks;                      // (sequence, KV head, block)
+  const int share = static_cast<int>(blockIdx.x) - join_ctas, shares = static_cast<int>(gridDim.x) - join_ctas;
+  const int w0 = part_begin(all, share, shares), w1 = part_begin(all, share + 1, shares);
+  if (w0 >= w1) return;
+  Place at;
+  at.find(p, w0 * p.chunks, lane);                       // (sequences have `chunks` times as many units)
+  const int half = threadIdx.x >> 6, slot = threadIdx.x & 63;
+  for (int u = w0; u < w1;) {
+    // the blocks of one head from u on
+    at.go(p, u * p.chunks);
+    const int in_seq = u - at.before / p.chunks;
+    const int h = in_seq / at.nblk, blk0 = in_seq - h * at.nblk;
+    const int blk1 = min(at.nblk, blk0 + (w1 - u));
     __syncthreads();
-    stage_queries<D>(sq, qs, p.q + qrow * p.c.d, p.R, 0, ntiles * 8, p.c.d, warp, lane);
-    for (int col = tid; col < ntiles * 8; col += kThreads) {
-      lse2[col] = col < p.R ? p.lse[qrow + col] * kLog2e : INFINITY;
-      lim[col] = p.causal ? min(len, max(0, len - p.Nq + col % p.Nq + 1)) : len;
+    for (int r = threadIdx.x; r < p.R; r += kFinishWarps * 32) {
+      // a row in several parts is being joined by another CTA: its LSE from the parts, as there
+      const RowParts rp(total, parts, at.before + (h * p.chunks + r / cols) * at.nblk, at.nblk, cols, r % cols);
+      float v;
+      if (rp.c0 == rp.c1) {
+        v = p.lse[(static_cast<size_t>(at.b) * p.Hq + static_cast<size_t>(h) * p.G) * p.Nq + r] * kLog2e;
+      } else {
+        float ml = -INFINITY, sum = 0.f;
+        for (int c = rp.c0; c <= rp.c1; ++c) ml = fmaxf(ml, p.part_s[rp.slot(c) * 3]);
+        for (int c = rp.c0; c <= rp.c1; ++c) {
+          const float* const s3 = p.part_s + rp.slot(c) * 3;
+          sum += s3[0] == -INFINITY ? s3[1] : s3[1] * ex2_approx(s3[0] - ml);
+        }
+        v = sum == 0.f ? -INFINITY : ml + log2f(sum);
+      }
+      lse2[r] = v == -INFINITY ? INFINITY : v;           // a row that sees no key adds nothing
     }
     __syncthreads();
-    const int* const table = p.table + static_cast<long long>(b) * p.max_blocks;
-    for (int s = blk0 * 4 + warp; s < blk1 * 4; s += kWarps) {
-      const int key0 = s * 16;
-      if (key0 >= len) break;
-      const int page = table[s >> 2];
+    for (int blk = blk0 + half; blk < blk1; blk += 2) {
+      if (blk * kCacheBlock + slot >= at.len) continue;
+      const int page = p.table[static_cast<long long>(at.b) * p.max_blocks + blk];
       if (page < 0 || page >= p.c.num_blocks) continue;
-      const size_t ph = static_cast<size_t>(page) * p.c.Hkv + h;
-      const uint8_t* const k = p.c.k + (ph * kCacheBlock + (s & 3) * 16) * p.c.d;
-      uint4 kk[2][D / 64];
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          const int row = g + 8 * r, col = 64 * c + 16 * t;
-          kk[r][c] = (key0 + row < len && col < p.c.d) ? __ldg(reinterpret_cast<const uint4*>(k + row * p.c.d + col))
-                                                       : make_uint4(0, 0, 0, 0);
-        }
-      const float ks = __ldg(p.c.k_scale + ph) * p.scale_log2;
-      float w0 = 0.f, w1 = 0.f;                               // keys key0 + g, key0 + g + 8
-      for (int n = 0; n < ntiles; ++n) {
-        float x[1][4];
-        scores<D, 1>(x, kk, sq + n * (D / 16) * 32, lane);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int col = 8 * n + 2 * t + (e & 1);
-          const int key = key0 + g + 8 * (e >> 1);
-          const float l2 = lse2[col];
-          // a row that sees no key has LSE -inf and adds nothing
-          const float pr = key < lim[col] && l2 != -INFINITY ? ex2_approx(x[0][e] * (ks * qs[col]) - l2) : 0.f;
-          if (e < 2) w0 += pr;
-          else w1 += pr;
+      float sum = 0.f;
+      for (int chunk = 0; chunk < p.chunks; ++chunk) {
+        const size_t unit = static_cast<size_t>(at.before + (h * p.chunks + chunk) * at.nblk + blk);
+        const float4* const x = reinterpret_cast<const float4*>(p.scores + (unit * kCacheBlock + slot) * cols);
+        const int rows = min(cols, p.R - chunk * cols);
+        for (int q = 0; q < rows; q += 4) {
+          const float4 y = x[q / 4];
+          const float* const l = lse2 + chunk * cols + q;
+          sum += ex2_approx(y.x - l[0]);
+          if (q + 1 < rows) sum += ex2_approx(y.y - l[1]);
+          if (q + 2 < rows) sum += ex2_approx(y.z - l[2]);
+          if (q + 3 < rows) sum += ex2_approx(y.w - l[3]);
         }
       }
-#pragma unroll
-      for (int sh = 1; sh < 4; sh <<= 1) {
-        w0 += __shfl_xor_sync(0xffffffffu, w0, sh);
-        w1 += __shfl_xor_sync(0xffffffffu, w1, sh);
-      }
-      if (t < 2) {
-        const int key = key0 + g + 8 * t;
-        float* const dst = p.c.weight + ph * kCacheBlock + (s & 3) * 16 + g + 8 * t;
-        // (a decay of 0 drops what was there, a NaN too)
-        if (key < len) *dst = (p.decay == 0.f ? 0.f : p.decay * *dst) + (t ? w1 : w0);
-      }
+      float* const dst = p.c.weight + (static_cast<size_t>(page) * p.c.Hkv + h) * kCacheBlock + slot;
+      // (a decay of 0 drops what was there, a NaN too)
+      *dst = (p.decay == 0.f ? 0.f : p.decay * *dst) + sum;
     }
     u += blk1 - blk0;
-    if (u - before >= static_cast<long long>(nblk) * per_block) {
-      before += static_cast<long long>(nblk) * per_block;
-      ++b;
-    }
   }
 }
 
-template <int D, int NT>
-cudaError_t launch_fwd(const Cache8Params& p, int parts, cudaStream_t stream) {
+template <int D, int R>
+cudaError_t launch_fwd(const CUtensorMap& mk, const CUtensorMap& mv, const Cache8Params& p, int parts, cudaStream_t stream) {
   static PerDeviceOnce attr;
   const cudaError_t e = attr.run([] {
-    return cudaFuncSetAttribute(cache8_fwd_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, NT>::kSmem);
+    return cudaFuncSetAttribute(cache8_fwd_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, R>::kSmem);
   });
   if (e != cudaSuccess) return e;
-  cache8_fwd_kernel<D, NT><<<parts, kThreads, Cfg<D, NT>::kSmem, stream>>>(p);
+  cache8_fwd_kernel<D, R><<<parts, kThreads, Cfg<D, R>::kSmem, stream>>>(mk, mv, p);
   return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t launch_all(const Cache8Params& p, int parts, cudaStream_t stream) {
+cudaError_t launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const Cache8Params& p, int parts, cudaStream_t stream) {
   const int cols = cache8_columns(p.c.d, p.R);
   cudaError_t e = cudaErrorInvalidValue;
-  if (cols == 8) e = launch_fwd<D, 1>(p, parts, stream);
-  else if (cols == 16) e = launch_fwd<D, 2>(p, parts, stream);
-  else if constexpr (D <= 128) e = launch_fwd<D, 4>(p, parts, stream);
+  if (cols == 8) e = launch_fwd<D, 8>(mk, mv, p, parts, stream);
+  else if (cols == 16) e = launch_fwd<D, 16>(mk, mv, p, parts, stream);
+  else if constexpr (D == 128) e = launch_fwd<D, 32>(mk, mv, p, parts, stream);
   if (e != cudaSuccess) return e;
-  if (parts > 1) {
-    cache8_join_kernel<D><<<dim3(p.c.Hkv * p.R, p.B), D / 4 < 32 ? 32 : D / 4, 0, stream>>>(p, cols, parts);
-    e = cudaGetLastError();
-  }
-  if (e != cudaSuccess || !p.add_weights) return e;
-  static PerDeviceOnce attr;
-  e = attr.run([] {
-    return cudaFuncSetAttribute(cache8_weight_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (kCache8MaxRows / 8) * (D / 16) * 256 + kCache8MaxRows * 12);
-  });
-  if (e != cudaSuccess) return e;
-  const int ntiles = (p.R + 7) / 8;
-  const long long units = static_cast<long long>(p.B) * p.c.Hkv * p.max_blocks;
-  const int grid = static_cast<int>(units < kCache8Parts ? units : kCache8Parts);
-  cache8_weight_kernel<D><<<grid, kThreads, ntiles * ((D / 16) * 256 + 96), stream>>>(p);
-  return cudaGetLastError();
+  const long long rows = static_cast<long long>(p.B) * p.c.Hkv * p.R;
+  const int join = parts > 1 ? static_cast<int>((rows + kFinishWarps - 1) / kFinishWarps) : 0;
+  const long long blocks = static_cast<long long>(p.B) * p.c.Hkv * p.max_blocks;
+  const int weigh = p.add_weights ? static_cast<int>(blocks < kWeightCtas ? blocks : kWeightCtas) : 0;
+  if (join + weigh == 0) return cudaSuccess;
+  // launched while the first kernel runs: its start is hidden behind it
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(join + weigh);
+  cfg.blockDim = dim3(kFinishWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache8_finish_kernel<D>, p, cols, parts, join);
 }
 
 }  // namespace
 
 int cache8_columns(int d, int R) { return R <= 8 ? 8 : R <= 16 || d > 128 ? 16 : 32; }
 
-int cache8_parts(int B, int Hkv, int chunks, int max_blocks) {
+int cache8_parts(int B, int Hkv, int d, int R, int max_blocks) {
+  const int cols = cache8_columns(d, R), chunks = (R + cols - 1) / cols;
   const long long units = static_cast<long long>(B) * Hkv * chunks * max_blocks;
-  return static_cast<int>(units < kCache8Parts ? units : kCache8Parts);
+  const int most = kCache8Sms * (d > 128 && cols > 8 ? 1 : 2);         // Cfg::kPerSm CTAs per SM
+  return static_cast<int>(units < most ? units : most);
 }
 
-cudaError_t launch_cache8_fwd(const Cache8Params& p, cudaStream_t stream) {
-  const int parts = cache8_parts(p.B, p.c.Hkv, p.chunks, p.max_blocks);
-  if (p.c.d <= 64) return launch_all<64>(p, parts, stream);
-  if (p.c.d <= 128) return launch_all<128>(p, parts, stream);
-  return launch_all<256>(p, parts, stream);
+cudaError_t launch_cache8_fwd(const CUtensorMap& mk, const CUtensorMap& mv, const Cache8Params& p, cudaStream_t stream) {
+  const int parts = cache8_parts(p.B, p.c.Hkv, p.c.d, p.R, p.max_blocks);
+  return p.c.d <= 128 ? launch_all<128>(mk, mv, p, parts, stream) : launch_all<256>(mk, mv, p, parts, stream);
 }
 
 }  // namespace fa

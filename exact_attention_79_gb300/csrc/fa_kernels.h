@@ -166,8 +166,12 @@ struct Cache8Params {
   int chunks;                      // row chunks of cache8_columns() rows
   int causal, add_weights;
   float scale_log2, decay;
+  unsigned* status;                // device status word
+  unsigned long long timeout_ns;   // bound on every wait inside the kernel
+  int test_stall;                  // 1: the issuer first waits on a barrier nothing arrives on (timeout test)
   float* part_o;                   // partial results: [2 parts][columns][D] and [2 parts][columns][3]
   float* part_s;
+  float* scores;                   // with add_weights, else null: [units][64][columns] log2-scaled scores
 };
 struct Cache8EvictParams {
   Cache8Pools c;
@@ -179,11 +183,12 @@ struct Cache8EvictParams {
   int B, max_blocks, to_blocks, keep, recent;
 };
 constexpr int kCache8MaxRows = 128;   // G * Nq of one call
-constexpr int kCache8Parts = 304;     // CTAs of the attention: parts the work is cut into at most
+constexpr int kCache8Sms = 152;       // the attention's grid: one or two CTAs on each of them
 int cache8_columns(int d, int R);     // query rows a CTA takes at once
-int cache8_parts(int B, int Hkv, int chunks, int max_blocks);
+int cache8_parts(int B, int Hkv, int d, int R, int max_blocks);   // CTAs, parts the work is cut into at most
 cudaError_t launch_cache8_append(const Cache8AppendParams& p, cudaStream_t stream);
-cudaError_t launch_cache8_fwd(const Cache8Params& p, cudaStream_t stream);
+// maps over the codes as [num_blocks * Hkv, 64, d], boxes of 64 rows by 128 bytes
+cudaError_t launch_cache8_fwd(const CUtensorMap& mk, const CUtensorMap& mv, const Cache8Params& p, cudaStream_t stream);
 cudaError_t launch_cache8_evict(const Cache8EvictParams& p, cudaStream_t stream);
 
 }  // namespace fa

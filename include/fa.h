@@ -371,10 +371,13 @@ fa_status fa_cache8_append(const void* k, long long k_stride_h, long long k_stri
  * probabilities of key j over the Hq / Hkv heads and Nq queries, for every
  * key j < lengths[b] (weight_decay finite, >= 0; 0 overwrites). It needs
  * cache->weight, and no two sequences of the call may then share a block.
- * workspace: fa_fwd_cache8_workspace_bytes(B, Hq, Hkv, Nq, d, max_blocks)
- * bytes, 256-byte aligned, contents before and after of no meaning; calls
- * that may overlap on the GPU need one each. */
-size_t fa_fwd_cache8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int max_blocks);
+ * workspace: fa_fwd_cache8_workspace_bytes(B, Hq, Hkv, Nq, d, max_blocks,
+ * add_weights) bytes (a few MB; with weights also 4 bytes per row, rows rounded
+ * up to a multiple of 8, for every token and KV head that the block tables have
+ * room for), 256-byte aligned, contents before and after of no meaning; calls
+ * that may overlap on the GPU need one each. Returns 0 for sizes that the call
+ * refuses (B * Hkv * max_blocks row groups and blocks past 2^31 among them). */
+size_t fa_fwd_cache8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int max_blocks, int add_weights);
 fa_status fa_fwd_cache8(const void* q, const fa_cache8* cache, const int* block_table, int max_blocks,
                         const int* lengths, void* o, float* lse, void* workspace, size_t workspace_bytes, int B,
                         int Hq, int Nq, int causal, float scale, int add_weights, float weight_decay, void* stream);

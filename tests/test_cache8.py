@@ -65,18 +65,24 @@ def test_fwd_rules(lib):
                 dict(add=1, c=cache(weight=0)), dict(q=P((1 << 20) + 8))):
         assert fwd(lib, **bad) == 1, bad
     assert fwd(lib, Hq=4, Nq=65) == 2                      # 2 heads per KV head x 65 rows
-    need = lib.fa_fwd_cache8_workspace_bytes(1, 4, 2, 1, 64, 4)
-    assert need > 0
+    need = lib.fa_fwd_cache8_workspace_bytes(1, 4, 2, 1, 64, 4, 0)
+    more = lib.fa_fwd_cache8_workspace_bytes(1, 4, 2, 1, 64, 4, 1)
+    assert 0 < need < more and fwd(lib, add=1, nws=more - 1) == 6
+    assert fwd(lib, B=65535, Hq=64, c=cache(Hkv=16), mb=1 << 24) == 2      # more than 2^31 units of work
     assert fwd(lib, nws=need - 1) == 6 and fwd(lib, ws=NULL) == 6 and fwd(lib, ws=P((1 << 20) + 128)) == 6
 
 
 def test_workspace_bytes(lib):
-    # at most 304 parts of two partial results each, as many as units where fewer: [columns][D] and [columns][3] floats
-    assert lib.fa_fwd_cache8_workspace_bytes(1, 4, 2, 1, 64, 4) == 2 * 8 * 8 * 64 * 4 + 2 * 8 * 8 * 3 * 4
-    assert lib.fa_fwd_cache8_workspace_bytes(64, 64, 8, 1, 128, 1000) == 2 * 304 * 8 * (128 + 3) * 4
+    # at most 304 parts (152 at d > 128 with more than 8 rows) of two partial results each, as many as units where fewer: [columns][D] and [columns][3]
+    # floats; with weights the scores of every unit: 64 tokens x columns
+    ws = lib.fa_fwd_cache8_workspace_bytes
+    assert ws(1, 4, 2, 1, 64, 4, 0) == 2 * 8 * 8 * 128 * 4 + 2 * 8 * 8 * 3 * 4         # D = 128 up to d = 128
+    assert ws(1, 4, 2, 1, 64, 4, 1) == ws(1, 4, 2, 1, 64, 4, 0) + 8 * 64 * 8 * 4
+    assert ws(64, 64, 8, 1, 128, 1000, 0) == 2 * 304 * 8 * (128 + 3) * 4
+    assert ws(1, 40, 1, 1, 128, 10, 1) == 2 * 20 * 32 * (128 + 3) * 4 + 20 * 64 * 32 * 4      # two chunks of 32 columns
     for bad in ((0, 4, 2, 1, 64, 4), (1, 3, 2, 1, 64, 4), (1, 4, 2, 0, 64, 4), (1, 4, 2, 1, 100, 4), (1, 4, 2, 1, 64, 0),
-                (1, 4, 2, 65, 64, 4)):
-        assert lib.fa_fwd_cache8_workspace_bytes(*bad) == 0, bad
+                (1, 4, 2, 65, 64, 4), (65535, 64, 16, 1, 64, 1 << 24)):
+        assert ws(*bad, 0) == 0, bad
 
 
 def test_evict_rules(lib):
