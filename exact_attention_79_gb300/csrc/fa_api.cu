@@ -685,7 +685,9 @@ fa_status cache8_rows(int B, int Hq, int Hkv, int Nq, int d, int max_blocks) {
   if (static_cast<long long>(Hq / Hkv) * Nq > fa::kCache8MaxRows || !fp8_dim(d)) return FA_ERR_UNSUPPORTED;
   // units of work (row groups x blocks) are counted in 32 bits
   const int R = Hq / Hkv * Nq, cols = fa::cache8_columns(d, R), chunks = (R + cols - 1) / cols;
-  if (static_cast<double>(B) * Hkv * chunks * max_blocks >= 2147483648.0) return FA_ERR_UNSUPPORTED;
+  if (static_cast<double>(B) * Hkv * chunks * max_blocks >= 2147483648.0 ||
+      static_cast<double>(B) * Hq * Nq >= 2147483648.0)
+    return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
 }  // namespace

@@ -84,8 +84,9 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
 // The line of units: for sequence after sequence, row group (KV head, chunk)
 // after row group, its blocks. A sequence has at least one block of units, so
 // that rows without keys are written too.
+__device__ __forceinline__ int blocks_of(int len) { return max(1, (len + kCacheBlock - 1) / kCacheBlock); }
 __device__ __forceinline__ int line_blocks(const Cache8Params& p, int b) {
-  return max(1, (cache_length(p.lengths, b, p.max_blocks) + kCacheBlock - 1) / kCacheBlock);
+  return blocks_of(cache_length(p.lengths, b, p.max_blocks));
 }
 // All units; by a whole warp.
 __device__ __forceinline__ int line_total(const Cache8Params& p, int lane) {
@@ -109,8 +110,8 @@ struct Place {
   int b, before;             // sequence, units before it
   int nblk, len;             // its blocks of units and tokens
   __device__ __forceinline__ void load(const Cache8Params& p) {
-    nblk = line_blocks(p, b);
     len = cache_length(p.lengths, b, p.max_blocks);
+    nblk = blocks_of(len);
   }
   // to the sequence of unit u, by a whole warp
   __device__ __forceinline__ void find(const Cache8Params& p, int u, int lane) {
@@ -136,6 +137,37 @@ struct Place {
       base += __shfl_sync(0xffffffffu, incl, 31);
     }
     load(p);
+  }
+  // to the first unit of part `i` of `ctas`, whose units are [u0, u1); false: no such part. By a
+  // whole warp; one look at the lengths where a warp holds them all.
+  __device__ __forceinline__ bool start(const Cache8Params& p, int i, int ctas, int lane, int& u0, int& u1) {
+    const int per_block = p.c.Hkv * p.chunks;
+    int mine = 0, total;
+    if (p.B <= 32) {
+      mine = lane < p.B ? cache_length(p.lengths, lane, p.max_blocks) : -1;
+      total = __reduce_add_sync(0xffffffffu, mine < 0 ? 0 : blocks_of(mine)) * per_block;
+    } else {
+      total = line_total(p, lane);
+    }
+    const int parts = line_parts(total, ctas);
+    if (i >= parts) return false;
+    u0 = part_begin(total, i, parts);
+    u1 = part_begin(total, i + 1, parts);
+    if (p.B > 32) {
+      find(p, u0, lane);
+      return true;
+    }
+    int incl = mine < 0 ? 0 : blocks_of(mine);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    b = __ffs(__ballot_sync(0xffffffffu, u0 < incl * per_block)) - 1;
+    len = __shfl_sync(0xffffffffu, mine, b);
+    nblk = blocks_of(len);
+    before = (__shfl_sync(0xffffffffu, incl, b) - nblk) * per_block;
+    return true;
   }
   // onwards to the sequence of unit u (one that exists)
   __device__ __forceinline__ void go(const Cache8Params& p, int u) {
@@ -231,10 +263,9 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 
   // the second kernel may be set up meanwhile; it waits for this one's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int total = line_total(p, lane);
-  const int parts = line_parts(total, gridDim.x);
-  if (static_cast<int>(blockIdx.x) >= parts) return;
-  const int u0 = part_begin(total, blockIdx.x, parts), u1 = part_begin(total, blockIdx.x + 1, parts);
+  int u0, u1;
+  Place at;
+  if (!at.start(p, blockIdx.x, gridDim.x, lane, u0, u1)) return;
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < C::kRing; ++i) {
@@ -257,8 +288,6 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     tmem_alloc(smem_addr(tmem_slot), C::kTmem);
     tmem_relinquish();
   }
-  Place at;
-  at.find(p, u0, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -287,15 +316,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         for (int i = 0; i < 32 && blk + i < s.blk1 && ok; i += 2, ++tile) {
           const int za = __shfl_sync(0xffffffffu, z, i), zb = __shfl_sync(0xffffffffu, z, i + 1);
           const int there = (za >= 0) + (zb >= 0);
-          if (lane == i || lane == i + 1) {
-            volatile float* const dst = info + (tile % kInfo) * 8 + (lane - i) * 4;
-            dst[0] = ks;
-            dst[1] = vs;
-            dst[2] = page >= 0 ? 1.f : 0.f;
-          }
-          __syncwarp();
           if (lane == 0) {
-            mbar_arrive(bar_info(tile % kInfo));
             for (int kv = 0; kv < 2 && ok; ++kv, ++c) {
               const int slot = c % C::kRing;
               ok = wait(bar_kv_empty(slot), ((c / C::kRing) & 1) ^ 1, abort_flag, p.timeout_ns);
@@ -309,6 +330,15 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             }
           }
           ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
+          // (the scales come after the loads are on their way: nothing before them needs them)
+          if (lane == i || lane == i + 1) {
+            volatile float* const dst = info + (tile % kInfo) * 8 + (lane - i) * 4;
+            dst[0] = ks;
+            dst[1] = vs;
+            dst[2] = page >= 0 ? 1.f : 0.f;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_info(tile % kInfo));
         }
       }
       u += s.blk1 - s.blk0;
@@ -380,43 +410,56 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const uint32_t dst = s_q + buf * C::kQBytes;
-      for (int q = 0; q < R; ++q) {
-        float x[C::kChunks][4];
-        float amax = 0.f;
+      for (int q0 = 0; q0 < R; q0 += 8) {
+        uint2 v[8][C::kChunks];                          // eight rows' loads on their way together
 #pragma unroll
-        for (int ch = 0; ch < C::kChunks; ++ch) {
-          const int col = 128 * ch + 4 * lane;
-          uint2 v = make_uint2(0, 0);
-          if (q < rows && col < p.c.d) v = *reinterpret_cast<const uint2*>(p.q + (qrow + q) * p.c.d + col);
-          x[ch][0] = __uint_as_float(v.x << 16);
-          x[ch][1] = __uint_as_float(v.x & 0xFFFF0000u);
-          x[ch][2] = __uint_as_float(v.y << 16);
-          x[ch][3] = __uint_as_float(v.y & 0xFFFF0000u);
+        for (int e = 0; e < 8; ++e)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(x[ch][e]));
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        // exponent that brings the largest to [128, 256); bounded so that both powers are normal.
-        // An infinity among them becomes NaN, as its logits are.
-        const int e2 = amax > 0.f ? max(-100, min(100, static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 7)) : 0;
-        const float down = amax < INFINITY ? __uint_as_float(static_cast<uint32_t>(127 - e2) << 23) : NAN;
-        if (lane == 0) q_scale[buf * R + q] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
-#pragma unroll
-        for (int ch = 0; ch < C::kChunks; ++ch) {
-          uint32_t hi = 0, lo = 0;
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            const float a = x[ch][e] * down, b = x[ch][e + 1] * down;
-            const uint32_t c0 = pack_e4m3x2(a, b);
-            const float2 f = e4m3x2_to_float2(c0);
-            hi |= c0 << (8 * e);
-            lo |= pack_e4m3x2((a - f.x) * 16.f, (b - f.y) * 16.f) << (8 * e);
+          for (int ch = 0; ch < C::kChunks; ++ch) {
+            const int col = 128 * ch + 4 * lane;
+            v[e][ch] = make_uint2(0, 0);
+            if (q0 + e < rows && col < p.c.d) v[e][ch] = *reinterpret_cast<const uint2*>(p.q + (qrow + q0 + e) * p.c.d + col);
           }
-          // row q (first terms) and row R + q (second) of the operand, bytes 4 lane .. + 3
-          const uint32_t box = dst + ch * (C::kNS * 128);
-          asm volatile("st.shared.b32 [%0], %1;" :: "r"(swz128(box, q, lane >> 2) + (lane & 3) * 4), "r"(hi) : "memory");
-          asm volatile("st.shared.b32 [%0], %1;" :: "r"(swz128(box, R + q, lane >> 2) + (lane & 3) * 4), "r"(lo) : "memory");
+        float amax[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          amax[e] = 0.f;
+#pragma unroll
+          for (int ch = 0; ch < C::kChunks; ++ch) {
+            const uint32_t w[2] = {v[e][ch].x, v[e][ch].y};
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              amax[e] = fmaxf(amax[e], fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
+          }
+        }
+        // (non-negative floats order like their bits)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax[e] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax[e])));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int q = q0 + e;
+          // exponent that brings the largest to [128, 256); bounded so that both powers are normal.
+          // An infinity among them becomes NaN, as its logits are.
+          const int e2 = amax[e] > 0.f ? max(-100, min(100, static_cast<int>(__float_as_uint(amax[e]) >> 23) - 127 - 7)) : 0;
+          const float down = amax[e] < INFINITY ? __uint_as_float(static_cast<uint32_t>(127 - e2) << 23) : NAN;
+          if (lane == 0) q_scale[buf * R + q] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+#pragma unroll
+          for (int ch = 0; ch < C::kChunks; ++ch) {
+            const uint32_t w[2] = {v[e][ch].x, v[e][ch].y};
+            uint32_t hi = 0, lo = 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float a = __uint_as_float(w[k] << 16) * down, b = __uint_as_float(w[k] & 0xFFFF0000u) * down;
+              const uint32_t c0 = pack_e4m3x2(a, b);
+              const float2 f = e4m3x2_to_float2(c0);
+              hi |= c0 << (16 * k);
+              lo |= pack_e4m3x2((a - f.x) * 16.f, (b - f.y) * 16.f) << (16 * k);
+            }
+            // row q (first terms) and row R + q (second) of the operand, bytes 4 lane .. + 3
+            const uint32_t box = dst + ch * (C::kNS * 128);
+            asm volatile("st.shared.b32 [%0], %1;" :: "r"(swz128(box, q, lane >> 2) + (lane & 3) * 4), "r"(hi) : "memory");
+            asm volatile("st.shared.b32 [%0], %1;" :: "r"(swz128(box, R + q, lane >> 2) + (lane & 3) * 4), "r"(lo) : "memory");
+          }
         }
       }
       fence_proxy_async_smem();
@@ -441,12 +484,16 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       for (int q = 0; q < R; ++q) l[q] = 0.f;
       if (row < R) ref_l[row] = ref_o[row] = -INFINITY;
       named_bar_sync(1, 128);
-      // the queries' scales are there when their operand is
-      if (ok) ok = wait(bar_q_full(seg % C::kQBufs), (seg / C::kQBufs) & 1, abort_flag, p.timeout_ns);
       const float* const qs = q_scale + (seg % C::kQBufs) * R;
-      for (int j = 0; j < s.tiles; ++j, ++tile) {
+      // The first time the loop's code has to come from memory, which costs more
+      // than a tile: while the first tile's K is on its way the warps run through it once,
+      // with nothing seen and nothing told (j = -1, not `live`).
+      for (int j = seg == 0 ? -1 : 0; j < s.tiles; ++j) {
+        const bool live = j >= 0;
         const int buf = tile & 1;
-        if (ok)
+        // the queries' scales are there when their operand is
+        if (ok && j == 0) ok = wait(bar_q_full(seg % C::kQBufs), (seg / C::kQBufs) & 1, abort_flag, p.timeout_ns);
+        if (ok && live)
           ok = wait(bar_info(tile % kInfo), (tile / kInfo) & 1, abort_flag, p.timeout_ns) &&
                wait(bar_s_full(buf), (tile >> 1) & 1, abort_flag, p.timeout_ns);
         ok = __all_sync(0xffffffffu, ok);
@@ -455,7 +502,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         const int blk = s.blk0 + 2 * j + half;
         const int key = blk * kCacheBlock + (row & 63);
         // tokens past the length, of no block, or of another CTA's block are absent
-        const bool there = blk < s.blk1 && key < s.len && info[(tile % kInfo) * 8 + half * 4 + 2] != 0.f;
+        const bool there = live && blk < s.blk1 && key < s.len && info[(tile % kInfo) * 8 + half * 4 + 2] != 0.f;
         const float lvs = log2f(vs);
         float x[R];
         bool grow = !ok;
@@ -500,7 +547,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           for (int q = 0; q < R; ++q) grow |= x[q] > ref_l[q] + kTrail || x[q] + lvs > ref_o[q] + kTrail;
         }
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(bar_s_free(buf));
+        if (ok && live && lane == 0) mbar_arrive(bar_s_free(buf));
         if (meet_or(grow)) {
           if (meet_or(!ok)) {                            // a wait ran out somewhere: all leave together
             ok = false;
@@ -516,10 +563,10 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
               const uint32_t top = __reduce_max_sync(0xffffffffu, key_of);
               return top == 0u ? -INFINITY : __uint_as_float((top & 0x80000000u) ? top & 0x7FFFFFFFu : ~top);
             };
-            const float a = most(x[q]), b = most(x[q] + lvs);
+            const float a = most(x[q]);                  // (a warp's tokens are of one block: one V scale)
             if (lane == 0) {
               warp_l[warp * R + q] = a;
-              warp_o[warp * R + q] = b;
+              warp_o[warp * R + q] = a + lvs;
             }
           }
           named_bar_sync(1, 128);
@@ -562,7 +609,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             }
           }
         }
-        if (p.scores != nullptr && blk < s.blk1) {
+        if (p.scores != nullptr && live && blk < s.blk1) {
           // for the weights: this token's scores, -inf where hidden or absent
           float4* const keep = reinterpret_cast<float4*>(p.scores + (static_cast<size_t>(u + 2 * j + half) * kCacheBlock + (row & 63)) * R);
 #pragma unroll
@@ -570,7 +617,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             if (row0 + q < p.R) keep[q / 4] = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
         }
         // the P V that read this buffer two tiles ago has completed
-        if (ok) ok = wait(bar_p_empty(buf), ((tile >> 1) & 1) ^ 1, abort_flag, p.timeout_ns);
+        if (ok) ok = wait(bar_p_empty(buf), ((tile >> 1) & 1) ^ 1, abort_flag, p.timeout_ns);   // (at once when not live)
         const uint32_t dst = s_p + buf * C::kPBytes + (row & 15);
         const int unit = row >> 4;
 #pragma unroll
@@ -597,7 +644,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             store_byte(dst + (k * R + q + 1) * 128 + ((unit ^ ((q + 1) & 7)) << 4), codes[k] >> 8);
           }
         }
-        if (!there) {
+        if (live && !there) {
           // this token's V may be anything; P is 0, but 0 x NaN is not: clear it
           const int slot = (2 * tile + 1) % C::kRing;
           if (ok) ok = wait(bar_kv_full(slot), ((2 * tile + 1) / C::kRing) & 1, abort_flag, p.timeout_ns);
@@ -609,7 +656,10 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                 asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" :: "r"(s_kv(slot) + ch * 16384 + row * 128 + i * 16), "r"(0) : "memory");
         }
         fence_proxy_async_smem();
-        if (ok) mbar_arrive(bar_p_ready(buf));
+        if (ok && live) {
+          mbar_arrive(bar_p_ready(buf));
+          ++tile;
+        }
       }
       // ---------------------------------------------------------- the row group's result
       if (meet_or(!ok)) break;
@@ -709,16 +759,16 @@ struct RowParts {
 template <int D>
 __global__ void __launch_bounds__(kFinishWarps * 32) cache8_finish_kernel(const Cache8Params p, int cols, int ctas, int join_ctas) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int total = line_total(p, lane);
+  const int total = line_total(p, lane);                 // (lengths are the caller's: no need to wait for them)
   const int parts = line_parts(total, ctas);
   const int per_block = p.c.Hkv * p.chunks;
+  __shared__ float lse2[kCache8MaxRows];
   if (static_cast<int>(blockIdx.x) < join_ctas) {
-    // ---- join: row R0 of the B * Hkv * R
-    const long long row = static_cast<long long>(blockIdx.x) * kFinishWarps + warp;
+    // ---- join: one row of the B * Hkv * R; its parts dealt out to the warps
+    __shared__ float4 sum_o[kFinishWarps][32 * (D / 128)];
+    __shared__ float sum_l[kFinishWarps];
     const int per_seq = p.c.Hkv * p.R;
-    if (row >= static_cast<long long>(p.B) * per_seq) return;
-    const int b = static_cast<int>(row / per_seq), hr = static_cast<int>(row - static_cast<long long>(b) * per_seq);
+    const int b = static_cast<int>(blockIdx.x) / per_seq, hr = static_cast<int>(blockIdx.x) - b * per_seq;
     const int h = hr / p.R, r = hr - h * p.R;
     int before = 0;
     for (int i = lane; i < b; i += 32) before += line_blocks(p, i);
@@ -726,6 +776,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32) cache8_finish_kernel(const 
     const int nblk = line_blocks(p, b);
     const RowParts rp(total, parts, before + (h * p.chunks + r / cols) * nblk, nblk, cols, r % cols);
     if (rp.c0 == rp.c1) return;                          // written whole
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     float ml = -INFINITY, mo = -INFINITY;
     for (int c = rp.c0 + lane; c <= rp.c1; c += 32) {
       const float* const s3 = p.part_s + rp.slot(c) * 3;
@@ -743,34 +794,47 @@ __global__ void __launch_bounds__(kFinishWarps * 32) cache8_finish_kernel(const 
 #pragma unroll
     for (int i = 0; i < kPer; ++i) a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int c = rp.c0; c <= rp.c1; ++c) {
+    for (int c = rp.c0 + warp; c <= rp.c1; c += kFinishWarps) {
       const long long slot = rp.slot(c);
       const float* const s3 = p.part_s + slot * 3;
       sum += s3[0] == -INFINITY ? s3[1] : s3[1] * ex2_approx(s3[0] - ml);
       const float f = s3[2] == -INFINITY ? 1.f : ex2_approx(s3[2] - mo);   // (no term yet: O is 0, or a NaN that stays)
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        {
-          const float4 y = *reinterpret_cast<const float4*>(p.part_o + slot * D + 128 * i + 4 * lane);
-          a[i].x = fmaf(f, y.x, a[i].x);
-          a[i].y = fmaf(f, y.y, a[i].y);
-          a[i].z = fmaf(f, y.z, a[i].z);
-          a[i].w = fmaf(f, y.w, a[i].w);
-        }
+      for (int i = 0; i < kPer; ++i) {
+        const float4 y = *reinterpret_cast<const float4*>(p.part_o + slot * D + 128 * i + 4 * lane);
+        a[i].x = fmaf(f, y.x, a[i].x);
+        a[i].y = fmaf(f, y.y, a[i].y);
+        a[i].z = fmaf(f, y.z, a[i].z);
+        a[i].w = fmaf(f, y.w, a[i].w);
+      }
     }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sum_o[warp][32 * i + lane] = a[i];
+    if (lane == 0) sum_l[warp] = sum;
+    __syncthreads();
+    if (warp != 0) return;
+    sum = (sum_l[0] + sum_l[1]) + (sum_l[2] + sum_l[3]);
     const size_t at = (static_cast<size_t>(b) * p.Hq + static_cast<size_t>(h) * p.G) * p.Nq + r;
     const float f = sum == 0.f ? 0.f : ex2_approx(mo - ml) / sum;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
+    for (int i = 0; i < kPer; ++i) {
+#pragma unroll
+      for (int w = 1; w < kFinishWarps; ++w) {
+        const float4 y = sum_o[w][32 * i + lane];
+        a[i].x += y.x;
+        a[i].y += y.y;
+        a[i].z += y.z;
+        a[i].w += y.w;
+      }
       if (128 * i + 4 * lane < p.c.d)
         *reinterpret_cast<uint2*>(p.o + at * p.c.d + 128 * i + 4 * lane) =
             make_uint2(pack_bf16x2(a[i].x * f, a[i].y * f), pack_bf16x2(a[i].z * f, a[i].w * f));
+    }
     if (lane == 0) p.lse[at] = sum == 0.f ? -INFINITY : (ml + log2f(sum)) * kLn2;
     return;
   }
   // ---- weights: an equal share of the (sequence, KV head, block), two at a time,
   // one thread per token
-  __shared__ float lse2[kCache8MaxRows];
   const int all = total / p.chunks;                      // (sequence, KV head, block)
   const int share = static_cast<int>(blockIdx.x) - join_ctas, shares = static_cast<int>(gridDim.x) - join_ctas;
   const int w0 = part_begin(all, share, shares), w1 = part_begin(all, share + 1, shares);
@@ -778,6 +842,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32) cache8_finish_kernel(const 
   Place at;
   at.find(p, w0 * p.chunks, lane);                       // (sequences have `chunks` times as many units)
   const int half = threadIdx.x >> 6, slot = threadIdx.x & 63;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int u = w0; u < w1;) {
     // the blocks of one head from u on
     at.go(p, u * p.chunks);
@@ -794,10 +859,16 @@ __global__ void __launch_bounds__(kFinishWarps * 32) cache8_finish_kernel(const 
       } else {
         float ml = -INFINITY, sum = 0.f;
         for (int c = rp.c0; c <= rp.c1; ++c) ml = fmaxf(ml, p.part_s[rp.slot(c) * 3]);
-        for (int c = rp.c0; c <= rp.c1; ++c) {
-          const float* const s3 = p.part_s + rp.slot(c) * 3;
-          sum += s3[0] == -INFINITY ? s3[1] : s3[1] * ex2_approx(s3[0] - ml);
+        float part[kFinishWarps];                        // in the join's order: the same sum
+#pragma unroll
+        for (int w = 0; w < kFinishWarps; ++w) {
+          part[w] = 0.f;
+          for (int c = rp.c0 + w; c <= rp.c1; c += kFinishWarps) {
+            const float* const s3 = p.part_s + rp.slot(c) * 3;
+            part[w] += s3[0] == -INFINITY ? s3[1] : s3[1] * ex2_approx(s3[0] - ml);
+          }
         }
+        sum = (part[0] + part[1]) + (part[2] + part[3]);
         v = sum == 0.f ? -INFINITY : ml + log2f(sum);
       }
       lse2[r] = v == -INFINITY ? INFINITY : v;           // a row that sees no key adds nothing
@@ -848,8 +919,7 @@ cudaError_t launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const Cache
   else if (cols == 16) e = launch_fwd<D, 16>(mk, mv, p, parts, stream);
   else if constexpr (D == 128) e = launch_fwd<D, 32>(mk, mv, p, parts, stream);
   if (e != cudaSuccess) return e;
-  const long long rows = static_cast<long long>(p.B) * p.c.Hkv * p.R;
-  const int join = parts > 1 ? static_cast<int>((rows + kFinishWarps - 1) / kFinishWarps) : 0;
+  const int join = parts > 1 ? p.B * p.c.Hkv * p.R : 0;                // one CTA per row
   const long long blocks = static_cast<long long>(p.B) * p.c.Hkv * p.max_blocks;
   const int weigh = p.add_weights ? static_cast<int>(blocks < kWeightCtas ? blocks : kWeightCtas) : 0;
   if (join + weigh == 0) return cudaSuccess;
