@@ -667,6 +667,7 @@ fa_status cache8_pools(const fa_cache8* c, int B, int max_blocks, const void* bl
 // and, with weights, the scores of every token and row (off_x).
 struct Cache8Workspace {
   size_t off_s, off_x, total;
+  int score_row;                       // floats per token in the scores
 };
 Cache8Workspace cache8_workspace(int B, int Hkv, int R, int d, int max_blocks, bool weights) {
   const int cols = fa::cache8_columns(d, R), chunks = (R + cols - 1) / cols;
@@ -676,7 +677,8 @@ Cache8Workspace cache8_workspace(int B, int Hkv, int R, int d, int max_blocks, b
   Cache8Workspace w;
   w.off_s = align256(rows * D * 4);
   w.off_x = w.off_s + align256(rows * 3 * 4);
-  w.total = w.off_x + (weights ? units * FA_CACHE8_BLOCK * cols * 4 : 0);
+  w.score_row = R < cols ? (R + 3) / 4 * 4 : cols;
+  w.total = w.off_x + (weights ? units * FA_CACHE8_BLOCK * w.score_row * 4 : 0);
   return w;
 }
 
@@ -764,6 +766,7 @@ fa_status fa_fwd_cache8(const void* q, const fa_cache8* cache, const int* block_
   p.part_o = static_cast<float*>(workspace);
   p.part_s = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.off_s);
   p.scores = add_weights ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.off_x) : nullptr;
+  p.score_row = w.score_row;
   p.status = status;
   p.timeout_ns = wait_limit_ns();
   p.test_stall = test_stall();

@@ -261,9 +261,14 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   const uint32_t bar_stall = bars + 304;                               // nothing arrives (timeout test)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // the second kernel may be set up meanwhile; it waits for this one's end
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int u0, u1;
+  // This kernel may have been set up while the one before it still ran: nothing
+  // in memory is read or written ahead of that one's end. From then on the second
+  // kernel may be set up, which so may read what the caller's kernels wrote.
+  // (All warps find the part by the same code: a copy of it in each role costs
+  // more than it saves, since code, too, comes from memory the first time.)
+  wait_before();
+  let_next();
+  int u0, u1;                                            // this part's units
   Place at;
   if (!at.start(p, blockIdx.x, gridDim.x, lane, u0, u1)) return;
   if (threadIdx.x == 0) {
@@ -485,15 +490,11 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       if (row < R) ref_l[row] = ref_o[row] = -INFINITY;
       named_bar_sync(1, 128);
       const float* const qs = q_scale + (seg % C::kQBufs) * R;
-      // The first time the loop's code has to come from memory, which costs more
-      // than a tile: while the first tile's K is on its way the warps run through it once,
-      // with nothing seen and nothing told (j = -1, not `live`).
-      for (int j = seg == 0 ? -1 : 0; j < s.tiles; ++j) {
-        const bool live = j >= 0;
+      for (int j = 0; j < s.tiles; ++j, ++tile) {
         const int buf = tile & 1;
         // the queries' scales are there when their operand is
         if (ok && j == 0) ok = wait(bar_q_full(seg % C::kQBufs), (seg / C::kQBufs) & 1, abort_flag, p.timeout_ns);
-        if (ok && live)
+        if (ok)
           ok = wait(bar_info(tile % kInfo), (tile / kInfo) & 1, abort_flag, p.timeout_ns) &&
                wait(bar_s_full(buf), (tile >> 1) & 1, abort_flag, p.timeout_ns);
         ok = __all_sync(0xffffffffu, ok);
@@ -502,7 +503,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         const int blk = s.blk0 + 2 * j + half;
         const int key = blk * kCacheBlock + (row & 63);
         // tokens past the length, of no block, or of another CTA's block are absent
-        const bool there = live && blk < s.blk1 && key < s.len && info[(tile % kInfo) * 8 + half * 4 + 2] != 0.f;
+        const bool there = blk < s.blk1 && key < s.len && info[(tile % kInfo) * 8 + half * 4 + 2] != 0.f;
         const float lvs = log2f(vs);
         float x[R];
         bool grow = !ok;
@@ -547,7 +548,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           for (int q = 0; q < R; ++q) grow |= x[q] > ref_l[q] + kTrail || x[q] + lvs > ref_o[q] + kTrail;
         }
         __syncwarp();
-        if (ok && live && lane == 0) mbar_arrive(bar_s_free(buf));
+        if (ok && lane == 0) mbar_arrive(bar_s_free(buf));
         if (meet_or(grow)) {
           if (meet_or(!ok)) {                            // a wait ran out somewhere: all leave together
             ok = false;
@@ -609,15 +610,16 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             }
           }
         }
-        if (p.scores != nullptr && live && blk < s.blk1) {
+        if (p.scores != nullptr && blk < s.blk1) {
           // for the weights: this token's scores, -inf where hidden or absent
-          float4* const keep = reinterpret_cast<float4*>(p.scores + (static_cast<size_t>(u + 2 * j + half) * kCacheBlock + (row & 63)) * R);
+          float4* const keep =
+              reinterpret_cast<float4*>(p.scores + (static_cast<size_t>(u + 2 * j + half) * kCacheBlock + (row & 63)) * p.score_row);
 #pragma unroll
           for (int q = 0; q < R; q += 4)
             if (row0 + q < p.R) keep[q / 4] = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
         }
         // the P V that read this buffer two tiles ago has completed
-        if (ok) ok = wait(bar_p_empty(buf), ((tile >> 1) & 1) ^ 1, abort_flag, p.timeout_ns);   // (at once when not live)
+        if (ok) ok = wait(bar_p_empty(buf), ((tile >> 1) & 1) ^ 1, abort_flag, p.timeout_ns);
         const uint32_t dst = s_p + buf * C::kPBytes + (row & 15);
         const int unit = row >> 4;
 #pragma unroll
@@ -644,7 +646,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             store_byte(dst + (k * R + q + 1) * 128 + ((unit ^ ((q + 1) & 7)) << 4), codes[k] >> 8);
           }
         }
-        if (live && !there) {
+        if (!there) {
           // this token's V may be anything; P is 0, but 0 x NaN is not: clear it
           const int slot = (2 * tile + 1) % C::kRing;
           if (ok) ok = wait(bar_kv_full(slot), ((2 * tile + 1) / C::kRing) & 1, abort_flag, p.timeout_ns);
@@ -656,10 +658,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                 asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" :: "r"(s_kv(slot) + ch * 16384 + row * 128 + i * 16), "r"(0) : "memory");
         }
         fence_proxy_async_smem();
-        if (ok && live) {
-          mbar_arrive(bar_p_ready(buf));
-          ++tile;
-        }
+        if (ok) mbar_arrive(bar_p_ready(buf));
       }
       // ---------------------------------------------------------- the row group's result
       if (meet_or(!ok)) break;
@@ -743,7 +742,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 // probabilities need the whole row's LSE; reading K again instead costs d
 // bytes per token and head against 8 per row, mostly from L2).
 constexpr int kFinishWarps = 4;
-constexpr int kWeightCtas = 2432;        // 16 per SM: all its threads, waiting for memory most of the time
+constexpr int kWeightCtas = 1216;        // 8 per SM
 
 // Where a row's partial results lie.
 struct RowParts {
@@ -766,7 +765,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32) cache8_finish_kernel(const 
   if (static_cast<int>(blockIdx.x) < join_ctas) {
     // ---- join: one row of the B * Hkv * R; its parts dealt out to the warps
     __shared__ float4 sum_o[kFinishWarps][32 * (D / 128)];
-    __shared__ float sum_l[kFinishWarps];
+    __shared__ float sum_l[kFinishWarps], top_l[kFinishWarps], top_o[kFinishWarps];
     const int per_seq = p.c.Hkv * p.R;
     const int b = static_cast<int>(blockIdx.x) / per_seq, hr = static_cast<int>(blockIdx.x) - b * per_seq;
     const int h = hr / p.R, r = hr - h * p.R;
@@ -776,55 +775,88 @@ __global__ void __launch_bounds__(kFinishWarps * 32) cache8_finish_kernel(const 
     const int nblk = line_blocks(p, b);
     const RowParts rp(total, parts, before + (h * p.chunks + r / cols) * nblk, nblk, cols, r % cols);
     if (rp.c0 == rp.c1) return;                          // written whole
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    float ml = -INFINITY, mo = -INFINITY;
-    for (int c = rp.c0 + lane; c <= rp.c1; c += 32) {
-      const float* const s3 = p.part_s + rp.slot(c) * 3;
-      ml = fmaxf(ml, s3[0]);
-      mo = fmaxf(mo, s3[2]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      ml = fmaxf(ml, __shfl_xor_sync(0xffffffffu, ml, o));
-      mo = fmaxf(mo, __shfl_xor_sync(0xffffffffu, mo, o));
-    }
+    wait_before();
+    // eight parts a warp at a time, all their loads together
     constexpr int kPer = D / 128;                        // float4 per lane
-    float sum = 0.f;
+    float ml = -INFINITY, mo = -INFINITY, sum = 0.f;
     float4 a[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int c = rp.c0 + warp; c <= rp.c1; c += kFinishWarps) {
-      const long long slot = rp.slot(c);
-      const float* const s3 = p.part_s + slot * 3;
-      sum += s3[0] == -INFINITY ? s3[1] : s3[1] * ex2_approx(s3[0] - ml);
-      const float f = s3[2] == -INFINITY ? 1.f : ex2_approx(s3[2] - mo);   // (no term yet: O is 0, or a NaN that stays)
+    for (int c = rp.c0 + warp; c <= rp.c1; c += 8 * kFinishWarps) {
+      float s3[8][3];
+      float4 y[8][kPer];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int ck = min(c + k * kFinishWarps, rp.c1);
+        const long long slot = rp.slot(ck);
+        const bool mine = c + k * kFinishWarps <= rp.c1;
+#pragma unroll
+        for (int e = 0; e < 3; ++e) s3[k][e] = mine ? p.part_s[slot * 3 + e] : e == 1 ? 0.f : -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          y[k][i] = mine ? *reinterpret_cast<const float4*>(p.part_o + slot * D + 128 * i + 4 * lane)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float nl = ml, no = mo;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        nl = fmaxf(nl, s3[k][0]);
+        no = fmaxf(no, s3[k][2]);
+      }
+      sum = ml == -INFINITY ? sum : sum * ex2_approx(ml - nl);
+      const float f0 = mo == -INFINITY ? 1.f : ex2_approx(mo - no);
+      ml = nl;
+      mo = no;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const float4 y = *reinterpret_cast<const float4*>(p.part_o + slot * D + 128 * i + 4 * lane);
-        a[i].x = fmaf(f, y.x, a[i].x);
-        a[i].y = fmaf(f, y.y, a[i].y);
-        a[i].z = fmaf(f, y.z, a[i].z);
-        a[i].w = fmaf(f, y.w, a[i].w);
+        a[i].x *= f0;
+        a[i].y *= f0;
+        a[i].z *= f0;
+        a[i].w *= f0;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        sum += s3[k][0] == -INFINITY ? s3[k][1] : s3[k][1] * ex2_approx(s3[k][0] - ml);
+        const float f = s3[k][2] == -INFINITY ? 1.f : ex2_approx(s3[k][2] - mo);   // (no term yet: O is 0, or a NaN that stays)
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          a[i].x = fmaf(f, y[k][i].x, a[i].x);
+          a[i].y = fmaf(f, y[k][i].y, a[i].y);
+          a[i].z = fmaf(f, y[k][i].z, a[i].z);
+          a[i].w = fmaf(f, y[k][i].w, a[i].w);
+        }
       }
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) sum_o[warp][32 * i + lane] = a[i];
-    if (lane == 0) sum_l[warp] = sum;
+    if (lane == 0) {
+      sum_l[warp] = sum;
+      top_l[warp] = ml;
+      top_o[warp] = mo;
+    }
     __syncthreads();
     if (warp != 0) return;
-    sum = (sum_l[0] + sum_l[1]) + (sum_l[2] + sum_l[3]);
+    ml = fmaxf(fmaxf(top_l[0], top_l[1]), fmaxf(top_l[2], top_l[3]));
+    mo = fmaxf(fmaxf(top_o[0], top_o[1]), fmaxf(top_o[2], top_o[3]));
+    float fo[kFinishWarps];
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kFinishWarps; ++w) {
+      sum += top_l[w] == -INFINITY ? sum_l[w] : sum_l[w] * ex2_approx(top_l[w] - ml);
+      fo[w] = top_o[w] == -INFINITY ? 1.f : ex2_approx(top_o[w] - mo);
+    }
     const size_t at = (static_cast<size_t>(b) * p.Hq + static_cast<size_t>(h) * p.G) * p.Nq + r;
     const float f = sum == 0.f ? 0.f : ex2_approx(mo - ml) / sum;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
+      a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 1; w < kFinishWarps; ++w) {
+      for (int w = 0; w < kFinishWarps; ++w) {
         const float4 y = sum_o[w][32 * i + lane];
-        a[i].x += y.x;
-        a[i].y += y.y;
-        a[i].z += y.z;
-        a[i].w += y.w;
+        a[i].x = fmaf(fo[w], y.x, a[i].x);
+        a[i].y = fmaf(fo[w], y.y, a[i].y);
+        a[i].z = fmaf(fo[w], y.z, a[i].z);
+        a[i].w = fmaf(fo[w], y.w, a[i].w);
       }
       if (128 * i + 4 * lane < p.c.d)
         *reinterpret_cast<uint2*>(p.o + at * p.c.d + 128 * i + 4 * lane) =
@@ -842,7 +874,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32) cache8_finish_kernel(const 
   Place at;
   at.find(p, w0 * p.chunks, lane);                       // (sequences have `chunks` times as many units)
   const int half = threadIdx.x >> 6, slot = threadIdx.x & 63;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_before();
   for (int u = w0; u < w1;) {
     // the blocks of one head from u on
     at.go(p, u * p.chunks);
@@ -858,43 +890,60 @@ __global__ void __launch_bounds__(kFinishWarps * 32) cache8_finish_kernel(const 
         v = p.lse[(static_cast<size_t>(at.b) * p.Hq + static_cast<size_t>(h) * p.G) * p.Nq + r] * kLog2e;
       } else {
         float ml = -INFINITY, sum = 0.f;
+#pragma unroll 4
         for (int c = rp.c0; c <= rp.c1; ++c) ml = fmaxf(ml, p.part_s[rp.slot(c) * 3]);
-        float part[kFinishWarps];                        // in the join's order: the same sum
-#pragma unroll
-        for (int w = 0; w < kFinishWarps; ++w) {
-          part[w] = 0.f;
-          for (int c = rp.c0 + w; c <= rp.c1; c += kFinishWarps) {
-            const float* const s3 = p.part_s + rp.slot(c) * 3;
-            part[w] += s3[0] == -INFINITY ? s3[1] : s3[1] * ex2_approx(s3[0] - ml);
-          }
+#pragma unroll 4
+        for (int c = rp.c0; c <= rp.c1; ++c) {
+          const float* const s3 = p.part_s + rp.slot(c) * 3;
+          sum += s3[0] == -INFINITY ? s3[1] : s3[1] * ex2_approx(s3[0] - ml);
         }
-        sum = (part[0] + part[1]) + (part[2] + part[3]);
         v = sum == 0.f ? -INFINITY : ml + log2f(sum);
       }
       lse2[r] = v == -INFINITY ? INFINITY : v;           // a row that sees no key adds nothing
     }
     __syncthreads();
-    for (int blk = blk0 + half; blk < blk1; blk += 2) {
-      if (blk * kCacheBlock + slot >= at.len) continue;
-      const int page = p.table[static_cast<long long>(at.b) * p.max_blocks + blk];
-      if (page < 0 || page >= p.c.num_blocks) continue;
-      float sum = 0.f;
+    // four blocks a thread at a time: the tables' entries, then the scores and weights
+    for (int blk = blk0 + half; blk < blk1; blk += 8) {
+      int page[4];
+      float old[4], sum[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int bk = blk + 2 * k;
+        page[k] = bk < blk1 && bk * kCacheBlock + slot < at.len ? p.table[static_cast<long long>(at.b) * p.max_blocks + bk] : -1;
+        if (page[k] >= p.c.num_blocks) page[k] = -1;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        old[k] = sum[k] = 0.f;
+        // (a decay of 0 drops what was there, a NaN too)
+        if (page[k] >= 0 && p.decay != 0.f)
+          old[k] = p.c.weight[(static_cast<size_t>(page[k]) * p.c.Hkv + h) * kCacheBlock + slot];
+      }
       for (int chunk = 0; chunk < p.chunks; ++chunk) {
-        const size_t unit = static_cast<size_t>(at.before + (h * p.chunks + chunk) * at.nblk + blk);
-        const float4* const x = reinterpret_cast<const float4*>(p.scores + (unit * kCacheBlock + slot) * cols);
         const int rows = min(cols, p.R - chunk * cols);
+        const size_t unit = static_cast<size_t>(at.before + (h * p.chunks + chunk) * at.nblk + blk);
+        const float4* const x = reinterpret_cast<const float4*>(p.scores + (unit * kCacheBlock + slot) * p.score_row);
+        const int step = 2 * kCacheBlock * p.score_row / 4;   // float4 from block to block
         for (int q = 0; q < rows; q += 4) {
-          const float4 y = x[q / 4];
           const float* const l = lse2 + chunk * cols + q;
-          sum += ex2_approx(y.x - l[0]);
-          if (q + 1 < rows) sum += ex2_approx(y.y - l[1]);
-          if (q + 2 < rows) sum += ex2_approx(y.z - l[2]);
-          if (q + 3 < rows) sum += ex2_approx(y.w - l[3]);
+          float4 y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (page[k] >= 0) y[k] = x[k * step + q / 4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (page[k] >= 0) {
+              sum[k] += ex2_approx(y[k].x - l[0]);
+              if (q + 1 < rows) sum[k] += ex2_approx(y[k].y - l[1]);
+              if (q + 2 < rows) sum[k] += ex2_approx(y[k].z - l[2]);
+              if (q + 3 < rows) sum[k] += ex2_approx(y[k].w - l[3]);
+            }
         }
       }
-      float* const dst = p.c.weight + (static_cast<size_t>(page) * p.c.Hkv + h) * kCacheBlock + slot;
-      // (a decay of 0 drops what was there, a NaN too)
-      *dst = (p.decay == 0.f ? 0.f : p.decay * *dst) + sum;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (page[k] >= 0)
+          p.c.weight[(static_cast<size_t>(page[k]) * p.c.Hkv + h) * kCacheBlock + slot] = p.decay * old[k] + sum[k];
     }
     u += blk1 - blk0;
   }
@@ -907,8 +956,7 @@ cudaError_t launch_fwd(const CUtensorMap& mk, const CUtensorMap& mv, const Cache
     return cudaFuncSetAttribute(cache8_fwd_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, R>::kSmem);
   });
   if (e != cudaSuccess) return e;
-  cache8_fwd_kernel<D, R><<<parts, kThreads, Cfg<D, R>::kSmem, stream>>>(mk, mv, p);
-  return cudaGetLastError();
+  return launch_early(cache8_fwd_kernel<D, R>, dim3(parts), dim3(kThreads), Cfg<D, R>::kSmem, stream, mk, mv, p);
 }
 
 template <int D>
@@ -923,17 +971,7 @@ cudaError_t launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const Cache
   const long long blocks = static_cast<long long>(p.B) * p.c.Hkv * p.max_blocks;
   const int weigh = p.add_weights ? static_cast<int>(blocks < kWeightCtas ? blocks : kWeightCtas) : 0;
   if (join + weigh == 0) return cudaSuccess;
-  // launched while the first kernel runs: its start is hidden behind it
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(join + weigh);
-  cfg.blockDim = dim3(kFinishWarps * 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute early[1];
-  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = early;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache8_finish_kernel<D>, p, cols, parts, join);
+  return launch_early(cache8_finish_kernel<D>, dim3(join + weigh), dim3(kFinishWarps * 32), 0, stream, p, cols, parts, join);
 }
 
 }  // namespace

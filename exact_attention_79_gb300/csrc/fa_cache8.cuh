@@ -38,4 +38,26 @@ __device__ __forceinline__ int cache_length(const int* lengths, int b, int max_b
   return max(0, min(lengths[b], max_blocks * kCacheBlock));
 }
 
+// Launch that may be set up while the kernel before it in the stream still runs
+// (programmatic dependent launch): a kernel launched so calls wait_before(), which
+// returns when that one has ended and its writes are seen, before it reads or
+// writes anything that is not its own; one that calls let_next() allows the next
+// kernel's set-up from there on.
+__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename... Params, typename... Args>
+inline cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 }  // namespace fa

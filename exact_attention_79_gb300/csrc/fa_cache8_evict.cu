@@ -31,6 +31,8 @@ __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Cache8
   __shared__ int warp_eq[32], warp_sel[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.y, h = blockIdx.x;
+  let_next();
+  wait_before();
   const int n = cache_length(p.lengths, b, p.max_blocks);
   int* const kept = p.kept + (static_cast<size_t>(b) * p.c.Hkv + h) * p.keep;
   if (h == 0 && tid == 0) p.new_lengths[b] = min(n, p.keep);
@@ -128,6 +130,8 @@ __global__ void __launch_bounds__(kGatherThreads) cache8_gather_kernel(const Cac
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / p.to_blocks, blk = blockIdx.x - b * p.to_blocks;
   const int h = blockIdx.y, which = blockIdx.z;
+  let_next();
+  wait_before();
   const int n = cache_length(p.lengths, b, p.max_blocks);
   const int cnt = min(kCacheBlock, min(n, p.keep) - blk * kCacheBlock);
   if (cnt <= 0) return;
@@ -200,11 +204,9 @@ __global__ void __launch_bounds__(kGatherThreads) cache8_gather_kernel(const Cac
 }  // namespace
 
 cudaError_t launch_cache8_evict(const Cache8EvictParams& p, cudaStream_t stream) {
-  cache8_select_kernel<<<dim3(p.c.Hkv, p.B), kSelThreads, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_early(cache8_select_kernel, dim3(p.c.Hkv, p.B), dim3(kSelThreads), 0, stream, p);
   if (e != cudaSuccess) return e;
-  cache8_gather_kernel<<<dim3(p.B * p.to_blocks, p.c.Hkv, 2), kGatherThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_early(cache8_gather_kernel, dim3(p.B * p.to_blocks, p.c.Hkv, 2), dim3(kGatherThreads), 0, stream, p);
 }
 
 }  // namespace fa

@@ -41,6 +41,8 @@ __global__ void __launch_bounds__(kThreads) cache8_append_kernel(const Cache8App
   __shared__ int item[2];                       // sequence, block of it
   __shared__ float warp_max[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  let_next();
+  wait_before();
   const long long cap = static_cast<long long>(p.max_blocks) * kCacheBlock;
   // tokens [a, e) of sequence b go to positions from s on
   auto range = [&](int b, int& a, int& e, int& s) {
@@ -149,8 +151,7 @@ cudaError_t launch_cache8_append(const Cache8AppendParams& p, cudaStream_t strea
   // n tokens touch at most (n + 126) / 64 blocks of a sequence, and no more than n
   const long long most = (static_cast<long long>(p.T) + 126LL * p.B) / kCacheBlock;
   const unsigned items = static_cast<unsigned>(most < p.T ? most : p.T);
-  cache8_append_kernel<<<dim3(items, p.c.Hkv, 2), kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_early(cache8_append_kernel, dim3(items, p.c.Hkv, 2), dim3(kThreads), 0, stream, p);
 }
 
 }  // namespace fa

@@ -171,7 +171,8 @@ struct Cache8Params {
   int test_stall;                  // 1: the issuer first waits on a barrier nothing arrives on (timeout test)
   float* part_o;                   // partial results: [2 parts][columns][D] and [2 parts][columns][3]
   float* part_s;
-  float* scores;                   // with add_weights, else null: [units][64][columns] log2-scaled scores
+  float* scores;                   // with add_weights, else null: [units][64][score_row] log2-scaled scores
+  int score_row;                   // rows of a chunk, up to a multiple of 4
 };
 struct Cache8EvictParams {
   Cache8Pools c;
