@@ -756,18 +756,19 @@ struct RowParts {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kFinishWarps * 32) cache8_finish_kernel(const Cache8Params p, int cols, int ctas, int join_ctas) {
+__global__ void __launch_bounds__(kFinishWarps * 32, 8) cache8_finish_kernel(const Cache8Params p, int cols, int ctas, int shares) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int total = line_total(p, lane);                 // (lengths are the caller's: no need to wait for them)
   const int parts = line_parts(total, ctas);
   const int per_block = p.c.Hkv * p.chunks;
   __shared__ float lse2[kCache8MaxRows];
-  if (static_cast<int>(blockIdx.x) < join_ctas) {
+  if (static_cast<int>(blockIdx.x) >= shares) {          // (the weights' CTAs first: they take longer)
     // ---- join: one row of the B * Hkv * R; its parts dealt out to the warps
     __shared__ float4 sum_o[kFinishWarps][32 * (D / 128)];
     __shared__ float sum_l[kFinishWarps], top_l[kFinishWarps], top_o[kFinishWarps];
     const int per_seq = p.c.Hkv * p.R;
-    const int b = static_cast<int>(blockIdx.x) / per_seq, hr = static_cast<int>(blockIdx.x) - b * per_seq;
+    const int row = static_cast<int>(blockIdx.x) - shares;
+    const int b = row / per_seq, hr = row - b * per_seq;
     const int h = hr / p.R, r = hr - h * p.R;
     int before = 0;
     for (int i = lane; i < b; i += 32) before += line_blocks(p, i);
@@ -868,7 +869,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32) cache8_finish_kernel(const 
   // ---- weights: an equal share of the (sequence, KV head, block), two at a time,
   // one thread per token
   const int all = total / p.chunks;                      // (sequence, KV head, block)
-  const int share = static_cast<int>(blockIdx.x) - join_ctas, shares = static_cast<int>(gridDim.x) - join_ctas;
+  const int share = static_cast<int>(blockIdx.x);
   const int w0 = part_begin(all, share, shares), w1 = part_begin(all, share + 1, shares);
   if (w0 >= w1) return;
   Place at;
@@ -882,42 +883,42 @@ __global__ void __launch_bounds__(kFinishWarps * 32) cache8_finish_kernel(const 
     const int h = in_seq / at.nblk, blk0 = in_seq - h * at.nblk;
     const int blk1 = min(at.nblk, blk0 + (w1 - u));
     __syncthreads();
-    for (int r = threadIdx.x; r < p.R; r += kFinishWarps * 32) {
-      // a row in several parts is being joined by another CTA: its LSE from the parts, as there
+    for (int r = warp; r < p.R; r += kFinishWarps) {
+      // a row in several parts is being joined by another CTA: its LSE from the parts, one per lane
       const RowParts rp(total, parts, at.before + (h * p.chunks + r / cols) * at.nblk, at.nblk, cols, r % cols);
       float v;
       if (rp.c0 == rp.c1) {
         v = p.lse[(static_cast<size_t>(at.b) * p.Hq + static_cast<size_t>(h) * p.G) * p.Nq + r] * kLog2e;
       } else {
         float ml = -INFINITY, sum = 0.f;
-#pragma unroll 4
-        for (int c = rp.c0; c <= rp.c1; ++c) ml = fmaxf(ml, p.part_s[rp.slot(c) * 3]);
-#pragma unroll 4
-        for (int c = rp.c0; c <= rp.c1; ++c) {
+        for (int c = rp.c0 + lane; c <= rp.c1; c += 32) {
           const float* const s3 = p.part_s + rp.slot(c) * 3;
-          sum += s3[0] == -INFINITY ? s3[1] : s3[1] * ex2_approx(s3[0] - ml);
+          const float m = s3[0], s = s3[1], now = fmaxf(ml, m);
+          sum = (ml == -INFINITY ? sum : sum * ex2_approx(ml - now)) + (m == -INFINITY ? s : s * ex2_approx(m - now));
+          ml = now;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const float m = __shfl_xor_sync(0xffffffffu, ml, o), s = __shfl_xor_sync(0xffffffffu, sum, o), now = fmaxf(ml, m);
+          sum = (ml == -INFINITY ? sum : sum * ex2_approx(ml - now)) + (m == -INFINITY ? s : s * ex2_approx(m - now));
+          ml = now;
         }
         v = sum == 0.f ? -INFINITY : ml + log2f(sum);
       }
-      lse2[r] = v == -INFINITY ? INFINITY : v;           // a row that sees no key adds nothing
+      if (lane == 0) lse2[r] = v == -INFINITY ? INFINITY : v;   // a row that sees no key adds nothing
     }
     __syncthreads();
-    // four blocks a thread at a time: the tables' entries, then the scores and weights
+    // four blocks a thread at a time, the tables' entries and the scores together; then the weights
     for (int blk = blk0 + half; blk < blk1; blk += 8) {
       int page[4];
-      float old[4], sum[4];
+      float sum[4];
+      bool there[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int bk = blk + 2 * k;
-        page[k] = bk < blk1 && bk * kCacheBlock + slot < at.len ? p.table[static_cast<long long>(at.b) * p.max_blocks + bk] : -1;
-        if (page[k] >= p.c.num_blocks) page[k] = -1;
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        old[k] = sum[k] = 0.f;
-        // (a decay of 0 drops what was there, a NaN too)
-        if (page[k] >= 0 && p.decay != 0.f)
-          old[k] = p.c.weight[(static_cast<size_t>(page[k]) * p.c.Hkv + h) * kCacheBlock + slot];
+        there[k] = bk < blk1 && bk * kCacheBlock + slot < at.len;
+        page[k] = there[k] ? p.table[static_cast<long long>(at.b) * p.max_blocks + bk] : -1;
+        sum[k] = 0.f;
       }
       for (int chunk = 0; chunk < p.chunks; ++chunk) {
         const int rows = min(cols, p.R - chunk * cols);
@@ -929,10 +930,10 @@ __global__ void __launch_bounds__(kFinishWarps * 32) cache8_finish_kernel(const 
           float4 y[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (page[k] >= 0) y[k] = x[k * step + q / 4];
+            if (there[k]) y[k] = x[k * step + q / 4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (page[k] >= 0) {
+            if (there[k]) {
               sum[k] += ex2_approx(y[k].x - l[0]);
               if (q + 1 < rows) sum[k] += ex2_approx(y[k].y - l[1]);
               if (q + 2 < rows) sum[k] += ex2_approx(y[k].z - l[2]);
@@ -940,10 +941,19 @@ __global__ void __launch_bounds__(kFinishWarps * 32) cache8_finish_kernel(const 
             }
         }
       }
+      float old[4];
+      float* dst[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        old[k] = 0.f;
+        there[k] = there[k] && page[k] >= 0 && page[k] < p.c.num_blocks;
+        dst[k] = p.c.weight + (static_cast<size_t>(page[k]) * p.c.Hkv + h) * kCacheBlock + slot;
+        // (a decay of 0 drops what was there, a NaN too)
+        if (there[k] && p.decay != 0.f) old[k] = *dst[k];
+      }
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (page[k] >= 0)
-          p.c.weight[(static_cast<size_t>(page[k]) * p.c.Hkv + h) * kCacheBlock + slot] = p.decay * old[k] + sum[k];
+        if (there[k]) *dst[k] = p.decay * old[k] + sum[k];
     }
     u += blk1 - blk0;
   }
@@ -971,7 +981,7 @@ cudaError_t launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const Cache
   const long long blocks = static_cast<long long>(p.B) * p.c.Hkv * p.max_blocks;
   const int weigh = p.add_weights ? static_cast<int>(blocks < kWeightCtas ? blocks : kWeightCtas) : 0;
   if (join + weigh == 0) return cudaSuccess;
-  return launch_early(cache8_finish_kernel<D>, dim3(join + weigh), dim3(kFinishWarps * 32), 0, stream, p, cols, parts, join);
+  return launch_early(cache8_finish_kernel<D>, dim3(join + weigh), dim3(kFinishWarps * 32), 0, stream, p, cols, parts, weigh);
 }
 
 }  // namespace
