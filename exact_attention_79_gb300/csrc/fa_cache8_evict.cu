@@ -3,9 +3,11 @@
 // Per (sequence, KV head) of n tokens, `keep` of them stay: the last `recent`
 // and, of the others, the keep - recent with the largest weights (ties to the
 // lower position), all in their order. Two launches:
-//  1. cache8_select_kernel  one CTA per (sequence, head): the weights' order
-//     as integers, the smallest kept one by four passes over 8 bits each
-//     (histograms), then the positions, in order, by block-wide counts.
+//  1. cache8_select_kernel  one cluster per (sequence, head), a stretch of the tokens
+//     to each of its CTAs: the weights, read once, lie in shared memory as integers of
+//     the same order; the smallest kept one is found digit by digit (11, 11 and 10 bits;
+//     histograms that the CTAs read from one another), then every warp counts the
+//     tokens of its stretch that stay and writes their positions behind those before.
 //  2. cache8_gather_kernel  one CTA per (destination block, head, K or V): the
 //     kept tokens' codes, re-encoded with a scale of their own.
 #include "fa_cache8.cuh"
@@ -13,9 +15,11 @@
 namespace fa {
 namespace {
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kSelKeys = 49152;                 // keys of a CTA that stay in shared memory (192 KB)
 constexpr int kGatherThreads = 128;
-constexpr int kMaxChunks = kCacheBlock * 256 / 16 / kGatherThreads;   // 16-code chunks per thread, d <= 256
 
 // Floats as integers of the same order; -0 as 0, NaN above everything.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -24,107 +28,200 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Cache8EvictParams p) {
-  __shared__ int hist[256];
-  __shared__ uint32_t s_prefix;
+// All CTAs of the cluster meet; what they wrote before is seen after.
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// Address of this CTA's shared memory address `a` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(uint32_t a, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ int4 load_cluster4(uint32_t a) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ int warp_scan(int x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// Grid (cluster, heads, sequences). `room`: keys that shared memory holds.
+__global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Cache8EvictParams p, int room) {
+  extern __shared__ __align__(16) uint32_t keys[];       // [room] of this CTA's stretch; 0, below all keys, behind it
+  __shared__ __align__(16) int hist[2][kBins];
+  __shared__ int warp_sum[kSelWarps];
+  __shared__ int warp_eq[kSelWarps], warp_above[kSelWarps];
+  __shared__ __align__(16) int counts[4];                // this CTA's: equal, above
+  __shared__ uint32_t s_digit;
   __shared__ int s_need;
-  __shared__ int warp_eq[32], warp_sel[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.y, h = blockIdx.x;
+  const int b = blockIdx.z, h = blockIdx.y, rank = blockIdx.x, ctas = gridDim.x;
   let_next();
   wait_before();
   const int n = cache_length(p.lengths, b, p.max_blocks);
   int* const kept = p.kept + (static_cast<size_t>(b) * p.c.Hkv + h) * p.keep;
-  if (h == 0 && tid == 0) p.new_lengths[b] = min(n, p.keep);
-  if (n <= p.keep) {
-    for (int i = tid; i < p.keep; i += kSelThreads) kept[i] = i < n ? i : -1;
+  const int me = rank * kSelThreads + tid, all = ctas * kSelThreads;
+  if (h == 0 && me == 0) p.new_lengths[b] = min(n, p.keep);
+  if (n <= p.keep) {                                     // (all CTAs of the cluster)
+    for (int i = me; i < p.keep; i += all) kept[i] = i < n ? i : -1;
     return;
   }
-  const int nc = n - p.recent;                   // candidates
-  const int need_all = p.keep - p.recent;        // to choose among them, < nc
+  const int nc = n - p.recent;                           // candidates
+  const int need_all = p.keep - p.recent;                // to choose among them, < nc
+  for (int i = me; i < p.recent; i += all) kept[need_all + i] = nc + i;
+  if (need_all == 0) return;
+  // this CTA's stretch [i0, i1), and each warp's: whole blocks of 64 tokens
+  const int cta_blocks = (nc + kCacheBlock * ctas - 1) / (kCacheBlock * ctas);
+  const int warp_blocks = (cta_blocks + kSelWarps - 1) / kSelWarps;
+  const int i0 = min(nc, rank * cta_blocks * kCacheBlock), i1 = min(nc, i0 + cta_blocks * kCacheBlock);
+  const int w0 = warp * warp_blocks * kCacheBlock, w1 = min(cta_blocks * kCacheBlock, w0 + warp_blocks * kCacheBlock);
   const int* const table = p.table + static_cast<long long>(b) * p.max_blocks;
-  auto key_at = [&](int i) -> uint32_t {
+  // four keys from token i0 + at on (at a multiple of 4), from memory
+  auto keys_at = [&](int at) -> uint4 {
+    const int i = i0 + at;
+    if (i >= i1) return make_uint4(0, 0, 0, 0);
     const int page = table[i / kCacheBlock];
-    if (page < 0 || page >= p.c.num_blocks) return order_key(0.f);
-    return order_key(p.c.weight[(static_cast<size_t>(page) * p.c.Hkv + h) * kCacheBlock + i % kCacheBlock]);
+    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (page >= 0 && page < p.c.num_blocks)
+      w = *reinterpret_cast<const float4*>(p.c.weight + (static_cast<size_t>(page) * p.c.Hkv + h) * kCacheBlock + i % kCacheBlock);
+    return make_uint4(order_key(w.x), i + 1 < i1 ? order_key(w.y) : 0u, i + 2 < i1 ? order_key(w.z) : 0u,
+                      i + 3 < i1 ? order_key(w.w) : 0u);
   };
-  if (need_all > 0) {
-    // the key of the last one chosen, digit by digit from the top
-    uint32_t prefix = 0;
-    int need = need_all;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      const uint32_t high = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-      for (int i = tid; i < nc; i += kSelThreads) {
-        const uint32_t key = key_at(i);
-        if ((key & high) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1);
-      }
-      __syncthreads();
-      if (warp == 0) {
-        // bins from the largest down, 8 per lane: the bin where the count reaches `need`
-        int sum = 0;
-        for (int e = 0; e < 8; ++e) sum += hist[255 - (lane * 8 + e)];
-        int incl = sum;
+  // (a stretch longer than shared memory's room is read again where it does not fit)
+  auto keys4 = [&](int at) -> uint4 { return at < room ? *reinterpret_cast<const uint4*>(keys + at) : keys_at(at); };
+  const int held = min(room, cta_blocks * kCacheBlock);
+#pragma unroll 4
+  for (int at = tid * 4; at < held; at += kSelThreads * 4) *reinterpret_cast<uint4*>(keys + at) = keys_at(at);
+  for (int i = tid; i < kBins; i += kSelThreads) hist[0][i] = 0;
+  __syncthreads();
+
+  // the key of the last one chosen, digit by digit from the top
+  uint32_t prefix = 0, mask = 0;
+  int need = need_all;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t digit = pass == 2 ? 1023u : 2047u;
+    int* const bins = hist[pass & 1];
+    for (int at = tid * 4; at < cta_blocks * kCacheBlock; at += kSelThreads * 4) {
+      const uint4 k4 = keys4(at);
+      const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += y;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, incl >= need);
-        if (lane == __ffs(hit) - 1) {
-          int left = need - (incl - sum);
-          for (int e = 0; e < 8; ++e) {
-            const int bin = 255 - (lane * 8 + e);
-            if (hist[bin] >= left) {
-              s_prefix = prefix | static_cast<uint32_t>(bin) << shift;
-              s_need = left;
-              break;
-            }
-            left -= hist[bin];
-          }
-        }
-      }
-      __syncthreads();
-      prefix = s_prefix;
-      need = s_need;
+      for (int e = 0; e < 4; ++e)
+        if ((k[e] & mask) == prefix) atomicAdd(&bins[(k[e] >> shift) & digit], 1);
     }
-    // positions in order: keys above `prefix`, and the first `need` equal to it
-    int eq_base = 0, sel_base = 0;
-    for (int i0 = 0; i0 < nc; i0 += kSelThreads) {
-      const int i = i0 + tid;
-      const uint32_t key = i < nc ? key_at(i) : 0u;
-      const bool eq = i < nc && key == prefix, above = i < nc && key > prefix;
-      const unsigned beq = __ballot_sync(0xffffffffu, eq), bab = __ballot_sync(0xffffffffu, above);
-      if (lane == 0) {
-        warp_eq[warp] = __popc(beq);
-        warp_sel[warp] = __popc(bab);
-      }
-      __syncthreads();
-      int eq_before = eq_base, above_before = 0, eq_total = 0, above_total = 0;
-      for (int w = 0; w < 32; ++w) {
-        if (w < warp) {
-          eq_before += warp_eq[w];
-          above_before += warp_sel[w];
+    cluster_meet();
+    // (the other histogram has been read by all: they were here)
+    for (int i = tid; i < kBins; i += kSelThreads) hist[(pass + 1) & 1][i] = 0;
+    // bins from the largest down, 4 per thread: the one where the count reaches `need`
+    const uint32_t mine = smem_addr(&bins[kBins - 4 - 4 * tid]);
+    int4 c = make_int4(0, 0, 0, 0);
+    for (int r = 0; r < ctas; ++r) {
+      const int4 x = load_cluster4(in_cta(mine, r));
+      c.x += x.x;
+      c.y += x.y;
+      c.z += x.z;
+      c.w += x.w;
+    }
+    const int sum = c.x + c.y + c.z + c.w;
+    int incl = warp_scan(sum, lane);
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) incl += warp_sum[w];
+    if (incl >= need && incl - sum < need) {             // one thread: `need` keys at least have the prefix
+      int left = need - (incl - sum), bin = kBins - 1 - 4 * tid;
+      const int down[4] = {c.w, c.z, c.y, c.x};
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (e == kBins - 1 - 4 * tid - bin && down[e] < left) {
+          left -= down[e];
+          --bin;
         }
-        eq_total += warp_eq[w];
-        above_total += warp_sel[w];
-      }
-      const unsigned below = (1u << lane) - 1u;
-      eq_before += __popc(beq & below);
-      above_before += __popc(bab & below);
-      // chosen before this one: all above, and the equal ones within the first `need`
-      const int at = sel_base + above_before + min(eq_before, need) - min(eq_base, need);
-      if (above || (eq && eq_before < need)) kept[at] = i;
-      sel_base += above_total + min(eq_base + eq_total, need) - min(eq_base, need);
-      eq_base += eq_total;
-      __syncthreads();
+      s_digit = static_cast<uint32_t>(bin);
+      s_need = left;
+    }
+    __syncthreads();
+    prefix |= s_digit << shift;
+    mask |= digit << shift;
+    need = s_need;
+  }
+
+  // keys above `prefix` and those equal to it, of the warps and of the CTAs
+  int eq = 0, above = 0;
+  for (int at = w0; at < w1; at += 128) {
+    const uint4 k4 = at + 4 * lane < w1 ? keys4(at + 4 * lane) : make_uint4(0, 0, 0, 0);
+    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      eq += k[e] == prefix;
+      above += k[e] > prefix;
     }
   }
-  for (int i = tid; i < p.recent; i += kSelThreads) kept[need_all + i] = nc + i;
+  eq = __reduce_add_sync(0xffffffffu, eq);
+  above = __reduce_add_sync(0xffffffffu, above);
+  if (lane == 0) {
+    warp_eq[warp] = eq;
+    warp_above[warp] = above;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const int e = __reduce_add_sync(0xffffffffu, lane < kSelWarps ? warp_eq[lane] : 0);
+    const int a = __reduce_add_sync(0xffffffffu, lane < kSelWarps ? warp_above[lane] : 0);
+    if (lane == 0) {
+      counts[0] = e;
+      counts[1] = a;
+    }
+  }
+  cluster_meet();
+  int eq_before = 0, above_before = 0;
+  for (int r = 0; r < rank; ++r) {
+    const int4 x = load_cluster4(in_cta(smem_addr(counts), r));
+    eq_before += x.x;
+    above_before += x.y;
+  }
+  for (int w = 0; w < warp; ++w) {
+    eq_before += warp_eq[w];
+    above_before += warp_above[w];
+  }
+  // chosen: all above, and the equal ones within the first `need`; positions in order
+  for (int at = w0; at < w1; at += 128) {
+    const int mine = at + 4 * lane;
+    const uint4 k4 = mine < w1 ? keys4(mine) : make_uint4(0, 0, 0, 0);
+    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+    int e4 = 0, a4 = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      e4 += k[e] == prefix;
+      a4 += k[e] > prefix;
+    }
+    // both counts in one scan: at most 128 of each
+    const int both = warp_scan(e4 | a4 << 16, lane);
+    int eqs = eq_before + (both & 0xffff) - e4, aboves = above_before + (both >> 16) - a4;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool same = k[e] == prefix, over = k[e] > prefix;
+      if (over || (same && eqs < need)) kept[aboves + min(eqs, need)] = i0 + mine + e;
+      eqs += same;
+      aboves += over;
+    }
+    const int last = __shfl_sync(0xffffffffu, both, 31);
+    eq_before += last & 0xffff;
+    above_before += last >> 16;
+  }
+  cluster_meet();                                        // until the others have read this CTA's counts
 }
 
-__global__ void __launch_bounds__(kGatherThreads) cache8_gather_kernel(const Cache8EvictParams p) {
+// D: 128 or 256, d at most that.
+template <int D>
+__global__ void __launch_bounds__(kGatherThreads, D == 128 ? 12 : 8) cache8_gather_kernel(const Cache8EvictParams p) {
+  constexpr int kMaxChunks = kCacheBlock * D / 16 / kGatherThreads;    // 16-code chunks per thread
   __shared__ float warp_max[kGatherThreads / 32];
   __shared__ long long src[kCacheBlock];          // (block * Hkv + h) * 64 + slot of a kept token, -1: no such block
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -204,9 +301,32 @@ __global__ void __launch_bounds__(kGatherThreads) cache8_gather_kernel(const Cac
 }  // namespace
 
 cudaError_t launch_cache8_evict(const Cache8EvictParams& p, cudaStream_t stream) {
-  const cudaError_t e = launch_early(cache8_select_kernel, dim3(p.c.Hkv, p.B), dim3(kSelThreads), 0, stream, p);
+  // One CTA per (sequence, head) up to 8192 tokens, eight past that.
+  const int ctas = p.max_blocks > 128 ? 8 : 1;
+  const int most = (p.max_blocks + ctas - 1) / ctas;     // blocks per CTA, more than it will have
+  const int room = most < kSelKeys / kCacheBlock ? most * kCacheBlock : kSelKeys;
+  static PerDeviceOnce attr;
+  cudaError_t e = attr.run([] {
+    return cudaFuncSetAttribute(cache8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4);
+  });
   if (e != cudaSuccess) return e;
-  return launch_early(cache8_gather_kernel, dim3(p.B * p.to_blocks, p.c.Hkv, 2), dim3(kGatherThreads), 0, stream, p);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas, p.c.Hkv, p.B);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(room) * 4;
+  cfg.stream = stream;
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = ctas;
+  attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, cache8_select_kernel, p, room);
+  if (e != cudaSuccess) return e;
+  return launch_early(p.c.d > 128 ? cache8_gather_kernel<256> : cache8_gather_kernel<128>,
+                      dim3(p.B * p.to_blocks, p.c.Hkv, 2), dim3(kGatherThreads), 0, stream, p);
 }
 
 }  // namespace fa

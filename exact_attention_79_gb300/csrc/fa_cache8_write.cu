@@ -12,7 +12,6 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxChunks = kCacheBlock * 256 / 8 / kThreads;   // 16-byte chunks of one block per thread, d <= 256
 
 // Largest finite magnitude of eight bf16; infinities and NaN are left out.
 __device__ __forceinline__ float amax8(const uint4& x) {
@@ -36,58 +35,47 @@ __device__ __forceinline__ uint2 encode8(const uint4& x, float inv) {
   return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
 }
 
-// One CTA per (touched block, KV head, K or V).
-__global__ void __launch_bounds__(kThreads) cache8_append_kernel(const Cache8AppendParams p) {
-  __shared__ int item[2];                       // sequence, block of it
+// One CTA per (touched block, KV head, K or V). D: 128 or 256, d at most that.
+template <int D>
+__global__ void __launch_bounds__(kThreads, D == 128 ? 6 : 4) cache8_append_kernel(const Cache8AppendParams p) {
+  constexpr int kMaxChunks = kCacheBlock * D / 8 / kThreads;   // 16-byte chunks of one block per thread
   __shared__ float warp_max[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   let_next();
   wait_before();
   const long long cap = static_cast<long long>(p.max_blocks) * kCacheBlock;
-  // tokens [a, e) of sequence b go to positions from s on
-  auto range = [&](int b, int& a, int& e, int& s) {
-    a = max(0, min(p.cu[b], p.T));
-    e = max(a, min(p.cu[b + 1], p.T));
-    s = static_cast<int>(max(0LL, min(static_cast<long long>(p.start[b]), cap)));
-    e = static_cast<int>(min(static_cast<long long>(e), a + (cap - s)));    // behind the table's end: not written
-  };
-  if (warp == 0) {
-    int base = 0, found = -1, blk = 0;
-    for (int b0 = 0; b0 < p.B && found < 0; b0 += 32) {
-      int cnt = 0, first = 0;
-      if (b0 + lane < p.B) {
-        int a, e, s;
-        range(b0 + lane, a, e, s);
-        first = s / kCacheBlock;
-        if (e > a) cnt = (s + (e - a) - 1) / kCacheBlock - first + 1;
-      }
-      int incl = cnt;
+  // Tokens [a, e) of sequence b go to positions from s on. Every warp looks for the
+  // CTA's block by itself: one round of loads, and no barrier before the next.
+  int b = -1, blk = 0, a = 0, e = 0, s = 0;
+  for (int b0 = 0, base = 0; b0 < p.B && b < 0; b0 += 32) {
+    int cnt = 0, first = 0;
+    if (b0 + lane < p.B) {
+      a = max(0, min(p.cu[b0 + lane], p.T));
+      e = max(a, min(p.cu[b0 + lane + 1], p.T));
+      s = static_cast<int>(max(0LL, min(static_cast<long long>(p.start[b0 + lane]), cap)));
+      e = static_cast<int>(min(static_cast<long long>(e), a + (cap - s)));  // behind the table's end: not written
+      first = s / kCacheBlock;
+      if (e > a) cnt = (s + (e - a) - 1) / kCacheBlock - first + 1;
+    }
+    int incl = cnt;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      const int i = static_cast<int>(blockIdx.x) - base;
-      const unsigned hit = __ballot_sync(0xffffffffu, i < incl);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        found = b0 + src;
-        blk = __shfl_sync(0xffffffffu, first + i - (incl - cnt), src);
-      }
-      base += __shfl_sync(0xffffffffu, incl, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
     }
-    if (lane == 0) {
-      item[0] = found;
-      item[1] = blk;
+    const int i = static_cast<int>(blockIdx.x) - base;
+    const unsigned hit = __ballot_sync(0xffffffffu, i < incl);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      b = b0 + src;
+      blk = __shfl_sync(0xffffffffu, first + i - (incl - cnt), src);
+      a = __shfl_sync(0xffffffffu, a, src);
+      e = __shfl_sync(0xffffffffu, e, src);
+      s = __shfl_sync(0xffffffffu, s, src);
     }
+    base += __shfl_sync(0xffffffffu, incl, 31);
   }
-  __syncthreads();
-  const int b = item[0], blk = item[1];
   if (b < 0) return;
-  int a, e, s;
-  range(b, a, e, s);
-  const int page = p.table[static_cast<long long>(b) * p.max_blocks + blk];
-  if (page < 0 || page >= p.c.num_blocks) return;
   const int lo = max(0, s - blk * kCacheBlock);
   const int hi = min(kCacheBlock, s + (e - a) - blk * kCacheBlock);
   const int tok0 = a + (blk * kCacheBlock + lo - s);
@@ -97,9 +85,7 @@ __global__ void __launch_bounds__(kThreads) cache8_append_kernel(const Cache8App
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(which ? p.v : p.k) +
                            h * (which ? p.v_sh : p.k_sh);
   const long long st = which ? p.v_st : p.k_st;
-  const size_t ph = static_cast<size_t>(page) * p.c.Hkv + h;
-  uint8_t* codes = (which ? p.c.v : p.c.k) + ph * kCacheBlock * p.c.d;
-  float* scale = (which ? p.c.v_scale : p.c.k_scale) + ph;
+  const int page = p.table[static_cast<long long>(b) * p.max_blocks + blk];   // (needed after the values)
 
   uint4 val[kMaxChunks];
   float amax = 0.f;
@@ -109,12 +95,19 @@ __global__ void __launch_bounds__(kThreads) cache8_append_kernel(const Cache8App
     if (c < chunks) {
       const int row = c / cpr, col = c - row * cpr;
       val[i] = *reinterpret_cast<const uint4*>(x + (tok0 + row) * st + col * 8);
-      amax = fmaxf(amax, amax8(val[i]));
+    } else {
+      val[i] = make_uint4(0, 0, 0, 0);
     }
   }
+  if (page < 0 || page >= p.c.num_blocks) return;
+  const size_t ph = static_cast<size_t>(page) * p.c.Hkv + h;
+  uint8_t* codes = (which ? p.c.v : p.c.k) + ph * kCacheBlock * p.c.d;
+  float* scale = (which ? p.c.v_scale : p.c.k_scale) + ph;
+  const float old = lo > 0 ? *scale : 0.f;                    // read before the barrier, written after it
+#pragma unroll
+  for (int i = 0; i < kMaxChunks; ++i) amax = fmaxf(amax, amax8(val[i]));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const float old = lo > 0 ? *scale : 0.f;                    // read before the barrier, written after it
   if (lane == 0) warp_max[warp] = amax;
   __syncthreads();
 #pragma unroll
@@ -151,7 +144,7 @@ cudaError_t launch_cache8_append(const Cache8AppendParams& p, cudaStream_t strea
   // n tokens touch at most (n + 126) / 64 blocks of a sequence, and no more than n
   const long long most = (static_cast<long long>(p.T) + 126LL * p.B) / kCacheBlock;
   const unsigned items = static_cast<unsigned>(most < p.T ? most : p.T);
-  return launch_early(cache8_append_kernel, dim3(items, p.c.Hkv, 2), dim3(kThreads), 0, stream, p);
+  return launch_early(p.c.d > 128 ? cache8_append_kernel<256> : cache8_append_kernel<128>, dim3(items, p.c.Hkv, 2), dim3(kThreads), 0, stream, p);
 }
 
 }  // namespace fa

@@ -337,6 +337,17 @@ def test_evict_bit_for_bit(fa, lens, keep, recent, Hkv, d, ties):
         assert np.array_equal(getattr(g, n).cpu().numpy(), want[n], equal_nan=want[n].dtype == np.float32), n
 
 
+@pytest.mark.parametrize("lens,keep,recent,Hkv", [
+    ([9000, 20000, 100, 8193], 3000, 77, 2),          # several CTAs share a sequence; one has less than a stretch
+    ([8300], 8299, 0, 1),                             # all but one
+    ([8300], 8200, 8199, 1),                          # one besides the recent ones
+    ([430001], 66000, 64, 1),                         # more keys than the CTAs' shared memory holds
+])
+@pytest.mark.parametrize("ties", [False, True])
+def test_evict_long_caches(fa, lens, keep, recent, Hkv, ties):
+    test_evict_bit_for_bit(fa, lens, keep, recent, Hkv, 16, ties)
+
+
 def test_evict_with_absent_blocks(fa):
     lens, keep = [200], 120
     c, table = make(21, lens, 2, 64, spare=2)
