@@ -5,11 +5,13 @@
 // lower position), all in their order. Two launches:
 //  1. cache8_select_kernel  one cluster per (sequence, head), a stretch of the tokens
 //     to each of its CTAs: the weights, read once, lie in shared memory as integers of
-//     the same order; the smallest kept one is found digit by digit (11, 11 and 10 bits;
+//     the same order; the smallest kept one is found digit by digit (8 bits each;
 //     histograms that the CTAs read from one another), then every warp counts the
 //     tokens of its stretch that stay and writes their positions behind those before.
 //  2. cache8_gather_kernel  one CTA per (destination block, head, K or V): the
 //     kept tokens' codes, re-encoded with a scale of their own.
+#include <cuda_fp16.h>
+
 #include "fa_cache8.cuh"
 
 namespace fa {
@@ -17,9 +19,22 @@ namespace {
 
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kSelCtas = 8;                     // CTAs of a cluster at most
+constexpr int kBins = 256;
 constexpr int kSelKeys = 49152;                 // keys of a CTA that stay in shared memory (192 KB)
 constexpr int kGatherThreads = 128;
+
+__device__ __forceinline__ __half2 as_half2(uint32_t x) {
+  __half2 h;
+  asm("mov.b32 %0, %1;" : "=r"(reinterpret_cast<uint32_t&>(h)) : "r"(x));
+  return h;
+}
+// Two halves to e4m3 codes, rounded to nearest even, saturating to +-448.
+__device__ __forceinline__ uint32_t pack_halves(__half2 x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(reinterpret_cast<uint32_t&>(x)));
+  return r;
+}
 
 // Floats as integers of the same order; -0 as 0, NaN above everything.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -38,9 +53,9 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t a, int rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
   return r;
 }
-__device__ __forceinline__ int4 load_cluster4(uint32_t a) {
-  int4 v;
-  asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+__device__ __forceinline__ int load_cluster(uint32_t a) {
+  int v;
+  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
 __device__ __forceinline__ int warp_scan(int x, int lane) {
@@ -55,10 +70,10 @@ __device__ __forceinline__ int warp_scan(int x, int lane) {
 // Grid (cluster, heads, sequences). `room`: keys that shared memory holds.
 __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Cache8EvictParams p, int room) {
   extern __shared__ __align__(16) uint32_t keys[];       // [room] of this CTA's stretch; 0, below all keys, behind it
-  __shared__ __align__(16) int hist[2][kBins];
-  __shared__ int warp_sum[kSelWarps];
+  __shared__ int hist[2][kBins];
+  __shared__ int warp_sum[kBins / 32];
   __shared__ int warp_eq[kSelWarps], warp_above[kSelWarps];
-  __shared__ __align__(16) int counts[4];                // this CTA's: equal, above
+  __shared__ int counts[2];                              // this CTA's: equal, above
   __shared__ uint32_t s_digit;
   __shared__ int s_need;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -97,59 +112,57 @@ __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Cache8
   // (a stretch longer than shared memory's room is read again where it does not fit)
   auto keys4 = [&](int at) -> uint4 { return at < room ? *reinterpret_cast<const uint4*>(keys + at) : keys_at(at); };
   const int held = min(room, cta_blocks * kCacheBlock);
-#pragma unroll 4
-  for (int at = tid * 4; at < held; at += kSelThreads * 4) *reinterpret_cast<uint4*>(keys + at) = keys_at(at);
-  for (int i = tid; i < kBins; i += kSelThreads) hist[0][i] = 0;
+  if (tid < kBins) hist[0][tid] = hist[1][tid] = 0;
   __syncthreads();
 
   // the key of the last one chosen, digit by digit from the top
   uint32_t prefix = 0, mask = 0;
   int need = need_all;
 #pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const uint32_t digit = pass == 2 ? 1023u : 2047u;
-    int* const bins = hist[pass & 1];
-    for (int at = tid * 4; at < cta_blocks * kCacheBlock; at += kSelThreads * 4) {
-      const uint4 k4 = keys4(at);
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    int* const bins = hist[(shift >> 3) & 1];
+    auto add = [&](const uint4& k4) {
       const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if ((k[e] & mask) == prefix) atomicAdd(&bins[(k[e] >> shift) & digit], 1);
+        if ((k[e] & mask) == prefix) atomicAdd(&bins[(k[e] >> shift) & 255u], 1);
+    };
+    int at = tid * 4;
+    if (shift == 24) {
+#pragma unroll 2
+      for (; at < held; at += kSelThreads * 4) {
+        const uint4 k4 = keys_at(at);
+        *reinterpret_cast<uint4*>(keys + at) = k4;
+        add(k4);
+      }
     }
+    for (; at < cta_blocks * kCacheBlock; at += kSelThreads * 4) add(keys4(at));
     cluster_meet();
-    // (the other histogram has been read by all: they were here)
-    for (int i = tid; i < kBins; i += kSelThreads) hist[(pass + 1) & 1][i] = 0;
-    // bins from the largest down, 4 per thread: the one where the count reaches `need`
-    const uint32_t mine = smem_addr(&bins[kBins - 4 - 4 * tid]);
-    int4 c = make_int4(0, 0, 0, 0);
-    for (int r = 0; r < ctas; ++r) {
-      const int4 x = load_cluster4(in_cta(mine, r));
-      c.x += x.x;
-      c.y += x.y;
-      c.z += x.z;
-      c.w += x.w;
-    }
-    const int sum = c.x + c.y + c.z + c.w;
-    int incl = warp_scan(sum, lane);
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) incl += warp_sum[w];
-    if (incl >= need && incl - sum < need) {             // one thread: `need` keys at least have the prefix
-      int left = need - (incl - sum), bin = kBins - 1 - 4 * tid;
-      const int down[4] = {c.w, c.z, c.y, c.x};
+    // bins from the largest down, one per thread: the one where the count reaches `need`
+    int sum = 0, incl = 0;
+    if (tid < kBins) {
+      // (the other histogram has been read by all: they were here)
+      hist[((shift >> 3) + 1) & 1][tid] = 0;
+      const uint32_t mine = smem_addr(&bins[kBins - 1 - tid]);
 #pragma unroll
-      for (int e = 0; e < 3; ++e)
-        if (e == kBins - 1 - 4 * tid - bin && down[e] < left) {
-          left -= down[e];
-          --bin;
-        }
-      s_digit = static_cast<uint32_t>(bin);
-      s_need = left;
+      for (int r = 0; r < kSelCtas; ++r)
+        if (r < ctas) sum += load_cluster(in_cta(mine, r));
+      incl = warp_scan(sum, lane);
+      if (lane == 31) warp_sum[warp] = incl;
+    }
+    __syncthreads();
+    if (tid < kBins) {
+#pragma unroll
+      for (int w = 0; w < kBins / 32; ++w)
+        if (w < warp) incl += warp_sum[w];
+      if (incl >= need && incl - sum < need) {           // one thread: at least `need` keys have the prefix
+        s_digit = static_cast<uint32_t>(kBins - 1 - tid);
+        s_need = need - (incl - sum);
+      }
     }
     __syncthreads();
     prefix |= s_digit << shift;
-    mask |= digit << shift;
+    mask |= 255u << shift;
     need = s_need;
   }
 
@@ -181,15 +194,18 @@ __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Cache8
   }
   cluster_meet();
   int eq_before = 0, above_before = 0;
-  for (int r = 0; r < rank; ++r) {
-    const int4 x = load_cluster4(in_cta(smem_addr(counts), r));
-    eq_before += x.x;
-    above_before += x.y;
-  }
-  for (int w = 0; w < warp; ++w) {
-    eq_before += warp_eq[w];
-    above_before += warp_above[w];
-  }
+#pragma unroll
+  for (int r = 0; r < kSelCtas; ++r)
+    if (r < rank) {
+      eq_before += load_cluster(in_cta(smem_addr(&counts[0]), r));
+      above_before += load_cluster(in_cta(smem_addr(&counts[1]), r));
+    }
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w)
+    if (w < warp) {
+      eq_before += warp_eq[w];
+      above_before += warp_above[w];
+    }
   // chosen: all above, and the equal ones within the first `need`; positions in order
   for (int at = w0; at < w1; at += 128) {
     const int mine = at + 4 * lane;
@@ -246,31 +262,48 @@ __global__ void __launch_bounds__(kGatherThreads, D == 128 ? 12 : 8) cache8_gath
   __syncthreads();
   const uint8_t* const codes = which ? p.c.v : p.c.k;
   float* const scales = which ? p.c.v_scale : p.c.k_scale;
-  const int cpr = p.c.d / 16, chunks = cnt * cpr;
+  const int cpr = p.c.d / 16;                     // chunks per token
+  // this thread's chunks: tid, tid + kGatherThreads, ... as (row, column)
+  const int drow = kGatherThreads / cpr, dcol = kGatherThreads - drow * cpr;
   uint4 val[kMaxChunks];
   float sc[kMaxChunks];
-  float amax = 0.f;
+  int row = tid / cpr, col = tid - row * cpr;
 #pragma unroll
   for (int k = 0; k < kMaxChunks; ++k) {
-    const int c = tid + k * kGatherThreads;
     val[k] = make_uint4(0, 0, 0, 0);
     sc[k] = 0.f;
-    if (c < chunks) {
-      const int row = c / cpr, col = c - row * cpr;
+    if (row < cnt) {
       const long long at = src[row];
       if (at >= 0) {
         val[k] = *reinterpret_cast<const uint4*>(codes + at * p.c.d + col * 16);
         sc[k] = scales[at / kCacheBlock];
       }
-      const uint32_t w[4] = {val[k].x, val[k].y, val[k].z, val[k].w};
-      uint32_t m = 0;                             // the largest code without its sign; 0x7F is NaN
+    }
+    row += drow;
+    col += dcol;
+    if (col >= cpr) {
+      col -= cpr;
+      ++row;
+    }
+  }
+  float amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < kMaxChunks; ++k) {
+    // the largest magnitude of 16 codes, as halves, exact; a maximum passes over NaN
+    const uint32_t w[4] = {val[k].x, val[k].y, val[k].z, val[k].w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = __vimax3_u16x2(m, w[e] & 0x7F007F00u, (w[e] << 8) & 0x7F007F00u);
+    m = max(m & 0xFFFFu, m >> 16) >> 8;
+    if (m == 0x7Fu) {
+      m = 0;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const uint32_t code = (w[e / 4] >> (8 * (e % 4))) & 0x7Fu;
         m = max(m, code == 0x7Fu ? 0u : code);
       }
-      amax = fmaxf(amax, e4m3x2_to_float2(m).x * sc[k]);
     }
+    amax = fmaxf(amax, e4m3x2_to_float2(m).x * sc[k]);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -286,13 +319,24 @@ __global__ void __launch_bounds__(kGatherThreads, D == 128 ? 12 : 8) cache8_gath
 #pragma unroll
   for (int k = 0; k < kMaxChunks; ++k) {
     const int c = tid + k * kGatherThreads;
-    if (c >= chunks) continue;
+    if (c >= cnt * cpr) continue;
     const uint32_t w[4] = {val[k].x, val[k].y, val[k].z, val[k].w};
     uint32_t r[4];
+    const float ratio = sc[k] * inv;
+    // Scales that are powers of two, as fa_cache8_append makes them: the codes as halves
+    // times the ratio, exact down to 2^-24, where every code has long become 0.
+    if ((__float_as_uint(ratio) & 0x807FFFFFu) == 0 && ratio >= 0x1p-14f && ratio <= 0x1p15f) {
+      const __half2 f = __float2half2_rn(ratio);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 a = e4m3x2_to_float2(w[e] & 0xFFFFu), z = e4m3x2_to_float2(w[e] >> 16);
-      r[e] = pack_e4m3x2(a.x * sc[k] * inv, a.y * sc[k] * inv) | pack_e4m3x2(z.x * sc[k] * inv, z.y * sc[k] * inv) << 16;
+      for (int e = 0; e < 4; ++e)
+        r[e] = pack_halves(__hmul2(as_half2(e4m3x2_to_f16x2(w[e])), f)) |
+               pack_halves(__hmul2(as_half2(e4m3x2_to_f16x2(w[e] >> 16)), f)) << 16;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 a = e4m3x2_to_float2(w[e]), z = e4m3x2_to_float2(w[e] >> 16);
+        r[e] = pack_e4m3x2(a.x * sc[k] * inv, a.y * sc[k] * inv) | pack_e4m3x2(z.x * sc[k] * inv, z.y * sc[k] * inv) << 16;
+      }
     }
     *reinterpret_cast<uint4*>(dst + c * 16) = make_uint4(r[0], r[1], r[2], r[3]);
   }
@@ -302,7 +346,7 @@ __global__ void __launch_bounds__(kGatherThreads, D == 128 ? 12 : 8) cache8_gath
 
 cudaError_t launch_cache8_evict(const Cache8EvictParams& p, cudaStream_t stream) {
   // One CTA per (sequence, head) up to 8192 tokens, eight past that.
-  const int ctas = p.max_blocks > 128 ? 8 : 1;
+  const int ctas = p.max_blocks > 128 ? kSelCtas : 1;
   const int most = (p.max_blocks + ctas - 1) / ctas;     // blocks per CTA, more than it will have
   const int room = most < kSelKeys / kCacheBlock ? most * kCacheBlock : kSelKeys;
   static PerDeviceOnce attr;

@@ -13,17 +13,18 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Largest finite magnitude of eight bf16; infinities and NaN are left out.
-__device__ __forceinline__ float amax8(const uint4& x) {
+// Largest finite magnitude of two bf16; infinities and NaN are left out.
+__device__ __forceinline__ uint32_t finite_max(uint32_t m, uint32_t x) {
+  const uint32_t lo = x & 0x7FFFu, hi = (x >> 16) & 0x7FFFu;
+  m = max(m, lo < 0x7F80u ? lo : 0u);
+  return max(m, hi < 0x7F80u ? hi : 0u);
+}
+// Largest magnitudes of the lower and of the upper halves of eight bf16 and m; NaN are left out.
+__device__ __forceinline__ uint32_t max2(uint32_t m, const uint4& x) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t m = 0;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const uint32_t lo = w[e] & 0x7FFFu, hi = (w[e] >> 16) & 0x7FFFu;
-    m = max(m, lo < 0x7F80u ? lo : 0u);
-    m = max(m, hi < 0x7F80u ? hi : 0u);
-  }
-  return __uint_as_float(m << 16);
+  for (int e = 0; e < 4; ++e) asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[e] & 0x7FFF7FFFu));
+  return m;
 }
 
 __device__ __forceinline__ uint2 encode8(const uint4& x, float inv) {
@@ -88,15 +89,17 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 6 : 4) cache8_append_kern
   const int page = p.table[static_cast<long long>(b) * p.max_blocks + blk];   // (needed after the values)
 
   uint4 val[kMaxChunks];
-  float amax = 0.f;
+  // this thread's chunks: tid, tid + kThreads, ... as (row, column)
+  const int drow = kThreads / cpr, dcol = kThreads - drow * cpr;
+  int row = tid / cpr, col = tid - row * cpr;
 #pragma unroll
   for (int i = 0; i < kMaxChunks; ++i) {
-    const int c = tid + i * kThreads;
-    if (c < chunks) {
-      const int row = c / cpr, col = c - row * cpr;
-      val[i] = *reinterpret_cast<const uint4*>(x + (tok0 + row) * st + col * 8);
-    } else {
-      val[i] = make_uint4(0, 0, 0, 0);
+    val[i] = row < hi - lo ? *reinterpret_cast<const uint4*>(x + (tok0 + row) * st + col * 8) : make_uint4(0, 0, 0, 0);
+    row += drow;
+    col += dcol;
+    if (col >= cpr) {
+      col -= cpr;
+      ++row;
     }
   }
   if (page < 0 || page >= p.c.num_blocks) return;
@@ -104,8 +107,15 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 6 : 4) cache8_append_kern
   uint8_t* codes = (which ? p.c.v : p.c.k) + ph * kCacheBlock * p.c.d;
   float* scale = (which ? p.c.v_scale : p.c.k_scale) + ph;
   const float old = lo > 0 ? *scale : 0.f;                    // read before the barrier, written after it
+  uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < kMaxChunks; ++i) amax = fmaxf(amax, amax8(val[i]));
+  for (int i = 0; i < kMaxChunks; ++i) top = max2(top, val[i]);
+  top = max(top & 0xFFFFu, top >> 16);
+  if (top >= 0x7F80u) {                                       // an infinity: the largest of the others
+    top = 0;
+    for (int i = 0; i < kMaxChunks; ++i) top = finite_max(finite_max(finite_max(finite_max(top, val[i].x), val[i].y), val[i].z), val[i].w);
+  }
+  float amax = __uint_as_float(top << 16);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if (lane == 0) warp_max[warp] = amax;
