@@ -109,19 +109,25 @@ def _shape(q, k):
     return B, Hq, k.shape[1], N, d
 
 
+def _index(device):
+    """The index that tensors on a CUDA `device` report; one that none reports for others."""
+    return device.index if device.type == "cuda" else -2
+
+
 def _require(device, *specs):
     """Refuse, before any launch, a tensor the kernels would read or write past
     its end. specs: (tensor, name, dtype, shape). Every dtype and shape is
     checked before any placement (contiguous, CUDA, on the device of q), so
     the shape rules hold for CPU tensors too."""
     for t, name, dtype, shape in specs:
-        if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        if t.dtype != dtype or (t.shape != shape and tuple(t.shape) != tuple(shape)):
             raise ValueError(f"{name}: expected {dtype} of shape {tuple(shape)}, "
                              f"got {t.dtype} of shape {tuple(t.shape)}")
+    index = _index(device)
     for t, name, _, _ in specs:
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        if not t.is_cuda or t.device != device:
+        if t.get_device() != index:
             raise ValueError(f"{name} must be a CUDA tensor on {device}")
 
 
@@ -345,20 +351,21 @@ def _table_spec(block_table, name="block_table", B=None):
     import torch
     if block_table.dim() != 2 or (B is not None and block_table.shape[0] != B):
         raise ValueError(f"{name} must be [B, max_blocks]")
-    return block_table, name, torch.int32, tuple(block_table.shape)
+    return block_table, name, torch.int32, block_table.shape
 
 
 def _call_on(device, name, *args):
     """A library call on `device`'s current stream, with that device current."""
     import torch
     fn = getattr(load(), name)
-    stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-    if device.index == torch.cuda.current_device():
+    stream = torch._C._cuda_getCurrentRawStream(device.index)      # current_stream() without its Stream object
+    if device.index == torch._C._cuda_getDevice():
         code = fn(*args, stream)
     else:
         with torch.cuda.device(device):
             code = fn(*args, stream)
-    _check(name, code)
+    if code:
+        _check(name, code)
 
 
 def _heads_strides(t, name, H, T, d):
@@ -366,7 +373,7 @@ def _heads_strides(t, name, H, T, d):
     and 16-byte aligned: [H, T, d] itself, or [T, H, d].transpose(0, 1). A dimension of size 1 gets a stride that
     nothing reads through."""
     import torch
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != (H, T, d):
+    if t.dtype != torch.bfloat16 or t.shape != (H, T, d):
         raise ValueError(f"{name}: expected {torch.bfloat16} of shape {(H, T, d)}, got {t.dtype} of shape {tuple(t.shape)}")
     sh, st, sd = t.stride()
     sh, st = (sh if H > 1 else d), (st if T > 1 else d)
@@ -376,8 +383,9 @@ def _heads_strides(t, name, H, T, d):
 
 
 def _placed(device, *named):
+    index = _index(device)
     for t, name in named:
-        if not t.is_cuda or t.device != device:
+        if t.get_device() != index:
             raise ValueError(f"{name} must be a CUDA tensor on {device}")
 
 
@@ -397,7 +405,9 @@ def fwd_packed(q, k, v, cu_seqlens, causal=True, scale=None, out=None, lse=None)
         scale = d ** -0.5
     o = torch.empty_like(q) if out is None else out
     lse = torch.empty((Hq, T), dtype=torch.float32, device=dev) if lse is None else lse
-    strides = [(t, _heads_strides(t, n, H, T, d)) for t, n, H in ((q, "q", Hq), (k, "k", Hkv), (v, "v", Hkv), (o, "out", Hq))]
+    args = []
+    for t, n, H in ((q, "q", Hq), (k, "k", Hkv), (v, "v", Hkv), (o, "out", Hq)):
+        args += (t.data_ptr(), *_heads_strides(t, n, H, T, d))
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must be [S + 1]")
     S = cu_seqlens.shape[0] - 1
@@ -405,8 +415,8 @@ def fwd_packed(q, k, v, cu_seqlens, causal=True, scale=None, out=None, lse=None)
     _placed(dev, (k, "k"), (v, "v"), (o, "out"))
     if T == 0 or S == 0:
         return o, lse
-    args = [x for t, (sh, st) in strides for x in (_ptr(t), sh, st)]
-    _call_on(dev, "fa_fwd_packed", *args, _ptr(lse), _ptr(cu_seqlens), S, T, Hq, Hkv, d, int(bool(causal)), float(scale))
+    _call_on(dev, "fa_fwd_packed", *args, lse.data_ptr(), cu_seqlens.data_ptr(), S, T, Hq, Hkv, d, int(bool(causal)),
+             float(scale))
     return o, lse
 
 
@@ -428,8 +438,8 @@ def cache8_append(cache, k, v, cu_seqlens, block_table, start):
     _placed(dev, (k, "k"), (v, "v"))
     if T == 0:
         return
-    _call_on(dev, "fa_cache8_append", _ptr(k), *ks, _ptr(v), *vs, _ptr(cu_seqlens), _ptr(start), B, T, ctypes.byref(c),
-             _ptr(block_table), block_table.shape[1])
+    _call_on(dev, "fa_cache8_append", k.data_ptr(), *ks, v.data_ptr(), *vs, cu_seqlens.data_ptr(), start.data_ptr(), B, T,
+             ctypes.byref(c), block_table.data_ptr(), block_table.shape[1])
 
 
 def fwd_cache8(q, cache, block_table, lengths, causal=True, scale=None, out=None, lse=None, workspace=None,
@@ -450,19 +460,26 @@ def fwd_cache8(q, cache, block_table, lengths, causal=True, scale=None, out=None
         raise ValueError("weight_decay needs a cache with weights")
     if scale is None:
         scale = d ** -0.5
-    o = torch.empty((B, Hq, Nq, d), dtype=bf16, device=dev) if out is None else out
-    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev) if lse is None else lse
-    table = _table_spec(block_table, B=B)
+    specs += [(q, "q", bf16, (B, Hq, Nq, d)), _table_spec(block_table, B=B), (lengths, "lengths", torch.int32, (B,))]
+    if out is not None:
+        specs.append((out, "out", bf16, (B, Hq, Nq, d)))
+    if lse is not None:
+        specs.append((lse, "lse", torch.float32, (B, Hq, Nq)))
+    if workspace is not None:
+        specs.append((workspace, "workspace", torch.uint8, (workspace.numel(),)))
+    _require(dev, *specs)
+    if out is None:
+        out = torch.empty((B, Hq, Nq, d), dtype=bf16, device=dev)
+    if lse is None:
+        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev)
+    max_blocks, weigh = block_table.shape[1], int(weight_decay is not None)
     if workspace is None:
-        n = lib.fa_fwd_cache8_workspace_bytes(B, Hq, Hkv, Nq, d, block_table.shape[1], int(weight_decay is not None))
-        workspace = torch.empty(int(n), dtype=torch.uint8, device=dev)
-    _require(dev, (q, "q", bf16, (B, Hq, Nq, d)), *specs, table, (lengths, "lengths", torch.int32, (B,)),
-             (o, "out", bf16, (B, Hq, Nq, d)), (lse, "lse", torch.float32, (B, Hq, Nq)),
-             (workspace, "workspace", torch.uint8, (workspace.numel(),)))
-    _call_on(dev, "fa_fwd_cache8", _ptr(q), ctypes.byref(c), _ptr(block_table), block_table.shape[1], _ptr(lengths),
-             _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel(), B, Hq, Nq, int(bool(causal)), float(scale),
-             int(weight_decay is not None), float(weight_decay or 0.0))
-    return o, lse
+        n = lib.fa_fwd_cache8_workspace_bytes(B, Hq, Hkv, Nq, d, max_blocks, weigh)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    _call_on(dev, "fa_fwd_cache8", q.data_ptr(), ctypes.byref(c), block_table.data_ptr(), max_blocks, lengths.data_ptr(),
+             out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), B, Hq, Nq, int(bool(causal)),
+             float(scale), weigh, float(weight_decay or 0.0))
+    return out, lse
 
 
 def cache8_evict(cache, block_table, lengths, keep, recent, to_table, new_lengths=None, kept=None):
@@ -479,8 +496,8 @@ def cache8_evict(cache, block_table, lengths, keep, recent, to_table, new_length
     kept = torch.empty((B, Hkv, keep), dtype=i32, device=dev) if kept is None else kept
     _require(dev, *specs, _table_spec(block_table), _table_spec(to_table, "to_table", B), (lengths, "lengths", i32, (B,)),
              (new_lengths, "new_lengths", i32, (B,)), (kept, "kept", i32, (B, Hkv, keep)))
-    _call_on(dev, "fa_cache8_evict", ctypes.byref(c), _ptr(block_table), block_table.shape[1], _ptr(lengths), B, keep,
-             recent, _ptr(to_table), to_table.shape[1], _ptr(kept), _ptr(new_lengths))
+    _call_on(dev, "fa_cache8_evict", ctypes.byref(c), block_table.data_ptr(), block_table.shape[1], lengths.data_ptr(), B,
+             keep, recent, to_table.data_ptr(), to_table.shape[1], kept.data_ptr(), new_lengths.data_ptr())
     return new_lengths, kept
 
 
