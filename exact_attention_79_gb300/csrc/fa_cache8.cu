@@ -38,6 +38,7 @@ namespace {
 constexpr int kThreads = 224;
 constexpr float kTrail = 4.f;             // log2 of how far a reference may trail
 constexpr float kShift = 4.f;             // y = 2^(x - reference + kShift) <= 2^8
+constexpr int kTurn = 4;                  // blocks' time that a change of row groups costs
 constexpr int kInfo = 8;                  // tiles whose scales wait in shared memory
 
 // Whether `mine` holds for any of the softmax warps' 128 threads, which meet here.
@@ -94,33 +95,47 @@ __device__ __forceinline__ int line_total(const Cache8Params& p, int lane) {
   for (int b = lane; b < p.B; b += 32) sum += line_blocks(p, b);
   return __reduce_add_sync(0xffffffffu, sum) * p.c.Hkv * p.chunks;
 }
-// Parts the line is cut into by a grid of `ctas`: none of them empty, so that
-// every part between a row's first and last has a partial result of it.
-__device__ __forceinline__ int line_parts(int total, int ctas) { return min(ctas, total); }
-__device__ __forceinline__ int part_begin(int total, int i, int parts) {
-  return static_cast<int>(static_cast<long long>(total) * i / parts);
-}
-// the part that unit u belongs to
-__device__ __forceinline__ int part_of(int total, int u, int parts) {
-  return static_cast<int>(((u + 1LL) * parts - 1) / total);
-}
+// The line cut into equal parts for a grid of `ctas`. It is measured in units,
+// but a CTA that goes on to another row group loses the time of a few blocks
+// with the one's results and the other's queries: `turn` places more lie ahead
+// of each group's units. (With units alone CTAs with three groups ended 6 us
+// after those with one, of 59; with the turns all within 4.) A part is at least
+// twice a turn long, so that it has units, and where it begins in a turn its
+// first units are that group's; hence every part between a group's first and
+// last has a partial result of it.
+struct Line {
+  int turn, total, parts;
+  __device__ __forceinline__ Line(const Cache8Params& p, int units, int ctas) {
+    turn = units >> 28 ? 0 : min(kTurn, units / (2 * ctas));
+    total = units + turn * p.B * p.c.Hkv * p.chunks;
+    parts = min(ctas, total);
+  }
+  __device__ __forceinline__ int begin(int i) const {
+    return static_cast<int>(static_cast<long long>(total) * i / parts);
+  }
+  // the part that place u belongs to
+  __device__ __forceinline__ int part_of(int u) const {
+    return static_cast<int>(((u + 1LL) * parts - 1) / total);
+  }
+};
 
 // A place on the line.
 struct Place {
-  int b, before;             // sequence, units before it
+  int b, before;             // sequence, places before it
   int nblk, len;             // its blocks of units and tokens
+  int turn;                  // as the line's; 0: places are units
   __device__ __forceinline__ void load(const Cache8Params& p) {
     len = cache_length(p.lengths, b, p.max_blocks);
     nblk = blocks_of(len);
   }
-  // to the sequence of unit u, by a whole warp
+  // to the sequence of place u, by a whole warp
   __device__ __forceinline__ void find(const Cache8Params& p, int u, int lane) {
     const int per_block = p.c.Hkv * p.chunks;
     int base = 0;
     b = p.B - 1;
     before = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const int cnt = b0 + lane < p.B ? line_blocks(p, b0 + lane) : 0;
+      const int cnt = b0 + lane < p.B ? line_blocks(p, b0 + lane) + turn : 0;
       int incl = cnt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -138,26 +153,27 @@ struct Place {
     }
     load(p);
   }
-  // to the first unit of part `i` of `ctas`, whose units are [u0, u1); false: no such part. By a
+  // to the first place of part `i` of `ctas`, whose places are [u0, u1); false: no such part. By a
   // whole warp; one look at the lengths where a warp holds them all.
   __device__ __forceinline__ bool start(const Cache8Params& p, int i, int ctas, int lane, int& u0, int& u1) {
     const int per_block = p.c.Hkv * p.chunks;
-    int mine = 0, total;
+    int mine = 0, units;
     if (p.B <= 32) {
       mine = lane < p.B ? cache_length(p.lengths, lane, p.max_blocks) : -1;
-      total = __reduce_add_sync(0xffffffffu, mine < 0 ? 0 : blocks_of(mine)) * per_block;
+      units = __reduce_add_sync(0xffffffffu, mine < 0 ? 0 : blocks_of(mine)) * per_block;
     } else {
-      total = line_total(p, lane);
+      units = line_total(p, lane);
     }
-    const int parts = line_parts(total, ctas);
-    if (i >= parts) return false;
-    u0 = part_begin(total, i, parts);
-    u1 = part_begin(total, i + 1, parts);
+    const Line line(p, units, ctas);
+    if (i >= line.parts) return false;
+    u0 = line.begin(i);
+    u1 = line.begin(i + 1);
+    turn = line.turn;
     if (p.B > 32) {
       find(p, u0, lane);
       return true;
     }
-    int incl = mine < 0 ? 0 : blocks_of(mine);
+    int incl = mine < 0 ? 0 : blocks_of(mine) + turn;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -166,14 +182,14 @@ struct Place {
     b = __ffs(__ballot_sync(0xffffffffu, u0 < incl * per_block)) - 1;
     len = __shfl_sync(0xffffffffu, mine, b);
     nblk = blocks_of(len);
-    before = (__shfl_sync(0xffffffffu, incl, b) - nblk) * per_block;
+    before = (__shfl_sync(0xffffffffu, incl, b) - nblk - turn) * per_block;
     return true;
   }
-  // onwards to the sequence of unit u (one that exists)
+  // onwards to the sequence of place u (one that exists)
   __device__ __forceinline__ void go(const Cache8Params& p, int u) {
     const int per_block = p.c.Hkv * p.chunks;
-    while (u - before >= nblk * per_block) {
-      before += nblk * per_block;
+    while (u - before >= (nblk + turn) * per_block) {
+      before += (nblk + turn) * per_block;
       ++b;
       load(p);
     }
@@ -204,17 +220,23 @@ struct Cfg {
   static_assert(kRing >= 3 && kTmem * kPerSm <= 512, "shared memory or TMEM budget");
 };
 
-// A row group's share of a part: blocks [blk0, blk1) of (b, h, chunk).
+// A row group's share of a part: blocks [blk0, blk1) of (b, h, chunk), none where the
+// part ends in the group's turn.
 struct Segment {
   int b, h, chunk, blk0, blk1, nblk, len, tiles;
+  int unit0;                 // units of the line before the group's
+  int next;                  // place where the next segment begins
   __device__ __forceinline__ Segment(const Cache8Params& p, Place& at, int u, int u1) {
     at.go(p, u);
     b = at.b;
     nblk = at.nblk;
     len = at.len;
-    const int row = (u - at.before) / nblk;              // head * chunks + chunk
-    blk0 = u - at.before - row * nblk;
-    blk1 = min(nblk, blk0 + (u1 - u));
+    const int span = nblk + at.turn, row = (u - at.before) / span;     // head * chunks + chunk
+    const int off = u - at.before - row * span;
+    next = min(u1, u + span - off);
+    blk0 = max(0, off - at.turn);
+    blk1 = off + (next - u) - at.turn;
+    unit0 = at.before - at.turn * b * p.c.Hkv * p.chunks + row * nblk;
     h = row / p.chunks;
     chunk = row - h * p.chunks;
     tiles = (blk1 - blk0 + 1) / 2;
@@ -346,7 +368,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           if (lane == 0) mbar_arrive(bar_info(tile % kInfo));
         }
       }
-      u += s.blk1 - s.blk0;
+      u = s.next;
     }
     __syncwarp();
   } else if (warp == 5) {
@@ -374,6 +396,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       };
       for (int u = u0; u < u1 && ok; ++seg) {
         const Segment s(p, at, u, u1);
+        if (s.blk1 <= s.blk0) break;
         ok = wait(bar_q_full(seg % C::kQBufs), (seg / C::kQBufs) & 1, abort_flag, p.timeout_ns);
         if (!ok) break;
         scores(tile, seg);
@@ -398,7 +421,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           mma_commit(bar_p_empty(tile & 1));
           mma_commit(bar_kv_empty(slot));
         }
-        u += s.blk1 - s.blk0;
+        u = s.next;
       }
     }
     __syncwarp();
@@ -408,6 +431,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     int seg = 0;
     for (int u = u0; u < u1 && ok; ++seg) {
       const Segment s(p, at, u, u1);
+      if (s.blk1 <= s.blk0) break;
       const int buf = seg % C::kQBufs;
       const size_t qrow = (static_cast<size_t>(s.b) * p.Hq + static_cast<size_t>(s.h) * p.G) * p.Nq + s.chunk * R;
       const int rows = min(R, p.R - s.chunk * R);
@@ -470,7 +494,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_q_full(buf));
-      u += s.blk1 - s.blk0;
+      u = s.next;
     }
     __syncwarp();
   } else {
@@ -482,6 +506,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     int tile = 0, seg = 0;
     for (int u = u0; u < u1; ++seg) {
       const Segment s(p, at, u, u1);
+      if (s.blk1 <= s.blk0) break;
       const int row0 = s.chunk * R;
       const int all = p.causal ? max(0, s.len - p.Nq + 1) : s.len;     // keys below it are visible to every row
       float l[R];
@@ -613,7 +638,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         if (p.scores != nullptr && blk < s.blk1) {
           // for the weights: this token's scores, -inf where hidden or absent
           float4* const keep =
-              reinterpret_cast<float4*>(p.scores + (static_cast<size_t>(u + 2 * j + half) * kCacheBlock + (row & 63)) * p.score_row);
+              reinterpret_cast<float4*>(p.scores + (static_cast<size_t>(s.unit0 + blk) * kCacheBlock + (row & 63)) * p.score_row);
 #pragma unroll
           for (int q = 0; q < R; q += 4)
             if (row0 + q < p.R) keep[q / 4] = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
@@ -720,7 +745,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       }
       named_bar_sync(1, 128);                            // references and sums are free for the next row group
       if (row == 0) mbar_arrive(bar_q_empty(seg % C::kQBufs));
-      u += s.blk1 - s.blk0;
+      u = s.next;
     }
   }
 
@@ -747,10 +772,13 @@ constexpr int kWeightCtas = 1216;        // 8 per SM
 // Where a row's partial results lie.
 struct RowParts {
   int c0, c1, first, cols, r;                            // parts c0 .. c1; in c0 it is that part's first row or not
-  __device__ __forceinline__ RowParts(int total, int parts, int ua, int nblk, int cols_, int r_) : cols(cols_), r(r_) {
-    c0 = part_of(total, ua, parts);
-    c1 = part_of(total, ua + nblk - 1, parts);
-    first = part_begin(total, c0, parts) == ua ? 0 : 1;
+  // `before`: units before the sequence (b, nblk); row r of its head h
+  __device__ __forceinline__ RowParts(const Cache8Params& p, const Line& line, int before, int b, int nblk, int h, int row, int cols_)
+      : cols(cols_), r(row % cols_) {
+    const int ua = before + line.turn * b * p.c.Hkv * p.chunks + (h * p.chunks + row / cols_) * (nblk + line.turn);
+    c0 = line.part_of(ua + line.turn);
+    c1 = line.part_of(ua + line.turn + nblk - 1);
+    first = line.begin(c0) >= ua ? 0 : 1;
   }
   __device__ __forceinline__ long long slot(int c) const { return (2LL * c + (c == c0 ? first : 0)) * cols + r; }
 };
@@ -758,8 +786,8 @@ struct RowParts {
 template <int D>
 __global__ void __launch_bounds__(kFinishWarps * 32, 8) cache8_finish_kernel(const Cache8Params p, int cols, int ctas, int shares) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int total = line_total(p, lane);                 // (lengths are the caller's: no need to wait for them)
-  const int parts = line_parts(total, ctas);
+  const int units = line_total(p, lane);                 // (lengths are the caller's: no need to wait for them)
+  const Line line(p, units, ctas);
   const int per_block = p.c.Hkv * p.chunks;
   __shared__ float lse2[kCache8MaxRows];
   if (static_cast<int>(blockIdx.x) >= shares) {          // (the weights' CTAs first: they take longer)
@@ -774,7 +802,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 8) cache8_finish_kernel(con
     for (int i = lane; i < b; i += 32) before += line_blocks(p, i);
     before = __reduce_add_sync(0xffffffffu, before) * per_block;
     const int nblk = line_blocks(p, b);
-    const RowParts rp(total, parts, before + (h * p.chunks + r / cols) * nblk, nblk, cols, r % cols);
+    const RowParts rp(p, line, before, b, nblk, h, r, cols);
     if (rp.c0 == rp.c1) return;                          // written whole
     wait_before();
     // eight parts a warp at a time, all their loads together
@@ -868,11 +896,13 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 8) cache8_finish_kernel(con
   }
   // ---- weights: an equal share of the (sequence, KV head, block), two at a time,
   // one thread per token
-  const int all = total / p.chunks;                      // (sequence, KV head, block)
+  const int all = units / p.chunks;                      // (sequence, KV head, block)
   const int share = static_cast<int>(blockIdx.x);
-  const int w0 = part_begin(all, share, shares), w1 = part_begin(all, share + 1, shares);
+  const int w0 = static_cast<int>(static_cast<long long>(all) * share / shares);
+  const int w1 = static_cast<int>(static_cast<long long>(all) * (share + 1) / shares);
   if (w0 >= w1) return;
   Place at;
+  at.turn = 0;
   at.find(p, w0 * p.chunks, lane);                       // (sequences have `chunks` times as many units)
   const int half = threadIdx.x >> 6, slot = threadIdx.x & 63;
   wait_before();
@@ -885,7 +915,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 8) cache8_finish_kernel(con
     __syncthreads();
     for (int r = warp; r < p.R; r += kFinishWarps) {
       // a row in several parts is being joined by another CTA: its LSE from the parts, one per lane
-      const RowParts rp(total, parts, at.before + (h * p.chunks + r / cols) * at.nblk, at.nblk, cols, r % cols);
+      const RowParts rp(p, line, at.before, at.b, at.nblk, h, r, cols);
       float v;
       if (rp.c0 == rp.c1) {
         v = p.lse[(static_cast<size_t>(at.b) * p.Hq + static_cast<size_t>(h) * p.G) * p.Nq + r] * kLog2e;
