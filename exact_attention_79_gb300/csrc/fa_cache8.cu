@@ -203,12 +203,12 @@ struct Cfg {
   static constexpr int kNP = (3 * R + 15) / 16 * 16;       // O^T columns: three terms of P
   static constexpr int kPerSm = D == 256 && R > 8 ? 1 : 2;
   static constexpr int kTile = 16384 * kChunks;            // K or V of a tile
-  static constexpr int kQBufs = D == 256 ? 1 : 2;
+  static constexpr int kQBufs = 2;
   static constexpr int kQBytes = kNS * 128 * kChunks;
   static constexpr int kPBytes = kNP * 128;
   // references and their changes (4 R), the warps' maxima and sums (8 R), 1 / scale of Q per buffer
   static constexpr int kStatFloats = 4 * R + 8 * R + 2 * R;
-  static constexpr int kFixed = kQBufs * kQBytes + 2 * kPBytes + kStatFloats * 4 + kInfo * 32 + 512;
+  static constexpr int kFixed = kQBufs * kQBytes + 2 * kPBytes + kStatFloats * 4 + kInfo * 32 + 320;
   static constexpr int kBudget = (kPerSm == 2 ? 113 : 227) * 1024;
   static constexpr int kFit = (kBudget - kFixed) / kTile;
   static constexpr int kRing = kFit < 8 ? kFit : 8;        // tiles of K or V
