@@ -10,16 +10,19 @@
 // small enough for e4m3 are Q and P, as sums of e4m3 terms in columns of their own:
 //   Q, times a power of two per row that brings it to [128, 256): q = q0 + q1 / 16, which
 //      is exact for every bf16 value down to 2^-10 (2^-17 of the row's largest);
-//   P, y = 2^(s - reference + 4) <= 256: y = y0 + y1 / 16 + y2 / 256, each term the rounding
-//      of what the one before left, 2^-12 relative and 2^-18 absolute.
+//   P, y = 2^(s - reference + 5) <= 256: y = y0 + y1 / 32 + y2 / 1024, each term the rounding
+//      of what the one before left (at most 8, hence 32), 2^-12 relative and 2^-20 absolute,
+//      which is 2^-25 of the row's largest P: 2^17 keys that small are off by 2^-8 together.
 // fp32 accumulators in TMEM: S^T twice (the next tile's is computed while this one's
 // softmax runs), O^T with three columns per row.
 //
 // One thread per token. A block's K scale multiplies its logits; its V scale is
 // folded into P's exponent. Hence two references per row: ml for the sum of
 // probabilities, mo for O. Both are common to the CTA and may trail the true
-// maximum by up to 2^4; when a token exceeds that (told by the barrier that the
+// maximum by up to 2^3; when a token exceeds that (told by the barrier that the
 // softmax warps pass once a tile), all look up the maximum and rescale O in TMEM.
+// (By 2^4: as fast, P one bit coarser; by 2^2: one bit finer, 3% slower over 32
+// sequences of 8192.)
 //
 // HBM-bound: 2 d bytes per cached token and KV head, against which Q and O
 // are small. The work is a line of units, one per (sequence, KV head, chunk of
@@ -36,8 +39,8 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 224;
-constexpr float kTrail = 4.f;             // log2 of how far a reference may trail
-constexpr float kShift = 4.f;             // y = 2^(x - reference + kShift) <= 2^8
+constexpr float kTrail = 3.f;             // log2 of how far a reference may trail
+constexpr float kShift = 5.f;             // y = 2^(x - reference + kShift) <= 2^8
 constexpr int kTurn = 4;                  // blocks' time that a change of row groups costs
 constexpr int kInfo = 8;                  // tiles whose scales wait in shared memory
 
@@ -659,10 +662,10 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           if (!there) y[0] = y[1] = 0.f;                 // (no block: no scale either)
           const uint32_t c0 = pack_e4m3x2(y[0], y[1]);
           const float2 f0 = e4m3x2_to_float2(c0);
-          const float r0 = (y[0] - f0.x) * 16.f, r1 = (y[1] - f0.y) * 16.f;
+          const float r0 = (y[0] - f0.x) * 32.f, r1 = (y[1] - f0.y) * 32.f;
           const uint32_t c1 = pack_e4m3x2(r0, r1);
           const float2 f1 = e4m3x2_to_float2(c1);
-          const uint32_t c2 = pack_e4m3x2((r0 - f1.x) * 16.f, (r1 - f1.y) * 16.f);
+          const uint32_t c2 = pack_e4m3x2((r0 - f1.x) * 32.f, (r1 - f1.y) * 32.f);
           const uint32_t codes[3] = {c0, c1, c2};
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
@@ -721,7 +724,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int q = q0 + e;
-            const float v = __uint_as_float(o[0][e]) + (__uint_as_float(o[1][e]) + __uint_as_float(o[2][e]) * 0.0625f) * 0.0625f;
+            const float v = __uint_as_float(o[0][e]) + (__uint_as_float(o[1][e]) + __uint_as_float(o[2][e]) * 0.03125f) * 0.03125f;
             if (whole) {
               const float sum = warp_l[q] + warp_l[R + q] + warp_l[2 * R + q] + warp_l[3 * R + q];
               const float f = sum == 0.f ? 0.f : ex2_approx(ref_o[q] - kShift - ref_l[q]) / sum;

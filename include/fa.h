@@ -363,9 +363,10 @@ fa_status fa_cache8_append(const void* k, long long k_stride_h, long long k_stri
  * fa_fwd_kv on the values of the cache: key j is visible to query i iff
  * j < lengths[b] and, when causal, j <= i + lengths[b] - Nq; a row that sees
  * none gets O = 0, lse = -inf. Hq % Hkv == 0 and (Hq / Hkv) * Nq <= 128
- * (FA_ERR_UNSUPPORTED above). The products take the codes as they are, Q to
- * the bit (within 2^-39 of a row's largest value) and P rounded to 11 bits;
- * sums are fp32. A NaN among a sequence's V values reaches every query of the
+ * (FA_ERR_UNSUPPORTED above). The products take the codes as they are; Q
+ * to the bit down to 2^-17 of a row's largest value (smaller ones are off by at
+ * most 2^-21 of it); each P within 2^-12 of itself plus 2^-25 of the row's
+ * largest; sums are fp32. A NaN among a sequence's V values reaches every query of the
  * call on that sequence and head.
  * add_weights: also weight_j = weight_decay * weight_j + sum of the
  * probabilities of key j over the Hq / Hkv heads and Nq queries, for every

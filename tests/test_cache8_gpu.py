@@ -3,10 +3,11 @@ bit, the attention and its weights within bounds derived from the formats.
 
 Attention bound, per element, with A = scale max_j sum_c |q_c k_jc| of the row, n keys:
   logits   (d + 8) 2^-23 A: d exact products added in fp32 by the tensor core (2^-23 each, truncated), scales;
-  P        2^-11 (half rounding), 2^-20 (ex2, its argument's sum); as a ratio to l twice the logits' error;
+  P        2^-12 (three e4m3 terms), below 2^-11, 2^-20 (ex2, its argument's sum); as a ratio to l twice the logits' error;
   sums     n 2^-23 for O and for l;
   result   2^-8 |O| (bf16).
-A term below 2^-20 of O's reference may be rounded by 2^-31 of it, the reference trails by at most 2^8: n 2^-22 max|V| / l.
+P is also off by 2^-25 of the row's largest: no more than the other half of 2^-11 where the keys that matter are few (a
+long tail of small ones has a test of its own); n 2^-31 of the largest term on top.
 """
 import threading
 
@@ -209,6 +210,93 @@ def test_long_sequences_are_split_and_give_the_same_bits_every_time(fa):
         o2, l2 = fa.fwd_cache8(q.to(DEV), g, ints(table), ints(lens))
         assert torch.equal(o, o2) and torch.equal(lse, l2)
     check_attention(c, q, table, lens, True, 128 ** -0.5, o, lse, None)
+
+
+def test_a_long_tail_of_small_probabilities_counts(fa):
+    """One key takes nearly all of the softmax and 131071 share the rest, each 2^-23.5 of it: O is the tail's alone.
+    P is off by at most 2^-25 of the largest and 2^-12 of itself, so O by n 2^-25 max|V| + 2^-11 p|V| (P and l), and 2^-8 |O|."""
+    n, d = 131072, 64
+    P = n // 64
+    c = {"k": np.zeros((P, 1, 64, d), np.uint8), "v": np.full((P, 1, 64, d), 0x38, np.uint8),      # 0x38: 1.0
+         "k_scale": np.ones((P, 1), np.float32), "v_scale": np.ones((P, 1), np.float32)}
+    table = np.random.default_rng(13).permutation(P)[None].astype(np.int32)
+    first = table[0, 777], 0, 21                       # the heavy key, somewhere in the middle
+    c["k"][first], c["v"][first] = 0x38, 0
+    q = torch.full((1, 2, 1, d), 23.5 * np.log(2) / d, dtype=torch.bfloat16)
+    s = f64(q)[0, 0, 0].sum()
+    o, lse = fa.fwd_cache8(q.to(DEV), to_gpu(fa, c), ints(table), ints([n]), scale=1.0)
+    tail = (n - 1) * np.exp(-s)
+    want = tail / (1 + tail)
+    assert np.abs(f64(o) - want).max() <= 2.0 ** -8 * want + 2.0 ** -11 * want + n * 2.0 ** -25
+    assert np.abs(f64(lse) - (s + np.log1p(tail))).max() <= (d + 8) * 2.0 ** -23 * s + n * 2.0 ** -23 * want + 2.0 ** -20 * s
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,Nq,d", [
+    ([0, 200, 64, 1, 700, 65, 330] * 10, 4, 2, 1, 64),              # more sequences than a warp has lanes
+    ([1100, 900] * 20, 2, 1, 1, 128),                               # the same, several tiles a part
+    ([1500, 10, 2500, 0, 800] * 2, 4, 2, 2, 256),                   # row groups of one block among long ones
+    ([3000, 2000], 40, 2, 2, 128),                                  # two chunks of 32 rows each
+])
+def test_many_row_groups_split_between_ctas(fa, lens, Hq, Hkv, Nq, d):
+    c, table = make(sum(lens) + d, lens, Hkv, d)
+    q = bf16(np.random.default_rng(14), len(lens), Hq, Nq, d)
+    g = to_gpu(fa, c)
+    o, lse = fa.fwd_cache8(q.to(DEV), g, ints(table), ints(lens), weight_decay=0.5)
+    fa.check_device_status()
+    check_attention(c, q, table, lens, True, d ** -0.5, o, lse, None, f64(g.weight), 0.5)
+
+
+def test_sequences_may_share_blocks(fa):
+    """A prefix of two blocks in two tables: each sequence's result is what it gets from blocks of its own."""
+    c, table = make(15, [200, 200, 200], 2, 64, spare=0)
+    for x in ("k", "v", "k_scale", "v_scale"):
+        for i in range(2):
+            c[x][table[1, i]] = c[x][table[0, i]]
+    q = bf16(np.random.default_rng(16), 3, 4, 1, 64).to(DEV)
+    g = to_gpu(fa, c)
+    want = fa.fwd_cache8(q, g, ints(table), ints([200, 190, 200]))
+    table[1, :2] = table[0, :2]
+    got = fa.fwd_cache8(q, g, ints(table), ints([200, 190, 200]))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_graphs_may_share_a_workspace_one_after_the_other(fa):
+    lens = [700, 90]
+    c, table = make(17, lens, 2, 128)
+    g, tb, n = to_gpu(fa, c), ints(table), ints(lens)
+    qs = [bf16(np.random.default_rng(i), 2, 8, 1, 128).to(DEV) for i in range(2)]
+    want = [fa.fwd_cache8(q, g, tb, n) for q in qs]
+    size = fa.load().fa_fwd_cache8_workspace_bytes(2, 8, 2, 1, 128, table.shape[1], 0)
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device=DEV)      # NaN wherever it is read as floats
+    graphs, outs = [], []
+    for q in qs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(fa.fwd_cache8(q, g, tb, n, workspace=ws))
+    for _ in range(3):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(outs, want):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_a_stalled_call_reports_and_the_next_one_works(fa, monkeypatch):
+    lens = [700, 90]
+    c, table = make(18, lens, 2, 128)
+    q = bf16(np.random.default_rng(19), 2, 8, 1, 128).to(DEV)
+    g = to_gpu(fa, c)
+    want = fa.fwd_cache8(q, g, ints(table), ints(lens))
+    for decay in (None, 0.0):
+        monkeypatch.setenv("FA_TEST_STALL", "1")
+        fa.fwd_cache8(q, g, ints(table), ints(lens), weight_decay=decay)
+        with pytest.raises(fa.FAError) as e:
+            fa.check_device_status()
+        assert e.value.code == 5
+        monkeypatch.setenv("FA_TEST_STALL", "0")
+        got = fa.fwd_cache8(q, g, ints(table), ints(lens))
+        fa.check_device_status()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_pool_offsets_past_32_bits(fa):
