@@ -764,13 +764,16 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 }
 
 // ------------------------------------------------------------------ second kernel
-// Joins the rows whose units went to several parts (one warp per row), and adds
+// Joins the rows whose units went to several parts, and adds
 // the weights: weight_j = decay weight_j + sum over the group's rows of
 // 2^(s_rj - LSE_r), from the scores that the first kernel kept (the
 // probabilities need the whole row's LSE; reading K again instead costs d
 // bytes per token and head against 8 per row, mostly from L2).
 constexpr int kFinishWarps = 4;
 constexpr int kWeightCtas = 1216;        // 8 per SM
+// Up to two rows per SM: four warps join a row, which has many parts then (128 rows of 19: 87.7 us
+// for the call, 89.2 with one warp each); past that one warp (384 rows of two or three: 40.8 against 44.4).
+constexpr int kJoinRows = 2 * kCache8Sms;
 
 // Where a row's partial results lie.
 struct RowParts {
@@ -786,7 +789,8 @@ struct RowParts {
   __device__ __forceinline__ long long slot(int c) const { return (2LL * c + (c == c0 ? first : 0)) * cols + r; }
 };
 
-template <int D>
+// kJoin: warps that join a row together, kFinishWarps or one each.
+template <int D, int kJoin>
 __global__ void __launch_bounds__(kFinishWarps * 32, 8) cache8_finish_kernel(const Cache8Params p, int cols, int ctas, int shares) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int units = line_total(p, lane);                 // (lengths are the caller's: no need to wait for them)
@@ -794,12 +798,11 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 8) cache8_finish_kernel(con
   const int per_block = p.c.Hkv * p.chunks;
   __shared__ float lse2[kCache8MaxRows];
   if (static_cast<int>(blockIdx.x) >= shares) {          // (the weights' CTAs first: they take longer)
-    // ---- join: one row of the B * Hkv * R; its parts dealt out to the warps
-    __shared__ float4 sum_o[kFinishWarps][32 * (D / 128)];
-    __shared__ float sum_l[kFinishWarps], top_l[kFinishWarps], top_o[kFinishWarps];
+    // ---- join: rows of the B * Hkv * R
     const int per_seq = p.c.Hkv * p.R;
-    const int row = static_cast<int>(blockIdx.x) - shares;
+    const int row = kJoin == 1 ? (static_cast<int>(blockIdx.x) - shares) * kFinishWarps + warp : static_cast<int>(blockIdx.x) - shares;
     const int b = row / per_seq, hr = row - b * per_seq;
+    if (b >= p.B) return;
     const int h = hr / p.R, r = hr - h * p.R;
     int before = 0;
     for (int i = lane; i < b; i += 32) before += line_blocks(p, i);
@@ -808,20 +811,21 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 8) cache8_finish_kernel(con
     const RowParts rp(p, line, before, b, nblk, h, r, cols);
     if (rp.c0 == rp.c1) return;                          // written whole
     wait_before();
-    // eight parts a warp at a time, all their loads together
+    // several parts a warp at a time, all their loads together
     constexpr int kPer = D / 128;                        // float4 per lane
+    constexpr int kAtOnce = kJoin == 1 ? 3 : 8;
     float ml = -INFINITY, mo = -INFINITY, sum = 0.f;
     float4 a[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = rp.c0 + warp; c <= rp.c1; c += 8 * kFinishWarps) {
-      float s3[8][3];
-      float4 y[8][kPer];
+    for (int c = rp.c0 + (kJoin == 1 ? 0 : warp); c <= rp.c1; c += kAtOnce * kJoin) {
+      float s3[kAtOnce][3];
+      float4 y[kAtOnce][kPer];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int ck = min(c + k * kFinishWarps, rp.c1);
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int ck = min(c + k * kJoin, rp.c1);
         const long long slot = rp.slot(ck);
-        const bool mine = c + k * kFinishWarps <= rp.c1;
+        const bool mine = c + k * kJoin <= rp.c1;
 #pragma unroll
         for (int e = 0; e < 3; ++e) s3[k][e] = mine ? p.part_s[slot * 3 + e] : e == 1 ? 0.f : -INFINITY;
 #pragma unroll
@@ -831,7 +835,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 8) cache8_finish_kernel(con
       }
       float nl = ml, no = mo;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < kAtOnce; ++k) {
         nl = fmaxf(nl, s3[k][0]);
         no = fmaxf(no, s3[k][2]);
       }
@@ -847,7 +851,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 8) cache8_finish_kernel(con
         a[i].w *= f0;
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < kAtOnce; ++k) {
         sum += s3[k][0] == -INFINITY ? s3[k][1] : s3[k][1] * ex2_approx(s3[k][0] - ml);
         const float f = s3[k][2] == -INFINITY ? 1.f : ex2_approx(s3[k][2] - mo);   // (no term yet: O is 0, or a NaN that stays)
 #pragma unroll
@@ -859,41 +863,47 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 8) cache8_finish_kernel(con
         }
       }
     }
+    if constexpr (kJoin > 1) {
+      __shared__ float4 sum_o[kFinishWarps][32 * kPer];
+      __shared__ float sum_l[kFinishWarps], top_l[kFinishWarps], top_o[kFinishWarps];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) sum_o[warp][32 * i + lane] = a[i];
-    if (lane == 0) {
-      sum_l[warp] = sum;
-      top_l[warp] = ml;
-      top_o[warp] = mo;
-    }
-    __syncthreads();
-    if (warp != 0) return;
-    ml = fmaxf(fmaxf(top_l[0], top_l[1]), fmaxf(top_l[2], top_l[3]));
-    mo = fmaxf(fmaxf(top_o[0], top_o[1]), fmaxf(top_o[2], top_o[3]));
-    float fo[kFinishWarps];
-    sum = 0.f;
+      for (int i = 0; i < kPer; ++i) sum_o[warp][32 * i + lane] = a[i];
+      if (lane == 0) {
+        sum_l[warp] = sum;
+        top_l[warp] = ml;
+        top_o[warp] = mo;
+      }
+      __syncthreads();
+      if (warp != 0) return;
+      ml = fmaxf(fmaxf(top_l[0], top_l[1]), fmaxf(top_l[2], top_l[3]));
+      mo = fmaxf(fmaxf(top_o[0], top_o[1]), fmaxf(top_o[2], top_o[3]));
+      float fo[kFinishWarps];
+      sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kFinishWarps; ++w) {
-      sum += top_l[w] == -INFINITY ? sum_l[w] : sum_l[w] * ex2_approx(top_l[w] - ml);
-      fo[w] = top_o[w] == -INFINITY ? 1.f : ex2_approx(top_o[w] - mo);
+      for (int w = 0; w < kFinishWarps; ++w) {
+        sum += top_l[w] == -INFINITY ? sum_l[w] : sum_l[w] * ex2_approx(top_l[w] - ml);
+        fo[w] = top_o[w] == -INFINITY ? 1.f : ex2_approx(top_o[w] - mo);
+      }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kFinishWarps; ++w) {
+          const float4 y = sum_o[w][32 * i + lane];
+          a[i].x = fmaf(fo[w], y.x, a[i].x);
+          a[i].y = fmaf(fo[w], y.y, a[i].y);
+          a[i].z = fmaf(fo[w], y.z, a[i].z);
+          a[i].w = fmaf(fo[w], y.w, a[i].w);
+        }
+      }
     }
     const size_t at = (static_cast<size_t>(b) * p.Hq + static_cast<size_t>(h) * p.G) * p.Nq + r;
     const float f = sum == 0.f ? 0.f : ex2_approx(mo - ml) / sum;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kFinishWarps; ++w) {
-        const float4 y = sum_o[w][32 * i + lane];
-        a[i].x = fmaf(fo[w], y.x, a[i].x);
-        a[i].y = fmaf(fo[w], y.y, a[i].y);
-        a[i].z = fmaf(fo[w], y.z, a[i].z);
-        a[i].w = fmaf(fo[w], y.w, a[i].w);
-      }
+    for (int i = 0; i < kPer; ++i)
       if (128 * i + 4 * lane < p.c.d)
         *reinterpret_cast<uint2*>(p.o + at * p.c.d + 128 * i + 4 * lane) =
             make_uint2(pack_bf16x2(a[i].x * f, a[i].y * f), pack_bf16x2(a[i].z * f, a[i].w * f));
-    }
     if (lane == 0) p.lse[at] = sum == 0.f ? -INFINITY : (ml + log2f(sum)) * kLn2;
     return;
   }
@@ -1010,11 +1020,14 @@ cudaError_t launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const Cache
   else if (cols == 16) e = launch_fwd<D, 16>(mk, mv, p, parts, stream);
   else if constexpr (D == 128) e = launch_fwd<D, 32>(mk, mv, p, parts, stream);
   if (e != cudaSuccess) return e;
-  const int join = parts > 1 ? p.B * p.c.Hkv * p.R : 0;                // one CTA per row
+  const int rows = parts > 1 ? p.B * p.c.Hkv * p.R : 0;
+  const bool single = rows > kJoinRows;
+  const int join = single ? (rows + kFinishWarps - 1) / kFinishWarps : rows;
   const long long blocks = static_cast<long long>(p.B) * p.c.Hkv * p.max_blocks;
   const int weigh = p.add_weights ? static_cast<int>(blocks < kWeightCtas ? blocks : kWeightCtas) : 0;
   if (join + weigh == 0) return cudaSuccess;
-  return launch_early(cache8_finish_kernel<D>, dim3(join + weigh), dim3(kFinishWarps * 32), 0, stream, p, cols, parts, weigh);
+  return launch_early(single ? cache8_finish_kernel<D, 1> : cache8_finish_kernel<D, kFinishWarps>, dim3(join + weigh),
+                      dim3(kFinishWarps * 32), 0, stream, p, cols, parts, weigh);
 }
 
 }  // namespace
