@@ -733,7 +733,7 @@ size_t fa_fwd_cache8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int 
 fa_status fa_fwd_cache8(const void* q, const fa_cache8* cache, const int* block_table, int max_blocks,
                         const int* lengths, void* o, float* lse, void* workspace, size_t workspace_bytes, int B, int Hq,
                         int Nq, int causal, float scale, int add_weights, float weight_decay, void* stream) {
-  if (!q || !o || !lse || !lengths || !aligned16(q) || !aligned16(o) || !aligned16(lse)) return FA_ERR_INVALID_ARG;
+  if (!q || !o || q == o || !lse || !lengths || !aligned16(q) || !aligned16(o) || !aligned16(lse)) return FA_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
   if (add_weights && (!std::isfinite(weight_decay) || !(weight_decay >= 0.f))) return FA_ERR_INVALID_ARG;
   fa::Cache8Params p{};
@@ -780,7 +780,7 @@ fa_status fa_fwd_cache8(const void* q, const fa_cache8* cache, const int* block_
 fa_status fa_cache8_evict(const fa_cache8* cache, const int* block_table, int max_blocks, const int* lengths, int B,
                           int keep, int recent, const int* to_table, int to_blocks, int* kept, int* new_lengths,
                           void* stream) {
-  if (!lengths || !to_table || !kept || !new_lengths) return FA_ERR_INVALID_ARG;
+  if (!lengths || !to_table || !kept || !new_lengths || new_lengths == lengths) return FA_ERR_INVALID_ARG;
   if (keep < 1 || recent < 0 || recent > keep || to_blocks < 1 ||
       static_cast<long long>(to_blocks) * FA_CACHE8_BLOCK < keep)
     return FA_ERR_INVALID_ARG;
@@ -863,6 +863,6 @@ const char* fa_status_string(fa_status s) {
   return "unknown status";
 }
 
-int fa_version(void) { return 400; }
+int fa_version(void) { return 500; }
 
 }  // extern "C"

@@ -358,15 +358,15 @@ fa_status fa_cache8_append(const void* k, long long k_stride_h, long long k_stri
                            void* stream);
 
 /* Attention over the cache for the last Nq positions of each sequence: q, o
- * bf16 [B, Hq, Nq, d], lse fp32 [B, Hq, Nq], lengths int32 [B] (device): tokens
+ * bf16 [B, Hq, Nq, d], apart from one another, lse fp32 [B, Hq, Nq], lengths int32 [B] (device): tokens
  * held, the Nq new ones included (taken within 0 .. 64 max_blocks). As
  * fa_fwd_kv on the values of the cache: key j is visible to query i iff
  * j < lengths[b] and, when causal, j <= i + lengths[b] - Nq; a row that sees
  * none gets O = 0, lse = -inf. Hq % Hkv == 0 and (Hq / Hkv) * Nq <= 128
  * (FA_ERR_UNSUPPORTED above). The products take the codes as they are; Q
  * to the bit down to 2^-17 of a row's largest value (smaller ones are off by at
- * most 2^-21 of it); each P within 2^-12 of itself plus 2^-25 of the row's
- * largest; sums are fp32. A NaN among a sequence's V values reaches every query of the
+ * most 2^-21 of it); each P (times its block's V scale) within 2^-12 of
+ * itself plus 2^-25 of the row's largest; sums are fp32. A NaN among a sequence's V values reaches every query of the
  * call on that sequence and head.
  * add_weights: also weight_j = weight_decay * weight_j + sum of the
  * probabilities of key j over the Hq / Hkv heads and Nq queries, for every
@@ -391,7 +391,7 @@ fa_status fa_fwd_cache8(const void* q, const fa_cache8* cache, const int* block_
  * fa_cache8_append takes them, and their weights with them; slots behind them
  * are left as they were. kept int32 [B, Hkv, keep]: the tokens' positions
  * before, -1 past the sequence's new length; new_lengths int32 [B]:
- * min(lengths, keep). Heads keep different tokens but equally many. A block of
+ * min(lengths, keep), in an array other than lengths. Heads keep different tokens but equally many. A block of
  * to_table must be neither a source of this call nor named twice in it; the
  * sources are left as they were. keep >= 1; cache->weight is needed. */
 fa_status fa_cache8_evict(const fa_cache8* cache, const int* block_table, int max_blocks, const int* lengths, int B,
@@ -411,7 +411,7 @@ fa_status fa_cache8_evict(const fa_cache8* cache, const int* block_table, int ma
 fa_status fa_device_status(void* stream);
 
 /* Diagnostic: the mean SM clock, in MHz, of the forward (fa_fwd, fa_fwd_f32,
- * fa_fwd_kv, fa_fwd_blocksparse at d <= 128) and dK/dV (fa_bwd and its
+ * fa_fwd_kv, fa_fwd_blocksparse at d <= 128, fa_fwd_packed) and dK/dV (fa_bwd and its
  * variants) kernels launched on this device since the previous call, as
  * measured by the kernels themselves: each block adds the SM cycle count and
  * the nanoseconds between its start and its exit to two device-wide sums,

@@ -18,6 +18,7 @@ def lib():
 
 P = ctypes.c_void_p
 FAKE = P(1 << 20)       # never dereferenced: validation fails first
+OTHER = P(2 << 20)
 NULL = P(0)
 
 
@@ -31,13 +32,13 @@ def append(lib, c=None, k=FAKE, sh=64, st=64, B=1, T=1, cu=FAKE, start=FAKE, tab
     return lib.fa_cache8_append(k, sh, st, FAKE, 64, 64, cu, start, B, T, c if c is not None else cache(), table, mb, NULL)
 
 
-def fwd(lib, c=None, q=FAKE, table=FAKE, mb=4, lengths=FAKE, o=FAKE, lse=FAKE, ws=FAKE, nws=1 << 30, B=1, Hq=4, Nq=1,
+def fwd(lib, c=None, q=FAKE, table=FAKE, mb=4, lengths=FAKE, o=OTHER, lse=FAKE, ws=FAKE, nws=1 << 30, B=1, Hq=4, Nq=1,
         scale=0.1, add=0, decay=1.0):
     return lib.fa_fwd_cache8(q, c if c is not None else cache(), table, mb, lengths, o, lse, ws, nws, B, Hq, Nq, 1, scale,
                              add, decay, NULL)
 
 
-def evict(lib, c=None, B=1, keep=10, recent=2, to=FAKE, tb=1, kept=FAKE, new=FAKE, lengths=FAKE, mb=4):
+def evict(lib, c=None, B=1, keep=10, recent=2, to=FAKE, tb=1, kept=FAKE, new=OTHER, lengths=FAKE, mb=4):
     return lib.fa_cache8_evict(c if c is not None else cache(), FAKE, mb, lengths, B, keep, recent, to, tb, kept, new, NULL)
 
 
@@ -62,7 +63,7 @@ def test_append_rules(lib):
 def test_fwd_rules(lib):
     for bad in (dict(q=NULL), dict(o=NULL), dict(lse=NULL), dict(lengths=NULL), dict(table=NULL), dict(Hq=3), dict(Nq=0),
                 dict(scale=0.0), dict(scale=float("nan")), dict(add=1, decay=-1.0), dict(add=1, decay=float("inf")),
-                dict(add=1, c=cache(weight=0)), dict(q=P((1 << 20) + 8))):
+                dict(add=1, c=cache(weight=0)), dict(q=P((1 << 20) + 8)), dict(o=FAKE)):
         assert fwd(lib, **bad) == 1, bad
     assert fwd(lib, Hq=4, Nq=65) == 2                      # 2 heads per KV head x 65 rows
     need = lib.fa_fwd_cache8_workspace_bytes(1, 4, 2, 1, 64, 4, 0)
@@ -87,7 +88,7 @@ def test_workspace_bytes(lib):
 
 def test_evict_rules(lib):
     for bad in (dict(keep=0), dict(recent=-1), dict(recent=11), dict(tb=0), dict(keep=65, tb=1), dict(to=NULL), dict(kept=NULL),
-                dict(new=NULL), dict(lengths=NULL), dict(c=cache(weight=0))):
+                dict(new=NULL), dict(lengths=NULL), dict(new=FAKE, lengths=FAKE), dict(c=cache(weight=0))):
         assert evict(lib, **bad) == 1, bad
 
 

@@ -246,6 +246,52 @@ def test_many_row_groups_split_between_ctas(fa, lens, Hq, Hkv, Nq, d):
     check_attention(c, q, table, lens, True, d ** -0.5, o, lse, None, f64(g.weight), 0.5)
 
 
+@pytest.mark.parametrize("Hq,Nq,d", [(1, 1, 128), (128, 1, 256), (16, 8, 64)])
+def test_one_block_one_head(fa, Hq, Nq, d):
+    """A single unit of work: nothing to join; the most rows, in eight chunks."""
+    c, table = make(20 + d, [37], 1, d, spare=0)
+    q = bf16(np.random.default_rng(21), 1, Hq, Nq, d)
+    g = to_gpu(fa, c)
+    o, lse = fa.fwd_cache8(q.to(DEV), g, ints(table), ints([37]), weight_decay=0.25)
+    fa.check_device_status()
+    check_attention(c, q, table, [37], True, d ** -0.5, o, lse, None, f64(g.weight), 0.25)
+
+
+def test_scales_of_zero(fa):
+    """Blocks whose K or V scale is 0 hold zeros: logits of 0, values of 0."""
+    lens = [200, 100]
+    c, table = make(22, lens, 1, 64)
+    c["k_scale"][table[0, 1]] = 0.0
+    c["v_scale"][table[0, 2]] = c["v_scale"][table[1, :2]] = 0.0
+    q = bf16(np.random.default_rng(23), 2, 2, 1, 64)
+    o, lse = fa.fwd_cache8(q.to(DEV), to_gpu(fa, c), ints(table), ints(lens))
+    check_attention(c, q, table, lens, True, 64 ** -0.5, o, lse, None)
+    assert (o[1] == 0).all() and torch.isfinite(lse).all()
+
+
+def test_evict_follows_lengths_in_a_graph(fa):
+    lens, keep, recent = [9000, 300], 200, 16
+    c, table = make(24, lens, 2, 16, spare=4)
+    to, table = table[:, -4:].copy(), table[:, :-4].copy()
+    g, n = to_gpu(fa, c), ints(lens)
+    scratch = to_gpu(fa, c)
+    fa.cache8_evict(scratch, ints(table), n, keep, recent, ints(to))
+    tb, tt = ints(table), ints(to)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        new, kept = fa.cache8_evict(g, tb, n, keep, recent, tt)
+    for lens in ([9000, 300], [150, 257], [0, 201]):
+        n.copy_(ints(lens))
+        graph.replay()
+        torch.cuda.synchronize()
+        want, wn, wk = oc.evict(c, table, lens, keep, recent, to)
+        assert np.array_equal(new.cpu().numpy(), wn) and np.array_equal(kept.cpu().numpy(), wk)
+        for b in range(2):
+            for i in range(int(wn[b])):
+                page = to[b, i // 64], slice(None), i % 64
+                assert np.array_equal(g.k.cpu().numpy()[page], want["k"][page])
+
+
 def test_sequences_may_share_blocks(fa):
     """A prefix of two blocks in two tables: each sequence's result is what it gets from blocks of its own."""
     c, table = make(15, [200, 200, 200], 2, 64, spare=0)
