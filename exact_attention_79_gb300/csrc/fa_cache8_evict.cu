@@ -22,7 +22,7 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelCtas = 8;                     // CTAs of a cluster at most
 constexpr int kBins = 256;
 constexpr int kSelKeys = 49152;                 // keys of a CTA that stay in shared memory (192 KB)
-constexpr int kGatherThreads = 128;
+constexpr int kGatherThreads = 64;
 
 __device__ __forceinline__ __half2 as_half2(uint32_t x) {
   __half2 h;
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Cache8
 
 // D: 128 or 256, d at most that.
 template <int D>
-__global__ void __launch_bounds__(kGatherThreads, D == 128 ? 12 : 8) cache8_gather_kernel(const Cache8EvictParams p) {
+__global__ void __launch_bounds__(kGatherThreads, D == 128 ? 18 : 8) cache8_gather_kernel(const Cache8EvictParams p) {
   constexpr int kMaxChunks = kCacheBlock * D / 16 / kGatherThreads;    // 16-code chunks per thread
   __shared__ float warp_max[kGatherThreads / 32];
   __shared__ long long src[kCacheBlock];          // (block * Hkv + h) * 64 + slot of a kept token, -1: no such block
@@ -245,14 +245,15 @@ __global__ void __launch_bounds__(kGatherThreads, D == 128 ? 12 : 8) cache8_gath
   const int h = blockIdx.y, which = blockIdx.z;
   let_next();
   wait_before();
+  // (one round of loads for all three)
   const int n = cache_length(p.lengths, b, p.max_blocks);
-  const int cnt = min(kCacheBlock, min(n, p.keep) - blk * kCacheBlock);
-  if (cnt <= 0) return;
   const int page = p.to_table[static_cast<long long>(b) * p.to_blocks + blk];
-  if (page < 0 || page >= p.c.num_blocks) return;
+  const int slot = blk * kCacheBlock + tid;
+  const int i = tid < kCacheBlock && slot < p.keep ? p.kept[(static_cast<size_t>(b) * p.c.Hkv + h) * p.keep + slot] : -1;
+  const int cnt = min(kCacheBlock, min(n, p.keep) - blk * kCacheBlock);
+  if (cnt <= 0 || page < 0 || page >= p.c.num_blocks) return;
   const size_t ph = static_cast<size_t>(page) * p.c.Hkv + h;
   if (tid < cnt) {
-    const int i = p.kept[(static_cast<size_t>(b) * p.c.Hkv + h) * p.keep + blk * kCacheBlock + tid];
     const int from = p.table[static_cast<long long>(b) * p.max_blocks + i / kCacheBlock];
     const bool ok = from >= 0 && from < p.c.num_blocks;
     const long long at = (static_cast<long long>(from) * p.c.Hkv + h) * kCacheBlock + i % kCacheBlock;

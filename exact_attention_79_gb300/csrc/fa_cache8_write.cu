@@ -11,7 +11,7 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 // Largest finite magnitude of two bf16; infinities and NaN are left out.
 __device__ __forceinline__ uint32_t finite_max(uint32_t m, uint32_t x) {
@@ -38,7 +38,7 @@ __device__ __forceinline__ uint2 encode8(const uint4& x, float inv) {
 
 // One CTA per (touched block, KV head, K or V). D: 128 or 256, d at most that.
 template <int D>
-__global__ void __launch_bounds__(kThreads, D == 128 ? 6 : 4) cache8_append_kernel(const Cache8AppendParams p) {
+__global__ void __launch_bounds__(kThreads, D == 128 ? 8 : 4) cache8_append_kernel(const Cache8AppendParams p) {
   constexpr int kMaxChunks = kCacheBlock * D / 8 / kThreads;   // 16-byte chunks of one block per thread
   __shared__ float warp_max[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
