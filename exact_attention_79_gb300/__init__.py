@@ -119,11 +119,16 @@ def _require(device, *specs):
     its end. specs: (tensor, name, dtype, shape). Every dtype and shape is
     checked before any placement (contiguous, CUDA, on the device of q), so
     the shape rules hold for CPU tensors too."""
+    index = _index(device)
+    for t, name, dtype, shape in specs:                 # all of it at once where nothing is wrong
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+            break
+    else:
+        return
     for t, name, dtype, shape in specs:
-        if t.dtype != dtype or (t.shape != shape and tuple(t.shape) != tuple(shape)):
+        if t.dtype != dtype or tuple(t.shape) != tuple(shape):
             raise ValueError(f"{name}: expected {dtype} of shape {tuple(shape)}, "
                              f"got {t.dtype} of shape {tuple(t.shape)}")
-    index = _index(device)
     for t, name, _, _ in specs:
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
@@ -334,16 +339,18 @@ def new_cache8(num_blocks, Hkv, d, device="cuda", weight=False):
 def _cache8_specs(cache):
     """The cache's tensors as _require takes them, its C form and (num_blocks, Hkv, d)."""
     import torch
-    if cache.k.dim() != 4 or cache.k.shape[2] != CACHE8_BLOCK:
+    k, v, k_scale, v_scale, weight = cache
+    shape = k.shape
+    if len(shape) != 4 or shape[2] != CACHE8_BLOCK:
         raise ValueError(f"cache.k must be [num_blocks, Hkv, {CACHE8_BLOCK}, d]")
-    nb, Hkv, _, d = cache.k.shape
+    nb, Hkv, _, d = shape
     f32, u8 = torch.float32, torch.uint8
-    specs = [(cache.k, "cache.k", u8, (nb, Hkv, CACHE8_BLOCK, d)), (cache.v, "cache.v", u8, (nb, Hkv, CACHE8_BLOCK, d)),
-             (cache.k_scale, "cache.k_scale", f32, (nb, Hkv)), (cache.v_scale, "cache.v_scale", f32, (nb, Hkv))]
-    if cache.weight is not None:
-        specs.append((cache.weight, "cache.weight", f32, (nb, Hkv, CACHE8_BLOCK)))
-    c = _Cache8(cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(),
-                cache.weight.data_ptr() if cache.weight is not None else None, nb, Hkv, d)
+    specs = [(k, "cache.k", u8, shape), (v, "cache.v", u8, shape), (k_scale, "cache.k_scale", f32, (nb, Hkv)),
+             (v_scale, "cache.v_scale", f32, (nb, Hkv))]
+    if weight is not None:
+        specs.append((weight, "cache.weight", f32, (nb, Hkv, CACHE8_BLOCK)))
+    c = _Cache8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                None if weight is None else weight.data_ptr(), nb, Hkv, d)
     return specs, c, (nb, Hkv, d)
 
 
@@ -469,7 +476,7 @@ def fwd_cache8(q, cache, block_table, lengths, causal=True, scale=None, out=None
         specs.append((workspace, "workspace", torch.uint8, (workspace.numel(),)))
     _require(dev, *specs)
     if out is None:
-        out = torch.empty((B, Hq, Nq, d), dtype=bf16, device=dev)
+        out = torch.empty_like(q)
     if lse is None:
         lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev)
     max_blocks, weigh = block_table.shape[1], int(weight_decay is not None)

@@ -672,13 +672,16 @@ struct Cache8Workspace {
 Cache8Workspace cache8_workspace(int B, int Hkv, int R, int d, int max_blocks, bool weights) {
   const int cols = fa::cache8_columns(d, R), chunks = (R + cols - 1) / cols;
   const size_t D = d <= 128 ? 128 : 256;
-  const size_t rows = 2 * static_cast<size_t>(fa::cache8_parts(B, Hkv, d, R, max_blocks)) * cols;
+  const size_t rows = fa::cache8_whole(B, Hkv, d, R, max_blocks)
+                          ? 0
+                          : 2 * static_cast<size_t>(fa::cache8_parts(B, Hkv, d, R, max_blocks)) * cols;
   const size_t units = static_cast<size_t>(B) * Hkv * chunks * max_blocks;
   Cache8Workspace w;
   w.off_s = align256(rows * D * 4);
   w.off_x = w.off_s + align256(rows * 3 * 4);
   w.score_row = R < cols ? (R + 3) / 4 * 4 : cols;
   w.total = w.off_x + (weights ? units * FA_CACHE8_BLOCK * w.score_row * 4 : 0);
+  if (w.total == 0) w.total = 256;     // (0 says that the call refuses)
   return w;
 }
 

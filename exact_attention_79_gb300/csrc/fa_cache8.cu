@@ -25,7 +25,10 @@
 // sequences of 8192.)
 //
 // HBM-bound: 2 d bytes per cached token and KV head, against which Q and O
-// are small. The work is a line of units, one per (sequence, KV head, chunk of
+// are small. Measured: 32 sequences of 2048 to 8192 tokens, 64 heads on 8, d 128: 68 us, 5.1 TB/s; two of
+// 131072: 87 us, 5.8 TB/s; 6 of up to 5000, 16 heads, 4 queries, d 256: 40 us, 3.7 TB/s. The steady state
+// takes the memory's whole rate; lost are 8 us until the first tiles are there, the
+// spread of the CTAs' ends (4 us) and the join (3 us). The work is a line of units, one per (sequence, KV head, chunk of
 // rows, block of 64 tokens), cut into equal parts for the CTAs (two per SM, so
 // that one's row changes hide behind the other's stream) whatever the
 // sequences' lengths; a row whose units fall to several CTAs is joined from
@@ -41,6 +44,7 @@ namespace {
 constexpr int kThreads = 224;
 constexpr float kTrail = 3.f;             // log2 of how far a reference may trail
 constexpr float kShift = 5.f;             // y = 2^(x - reference + kShift) <= 2^8
+constexpr int kWholeBlocks = 8;
 constexpr int kTurn = 4;                  // blocks' time that a change of row groups costs
 constexpr int kInfo = 8;                  // tiles whose scales wait in shared memory
 
@@ -168,6 +172,18 @@ struct Place {
       units = line_total(p, lane);
     }
     const Line line(p, units, ctas);
+    if (p.whole) {
+      const int seq = i / per_block;                     // (the grid is B * per_block)
+      turn = 0;
+      b = seq;
+      load(p);
+      int sum = 0;
+      for (int x = lane; x < seq; x += 32) sum += line_blocks(p, x);
+      before = __reduce_add_sync(0xffffffffu, sum) * per_block;
+      u0 = before + (i - seq * per_block) * nblk;
+      u1 = u0 + nblk;
+      return true;
+    }
     if (i >= line.parts) return false;
     u0 = line.begin(i);
     u1 = line.begin(i + 1);
@@ -507,16 +523,16 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
     bool ok = true;
     int tile = 0, seg = 0;
-    for (int u = u0; u < u1; ++seg) {
-      const Segment s(p, at, u, u1);
-      if (s.blk1 <= s.blk0) break;
+    if (row < R) ref_l[row] = ref_o[row] = -INFINITY;
+    named_bar_sync(1, 128);
+    int u = u0;
+    Segment s(p, at, u0, u1);
+    for (; u < u1 && s.blk1 > s.blk0; ++seg) {
       const int row0 = s.chunk * R;
       const int all = p.causal ? max(0, s.len - p.Nq + 1) : s.len;     // keys below it are visible to every row
       float l[R];
 #pragma unroll
       for (int q = 0; q < R; ++q) l[q] = 0.f;
-      if (row < R) ref_l[row] = ref_o[row] = -INFINITY;
-      named_bar_sync(1, 128);
       const float* const qs = q_scale + (seg % C::kQBufs) * R;
       for (int j = 0; j < s.tiles; ++j, ++tile) {
         const int buf = tile & 1;
@@ -565,11 +581,12 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           }
           tc_fence_before();
           if (!there || key >= all) {
+            // row row0 + q is query (row0 + q) % Nq of its head, and sees the keys up to its own position
+            int query = p.causal ? row0 % p.Nq : p.Nq - 1;
 #pragma unroll
             for (int q = 0; q < R; ++q) {
-              // row row0 + q is query (row0 + q) % Nq of its head, and sees the keys up to its own position
-              const bool seen = there && (!p.causal || key <= s.len - p.Nq + (row0 + q) % p.Nq);
-              x[q] = seen ? x[q] : -INFINITY;
+              x[q] = there && key <= s.len - p.Nq + query ? x[q] : -INFINITY;
+              if (p.causal && ++query == p.Nq) query = 0;
             }
           }
 #pragma unroll
@@ -577,11 +594,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         }
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(bar_s_free(buf));
-        if (meet_or(grow)) {
-          if (meet_or(!ok)) {                            // a wait ran out somewhere: all leave together
-            ok = false;
-            break;
-          }
+        if (j == 0 || meet_or(grow)) {
           // the tile's maxima, as integers of the floats' order
 #pragma unroll
           for (int q = 0; q < R; ++q) {
@@ -598,7 +611,10 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
               warp_o[warp * R + q] = a + lvs;
             }
           }
-          named_bar_sync(1, 128);
+          if (meet_or(!ok)) {                            // a wait ran out somewhere: all leave together
+            ok = false;
+            break;
+          }
           if (row < R) {
             auto raise = [&](float* ref, const float* w, float* change) {
               const float old = ref[row];
@@ -689,10 +705,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         if (ok) mbar_arrive(bar_p_ready(buf));
       }
       // ---------------------------------------------------------- the row group's result
-      if (meet_or(!ok)) break;
-      const int last = tile - 1;
-      ok = wait(bar_p_empty(last & 1), (last >> 1) & 1, abort_flag, p.timeout_ns);
-      // the sums over the tile's 128 tokens
+      // (while the last P V runs) the sums over the tile's 128 tokens
 #pragma unroll
       for (int q = 0; q < R; ++q) {
         float sum = l[q];
@@ -701,11 +714,32 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         if (lane == 0) warp_l[warp * R + q] = sum;
       }
       if (meet_or(!ok)) break;
-      tc_fence_after();
+      if (row == 0) mbar_arrive(bar_q_empty(seg % C::kQBufs));         // all have read the queries' scales
       const bool whole = s.blk0 == 0 && s.blk1 == s.nblk;
       const long long slot0 = (2LL * blockIdx.x + (u == u0 ? 0 : 1)) * R;
       const size_t qrow = (static_cast<size_t>(s.b) * p.Hq + static_cast<size_t>(s.h) * p.G) * p.Nq + row0;
       const int rows = min(R, p.R - row0);
+      float* const factor = change_l;                    // of O, per row
+      if (row < R) {
+        const float sum = warp_l[row] + warp_l[R + row] + warp_l[2 * R + row] + warp_l[3 * R + row];
+        const float ml = ref_l[row], mo = ref_o[row] - kShift;
+        if (whole) {
+          factor[row] = sum == 0.f ? 0.f : ex2_approx(mo - ml) / sum;
+          if (row < rows) p.lse[qrow + row] = sum == 0.f ? -INFINITY : (ml + log2f(sum)) * kLn2;
+        } else {
+          float* const s3 = p.part_s + (slot0 + row) * 3;
+          s3[0] = ml;
+          s3[1] = sum;
+          s3[2] = mo;
+        }
+        ref_l[row] = ref_o[row] = -INFINITY;             // for the next row group
+      }
+      u = s.next;
+      if (u < u1) s = Segment(p, at, u, u1);
+      const int last = tile - 1;
+      ok = wait(bar_p_empty(last & 1), (last >> 1) & 1, abort_flag, p.timeout_ns);
+      if (meet_or(!ok)) break;
+      tc_fence_after();
 #pragma unroll
       for (int mb = 0; mb < C::kChunks; ++mb)
 #pragma unroll
@@ -721,34 +755,25 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           for (int k = 0; k < 3; ++k)
             asm volatile("" : "+r"(o[k][0]), "+r"(o[k][1]), "+r"(o[k][2]), "+r"(o[k][3]), "+r"(o[k][4]), "+r"(o[k][5]), "+r"(o[k][6]), "+r"(o[k][7]) :: "memory");
           const int col = 128 * mb + row;
+          float v[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int q = q0 + e;
-            const float v = __uint_as_float(o[0][e]) + (__uint_as_float(o[1][e]) + __uint_as_float(o[2][e]) * 0.03125f) * 0.03125f;
-            if (whole) {
-              const float sum = warp_l[q] + warp_l[R + q] + warp_l[2 * R + q] + warp_l[3 * R + q];
-              const float f = sum == 0.f ? 0.f : ex2_approx(ref_o[q] - kShift - ref_l[q]) / sum;
-              if (q < rows && col < p.c.d) p.o[(qrow + q) * p.c.d + col] = __float2bfloat16_rn(sum == 0.f ? 0.f : v * f);
-            } else {
-              p.part_o[(slot0 + q) * D + col] = v;
+          for (int e = 0; e < 8; ++e)
+            v[e] = __uint_as_float(o[0][e]) + (__uint_as_float(o[1][e]) + __uint_as_float(o[2][e]) * 0.03125f) * 0.03125f;
+          if (whole) {
+            __nv_bfloat16* const dst = p.o + (qrow + q0) * p.c.d + col;
+            if (col < p.c.d) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                // (a row that sees no key: 0, whatever V holds)
+                if (q0 + e < rows) dst[e * p.c.d] = __float2bfloat16_rn(factor[q0 + e] == 0.f ? 0.f : v[e] * factor[q0 + e]);
             }
+          } else {
+            float* const dst = p.part_o + (slot0 + q0) * D + col;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[e * D] = v[e];
           }
         }
       tc_fence_before();
-      if (row < R) {
-        const float sum = warp_l[row] + warp_l[R + row] + warp_l[2 * R + row] + warp_l[3 * R + row];
-        if (whole) {
-          if (row < rows) p.lse[qrow + row] = sum == 0.f ? -INFINITY : (ref_l[row] + log2f(sum)) * kLn2;
-        } else {
-          float* const s3 = p.part_s + (slot0 + row) * 3;
-          s3[0] = ref_l[row];
-          s3[1] = sum;
-          s3[2] = ref_o[row] - kShift;
-        }
-      }
-      named_bar_sync(1, 128);                            // references and sums are free for the next row group
-      if (row == 0) mbar_arrive(bar_q_empty(seg % C::kQBufs));
-      u = s.next;
     }
   }
 
@@ -930,7 +955,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 8) cache8_finish_kernel(con
       // a row in several parts is being joined by another CTA: its LSE from the parts, one per lane
       const RowParts rp(p, line, at.before, at.b, at.nblk, h, r, cols);
       float v;
-      if (rp.c0 == rp.c1) {
+      if (p.whole || rp.c0 == rp.c1) {
         v = p.lse[(static_cast<size_t>(at.b) * p.Hq + static_cast<size_t>(h) * p.G) * p.Nq + r] * kLog2e;
       } else {
         float ml = -INFINITY, sum = 0.f;
@@ -1020,7 +1045,7 @@ cudaError_t launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const Cache
   else if (cols == 16) e = launch_fwd<D, 16>(mk, mv, p, parts, stream);
   else if constexpr (D == 128) e = launch_fwd<D, 32>(mk, mv, p, parts, stream);
   if (e != cudaSuccess) return e;
-  const int rows = parts > 1 ? p.B * p.c.Hkv * p.R : 0;
+  const int rows = parts > 1 && !p.whole ? p.B * p.c.Hkv * p.R : 0;
   const bool single = rows > kJoinRows;
   const int join = single ? (rows + kFinishWarps - 1) / kFinishWarps : rows;
   const long long blocks = static_cast<long long>(p.B) * p.c.Hkv * p.max_blocks;
@@ -1032,16 +1057,33 @@ cudaError_t launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const Cache
 
 }  // namespace
 
+// CTAs that run at once, Cfg::kPerSm on each SM
+static int cache8_wave(int d, int cols) { return kCache8Sms * (d > 128 && cols > 8 ? 1 : 2); }
+
 int cache8_columns(int d, int R) { return R <= 8 ? 8 : R <= 16 || d > 128 ? 16 : 32; }
+
+// Short row groups: one CTA each, as they come, and no second launch. Up to 8 blocks: 8 groups of
+// 4 and 8 take 8.7 and 10.8 us on the GPU and 21.5 for the call, cut and joined 9.7 and 9.8, and 25;
+// 128 groups 10.6 and 12.8 against 15.9 and 16.4; at d 256 384 groups of 8 31 against 35. Up to 16
+// at d 128 with more groups than SMs: 240, 384 and 1024 groups 19, 35 and 72 against 27, 36 and 89
+// (fewer: 8 groups 15.4 against 10.8; d 256: 53 against 49; 32 blocks: 31, 55 and 115 against 35, 49
+// and 113).
+bool cache8_whole(int B, int Hkv, int d, int R, int max_blocks) {
+  const int cols = cache8_columns(d, R), chunks = (R + cols - 1) / cols;
+  const bool many = static_cast<long long>(B) * Hkv * chunks > kCache8Sms && d <= 128;
+  return max_blocks <= (many ? 2 * kWholeBlocks : kWholeBlocks);
+}
 
 int cache8_parts(int B, int Hkv, int d, int R, int max_blocks) {
   const int cols = cache8_columns(d, R), chunks = (R + cols - 1) / cols;
-  const long long units = static_cast<long long>(B) * Hkv * chunks * max_blocks;
-  const int most = kCache8Sms * (d > 128 && cols > 8 ? 1 : 2);         // Cfg::kPerSm CTAs per SM
+  const long long groups = static_cast<long long>(B) * Hkv * chunks, units = groups * max_blocks;
+  if (cache8_whole(B, Hkv, d, R, max_blocks)) return static_cast<int>(groups);
+  const int most = cache8_wave(d, cols);
   return static_cast<int>(units < most ? units : most);
 }
 
-cudaError_t launch_cache8_fwd(const CUtensorMap& mk, const CUtensorMap& mv, const Cache8Params& p, cudaStream_t stream) {
+cudaError_t launch_cache8_fwd(const CUtensorMap& mk, const CUtensorMap& mv, Cache8Params p, cudaStream_t stream) {
+  p.whole = cache8_whole(p.B, p.c.Hkv, p.c.d, p.R, p.max_blocks) ? 1 : 0;
   const int parts = cache8_parts(p.B, p.c.Hkv, p.c.d, p.R, p.max_blocks);
   return p.c.d <= 128 ? launch_all<128>(mk, mv, p, parts, stream) : launch_all<256>(mk, mv, p, parts, stream);
 }

@@ -164,6 +164,7 @@ struct Cache8Params {
   int B, max_blocks, Hq, Nq;
   int G, R;                        // query heads per KV head; rows of a KV head's group, G * Nq
   int chunks;                      // row chunks of cache8_columns() rows
+  int whole;                       // 1: one row group per CTA, nothing to join (set at the launch)
   int causal, add_weights;
   float scale_log2, decay;
   unsigned* status;                // device status word
@@ -186,10 +187,11 @@ struct Cache8EvictParams {
 constexpr int kCache8MaxRows = 128;   // G * Nq of one call
 constexpr int kCache8Sms = 152;       // the attention's grid: one or two CTAs on each of them
 int cache8_columns(int d, int R);     // query rows a CTA takes at once
+bool cache8_whole(int B, int Hkv, int d, int R, int max_blocks);  // one row group per CTA, no partial results
 int cache8_parts(int B, int Hkv, int d, int R, int max_blocks);   // CTAs, parts the work is cut into at most
 cudaError_t launch_cache8_append(const Cache8AppendParams& p, cudaStream_t stream);
 // maps over the codes as [num_blocks * Hkv, 64, d], boxes of 64 rows by 128 bytes
-cudaError_t launch_cache8_fwd(const CUtensorMap& mk, const CUtensorMap& mv, const Cache8Params& p, cudaStream_t stream);
+cudaError_t launch_cache8_fwd(const CUtensorMap& mk, const CUtensorMap& mv, Cache8Params p, cudaStream_t stream);
 cudaError_t launch_cache8_evict(const Cache8EvictParams& p, cudaStream_t stream);
 
 }  // namespace fa
