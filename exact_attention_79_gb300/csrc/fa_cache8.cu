@@ -25,10 +25,11 @@
 // sequences of 8192.)
 //
 // HBM-bound: 2 d bytes per cached token and KV head, against which Q and O
-// are small. Measured: 32 sequences of 2048 to 8192 tokens, 64 heads on 8, d 128: 68 us, 5.1 TB/s; two of
-// 131072: 87 us, 5.8 TB/s; 6 of up to 5000, 16 heads, 4 queries, d 256: 40 us, 3.7 TB/s. The steady state
-// takes the memory's whole rate; lost are 8 us until the first tiles are there, the
-// spread of the CTAs' ends (4 us) and the join (3 us). The work is a line of units, one per (sequence, KV head, chunk of
+// are small. Measured: 32 sequences of 2048 to 8192 tokens, 64 heads on 8, d 128: 67 us,
+// 5.2 TB/s; two of 131072: 87 us, 5.8 TB/s; 6 of up to 5000, 16 heads, 4 queries, d 256: 38
+// us, 3.9 TB/s. The steady state takes the memory's whole rate (a tile per CTA in 2700 cycles,
+// 2000 of them softmax); lost are 8 us until the first tiles are there, the spread of the
+// CTAs' ends (4 us), the changes of row groups and the join (3 us). The work is a line of units, one per (sequence, KV head, chunk of
 // rows, block of 64 tokens), cut into equal parts for the CTAs (two per SM, so
 // that one's row changes hide behind the other's stream) whatever the
 // sequences' lengths; a row whose units fall to several CTAs is joined from
@@ -106,7 +107,7 @@ __device__ __forceinline__ int line_total(const Cache8Params& p, int lane) {
 // but a CTA that goes on to another row group loses the time of a few blocks
 // with the one's results and the other's queries: `turn` places more lie ahead
 // of each group's units. (With units alone CTAs with three groups ended 6 us
-// after those with one, of 59; with the turns all within 4.) A part is at least
+// after those with one, of 59. Turns of 3 and 4 blocks measure alike, 2 and 8 slower.) A part is at least
 // twice a turn long, so that it has units, and where it begins in a turn its
 // first units are that group's; hence every part between a group's first and
 // last has a partial result of it.

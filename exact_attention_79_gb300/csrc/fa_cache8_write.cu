@@ -5,7 +5,10 @@
 // largest magnitude within 448. When a block that already holds tokens gets a
 // larger one, its scale grows and the codes there are re-encoded by the ratio
 // (a power of two). HBM-bound: each new value is read once (2 bytes) and
-// written once (1 byte).
+// written once (1 byte). One CTA of 128 threads per block, head and K or V, eight
+// 16-byte loads in flight per thread; 256 threads with four each spent a third more
+// instructions on finding their block (35 us). 30011 tokens of 8 heads, d 128: 31 us, 6.0 TB/s;
+// one token each for 64 sequences 5.3 us, which is the launch and two rounds of loads.
 #include "fa_cache8.cuh"
 
 namespace fa {

@@ -19,6 +19,15 @@
 // c of the first round of gridDim.x items, the c-th from the end of the second, and so
 // on: costs fall along the line, so the two directions even out.
 //
+// What bounds it (64 heads on 8, d 128, causal, 16384 rows). A step of two tiles takes about
+// 2700 cycles where the tensor core needs 2048: the issuing thread's pace, as in fa_fwd.cu. Around
+// an item 2800 more: the diagonal tile's softmax (700 above the others'), its P V with nothing
+// beside it, and O's way out (1900 to 3000, through 4 KB per warp that wait for the TMA unit
+// once; 16-byte stores from registers take 10% longer). Sequences of 128, 512, 1024, 2048, 8192 rows: 132, 190, 267,
+// 420, 1400 us, the last at 1.57 PFLOP/s; 24 of 32 to 1593 rows 292 us (0.92 PFLOP/s of what the
+// causal rule needs, 1.16 with the diagonal tiles whole). Up to 128 rows the bytes of Q and O
+// bound it (4.6 TB/s).
+//
 // Warps: 0-3 and 4-7 the two softmax groups (one thread per query row), 8 TMA
 // producer, 9 tensor-core issuer, 10 ring watcher, 11 scheduler. Barriers and
 // parities run on across items; the steps within an item are as in fa_fwd.cu, but
