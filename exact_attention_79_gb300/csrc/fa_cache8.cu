@@ -293,7 +293,6 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   auto bar_kv_empty = [&](int i) { return bars + 64u + 8u * i; };      // 8
   auto bar_info = [&](int i) { return bars + 128u + 8u * i; };         // kInfo
   auto bar_s_full = [&](int i) { return bars + 192u + 8u * i; };
-  auto bar_s_free = [&](int i) { return bars + 208u + 8u * i; };
   auto bar_p_ready = [&](int i) { return bars + 224u + 8u * i; };
   auto bar_p_empty = [&](int i) { return bars + 240u + 8u * i; };      // P V done
   auto bar_q_full = [&](int i) { return bars + 256u + 8u * i; };
@@ -322,7 +321,6 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     for (int i = 0; i < kInfo; ++i) mbar_init(bar_info(i), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar_s_full(i), 1);
-      mbar_init(bar_s_free(i), 4);
       mbar_init(bar_p_ready(i), 128);
       mbar_init(bar_p_empty(i), 1);
       mbar_init(bar_q_full(i), 1);
@@ -402,8 +400,8 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       // S^T of tile `t`, whose K is load 2 t, with the queries of segment `g`
       auto scores = [&](int t, int g) {
         const int slot = (2 * t) % C::kRing;
-        ok = wait(bar_kv_full(slot), ((2 * t) / C::kRing) & 1, abort_flag, p.timeout_ns) &&
-             wait(bar_s_free(t & 1), ((t >> 1) & 1) ^ 1, abort_flag, p.timeout_ns);
+        // (its buffer is free: S of two tiles before was read ahead of that tile's P-ready, long waited for)
+        ok = wait(bar_kv_full(slot), ((2 * t) / C::kRing) & 1, abort_flag, p.timeout_ns);
         if (!ok) return;
         tc_fence_after();
         const uint64_t kd = smem_desc_sw128(s_kv(slot), 16, 1024);
@@ -593,8 +591,6 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
           for (int q = 0; q < R; ++q) grow |= x[q] > ref_l[q] + kTrail || x[q] + lvs > ref_o[q] + kTrail;
         }
-        __syncwarp();
-        if (ok && lane == 0) mbar_arrive(bar_s_free(buf));
         if (j == 0 || meet_or(grow)) {
           // the tile's maxima, as integers of the floats' order
 #pragma unroll
@@ -663,8 +659,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           for (int q = 0; q < R; q += 4)
             if (row0 + q < p.R) keep[q / 4] = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
         }
-        // the P V that read this buffer two tiles ago has completed
-        if (ok) ok = wait(bar_p_empty(buf), ((tile >> 1) & 1) ^ 1, abort_flag, p.timeout_ns);
+        // (the P V that read this buffer two tiles ago was issued ahead of this tile's S, so it has completed)
         const uint32_t dst = s_p + buf * C::kPBytes + (row & 15);
         const int unit = row >> 4;
 #pragma unroll
