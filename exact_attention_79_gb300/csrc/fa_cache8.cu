@@ -165,6 +165,18 @@ struct Place {
   // whole warp; one look at the lengths where a warp holds them all.
   __device__ __forceinline__ bool start(const Cache8Params& p, int i, int ctas, int lane, int& u0, int& u1) {
     const int per_block = p.c.Hkv * p.chunks;
+    if (p.whole) {                                       // (the grid is B * per_block)
+      b = i / per_block;
+      load(p);
+      turn = before = 0;
+      if (p.scores != nullptr) {
+        for (int x = lane; x < b; x += 32) before += line_blocks(p, x);
+        before = __reduce_add_sync(0xffffffffu, before) * per_block;
+      }
+      u0 = before + (i - b * per_block) * nblk;
+      u1 = u0 + nblk;
+      return true;
+    }
     int mine = 0, units;
     if (p.B <= 32) {
       mine = lane < p.B ? cache_length(p.lengths, lane, p.max_blocks) : -1;
@@ -173,18 +185,6 @@ struct Place {
       units = line_total(p, lane);
     }
     const Line line(p, units, ctas);
-    if (p.whole) {
-      const int seq = i / per_block;                     // (the grid is B * per_block)
-      turn = 0;
-      b = seq;
-      load(p);
-      int sum = 0;
-      for (int x = lane; x < seq; x += 32) sum += line_blocks(p, x);
-      before = __reduce_add_sync(0xffffffffu, sum) * per_block;
-      u0 = before + (i - seq * per_block) * nblk;
-      u1 = u0 + nblk;
-      return true;
-    }
     if (i >= line.parts) return false;
     u0 = line.begin(i);
     u1 = line.begin(i + 1);
