@@ -410,19 +410,27 @@ def fwd_packed(q, k, v, cu_seqlens, causal=True, scale=None, out=None, lse=None)
     Hkv, dev = k.shape[0], q.device
     if scale is None:
         scale = d ** -0.5
-    o = torch.empty_like(q) if out is None else out
-    lse = torch.empty((Hq, T), dtype=torch.float32, device=dev) if lse is None else lse
-    args = []
-    for t, n, H in ((q, "q", Hq), (k, "k", Hkv), (v, "v", Hkv), (o, "out", Hq)):
-        args += (t.data_ptr(), *_heads_strides(t, n, H, T, d))
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must be [S + 1]")
     S = cu_seqlens.shape[0] - 1
-    _require(dev, (cu_seqlens, "cu_seqlens", torch.int32, (S + 1,)), (lse, "lse", torch.float32, (Hq, T)))
-    _placed(dev, (k, "k"), (v, "v"), (o, "out"))
+    specs = [(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,))]
+    strides = [*_heads_strides(q, "q", Hq, T, d), *_heads_strides(k, "k", Hkv, T, d), *_heads_strides(v, "v", Hkv, T, d)]
+    placed = [(k, "k"), (v, "v")]
+    if out is not None:
+        _heads_strides(out, "out", Hq, T, d)
+        placed.append((out, "out"))
+    if lse is not None:
+        specs.append((lse, "lse", torch.float32, (Hq, T)))
+    _require(dev, *specs)
+    _placed(dev, *placed)
+    o = torch.empty_like(q) if out is None else out
+    if lse is None:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
     if T == 0 or S == 0:
         return o, lse
-    _call_on(dev, "fa_fwd_packed", *args, lse.data_ptr(), cu_seqlens.data_ptr(), S, T, Hq, Hkv, d, int(bool(causal)),
+    q_h, q_t, k_h, k_t, v_h, v_t = strides
+    _call_on(dev, "fa_fwd_packed", q.data_ptr(), q_h, q_t, k.data_ptr(), k_h, k_t, v.data_ptr(), v_h, v_t, o.data_ptr(),
+             *_heads_strides(o, "out", Hq, T, d), lse.data_ptr(), cu_seqlens.data_ptr(), S, T, Hq, Hkv, d, int(bool(causal)),
              float(scale))
     return o, lse
 
@@ -499,10 +507,16 @@ def cache8_evict(cache, block_table, lengths, keep, recent, to_table, new_length
     if cache.weight is None:
         raise ValueError("eviction needs a cache with weights")
     B, dev, i32 = block_table.shape[0], cache.k.device, torch.int32
-    new_lengths = torch.empty(B, dtype=i32, device=dev) if new_lengths is None else new_lengths
-    kept = torch.empty((B, Hkv, keep), dtype=i32, device=dev) if kept is None else kept
-    _require(dev, *specs, _table_spec(block_table), _table_spec(to_table, "to_table", B), (lengths, "lengths", i32, (B,)),
-             (new_lengths, "new_lengths", i32, (B,)), (kept, "kept", i32, (B, Hkv, keep)))
+    specs += [_table_spec(block_table), _table_spec(to_table, "to_table", B), (lengths, "lengths", i32, (B,))]
+    if new_lengths is not None:
+        specs.append((new_lengths, "new_lengths", i32, (B,)))
+    if kept is not None:
+        specs.append((kept, "kept", i32, (B, Hkv, keep)))
+    _require(dev, *specs)
+    if new_lengths is None:
+        new_lengths = torch.empty(B, dtype=i32, device=dev)
+    if kept is None:
+        kept = torch.empty((B, Hkv, max(keep, 0)), dtype=i32, device=dev)
     _call_on(dev, "fa_cache8_evict", ctypes.byref(c), block_table.data_ptr(), block_table.shape[1], lengths.data_ptr(), B,
              keep, recent, to_table.data_ptr(), to_table.shape[1], kept.data_ptr(), new_lengths.data_ptr())
     return new_lengths, kept
