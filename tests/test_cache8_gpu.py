@@ -383,6 +383,7 @@ APPENDS = [
     ([65, 62], [63, 2], 2, 16, False),
     ([129, 3], [30, 61], 5, 80, True),
     ([40], [0], 1, 192, True),
+    ([1, 0, 3, 70, 0] * 20, [0, 64, 62, 10, 5] * 20, 2, 32, True),          # more sequences than a warp has lanes
 ]
 
 
@@ -450,6 +451,7 @@ EVICTS = [
     ([1025, 1024], 1023, 1, 2, 80),
     ([300], 300, 10, 3, 256),             # nothing to drop
     ([70, 9], 1, 0, 1, 192),
+    ([200, 0, 64, 130] * 12, 100, 7, 2, 16),
 ]
 
 

@@ -71,6 +71,8 @@ CASES = [
     ([200, 77], 4, 1, 112, False, "fused"),
     ([3] * 70 + [260], 2, 1, 64, True, "token"),                # more sequences than a warp has lanes
     ([1500, 1400, 300], 1, 1, 128, True, "head"),
+    ([2] * 300 + [130, 0, 700] + [1, 0] * 100 + [290], 2, 1, 64, True, "token"),    # more than the look-up keeps in registers
+    ([5, 0, 1] * 120 + [385], 3, 3, 128, False, "head"),
 ]
 
 
