@@ -22,10 +22,11 @@
 // What bounds it (64 heads on 8, d 128, causal, 16384 rows). A step of two tiles takes about
 // 2700 cycles where the tensor core needs 2048: the issuing thread's pace, as in fa_fwd.cu. Around
 // an item 2800 more: the diagonal tile's softmax (700 above the others'), its P V with nothing
-// beside it, and O's way out (1900 to 3000, through 4 KB per warp that wait for the TMA unit
-// once; 16-byte stores from registers take 10% longer). Sequences of 128, 512, 1024, 2048, 8192 rows: 132, 190, 267,
-// 420, 1400 us, the last at 1.57 PFLOP/s; 24 of 32 to 1593 rows 292 us (0.92 PFLOP/s of what the
-// causal rule needs, 1.16 with the diagonal tiles whole). Up to 128 rows the bytes of Q and O
+// beside it, and O's way out (1900 to 3000, through 4 KB per warp, whose second half is read
+// and packed while the TMA unit takes the first; 16-byte stores from registers take 10% longer,
+// coalesced ones through the same 4 KB 30%). Sequences of 128, 512, 1024, 2048, 8192 rows: 130, 188,
+// 264, 420, 1400 us, the last at 1.57 PFLOP/s; 24 of 32 to 1593 rows 290 us (0.93 PFLOP/s of what
+// the causal rule needs, 1.18 with the diagonal tiles whole). Up to 128 rows the bytes of Q and O
 // bound it (4.6 TB/s).
 //
 // Warps: 0-3 and 4-7 the two softmax groups (one thread per query row), 8 TMA
@@ -651,25 +652,26 @@ fwd_packed_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
       if (!__all_sync(0xffffffffu, ok)) break;
       no ^= 1;
       tc_fence_after();
-      uint32_t o[D / 32][32], r[D / 2];
-#pragma unroll
-      for (int x = 0; x < D / 32; ++x) tmem_ld_32x32b_x32(t_o + 32 * x, o[x]);
-      tmem_wait_ld();
-#pragma unroll
-      for (int x = 0; x < D / 32; ++x) {
-        reg_fence_x32(o[x]);
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          r[16 * x + e] = pack_bf16x2(__uint_as_float(o[x][2 * e]) * inv_l, __uint_as_float(o[x][2 * e + 1]) * inv_l);
-      }
 #pragma unroll
       for (int x0 = 0; x0 < D; x0 += 64) {
+        // (the second half is read and packed while the first one leaves)
+        uint32_t o[2][32], r[32];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) tmem_ld_32x32b_x32(t_o + x0 + 32 * x, o[x]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          reg_fence_x32(o[x]);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            r[16 * x + e] = pack_bf16x2(__uint_as_float(o[x][2 * e]) * inv_l, __uint_as_float(o[x][2 * e + 1]) * inv_l);
+        }
         if (lane == 0) tma_store_wait_read0();           // the warp's last store has left its buffer
         __syncwarp();
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(swz128(stage, lane, u)), "r"(r[x0 / 2 + 4 * u]),
-                       "r"(r[x0 / 2 + 4 * u + 1]), "r"(r[x0 / 2 + 4 * u + 2]), "r"(r[x0 / 2 + 4 * u + 3]) : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(swz128(stage, lane, u)), "r"(r[4 * u]), "r"(r[4 * u + 1]),
+                       "r"(r[4 * u + 2]), "r"(r[4 * u + 3]) : "memory");
         if (valid == 32) {
           fence_proxy_async_smem();
           __syncwarp();
