@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelCtas = 8;                     // CTAs of a cluster at most
+constexpr int kSelCtas = 4;                     // CTAs of a cluster at most
 constexpr int kBins = 256;
 constexpr int kSelKeys = 49152;                 // keys of a CTA that stay in shared memory (192 KB)
 constexpr int kGatherThreads = 64;
@@ -350,11 +350,11 @@ __global__ void __launch_bounds__(kGatherThreads, D == 128 ? 18 : 8) cache8_gath
 }  // namespace
 
 cudaError_t launch_cache8_evict(const Cache8EvictParams& p, cudaStream_t stream) {
-  // One CTA per (sequence, head) or a cluster of eight. 8 of them: up to 4096 tokens one is as fast
-  // (12.8 us against 12.3 for both kernels; 10.8 against 11.8 at 1024), at 8192 and 32768 eight, 12.8 and
-  // 17 against 15.9 and 36. 64 of them, whose clusters fill the SMs: at 8192 23.6 and 25.4, at 16384 44 and 34.
-  const bool few = static_cast<long long>(p.B) * p.c.Hkv * kSelCtas <= kCache8Sms;
-  const int ctas = p.max_blocks > (few ? 64 : 128) ? kSelCtas : 1;
+  // One CTA per (sequence, head) or a cluster of four, whichever fills the SMs. Both kernels, us, one / four / eight:
+  // 16 of them, 2048 tokens 11.3 / 11.3 / 13.7, 4608 13.9 / 11.8 / 14.8, 32768 40 / 22 / 23;
+  // 64, 4608 17 / 18 / 22, 8192 24 / 20 / 25, 32768 72 / 56 / 57; 256, 8192 56 / 64 / 91, 16384 115 / 105 / 127.
+  const bool many = static_cast<long long>(p.B) * p.c.Hkv > kCache8Sms;
+  const int ctas = p.max_blocks > (many ? 128 : 64) ? kSelCtas : 1;
   const int most = (p.max_blocks + ctas - 1) / ctas;     // blocks per CTA, more than it will have
   const int room = most < kSelKeys / kCacheBlock ? most * kCacheBlock : kSelKeys;
   static PerDeviceOnce attr;

@@ -478,6 +478,8 @@ def test_evict_bit_for_bit(fa, lens, keep, recent, Hkv, d, ties):
     ([8300], 8299, 0, 1),                             # all but one
     ([8300], 8200, 8199, 1),                          # one besides the recent ones
     ([430001], 66000, 64, 1),                         # more keys than the CTAs' shared memory holds
+    ([5000, 4097, 4300, 64] * 3, 700, 5, 3),
+    ([9000, 8193] + [10] * 158, 900, 0, 1),           # more sequences than SMs
 ])
 @pytest.mark.parametrize("ties", [False, True])
 def test_evict_long_caches(fa, lens, keep, recent, Hkv, ties):
