@@ -219,7 +219,8 @@ struct Place {
 template <int D, int R>
 struct Cfg {
   static constexpr int kChunks = D / 128;                  // 128-byte columns of K and V
-  static constexpr int kNS = 2 * R;                        // S^T columns: two terms of Q
+  static constexpr int kNS = R < 8 ? 16 : 2 * R;           // S^T columns: two terms of Q (16 at least)
+  static constexpr int kE = R < 8 ? R : 8;                 // rows dealt with together
   static constexpr int kNP = (3 * R + 15) / 16 * 16;       // O^T columns: three terms of P
   static constexpr int kPerSm = D == 256 && R > 8 ? 1 : 2;
   static constexpr int kTile = 16384 * kChunks;            // K or V of a tile
@@ -458,18 +459,18 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       if (!ok) break;
       const uint32_t dst = s_q + buf * C::kQBytes;
       for (int q0 = 0; q0 < R; q0 += 8) {
-        uint2 v[8][C::kChunks];                          // eight rows' loads on their way together
+        uint2 v[C::kE][C::kChunks];                      // the rows' loads on their way together
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < C::kE; ++e)
 #pragma unroll
           for (int ch = 0; ch < C::kChunks; ++ch) {
             const int col = 128 * ch + 4 * lane;
             v[e][ch] = make_uint2(0, 0);
             if (q0 + e < rows && col < p.c.d) v[e][ch] = *reinterpret_cast<const uint2*>(p.q + (qrow + q0 + e) * p.c.d + col);
           }
-        float amax[8];
+        float amax[C::kE];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < C::kE; ++e) {
           amax[e] = 0.f;
 #pragma unroll
           for (int ch = 0; ch < C::kChunks; ++ch) {
@@ -481,9 +482,9 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         }
         // (non-negative floats order like their bits)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax[e] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax[e])));
+        for (int e = 0; e < C::kE; ++e) amax[e] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax[e])));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < C::kE; ++e) {
           const int q = q0 + e;
           // exponent that brings the largest to [128, 256); bounded so that both powers are normal.
           // An infinity among them becomes NaN, as its logits are.
@@ -533,9 +534,9 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
       for (int q = 0; q < R; ++q) l[q] = 0.f;
       const float* const qs = q_scale + (seg % C::kQBufs) * R;
-      // for 8 rows the references and the queries' scales stay in registers between their
+      // for 4 and 8 rows the references and the queries' scales stay in registers between their
       // changes (65.4 -> 64.7 us over 32 sequences; more rows have none to spare)
-      constexpr bool kKeep = R == 8;
+      constexpr bool kKeep = R <= 8;
       float ml[kKeep ? R : 1], mo[kKeep ? R : 1], sq[kKeep ? R : 1];
 #pragma unroll
       for (int q = 0; q < (kKeep ? R : 1); ++q) {
@@ -572,12 +573,12 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           for (int q0 = 0; q0 < R; q0 += 8) {
             // columns q0 .. + 7 of both terms
             uint32_t hi[16], lo[16];
-            if constexpr (R == 8) {
+            if constexpr (R <= 8) {
               tmem_ld_x16(tbase + lane_off + buf * C::kNS, hi);
               tmem_wait_ld();
               reg_fence_x16(hi);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) lo[e] = hi[8 + e];
+              for (int e = 0; e < R; ++e) lo[e] = hi[R + e];
             } else if (q0 % 16 == 0) {
               tmem_ld_x16(tbase + lane_off + buf * C::kNS + q0, hi);
               tmem_ld_x16(tbase + lane_off + buf * C::kNS + R + q0, lo);
@@ -591,7 +592,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
               continue;
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < C::kE; ++e)
               x[q0 + e] = fmaf(__uint_as_float(lo[e]), 0.0625f, __uint_as_float(hi[e])) * (ks * scale_q(q0 + e));
           }
           tc_fence_before();
@@ -703,9 +704,9 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           const uint32_t codes[3] = {c0, c1, c2};
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
-            // rows k R + q and k R + q + 1 of the operand (R a multiple of 8), byte `row`
-            store_byte(dst + (k * R + q) * 128 + ((unit ^ (q & 7)) << 4), codes[k]);
-            store_byte(dst + (k * R + q + 1) * 128 + ((unit ^ ((q + 1) & 7)) << 4), codes[k] >> 8);
+            // rows k R + q and k R + q + 1 of the operand, byte `row`
+            store_byte(dst + (k * R + q) * 128 + ((unit ^ ((k * R + q) & 7)) << 4), codes[k]);
+            store_byte(dst + (k * R + q + 1) * 128 + ((unit ^ ((k * R + q + 1) & 7)) << 4), codes[k] >> 8);
           }
         }
         if (!there) {
@@ -773,22 +774,22 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           for (int k = 0; k < 3; ++k)
             asm volatile("" : "+r"(o[k][0]), "+r"(o[k][1]), "+r"(o[k][2]), "+r"(o[k][3]), "+r"(o[k][4]), "+r"(o[k][5]), "+r"(o[k][6]), "+r"(o[k][7]) :: "memory");
           const int col = 128 * mb + row;
-          float v[8];
+          float v[C::kE];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
+          for (int e = 0; e < C::kE; ++e)
             v[e] = __uint_as_float(o[0][e]) + (__uint_as_float(o[1][e]) + __uint_as_float(o[2][e]) * 0.03125f) * 0.03125f;
           if (whole) {
             __nv_bfloat16* const dst = p.o + (qrow + q0) * p.c.d + col;
             if (col < p.c.d) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
+              for (int e = 0; e < C::kE; ++e)
                 // (a row that sees no key: 0, whatever V holds)
                 if (q0 + e < rows) dst[e * p.c.d] = __float2bfloat16_rn(factor[q0 + e] == 0.f ? 0.f : v[e] * factor[q0 + e]);
             }
           } else {
             float* const dst = p.part_o + (slot0 + q0) * D + col;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e * D] = v[e];
+            for (int e = 0; e < C::kE; ++e) dst[e * D] = v[e];
           }
         }
       tc_fence_before();
@@ -1059,7 +1060,8 @@ template <int D>
 cudaError_t launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const Cache8Params& p, int parts, cudaStream_t stream) {
   const int cols = cache8_columns(p.c.d, p.R);
   cudaError_t e = cudaErrorInvalidValue;
-  if (cols == 8) e = launch_fwd<D, 8>(mk, mv, p, parts, stream);
+  if (cols == 4) e = launch_fwd<D, 4>(mk, mv, p, parts, stream);
+  else if (cols == 8) e = launch_fwd<D, 8>(mk, mv, p, parts, stream);
   else if (cols == 16) e = launch_fwd<D, 16>(mk, mv, p, parts, stream);
   else if constexpr (D == 128) e = launch_fwd<D, 32>(mk, mv, p, parts, stream);
   if (e != cudaSuccess) return e;
@@ -1078,7 +1080,7 @@ cudaError_t launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const Cache
 // CTAs that run at once, Cfg::kPerSm on each SM
 static int cache8_wave(int d, int cols) { return kCache8Sms * (d > 128 && cols > 8 ? 1 : 2); }
 
-int cache8_columns(int d, int R) { return R <= 8 ? 8 : R <= 16 || d > 128 ? 16 : 32; }
+int cache8_columns(int d, int R) { return R <= 4 ? 4 : R <= 8 ? 8 : R <= 16 || d > 128 ? 16 : 32; }
 
 // Short row groups: one CTA each, as they come, and no second launch. Up to 8 blocks: 8 groups of
 // 4 and 8 take 8.7 and 10.8 us on the GPU and 21.5 for the call, cut and joined 9.7 and 9.8, and 25;

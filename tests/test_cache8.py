@@ -78,7 +78,7 @@ def test_workspace_bytes(lib):
     # [columns][D] and [columns][3] floats; none where row groups have 8 blocks or fewer each (16 where there are more than 152 of
     # them). With weights the scores of every unit: 64 tokens x rows
     ws = lib.fa_fwd_cache8_workspace_bytes
-    assert ws(1, 4, 2, 1, 64, 9, 0) == 2 * 18 * 8 * 128 * 4 + -(-2 * 18 * 8 * 3 * 4 // 256) * 256     # D = 128 up to d = 128
+    assert ws(1, 4, 2, 1, 64, 9, 0) == 2 * 18 * 4 * 128 * 4 + -(-2 * 18 * 4 * 3 * 4 // 256) * 256     # D = 128 up to d = 128
     assert ws(1, 4, 2, 1, 64, 9, 1) == ws(1, 4, 2, 1, 64, 9, 0) + 18 * 64 * 4 * 4         # 2 rows, kept as 4
     assert ws(1, 4, 2, 1, 64, 8, 0) == 256 and ws(1, 4, 2, 1, 64, 4, 1) == 8 * 64 * 4 * 4
     assert ws(80, 4, 2, 1, 64, 16, 0) == 256 and ws(76, 4, 2, 1, 64, 16, 0) > 256
