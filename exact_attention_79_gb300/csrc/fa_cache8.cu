@@ -30,7 +30,7 @@
 // us, 3.9 TB/s. The steady state takes the memory's whole rate (a tile per CTA in 2700 cycles,
 // 2000 of them softmax); lost are 8 us until the first tiles are there, the spread of the
 // CTAs' ends (4 us), the changes of row groups and the join (3 us). The work is a line of units, one per (sequence, KV head, chunk of
-// rows, block of 64 tokens), cut into equal parts for the CTAs (two per SM, so
+// rows, block of 64 tokens), cut into equal parts for the CTAs (mostly two per SM, so
 // that one's row changes hide behind the other's stream) whatever the
 // sequences' lengths; a row whose units fall to several CTAs is joined from
 // their partial results by a second kernel.
@@ -216,13 +216,14 @@ struct Place {
   }
 };
 
-template <int D, int R>
+// D: 128 or 256, d at most that; R: query rows a CTA takes at once; S: CTAs per SM.
+template <int D, int R, int S>
 struct Cfg {
   static constexpr int kChunks = D / 128;                  // 128-byte columns of K and V
   static constexpr int kNS = R < 8 ? 16 : 2 * R;           // S^T columns: two terms of Q (16 at least)
   static constexpr int kE = R < 8 ? R : 8;                 // rows dealt with together
   static constexpr int kNP = (3 * R + 15) / 16 * 16;       // O^T columns: three terms of P
-  static constexpr int kPerSm = D == 256 && R > 8 ? 1 : 2;
+  static constexpr int kPerSm = S;
   static constexpr int kTile = 16384 * kChunks;            // K or V of a tile
   static constexpr int kQBufs = 2;
   static constexpr int kQBytes = kNS * 128 * kChunks;
@@ -230,7 +231,7 @@ struct Cfg {
   // references and their changes (4 R), the warps' maxima and sums (8 R), 1 / scale of Q per buffer
   static constexpr int kStatFloats = 4 * R + 8 * R + 2 * R;
   static constexpr int kFixed = kQBufs * kQBytes + 2 * kPBytes + kStatFloats * 4 + kInfo * 32 + 320;
-  static constexpr int kBudget = (kPerSm == 2 ? 113 : 227) * 1024;
+  static constexpr int kBudget = (S == 3 ? 75 : S == 2 ? 113 : 227) * 1024;
   static constexpr int kFit = (kBudget - kFixed) / kTile;
   static constexpr int kRing = kFit < 8 ? kFit : 8;        // tiles of K or V
   static constexpr int kLayout = kRing * kTile + kFixed;
@@ -264,10 +265,10 @@ struct Segment {
   }
 };
 
-template <int D, int R>
-__global__ void __launch_bounds__(kThreads, Cfg<D, R>::kPerSm)
+template <int D, int R, int S>
+__global__ void __launch_bounds__(kThreads, Cfg<D, R, S>::kPerSm)
 cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Cache8Params p) {
-  using C = Cfg<D, R>;
+  using C = Cfg<D, R, S>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -534,9 +535,9 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
       for (int q = 0; q < R; ++q) l[q] = 0.f;
       const float* const qs = q_scale + (seg % C::kQBufs) * R;
-      // for 4 and 8 rows the references and the queries' scales stay in registers between their
-      // changes (65.4 -> 64.7 us over 32 sequences; more rows have none to spare)
-      constexpr bool kKeep = R <= 8;
+      // where there are registers to spare, the references and the queries' scales stay in them between
+      // their changes (65.4 -> 64.7 us over 32 sequences; 16 rows of d 256 52 -> 46)
+      constexpr bool kKeep = R * S <= 16;
       float ml[kKeep ? R : 1], mo[kKeep ? R : 1], sq[kKeep ? R : 1];
 #pragma unroll
       for (int q = 0; q < (kKeep ? R : 1); ++q) {
@@ -1046,24 +1047,36 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 8) cache8_finish_kernel(con
   }
 }
 
-template <int D, int R>
+// CTAs per SM: at d 64 the softmax, not the memory, paces two of four rows each (32 and 256
+// sequences of up to 4096 tokens 32 and 194 us, with three 30 and 162; at d 128 62 and 63; eight rows
+// have no registers for three: 17 against 21 us for 8 sequences).
+int cache8_per_sm(int d, int cols) { return d > 128 && cols > 8 ? 1 : d <= 64 && cols == 4 ? 3 : 2; }
+
+template <int D, int R, int S>
 cudaError_t launch_fwd(const CUtensorMap& mk, const CUtensorMap& mv, const Cache8Params& p, int parts, cudaStream_t stream) {
   static PerDeviceOnce attr;
   const cudaError_t e = attr.run([] {
-    return cudaFuncSetAttribute(cache8_fwd_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, R>::kSmem);
+    return cudaFuncSetAttribute(cache8_fwd_kernel<D, R, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, R, S>::kSmem);
   });
   if (e != cudaSuccess) return e;
-  return launch_early(cache8_fwd_kernel<D, R>, dim3(parts), dim3(kThreads), Cfg<D, R>::kSmem, stream, mk, mv, p);
+  return launch_early(cache8_fwd_kernel<D, R, S>, dim3(parts), dim3(kThreads), Cfg<D, R, S>::kSmem, stream, mk, mv, p);
 }
 
 template <int D>
 cudaError_t launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const Cache8Params& p, int parts, cudaStream_t stream) {
   const int cols = cache8_columns(p.c.d, p.R);
   cudaError_t e = cudaErrorInvalidValue;
-  if (cols == 4) e = launch_fwd<D, 4>(mk, mv, p, parts, stream);
-  else if (cols == 8) e = launch_fwd<D, 8>(mk, mv, p, parts, stream);
-  else if (cols == 16) e = launch_fwd<D, 16>(mk, mv, p, parts, stream);
-  else if constexpr (D == 128) e = launch_fwd<D, 32>(mk, mv, p, parts, stream);
+  if (cols == 4 && cache8_per_sm(p.c.d, cols) == 3) {
+    if constexpr (D == 128) e = launch_fwd<D, 4, 3>(mk, mv, p, parts, stream);
+  } else if (cols == 4) {
+    e = launch_fwd<D, 4, 2>(mk, mv, p, parts, stream);
+  } else if (cols == 8) {
+    e = launch_fwd<D, 8, 2>(mk, mv, p, parts, stream);
+  } else if (cols == 16) {
+    e = launch_fwd<D, 16, D == 256 ? 1 : 2>(mk, mv, p, parts, stream);
+  } else if constexpr (D == 128) {
+    e = launch_fwd<D, 32, 2>(mk, mv, p, parts, stream);
+  }
   if (e != cudaSuccess) return e;
   const int rows = parts > 1 && !p.whole ? p.B * p.c.Hkv * p.R : 0;
   const bool single = rows > kJoinRows;
@@ -1077,8 +1090,8 @@ cudaError_t launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const Cache
 
 }  // namespace
 
-// CTAs that run at once, Cfg::kPerSm on each SM
-static int cache8_wave(int d, int cols) { return kCache8Sms * (d > 128 && cols > 8 ? 1 : 2); }
+// CTAs that run at once
+static int cache8_wave(int d, int cols) { return kCache8Sms * cache8_per_sm(d, cols); }
 
 int cache8_columns(int d, int R) { return R <= 4 ? 4 : R <= 8 ? 8 : R <= 16 || d > 128 ? 16 : 32; }
 

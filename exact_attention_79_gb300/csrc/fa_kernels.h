@@ -185,7 +185,7 @@ struct Cache8EvictParams {
   int B, max_blocks, to_blocks, keep, recent;
 };
 constexpr int kCache8MaxRows = 128;   // G * Nq of one call
-constexpr int kCache8Sms = 152;       // the attention's grid: one or two CTAs on each of them
+constexpr int kCache8Sms = 152;       // the attention's grid: one to three CTAs on each of them
 int cache8_columns(int d, int R);     // query rows a CTA takes at once
 bool cache8_whole(int B, int Hkv, int d, int R, int max_blocks);  // one row group per CTA, no partial results
 int cache8_parts(int B, int Hkv, int d, int R, int max_blocks);   // CTAs, parts the work is cut into at most

@@ -74,7 +74,7 @@ def test_fwd_rules(lib):
 
 
 def test_workspace_bytes(lib):
-    # at most 304 parts (152 at d > 128 with more than 8 rows) of two partial results each, as many as units where fewer:
+    # at most 304 parts (152 at d > 128 with more than 8 rows, 456 at d <= 64 with up to 4) of two partial results each, as many as units where fewer:
     # [columns][D] and [columns][3] floats; none where row groups have 8 blocks or fewer each (16 where there are more than 152 of
     # them). With weights the scores of every unit: 64 tokens x rows
     ws = lib.fa_fwd_cache8_workspace_bytes
@@ -83,6 +83,7 @@ def test_workspace_bytes(lib):
     assert ws(1, 4, 2, 1, 64, 8, 0) == 256 and ws(1, 4, 2, 1, 64, 4, 1) == 8 * 64 * 4 * 4
     assert ws(80, 4, 2, 1, 64, 16, 0) == 256 and ws(76, 4, 2, 1, 64, 16, 0) > 256
     assert ws(64, 64, 8, 1, 128, 1000, 0) == 2 * 304 * 8 * (128 + 3) * 4
+    assert ws(64, 32, 8, 1, 64, 1000, 0) == 2 * 456 * 4 * (128 + 3) * 4
     assert ws(1, 40, 1, 1, 128, 10, 1) == 2 * 20 * 32 * (128 + 3) * 4 + 20 * 64 * 32 * 4      # two chunks of 32 columns
     for bad in ((0, 4, 2, 1, 64, 4), (1, 3, 2, 1, 64, 4), (1, 4, 2, 0, 64, 4), (1, 4, 2, 1, 100, 4), (1, 4, 2, 1, 64, 0),
                 (1, 4, 2, 65, 64, 4), (65535, 64, 16, 1, 64, 1 << 24)):

@@ -236,6 +236,8 @@ def test_a_long_tail_of_small_probabilities_counts(fa):
     ([1100, 900] * 20, 2, 1, 1, 128),                               # the same, several tiles a part
     ([1500, 10, 2500, 0, 800] * 2, 4, 2, 2, 256),                   # row groups of one block among long ones
     ([3000, 2000], 40, 2, 2, 128),                                  # two chunks of 32 rows each
+    ([4000, 100, 2500, 3100], 8, 2, 1, 64),                         # four rows: three CTAs per SM
+    ([1700, 2900], 3, 1, 5, 256),                                   # fifteen rows: one
 ])
 def test_many_row_groups_split_between_ctas(fa, lens, Hq, Hkv, Nq, d):
     c, table = make(sum(lens) + d, lens, Hkv, d)
