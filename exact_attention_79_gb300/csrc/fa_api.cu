@@ -670,7 +670,7 @@ struct Cache8Workspace {
   int score_row;                       // floats per token in the scores
 };
 Cache8Workspace cache8_workspace(int B, int Hkv, int R, int d, int max_blocks, bool weights) {
-  const int cols = fa::cache8_columns(d, R), chunks = (R + cols - 1) / cols;
+  const int cols = fa::cache8_columns(R), chunks = (R + cols - 1) / cols;
   const size_t D = d <= 128 ? 128 : 256;
   const size_t rows = fa::cache8_whole(B, Hkv, d, R, max_blocks)
                           ? 0
@@ -689,7 +689,7 @@ fa_status cache8_rows(int B, int Hq, int Hkv, int Nq, int d, int max_blocks) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Nq < 1 || Hq % Hkv != 0 || d < 1 || max_blocks < 1) return FA_ERR_INVALID_ARG;
   if (static_cast<long long>(Hq / Hkv) * Nq > fa::kCache8MaxRows || !fp8_dim(d)) return FA_ERR_UNSUPPORTED;
   // units of work (row groups x blocks) are counted in 32 bits
-  const int R = Hq / Hkv * Nq, cols = fa::cache8_columns(d, R), chunks = (R + cols - 1) / cols;
+  const int R = Hq / Hkv * Nq, cols = fa::cache8_columns(R), chunks = (R + cols - 1) / cols;
   if (static_cast<double>(B) * Hkv * chunks * max_blocks >= 2147483648.0 ||
       static_cast<double>(B) * Hq * Nq >= 2147483648.0)
     return FA_ERR_UNSUPPORTED;
@@ -745,7 +745,7 @@ fa_status fa_fwd_cache8(const void* q, const fa_cache8* cache, const int* block_
   if (st != FA_OK) return st;
   p.G = Hq / p.c.Hkv;
   p.R = p.G * Nq;
-  const int cols = fa::cache8_columns(p.c.d, p.R);
+  const int cols = fa::cache8_columns(p.R);
   p.chunks = (p.R + cols - 1) / cols;
   const Cache8Workspace w = cache8_workspace(B, p.c.Hkv, p.R, p.c.d, max_blocks, add_weights != 0);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < w.total)

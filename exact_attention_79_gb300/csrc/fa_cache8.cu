@@ -216,9 +216,10 @@ struct Place {
   }
 };
 
-// D: 128 or 256, d at most that; R: query rows a CTA takes at once; S: CTAs per SM.
+// D: 128 or 256, d at most that; R: query rows a CTA takes at once, 4, 8 or 16; S: CTAs per SM.
 template <int D, int R, int S>
 struct Cfg {
+  static_assert(R == 4 || R == 8 || R == 16, "rows");
   static constexpr int kChunks = D / 128;                  // 128-byte columns of K and V
   static constexpr int kNS = R < 8 ? 16 : 2 * R;           // S^T columns: two terms of Q (16 at least)
   static constexpr int kE = R < 8 ? R : 8;                 // rows dealt with together
@@ -570,32 +571,15 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         bool grow = !ok;
         if (ok) {
           tc_fence_after();
+          uint32_t hi[16], lo[16];                       // both terms
+          tmem_ld_x16(tbase + lane_off + buf * C::kNS, hi);
+          if (R > 8) tmem_ld_x16(tbase + lane_off + buf * C::kNS + R, lo);
+          tmem_wait_ld();
+          reg_fence_x16(hi);
+          if (R > 8) reg_fence_x16(lo);
 #pragma unroll
-          for (int q0 = 0; q0 < R; q0 += 8) {
-            // columns q0 .. + 7 of both terms
-            uint32_t hi[16], lo[16];
-            if constexpr (R <= 8) {
-              tmem_ld_x16(tbase + lane_off + buf * C::kNS, hi);
-              tmem_wait_ld();
-              reg_fence_x16(hi);
-#pragma unroll
-              for (int e = 0; e < R; ++e) lo[e] = hi[R + e];
-            } else if (q0 % 16 == 0) {
-              tmem_ld_x16(tbase + lane_off + buf * C::kNS + q0, hi);
-              tmem_ld_x16(tbase + lane_off + buf * C::kNS + R + q0, lo);
-              tmem_wait_ld();
-              reg_fence_x16(hi);
-              reg_fence_x16(lo);
-#pragma unroll
-              for (int e = 8; e < 16; ++e)
-                x[(q0 + e) % R] = fmaf(__uint_as_float(lo[e]), 0.0625f, __uint_as_float(hi[e])) * (ks * scale_q((q0 + e) % R));
-            } else {
-              continue;
-            }
-#pragma unroll
-            for (int e = 0; e < C::kE; ++e)
-              x[q0 + e] = fmaf(__uint_as_float(lo[e]), 0.0625f, __uint_as_float(hi[e])) * (ks * scale_q(q0 + e));
-          }
+          for (int q = 0; q < R; ++q)
+            x[q] = fmaf(__uint_as_float(R > 8 ? lo[q] : hi[(R + q) % 16]), 0.0625f, __uint_as_float(hi[q])) * (ks * scale_q(q));
           tc_fence_before();
           if (!there || key >= all) {
             // row row0 + q is query (row0 + q) % Nq of its head, and sees the keys up to its own position
@@ -1064,7 +1048,7 @@ cudaError_t launch_fwd(const CUtensorMap& mk, const CUtensorMap& mv, const Cache
 
 template <int D>
 cudaError_t launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const Cache8Params& p, int parts, cudaStream_t stream) {
-  const int cols = cache8_columns(p.c.d, p.R);
+  const int cols = cache8_columns(p.R);
   cudaError_t e = cudaErrorInvalidValue;
   if (cols == 4 && cache8_per_sm(p.c.d, cols) == 3) {
     if constexpr (D == 128) e = launch_fwd<D, 4, 3>(mk, mv, p, parts, stream);
@@ -1072,10 +1056,8 @@ cudaError_t launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const Cache
     e = launch_fwd<D, 4, 2>(mk, mv, p, parts, stream);
   } else if (cols == 8) {
     e = launch_fwd<D, 8, 2>(mk, mv, p, parts, stream);
-  } else if (cols == 16) {
+  } else {
     e = launch_fwd<D, 16, D == 256 ? 1 : 2>(mk, mv, p, parts, stream);
-  } else if constexpr (D == 128) {
-    e = launch_fwd<D, 32, 2>(mk, mv, p, parts, stream);
   }
   if (e != cudaSuccess) return e;
   const int rows = parts > 1 && !p.whole ? p.B * p.c.Hkv * p.R : 0;
@@ -1093,22 +1075,25 @@ cudaError_t launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const Cache
 // CTAs that run at once
 static int cache8_wave(int d, int cols) { return kCache8Sms * cache8_per_sm(d, cols); }
 
-int cache8_columns(int d, int R) { return R <= 4 ? 4 : R <= 8 ? 8 : R <= 16 || d > 128 ? 16 : 32; }
+// Rows a CTA takes at once: as many as there are up to 16, past that 16 or 8, whichever leaves fewer
+// empty. 16 sequences of up to 8000, d 128: 32 rows by 16 93 us, by 8 101, by 32 118 (its softmax has too few
+// registers); 20 rows 90, 79, 113; 40 rows 130, 124, 190. K and V come from L2 again for the others.
+int cache8_columns(int R) { return R <= 4 ? 4 : (R - 1) / 8 % 2 == 0 ? 8 : 16; }
 
-// Short row groups: one CTA each, as they come, and no second launch. Up to 8 blocks: 8 groups of
-// 4 and 8 take 8.7 and 10.8 us on the GPU and 21.5 for the call, cut and joined 9.7 and 9.8, and 25;
-// 128 groups 10.6 and 12.8 against 15.9 and 16.4; at d 256 384 groups of 8 31 against 35. Up to 16
-// at d 128 with more groups than SMs: 240, 384 and 1024 groups 19, 35 and 72 against 27, 36 and 89
-// (fewer: 8 groups 15.4 against 10.8; d 256: 53 against 49; 32 blocks: 31, 55 and 115 against 35, 49
-// and 113).
+// Short row groups: one CTA each, as they come, and no second launch (4 us less for the caller).
+// GPU time in us, 64 heads on 8, against cut and joined. Up to 8 blocks: 8 groups of 4 and 8
+// 6.7 and 8.7 against 8.7 and 8.8, 128 groups 8.3 and 10.3 against 14.1 and 14.3, 1024 30 and 40
+// against 42 and 55; at d 256 384 groups 14.5 and 23 against 20 and 26.5. Up to 16 at d 128 with more
+// groups than SMs: 240, 384 and 1024 groups 16, 29 and 61 against 21, 29 and 66 (8 groups 12.8
+// against 9.8; d 256 45 against 41; 32 blocks 29, 51 and 105 against 33, 44 and 94).
 bool cache8_whole(int B, int Hkv, int d, int R, int max_blocks) {
-  const int cols = cache8_columns(d, R), chunks = (R + cols - 1) / cols;
+  const int cols = cache8_columns(R), chunks = (R + cols - 1) / cols;
   const bool many = static_cast<long long>(B) * Hkv * chunks > kCache8Sms && d <= 128;
   return max_blocks <= (many ? 2 * kWholeBlocks : kWholeBlocks);
 }
 
 int cache8_parts(int B, int Hkv, int d, int R, int max_blocks) {
-  const int cols = cache8_columns(d, R), chunks = (R + cols - 1) / cols;
+  const int cols = cache8_columns(R), chunks = (R + cols - 1) / cols;
   const long long groups = static_cast<long long>(B) * Hkv * chunks, units = groups * max_blocks;
   if (cache8_whole(B, Hkv, d, R, max_blocks)) return static_cast<int>(groups);
   const int most = cache8_wave(d, cols);

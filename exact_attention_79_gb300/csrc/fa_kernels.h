@@ -186,7 +186,7 @@ struct Cache8EvictParams {
 };
 constexpr int kCache8MaxRows = 128;   // G * Nq of one call
 constexpr int kCache8Sms = 152;       // the attention's grid: one to three CTAs on each of them
-int cache8_columns(int d, int R);     // query rows a CTA takes at once
+int cache8_columns(int R);            // query rows a CTA takes at once
 bool cache8_whole(int B, int Hkv, int d, int R, int max_blocks);  // one row group per CTA, no partial results
 int cache8_parts(int B, int Hkv, int d, int R, int max_blocks);   // CTAs, parts the work is cut into at most
 cudaError_t launch_cache8_append(const Cache8AppendParams& p, cudaStream_t stream);

@@ -374,7 +374,7 @@ fa_status fa_cache8_append(const void* k, long long k_stride_h, long long k_stri
  * cache->weight, and no two sequences of the call may then share a block.
  * workspace: fa_fwd_cache8_workspace_bytes(B, Hq, Hkv, Nq, d, max_blocks,
  * add_weights) bytes (a few MB; with weights also 4 bytes per row, rows rounded
- * up to a multiple of 4 (of 32 past 16), for every token and KV head that the
+ * up to a multiple of 4 (of 8 or 16 past 8), for every token and KV head that the
  * block tables have room for), 256-byte aligned, contents before and after of no meaning; calls
  * that may overlap on the GPU need one each. Returns 0 for sizes that the call
  * refuses (B * Hkv * max_blocks row groups and blocks past 2^31 among them). */

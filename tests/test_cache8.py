@@ -84,7 +84,8 @@ def test_workspace_bytes(lib):
     assert ws(80, 4, 2, 1, 64, 16, 0) == 256 and ws(76, 4, 2, 1, 64, 16, 0) > 256
     assert ws(64, 64, 8, 1, 128, 1000, 0) == 2 * 304 * 8 * (128 + 3) * 4
     assert ws(64, 32, 8, 1, 64, 1000, 0) == 2 * 456 * 4 * (128 + 3) * 4
-    assert ws(1, 40, 1, 1, 128, 10, 1) == 2 * 20 * 32 * (128 + 3) * 4 + 20 * 64 * 32 * 4      # two chunks of 32 columns
+    assert ws(1, 32, 1, 1, 128, 10, 1) == 2 * 20 * 16 * (128 + 3) * 4 + 20 * 64 * 16 * 4      # two chunks of 16 rows
+    assert ws(1, 40, 1, 1, 128, 10, 1) == 2 * 50 * 8 * 128 * 4 + -(-2 * 50 * 8 * 3 * 4 // 256) * 256 + 50 * 64 * 8 * 4     # five of 8
     for bad in ((0, 4, 2, 1, 64, 4), (1, 3, 2, 1, 64, 4), (1, 4, 2, 0, 64, 4), (1, 4, 2, 1, 100, 4), (1, 4, 2, 1, 64, 0),
                 (1, 4, 2, 65, 64, 4), (65535, 64, 16, 1, 64, 1 << 24)):
         assert ws(*bad, 0) == 0, bad

@@ -103,11 +103,11 @@ CASES = [
     # lens, Hq, Hkv, Nq, d, causal
     ([0, 1, 15, 16, 17, 63, 64, 65, 130], 8, 2, 1, 128, True),     # 4 rows per KV head
     ([1000, 333], 8, 1, 1, 128, True),                              # exactly one tile of 8
-    ([300, 5], 9, 1, 1, 64, True),                                  # 9 rows: two tiles
+    ([300, 5], 9, 1, 1, 64, True),                                  # 9 rows in a chunk of 16
     ([257], 4, 2, 8, 128, True),                                    # 16 rows, eight new tokens
     ([3, 200], 4, 4, 5, 64, True),                                  # more new tokens than keys
-    ([190, 70], 17, 1, 1, 128, False),                              # 17 rows: four tiles, most empty
-    ([700], 32, 1, 2, 128, True),                                   # 64 rows: two chunks of 32
+    ([190, 70], 17, 1, 1, 128, False),                              # 17 rows: three chunks of 8, the last nearly empty
+    ([700], 32, 1, 2, 128, True),                                   # 64 rows: four chunks of 16
     ([129], 33, 1, 1, 64, True),
     ([150, 2], 64, 1, 2, 128, True),                                # the most rows: 128
     ([400, 65], 6, 3, 3, 256, True),                                # wide
@@ -235,7 +235,8 @@ def test_a_long_tail_of_small_probabilities_counts(fa):
     ([0, 200, 64, 1, 700, 65, 330] * 10, 4, 2, 1, 64),              # more sequences than a warp has lanes
     ([1100, 900] * 20, 2, 1, 1, 128),                               # the same, several tiles a part
     ([1500, 10, 2500, 0, 800] * 2, 4, 2, 2, 256),                   # row groups of one block among long ones
-    ([3000, 2000], 40, 2, 2, 128),                                  # two chunks of 32 rows each
+    ([3000, 2000], 40, 2, 2, 128),                                  # five chunks of 8 rows each
+    ([3000, 2000], 32, 2, 2, 128),                                  # two of 16
     ([4000, 100, 2500, 3100], 8, 2, 1, 64),                         # four rows: three CTAs per SM
     ([1700, 2900], 3, 1, 5, 256),                                   # fifteen rows: one
 ])
