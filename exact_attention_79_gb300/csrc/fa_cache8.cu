@@ -25,15 +25,17 @@
 // sequences of 8192.)
 //
 // HBM-bound: 2 d bytes per cached token and KV head, against which Q and O
-// are small. Measured: 32 sequences of 2048 to 8192 tokens, 64 heads on 8, d 128: 67 us,
-// 5.2 TB/s; two of 131072: 87 us, 5.8 TB/s; 6 of up to 5000, 16 heads, 4 queries, d 256: 38
-// us, 3.9 TB/s. The steady state takes the memory's whole rate (a tile per CTA in 2700 cycles,
+// are small. Measured: 32 sequences of 2048 to 8192 tokens, 64 heads on 8, d 128: 65 us,
+// 5.4 TB/s; two of 131072: 87 us, 5.8 TB/s; 6 of up to 5000, 16 heads, 4 queries, d 256: 34
+// us, 4.3 TB/s. The steady state takes the memory's whole rate (a tile per CTA in 2700 cycles,
 // 2000 of them softmax); lost are 8 us until the first tiles are there, the spread of the
-// CTAs' ends (4 us), the changes of row groups and the join (3 us). The work is a line of units, one per (sequence, KV head, chunk of
-// rows, block of 64 tokens), cut into equal parts for the CTAs (mostly two per SM, so
-// that one's row changes hide behind the other's stream) whatever the
-// sequences' lengths; a row whose units fall to several CTAs is joined from
-// their partial results by a second kernel.
+// CTAs' ends (4 us), the changes of row groups and the join (3 us).
+//
+// The work is a line of units, one per (sequence, KV head, chunk of rows, block of
+// 64 tokens), cut into equal parts for the CTAs (mostly two per SM, so that one's
+// row changes hide behind the other's stream) whatever the sequences' lengths; a
+// row whose units fall to several CTAs is joined from their partial results by a
+// second kernel. Short row groups stay whole, one CTA each.
 //
 // Warps: 0-3 softmax, 4 producer (block table, scales, TMA), 5 tensor-core issuer, 6
 // Q (reads, splits and lays out the next row group's queries).
