@@ -488,12 +488,12 @@ def fwd_cache8(q, cache, block_table, lengths, causal=True, scale=None, out=None
     if lse is None:
         lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev)
     max_blocks, weigh = block_table.shape[1], int(weight_decay is not None)
-    if workspace is None:
-        n = lib.fa_fwd_cache8_workspace_bytes(B, Hq, Hkv, Nq, d, max_blocks, weigh)
+    n = lib.fa_fwd_cache8_workspace_bytes(B, Hq, Hkv, Nq, d, max_blocks, weigh) if workspace is None else workspace.numel()
+    if workspace is None and n > 256:                   # 256: none is needed
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
     _call_on(dev, "fa_fwd_cache8", q.data_ptr(), ctypes.byref(c), block_table.data_ptr(), max_blocks, lengths.data_ptr(),
-             out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), B, Hq, Nq, int(bool(causal)),
-             float(scale), weigh, float(weight_decay or 0.0))
+             out.data_ptr(), lse.data_ptr(), None if workspace is None else workspace.data_ptr(), n, B, Hq, Nq,
+             int(bool(causal)), float(scale), weigh, float(weight_decay or 0.0))
     return out, lse
 
 

@@ -665,6 +665,7 @@ fa_status cache8_pools(const fa_cache8* c, int B, int max_blocks, const void* bl
 
 // Bytes of fa_fwd_cache8's workspace: partial results, their statistics (off_s)
 // and, with weights, the scores of every token and row (off_x).
+constexpr size_t kNoWorkspace = 256;   // what is said where none is needed (0 says that the call refuses; all others are larger)
 struct Cache8Workspace {
   size_t off_s, off_x, total;
   int score_row;                       // floats per token in the scores
@@ -681,7 +682,7 @@ Cache8Workspace cache8_workspace(int B, int Hkv, int R, int d, int max_blocks, b
   w.off_x = w.off_s + align256(rows * 3 * 4);
   w.score_row = R < cols ? (R + 3) / 4 * 4 : cols;
   w.total = w.off_x + (weights ? units * FA_CACHE8_BLOCK * w.score_row * 4 : 0);
-  if (w.total == 0) w.total = 256;     // (0 says that the call refuses)
+  if (w.total == 0) w.total = kNoWorkspace;
   return w;
 }
 
@@ -748,7 +749,8 @@ fa_status fa_fwd_cache8(const void* q, const fa_cache8* cache, const int* block_
   const int cols = fa::cache8_columns(p.R);
   p.chunks = (p.R + cols - 1) / cols;
   const Cache8Workspace w = cache8_workspace(B, p.c.Hkv, p.R, p.c.d, max_blocks, add_weights != 0);
-  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < w.total)
+  if (w.total > kNoWorkspace &&
+      (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < w.total))
     return FA_ERR_WORKSPACE;
   unsigned* status = nullptr;
   st = device_state(stream, &status);

@@ -66,11 +66,12 @@ def test_fwd_rules(lib):
                 dict(add=1, c=cache(weight=0)), dict(q=P((1 << 20) + 8)), dict(o=FAKE)):
         assert fwd(lib, **bad) == 1, bad
     assert fwd(lib, Hq=4, Nq=65) == 2                      # 2 heads per KV head x 65 rows
-    need = lib.fa_fwd_cache8_workspace_bytes(1, 4, 2, 1, 64, 4, 0)
-    more = lib.fa_fwd_cache8_workspace_bytes(1, 4, 2, 1, 64, 4, 1)
-    assert 0 < need < more and fwd(lib, add=1, nws=more - 1) == 6
+    need = lib.fa_fwd_cache8_workspace_bytes(1, 4, 2, 1, 64, 9, 0)
+    more = lib.fa_fwd_cache8_workspace_bytes(1, 4, 2, 1, 64, 9, 1)
+    assert 256 < need < more and fwd(lib, mb=9, add=1, nws=more - 1) == 6
+    assert fwd(lib, mb=4, add=1, ws=NULL) == 6 and fwd(lib, mb=4, ws=NULL, nws=0) not in (1, 6)      # none is needed
     assert fwd(lib, B=65535, Hq=64, c=cache(Hkv=16), mb=1 << 24) == 2      # more than 2^31 units of work
-    assert fwd(lib, nws=need - 1) == 6 and fwd(lib, ws=NULL) == 6 and fwd(lib, ws=P((1 << 20) + 128)) == 6
+    assert fwd(lib, mb=9, nws=need - 1) == 6 and fwd(lib, mb=9, ws=NULL) == 6 and fwd(lib, mb=9, ws=P((1 << 20) + 128)) == 6
 
 
 def test_workspace_bytes(lib):
