@@ -370,7 +370,8 @@ fa_status fa_cache8_append(const void* k, long long k_stride_h, long long k_stri
  * call on that sequence and head.
  * add_weights: also weight_j = weight_decay * weight_j + sum of the
  * probabilities of key j over the Hq / Hkv heads and Nq queries, for every
- * key j < lengths[b] (weight_decay finite, >= 0; 0 overwrites). It needs
+ * key j < lengths[b] (weight_decay finite, >= 0; 0 overwrites; probabilities
+ * below 2^-126 count as 0). It needs
  * cache->weight, and no two sequences of the call may then share a block.
  * workspace: fa_fwd_cache8_workspace_bytes(B, Hq, Hkv, Nq, d, max_blocks,
  * add_weights) bytes (a few MB; with weights also 4 bytes per row, rows rounded
