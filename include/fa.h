@@ -358,28 +358,29 @@ fa_status fa_cache8_append(const void* k, long long k_stride_h, long long k_stri
                            void* stream);
 
 /* Attention over the cache for the last Nq positions of each sequence: q, o
- * bf16 [B, Hq, Nq, d], apart from one another, lse fp32 [B, Hq, Nq], lengths int32 [B] (device): tokens
- * held, the Nq new ones included (taken within 0 .. 64 max_blocks). As
+ * bf16 [B, Hq, Nq, d], apart from one another, lse fp32 [B, Hq, Nq], lengths
+ * int32 [B] (device): tokens held, the Nq new ones included (taken within
+ * 0 .. 64 max_blocks). As
  * fa_fwd_kv on the values of the cache: key j is visible to query i iff
  * j < lengths[b] and, when causal, j <= i + lengths[b] - Nq; a row that sees
  * none gets O = 0, lse = -inf. Hq % Hkv == 0 and (Hq / Hkv) * Nq <= 128
  * (FA_ERR_UNSUPPORTED above). The products take the codes as they are; Q
  * to the bit down to 2^-17 of a row's largest value (smaller ones are off by at
  * most 2^-21 of it); each P (times its block's V scale) within 2^-12 of
- * itself plus 2^-25 of the row's largest; sums are fp32. A NaN among a sequence's V values reaches every query of the
- * call on that sequence and head.
+ * itself plus 2^-25 of the row's largest; sums are fp32. A NaN among a
+ * sequence's V values reaches every query of the call on that sequence and head.
  * add_weights: also weight_j = weight_decay * weight_j + sum of the
  * probabilities of key j over the Hq / Hkv heads and Nq queries, for every
  * key j < lengths[b] (weight_decay finite, >= 0; 0 overwrites; probabilities
- * below 2^-126 count as 0). It needs
- * cache->weight, and no two sequences of the call may then share a block.
+ * below 2^-126 count as 0). It needs cache->weight, and no two sequences of the
+ * call may then share a block.
  * workspace: fa_fwd_cache8_workspace_bytes(B, Hq, Hkv, Nq, d, max_blocks,
  * add_weights) bytes (a few MB; with weights also 4 bytes per row, rows rounded
- * up to a multiple of 4 (of 8 or 16 past 8), for every token and KV head that the
- * block tables have room for), 256-byte aligned, contents before and after of no meaning; calls
- * that may overlap on the GPU need one each. 256 says that short sequences need
- * none: the call then looks at no workspace, NULL will do. 0 for sizes that it
- * refuses (B * Hkv * max_blocks row groups and blocks past 2^31 among them). */
+ * up to a multiple of 4 (of 8 or 16 past 8), for every token and KV head that
+ * the block tables have room for), 256-byte aligned, contents before and after
+ * of no meaning; calls that may overlap on the GPU need one each. 256 says that
+ * short sequences need none: the call then looks at no workspace, NULL will do.
+ * 0 for sizes that it refuses (B * Hkv * max_blocks row groups and blocks past 2^31 among them). */
 size_t fa_fwd_cache8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int max_blocks, int add_weights);
 fa_status fa_fwd_cache8(const void* q, const fa_cache8* cache, const int* block_table, int max_blocks,
                         const int* lengths, void* o, float* lse, void* workspace, size_t workspace_bytes, int B,
