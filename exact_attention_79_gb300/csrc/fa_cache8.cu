@@ -273,6 +273,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, S>::kPerSm)
 cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Cache8Params p) {
   using C = Cfg<D, R, S>;
   extern __shared__ uint8_t smem_raw[];
+  // This kernel may have been set up while the one before it still ran: nothing
+  // in memory is read or written ahead of that one's end. From then on the second
+  // kernel may be set up, which so may read what the caller's kernels wrote.
+  wait_before();
+  let_next();
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const gbase = smem_raw + (base - raw);
@@ -307,13 +312,8 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   const uint32_t bar_stall = bars + 304;                               // nothing arrives (timeout test)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // This kernel may have been set up while the one before it still ran: nothing
-  // in memory is read or written ahead of that one's end. From then on the second
-  // kernel may be set up, which so may read what the caller's kernels wrote.
   // (All warps find the part by the same code: a copy of it in each role costs
   // more than it saves, since code, too, comes from memory the first time.)
-  wait_before();
-  let_next();
   int u0, u1;                                            // this part's units
   Place at;
   if (!at.start(p, blockIdx.x, gridDim.x, lane, u0, u1)) return;
@@ -821,6 +821,9 @@ struct RowParts {
 };
 
 // kJoin: warps that join a row together, kFinishWarps or one each.
+// Every CTA waits for the first kernel before it ends, also where nothing is left to join: what
+// follows in the stream, or in a graph, is ordered behind this kernel alone, and would run beside the
+// first one if this one could end before it.
 template <int D, int kJoin>
 __global__ void __launch_bounds__(kFinishWarps * 32, 8) cache8_finish_kernel(const Cache8Params p, int cols, int ctas, int shares) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -833,15 +836,18 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 8) cache8_finish_kernel(con
     const int per_seq = p.c.Hkv * p.R;
     const int row = kJoin == 1 ? (static_cast<int>(blockIdx.x) - shares) * kFinishWarps + warp : static_cast<int>(blockIdx.x) - shares;
     const int b = row / per_seq, hr = row - b * per_seq;
-    if (b >= p.B) return;
+    if (b >= p.B) {
+      wait_before();
+      return;
+    }
     const int h = hr / p.R, r = hr - h * p.R;
     int before = 0;
     for (int i = lane; i < b; i += 32) before += line_blocks(p, i);
     before = __reduce_add_sync(0xffffffffu, before) * per_block;
     const int nblk = line_blocks(p, b);
     const RowParts rp(p, line, before, b, nblk, h, r, cols);
-    if (rp.c0 == rp.c1) return;                          // written whole
     wait_before();
+    if (rp.c0 == rp.c1) return;                          // written whole
     // several parts a warp at a time, all their loads together
     constexpr int kPer = D / 128;                        // float4 per lane
     constexpr int kAtOnce = kJoin == 1 ? 3 : 8;
@@ -944,7 +950,10 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 8) cache8_finish_kernel(con
   const int share = static_cast<int>(blockIdx.x);
   const int w0 = static_cast<int>(static_cast<long long>(all) * share / shares);
   const int w1 = static_cast<int>(static_cast<long long>(all) * (share + 1) / shares);
-  if (w0 >= w1) return;
+  if (w0 >= w1) {
+    wait_before();
+    return;
+  }
   Place at;
   at.turn = 0;
   at.find(p, w0 * p.chunks, lane);                       // (sequences have `chunks` times as many units)

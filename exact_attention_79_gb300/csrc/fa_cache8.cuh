@@ -41,7 +41,8 @@ __device__ __forceinline__ int cache_length(const int* lengths, int b, int max_b
 // Launch that may be set up while the kernel before it in the stream still runs
 // (programmatic dependent launch): a kernel launched so calls wait_before(), which
 // returns when that one has ended and its writes are seen, before it reads or
-// writes anything that is not its own; one that calls let_next() allows the next
+// writes anything that is not its own, and in every CTA before it ends: the kernels behind
+// are ordered behind this one only. One that calls let_next() allows the next
 // kernel's set-up from there on.
 __device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
