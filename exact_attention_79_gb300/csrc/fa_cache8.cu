@@ -361,7 +361,8 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         int page = mine < s.blk1 && mine < held ? table[mine] : -1;
         if (page >= p.c.num_blocks) page = -1;
         const long long ph = page >= 0 ? static_cast<long long>(page) * p.c.Hkv + s.h : -1;
-        const float ks = page >= 0 ? __ldg(p.c.k_scale + ph) : 0.f, vs = page >= 0 ? __ldg(p.c.v_scale + ph) : 0.f;
+        // (not by the read-only path: the append before may still have been writing them when this kernel was set up)
+        const float ks = page >= 0 ? p.c.k_scale[ph] : 0.f, vs = page >= 0 ? p.c.v_scale[ph] : 0.f;
         const int z = static_cast<int>(ph);
         for (int i = 0; i < 32 && blk + i < s.blk1 && ok; i += 2, ++tile) {
           const int za = __shfl_sync(0xffffffffu, z, i), zb = __shfl_sync(0xffffffffu, z, i + 1);

@@ -62,6 +62,12 @@ def test_no_cta_ends_without_waiting(file, kernel):
     assert unwaited_exits(body(read(file), kernel)) == []
 
 
+@pytest.mark.parametrize("file", sorted({f for f, _ in EARLY} | {"fa_cache8.cuh"}))
+def test_no_loads_by_the_read_only_path(file):
+    """ld.global.nc wants memory that nothing writes while the kernel lives, and an early kernel lives from its set-up on."""
+    assert not re.search(r"__ldg|\.nc\b|__restrict__", read(file))
+
+
 def test_the_reading_of_exits():
     assert unwaited_exits("wait_before(); if (a) return; b();") == []
     assert unwaited_exits("if (a) return; wait_before();") == [0]
