@@ -792,7 +792,8 @@ fa_status fa_cache8_evict(const fa_cache8* cache, const int* block_table, int ma
   fa::Cache8EvictParams p{};
   fa_status st = cache8_pools(cache, B, max_blocks, block_table, true, &p.c);
   if (st != FA_OK) return st;
-  if (static_cast<long long>(B) * to_blocks >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
+  // one CTA per destination block that is used
+  if (static_cast<long long>(B) * ((keep - 1) / FA_CACHE8_BLOCK + 1) >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
   unsigned* status = nullptr;
   st = device_state(stream, &status);
   if (st != FA_OK) return st;

@@ -40,6 +40,10 @@ __device__ __forceinline__ uint32_t pack_halves(__half2 x) {
   return r;
 }
 
+// Blocks that `keep` tokens take up. The gather runs over these alone, however wide to_table is: their
+// slots stay within an int, and none but theirs can be written.
+__host__ __device__ __forceinline__ int dest_blocks(int keep) { return (keep - 1) / kCacheBlock + 1; }
+
 // Floats as integers of the same order; -0 as 0, NaN above everything.
 __device__ __forceinline__ uint32_t order_key(float x) {
   if (x != x) return 0xFFFFFFFFu;
@@ -89,7 +93,8 @@ __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Cache8
   const int me = rank * kSelThreads + tid, all = ctas * kSelThreads;
   if (h == 0 && me == 0) p.new_lengths[b] = min(n, p.keep);
   if (n <= p.keep) {                                     // (all CTAs of the cluster)
-    for (int i = me; i < p.keep; i += all) kept[i] = i < n ? i : -1;
+    // (unsigned: the step past the largest `keep` is no int)
+    for (unsigned i = me; i < static_cast<unsigned>(p.keep); i += all) kept[i] = i < static_cast<unsigned>(n) ? static_cast<int>(i) : -1;
     return;
   }
   const int nc = n - p.recent;                           // candidates
@@ -245,7 +250,7 @@ __global__ void __launch_bounds__(kGatherThreads, D == 128 ? 18 : 8) cache8_gath
   __shared__ float warp_max[kGatherThreads / 32];
   __shared__ long long src[kCacheBlock];          // (block * Hkv + h) * 64 + slot of a kept token, -1: no such block
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x / p.to_blocks, blk = blockIdx.x - b * p.to_blocks;
+  const int blocks = dest_blocks(p.keep), b = blockIdx.x / blocks, blk = blockIdx.x - b * blocks;
   const int h = blockIdx.y, which = blockIdx.z;
   let_next();
   wait_before();
@@ -378,7 +383,7 @@ cudaError_t launch_cache8_evict(const Cache8EvictParams& p, cudaStream_t stream)
   e = cudaLaunchKernelEx(&cfg, cache8_select_kernel, p, room);
   if (e != cudaSuccess) return e;
   return launch_early(p.c.d > 128 ? cache8_gather_kernel<256> : cache8_gather_kernel<128>,
-                      dim3(p.B * p.to_blocks, p.c.Hkv, 2), dim3(kGatherThreads), 0, stream, p);
+                      dim3(p.B * dest_blocks(p.keep), p.c.Hkv, 2), dim3(kGatherThreads), 0, stream, p);
 }
 
 }  // namespace fa

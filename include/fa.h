@@ -389,8 +389,9 @@ fa_status fa_fwd_cache8(const void* q, const fa_cache8* cache, const int* block_
 /* Evict: of each sequence's tokens, per KV head, keep at most `keep`: the last
  * `recent` (0 <= recent <= keep) and of the others those with the largest
  * weight (a NaN counts as the largest; ties go to the earlier token), in their
- * order. Their codes go to the blocks of to_table [B, to_blocks] (device
- * int32, 64 * to_blocks >= keep), with scales from their own values as
+ * order. Their codes go to the first ceil(keep / 64) blocks of to_table
+ * [B, to_blocks] (device int32, 64 * to_blocks >= keep; entries behind are not
+ * looked at; FA_ERR_UNSUPPORTED for 2^31 such blocks or more), with scales from their own values as
  * fa_cache8_append takes them, and their weights with them; slots behind them
  * are left as they were. kept int32 [B, Hkv, keep]: the tokens' positions
  * before, -1 past the sequence's new length; new_lengths int32 [B]:
