@@ -47,6 +47,7 @@ namespace {
 constexpr int kThreads = 224;
 constexpr float kTrail = 3.f;             // log2 of how far a reference may trail
 constexpr float kShift = 5.f;             // y = 2^(x - reference + kShift) <= 2^8
+constexpr float kNoKey = -1.f;            // factor of O for a row that sees no key
 constexpr int kWholeBlocks = 8;
 constexpr int kTurn = 4;                  // blocks' time that a change of row groups costs
 constexpr int kInfo = 8;                  // tiles whose scales wait in shared memory
@@ -74,6 +75,9 @@ __device__ __forceinline__ void reg_fence_x16(uint32_t (&r)[16]) {
 __device__ __forceinline__ void store_byte(uint32_t addr, uint32_t x) {
   asm volatile("st.shared.b8 [%0], %1;" :: "r"(addr), "r"(x) : "memory");
 }
+// O of a row that sees no key is 0 whatever V holds: its P is 0, but 0 x NaN is not. (By a mark of its own: the
+// factor of V scales of 0 is 0 as well.)
+__device__ __forceinline__ float times_factor(float o, float factor) { return factor == kNoKey ? 0.f : o * factor; }
 // Bounded wait whose limit starts at its own first look at the timer.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned long long limit_ns) {
   uint32_t polls = 0;
@@ -731,7 +735,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         const float sum = warp_l[row] + warp_l[R + row] + warp_l[2 * R + row] + warp_l[3 * R + row];
         const float ml = ref_l[row], mo = ref_o[row] - kShift;
         if (whole) {
-          factor[row] = sum == 0.f ? 0.f : ex2_approx(mo - ml) / sum;
+          factor[row] = sum == 0.f ? kNoKey : ex2_approx(mo - ml) / sum;
           if (row < rows) p.lse[qrow + row] = sum == 0.f ? -INFINITY : (ml + log2f(sum)) * kLn2;
         } else {
           float* const s3 = p.part_s + (slot0 + row) * 3;
@@ -771,8 +775,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             if (col < p.c.d) {
 #pragma unroll
               for (int e = 0; e < C::kE; ++e)
-                // (a row that sees no key: 0, whatever V holds)
-                if (q0 + e < rows) dst[e * p.c.d] = __float2bfloat16_rn(factor[q0 + e] == 0.f ? 0.f : v[e] * factor[q0 + e]);
+                if (q0 + e < rows) dst[e * p.c.d] = __float2bfloat16_rn(times_factor(v[e], factor[q0 + e]));
             }
           } else {
             float* const dst = p.part_o + (slot0 + q0) * D + col;
@@ -936,12 +939,13 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 8) cache8_finish_kernel(con
       }
     }
     const size_t at = (static_cast<size_t>(b) * p.Hq + static_cast<size_t>(h) * p.G) * p.Nq + r;
-    const float f = sum == 0.f ? 0.f : ex2_approx(mo - ml) / sum;
+    const float f = sum == 0.f ? kNoKey : ex2_approx(mo - ml) / sum;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (128 * i + 4 * lane < p.c.d)
         *reinterpret_cast<uint2*>(p.o + at * p.c.d + 128 * i + 4 * lane) =
-            make_uint2(pack_bf16x2(a[i].x * f, a[i].y * f), pack_bf16x2(a[i].z * f, a[i].w * f));
+            make_uint2(pack_bf16x2(times_factor(a[i].x, f), times_factor(a[i].y, f)),
+                       pack_bf16x2(times_factor(a[i].z, f), times_factor(a[i].w, f)));
     if (lane == 0) p.lse[at] = sum == 0.f ? -INFINITY : (ml + log2f(sum)) * kLn2;
     return;
   }
