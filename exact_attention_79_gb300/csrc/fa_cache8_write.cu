@@ -39,6 +39,17 @@ __device__ __forceinline__ uint2 encode8(const uint4& x, float inv) {
   return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
 }
 
+// The same where the scale is no power of two, a held one of the caller's: x / s rounded once to fp32, then to
+// the code. (1 / s would round twice, and is infinite for the smallest s.) A call, so that its divisions stay out of the way.
+__device__ __noinline__ uint2 divide8(uint4 x, float s) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t q[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    q[e] = pack_e4m3x2(__fdiv_rn(__uint_as_float(w[e] << 16), s), __fdiv_rn(__uint_as_float(w[e] & 0xFFFF0000u), s));
+  return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+}
+
 // One CTA per (touched block, KV head, K or V). D: 128 or 256, d at most that.
 template <int D>
 __global__ void __launch_bounds__(kThreads, D == 128 ? 8 : 4) cache8_append_kernel(const Cache8AppendParams p) {
@@ -142,11 +153,19 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 8 : 4) cache8_append_kern
     }
   }
   if (tid == 0) *scale = now;
-  const float inv = __fdiv_rn(1.f, now);                      // exact: `now` is a power of two here or the block's own
+  if ((__float_as_uint(now) & 0x7FFFFFu) == 0) {                              // a normal power of two, as all made here are: 1 / now is exact
+    const float inv = __fdiv_rn(1.f, now);
 #pragma unroll
-  for (int i = 0; i < kMaxChunks; ++i) {
-    const int c = tid + i * kThreads;
-    if (c < chunks) *reinterpret_cast<uint2*>(codes + (lo * cpr + c) * 8) = encode8(val[i], inv);
+    for (int i = 0; i < kMaxChunks; ++i) {
+      const int c = tid + i * kThreads;
+      if (c < chunks) *reinterpret_cast<uint2*>(codes + (lo * cpr + c) * 8) = encode8(val[i], inv);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kMaxChunks; ++i) {
+      const int c = tid + i * kThreads;
+      if (c < chunks) *reinterpret_cast<uint2*>(codes + (lo * cpr + c) * 8) = divide8(val[i], now);
+    }
   }
   if (which == 0 && p.c.weight != nullptr && lo + tid < hi) p.c.weight[ph * kCacheBlock + lo + tid] = 0.f;
 }

@@ -4,7 +4,8 @@ import pytest
 import torch
 
 from oracle import cache8 as oc
-from test_cache8_gpu import DEV, bf16, ints, make, to_gpu
+from oracle.fp8 import e4m3_decode
+from test_cache8_gpu import DEV, bf16, f64, ints, make, to_gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -71,3 +72,39 @@ def test_a_nan_under_a_scale_of_zero_is_a_nan(fa, width):
     o, lse = fa.fwd_cache8(q, to_gpu(fa, c), ints(table), ints([100]))
     assert bool(torch.isnan(o[..., 3]).all()) and bool((o[..., :3] == 0).all()) and bool((o[..., 4:] == 0).all())
     assert bool(torch.isfinite(lse).all())
+
+
+@pytest.mark.parametrize("new,past,Hkv,d", [([70, 1, 5, 64], [30, 63, 0, 10], 2, 64), ([40, 3], [0, 100], 3, 256)])
+def test_append_under_scales_of_any_value(fa, new, past, Hkv, d):
+    c, table = make(sum(new) + d, [a + b for a, b in zip(new, past)], Hkv, d, spread=2, po2=False)
+    rng = np.random.default_rng(d)
+    k, v = (torch.from_numpy((rng.standard_normal((Hkv, sum(new), d)) * np.exp2(rng.integers(-6, 6, (Hkv, sum(new), 1)))).astype(np.float32))
+            .to(torch.bfloat16) for _ in range(2))
+    cu = np.concatenate([[0], np.cumsum(new)])
+    g = to_gpu(fa, c)
+    fa.cache8_append(g, k.to(DEV), v.to(DEV), ints(cu), ints(table), ints(past))
+    fa.check_device_status()
+    same_cache(g, oc.append(c, f64(k), f64(v), cu, past, table))
+
+
+def test_append_divides_by_a_held_scale(fa):
+    """Quotients next to the border of two codes, where x times the rounded 1 / s falls on the other side; and scales so
+    small that 1 / s is infinite."""
+    pairs = [("0x1.733332p+0", 145), ("0x1.77bdf0p+0", 182), ("0x1.5b6db6p+0", 228), ("0x1.d642cap+0", 169),
+             ("0x1.dffffep+0", 255), ("0x1.696968p+0", 192), ("0x1.ba6f4ep+0", 159), ("0x1.0p-140", 0), ("0x1.6p-130", 0)]
+    B, d = len(pairs), 16
+    c, table = make(65, [2] * B, 1, d, spare=0)
+    k = torch.zeros(1, B, d, dtype=torch.bfloat16)
+    for b, (s, x) in enumerate(pairs):
+        c["k_scale"][table[b, 0], 0] = c["v_scale"][table[b, 0], 0] = float.fromhex(s)
+        c["k"][table[b, 0], 0, :2], c["v"][table[b, 0], 0, :2] = 0x38, 0xB8
+        k[0, b, :9] = x
+    g = to_gpu(fa, c)
+    fa.cache8_append(g, k.to(DEV), -k.to(DEV), ints(np.arange(B + 1)), ints(table), ints([1] * B))
+    fa.check_device_status()
+    want = oc.append(c, f64(k), -f64(k), np.arange(B + 1), [1] * B, table)
+    for n in ("k_scale", "v_scale", "weight"):
+        assert np.array_equal(getattr(g, n).cpu().numpy(), want[n], equal_nan=True), n
+    for n in ("k", "v"):                                # (the sign of a zero says nothing)
+        got, ref = (e4m3_decode(x[n] if isinstance(x, dict) else getattr(x, n).cpu().numpy()) for x in (g, want))
+        assert np.array_equal(got, ref, equal_nan=True), n
