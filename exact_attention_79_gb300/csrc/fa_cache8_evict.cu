@@ -313,7 +313,8 @@ __global__ void __launch_bounds__(kGatherThreads, D == 128 ? 18 : 8) cache8_gath
         m = max(m, code == 0x7Fu ? 0u : code);
       }
     }
-    amax = fmaxf(amax, e4m3x2_to_float2(m).x * sc[k]);
+    // (rounded up: above 448 times a power of two if and only if the exact product is)
+    amax = fmaxf(amax, __fmul_ru(e4m3x2_to_float2(m).x, sc[k]));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -342,10 +343,12 @@ __global__ void __launch_bounds__(kGatherThreads, D == 128 ? 18 : 8) cache8_gath
         r[e] = pack_halves(__hmul2(as_half2(e4m3x2_to_f16x2(w[e])), f)) |
                pack_halves(__hmul2(as_half2(e4m3x2_to_f16x2(w[e] >> 16)), f)) << 16;
     } else {
+      // the ratio is exact, or so small that every code becomes 0, or past all floats where every code is 0
+      const float f = fminf(ratio, 0x1p127f);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 a = e4m3x2_to_float2(w[e]), z = e4m3x2_to_float2(w[e] >> 16);
-        r[e] = pack_e4m3x2(a.x * sc[k] * inv, a.y * sc[k] * inv) | pack_e4m3x2(z.x * sc[k] * inv, z.y * sc[k] * inv) << 16;
+        r[e] = pack_e4m3x2(a.x * f, a.y * f) | pack_e4m3x2(z.x * f, z.y * f) << 16;
       }
     }
     *reinterpret_cast<uint4*>(dst + c * 16) = make_uint4(r[0], r[1], r[2], r[3]);

@@ -108,3 +108,67 @@ def test_append_divides_by_a_held_scale(fa):
     for n in ("k", "v"):                                # (the sign of a zero says nothing)
         got, ref = (e4m3_decode(x[n] if isinstance(x, dict) else getattr(x, n).cpu().numpy()) for x in (g, want))
         assert np.array_equal(got, ref, equal_nan=True), n
+
+
+@pytest.mark.parametrize("lens,keep,recent,Hkv,d", [([517, 192], 130, 32, 3, 64), ([400], 200, 0, 1, 256)])
+def test_evict_from_blocks_with_scales_of_any_value(fa, lens, keep, recent, Hkv, d):
+    room = -(-keep // 64)
+    c, table = make(sum(lens) + keep, lens, Hkv, d, spare=room, po2=False)
+    to, table = table[:, -room:].copy(), table[:, :-room].copy()
+    g = to_gpu(fa, c)
+    new, kept = fa.cache8_evict(g, ints(table), ints(lens), keep, recent, ints(to))
+    fa.check_device_status()
+    want, wn, wk = oc.evict(c, table, lens, keep, recent, to)
+    assert np.array_equal(new.cpu().numpy(), wn) and np.array_equal(kept.cpu().numpy(), wk)
+    same_cache(g, want)
+
+
+def border_scales():
+    """(code, scale) whose exact product is above 448 and rounds to 448."""
+    for code in range(1, 0x7F):
+        x = float(e4m3_decode(np.uint8(code)))
+        s = np.float32(448.0 / x)
+        if x * float(s) > 448.0 and np.float32(x * float(s)) == np.float32(448.0):
+            yield code, s
+
+
+def test_evict_takes_the_largest_value_as_it_is(fa):
+    """The scale is the smallest power of two with max|x| <= 448 s for x = code * scale, not for x rounded; and values of
+    scales below 2^-126 are not rounded to that grid first."""
+    cases = list(border_scales())
+    assert len(cases) >= 8
+    # the largest value has a scale of 2^-126 of its own; every code under a subnormal scale beside it
+    cases += [(0x7E, np.float32(float.fromhex("0x1.8p-127"))), (0x7E, np.float32(float.fromhex("0x1.2345678p-128")))]
+    B, d = len(cases), 128
+    lens = [3] * B
+    c, table = make(66, lens, 1, d, spare=1)
+    to, table = table[:, -1:].copy(), table[:, :-1].copy()
+    for b, (code, s) in enumerate(cases):
+        c["k_scale"][table[b, 0], 0] = c["v_scale"][table[b, 0], 0] = s
+        few = np.arange(min(code, d - 1) + 1, dtype=np.uint8)
+        for x in ("k", "v"):
+            c[x][table[b, 0], 0, :3] = 0
+            c[x][table[b, 0], 0, 1, : len(few)] = few[::-1]
+    g = to_gpu(fa, c)
+    new, kept = fa.cache8_evict(g, ints(table), ints(lens), 2, 0, ints(to))
+    fa.check_device_status()
+    c2 = {n: x.copy() for n, x in c.items()}
+    want, wn, wk = oc.evict(c2, table, lens, 2, 0, to)
+    assert np.array_equal(kept.cpu().numpy(), wk)
+    same_cache(g, want)
+
+
+def test_evict_of_zeros_under_a_huge_scale(fa):
+    """The ratio of the scales is past all floats, and the codes it multiplies are 0."""
+    lens, d = [66], 32
+    c, table = make(69, lens, 1, d, spare=1)
+    to, table = table[:, -1:].copy(), table[:, :-1].copy()
+    for x in ("k", "v"):
+        c[x][table[0, 0]] = 0
+        c[x + "_scale"][table[0]] = np.array([[1.5 * 2.0 ** 126], [1.25 * 2.0 ** -126]], np.float32)
+    c["weight"][table[0, 0]] = 1.0
+    g = to_gpu(fa, c)
+    new, kept = fa.cache8_evict(g, ints(table), ints(lens), 40, 2, ints(to))
+    want, wn, wk = oc.evict(c, table, lens, 40, 2, to)
+    assert np.array_equal(kept.cpu().numpy(), wk)
+    same_cache(g, want)
