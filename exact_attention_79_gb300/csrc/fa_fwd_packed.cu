@@ -644,8 +644,8 @@ fwd_packed_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
       const int at = it[0] + first;
       __syncwarp();
       if (lane == 0) release(n);
-      if (ok && lane < valid)
-        p.lse[static_cast<long long>(head) * p.T + at + lane] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      if (ok && lane < valid)                              // (a NaN among the logits stays one)
+        p.lse[static_cast<long long>(head) * p.T + at + lane] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       ++n;
       next();                                              // while the last P V runs
       if (ok) ok = wait(bar_o_final(g), no, abort_flag, p.timeout_ns);

@@ -6,6 +6,7 @@ import torch
 from oracle import cache8 as oc
 from oracle.fp8 import e4m3_decode
 from test_cache8_gpu import DEV, bf16, f64, ints, make, to_gpu
+from test_packed_gpu import inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -172,3 +173,20 @@ def test_evict_of_zeros_under_a_huge_scale(fa):
     want, wn, wk = oc.evict(c, table, lens, 40, 2, to)
     assert np.array_equal(kept.cpu().numpy(), wk)
     same_cache(g, want)
+
+
+def test_packed_rows_of_nan(fa):
+    """A NaN in a row of Q, or in a key that a row sees, is that row's O and LSE, and no other row's."""
+    q, k, v, cu = inputs(7, [200, 150], 4, 2, 64)
+    cu_d = ints(cu)
+    g = [x.to(DEV) for x in (q, k, v)]
+    want, wl = fa.fwd_packed(*g, cu_d)
+    g[0][1, 40, 3] = float("nan")
+    g[1][1, 320, 5] = float("nan")                      # the second sequence's row 120, of heads 2 and 3
+    got, gl = fa.fwd_packed(*g, cu_d)
+    fa.check_device_status()
+    hit = torch.zeros(4, 350, dtype=torch.bool, device=DEV)
+    hit[1, 40] = True
+    hit[2:, 320:] = True
+    assert torch.equal(got[~hit], want[~hit]) and torch.equal(gl[~hit], wl[~hit])
+    assert bool(torch.isnan(got[hit]).all()) and bool(torch.isnan(gl[hit]).all())
