@@ -612,6 +612,8 @@ fwd_packed_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
             const float p0 = ex2_approx(x0);
             const float p1 = ex2_approx(x1);
             add2_acc(sum0, sum1, p0, p1);
+            // P in bf16, as in fa_fwd.cu: the product wants it in V's type, and each term is within 2^-8 of
+            // itself, as O is. Two bf16 terms would double the P V products, half of all. l sums P unrounded.
             pr[x] = pack_bf16x2(p0, p1);
           }
           tmem_st_32x32b_x32(t_s + h2 * 32, pr);

@@ -105,7 +105,13 @@ fa_status fa_fwd_kv(const void* q, const void* k, const void* v, void* o, float*
  * [T, H, d] projection needs no copy. cu_seqlens: device int32 [S + 1], not
  * decreasing, within 0 .. T; sequence s has rows cu_seqlens[s] ..
  * cu_seqlens[s + 1] - 1 and may be empty. lse [Hq, T]. Row i of a sequence sees
- * its rows j (j <= i when causal) and nothing of the others, whatever they hold.
+ * its rows j (j <= i when causal) and nothing of other sequences, whatever they
+ * hold. Of its own sequence's rows behind it, when causal, it takes no part of K
+ * either; an infinity or NaN in V of such a row j makes its column of O NaN
+ * where i and j are of the same 128 rows, counted from the sequence's start (P
+ * is 0 there, and 0 x inf is NaN), and reaches no LSE. As in fa_fwd, P is rounded
+ * to bf16 for its product with V, each term within 2^-8 of itself; sums and LSE are
+ * fp32, of P unrounded.
  * Rows of no sequence (before the first, behind the last) are left as they
  * were, in o and in lse. Values outside the rules for cu_seqlens are taken
  * within 0 .. T, and some rows may then not be written. d <= 128

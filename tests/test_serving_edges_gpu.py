@@ -190,3 +190,20 @@ def test_packed_rows_of_nan(fa):
     hit[2:, 320:] = True
     assert torch.equal(got[~hit], want[~hit]) and torch.equal(gl[~hit], wl[~hit])
     assert bool(torch.isnan(got[hit]).all()) and bool(torch.isnan(gl[hit]).all())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_packed_values_that_are_no_numbers_reach_their_128_rows_at_most(fa, bad):
+    """V of row 150: rows that see it, and O of those before it in the same 128 rows of its sequence, whose P is 0; no LSE."""
+    lens, at = [70, 300], 150
+    q, k, v, cu = inputs(8, lens, 4, 2, 128)
+    g = [x.to(DEV) for x in (q, k, v)]
+    want, wl = fa.fwd_packed(*g, ints(cu))
+    g[2][1, 70 + at, 9] = bad
+    got, gl = fa.fwd_packed(*g, ints(cu))
+    fa.check_device_status()
+    assert torch.equal(gl, wl)
+    assert torch.equal(got[:2], want[:2]) and torch.equal(got[2:, : 70 + 128], want[2:, : 70 + 128])
+    other = torch.arange(128, device=DEV) != 9
+    assert torch.equal(got[..., other], want[..., other])
+    assert not torch.isfinite(got[2:, 70 + at:, 9]).any()
