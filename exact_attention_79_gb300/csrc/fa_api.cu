@@ -506,7 +506,8 @@ fa_status fa_fwd_packed(const void* q, long long q_stride_h, long long q_stride_
                                v_stride_h, v_stride_t, o_stride_h, o_stride_t};
   for (long long s : strides)
     if (s < d || s % 8 != 0 || s >= (1LL << 39)) return FA_ERR_INVALID_ARG;
-  if (d > 128) return FA_ERR_UNSUPPORTED;
+  // (past 2^24 sequences the look for an item could outlast the waits for it)
+  if (d > 128 || S > (1 << 24)) return FA_ERR_UNSUPPORTED;
   unsigned* status = nullptr;
   unsigned long long* clock_acc = nullptr;
   int num_sms = 0;

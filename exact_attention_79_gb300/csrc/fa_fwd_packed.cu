@@ -73,13 +73,17 @@ __device__ __forceinline__ void sequence(const FwdParams& p, int s, int& start, 
 // Finds items in the line's order, by one warp: C(w) = sum_s max(0, n_s - w)
 // counts the (sequence, tile) of index w or more; the r-th has the index w with
 // C(w) > r >= C(w + 1). r only grows, so w only falls. The first 256
-// sequences' counts stay in registers, 8 per lane; others are read again.
+// sequences' counts stay in registers, 8 per lane; others are read again. Within an
+// index the sequence only grows too, and each look-up goes on from where the one before
+// ended: from the first sequence on every time, 16384 of four rows took 61 ms, now 4.9, and the time grew with the
+// square of their number, up to look-ups that outlast the other warps' waits.
 struct Finder {
   const FwdParams& p;
   const int unit, lane;
   int n[8];
   int w, above;                                            // index, C(w + 1)
   int upto;                                                // C(w)
+  int at, before;                                          // the last look-up's 32 sequences; how many before them have more than w tiles
   __device__ __forceinline__ int tiles(int s) const {
     if (s >= p.S) return 0;
     int start, len;
@@ -103,6 +107,7 @@ struct Finder {
     for (int s = 256 + lane; s < p.S; s += 32) top = max(top, tiles(s));
     w = __reduce_max_sync(0xffffffffu, top);
     above = upto = 0;                                      // nothing has index w
+    at = before = 0;
   }
   // r >= the r of earlier calls; false: there are not that many
   __device__ __forceinline__ bool find(int r, Item& it) {
@@ -118,9 +123,10 @@ struct Finder {
       w = lo;
       above = count(lo + 1);
       upto = count(lo);
+      at = before = 0;
     }
-    int k = r - above;                                     // the k-th sequence with more than w tiles
-    for (int s0 = 0; s0 < p.S; s0 += 32) {
+    int k = r - above - before;                            // of those from `at` on, the k-th sequence with more than w tiles
+    for (int s0 = at; s0 < p.S; s0 += 32) {
       int np = 0;
       if (s0 < 256) {
 #pragma unroll
@@ -131,6 +137,7 @@ struct Finder {
       unsigned hit = __ballot_sync(0xffffffffu, np > w);
       const int c = __popc(hit);
       if (k < c) {
+        at = s0;
         for (; k > 0; --k) hit &= hit - 1;
         const int s = s0 + __ffs(hit) - 1;
         sequence(p, s, it.start, it.len);
@@ -138,6 +145,7 @@ struct Finder {
         return true;
       }
       k -= c;
+      before += c;
     }
     return false;
   }

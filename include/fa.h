@@ -114,7 +114,7 @@ fa_status fa_fwd_kv(const void* q, const void* k, const void* v, void* o, float*
  * fp32, of P unrounded.
  * Rows of no sequence (before the first, behind the last) are left as they
  * were, in o and in lse. Values outside the rules for cu_seqlens are taken
- * within 0 .. T, and some rows may then not be written. d <= 128
+ * within 0 .. T, and some rows may then not be written. d <= 128 and S <= 2^24
  * (FA_ERR_UNSUPPORTED above). One launch; nothing is read on the host. */
 fa_status fa_fwd_packed(const void* q, long long q_stride_h, long long q_stride_t, const void* k,
                         long long k_stride_h, long long k_stride_t, const void* v, long long v_stride_h,

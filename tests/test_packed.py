@@ -80,3 +80,7 @@ def test_every_pair_is_taken_once_largest_first(lens):
     assert sorted(got) == sorted((w, s) for s, n in enumerate(pairs) for w in range(n))
     assert [w for w, _ in got] == sorted((w for w, _ in got), reverse=True)
     assert item(total, pairs) is None and total <= (sum(lens) + 255 * len(lens)) // 256
+
+
+def test_more_sequences_than_can_be_looked_up_in_time(lib):
+    assert call(lib, S=(1 << 24) + 1) == 2

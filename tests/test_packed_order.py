@@ -6,13 +6,15 @@ import pytest
 
 
 class Finder:
-    """r only grows: the index w only falls, and C(w + 1), C(w) are kept between calls."""
+    """r only grows: the index w only falls, and C(w + 1), C(w) are kept between calls, and within an index where the last
+    look-up ended."""
 
     def __init__(self, lens, unit):
         self.n = [-(-x // unit) for x in lens]
         self.w = max(self.n, default=0)
         self.above = self.upto = 0
-        self.searches = 0
+        self.at = self.before = 0
+        self.searches = self.steps = 0
 
     def count(self, x):
         return sum(max(0, n - x) for n in self.n)
@@ -30,12 +32,16 @@ class Finder:
                 else:
                     hi = mid
             self.w, self.above, self.upto = lo, self.count(lo + 1), self.count(lo)
-        k = r - self.above
-        for s0 in range(0, len(self.n), 32):                # a warp's 32 sequences at a time
+            self.at = self.before = 0
+        k = r - self.above - self.before
+        for s0 in range(self.at, len(self.n), 32):          # a warp's 32 sequences at a time
+            self.steps += 1
             hit = [s for s in range(s0, min(s0 + 32, len(self.n))) if self.n[s] > self.w]
             if k < len(hit):
+                self.at = s0
                 return self.w, hit[k]
             k -= len(hit)
+            self.before += len(hit)
         return None
 
 
@@ -81,3 +87,13 @@ def test_the_index_is_searched_once_per_change():
     f = Finder([1000] * 40, 128)
     assert [f.find(r)[0] for r in range(320)] == [w for w in range(7, -1, -1) for _ in range(40)] and f.searches == 8
     assert f.find(320) is None
+
+
+def test_the_look_up_goes_on_where_it_ended():
+    """The steps of a CTA's look-ups: the sequences once per index, and one for each item."""
+    lens = [70] * 5000 + [0, 300] * 500
+    f = Finder(lens, 128)
+    total = sum(-(-n // 128) for n in lens)
+    for r in range(0, total, 7):
+        f.find(r)
+    assert f.steps <= f.searches * -(-len(lens) // 32) + -(-total // 7)

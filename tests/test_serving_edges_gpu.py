@@ -207,3 +207,36 @@ def test_packed_values_that_are_no_numbers_reach_their_128_rows_at_most(fa, bad)
     other = torch.arange(128, device=DEV) != 9
     assert torch.equal(got[..., other], want[..., other])
     assert not torch.isfinite(got[2:, 70 + at:, 9]).any()
+
+
+def test_packed_hundreds_of_thousands_of_sequences(fa):
+    """2^18 sequences of one row, of three, or of none: O is V where a row sees itself alone. The look for an item goes on
+    where the one before ended: a time that grows with the square of the sequences would be ten times what is allowed here."""
+    S, Hq, d = 2 ** 18, 4, 64
+    lens = np.array([1, 3, 0, 1])[np.random.default_rng(70).integers(0, 4, S)]
+    cu = torch.from_numpy(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)).to(DEV)
+    T = int(lens.sum())
+    gen = torch.Generator(device=DEV).manual_seed(71)
+    q, k, v = (torch.randn(H, T, d, device=DEV, generator=gen).to(torch.bfloat16) for H in (Hq, 2, 2))
+    fa.fwd_packed(q[:, :9], k[:, :9], v[:, :9], ints([0, 9]))
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    o, lse = fa.fwd_packed(q, k, v, cu)
+    end.record()
+    torch.cuda.synchronize()
+    fa.check_device_status()
+    assert start.elapsed_time(end) < 1500
+    first = torch.from_numpy(np.cumsum(lens) - lens).to(DEV)[torch.from_numpy(lens > 0).to(DEV)]
+    assert torch.equal(o[:, first], v.repeat_interleave(2, 0)[:, first])
+    three = (torch.from_numpy(np.cumsum(lens) - lens).to(DEV)[torch.from_numpy(lens == 3).to(DEV)])[:10000, None] + torch.arange(3, device=DEV)
+    qs, ks, vs = (x.double()[:, three] for x in (q, k.repeat_interleave(2, 0), v.repeat_interleave(2, 0)))       # [Hq, n, 3, d]
+    s = (qs @ ks.transpose(-1, -2)) * d ** -0.5
+    s = s.masked_fill(torch.ones(3, 3, device=DEV, dtype=torch.bool).triu(1), float("-inf"))
+    p = s.softmax(-1)
+    want, size = p @ vs, p @ vs.abs()
+    # logits (d + 8) 2^-23 A, P 2^-8 and 2^-20, sums 3 2^-23 twice, O 2^-8
+    A = (qs.abs() @ ks.abs().transpose(-1, -2)).amax(-1, keepdim=True) * d ** -0.5
+    rel = 2.0 ** -8 + 2.0 ** -20 + 2 * (d + 8) * 2.0 ** -23 * A + 6 * 2.0 ** -23
+    assert bool(((o.double()[:, three] - want).abs() <= 2.0 ** -8 * want.abs() + rel * size + 1e-30).all())
+    ltol = (d + 8) * 2.0 ** -23 * A[..., 0] + 2.0 ** -20 + 3 * 2.0 ** -23 + s.logsumexp(-1).abs() * 2.0 ** -22
+    assert bool(((lse.double()[:, three] - s.logsumexp(-1)).abs() <= ltol).all())
