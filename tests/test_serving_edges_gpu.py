@@ -230,12 +230,12 @@ def test_packed_hundreds_of_thousands_of_sequences(fa):
     assert torch.equal(o[:, first], v.repeat_interleave(2, 0)[:, first])
     three = (torch.from_numpy(np.cumsum(lens) - lens).to(DEV)[torch.from_numpy(lens == 3).to(DEV)])[:10000, None] + torch.arange(3, device=DEV)
     qs, ks, vs = (x.double()[:, three] for x in (q, k.repeat_interleave(2, 0), v.repeat_interleave(2, 0)))       # [Hq, n, 3, d]
-    s = (qs @ ks.transpose(-1, -2)) * d ** -0.5
+    s = (qs[..., :, None, :] * ks[..., None, :, :]).sum(-1) * d ** -0.5
     s = s.masked_fill(torch.ones(3, 3, device=DEV, dtype=torch.bool).triu(1), float("-inf"))
     p = s.softmax(-1)
-    want, size = p @ vs, p @ vs.abs()
+    want, size = ((p[..., None] * x[..., None, :, :]).sum(-2) for x in (vs, vs.abs()))
     # logits (d + 8) 2^-23 A, P 2^-8 and 2^-20, sums 3 2^-23 twice, O 2^-8
-    A = (qs.abs() @ ks.abs().transpose(-1, -2)).amax(-1, keepdim=True) * d ** -0.5
+    A = (qs[..., :, None, :] * ks[..., None, :, :]).abs().sum(-1).amax(-1, keepdim=True) * d ** -0.5
     rel = 2.0 ** -8 + 2.0 ** -20 + 2 * (d + 8) * 2.0 ** -23 * A + 6 * 2.0 ** -23
     assert bool(((o.double()[:, three] - want).abs() <= 2.0 ** -8 * want.abs() + rel * size + 1e-30).all())
     ltol = (d + 8) * 2.0 ** -23 * A[..., 0] + 2.0 ** -20 + 3 * 2.0 ** -23 + s.logsumexp(-1).abs() * 2.0 ** -22
