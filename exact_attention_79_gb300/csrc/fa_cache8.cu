@@ -1101,7 +1101,8 @@ int cache8_columns(int R) { return R <= 4 ? 4 : (R - 1) / 8 % 2 == 0 ? 8 : 16; }
 // 6.7 and 8.7 against 8.7 and 8.8, 128 groups 8.3 and 10.3 against 14.1 and 14.3, 1024 30 and 40
 // against 42 and 55; at d 256 384 groups 14.5 and 23 against 20 and 26.5. Up to 16 at d 128 with more
 // groups than SMs: 240, 384 and 1024 groups 16, 29 and 61 against 21, 29 and 66 (8 groups 12.8
-// against 9.8; d 256 45 against 41; 32 blocks 29, 51 and 105 against 33, 44 and 94).
+// against 9.8; d 256 45 against 41; 32 blocks 29, 51 and 105 against 33, 44 and 94). By the table's width,
+// since the lengths are on the device: eight sequences of 300 tokens under a wider table lose those 4 us.
 bool cache8_whole(int B, int Hkv, int d, int R, int max_blocks) {
   const int cols = cache8_columns(R), chunks = (R + cols - 1) / cols;
   const bool many = static_cast<long long>(B) * Hkv * chunks > kCache8Sms && d <= 128;

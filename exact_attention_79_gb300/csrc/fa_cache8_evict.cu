@@ -10,7 +10,7 @@
 //     tokens of its stretch that stay and writes their positions behind those before.
 //  2. cache8_gather_kernel  one CTA per (destination block, head, K or V): the
 //     kept tokens' codes, re-encoded with a scale of their own.
-// Measured: 8 sequences of 8192 to 32768 tokens, 8 heads, d 128, cut to 4096: 45 us, of which the
+// Measured: 8 sequences of 8192 to 32768 tokens, 8 heads, d 128, cut to 4096: 46 us, of which the
 // selection some 18 (7 MB; its rounds of histograms and barriers bound it: one CTA per head took
 // 100, bins of 11 bits 40) and the gathering 27 (140 MB in rows of d bytes: 5 TB/s). 2 sequences
 // of 517 tokens: 11 us, two launches and their chains of loads.

@@ -8,7 +8,8 @@
 // written once (1 byte). One CTA of 128 threads per block, head and K or V, eight
 // 16-byte loads in flight per thread; 256 threads with four each spent a third more
 // instructions on finding their block (35 us). 30011 tokens of 8 heads, d 128: 31 us, 6.0 TB/s;
-// one token each for 64 sequences 5.3 us, which is the launch and two rounds of loads.
+// one token each for 64 sequences 5.3 us, which is the launch and two rounds of loads. Every CTA looks through
+// the sequences 32 at a time: 256 sequences take 21 us, 1024 131, 4096 1475.
 #include "fa_cache8.cuh"
 
 namespace fa {

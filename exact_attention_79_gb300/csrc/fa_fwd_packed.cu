@@ -25,8 +25,8 @@
 // beside it, and O's way out (1900 to 3000, through 4 KB per warp, whose second half is read
 // and packed while the TMA unit takes the first; 16-byte stores from registers take 10% longer,
 // coalesced ones through the same 4 KB 30%). Sequences of 128, 512, 1024, 2048, 8192 rows: 130, 188,
-// 264, 420, 1400 us, the last at 1.57 PFLOP/s; 24 of 32 to 1593 rows 290 us (0.93 PFLOP/s of what
-// the causal rule needs, 1.18 with the diagonal tiles whole). Up to 128 rows the bytes of Q and O
+// 264, 420, 1400 us, the last at 1.57 PFLOP/s; 24 of 32 to 1593 rows 297 us (0.91 PFLOP/s of what
+// the causal rule needs, 1.15 with the diagonal tiles whole). Up to 128 rows the bytes of Q and O
 // bound it (4.6 TB/s).
 //
 // Warps: 0-3 and 4-7 the two softmax groups (one thread per query row), 8 TMA

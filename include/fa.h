@@ -383,9 +383,10 @@ fa_status fa_cache8_append(const void* k, long long k_stride_h, long long k_stri
  * workspace: fa_fwd_cache8_workspace_bytes(B, Hq, Hkv, Nq, d, max_blocks,
  * add_weights) bytes (a few MB; with weights also 4 bytes per row, rows rounded
  * up to a multiple of 4 (of 8 or 16 past 8), for every token and KV head that
- * the block tables have room for), 256-byte aligned, contents before and after
+ * the block tables have room for, however few are held), 256-byte aligned, contents before and after
  * of no meaning; calls that may overlap on the GPU need one each. 256 says that
- * short sequences need none: the call then looks at no workspace, NULL will do.
+ * narrow tables (of up to 8 blocks, of 16 in large batches) need none: the call
+ * then looks at no workspace, NULL will do.
  * 0 for sizes that it refuses (B * Hkv * max_blocks row groups and blocks past 2^31 among them). */
 size_t fa_fwd_cache8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int max_blocks, int add_weights);
 fa_status fa_fwd_cache8(const void* q, const fa_cache8* cache, const int* block_table, int max_blocks,
