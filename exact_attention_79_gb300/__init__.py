@@ -51,6 +51,9 @@ SIGNATURES = {
     "fa_fwd_packed": (_I, [_VP, _LL, _LL, _VP, _LL, _LL, _VP, _LL, _LL, _VP, _LL, _LL, _VP, _VP,
                            _I, _I, _I, _I, _I, _I, _F, _VP]),
     "fa_cache8_append": (_I, [_VP, _LL, _LL, _VP, _LL, _LL, _VP, _VP, _I, _I, _VP, _VP, _I, _VP]),
+    "fa_cache8_append_rope": (_I, [_VP, _LL, _LL, _VP, _LL, _LL, _VP, _VP, _I, _I, _VP, _VP, _I, _VP, _VP, _LL, _VP]),
+    "fa_rope": (_I, [_VP, _LL, _LL, _LL, _VP, _LL, _LL, _LL, _I, _VP, _LL, _LL, _LL, _VP, _LL, _LL, _LL, _I, _I, _I, _I, _I,
+                     _VP, _VP, _LL, _LL, _I, _VP]),
     "fa_fwd_cache8_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
     "fa_fwd_cache8": (_I, [_VP, _VP, _VP, _I, _VP, _VP, _VP, _VP, _SZ, _I, _I, _I, _I, _F, _I, _F, _VP]),
     "fa_cache8_evict": (_I, [_VP, _VP, _I, _VP, _I, _I, _I, _VP, _I, _VP, _VP, _VP]),
@@ -307,6 +310,120 @@ def bwd(q, k, v, o, lse, do, causal=False, scale=None, workspace=None, dq=None, 
     return dq, dk, dv
 
 
+class Rope(NamedTuple):
+    """A rotation by positions (fa_rope_plan). turns: int64 [pairs], each pair's frequency / 2 pi in units of 2^-64,
+    modulo 2^64; axis: int32 [pairs], which row of the positions a pair goes by, or None (the first); interleaved: pair i
+    is columns (2 i, 2 i + 1), otherwise (i, i + pairs). CUDA tensors; `new_rope` makes them."""
+    turns: "torch.Tensor"       # noqa: F821
+    axis: "torch.Tensor" = None     # noqa: F821
+    interleaved: bool = False
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("turns", _VP), ("axis", _VP), ("pairs", _I), ("axes", _I), ("interleaved", _I)]
+
+
+def new_rope(freqs, axis=None, interleaved=False, device="cuda"):
+    """A Rope of the frequencies `freqs` (radians per position, one per pair, a multiple of 4 of them), pair i going by
+    axis[i] of the positions (None: all by one)."""
+    from fractions import Fraction
+    import torch
+    # in whole numbers: a double's 2^-53 of a turn, times a position of 2^31, would show
+    two_pi = Fraction(628318530717958647692528676655900576839433879875021, 10 ** 50)
+    turns = [round(Fraction(float(f)) / two_pi * 2 ** 64) % 2 ** 64 for f in freqs]
+    turns = torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in turns], dtype=torch.int64, device=device)
+    if axis is not None:
+        axis = torch.tensor([int(a) for a in axis], dtype=torch.int32, device=device)
+    return Rope(turns, axis, bool(interleaved))
+
+
+def _rope_specs(rope, axes):
+    """The plan's tensors as _require takes them and its C form."""
+    import torch
+    pairs = rope.turns.numel()
+    specs = [(rope.turns, "rope.turns", torch.int64, (pairs,))]
+    if rope.axis is not None:
+        specs.append((rope.axis, "rope.axis", torch.int32, (pairs,)))
+    return specs, _Rope(rope.turns.data_ptr(), None if rope.axis is None else rope.axis.data_ptr(), pairs, axes,
+                        int(bool(rope.interleaved)))
+
+
+def _rope_strides(x, name, shape, dtype):
+    """Batch, head and token strides of a [B, H, T, d] (or [H, T, d]) tensor whose rows of d values are contiguous and
+    16-byte aligned. A dimension of size 1 gets a stride that nothing reads through."""
+    if x.dtype != dtype or x.shape != shape:
+        raise ValueError(f"{name}: expected {dtype} of shape {tuple(shape)}, got {x.dtype} of shape {tuple(x.shape)}")
+    d, unit = shape[-1], 16 // dtype.itemsize
+    if d > 1 and x.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    strides = [s if n > 1 else d for n, s in zip(shape[:-1], x.stride()[:-1])]
+    if any(s % unit for s in strides):
+        raise ValueError(f"{name}: strides other than the last must be multiples of {unit}")
+    return strides if len(strides) == 3 else [0, *strides]
+
+
+def rope(q, k, rope, positions, inverse=False, q_out=None, k_out=None):
+    """Q and K turned by their positions (fa_rope), on the current stream; inverse=True: turned back, which takes the
+    gradients of the results to those of q and k.
+
+    q: [B, Hq, T, d] or [Hq, T, d], bf16 or fp32, any strides that are multiples of 16 bytes (a projection's
+    [B, T, H, d].transpose(1, 2) too); k: the same with its own heads, or None. positions: int32, [axes, B, T] (3-D q:
+    [axes, T]); the batch may be left out where all share them, and the axes where there is one. q_out, k_out: where the
+    results go, in any such layout (q and k themselves too); otherwise tensors laid out like q and k. Returns (q_out,
+    k_out), k_out None without k."""
+    import torch
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [B, H, T, d] or [H, T, d]")
+    dtype, dev, batched = q.dtype, q.device, q.dim() == 4
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("q and k must be bf16 or fp32")
+    B, (Hq, T, d) = q.shape[0] if batched else 1, q.shape[-3:]
+    qs = _rope_strides(q, "q", q.shape, dtype)
+    placed, Hkv, ks, kos = [], 0, [0, 0, 0], [0, 0, 0]
+    if q_out is not None:
+        placed.append((q_out, "q_out"))
+    if k is not None:
+        if k.dim() != q.dim():
+            raise ValueError("k must have as many dimensions as q")
+        Hkv = k.shape[-3]
+        shape = (*k.shape[:-3], Hkv, T, d) if not batched else (B, Hkv, T, d)
+        ks = _rope_strides(k, "k", shape, dtype)
+        placed.append((k, "k"))
+        if k_out is not None:
+            kos = _rope_strides(k_out, "k_out", shape, dtype)
+            placed.append((k_out, "k_out"))
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if q_out is not None:
+        _rope_strides(q_out, "q_out", q.shape, dtype)
+    # positions to [axes, B, T]: with the batch's dimension or without it
+    n = positions.dim()
+    if positions.dtype != torch.int32 or n < 1 or positions.shape[-1] != T or n > (3 if batched else 2) or \
+            (T > 1 and positions.stride(-1) != 1):
+        raise ValueError("positions must be int32 [axes, B, T], [axes, T] or [T], the last dimension contiguous")
+    if batched and n == 2 and positions.shape[0] == B and rope.axis is None:
+        axes, sa, sb = 1, 0, positions.stride(0)                    # [B, T], one axis
+    elif n == 3:
+        if positions.shape[1] != B:
+            raise ValueError("positions must be [axes, B, T]")
+        axes, sa, sb = positions.shape[0], positions.stride(0), positions.stride(1)
+    else:
+        axes, sa, sb = (positions.shape[0], positions.stride(0), 0) if n == 2 else (1, 0, 0)
+    specs, plan = _rope_specs(rope, axes)
+    _require(dev, *specs)
+    _placed(dev, (positions, "positions"), *placed)
+    q_out = torch.empty_like(q) if q_out is None else q_out
+    if k is not None and k_out is None:
+        k_out = torch.empty_like(k)
+        kos = _rope_strides(k_out, "k_out", k.shape, dtype)
+    if q.numel() == 0:
+        return q_out, k_out
+    _call_on(dev, "fa_rope", q.data_ptr(), *qs, q_out.data_ptr(), *_rope_strides(q_out, "q_out", q.shape, dtype), Hq,
+             None if k is None else k.data_ptr(), *ks, None if k is None else k_out.data_ptr(), *kos, Hkv, B, T, d,
+             dtype.itemsize, ctypes.byref(plan), positions.data_ptr(), sa, sb, int(bool(inverse)))
+    return q_out, k_out
+
+
 CACHE8_BLOCK = 64       # tokens per cache block (FA_CACHE8_BLOCK)
 
 
@@ -435,12 +552,14 @@ def fwd_packed(q, k, v, cu_seqlens, causal=True, scale=None, out=None, lse=None)
     return o, lse
 
 
-def cache8_append(cache, k, v, cu_seqlens, block_table, start):
+def cache8_append(cache, k, v, cu_seqlens, block_table, start, rope=None, positions=None):
     """Append tokens to the sequences of an 8-bit cache (fa_cache8_append), in place on the current stream.
 
     k, v: bf16 [Hkv, T, d] (strided: [T, Hkv, d].transpose(0, 1) as well), the new tokens of all sequences one behind
     the other; sequence b's are cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32 [B + 1]) and become its positions from
-    start[b] (int32 [B]) on. One token each: cu_seqlens = 0, 1, ..., B."""
+    start[b] (int32 [B]) on. One token each: cu_seqlens = 0, 1, ..., B.
+    rope (a Rope): K is turned by its positions on the way (fa_cache8_append_rope); positions: int32 [axes, T] or [T], None:
+    each token's position in its sequence."""
     import torch
     specs, c, (_, Hkv, d) = _cache8_specs(cache)
     if k.dim() != 3:
@@ -449,12 +568,28 @@ def cache8_append(cache, k, v, cu_seqlens, block_table, start):
     B = block_table.shape[0]
     i32 = torch.int32
     ks, vs = _heads_strides(k, "k", Hkv, T, d), _heads_strides(v, "v", Hkv, T, d)
+    if positions is not None:
+        if rope is None:
+            raise ValueError("positions without rope")
+        n = positions.dim()
+        if positions.dtype != i32 or n not in (1, 2) or positions.shape[-1] != T or (T > 1 and positions.stride(-1) != 1):
+            raise ValueError("positions must be int32 [axes, T] or [T], the last dimension contiguous")
+        axes, sa = (positions.shape[0], positions.stride(0)) if n == 2 else (1, 0)
+    else:
+        axes, sa = 1, 0
+    if rope is not None:
+        more, plan = _rope_specs(rope, axes)
+        specs += more
     _require(dev, *specs, (cu_seqlens, "cu_seqlens", i32, (B + 1,)), _table_spec(block_table), (start, "start", i32, (B,)))
-    _placed(dev, (k, "k"), (v, "v"))
+    _placed(dev, (k, "k"), (v, "v"), *([] if positions is None else [(positions, "positions")]))
     if T == 0:
         return
-    _call_on(dev, "fa_cache8_append", k.data_ptr(), *ks, v.data_ptr(), *vs, cu_seqlens.data_ptr(), start.data_ptr(), B, T,
-             ctypes.byref(c), block_table.data_ptr(), block_table.shape[1])
+    args = (k.data_ptr(), *ks, v.data_ptr(), *vs, cu_seqlens.data_ptr(), start.data_ptr(), B, T, ctypes.byref(c),
+            block_table.data_ptr(), block_table.shape[1])
+    if rope is None:
+        _call_on(dev, "fa_cache8_append", *args)
+    else:
+        _call_on(dev, "fa_cache8_append_rope", *args, ctypes.byref(plan), None if positions is None else positions.data_ptr(), sa)
 
 
 def fwd_cache8(q, cache, block_table, lengths, causal=True, scale=None, out=None, lse=None, workspace=None,

@@ -697,13 +697,24 @@ fa_status cache8_rows(int B, int Hq, int Hkv, int Nq, int d, int max_blocks) {
     return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
-}  // namespace
 
-extern "C" {
+// A rotation's table for heads of d columns; its positions are the caller's to set.
+fa_status rope_plan(const fa_rope_plan* r, int d, fa::RopePlan* out) {
+  if (!r || !r->turns || r->axes < 1 || r->pairs < 1 || 2LL * r->pairs > d) return FA_ERR_INVALID_ARG;
+  if (r->pairs % 4 != 0) return FA_ERR_UNSUPPORTED;
+  *out = fa::RopePlan{};
+  out->turns = r->turns;
+  out->axis = r->axis;
+  out->pairs = r->pairs;
+  out->axes = r->axes;
+  out->interleaved = r->interleaved ? 1 : 0;
+  return FA_OK;
+}
 
-fa_status fa_cache8_append(const void* k, long long k_stride_h, long long k_stride_t, const void* v,
-                           long long v_stride_h, long long v_stride_t, const int* cu_seqlens, const int* start, int B,
-                           int T, const fa_cache8* cache, const int* block_table, int max_blocks, void* stream) {
+fa_status append_common(const void* k, long long k_stride_h, long long k_stride_t, const void* v, long long v_stride_h,
+                        long long v_stride_t, const int* cu_seqlens, const int* start, int B, int T,
+                        const fa_cache8* cache, const int* block_table, int max_blocks, const fa::RopePlan& rope,
+                        void* stream) {
   if (!k || !v || !cu_seqlens || !start || !aligned16(k) || !aligned16(v)) return FA_ERR_INVALID_ARG;
   const long long strides[] = {k_stride_h, k_stride_t, v_stride_h, v_stride_t};
   for (long long s : strides)
@@ -727,7 +738,71 @@ fa_status fa_cache8_append(const void* k, long long k_stride_h, long long k_stri
   p.B = B;
   p.T = T;
   p.max_blocks = max_blocks;
+  p.rope = rope;
   return fa::launch_cache8_append(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+}  // namespace
+
+extern "C" {
+
+fa_status fa_cache8_append(const void* k, long long k_stride_h, long long k_stride_t, const void* v,
+                           long long v_stride_h, long long v_stride_t, const int* cu_seqlens, const int* start, int B,
+                           int T, const fa_cache8* cache, const int* block_table, int max_blocks, void* stream) {
+  return append_common(k, k_stride_h, k_stride_t, v, v_stride_h, v_stride_t, cu_seqlens, start, B, T, cache, block_table,
+                       max_blocks, fa::RopePlan{}, stream);
+}
+
+fa_status fa_cache8_append_rope(const void* k, long long k_stride_h, long long k_stride_t, const void* v,
+                                long long v_stride_h, long long v_stride_t, const int* cu_seqlens, const int* start, int B,
+                                int T, const fa_cache8* cache, const int* block_table, int max_blocks,
+                                const fa_rope_plan* rope, const int* positions, long long pos_stride_axis, void* stream) {
+  if (!cache) return FA_ERR_INVALID_ARG;
+  fa::RopePlan plan{};
+  const fa_status st = rope_plan(rope, cache->d, &plan);
+  if (st != FA_OK) return st;
+  if (pos_stride_axis < 0) return FA_ERR_INVALID_ARG;
+  plan.positions = positions;
+  plan.pos_sa = pos_stride_axis;
+  return append_common(k, k_stride_h, k_stride_t, v, v_stride_h, v_stride_t, cu_seqlens, start, B, T, cache, block_table,
+                       max_blocks, plan, stream);
+}
+
+fa_status fa_rope(const void* q, long long q_stride_b, long long q_stride_h, long long q_stride_t, void* q_out,
+                  long long q_out_stride_b, long long q_out_stride_h, long long q_out_stride_t, int Hq, const void* k,
+                  long long k_stride_b, long long k_stride_h, long long k_stride_t, void* k_out,
+                  long long k_out_stride_b, long long k_out_stride_h, long long k_out_stride_t, int Hkv, int B, int T,
+                  int d, int elt_bytes, const fa_rope_plan* rope, const int* positions, long long pos_stride_axis,
+                  long long pos_stride_b, int inverse, void* stream) {
+  if (B < 1 || T < 1 || d < 8 || d > 256 || d % 8 != 0 || (elt_bytes != 2 && elt_bytes != 4) || !positions ||
+      pos_stride_axis < 0 || pos_stride_b < 0)
+    return FA_ERR_INVALID_ARG;
+  fa::RopeParams p{};
+  const fa_status st = rope_plan(rope, d, &p.rope);
+  if (st != FA_OK) return st;
+  p.x[0] = {q, q_out, q_stride_b, q_stride_h, q_stride_t, q_out_stride_b, q_out_stride_h, q_out_stride_t, Hq};
+  p.x[1] = {k, k_out, k_stride_b, k_stride_h, k_stride_t, k_out_stride_b, k_out_stride_h, k_out_stride_t, Hkv};
+  for (int i = 0; i < 2; ++i) {
+    const fa::RopeTensor& x = p.x[i];
+    if (i == 1 && x.H == 0) continue;                  // no K
+    if (!x.in || !x.out || !aligned16(x.in) || !aligned16(x.out) || x.H < 1) return FA_ERR_INVALID_ARG;
+    const long long strides[] = {x.in_sb, x.in_sh, x.in_st, x.out_sb, x.out_sh, x.out_st};
+    for (long long s : strides)
+      if (s < 0 || s % (16 / elt_bytes) != 0) return FA_ERR_INVALID_ARG;
+    // no broadcast output: rows would be written by several threads
+    if ((B > 1 && x.out_sb < d) || (x.H > 1 && x.out_sh < d) || (T > 1 && x.out_st < d)) return FA_ERR_INVALID_ARG;
+  }
+  if (static_cast<long long>(B) * T >= (1LL << 31) || static_cast<long long>(Hq) + Hkv > 65535) return FA_ERR_UNSUPPORTED;
+  unsigned* status = nullptr;
+  const fa_status dev = device_state(stream, &status);
+  if (dev != FA_OK) return dev;
+  p.rope.positions = positions;
+  p.rope.pos_sa = pos_stride_axis;
+  p.rope.pos_sb = pos_stride_b;
+  p.B = B;
+  p.T = T;
+  p.d = d;
+  p.inverse = inverse ? 1 : 0;
+  return fa::launch_rope(elt_bytes, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 size_t fa_fwd_cache8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int max_blocks, int add_weights) {

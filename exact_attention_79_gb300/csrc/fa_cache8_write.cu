@@ -11,6 +11,7 @@
 // one token each for 64 sequences 5.3 us, which is the launch and two rounds of loads. Every CTA looks through
 // the sequences 32 at a time: 256 sequences take 21 us, 1024 131, 4096 1475.
 #include "fa_cache8.cuh"
+#include "fa_rope.cuh"
 
 namespace fa {
 namespace {
@@ -51,9 +52,136 @@ __device__ __noinline__ uint2 divide8(uint4 x, float s) {
   return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
 }
 
-// One CTA per (touched block, KV head, K or V). D: 128 or 256, d at most that.
-template <int D>
-__global__ void __launch_bounds__(kThreads, D == 128 ? 8 : 4) cache8_append_kernel(const Cache8AppendParams p) {
+// The codes of a block's tokens [0, lo) when its scale grows, eight at a time.
+__device__ __forceinline__ void rescale_codes(uint8_t* codes, int chunks, float ratio, int tid, int threads) {
+  for (int c = tid; c < chunks; c += threads) {
+    uint2 w = *reinterpret_cast<const uint2*>(codes + c * 8);
+    uint32_t r[4] = {w.x & 0xFFFFu, w.x >> 16, w.y & 0xFFFFu, w.y >> 16};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = e4m3x2_to_float2(r[k]);
+      r[k] = pack_e4m3x2(f.x * ratio, f.y * ratio);
+    }
+    *reinterpret_cast<uint2*>(codes + c * 8) = make_uint2(r[0] | r[1] << 16, r[2] | r[3] << 16);
+  }
+}
+
+// Where a CTA's block lies: slots [lo, hi) of page `page` get the tokens from tok0 on; the first is position pos0.
+struct NewTokens {
+  int lo, hi, tok0, pos0, page;
+};
+
+// K of one block for heads [h0, h1), each pair of columns turned by its angle on the way. A thread has
+// four pairs (eight columns) of up to kUnits tokens; their cosines and sines are computed once and serve
+// all its heads. The rotated values stay in fp32 until they are codes.
+template <int D, int N>
+__device__ __forceinline__ void append_rotated(const Cache8AppendParams& p, const NewTokens& n, int h0, int h1, float (*warp_max)[N / 32]) {
+  constexpr int kUnits = kCacheBlock * D / 8 / N;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int upt = p.c.d / 8, slots = N / upt;               // units of a token, tokens at a time
+  const int slot = tid / upt, c = tid - slot * upt;
+  const bool turned = 4 * c < p.rope.pairs;
+  const bool apart = turned && !p.rope.interleaved;
+  const int ca = apart ? 4 * c : 8 * c, cb = apart ? ca + p.rope.pairs : ca + 4;
+  const int count = n.hi - n.lo;
+  auto row_of = [&](int i) { return slot + i * slots; };
+  auto mine = [&](int i) { return slot < slots && row_of(i) < count; };
+  uint2 raw[kUnits][2];
+  auto load = [&](int h) {
+    const __nv_bfloat16* const x = static_cast<const __nv_bfloat16*>(p.k) + h * p.k_sh;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      raw[i][0] = raw[i][1] = make_uint2(0, 0);
+      if (mine(i)) {
+        const __nv_bfloat16* const row = x + (n.tok0 + row_of(i)) * p.k_st;
+        raw[i][0] = *reinterpret_cast<const uint2*>(row + ca);
+        raw[i][1] = *reinterpret_cast<const uint2*>(row + cb);
+      }
+    }
+  };
+  load(h0);
+  float2 cs[kUnits][4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    unsigned long long turns = 0;
+    const int* at = nullptr;
+    if (turned) {
+      turns = static_cast<unsigned long long>(p.rope.turns[4 * c + e]);
+      const int axis = p.rope.axis == nullptr ? 0 : max(0, min(p.rope.axis[4 * c + e], p.rope.axes - 1));
+      if (p.rope.positions != nullptr) at = p.rope.positions + axis * p.rope.pos_sa + n.tok0;
+    }
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      int pos = n.pos0 + row_of(i);
+      if (at != nullptr && mine(i)) pos = at[row_of(i)];
+      cs[i][e] = cos_sin_turns(turns, pos);
+    }
+  }
+  if (n.page < 0 || n.page >= p.c.num_blocks) return;
+  for (int h = h0; h < h1; ++h) {
+    const size_t ph = static_cast<size_t>(n.page) * p.c.Hkv + h;
+    uint8_t* const codes = p.c.k + ph * kCacheBlock * p.c.d;
+    float* const scale = p.c.k_scale + ph;
+    const float old = n.lo > 0 ? *scale : 0.f;              // read before the barrier, written after it
+    float f[kUnits][8];
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const uint32_t w[4] = {raw[i][0].x, raw[i][0].y, raw[i][1].x, raw[i][1].y};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f[i][2 * e] = __uint_as_float(w[e] << 16);
+        f[i][2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+      }
+      if (apart) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) rotate(f[i][e], f[i][4 + e], cs[i][e]);
+      } else if (turned) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) rotate(f[i][2 * e], f[i][2 * e + 1], cs[i][e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float a = fabsf(f[i][e]);
+        amax = fmaxf(amax, a < INFINITY ? a : 0.f);         // infinities and NaN are left out
+      }
+    }
+    if (h + 1 < h1) load(h + 1);
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));   // (non-negative floats order like their bits)
+    float* const maxima = warp_max[(h - h0) & 1];           // (the other buffer may still be read for the head before)
+    if (lane == 0) maxima[warp] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < N / 32; ++w) amax = fmaxf(amax, maxima[w]);
+    float now = fmaxf(old, power_scale(amax));
+    if (!(now > 0.f)) now = 1.f;
+    if (n.lo > 0 && now != old) rescale_codes(codes, n.lo * upt, __fdiv_rn(old, now), tid, N);
+    if (tid == 0) *scale = now;
+    const bool power = (__float_as_uint(now) & 0x7FFFFFu) == 0;   // as all made here are: 1 / now is exact
+    const float inv = __fdiv_rn(1.f, now);
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      if (!mine(i)) continue;
+      if (power) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[i][e] *= inv;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[i][e] = __fdiv_rn(f[i][e], now);
+      }
+      uint8_t* const dst = codes + (n.lo + row_of(i)) * p.c.d;
+      *reinterpret_cast<uint32_t*>(dst + ca) = pack_e4m3x2(f[i][0], f[i][1]) | pack_e4m3x2(f[i][2], f[i][3]) << 16;
+      *reinterpret_cast<uint32_t*>(dst + cb) = pack_e4m3x2(f[i][4], f[i][5]) | pack_e4m3x2(f[i][6], f[i][7]) << 16;
+    }
+    if (p.c.weight != nullptr && tid < count) p.c.weight[ph * kCacheBlock + n.lo + tid] = 0.f;
+  }
+}
+
+// D: 128 or 256, d at most that. Without rotation one CTA of kThreads per (touched block, KV head, K or V). With it (kRope, N threads) one per
+// (block, KV head) for V, and behind them one per (block, k_heads KV heads) for K.
+template <int D, bool kRope, int N>
+__global__ void __launch_bounds__(N, kRope ? 512 / N : D == 128 ? 8 : 4) cache8_append_kernel(const Cache8AppendParams p) {
+  constexpr int kThreads = N;
   constexpr int kMaxChunks = kCacheBlock * D / 8 / kThreads;   // 16-byte chunks of one block per thread
   __shared__ float warp_max[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -95,7 +223,16 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 8 : 4) cache8_append_kern
   const int lo = max(0, s - blk * kCacheBlock);
   const int hi = min(kCacheBlock, s + (e - a) - blk * kCacheBlock);
   const int tok0 = a + (blk * kCacheBlock + lo - s);
-  const int h = blockIdx.y, which = blockIdx.z;
+  if constexpr (kRope) {
+    if (static_cast<int>(blockIdx.y) >= p.c.Hkv) {
+      __shared__ float maxima[2][N / 32];
+      const int h0 = (static_cast<int>(blockIdx.y) - p.c.Hkv) * p.k_heads;
+      const NewTokens n{lo, hi, tok0, blk * kCacheBlock + lo, p.table[static_cast<long long>(b) * p.max_blocks + blk]};
+      append_rotated<D, N>(p, n, h0, min(h0 + p.k_heads, p.c.Hkv), maxima);
+      return;
+    }
+  }
+  const int h = blockIdx.y, which = kRope ? 1 : blockIdx.z;
   const int cpr = p.c.d / 8;                                  // chunks of eight values per token
   const int chunks = (hi - lo) * cpr;
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(which ? p.v : p.k) +
@@ -140,18 +277,8 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 8 : 4) cache8_append_kern
   float now = fmaxf(old, power_scale(amax));
   if (!(now > 0.f)) now = 1.f;
   if (lo > 0 && now != old) {
-    // the tokens there, 8 codes at a time, by the ratio of the scales
-    const float ratio = __fdiv_rn(old, now);
-    for (int c = tid; c < lo * cpr; c += kThreads) {
-      uint2 w = *reinterpret_cast<const uint2*>(codes + c * 8);
-      uint32_t r[4] = {w.x & 0xFFFFu, w.x >> 16, w.y & 0xFFFFu, w.y >> 16};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 f = e4m3x2_to_float2(r[k]);
-        r[k] = pack_e4m3x2(f.x * ratio, f.y * ratio);
-      }
-      *reinterpret_cast<uint2*>(codes + c * 8) = make_uint2(r[0] | r[1] << 16, r[2] | r[3] << 16);
-    }
+    // the tokens there, by the ratio of the scales
+    rescale_codes(codes, lo * cpr, __fdiv_rn(old, now), tid, kThreads);
   }
   if (tid == 0) *scale = now;
   if ((__float_as_uint(now) & 0x7FFFFFu) == 0) {                              // a normal power of two, as all made here are: 1 / now is exact
@@ -177,7 +304,17 @@ cudaError_t launch_cache8_append(const Cache8AppendParams& p, cudaStream_t strea
   // n tokens touch at most (n + 126) / 64 blocks of a sequence, and no more than n
   const long long most = (static_cast<long long>(p.T) + 126LL * p.B) / kCacheBlock;
   const unsigned items = static_cast<unsigned>(most < p.T ? most : p.T);
-  return launch_early(p.c.d > 128 ? cache8_append_kernel<256> : cache8_append_kernel<128>, dim3(items, p.c.Hkv, 2), dim3(kThreads), 0, stream, p);
+  if (p.rope.pairs > 0) {
+    // Heads per CTA that rotates K: one where there are few blocks (a decoding step), all where there are many, whose
+    // angles are then computed once.
+    Cache8AppendParams r = p;
+    r.k_heads = static_cast<long long>(items) * p.c.Hkv <= 1216 ? 1 : p.c.Hkv < 8 ? p.c.Hkv : 8;
+    const dim3 grid(items, p.c.Hkv + (p.c.Hkv + r.k_heads - 1) / r.k_heads);
+    return p.c.d > 128 ? launch_early(cache8_append_kernel<256, true, 512>, grid, dim3(512), 0, stream, r)
+                       : launch_early(cache8_append_kernel<128, true, 256>, grid, dim3(256), 0, stream, r);
+  }
+  return launch_early(p.c.d > 128 ? cache8_append_kernel<256, false, kThreads> : cache8_append_kernel<128, false, kThreads>,
+                      dim3(items, p.c.Hkv, 2), dim3(kThreads), 0, stream, p);
 }
 
 }  // namespace fa

@@ -134,6 +134,28 @@ cudaError_t launch_bwd_wide(const BwdMaps& m, const BwdMaps& m64, const BwdParam
 // (two launches on `stream`); reads only the LSE and D parts of the workspace.
 cudaError_t launch_bwd_deterministic(int d, const BwdMaps& m, const BwdParams& p, cudaStream_t stream);
 
+// ---- rotary positions (fa_rope.cu)
+struct RopePlan {
+  const long long* turns;          // [pairs] what one position turns a pair by, in units of 2^-64 of a turn
+  const int* axis;                 // [pairs] which row of the positions it goes by; nullptr: the first
+  const int* positions;            // [axes][B][T] with strides; nullptr (append): the cache's own positions, on every axis
+  long long pos_sa, pos_sb;
+  int pairs, axes, interleaved;
+};
+struct RopeTensor {
+  const void* in;
+  void* out;
+  long long in_sb, in_sh, in_st, out_sb, out_sh, out_st;   // in elements
+  int H;                           // 0: no such tensor
+};
+struct RopeParams {
+  RopeTensor x[2];                 // Q and K
+  RopePlan rope;
+  int B, T, d, inverse;
+  int tokens, heads;               // of a CTA (set at the launch)
+};
+cudaError_t launch_rope(int elt_bytes, const RopeParams& p, cudaStream_t stream);
+
 // ---- the 8-bit block cache (fa_cache8*.cu): pools of blocks of 64 tokens, codes
 // [num_blocks, Hkv, 64, d], scales [num_blocks, Hkv], weights [num_blocks, Hkv, 64]
 struct Cache8Pools {
@@ -153,6 +175,8 @@ struct Cache8AppendParams {
   const int* start;                // [B] tokens held before
   const int* table;                // [B, max_blocks]
   int B, T, max_blocks;
+  RopePlan rope;                   // pairs = 0: K as it is
+  int k_heads;                     // heads of a CTA that rotates K (set at the launch)
 };
 struct Cache8Params {
   Cache8Pools c;

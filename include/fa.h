@@ -311,6 +311,43 @@ fa_status fa_bwd_noalloc(const void* q, const void* k, const void* v, const void
                          const void* dO, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int N, int d,
                          int causal, float scale, void* stream);
 
+/* ---- Rotary positions.
+ *
+ * A plan says by how much each pair of a head's columns is turned per
+ * position: pair i, of frequency f_i (radians per position), is turned at token t by
+ * the angle f_i * positions[axis[i]][t], so that (x, y) becomes (x cos - y sin,
+ * x sin + y cos). Several axes serve images and video (rows of the positions for
+ * time, height and width). Device arrays, owned by the caller:
+ *   turns    int64 [pairs], f_i / 2 pi in units of 2^-64, modulo 2^64: the part of
+ *            a turn per position, so that the angle is exact at every int32 position
+ *   axis     int32 [pairs], 0 .. axes - 1 (others are taken within), or NULL: all 0
+ *   interleaved  pair i is columns (2 i, 2 i + 1); otherwise (i, i + pairs)
+ * 2 * pairs <= d; the columns from 2 * pairs on stay as they are. pairs a
+ * multiple of 4 (FA_ERR_UNSUPPORTED otherwise), axes >= 1. */
+typedef struct {
+  const long long* turns;
+  const int* axis;
+  int pairs;
+  int axes;
+  int interleaved;
+} fa_rope_plan;
+
+/* Turn Q [B, Hq, T, d] and, where Hkv > 0, K [B, Hkv, T, d] in one launch; with
+ * `inverse` by the negative angles, which is the gradient: d x = R^T d y. bf16
+ * (elt_bytes 2) or fp32 (4); computed in fp32 and rounded once. Strides in
+ * elements, multiples of 16 bytes, the d values of a row contiguous, inputs and
+ * outputs each with their own: a [B, T, H, d] projection can go to the
+ * [B, H, T, d] of fa_fwd. An output may be its input (same pointer and strides) and
+ * otherwise lies apart from the inputs and the other output. positions: device int32,
+ * positions[a * pos_stride_axis + b * pos_stride_b + t], pos_stride_b 0 where batches
+ * share them. d a multiple of 8 from 8 to 256; pointers 16-byte aligned. */
+fa_status fa_rope(const void* q, long long q_stride_b, long long q_stride_h, long long q_stride_t, void* q_out,
+                  long long q_out_stride_b, long long q_out_stride_h, long long q_out_stride_t, int Hq, const void* k,
+                  long long k_stride_b, long long k_stride_h, long long k_stride_t, void* k_out,
+                  long long k_out_stride_b, long long k_out_stride_h, long long k_out_stride_t, int Hkv, int B, int T,
+                  int d, int elt_bytes, const fa_rope_plan* rope, const int* positions, long long pos_stride_axis,
+                  long long pos_stride_b, int inverse, void* stream);
+
 /* ---- Serving: an 8-bit cache of keys and values.
  *
  * fa_cache8: a pool of blocks of FA_CACHE8_BLOCK = 64 tokens. Block p, KV head
@@ -362,6 +399,16 @@ fa_status fa_cache8_append(const void* k, long long k_stride_h, long long k_stri
                            long long v_stride_h, long long v_stride_t, const int* cu_seqlens, const int* start,
                            int B, int T, const fa_cache8* cache, const int* block_table, int max_blocks,
                            void* stream);
+
+/* fa_cache8_append with K turned by its positions on the way: the scale and the
+ * codes are of the rotated values, in fp32, so K is rounded once. positions:
+ * device int32, positions[a * pos_stride_axis + t] for token t of T on axis a; NULL:
+ * the position that the token gets in the cache, start[b] + i, on every axis. V as
+ * fa_cache8_append takes it. */
+fa_status fa_cache8_append_rope(const void* k, long long k_stride_h, long long k_stride_t, const void* v,
+                                long long v_stride_h, long long v_stride_t, const int* cu_seqlens, const int* start,
+                                int B, int T, const fa_cache8* cache, const int* block_table, int max_blocks,
+                                const fa_rope_plan* rope, const int* positions, long long pos_stride_axis, void* stream);
 
 /* Attention over the cache for the last Nq positions of each sequence: q, o
  * bf16 [B, Hq, Nq, d], apart from one another, lse fp32 [B, Hq, Nq], lengths
