@@ -56,6 +56,8 @@ SIGNATURES = {
                      _VP, _VP, _LL, _LL, _I, _VP]),
     "fa_fwd_cache8_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
     "fa_fwd_cache8": (_I, [_VP, _VP, _VP, _I, _VP, _VP, _VP, _VP, _SZ, _I, _I, _I, _I, _F, _I, _F, _VP]),
+    "fa_fwd_cache8_packed_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "fa_fwd_cache8_packed": (_I, [_VP, _LL, _LL, _VP, _VP, _I, _VP, _VP, _VP, _LL, _LL, _VP, _VP, _SZ, _I, _I, _I, _I, _F, _VP]),
     "fa_cache8_evict": (_I, [_VP, _VP, _I, _VP, _I, _I, _I, _VP, _I, _VP, _VP, _VP]),
     "fa_ex2_throughput": (_I, [ctypes.POINTER(ctypes.c_double), _VP]),
     "fa_sm_clock_mhz": (_I, [ctypes.POINTER(ctypes.c_double), _VP]),
@@ -629,6 +631,51 @@ def fwd_cache8(q, cache, block_table, lengths, causal=True, scale=None, out=None
     _call_on(dev, "fa_fwd_cache8", q.data_ptr(), ctypes.byref(c), block_table.data_ptr(), max_blocks, lengths.data_ptr(),
              out.data_ptr(), lse.data_ptr(), None if workspace is None else workspace.data_ptr(), n, B, Hq, Nq,
              int(bool(causal)), float(scale), weigh, float(weight_decay or 0.0))
+    return out, lse
+
+
+def fwd_cache8_packed(q, cache, cu_seqlens, block_table, lengths, causal=True, scale=None, out=None, lse=None, workspace=None):
+    """O, LSE of chunks of new tokens of B sequences over an 8-bit cache that holds them already (fa_fwd_cache8_packed), on
+    the current stream.
+
+    q: bf16 [Hq, T, d] or a [T, Hq, d] tensor's .transpose(0, 1), the chunks one behind the other; sequence b's are rows
+    cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32 [B + 1]) and the last of its lengths[b] tokens (int32 [B]). Returns (o with
+    q's layout, lse fp32 [Hq, T]); rows of no sequence are left as they were (unset in new tensors). workspace: uint8, of
+    fa_fwd_cache8_packed_workspace_bytes (about 40 MB); made by the call otherwise."""
+    import torch
+    lib = load()
+    if q.dim() != 3:
+        raise ValueError("q must be [Hq, T, d]")
+    specs, c, (_, Hkv, d) = _cache8_specs(cache)
+    Hq, T, _ = q.shape
+    B, dev = block_table.shape[0], q.device
+    if scale is None:
+        scale = d ** -0.5
+    qs = _heads_strides(q, "q", Hq, T, d)
+    i32 = torch.int32
+    specs += [_table_spec(block_table), (cu_seqlens, "cu_seqlens", i32, (B + 1,)), (lengths, "lengths", i32, (B,))]
+    if out is not None:
+        _heads_strides(out, "out", Hq, T, d)
+    if lse is not None:
+        specs.append((lse, "lse", torch.float32, (Hq, T)))
+    if workspace is not None:
+        specs.append((workspace, "workspace", torch.uint8, (workspace.numel(),)))
+    _require(dev, *specs)
+    if out is not None:
+        _placed(dev, (out, "out"))
+    else:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
+    if T == 0 or B == 0:
+        return out, lse
+    max_blocks = block_table.shape[1]
+    n = lib.fa_fwd_cache8_packed_workspace_bytes(B, T, Hq, Hkv, d, max_blocks) if workspace is None else workspace.numel()
+    if workspace is None and n > 256:                   # 256: none is needed
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    _call_on(dev, "fa_fwd_cache8_packed", q.data_ptr(), *qs, ctypes.byref(c), block_table.data_ptr(), max_blocks,
+             cu_seqlens.data_ptr(), lengths.data_ptr(), out.data_ptr(), *_heads_strides(out, "out", Hq, T, d), lse.data_ptr(),
+             None if workspace is None else workspace.data_ptr(), n, B, T, Hq, int(bool(causal)), float(scale))
     return out, lse
 
 

@@ -698,6 +698,23 @@ fa_status cache8_rows(int B, int Hq, int Hkv, int Nq, int d, int max_blocks) {
   return FA_OK;
 }
 
+// Bytes of fa_fwd_cache8_packed's workspace: two partial results per CTA and their statistics (off_s).
+struct ChunkWorkspace {
+  size_t off_s, total;
+};
+ChunkWorkspace chunk_workspace(int d, int max_blocks) {
+  if (max_blocks <= 2) return {0, kNoWorkspace};       // one key tile: nothing is split
+  const size_t D = d <= 128 ? 128 : 256, rows = 2 * static_cast<size_t>(fa::kCache8Sms) * fa::chunk_rows(d);
+  const size_t off = align256(rows * D * 4);
+  return {off, off + align256(rows * 3 * 4)};
+}
+fa_status chunk_sizes(int B, int T, int Hq, int Hkv, int d, int max_blocks) {
+  if (B < 1 || B > 65535 || T < 1 || Hq < 1 || Hkv < 1 || Hkv > 65535 || Hq % Hkv != 0 || d < 1 || max_blocks < 1 ||
+      max_blocks > (1 << 24))
+    return FA_ERR_INVALID_ARG;
+  if (!fp8_dim(d) || Hq / Hkv > 128 || T > (1 << 30)) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
 // A rotation's table for heads of d columns; its positions are the caller's to set.
 fa_status rope_plan(const fa_rope_plan* r, int d, fa::RopePlan* out) {
   if (!r || !r->turns || r->axes < 1 || r->pairs < 1 || 2LL * r->pairs > d) return FA_ERR_INVALID_ARG;
@@ -856,6 +873,63 @@ fa_status fa_fwd_cache8(const void* q, const fa_cache8* cache, const int* block_
   if (!make_map(&mk, p.c.k, 1, p.c.d, FA_CACHE8_BLOCK, rows, 64) || !make_map(&mv, p.c.v, 1, p.c.d, FA_CACHE8_BLOCK, rows, 64))
     return FA_ERR_CUDA;
   return fa::launch_cache8_fwd(mk, mv, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_fwd_cache8_packed_workspace_bytes(int B, int T, int Hq, int Hkv, int d, int max_blocks) {
+  if (chunk_sizes(B, T, Hq, Hkv, d, max_blocks) != FA_OK) return 0;
+  return chunk_workspace(d, max_blocks).total;
+}
+
+fa_status fa_fwd_cache8_packed(const void* q, long long q_stride_h, long long q_stride_t, const fa_cache8* cache,
+                               const int* block_table, int max_blocks, const int* cu_seqlens, const int* lengths, void* o,
+                               long long o_stride_h, long long o_stride_t, float* lse, void* workspace,
+                               size_t workspace_bytes, int B, int T, int Hq, int causal, float scale, void* stream) {
+  if (!q || !o || q == o || !lse || !cu_seqlens || !lengths || !aligned16(q) || !aligned16(o) || !aligned16(lse))
+    return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
+  fa::ChunkParams p{};
+  fa_status st = cache8_pools(cache, B, max_blocks, block_table, false, &p.c);
+  if (st == FA_OK) st = chunk_sizes(B, T, Hq, p.c.Hkv, p.c.d, max_blocks);
+  if (st != FA_OK) return st;
+  const long long strides[] = {q_stride_h, q_stride_t, o_stride_h, o_stride_t};
+  for (long long s : strides)
+    if (s < p.c.d || s % 8 != 0) return FA_ERR_INVALID_ARG;
+  const ChunkWorkspace w = chunk_workspace(p.c.d, max_blocks);
+  if (w.total > kNoWorkspace &&
+      (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < w.total))
+    return FA_ERR_WORKSPACE;
+  unsigned* status = nullptr;
+  int num_sms = 0;
+  st = device_state(stream, &status, &num_sms);
+  if (st != FA_OK) return st;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.q_sh = q_stride_h;
+  p.q_st = q_stride_t;
+  p.o_sh = o_stride_h;
+  p.o_st = o_stride_t;
+  p.lse = lse;
+  p.cu = cu_seqlens;
+  p.lengths = lengths;
+  p.table = block_table;
+  p.B = B;
+  p.T = T;
+  p.max_blocks = max_blocks;
+  p.G = Hq / p.c.Hkv;
+  p.tt = 128 / p.G;
+  p.causal = causal ? 1 : 0;
+  p.ctas = num_sms < fa::kCache8Sms ? num_sms : fa::kCache8Sms;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.status = status;
+  p.timeout_ns = wait_limit_ns();
+  p.test_stall = test_stall();
+  p.part_o = static_cast<float*>(workspace);
+  p.part_s = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.off_s);
+  CUtensorMap mk, mv;
+  const long long rows = static_cast<long long>(p.c.num_blocks) * p.c.Hkv;
+  if (!make_map(&mk, p.c.k, 1, p.c.d, FA_CACHE8_BLOCK, rows, 64) || !make_map(&mv, p.c.v, 1, p.c.d, FA_CACHE8_BLOCK, rows, 64))
+    return FA_ERR_CUDA;
+  return fa::launch_cache8_chunk(mk, mv, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 fa_status fa_cache8_evict(const fa_cache8* cache, const int* block_table, int max_blocks, const int* lengths, int B,

@@ -1,0 +1,1016 @@
+// Attention of chunks of new tokens over the 8-bit block cache: any number of
+// new tokens per sequence, different in each, behind any number of cached ones.
+//
+// Rows. For KV head h, a row tile is up to 128 rows: tt = 128 / G neighbouring tokens of
+// the G query heads that share it, row r being token r / G, head r % G. So all rows of a
+// tile see nearly the same keys (the causal border falls within tt tokens), and few new tokens still
+// fill tiles. An item is kGroups row tiles of one sequence and KV head, which read the same
+// K and V.
+//
+// Products, per tile of 128 keys (two cache blocks), on the tensor cores:
+//   S [128 x 128 keys] = Q K^T   e4m3 (kind::f8f6f4): K's codes as they are, Q in two e4m3 terms
+//      q = q0 + q1 of the row scaled by a power of two to [128, 256): exact down to 2^-9 of the row's largest value,
+//      2^-17 of it below that. Two terms at the e4m3 rate cost what one bf16 product does.
+//   O [128 x d] += P V           f16 (kind::f16): V's codes as halves (exact), P in f16.
+// A block's K scale multiplies its logits, its V scale its P, by a factor that keeps them within f16:
+// hence two references per row, ml for the sum of probabilities and mo for O, P' = 2^(x - ml) 2^(ml - mo) vs <= 2^15, each
+// P' within 2^-11 of itself or 2^-31 of the row's largest. O's error against 64 bits is then its own rounding to bf16.
+// (P in two e4m3 terms would save V's conversion but is 2^-8, and three cost half as much again.)
+//
+// K goes from memory into the product untouched (TMA). V passes through four converting
+// warps: 16 codes a thread at a time from the landing buffer to the MN-major f16 tile; they
+// clear keys that are not there (P is 0, but 0 x NaN is not) and also lay out Q.
+//
+// The work is a line of units, one per (item, key tile), cut into equal parts for a
+// persistent grid of one CTA per SM, whatever the lengths; an item whose units fall to several
+// CTAs is joined from partial results by a second kernel. An item of no more than one row tile
+// gives its even key tiles to one softmax group and its odd ones to the other, joined in TMEM.
+//
+// Warps: 0-3 and 4-7 the softmax groups (one thread per row), 8 producer (block table, scales,
+// TMA), 9 tensor-core issuer, 12-15 converters. At d > 128 (kGroups = 1) O takes half of TMEM, S is
+// double-buffered and warps 4-7 rest.
+#include "fa_cache8.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr float kTrailL = 8.f;            // log2 of how far the references may trail
+constexpr float kTopO = 7.f, kTrailO = 15.f;   // P' of the row's largest is 2^7 where mo is set, at most 2^15
+constexpr float kNoKey = -1.f;            // factor of O for a row that sees no key
+constexpr int kInfo = 8;                  // tiles whose scales wait in shared memory
+constexpr int kTurn = 1;                  // key tiles' time that a change of items costs
+
+template <int D>
+struct Cfg {
+  static constexpr int kGroups = D == 128 ? 2 : 1;
+  static constexpr int kCh = D / 128;                      // 128-byte columns of codes
+  static constexpr int kRows = 128 * kGroups;              // of an item
+  static constexpr int kKeysV = D == 128 ? 128 : 64;       // keys of a V stage
+  static constexpr int kPerTile = 128 / kKeysV;            // V stages of a key tile
+  static constexpr int kQTerm = 16384 * kCh;               // one term of a row tile
+  static constexpr int kQBytes = kGroups * 2 * kQTerm;
+  static constexpr int kTileK = 16384 * kCh;
+  static constexpr int kRingK = D == 128 ? 3 : 2;
+  static constexpr int kCodesV = 16384, kHalfV = 32768;    // a V stage as codes and as halves
+  static constexpr int kRingV = 2;
+  static constexpr int kBoxV = kKeysV * 128;               // 64 columns of halves
+  static constexpr int kOffK = kQBytes, kOffCodes = kOffK + kRingK * kTileK, kOffHalf = kOffCodes + kRingV * kCodesV;
+  static constexpr int kOffStat = kOffHalf + kRingV * kHalfV;
+  static constexpr int kStat = kRows * 4 + (kGroups == 2 ? 128 * 12 : 0) + kInfo * 32;
+  static constexpr int kLayout = kOffStat + kStat + 272;
+  static constexpr int kSmem = kLayout + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+  // setmaxnreg: 256 x 184 + 256 x 72 = 512 x 128
+  static constexpr uint32_t kRegsSoftmax = 184, kRegsOther = 72;
+  static __device__ __forceinline__ uint32_t col_s(int i) { return 128u * i; }
+  static __device__ __forceinline__ uint32_t col_o(int i) { return 256u + 128u * i; }
+};
+
+// Bounded wait whose limit starts at its own first look at the timer.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned long long limit_ns) {
+  uint32_t polls = 0;
+  uint64_t until = 0;
+  while (!mbar_try_wait(bar, parity)) {
+    if ((++polls & 255u) == 0) {
+      if (*abort_flag) return false;
+      const uint64_t now = global_timer_ns();
+      if (until == 0) until = now + limit_ns;
+      if (now > until) {
+        *abort_flag = 1;
+        return false;
+      }
+    }
+  }
+  return true;
+}
+
+// ------------------------------------------------------------------ the line of units
+// A sequence's new tokens (rows row0 .. row0 + n - 1 of the packed ones) and length.
+struct Sequence {
+  int row0, n, len;
+  __device__ __forceinline__ Sequence(const ChunkParams& p, int b) {
+    row0 = max(0, min(p.cu[b], p.T));
+    n = max(0, min(p.cu[b + 1], p.T) - row0);
+    len = cache_length(p.lengths, b, p.max_blocks);
+  }
+  // keys that its tokens below `last` see
+  __device__ __forceinline__ int seen(const ChunkParams& p, int last) const { return p.causal ? len - n + last : len; }
+  __device__ __forceinline__ int items(const ChunkParams& p) const { return static_cast<int>((n + static_cast<unsigned>(p.span) - 1) / p.span); }
+  // key tiles of the tokens below `last`; a row without keys has one, so that it is written
+  __device__ __forceinline__ int tiles(const ChunkParams& p, int last) const { return max(1, (seen(p, last) + 127) >> 7); }
+  __device__ __forceinline__ int end_of(const ChunkParams& p, int item) const {
+    return static_cast<int>(min(static_cast<long long>(n), (item + 1LL) * p.span));
+  }
+};
+// sum over j < n of floor((a j + b) / m), by Euclid's steps on (a, m)
+__device__ __forceinline__ long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
+  long long sum = 0;
+  while (n > 0) {
+    sum += static_cast<long long>(n) * (n - 1LL) / 2 * (a / m) + static_cast<long long>(n) * (b / m);
+    a %= m;
+    b %= m;
+    const unsigned y = a * n + b;                          // a n is at most about T
+    n = y / m;
+    b = y % m;
+    const unsigned t = m;
+    m = a;
+    a = t;
+    if (m == 0) break;
+  }
+  return sum;
+}
+// Key tiles of the first x items of one KV head, x at most the sequence's items.
+__device__ __forceinline__ long long tiles_before(const ChunkParams& p, const Sequence& s, int x) {
+  if (x == 0) return 0;
+  if (!p.causal) return static_cast<long long>(x) * s.tiles(p, s.n);
+  long long sum = 0;
+  if (x == s.items(p)) {                                   // the last item may end early
+    --x;
+    sum = s.tiles(p, s.n);
+  }
+  if (x == 0) return sum;
+  // item i has max(1, ceil(((i + 1) span + past) / 128)): 1 for the first `ones`
+  const int past = s.len - s.n;
+  const int ones = past > 128 ? 0 : static_cast<int>(min(static_cast<long long>(x), (128LL - past) / p.span));
+  sum += ones;
+  if (x > ones)
+    sum += floor_sum(x - ones, 128, p.span, static_cast<unsigned>((ones + 1LL) * p.span + past + 127));
+  return sum;
+}
+// Places of a sequence on one KV head: `turn` more for every item, the time that a change of items costs.
+__device__ __forceinline__ long long places(const ChunkParams& p, const Sequence& s, int turn) {
+  const int n = s.items(p);
+  return tiles_before(p, s, n) + static_cast<long long>(turn) * n;
+}
+__device__ __forceinline__ long long warp_sum(long long x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// The line, cut into `parts` equal parts. A part is at least twice a turn long, so that it
+// has units, and where it begins in a turn its first units are that item's.
+struct Line {
+  long long total;
+  int turn, parts;
+  // by a whole warp
+  __device__ __forceinline__ Line(const ChunkParams& p, int lane) {
+    long long units = 0, items = 0;
+    for (int b = lane; b < p.B; b += 32) {
+      const Sequence s(p, b);
+      units += places(p, s, 0);
+      items += s.items(p);
+    }
+    units = warp_sum(units) * p.c.Hkv;
+    items = warp_sum(items) * p.c.Hkv;
+    turn = static_cast<int>(min(static_cast<long long>(kTurn), units / (2 * p.ctas)));
+    total = units + turn * items;
+    parts = static_cast<int>(min(static_cast<long long>(p.ctas), total));
+  }
+  __device__ __forceinline__ long long begin(int i) const { return total * i / parts; }
+  __device__ __forceinline__ int part_of(long long u) const { return static_cast<int>(((u + 1) * parts - 1) / total); }
+};
+
+// A place of the line: `off` places into an item (its turn, then its units).
+struct Place {
+  int b, h, item, off;
+  long long start;                                         // places before the item
+  // by a whole warp; u below the total
+  __device__ __forceinline__ Place(const ChunkParams& p, int turn, long long u, int lane) {
+    long long before = 0, each = 0;
+    b = p.B - 1;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      long long cnt = 0;
+      if (b0 + lane < p.B) cnt = places(p, Sequence(p, b0 + lane), turn);
+      long long incl = cnt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, u < before + incl * p.c.Hkv);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        b = b0 + src;
+        each = __shfl_sync(0xffffffffu, cnt, src);
+        before += __shfl_sync(0xffffffffu, incl - cnt, src) * p.c.Hkv;
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31) * p.c.Hkv;
+    }
+    const Sequence s(p, b);
+    h = static_cast<int>((u - before) / each);
+    before += h * each;
+    // the last item that does not begin behind u, 32 at a time
+    int lo = 0, n = s.items(p);
+    while (n > 1) {
+      const int step = (n + 31) / 32, i = lo + min(lane * step, n - 1);
+      const bool not_behind = before + tiles_before(p, s, i) + static_cast<long long>(turn) * i <= u;
+      const int k = __popc(__ballot_sync(0xffffffffu, not_behind && lane * step < n)) - 1;
+      const int left = n - k * step;
+      lo += k * step;
+      n = min(step, left);
+    }
+    item = lo;
+    start = before + tiles_before(p, s, lo) + static_cast<long long>(turn) * lo;
+    off = static_cast<int>(u - start);
+  }
+};
+
+// An item's share of a part: key tiles [t0, t1) of `tiles`.
+struct Segment {
+  int b, h, row0, n, len;
+  int tok0;                                                // the item's first token, counted from the sequence's first new one
+  int t0, t1, tiles;
+  bool split;                                              // one row tile, whose key tiles alternate between the groups
+  int n0;                                                  // group 0's key tiles (not split): its rows see fewer
+};
+// From the part's first place on, segment by segment.
+struct Walk {
+  int b, h, item, off, turn;
+  long long left;
+  Sequence s;
+  __device__ __forceinline__ Walk(const ChunkParams& p, const volatile int* at)
+      : b(at[0]), h(at[1]), item(at[2]), off(at[3]), turn(at[4]),
+        left(static_cast<long long>(static_cast<unsigned>(at[5])) | static_cast<long long>(at[6]) << 32), s(p, at[0]) {}
+  template <int kGroups>
+  __device__ __forceinline__ bool next(const ChunkParams& p, Segment& g) {
+    if (left <= 0) return false;
+    g.b = b;
+    g.h = h;
+    g.row0 = s.row0;
+    g.n = s.n;
+    g.len = s.len;
+    g.tok0 = item * p.span;
+    g.tiles = s.tiles(p, s.end_of(p, item));
+    const int take = static_cast<int>(min(left, static_cast<long long>(turn + g.tiles - off)));
+    g.t0 = max(0, off - turn);
+    g.t1 = off + take - turn;
+    g.split = kGroups == 2 && g.tok0 + p.tt >= s.n;
+    g.n0 = max(0, min(s.tiles(p, min(s.n, g.tok0 + p.tt)), g.t1) - g.t0);
+    left -= take;
+    off = 0;
+    if (++item == s.items(p)) {
+      item = 0;
+      if (++h == p.c.Hkv) {
+        h = 0;
+        while (left > 0 && ++b < p.B) {
+          s = Sequence(p, b);
+          if (s.n > 0) break;
+        }
+        if (b >= p.B) left = 0;
+      }
+    }
+    return g.t1 > g.t0;                                    // (false: the part ends in a turn)
+  }
+};
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void mul2_b(float& d0, float& d1, float a0, float a1, float b) {
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b));
+}
+__device__ __forceinline__ void store16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ float times_factor(float o, float factor) { return factor == kNoKey ? 0.f : o * factor; }
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const ChunkParams p) {
+  using C = Cfg<D>;
+  constexpr int kGroups = C::kGroups;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const gbase = smem_raw + (base - raw);
+  auto s_q = [&](int group, int term) { return base + (group * 2 + term) * C::kQTerm; };
+  auto s_k = [&](int i) { return base + C::kOffK + i * C::kTileK; };
+  auto s_codes = [&](int i) { return base + C::kOffCodes + i * C::kCodesV; };
+  auto s_half = [&](int i) { return base + C::kOffHalf + i * C::kHalfV; };
+  float* const row_scale = reinterpret_cast<float*>(gbase + C::kOffStat);           // [kRows] what Q's rows were divided by
+  float* const other = row_scale + C::kRows;                                       // [3][128] group 1's ml, mo, l (split)
+  volatile float* const info = reinterpret_cast<volatile float*>(other + (kGroups == 2 ? 3 * 128 : 0));   // [kInfo][8]: per half K scale, V scale, there
+  const uint32_t bars = base + C::kOffStat + C::kStat;
+  uint8_t* const gbars = gbase + (bars - base);
+  auto bar_k_full = [&](int i) { return bars + 8u * i; };              // 3
+  auto bar_k_empty = [&](int i) { return bars + 24u + 8u * i; };       // 3
+  auto bar_c_full = [&](int i) { return bars + 48u + 8u * i; };        // V's codes
+  auto bar_c_empty = [&](int i) { return bars + 64u + 8u * i; };
+  auto bar_v_full = [&](int i) { return bars + 80u + 8u * i; };        // V's halves
+  auto bar_v_empty = [&](int i) { return bars + 96u + 8u * i; };
+  auto bar_s_full = [&](int i) { return bars + 112u + 8u * i; };
+  auto bar_p_ready = [&](int i) { return bars + 128u + 8u * i; };
+  auto bar_o_final = [&](int i) { return bars + 144u + 8u * i; };
+  const uint32_t bar_q_full = bars + 160u, bar_q_empty = bars + 168u;
+  const uint32_t bar_other_full = bars + 176u, bar_other_empty = bars + 184u;
+  auto bar_info = [&](int t) { return bars + 192u + 8u * (t % kInfo); };
+  const uint32_t bar_stall = bars + 256u;                              // nothing arrives (timeout test)
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbars + 264);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(gbars + 268);
+  volatile int* const first = reinterpret_cast<volatile int*>(row_scale);          // [7] the part's first place, until the roles begin
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < C::kRingK; ++i) {
+      mbar_init(bar_k_full(i), 1);
+      mbar_init(bar_k_empty(i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_c_full(i), 1);
+      mbar_init(bar_c_empty(i), 4);
+      mbar_init(bar_v_full(i), 4);
+      mbar_init(bar_v_empty(i), 1);
+      mbar_init(bar_s_full(i), 1);
+      mbar_init(bar_p_ready(i), 128);
+      mbar_init(bar_o_final(i), 1);
+    }
+    mbar_init(bar_q_full, 4);
+    mbar_init(bar_q_empty, 1 + 4 * kGroups);               // its products done, its scales read by every softmax warp
+    mbar_init(bar_other_full, 128);
+    mbar_init(bar_other_empty, 128);
+    for (int i = 0; i < kInfo; ++i) mbar_init(bar_info(i), 1);
+    mbar_init(bar_stall, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  if (warp == 2) {
+    const Line line(p, lane);
+    int at[7] = {0, 0, 0, 0, 0, 0, 0};
+    if (static_cast<int>(blockIdx.x) < line.parts) {
+      const long long u = line.begin(blockIdx.x), n = line.begin(blockIdx.x + 1) - u;
+      const Place place(p, line.turn, u, lane);
+      at[0] = place.b;
+      at[1] = place.h;
+      at[2] = place.item;
+      at[3] = place.off;
+      at[4] = line.turn;
+      at[5] = static_cast<int>(n);
+      at[6] = static_cast<int>(n >> 32);
+    }
+    if (lane == 0)
+#pragma unroll
+      for (int i = 0; i < 7; ++i) first[i] = at[i];
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  Walk walk(p, first);
+  __syncthreads();                                         // (row_scale is the converters' from here on)
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ producer
+    setmaxnreg_dec<C::kRegsOther>();
+    if (lane == 0) {
+      tma_prefetch_map(&map_k);
+      tma_prefetch_map(&map_v);
+    }
+    int tile = 0;                                          // tiles so far
+    bool ok = true;
+    Segment s;
+    while (ok && walk.next<kGroups>(p, s)) {
+      const int* const table = p.table + static_cast<long long>(s.b) * p.max_blocks;
+      const int held = (s.len + kCacheBlock - 1) / kCacheBlock;
+      for (int blk = 2 * s.t0; blk < 2 * s.t1 && ok; blk += 32) {
+        // 32 blocks at a time, one per lane
+        const int mine = blk + lane;
+        int page = mine < 2 * s.t1 && mine < held ? table[mine] : -1;
+        if (page >= p.c.num_blocks) page = -1;
+        const long long ph = page >= 0 ? static_cast<long long>(page) * p.c.Hkv + s.h : -1;
+        const float ks = page >= 0 ? p.c.k_scale[ph] : 0.f, vs = page >= 0 ? p.c.v_scale[ph] : 0.f;
+        const int z = static_cast<int>(ph);
+        for (int i = 0; i < 32 && blk + i < 2 * s.t1 && ok; i += 2, ++tile) {
+          const int za = __shfl_sync(0xffffffffu, z, i), zb = __shfl_sync(0xffffffffu, z, i + 1);
+          if (lane == 0) {
+            const int slot = tile % C::kRingK;
+            ok = wait(bar_k_empty(slot), ((tile / C::kRingK) & 1) ^ 1, abort_flag, p.timeout_ns);
+            if (ok) {
+              mbar_arrive_expect_tx(bar_k_full(slot), ((za >= 0) + (zb >= 0)) * 8192 * C::kCh);
+              for (int ch = 0; ch < C::kCh; ++ch) {
+                if (za >= 0) tma_load_3d(s_k(slot) + ch * 16384, &map_k, bar_k_full(slot), ch * 128, 0, za);
+                if (zb >= 0) tma_load_3d(s_k(slot) + ch * 16384 + 8192, &map_k, bar_k_full(slot), ch * 128, 0, zb);
+              }
+            }
+          }
+          // The scales. Their slot is free: K's slot was, so S of tile - kRingK is done, which was issued behind the
+          // product of the tile before it, or two before it: the softmax of that one and of all before is done.
+          ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
+          if (!ok) break;
+          if (lane == i || lane == i + 1) {
+            volatile float* const dst = info + (tile % kInfo) * 8 + (lane - i) * 4;
+            dst[0] = ks;
+            dst[1] = vs;
+            dst[2] = page >= 0 ? 1.f : 0.f;
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar_info(tile));
+#pragma unroll
+            for (int x = 0; x < C::kPerTile && ok; ++x) {
+              const int c = tile * C::kPerTile + x, cs = c % C::kRingV;
+              ok = wait(bar_c_empty(cs), ((c / C::kRingV) & 1) ^ 1, abort_flag, p.timeout_ns);
+              if (!ok) break;
+              if (C::kPerTile == 1) {
+                mbar_arrive_expect_tx(bar_c_full(cs), ((za >= 0) + (zb >= 0)) * 8192);
+                if (za >= 0) tma_load_3d(s_codes(cs), &map_v, bar_c_full(cs), 0, 0, za);
+                if (zb >= 0) tma_load_3d(s_codes(cs) + 8192, &map_v, bar_c_full(cs), 0, 0, zb);
+              } else {
+                const int zx = x ? zb : za;
+                mbar_arrive_expect_tx(bar_c_full(cs), zx >= 0 ? 8192 * C::kCh : 0);
+                for (int ch = 0; ch < C::kCh; ++ch)
+                  if (zx >= 0) tma_load_3d(s_codes(cs) + ch * 8192, &map_v, bar_c_full(cs), ch * 128, 0, zx);
+              }
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ tensor-core issuer
+    setmaxnreg_dec<C::kRegsOther>();
+    if (lane == 0) {
+      const uint32_t id_s = make_idesc(0, 128, 128, 0, 0);             // e4m3, both K-major
+      const uint32_t id_o = make_idesc(0, 128, p.c.d, 0, 1);           // f16, V MN-major
+      const int steps = (p.c.d + 31) / 32;                             // products over d that are not all zeros
+      bool ok = !p.test_stall || wait(bar_stall, 0, abort_flag, p.timeout_ns);   // runs out by design
+      int tile = 0, seg = 0;                                           // tiles before the segment, segments
+      uint32_t np[2] = {0, 0};                                         // P-ready phases of each buffer
+      // S of rows `group` with tile `t` into buffer `buf`
+      auto scores = [&](int buf, int group, int t, bool last_user) {
+        const int slot = t % C::kRingK;
+        ok = wait(bar_k_full(slot), (t / C::kRingK) & 1, abort_flag, p.timeout_ns);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t kd = smem_desc_sw128(s_k(slot), 16, 1024);
+#pragma unroll
+        for (int term = 0; term < 2; ++term) {
+          const uint64_t qd = smem_desc_sw128(s_q(group, term), 16, 1024);
+          for (int k = 0; k < steps; ++k) {
+            const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
+            mma_fp8_ss(tbase + C::col_s(buf), desc_add(qd, off), desc_add(kd, off), id_s, term > 0 || k > 0);
+          }
+        }
+        mma_commit(bar_s_full(buf));
+        if (last_user) mma_commit(bar_k_empty(slot));
+      };
+      // O of `group` += P in buffer `buf` times V of tile `t`
+      auto product = [&](int buf, int group, int t, bool acc, bool last_user) {
+        ok = wait(bar_p_ready(buf), np[buf], abort_flag, p.timeout_ns);
+        if (!ok) return;
+        np[buf] ^= 1;
+#pragma unroll
+        for (int x = 0; x < C::kPerTile; ++x) {
+          const int c = t * C::kPerTile + x, slot = c % C::kRingV;
+          ok = wait(bar_v_full(slot), (c / C::kRingV) & 1, abort_flag, p.timeout_ns);
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t vd = smem_desc_sw128(s_half(slot), C::kBoxV, 1024);
+#pragma unroll
+          for (int k = 0; k < C::kKeysV / 16; ++k)
+            mma_bf16_ts(tbase + C::col_o(group), tbase + C::col_s(buf) + (x * (C::kKeysV / 16) + k) * 8, desc_add(vd, k * 2048), id_o,
+                        acc || x > 0 || k > 0);
+          if (last_user) mma_commit(bar_v_empty(slot));
+        }
+      };
+      Segment s;
+      for (; ok && walk.next<kGroups>(p, s); ++seg) {
+        const int n = s.t1 - s.t0;
+        ok = wait(bar_q_full, seg & 1, abort_flag, p.timeout_ns);
+        if (!ok) break;
+        if (kGroups == 1) {
+          scores(tile & 1, 0, tile, true);
+          for (int j = 0; j < n && ok; ++j) {
+            if (j + 1 < n) scores((tile + j + 1) & 1, 0, tile + j + 1, true);
+            else mma_commit(bar_q_empty);
+            if (ok) product((tile + j) & 1, 0, tile + j, j > 0, true);
+          }
+          if (ok) mma_commit(bar_o_final(0));
+        } else if (s.split) {
+          for (int x = 0; x < min(n, 2) && ok; ++x) scores(x, 0, tile + x, true);
+          if (n <= 2) mma_commit(bar_q_empty);
+          for (int x = 0; x < n && ok; ++x) {
+            const int g = x & 1;
+            product(g, g, tile + x, x > 1, true);
+            if (!ok) break;
+            if (x + 2 < n) scores(g, 0, tile + x + 2, true);
+            else mma_commit(bar_o_final(g));
+            if (x + 3 == n) mma_commit(bar_q_empty);
+          }
+        } else {
+          if (s.n0 > 0) scores(0, 0, tile, false);
+          if (ok) scores(1, 1, tile, true);
+          if (n == 1) mma_commit(bar_q_empty);
+          for (int j = 0; j < n && ok; ++j) {
+            if (j < s.n0) {
+              product(0, 0, tile + j, j > 0, false);
+              if (!ok) break;
+              if (j + 1 < s.n0) scores(0, 0, tile + j + 1, false);
+              else mma_commit(bar_o_final(0));
+              if (!ok) break;
+            }
+            product(1, 1, tile + j, j > 0, true);
+            if (!ok) break;
+            if (j + 1 < n) scores(1, 1, tile + j + 1, true);
+            else mma_commit(bar_o_final(1));
+            if (j + 2 == n) mma_commit(bar_q_empty);
+          }
+        }
+        tile += n;
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------ converters
+    setmaxnreg_dec<C::kRegsOther>();
+    const int cw = warp - 12, tid = threadIdx.x - 384;
+    bool ok = true;
+    int tile = 0;
+    Segment s;
+    for (int seg = 0; ok && walk.next<kGroups>(p, s); ++seg) {
+      // ---- Q: this warp's 32 rows of each row tile, four at a time
+      ok = wait(bar_q_empty, (seg & 1) ^ 1, abort_flag, p.timeout_ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+#pragma unroll 1
+      for (int r0 = 0; r0 < (s.split ? 128 : C::kRows); r0 += 16) {
+        uint2 v[4][C::kCh];
+        const int tile_row = (r0 & 127) + 4 * cw, group = r0 >> 7;     // rows tile_row .. + 3 of the row tile
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = tile_row + e, tok = row / p.G, token = s.tok0 + group * p.tt + tok;
+          const bool real = tok < p.tt && token < s.n;
+          const __nv_bfloat16* const src =
+              p.q + (s.h * p.G + (row - tok * p.G)) * p.q_sh + (static_cast<long long>(s.row0) + token) * p.q_st;
+#pragma unroll
+          for (int ch = 0; ch < C::kCh; ++ch) {
+            const int col = 128 * ch + 4 * lane;
+            v[e][ch] = real && col < p.c.d ? *reinterpret_cast<const uint2*>(src + col) : make_uint2(0, 0);
+          }
+        }
+        uint32_t amax[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t m = 0;                                  // both halves' largest magnitudes, as bits
+#pragma unroll
+          for (int ch = 0; ch < C::kCh; ++ch) {
+            const uint32_t w[2] = {v[e][ch].x & 0x7FFF7FFFu, v[e][ch].y & 0x7FFF7FFFu};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) m = max(m, max(w[k] & 0xFFFFu, w[k] >> 16));
+          }
+          amax[e] = __reduce_max_sync(0xffffffffu, m);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // exponent that brings the largest to [128, 256); bounded so that both powers are normal.
+          // A row with an infinity or NaN becomes NaN, as its logits are.
+          const int e2 = amax[e] > 0 ? max(-100, min(100, static_cast<int>(amax[e] >> 7) - 127 - 7)) : 0;
+          const float down = amax[e] < 0x7F80u ? __uint_as_float(static_cast<uint32_t>(127 - e2) << 23) : NAN;
+          if (lane == 0) row_scale[group * 128 + tile_row + e] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+#pragma unroll
+          for (int ch = 0; ch < C::kCh; ++ch) {
+            const uint32_t w[2] = {v[e][ch].x, v[e][ch].y};
+            uint32_t hi = 0, lo = 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              // (eight significant bits and at most 256: f16 holds what the two terms can)
+              const uint32_t x = pack_f16x2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
+              const uint32_t c0 = f16x2_to_e4m3x2(x);
+              hi |= c0 << (16 * k);
+              lo |= f16x2_to_e4m3x2(sub_f16x2(x, e4m3x2_to_f16x2(c0))) << (16 * k);
+            }
+            const uint32_t at = swz128(ch * 16384, tile_row + e, lane >> 2) + (lane & 3) * 4;
+            asm volatile("st.shared.b32 [%0], %1;" :: "r"(s_q(group, 0) + at), "r"(hi) : "memory");
+            asm volatile("st.shared.b32 [%0], %1;" :: "r"(s_q(group, 1) + at), "r"(lo) : "memory");
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_q_full);
+      // ---- V: 16 codes of a key at a time
+      constexpr int kPieces = D / 16;                      // of a key
+      const int piece = tid % kPieces, key0 = tid / kPieces;
+      for (int j = s.t0; j < s.t1 && ok; ++j, ++tile) {
+        ok = wait(bar_info(tile), (tile / kInfo) & 1, abort_flag, p.timeout_ns);
+        const volatile float* const there = info + (tile % kInfo) * 8;
+#pragma unroll
+        for (int x = 0; x < C::kPerTile; ++x) {
+          const int c = tile * C::kPerTile + x, slot = c % C::kRingV;
+          if (ok) ok = wait(bar_c_full(slot), (c / C::kRingV) & 1, abort_flag, p.timeout_ns);
+          if (ok) ok = wait(bar_v_empty(slot), ((c / C::kRingV) & 1) ^ 1, abort_flag, p.timeout_ns);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          // keys of the stage that there are, in each of its blocks
+          const int valid = s.len - j * 128 - x * C::kKeysV;
+          const bool here0 = there[C::kPerTile == 1 ? 2 : 4 * x + 2] != 0.f, here1 = there[6] != 0.f;
+          const uint32_t src = s_codes(slot) + (piece >> 3) * 8192, dst = s_half(slot) + (piece >> 2) * C::kBoxV;
+          const int u0 = 2 * (piece & 3), flip = (piece >> 2) & 1;     // (every other box the second unit first: no bank twice)
+          if (16 * piece < p.c.d) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int key = key0 + i * (128 / kPieces);
+              uint4 w = make_uint4(0, 0, 0, 0);
+              if (key < valid && (key < 64 ? here0 : here1))
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                             : "r"(swz128(src, key, piece & 7)) : "memory");
+              uint32_t f[8];
+              const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                f[2 * e] = e4m3x2_to_f16x2(in[e] & 0xFFFFu);
+                f[2 * e + 1] = e4m3x2_to_f16x2(in[e] >> 16);
+              }
+              if (flip) {
+                store16(swz128(dst, key, u0 + 1), f[4], f[5], f[6], f[7]);
+                store16(swz128(dst, key, u0), f[0], f[1], f[2], f[3]);
+              } else {
+                store16(swz128(dst, key, u0), f[0], f[1], f[2], f[3]);
+                store16(swz128(dst, key, u0 + 1), f[4], f[5], f[6], f[7]);
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar_c_empty(slot));
+            mbar_arrive(bar_v_full(slot));
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 8) {
+    setmaxnreg_dec<C::kRegsOther>();
+  } else {
+    // ------------------------------------------------------------ softmax groups
+    setmaxnreg_inc<C::kRegsSoftmax>();
+    const int g = warp >> 2;
+    const int quarter = warp & 3;                          // TMEM lane quarter this warp may access
+    const int row = quarter * 32 + lane;                   // of the row tile
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const int tok = row / p.G;                             // of the row tile's tokens
+    int tile = 0;                                          // tiles before the segment
+    uint32_t ns[2] = {0, 0}, no = 0, nm = 0;               // parities: S of each buffer, O final, group 1's results
+    bool ok = g < kGroups;
+    Segment s;
+    for (int seg = 0; ok && walk.next<kGroups>(p, s); ++seg) {
+      const int n = s.t1 - s.t0;
+      const int x0 = s.split ? g : 0, dx = s.split ? 2 : 1;            // this group's tiles: x0, x0 + dx, ... below nx
+      const int nx = s.split || g == 1 || kGroups == 1 ? n : s.n0;
+      const int token = s.tok0 + (s.split ? 0 : g * p.tt) + tok;       // counted from the sequence's first new one
+      const bool real = tok < p.tt && token < s.n;
+      const int seen = p.causal ? min(s.len, s.len - s.n + token + 1) : s.len;
+      ok = wait(bar_q_full, seg & 1, abort_flag, p.timeout_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const float sl2 = p.scale_log2 * row_scale[(s.split ? 0 : g * 128) + row];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_q_empty);
+      float ml = -INFINITY, mo = -INFINITY;                // references, log2 units of the logits
+      float l = 0.f;                                       // running sum relative to ml
+      for (int x = x0; x < nx; x += dx) {
+        const int buf = kGroups == 1 ? (tile + x) & 1 : g;
+        ok = wait(bar_info(tile + x), ((tile + x) / kInfo) & 1, abort_flag, p.timeout_ns) &&
+             wait(bar_s_full(buf), kGroups == 1 ? (((tile + x) >> 1) & 1) : ns[0], abort_flag, p.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ns[0] ^= 1;
+        tc_fence_after();
+        const volatile float* const sc = info + ((tile + x) % kInfo) * 8;
+        // (at least the smallest normal number: a K scale of 0 makes 0 of every logit, but would make NaN of the -inf of
+        // keys that are not there)
+        const float ka = fmaxf(sc[0] * sl2, 1.17549435e-38f), kb = fmaxf(sc[4] * sl2, 1.17549435e-38f);
+        const float lva = log2f(sc[1]), lvb = log2f(sc[5]);
+        const uint32_t t_s = tbase + lane_off + C::col_s(buf);
+        const uint32_t t_o = tbase + lane_off + C::col_o(g);
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) tmem_ld_32x32b_x32(t_s + q4 * 32, sr[q4]);
+        const bool whole = sc[2] != 0.f && sc[6] != 0.f;
+        tmem_wait_ld();
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) reg_fence_x32(sr[q4]);
+        float v[128];
+#pragma unroll
+        for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(sr[i >> 5][i & 31]);
+        const int lim = seen - (s.t0 + x) * 128;
+        if (lim < 128 || !whole) {
+          const int la = sc[2] != 0.f ? lim : 0, lb = sc[6] != 0.f ? lim : 0;
+#pragma unroll
+          for (int i = 0; i < 64; ++i) v[i] = i < la ? v[i] : -INFINITY;
+#pragma unroll
+          for (int i = 64; i < 128; ++i) v[i] = i < lb ? v[i] : -INFINITY;
+        }
+        float mk[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float* w = v + 32 * k;
+          float a = fmax3(w[0], w[1], w[2]);
+#pragma unroll
+          for (int e = 3; e < 31; e += 2) a = fmax3(a, w[e], w[e + 1]);
+          mk[k] = fmaxf(a, w[31]);
+        }
+        const float xa = fmaxf(mk[0], mk[1]) * ka, xb = fmaxf(mk[2], mk[3]) * kb;
+        const float xl = fmaxf(xa, xb), xo = fmaxf(xa + lva, xb + lvb);
+        const bool grow_l = xl > ml + kTrailL;             // also true on the first tile with a key (ml = -inf)
+        const bool grow_o = xo > mo + kTrailO;
+        const float ml_new = grow_l ? xl : ml, mo_new = grow_o ? xo - kTopO : mo;
+        const float alpha_l = grow_l ? ex2_approx(ml - ml_new) : 1.f;
+        const float alpha_o = grow_o ? ex2_approx(mo - mo_new) : 1.f;
+        ml = ml_new;
+        mo = mo_new;
+        const float neg_m = ml == -INFINITY ? 0.f : -ml;
+        float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+        for (int h2 = 0; h2 < 2; ++h2) {
+          const float k = h2 ? kb : ka;
+          // V's scale relative to mo (0 where mo is not set: no V so far has a scale)
+          const float f = mo == -INFINITY ? 0.f : ex2_approx(fminf((h2 ? lvb : lva) - neg_m - mo, 126.f));
+          uint32_t pr[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float x0, x1, y0, y1;
+            fma2_bc(x0, x1, v[h2 * 64 + 2 * i], v[h2 * 64 + 2 * i + 1], k, neg_m);
+            const float p0 = ex2_approx(x0);
+            const float p1 = ex2_approx(x1);
+            add2_acc(sum0, sum1, p0, p1);
+            mul2_b(y0, y1, p0, p1, f);
+            pr[i] = pack_f16x2(y0, y1);                    // within 2^-11; l sums P unrounded
+          }
+          tmem_st_32x32b_x32(t_s + h2 * 32, pr);
+        }
+        l = l * alpha_l + (sum0 + sum1);
+        // O <- alpha_o O; the P V before it is done: it was issued before the S just waited for (one group:
+        // before the S of the tile after this one, so it has to be waited for)
+        if (x > x0 && __any_sync(0xffffffffu, grow_o)) {
+          if (kGroups == 1) {
+            const int c = (tile + x) * C::kPerTile - 1;    // V's stage that the product before read last
+            ok = wait(bar_v_empty(c % C::kRingV), (c / C::kRingV) & 1, abort_flag, p.timeout_ns);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+          }
+#pragma unroll
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            if (c0 >= p.c.d) continue;
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(t_o + c0, o);
+            tmem_wait_ld();
+            reg_fence_x32(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha_o);
+            tmem_st_32x32b_x32(t_o + c0, o);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar_p_ready(buf));
+      }
+      if (!ok) break;
+      tile += n;
+      // ---------------------------------------------------------- the item's result
+      if (nx > x0) {
+        ok = wait(bar_o_final(g), no, abort_flag, p.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        no ^= 1;
+        tc_fence_after();
+      }
+      if (s.split && g == 1) {
+        // group 0 joins both: this group's O stays in TMEM until it has
+        other[row] = ml;
+        other[128 + row] = mo;
+        other[256 + row] = l;
+        tc_fence_before();
+        mbar_arrive(bar_other_full);
+        ok = wait(bar_other_empty, nm, abort_flag, p.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        nm ^= 1;
+        tc_fence_after();
+        continue;
+      }
+      float f0 = 1.f, f1 = kNoKey;                         // factors of this group's O and of the other's
+      if (l == 0.f) f0 = kNoKey;
+      if (kGroups == 2 && s.split) {
+        ok = wait(bar_other_full, nm, abort_flag, p.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        nm ^= 1;
+        tc_fence_after();
+        const float ml1 = other[row], mo1 = other[128 + row], l1 = other[256 + row];
+        if (l1 != 0.f) {
+          const float m = fmaxf(ml, ml1), mm = fmaxf(mo, mo1);
+          // (a reference that is not set has nothing summed)
+          l = (l == 0.f ? 0.f : l * ex2_approx(ml - m)) + l1 * ex2_approx(ml1 - m);
+          f0 = f0 == kNoKey ? kNoKey : mo == -INFINITY ? 0.f : ex2_approx(mo - mm);
+          f1 = mo1 == -INFINITY ? 0.f : ex2_approx(mo1 - mm);
+          ml = m;
+          mo = mm;
+        }
+      }
+      const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+      const int head = s.h * p.G + (row - tok * p.G);
+      const long long at = static_cast<long long>(s.row0) + token;
+      const int slot_row = (s.split ? 0 : g * 128) + row;
+      float* part = nullptr;
+      if (whole) {
+        const float factor = l == 0.f ? 0.f : ex2_approx(mo - ml) / l;   // (0 where mo is not set)
+        f0 = f0 == kNoKey ? kNoKey : f0 * factor;
+        f1 = f1 == kNoKey ? kNoKey : f1 * factor;
+        if (real) p.lse[static_cast<long long>(head) * p.T + at] = l == 0.f ? -INFINITY : (ml + log2f(l)) * kLn2;
+      } else {
+        const int slot = 2 * blockIdx.x + (seg == 0 ? 0 : 1);
+        part = p.part_o + static_cast<long long>(slot) * C::kRows * D;
+        float* const st = p.part_s + static_cast<long long>(slot) * C::kRows * 3;
+        if (real) {
+          st[slot_row] = ml;
+          st[C::kRows + slot_row] = mo;
+          st[2 * C::kRows + slot_row] = l;
+        }
+      }
+      __nv_bfloat16* const dst = p.o + head * p.o_sh + at * p.o_st;
+#pragma unroll
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        if (c0 >= p.c.d) continue;
+        uint32_t o[32], o1[32];
+        tmem_ld_32x32b_x32(tbase + lane_off + C::col_o(g) + c0, o);
+        if (kGroups == 2 && s.split) tmem_ld_32x32b_x32(tbase + lane_off + C::col_o(1) + c0, o1);
+        tmem_wait_ld();
+        reg_fence_x32(o);
+        float y[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) y[i] = times_factor(__uint_as_float(o[i]), f0);
+        if (kGroups == 2 && s.split) {
+          reg_fence_x32(o1);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] += times_factor(__uint_as_float(o1[i]), f1);
+        }
+        if (!real) continue;
+        if (whole) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            if (c0 + i < p.c.d)
+              *reinterpret_cast<uint4*>(dst + c0 + i) = make_uint4(pack_bf16x2(y[i], y[i + 1]), pack_bf16x2(y[i + 2], y[i + 3]),
+                                                                   pack_bf16x2(y[i + 4], y[i + 5]), pack_bf16x2(y[i + 6], y[i + 7]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            if (c0 + i < p.c.d)
+              reinterpret_cast<float4*>(part)[((c0 + i) / 4) * C::kRows + slot_row] = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+        }
+      }
+      tc_fence_before();
+      if (kGroups == 2 && s.split) mbar_arrive(bar_other_empty);
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {
+    if (threadIdx.x == 0) atomicOr(p.status, kDevTimeout);
+    abort_grace_period();
+  }
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tbase, 512);
+}
+
+// ------------------------------------------------------------------ second kernel
+// Joins the items whose key tiles went to several parts: CTA (i, rows) those whose second part is i.
+constexpr int kJoinRows = 32;
+constexpr int kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) cache8_chunk_join_kernel(const ChunkParams p) {
+  using C = Cfg<D>;
+  __shared__ int shared[8];
+  const int lane = threadIdx.x & 31, i = blockIdx.x + 1;
+  if (threadIdx.x < 32) {
+    const Line line(p, lane);
+    int c0 = 0, c1 = -1, second = 0;
+    int b = 0, h = 0, item = 0;
+    if (i < line.parts) {
+      const Place place(p, line.turn, line.begin(i), lane);
+      if (place.off > line.turn) {
+        const Sequence s(p, place.b);
+        c0 = line.part_of(place.start + line.turn);
+        c1 = c0 == i - 1 ? line.part_of(place.start + line.turn + s.tiles(p, s.end_of(p, place.item)) - 1) : -1;
+        second = line.begin(c0) >= place.start ? 0 : 1;    // the item is that part's first or not
+        b = place.b;
+        h = place.h;
+        item = place.item;
+      }
+    }
+    if (lane == 0) {
+      shared[0] = c0;
+      shared[1] = c1;
+      shared[2] = second;
+      shared[3] = b;
+      shared[4] = h;
+      shared[5] = item;
+    }
+  }
+  __syncthreads();
+  const int c0 = shared[0], c1 = shared[1];
+  if (c1 < c0) return;
+  const Sequence s(p, shared[3]);
+  const int r = blockIdx.y * kJoinRows + lane;             // row of the item
+  const int group = r >> 7, tok = (r & 127) / p.G;
+  const int token = shared[5] * p.span + group * p.tt + tok;
+  if (tok >= p.tt || token >= s.n) return;
+  auto slot = [&](int c) { return 2LL * c + (c == c0 ? shared[2] : 0); };
+  float ml = -INFINITY, mo = -INFINITY;
+  for (int c = c0; c <= c1; ++c) {
+    const float* const st = p.part_s + slot(c) * C::kRows * 3 + r;
+    if (st[2 * C::kRows] == 0.f) continue;
+    ml = fmaxf(ml, st[0]);
+    mo = fmaxf(mo, st[C::kRows]);
+  }
+  // eight columns at a time
+  constexpr int kWide = D / 8 / (kJoinThreads / 32);       // per thread
+  float4 a[kWide][2];
+#pragma unroll
+  for (int x = 0; x < kWide; ++x) a[x][0] = a[x][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+  for (int c = c0; c <= c1; ++c) {
+    const float* const st = p.part_s + slot(c) * C::kRows * 3 + r;
+    const float lc = st[2 * C::kRows], moc = st[C::kRows];
+    if (lc == 0.f) continue;                               // no key: its O is not there either
+    l += lc * ex2_approx(st[0] - ml);
+    const float f = moc == -INFINITY ? 0.f : ex2_approx(moc - mo);
+    const float4* const o = reinterpret_cast<const float4*>(p.part_o + slot(c) * C::kRows * D);
+#pragma unroll
+    for (int x = 0; x < kWide; ++x) {
+      const int col = 8 * ((threadIdx.x >> 5) + x * (kJoinThreads / 32));
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+        if (col < p.c.d) {
+          const float4 v = o[(col / 4 + y) * C::kRows + r];
+          a[x][y].x = fmaf(v.x, f, a[x][y].x);
+          a[x][y].y = fmaf(v.y, f, a[x][y].y);
+          a[x][y].z = fmaf(v.z, f, a[x][y].z);
+          a[x][y].w = fmaf(v.w, f, a[x][y].w);
+        }
+    }
+  }
+  const int head = shared[4] * p.G + ((r & 127) - tok * p.G);
+  const long long at = static_cast<long long>(s.row0) + token;
+  const float factor = l == 0.f ? 0.f : ex2_approx(mo - ml) / l;
+  if (threadIdx.x < 32) p.lse[static_cast<long long>(head) * p.T + at] = l == 0.f ? -INFINITY : (ml + log2f(l)) * kLn2;
+  __nv_bfloat16* const dst = p.o + head * p.o_sh + at * p.o_st;
+#pragma unroll
+  for (int x = 0; x < kWide; ++x) {
+    const int col = 8 * ((threadIdx.x >> 5) + x * (kJoinThreads / 32));
+    if (col < p.c.d)
+      *reinterpret_cast<uint4*>(dst + col) =
+          make_uint4(pack_bf16x2(a[x][0].x * factor, a[x][0].y * factor), pack_bf16x2(a[x][0].z * factor, a[x][0].w * factor),
+                     pack_bf16x2(a[x][1].x * factor, a[x][1].y * factor), pack_bf16x2(a[x][1].z * factor, a[x][1].w * factor));
+  }
+}
+
+template <int D>
+cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, ChunkParams p, cudaStream_t stream) {
+  using C = Cfg<D>;
+  static PerDeviceOnce attr;
+  const cudaError_t e = attr.run(
+      [] { return cudaFuncSetAttribute(cache8_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem); });
+  if (e != cudaSuccess) return e;
+  p.span = p.tt * C::kGroups;
+  cache8_chunk_kernel<D><<<p.ctas, kThreads, C::kSmem, stream>>>(mk, mv, p);
+  if (p.max_blocks > 2 && p.ctas > 1)                      // (of one key tile nothing is split)
+    cache8_chunk_join_kernel<D><<<dim3(p.ctas - 1, C::kRows / kJoinRows), kJoinThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int chunk_rows(int d) { return d <= 128 ? Cfg<128>::kRows : Cfg<256>::kRows; }
+
+cudaError_t launch_cache8_chunk(const CUtensorMap& mk, const CUtensorMap& mv, const ChunkParams& p, cudaStream_t stream) {
+  return p.c.d <= 128 ? launch<128>(mk, mv, p, stream) : launch<256>(mk, mv, p, stream);
+}
+
+}  // namespace fa

@@ -199,6 +199,27 @@ struct Cache8Params {
   float* scores;                   // with add_weights, else null: [units][64][score_row] log2-scaled scores
   int score_row;                   // rows of a chunk, up to a multiple of 4
 };
+// Chunks of new tokens, packed one sequence behind the other, over the cache (fa_cache8_chunk.cu).
+struct ChunkParams {
+  Cache8Pools c;
+  const __nv_bfloat16* q;          // [Hq, T, d] with strides in elements
+  __nv_bfloat16* o;
+  long long q_sh, q_st, o_sh, o_st;
+  float* lse;                      // [Hq, T]
+  const int* cu;                   // [B + 1] where each sequence's new tokens begin
+  const int* lengths;              // [B] tokens held, the new ones among them
+  const int* table;                // [B, max_blocks]
+  int B, T, max_blocks;
+  int G, tt;                       // query heads per KV head; tokens of a row tile, 128 / G
+  int span;                        // tokens of an item (set at the launch)
+  int causal, ctas;
+  float scale_log2;
+  unsigned* status;                // device status word
+  unsigned long long timeout_ns;   // bound on every wait inside the kernel
+  int test_stall;                  // 1: the issuer first waits on a barrier nothing arrives on (timeout test)
+  float* part_o;                   // partial results: [2 ctas][D / 4][rows of an item][4] and [2 ctas][3][rows]
+  float* part_s;
+};
 struct Cache8EvictParams {
   Cache8Pools c;
   const int* table;
@@ -216,6 +237,8 @@ int cache8_parts(int B, int Hkv, int d, int R, int max_blocks);   // CTAs, parts
 cudaError_t launch_cache8_append(const Cache8AppendParams& p, cudaStream_t stream);
 // maps over the codes as [num_blocks * Hkv, 64, d], boxes of 64 rows by 128 bytes
 cudaError_t launch_cache8_fwd(const CUtensorMap& mk, const CUtensorMap& mv, Cache8Params p, cudaStream_t stream);
+int chunk_rows(int d);                // rows of an item of the chunks' attention
+cudaError_t launch_cache8_chunk(const CUtensorMap& mk, const CUtensorMap& mv, const ChunkParams& p, cudaStream_t stream);
 cudaError_t launch_cache8_evict(const Cache8EvictParams& p, cudaStream_t stream);
 
 }  // namespace fa

@@ -440,6 +440,32 @@ fa_status fa_fwd_cache8(const void* q, const fa_cache8* cache, const int* block_
                         const int* lengths, void* o, float* lse, void* workspace, size_t workspace_bytes, int B,
                         int Hq, int Nq, int causal, float scale, int add_weights, float weight_decay, void* stream);
 
+/* Attention over the cache for chunks of new tokens, as many in each sequence as
+ * there are: q, o bf16 [Hq, T, d] with strides in elements between heads and
+ * between tokens (multiples of 8, at least d; the d values of a row contiguous), apart
+ * from one another; rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (device int32 [B + 1], not
+ * decreasing, within 0 .. T) are the last positions of sequence b, which holds
+ * lengths[b] tokens (device int32 [B]), the new ones among them: they have been
+ * appended before. Row i of a chunk of n sees key j iff j < lengths[b] and, when
+ * causal, j <= i + lengths[b] - n; a row that sees none gets O = 0, lse = -inf. lse
+ * fp32 [Hq, T]. Rows of no sequence are left as they were, in o and in lse; a sequence
+ * may have no new tokens. Hq / Hkv <= 128 and T <= 2^30 (FA_ERR_UNSUPPORTED above). K's
+ * codes enter the products as they are; Q to the bit down to 2^-9 of a row's largest
+ * value (smaller ones are off by at most 2^-17 of it); each P (times its block's V scale)
+ * within 2^-11 of itself plus 2^-31 of the row's largest; probabilities below
+ * 2^-126 of the largest count as 0; sums are fp32. A NaN among the V
+ * values of a tile of 128 keys that a row tile looks at reaches all its rows.
+ * workspace: fa_fwd_cache8_packed_workspace_bytes(B, T, Hq, Hkv, d, max_blocks)
+ * bytes (40 MB; 256 says that a table of one or two blocks needs none, NULL will do), 256-byte aligned,
+ * contents before and after of no meaning; calls that may overlap on the GPU need
+ * one each. 0 for sizes that it refuses. Two launches. Every call gives the same
+ * bits. fa_fwd_cache8 is the call for single tokens, and the one that adds up weights. */
+size_t fa_fwd_cache8_packed_workspace_bytes(int B, int T, int Hq, int Hkv, int d, int max_blocks);
+fa_status fa_fwd_cache8_packed(const void* q, long long q_stride_h, long long q_stride_t, const fa_cache8* cache,
+                               const int* block_table, int max_blocks, const int* cu_seqlens, const int* lengths, void* o,
+                               long long o_stride_h, long long o_stride_t, float* lse, void* workspace,
+                               size_t workspace_bytes, int B, int T, int Hq, int causal, float scale, void* stream);
+
 /* Evict: of each sequence's tokens, per KV head, keep at most `keep`: the last
  * `recent` (0 <= recent <= keep) and of the others those with the largest
  * weight (a NaN counts as the largest; ties go to the earlier token), in their
