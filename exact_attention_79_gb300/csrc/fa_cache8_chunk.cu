@@ -39,6 +39,7 @@ constexpr float kTrailL = 8.f;            // log2 of how far the references may 
 constexpr float kTopO = 7.f, kTrailO = 15.f;   // P' of the row's largest is 2^7 where mo is set, at most 2^15
 constexpr float kNoKey = -1.f;            // factor of O for a row that sees no key
 constexpr int kInfo = 8;                  // tiles whose scales wait in shared memory
+constexpr int kStateInts = 20;            // a softmax warp's place on the line and its segment, kept in shared memory
 constexpr int kTurn = 1;                  // key tiles' time that a change of items costs
 
 template <int D>
@@ -57,12 +58,12 @@ struct Cfg {
   static constexpr int kBoxV = kKeysV * 128;               // 64 columns of halves
   static constexpr int kOffK = kQBytes, kOffCodes = kOffK + kRingK * kTileK, kOffHalf = kOffCodes + kRingV * kCodesV;
   static constexpr int kOffStat = kOffHalf + kRingV * kHalfV;
-  static constexpr int kStat = kRows * 4 + (kGroups == 2 ? 128 * 12 : 0) + kInfo * 32;
+  static constexpr int kStat = kRows * 4 + (kGroups == 2 ? 128 * 12 : 0) + kInfo * 32 + (4 * kGroups + 1) * kStateInts * 4;
   static constexpr int kLayout = kOffStat + kStat + 272;
   static constexpr int kSmem = kLayout + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
-  // setmaxnreg: 256 x 184 + 256 x 72 = 512 x 128
-  static constexpr uint32_t kRegsSoftmax = 184, kRegsOther = 72;
+  // setmaxnreg, of the 512 x 128 launched: without spills, which L1 beside so much shared memory does not hold
+  static constexpr uint32_t kRegsSoftmax = D == 128 ? 192 : 184, kRegsOther = 256 - kRegsSoftmax;
   static __device__ __forceinline__ uint32_t col_s(int i) { return 128u * i; }
   static __device__ __forceinline__ uint32_t col_o(int i) { return 256u + 128u * i; }
 };
@@ -234,6 +235,30 @@ struct Walk {
   __device__ __forceinline__ Walk(const ChunkParams& p, const volatile int* at)
       : b(at[0]), h(at[1]), item(at[2]), off(at[3]), turn(at[4]),
         left(static_cast<long long>(static_cast<unsigned>(at[5])) | static_cast<long long>(at[6]) << 32), s(p, at[0]) {}
+  // to and from ten ints of shared memory
+  __device__ __forceinline__ void save(volatile int* m) const {
+    m[0] = b;
+    m[1] = h;
+    m[2] = item;
+    m[3] = off;
+    m[4] = turn;
+    m[5] = static_cast<int>(left);
+    m[6] = static_cast<int>(left >> 32);
+    m[7] = s.row0;
+    m[8] = s.n;
+    m[9] = s.len;
+  }
+  __device__ __forceinline__ void restore(const volatile int* m) {
+    b = m[0];
+    h = m[1];
+    item = m[2];
+    off = m[3];
+    turn = m[4];
+    left = static_cast<long long>(static_cast<unsigned>(m[5])) | static_cast<long long>(m[6]) << 32;
+    s.row0 = m[7];
+    s.n = m[8];
+    s.len = m[9];
+  }
   template <int kGroups>
   __device__ __forceinline__ bool next(const ChunkParams& p, Segment& g) {
     if (left <= 0) return false;
@@ -307,7 +332,8 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   auto s_half = [&](int i) { return base + C::kOffHalf + i * C::kHalfV; };
   float* const row_scale = reinterpret_cast<float*>(gbase + C::kOffStat);           // [kRows] what Q's rows were divided by
   float* const other = row_scale + C::kRows;                                       // [3][128] group 1's ml, mo, l (split)
-  volatile float* const info = reinterpret_cast<volatile float*>(other + (kGroups == 2 ? 3 * 128 : 0));   // [kInfo][8]: per half K scale, V scale, there
+  volatile float* const info = reinterpret_cast<volatile float*>(other + (kGroups == 2 ? 3 * 128 : 0));   // [kInfo][8]: per half K scale, log2 of V's, there
+  volatile int* const states = reinterpret_cast<volatile int*>(gbase + C::kOffStat + C::kStat - (4 * kGroups + 1) * kStateInts * 4);
   const uint32_t bars = base + C::kOffStat + C::kStat;
   uint8_t* const gbars = gbase + (bars - base);
   auto bar_k_full = [&](int i) { return bars + 8u * i; };              // 3
@@ -421,7 +447,7 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           if (lane == i || lane == i + 1) {
             volatile float* const dst = info + (tile % kInfo) * 8 + (lane - i) * 4;
             dst[0] = ks;
-            dst[1] = vs;
+            dst[1] = log2f(vs);
             dst[2] = page >= 0 ? 1.f : 0.f;
           }
           __syncwarp();
@@ -455,91 +481,117 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     if (lane == 0) {
       const uint32_t id_s = make_idesc(0, 128, 128, 0, 0);             // e4m3, both K-major
       const uint32_t id_o = make_idesc(0, 128, p.c.d, 0, 1);           // f16, V MN-major
+      // The issuing thread paces the kernel (a product takes 64 cycles): descriptors are stepped, slots and parities
+      // counted along, and at full width the products stand in a row.
       const int steps = (p.c.d + 31) / 32;                             // products over d that are not all zeros
+      const uint64_t kd0 = smem_desc_sw128(s_k(0), 16, 1024), qd0 = smem_desc_sw128(s_q(0, 0), 16, 1024);
+      const uint64_t vd0 = smem_desc_sw128(s_half(0), C::kBoxV, 1024);
       bool ok = !p.test_stall || wait(bar_stall, 0, abort_flag, p.timeout_ns);   // runs out by design
-      int tile = 0, seg = 0;                                           // tiles before the segment, segments
-      uint32_t np[2] = {0, 0};                                         // P-ready phases of each buffer
-      // S of rows `group` with tile `t` into buffer `buf`
-      auto scores = [&](int buf, int group, int t, bool last_user) {
-        const int slot = t % C::kRingK;
-        ok = wait(bar_k_full(slot), (t / C::kRingK) & 1, abort_flag, p.timeout_ns);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t kd = smem_desc_sw128(s_k(slot), 16, 1024);
-#pragma unroll
-        for (int term = 0; term < 2; ++term) {
-          const uint64_t qd = smem_desc_sw128(s_q(group, term), 16, 1024);
-          for (int k = 0; k < steps; ++k) {
-            const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-            mma_fp8_ss(tbase + C::col_s(buf), desc_add(qd, off), desc_add(kd, off), id_s, term > 0 || k > 0);
-          }
-        }
-        mma_commit(bar_s_full(buf));
-        if (last_user) mma_commit(bar_k_empty(slot));
-      };
-      // O of `group` += P in buffer `buf` times V of tile `t`
-      auto product = [&](int buf, int group, int t, bool acc, bool last_user) {
-        ok = wait(bar_p_ready(buf), np[buf], abort_flag, p.timeout_ns);
-        if (!ok) return;
-        np[buf] ^= 1;
-#pragma unroll
-        for (int x = 0; x < C::kPerTile; ++x) {
-          const int c = t * C::kPerTile + x, slot = c % C::kRingV;
-          ok = wait(bar_v_full(slot), (c / C::kRingV) & 1, abort_flag, p.timeout_ns);
+      int seg = 0;
+      uint32_t np = 0;                                                 // parities of the buffers' P-ready
+      [[maybe_unused]] int buf = 1;                                    // one group: S's buffer of the last tile
+      int k_slot = 0, v_slot = 0;                                      // of the next tile for S, of the next V stage
+      uint32_t k_par = 0, v_par = 0;
+      // S of rows `group` with K of k_slot into buffer `buf`; the last user of the tile hands it back and steps on
+      auto scores = [&](int buf, int group, bool first_user, bool last_user) {
+        if (first_user) {
+          ok = wait(bar_k_full(k_slot), k_par, abort_flag, p.timeout_ns);
           if (!ok) return;
           tc_fence_after();
-          const uint64_t vd = smem_desc_sw128(s_half(slot), C::kBoxV, 1024);
+        }
+        const uint64_t kd = kd0 + static_cast<uint32_t>(k_slot * (C::kTileK >> 4));
+        const uint64_t qd = qd0 + static_cast<uint32_t>(group * (2 * C::kQTerm >> 4));
+        const uint32_t dst = tbase + C::col_s(buf);
+        if (steps == 4 * C::kCh) {
 #pragma unroll
-          for (int k = 0; k < C::kKeysV / 16; ++k)
-            mma_bf16_ts(tbase + C::col_o(group), tbase + C::col_s(buf) + (x * (C::kKeysV / 16) + k) * 8, desc_add(vd, k * 2048), id_o,
-                        acc || x > 0 || k > 0);
-          if (last_user) mma_commit(bar_v_empty(slot));
+          for (int i = 0; i < 8 * C::kCh; ++i) {
+            const int term = i / (4 * C::kCh), k = i % (4 * C::kCh), off = (k >> 2) * 16384 + (k & 3) * 32;
+            mma_fp8_ss(dst, desc_add(qd, term * C::kQTerm + off), desc_add(kd, off), id_s, i > 0);
+          }
+        } else {
+          for (int term = 0; term < 2; ++term)
+            for (int k = 0; k < steps; ++k) {
+              const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
+              mma_fp8_ss(dst, desc_add(qd, term * C::kQTerm + off), desc_add(kd, off), id_s, term > 0 || k > 0);
+            }
+        }
+        mma_commit(bar_s_full(buf));
+        if (last_user) {
+          mma_commit(bar_k_empty(k_slot));
+          if (++k_slot == C::kRingK) {
+            k_slot = 0;
+            k_par ^= 1;
+          }
         }
       };
-      Segment s;
-      for (; ok && walk.next<kGroups>(p, s); ++seg) {
-        const int n = s.t1 - s.t0;
+      // O of `group` += P in buffer `buf` times V of the tile
+      auto product = [&](int buf, int group, bool acc, bool first_user, bool last_user) {
+        ok = wait(bar_p_ready(buf), np >> buf & 1u, abort_flag, p.timeout_ns);
+        if (!ok) return;
+        np ^= 1u << buf;
+#pragma unroll
+        for (int x = 0; x < C::kPerTile; ++x) {
+          if (first_user) {
+            ok = wait(bar_v_full(v_slot), v_par, abort_flag, p.timeout_ns);
+            if (!ok) return;
+          }
+          tc_fence_after();
+          const uint64_t vd = vd0 + static_cast<uint32_t>(v_slot * (C::kHalfV >> 4));
+          const uint32_t src = tbase + C::col_s(buf) + x * (C::kKeysV / 2);
+#pragma unroll
+          for (int k = 0; k < C::kKeysV / 16; ++k)
+            mma_bf16_ts(tbase + C::col_o(group), src + k * 8, desc_add(vd, k * 2048), id_o, acc || x > 0 || k > 0);
+          if (last_user) {
+            mma_commit(bar_v_empty(v_slot));
+            if (++v_slot == C::kRingV) {
+              v_slot = 0;
+              v_par ^= 1;
+            }
+          }
+        }
+      };
+      volatile int* const state = states + 4 * kGroups * kStateInts;
+      walk.save(state);
+      for (;; ++seg) {
+        int n, n0;
+        bool split;
+        {
+          Segment s;
+          Walk w = walk;
+          w.restore(state);
+          if (!ok || !w.next<kGroups>(p, s)) break;
+          w.save(state);
+          n = s.t1 - s.t0;
+          n0 = s.n0;
+          split = s.split;
+        }
         ok = wait(bar_q_full, seg & 1, abort_flag, p.timeout_ns);
         if (!ok) break;
         if (kGroups == 1) {
-          scores(tile & 1, 0, tile, true);
-          for (int j = 0; j < n && ok; ++j) {
-            if (j + 1 < n) scores((tile + j + 1) & 1, 0, tile + j + 1, true);
+          // S of the next tile is out before this one's P V
+          for (int j = -1; j < n && ok; ++j) {
+            if (j + 1 < n) scores(buf ^ 1, 0, true, true);
             else mma_commit(bar_q_empty);
-            if (ok) product((tile + j) & 1, 0, tile + j, j > 0, true);
+            if (ok && j >= 0) product(buf, 0, j > 0, true, true);
+            if (j + 1 < n) buf ^= 1;
           }
           if (ok) mma_commit(bar_o_final(0));
-        } else if (s.split) {
-          for (int x = 0; x < min(n, 2) && ok; ++x) scores(x, 0, tile + x, true);
-          if (n <= 2) mma_commit(bar_q_empty);
-          for (int x = 0; x < n && ok; ++x) {
-            const int g = x & 1;
-            product(g, g, tile + x, x > 1, true);
-            if (!ok) break;
-            if (x + 2 < n) scores(g, 0, tile + x + 2, true);
-            else mma_commit(bar_o_final(g));
-            if (x + 3 == n) mma_commit(bar_q_empty);
-          }
         } else {
-          if (s.n0 > 0) scores(0, 0, tile, false);
-          if (ok) scores(1, 1, tile, true);
-          if (n == 1) mma_commit(bar_q_empty);
-          for (int j = 0; j < n && ok; ++j) {
-            if (j < s.n0) {
-              product(0, 0, tile + j, j > 0, false);
-              if (!ok) break;
-              if (j + 1 < s.n0) scores(0, 0, tile + j + 1, false);
-              else mma_commit(bar_o_final(0));
-              if (!ok) break;
-            }
-            product(1, 1, tile + j, j > 0, true);
+          // Step i is group i & 1's P V of a tile and its S of the next one: split, tile i, then i + 2; else tile
+          // i / 2 of either group, then the one behind it. The first two steps have no P V yet.
+          const int steps_all = split ? n : 2 * n;
+          for (int i = -2; i < steps_all && ok; ++i) {
+            const int gr = i & 1, j = split ? i : i >> 1;
+            const int mine = split || gr ? n : n0, next_j = split ? i + 2 : j + 1;
+            const bool last = split || gr;
+            if (j >= mine) continue;
+            if (i >= 0) product(gr, gr, split ? i > 1 : j > 0, split || !gr || j >= n0, last);
             if (!ok) break;
-            if (j + 1 < n) scores(1, 1, tile + j + 1, true);
-            else mma_commit(bar_o_final(1));
-            if (j + 2 == n) mma_commit(bar_q_empty);
+            if (next_j < mine) scores(gr, split ? 0 : gr, split || !gr || next_j >= n0, last);
+            else if (i >= 0) mma_commit(bar_o_final(gr));
+            if (last && next_j + 1 == n) mma_commit(bar_q_empty);      // every S is out
           }
         }
-        tile += n;
       }
     }
     __syncwarp();
@@ -671,54 +723,77 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     const int quarter = warp & 3;                          // TMEM lane quarter this warp may access
     const int row = quarter * 32 + lane;                   // of the row tile
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const int tok = row / p.G;                             // of the row tile's tokens
-    int tile = 0;                                          // tiles before the segment
-    uint32_t ns[2] = {0, 0}, no = 0, nm = 0;               // parities: S of each buffer, O final, group 1's results
+    volatile int* const state = states + (warp & (4 * kGroups - 1)) * kStateInts;   // (registers hold a tile of S)
+    uint32_t par = 0;                                      // parities: bit 0 S, 1 O final, 2 group 1's results, 3 Q; 4: not the first segment
     bool ok = g < kGroups;
-    Segment s;
-    for (int seg = 0; ok && walk.next<kGroups>(p, s); ++seg) {
-      const int n = s.t1 - s.t0;
-      const int x0 = s.split ? g : 0, dx = s.split ? 2 : 1;            // this group's tiles: x0, x0 + dx, ... below nx
-      const int nx = s.split || g == 1 || kGroups == 1 ? n : s.n0;
-      const int token = s.tok0 + (s.split ? 0 : g * p.tt) + tok;       // counted from the sequence's first new one
-      const bool real = tok < p.tt && token < s.n;
-      const int seen = p.causal ? min(s.len, s.len - s.n + token + 1) : s.len;
-      ok = wait(bar_q_full, seg & 1, abort_flag, p.timeout_ns);
+    if (ok) {
+      walk.save(state);
+      state[17] = 0;                                       // tiles before the segment
+    }
+    while (ok) {
+      uint32_t at, end;                                    // this group's tiles at, at + dx, ... below end, counted from the kernel's start
+      int dx, lim;                                         // lim: keys that this row sees from the tile on
+      {
+        Segment s;
+        Walk w = walk;
+        __syncwarp();
+        w.restore(state);
+        if (!w.next<kGroups>(p, s)) break;
+        __syncwarp();
+        w.save(state);
+        state[10] = s.h;
+        state[11] = s.row0;
+        state[12] = s.n;
+        state[13] = s.tok0;
+        state[16] = s.t0 == 0 && s.t1 == s.tiles;
+        const uint32_t tile = state[17];
+        __syncwarp();
+        state[17] = tile + s.t1 - s.t0;
+        const int x = s.split ? g : 0;
+        dx = s.split ? 2 : 1;
+        at = tile + x;
+        end = tile + (s.split || g == 1 || kGroups == 1 ? s.t1 - s.t0 : s.n0);
+        const int last = s.tok0 + (s.split ? 0 : g * p.tt) + row / p.G + 1;   // tokens up to this row's
+        lim = (p.causal ? min(s.len, s.len - s.n + last) : s.len) - (s.t0 + x) * 128;
+      }
+      const bool any = at < end, split = dx == 2;
+      ok = wait(bar_q_full, par >> 3 & 1u, abort_flag, p.timeout_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const float sl2 = p.scale_log2 * row_scale[(s.split ? 0 : g * 128) + row];
+      par ^= 8u;
+      const float sl2 = p.scale_log2 * row_scale[(split ? 0 : g * 128) + row];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_q_empty);
+      bool rescale = false;                                // O holds something
       float ml = -INFINITY, mo = -INFINITY;                // references, log2 units of the logits
       float l = 0.f;                                       // running sum relative to ml
-      for (int x = x0; x < nx; x += dx) {
-        const int buf = kGroups == 1 ? (tile + x) & 1 : g;
-        ok = wait(bar_info(tile + x), ((tile + x) / kInfo) & 1, abort_flag, p.timeout_ns) &&
-             wait(bar_s_full(buf), kGroups == 1 ? (((tile + x) >> 1) & 1) : ns[0], abort_flag, p.timeout_ns);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        ns[0] ^= 1;
-        tc_fence_after();
-        const volatile float* const sc = info + ((tile + x) % kInfo) * 8;
+      for (; at < end; at += dx, lim -= 128 * dx) {
+        const int buf = kGroups == 1 ? at & 1 : g;
+        ok = wait(bar_info(at), (at / kInfo) & 1, abort_flag, p.timeout_ns);
+        const volatile float* const sc = info + (at % kInfo) * 8;
         // (at least the smallest normal number: a K scale of 0 makes 0 of every logit, but would make NaN of the -inf of
         // keys that are not there)
         const float ka = fmaxf(sc[0] * sl2, 1.17549435e-38f), kb = fmaxf(sc[4] * sl2, 1.17549435e-38f);
-        const float lva = log2f(sc[1]), lvb = log2f(sc[5]);
+        const float lva = sc[1], lvb = sc[5];
+        const bool here_a = sc[2] != 0.f, here_b = sc[6] != 0.f;
+        if (ok) ok = wait(bar_s_full(buf), kGroups == 1 ? at >> 1 & 1u : par & 1u, abort_flag, p.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        par ^= 1u;
+        tc_fence_after();
         const uint32_t t_s = tbase + lane_off + C::col_s(buf);
         const uint32_t t_o = tbase + lane_off + C::col_o(g);
         uint32_t sr[4][32];
 #pragma unroll
         for (int q4 = 0; q4 < 4; ++q4) tmem_ld_32x32b_x32(t_s + q4 * 32, sr[q4]);
-        const bool whole = sc[2] != 0.f && sc[6] != 0.f;
         tmem_wait_ld();
 #pragma unroll
         for (int q4 = 0; q4 < 4; ++q4) reg_fence_x32(sr[q4]);
         float v[128];
 #pragma unroll
         for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(sr[i >> 5][i & 31]);
-        const int lim = seen - (s.t0 + x) * 128;
-        if (lim < 128 || !whole) {
-          const int la = sc[2] != 0.f ? lim : 0, lb = sc[6] != 0.f ? lim : 0;
+        if (lim < 128 || !here_a || !here_b) {
+          const int la = here_a ? lim : 0, lb = here_b ? lim : 0;
 #pragma unroll
           for (int i = 0; i < 64; ++i) v[i] = i < la ? v[i] : -INFINITY;
 #pragma unroll
@@ -765,9 +840,9 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         l = l * alpha_l + (sum0 + sum1);
         // O <- alpha_o O; the P V before it is done: it was issued before the S just waited for (one group:
         // before the S of the tile after this one, so it has to be waited for)
-        if (x > x0 && __any_sync(0xffffffffu, grow_o)) {
+        if (rescale && __any_sync(0xffffffffu, grow_o)) {
           if (kGroups == 1) {
-            const int c = (tile + x) * C::kPerTile - 1;    // V's stage that the product before read last
+            const uint32_t c = at * C::kPerTile - 1;       // V's stage that the product before read last
             ok = wait(bar_v_empty(c % C::kRingV), (c / C::kRingV) & 1, abort_flag, p.timeout_ns);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -785,40 +860,41 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
             tmem_st_32x32b_x32(t_o + c0, o);
           }
         }
+        rescale = true;
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(bar_p_ready(buf));
       }
       if (!ok) break;
-      tile += n;
       // ---------------------------------------------------------- the item's result
-      if (nx > x0) {
-        ok = wait(bar_o_final(g), no, abort_flag, p.timeout_ns);
+      if (any) {
+        ok = wait(bar_o_final(g), par >> 1 & 1u, abort_flag, p.timeout_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        no ^= 1;
+        par ^= 2u;
         tc_fence_after();
       }
-      if (s.split && g == 1) {
+      if (split && g == 1) {
         // group 0 joins both: this group's O stays in TMEM until it has
         other[row] = ml;
         other[128 + row] = mo;
         other[256 + row] = l;
         tc_fence_before();
         mbar_arrive(bar_other_full);
-        ok = wait(bar_other_empty, nm, abort_flag, p.timeout_ns);
+        ok = wait(bar_other_empty, par >> 2 & 1u, abort_flag, p.timeout_ns);
         ok = __all_sync(0xffffffffu, ok);
-        nm ^= 1;
+        par ^= 4u;
         tc_fence_after();
+        par |= 16u;
         continue;
       }
       float f0 = 1.f, f1 = kNoKey;                         // factors of this group's O and of the other's
       if (l == 0.f) f0 = kNoKey;
-      if (kGroups == 2 && s.split) {
-        ok = wait(bar_other_full, nm, abort_flag, p.timeout_ns);
+      if (kGroups == 2 && split) {
+        ok = wait(bar_other_full, par >> 2 & 1u, abort_flag, p.timeout_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        nm ^= 1;
+        par ^= 4u;
         tc_fence_after();
         const float ml1 = other[row], mo1 = other[128 + row], l1 = other[256 + row];
         if (l1 != 0.f) {
@@ -831,18 +907,20 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           mo = mm;
         }
       }
-      const bool whole = s.t0 == 0 && s.t1 == s.tiles;
-      const int head = s.h * p.G + (row - tok * p.G);
-      const long long at = static_cast<long long>(s.row0) + token;
-      const int slot_row = (s.split ? 0 : g * 128) + row;
+      const bool whole = state[16];
+      const int tok = row / p.G, token = state[13] + (split ? 0 : g * p.tt) + tok;   // counted from the sequence's first new one
+      const bool real = tok < p.tt && token < state[12];
+      const int head = state[10] * p.G + (row - tok * p.G);
+      const long long at_row = static_cast<long long>(state[11]) + token;
+      const int slot_row = (split ? 0 : g * 128) + row;
       float* part = nullptr;
       if (whole) {
         const float factor = l == 0.f ? 0.f : ex2_approx(mo - ml) / l;   // (0 where mo is not set)
         f0 = f0 == kNoKey ? kNoKey : f0 * factor;
         f1 = f1 == kNoKey ? kNoKey : f1 * factor;
-        if (real) p.lse[static_cast<long long>(head) * p.T + at] = l == 0.f ? -INFINITY : (ml + log2f(l)) * kLn2;
+        if (real) p.lse[static_cast<long long>(head) * p.T + at_row] = l == 0.f ? -INFINITY : (ml + log2f(l)) * kLn2;
       } else {
-        const int slot = 2 * blockIdx.x + (seg == 0 ? 0 : 1);
+        const int slot = 2 * blockIdx.x + (par >> 4);
         part = p.part_o + static_cast<long long>(slot) * C::kRows * D;
         float* const st = p.part_s + static_cast<long long>(slot) * C::kRows * 3;
         if (real) {
@@ -851,19 +929,19 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           st[2 * C::kRows + slot_row] = l;
         }
       }
-      __nv_bfloat16* const dst = p.o + head * p.o_sh + at * p.o_st;
+      __nv_bfloat16* const dst = p.o + head * p.o_sh + at_row * p.o_st;
 #pragma unroll
       for (int c0 = 0; c0 < D; c0 += 32) {
         if (c0 >= p.c.d) continue;
         uint32_t o[32], o1[32];
         tmem_ld_32x32b_x32(tbase + lane_off + C::col_o(g) + c0, o);
-        if (kGroups == 2 && s.split) tmem_ld_32x32b_x32(tbase + lane_off + C::col_o(1) + c0, o1);
+        if (kGroups == 2 && split) tmem_ld_32x32b_x32(tbase + lane_off + C::col_o(1) + c0, o1);
         tmem_wait_ld();
         reg_fence_x32(o);
         float y[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) y[i] = times_factor(__uint_as_float(o[i]), f0);
-        if (kGroups == 2 && s.split) {
+        if (kGroups == 2 && split) {
           reg_fence_x32(o1);
 #pragma unroll
           for (int i = 0; i < 32; ++i) y[i] += times_factor(__uint_as_float(o1[i]), f1);
@@ -883,7 +961,8 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         }
       }
       tc_fence_before();
-      if (kGroups == 2 && s.split) mbar_arrive(bar_other_empty);
+      if (kGroups == 2 && split) mbar_arrive(bar_other_empty);
+      par |= 16u;
     }
   }
 
