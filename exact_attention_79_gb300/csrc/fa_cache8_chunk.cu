@@ -27,8 +27,10 @@
 // gives its even key tiles to one softmax group and its odd ones to the other, joined in TMEM.
 //
 // Warps: 0-3 and 4-7 the softmax groups (one thread per row), 8 producer (block table, scales,
-// TMA), 9 tensor-core issuer, 12-15 converters. At d > 128 (kGroups = 1) O takes half of TMEM, S is
+// TMA), 9 tensor-core issuer, 10 ring watcher, 12-15 converters. At d > 128 (kGroups = 1) O takes half of TMEM, S is
 // double-buffered and warps 4-7 rest.
+#include <type_traits>
+
 #include "fa_cache8.cuh"
 
 namespace fa {
@@ -59,7 +61,7 @@ struct Cfg {
   static constexpr int kOffK = kQBytes, kOffCodes = kOffK + kRingK * kTileK, kOffHalf = kOffCodes + kRingV * kCodesV;
   static constexpr int kOffStat = kOffHalf + kRingV * kHalfV;
   static constexpr int kStat = kRows * 4 + (kGroups == 2 ? 128 * 12 : 0) + kInfo * 32 + (4 * kGroups + 1) * kStateInts * 4;
-  static constexpr int kLayout = kOffStat + kStat + 272;
+  static constexpr int kLayout = kOffStat + kStat + 208;
   static constexpr int kSmem = kLayout + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   // setmaxnreg, of the 512 x 128 launched: without spills, which L1 beside so much shared memory does not hold
@@ -347,10 +349,9 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   auto bar_o_final = [&](int i) { return bars + 144u + 8u * i; };
   const uint32_t bar_q_full = bars + 160u, bar_q_empty = bars + 168u;
   const uint32_t bar_other_full = bars + 176u, bar_other_empty = bars + 184u;
-  auto bar_info = [&](int t) { return bars + 192u + 8u * (t % kInfo); };
-  const uint32_t bar_stall = bars + 256u;                              // nothing arrives (timeout test)
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbars + 264);
-  volatile int* const abort_flag = reinterpret_cast<volatile int*>(gbars + 268);
+  const uint32_t bar_stall = bars + 192u;                              // nothing arrives (timeout test)
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbars + 200);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(gbars + 204);
   volatile int* const first = reinterpret_cast<volatile int*>(row_scale);          // [7] the part's first place, until the roles begin
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -366,14 +367,13 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       mbar_init(bar_v_full(i), 4);
       mbar_init(bar_v_empty(i), 1);
       mbar_init(bar_s_full(i), 1);
-      mbar_init(bar_p_ready(i), 128);
+      mbar_init(bar_p_ready(i), kGroups == 2 ? 129 : 128);   // + the watcher
       mbar_init(bar_o_final(i), 1);
     }
     mbar_init(bar_q_full, 4);
     mbar_init(bar_q_empty, 1 + 4 * kGroups);               // its products done, its scales read by every softmax warp
     mbar_init(bar_other_full, 128);
     mbar_init(bar_other_empty, 128);
-    for (int i = 0; i < kInfo; ++i) mbar_init(bar_info(i), 1);
     mbar_init(bar_stall, 1);
     fence_mbar_init();
   }
@@ -418,41 +418,48 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     Segment s;
     while (ok && walk.next<kGroups>(p, s)) {
       const int* const table = p.table + static_cast<long long>(s.b) * p.max_blocks;
-      const int held = (s.len + kCacheBlock - 1) / kCacheBlock;
-      for (int blk = 2 * s.t0; blk < 2 * s.t1 && ok; blk += 32) {
-        // 32 blocks at a time, one per lane
-        const int mine = blk + lane;
-        int page = mine < 2 * s.t1 && mine < held ? table[mine] : -1;
-        if (page >= p.c.num_blocks) page = -1;
+      const int held = min(2 * s.t1, (s.len + kCacheBlock - 1) / kCacheBlock);
+      // 32 blocks at a time, one per lane; the next 32 are looked up while these are loaded
+      auto page_of = [&](int blk) {
+        const int page = blk + lane < held ? table[blk + lane] : -1;
+        return page < p.c.num_blocks ? page : -1;
+      };
+      float ks = 0.f, vs = 0.f;
+      int z = -1;
+      auto scales_of = [&](int page) {
         const long long ph = page >= 0 ? static_cast<long long>(page) * p.c.Hkv + s.h : -1;
-        const float ks = page >= 0 ? p.c.k_scale[ph] : 0.f, vs = page >= 0 ? p.c.v_scale[ph] : 0.f;
-        const int z = static_cast<int>(ph);
+        ks = page >= 0 ? p.c.k_scale[ph] : 0.f;
+        vs = page >= 0 ? p.c.v_scale[ph] : 0.f;
+        z = static_cast<int>(ph);
+      };
+      scales_of(page_of(2 * s.t0));
+      for (int blk = 2 * s.t0; blk < 2 * s.t1 && ok; blk += 32) {
+        const float ks_now = ks, vs_now = vs;
+        const int z_now = z, next_page = page_of(blk + 32);
         for (int i = 0; i < 32 && blk + i < 2 * s.t1 && ok; i += 2, ++tile) {
-          const int za = __shfl_sync(0xffffffffu, z, i), zb = __shfl_sync(0xffffffffu, z, i + 1);
+          const int za = __shfl_sync(0xffffffffu, z_now, i), zb = __shfl_sync(0xffffffffu, z_now, i + 1);
+          const int slot = tile % C::kRingK;
           if (lane == 0) {
-            const int slot = tile % C::kRingK;
             ok = wait(bar_k_empty(slot), ((tile / C::kRingK) & 1) ^ 1, abort_flag, p.timeout_ns);
-            if (ok) {
-              mbar_arrive_expect_tx(bar_k_full(slot), ((za >= 0) + (zb >= 0)) * 8192 * C::kCh);
-              for (int ch = 0; ch < C::kCh; ++ch) {
-                if (za >= 0) tma_load_3d(s_k(slot) + ch * 16384, &map_k, bar_k_full(slot), ch * 128, 0, za);
-                if (zb >= 0) tma_load_3d(s_k(slot) + ch * 16384 + 8192, &map_k, bar_k_full(slot), ch * 128, 0, zb);
-              }
+            for (int ch = 0; ch < C::kCh && ok; ++ch) {
+              if (za >= 0) tma_load_3d(s_k(slot) + ch * 16384, &map_k, bar_k_full(slot), ch * 128, 0, za);
+              if (zb >= 0) tma_load_3d(s_k(slot) + ch * 16384 + 8192, &map_k, bar_k_full(slot), ch * 128, 0, zb);
             }
           }
-          // The scales. Their slot is free: K's slot was, so S of tile - kRingK is done, which was issued behind the
-          // product of the tile before it, or two before it: the softmax of that one and of all before is done.
           ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
           if (!ok) break;
+          // The scales, ahead of the one arrival that K's barrier waits for beside its bytes: who sees K's product sees
+          // them. Their slot is free: K's slot was, so S of tile - kRingK is done, which was issued behind the
+          // product of the tile before it, or two before it: the softmax of that one and of all before is done.
           if (lane == i || lane == i + 1) {
             volatile float* const dst = info + (tile % kInfo) * 8 + (lane - i) * 4;
-            dst[0] = ks;
-            dst[1] = log2f(vs);
-            dst[2] = page >= 0 ? 1.f : 0.f;
+            dst[0] = ks_now;
+            dst[1] = log2f(vs_now);
+            dst[2] = z_now >= 0 ? 1.f : 0.f;
           }
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(bar_info(tile));
+            mbar_arrive_expect_tx(bar_k_full(slot), ((za >= 0) + (zb >= 0)) * 8192 * C::kCh);
 #pragma unroll
             for (int x = 0; x < C::kPerTile && ok; ++x) {
               const int c = tile * C::kPerTile + x, cs = c % C::kRingV;
@@ -471,6 +478,7 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
             }
           }
           ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
+          if (i == 16) scales_of(next_page);
         }
       }
     }
@@ -481,8 +489,9 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     if (lane == 0) {
       const uint32_t id_s = make_idesc(0, 128, 128, 0, 0);             // e4m3, both K-major
       const uint32_t id_o = make_idesc(0, 128, p.c.d, 0, 1);           // f16, V MN-major
-      // The issuing thread paces the kernel (a product takes 64 cycles): descriptors are stepped, slots and parities
-      // counted along, and at full width the products stand in a row.
+      // The issuing thread paces the kernel (a product takes 64 cycles, a look at a barrier 90 to 200, a commit 46):
+      // descriptors are stepped, slots and parities counted along, and a step's products stand in a row. With two
+      // groups P-ready stands for V and the next K too (the watcher's arrival), and the watcher hands the rings back.
       const int steps = (p.c.d + 31) / 32;                             // products over d that are not all zeros
       const uint64_t kd0 = smem_desc_sw128(s_k(0), 16, 1024), qd0 = smem_desc_sw128(s_q(0, 0), 16, 1024);
       const uint64_t vd0 = smem_desc_sw128(s_half(0), C::kBoxV, 1024);
@@ -492,63 +501,54 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       [[maybe_unused]] int buf = 1;                                    // one group: S's buffer of the last tile
       int k_slot = 0, v_slot = 0;                                      // of the next tile for S, of the next V stage
       uint32_t k_par = 0, v_par = 0;
-      // S of rows `group` with K of k_slot into buffer `buf`; the last user of the tile hands it back and steps on
-      auto scores = [&](int buf, int group, bool first_user, bool last_user) {
-        if (first_user) {
-          ok = wait(bar_k_full(k_slot), k_par, abort_flag, p.timeout_ns);
-          if (!ok) return;
-          tc_fence_after();
+      auto step_k = [&]() {
+        if (++k_slot == C::kRingK) {
+          k_slot = 0;
+          k_par ^= 1;
         }
+      };
+      // S of rows `group` with K of k_slot into buffer `buf`
+      auto scores = [&](int buf, int group) {
         const uint64_t kd = kd0 + static_cast<uint32_t>(k_slot * (C::kTileK >> 4));
         const uint64_t qd = qd0 + static_cast<uint32_t>(group * (2 * C::kQTerm >> 4));
         const uint32_t dst = tbase + C::col_s(buf);
-        if (steps == 4 * C::kCh) {
+        auto row = [&](auto count) {
+          constexpr int n = decltype(count)::value;
 #pragma unroll
-          for (int i = 0; i < 8 * C::kCh; ++i) {
-            const int term = i / (4 * C::kCh), k = i % (4 * C::kCh), off = (k >> 2) * 16384 + (k & 3) * 32;
+          for (int i = 0; i < 2 * n; ++i) {
+            const int term = i / n, k = i % n, off = (k >> 2) * 16384 + (k & 3) * 32;
             mma_fp8_ss(dst, desc_add(qd, term * C::kQTerm + off), desc_add(kd, off), id_s, i > 0);
           }
-        } else {
-          for (int term = 0; term < 2; ++term)
-            for (int k = 0; k < steps; ++k) {
-              const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-              mma_fp8_ss(dst, desc_add(qd, term * C::kQTerm + off), desc_add(kd, off), id_s, term > 0 || k > 0);
-            }
-        }
+        };
+        constexpr int most = 4 * C::kCh;
+        if (steps == most) row(std::integral_constant<int, most>());
+        else if (steps == most - 2) row(std::integral_constant<int, most - 2>());
+        else if (steps == most - 1) row(std::integral_constant<int, most - 1>());
+        else row(std::integral_constant<int, most - 3>());
         mma_commit(bar_s_full(buf));
-        if (last_user) {
-          mma_commit(bar_k_empty(k_slot));
-          if (++k_slot == C::kRingK) {
-            k_slot = 0;
-            k_par ^= 1;
-          }
+      };
+      // O of `group` += P in buffer `buf` times a V stage
+      auto product = [&](int buf, int group, int x, bool acc) {
+        const uint64_t vd = vd0 + static_cast<uint32_t>(v_slot * (C::kHalfV >> 4));
+        const uint32_t src = tbase + C::col_s(buf) + x * (C::kKeysV / 2);
+#pragma unroll
+        for (int k = 0; k < C::kKeysV / 16; ++k)
+          mma_bf16_ts(tbase + C::col_o(group), src + k * 8, desc_add(vd, k * 2048), id_o, acc || k > 0);
+      };
+      auto step_v = [&]() {
+        if (++v_slot == C::kRingV) {
+          v_slot = 0;
+          v_par ^= 1;
         }
       };
-      // O of `group` += P in buffer `buf` times V of the tile
-      auto product = [&](int buf, int group, bool acc, bool first_user, bool last_user) {
+      auto k_there = [&]() {
+        ok = wait(bar_k_full(k_slot), k_par, abort_flag, p.timeout_ns);
+        tc_fence_after();
+      };
+      auto p_there = [&](int buf) {
         ok = wait(bar_p_ready(buf), np >> buf & 1u, abort_flag, p.timeout_ns);
-        if (!ok) return;
         np ^= 1u << buf;
-#pragma unroll
-        for (int x = 0; x < C::kPerTile; ++x) {
-          if (first_user) {
-            ok = wait(bar_v_full(v_slot), v_par, abort_flag, p.timeout_ns);
-            if (!ok) return;
-          }
-          tc_fence_after();
-          const uint64_t vd = vd0 + static_cast<uint32_t>(v_slot * (C::kHalfV >> 4));
-          const uint32_t src = tbase + C::col_s(buf) + x * (C::kKeysV / 2);
-#pragma unroll
-          for (int k = 0; k < C::kKeysV / 16; ++k)
-            mma_bf16_ts(tbase + C::col_o(group), src + k * 8, desc_add(vd, k * 2048), id_o, acc || x > 0 || k > 0);
-          if (last_user) {
-            mma_commit(bar_v_empty(v_slot));
-            if (++v_slot == C::kRingV) {
-              v_slot = 0;
-              v_par ^= 1;
-            }
-          }
-        }
+        tc_fence_after();
       };
       volatile int* const state = states + 4 * kGroups * kStateInts;
       walk.save(state);
@@ -570,28 +570,98 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         if (kGroups == 1) {
           // S of the next tile is out before this one's P V
           for (int j = -1; j < n && ok; ++j) {
-            if (j + 1 < n) scores(buf ^ 1, 0, true, true);
-            else mma_commit(bar_q_empty);
-            if (ok && j >= 0) product(buf, 0, j > 0, true, true);
+            if (j + 1 < n) {
+              k_there();
+              if (!ok) break;
+              scores(buf ^ 1, 0);
+              mma_commit(bar_k_empty(k_slot));
+              step_k();
+            } else {
+              mma_commit(bar_q_empty);
+            }
+            if (j >= 0) {
+              p_there(buf);
+#pragma unroll
+              for (int x = 0; x < C::kPerTile && ok; ++x) {
+                ok = wait(bar_v_full(v_slot), v_par, abort_flag, p.timeout_ns);
+                if (!ok) break;
+                tc_fence_after();
+                product(buf, 0, x, j > 0 || x > 0);
+                mma_commit(bar_v_empty(v_slot));
+                step_v();
+              }
+            }
             if (j + 1 < n) buf ^= 1;
           }
           if (ok) mma_commit(bar_o_final(0));
         } else {
           // Step i is group i & 1's P V of a tile and its S of the next one: split, tile i, then i + 2; else tile
           // i / 2 of either group, then the one behind it. The first two steps have no P V yet.
-          const int steps_all = split ? n : 2 * n;
-          for (int i = -2; i < steps_all && ok; ++i) {
+          const int all = split ? n : 2 * n;
+          for (int i = -2; i < all; ++i) {
             const int gr = i & 1, j = split ? i : i >> 1;
             const int mine = split || gr ? n : n0, next_j = split ? i + 2 : j + 1;
             const bool last = split || gr;
             if (j >= mine) continue;
-            if (i >= 0) product(gr, gr, split ? i > 1 : j > 0, split || !gr || j >= n0, last);
-            if (!ok) break;
-            if (next_j < mine) scores(gr, split ? 0 : gr, split || !gr || next_j >= n0, last);
-            else if (i >= 0) mma_commit(bar_o_final(gr));
+            if (i >= 0) {
+              p_there(gr);
+              if (!ok) break;
+              product(gr, gr, 0, split ? i > 1 : j > 0);
+              if (last) step_v();
+            } else if (next_j < mine && (split || !gr || n0 <= 0)) {
+              k_there();
+              if (!ok) break;
+            }
+            if (next_j < mine) {
+              scores(gr, split ? 0 : gr);
+              if (last) step_k();
+            } else if (i >= 0) {
+              mma_commit(bar_o_final(gr));
+            }
             if (last && next_j + 1 == n) mma_commit(bar_q_empty);      // every S is out
           }
         }
+      }
+    }
+    __syncwarp();
+  } else if (kGroups == 2 && warp == 10) {
+    // ------------------------------------------------------------ ring watcher
+    // One arrival on P-ready when V of its tile and K of the next S behind it have landed, and the rings' slots back when
+    // the S that shows them read is done: K of that S, and V up to the tile whose product was issued before it. It
+    // waits for every load in order, so no parity is taken for that of two phases earlier.
+    setmaxnreg_dec<C::kRegsOther>();
+    if (lane == 0) {
+      Segment s;
+      bool ok = true;
+      int tile = 0, k_seen = 0, v_back = 0;                // tiles before the segment, K tiles waited for, V stages handed back
+      uint32_t ns0 = 0, ns1 = 0, np0 = 0, np1 = 0;         // phases of S and of P-ready
+      auto hand = [&](int g) {
+        uint32_t& np = g ? np1 : np0;
+        // arrive for a phase only once the one before it has completed
+        if (np > 0) ok = wait(bar_p_ready(g), (np - 1) & 1, abort_flag, p.timeout_ns);
+        if (ok) mbar_arrive(bar_p_ready(g));
+        ++np;
+      };
+      while (ok && walk.next<kGroups>(p, s)) {
+        const int n = s.t1 - s.t0;
+        for (int x = 0; x < n && ok; ++x) {
+          const int t = tile + x, g = s.split ? x & 1 : 1;
+          // (S first: V of this tile may wait for the slot that goes back here)
+          ok = wait(bar_s_full(g), (g ? ns1 : ns0) & 1, abort_flag, p.timeout_ns);
+          if (!ok) break;
+          if (g) ++ns1;
+          else ++ns0;
+          mbar_arrive(bar_k_empty(t % C::kRingK));
+          for (const int upto = s.split && x > 0 ? t - 2 : t - 1; v_back <= upto; ++v_back) mbar_arrive(bar_v_empty(v_back & 1));
+          ok = wait(bar_v_full(t & 1), (t >> 1) & 1, abort_flag, p.timeout_ns);
+          const int k_last = tile + min(n - 1, s.split ? x + 2 : x + 1);
+          for (; k_seen <= k_last && ok; ++k_seen)
+            ok = wait(bar_k_full(k_seen % C::kRingK), (k_seen / C::kRingK) & 1, abort_flag, p.timeout_ns);
+          if (ok && !s.split && x < s.n0) hand(0);
+          if (ok) hand(g);
+        }
+        if (!s.split) ns0 += s.n0;
+        tile += n;
       }
     }
     __syncwarp();
@@ -666,7 +736,6 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       constexpr int kPieces = D / 16;                      // of a key
       const int piece = tid % kPieces, key0 = tid / kPieces;
       for (int j = s.t0; j < s.t1 && ok; ++j, ++tile) {
-        ok = wait(bar_info(tile), (tile / kInfo) & 1, abort_flag, p.timeout_ns);
         const volatile float* const there = info + (tile % kInfo) * 8;
 #pragma unroll
         for (int x = 0; x < C::kPerTile; ++x) {
@@ -769,18 +838,17 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       float l = 0.f;                                       // running sum relative to ml
       for (; at < end; at += dx, lim -= 128 * dx) {
         const int buf = kGroups == 1 ? at & 1 : g;
-        ok = wait(bar_info(at), (at / kInfo) & 1, abort_flag, p.timeout_ns);
+        ok = wait(bar_s_full(buf), kGroups == 1 ? at >> 1 & 1u : par & 1u, abort_flag, p.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        par ^= 1u;
+        tc_fence_after();
         const volatile float* const sc = info + (at % kInfo) * 8;
         // (at least the smallest normal number: a K scale of 0 makes 0 of every logit, but would make NaN of the -inf of
         // keys that are not there)
         const float ka = fmaxf(sc[0] * sl2, 1.17549435e-38f), kb = fmaxf(sc[4] * sl2, 1.17549435e-38f);
         const float lva = sc[1], lvb = sc[5];
         const bool here_a = sc[2] != 0.f, here_b = sc[6] != 0.f;
-        if (ok) ok = wait(bar_s_full(buf), kGroups == 1 ? at >> 1 & 1u : par & 1u, abort_flag, p.timeout_ns);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        par ^= 1u;
-        tc_fence_after();
         const uint32_t t_s = tbase + lane_off + C::col_s(buf);
         const uint32_t t_o = tbase + lane_off + C::col_o(g);
         uint32_t sr[4][32];

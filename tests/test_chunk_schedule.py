@@ -206,7 +206,7 @@ def test_every_key_tile_is_some_parts_once_and_joined(groups, causal):
 
 
 # ------------------------------------------------------------------ the hand-offs
-def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, infos=8, softmax=(300, 1500), convert=(200, 900)):
+def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, infos=8, v_late=2, s_first=True, horizon=2e6, softmax=(300, 1500), convert=(200, 900)):
     """segments: (split, n0, n). WARPS stand for a softmax group's four, and for the converters'."""
     WARPS, RING_V = 2, 2
     per = 1 if groups == 2 else 2
@@ -215,10 +215,11 @@ def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, 
     k_full, k_empty = [Barrier(1) for _ in range(ring_k)], [Barrier(1) for _ in range(ring_k)]
     c_full, c_empty = [Barrier(1) for _ in range(2)], [Barrier(WARPS) for _ in range(2)]
     v_full, v_empty = [Barrier(WARPS) for _ in range(2)], [Barrier(1) for _ in range(2)]
-    s_full, p_ready, o_final = ([Barrier(1), Barrier(1)], [Barrier(WARPS), Barrier(WARPS)], [Barrier(1), Barrier(1)])
+    watched = groups == 2
+    s_full, p_ready, o_final = ([Barrier(1), Barrier(1)], [Barrier(WARPS + watched), Barrier(WARPS + watched)], [Barrier(1), Barrier(1)])
     q_full, q_empty = Barrier(WARPS), Barrier(1 + (WARPS * groups if q_read else 0))
     other_full, other_emptied = Barrier(WARPS), Barrier(WARPS)
-    info_bar, info = [Barrier(1) for _ in range(infos)], [None] * infos
+    info = [None] * infos
     k_slot, c_slot, v_slot = [None] * ring_k, [None] * 2, [set() for _ in range(2)]
     q_now, scale_now = [set()], [set()]
     tmem_s, o_owner = [None, None], [None, None]
@@ -268,13 +269,20 @@ def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, 
             for _ in range(n):
                 yield from run.wait(k_empty[t % ring_k], ((t // ring_k) & 1) ^ 1, "producer K", t // ring_k - 1)
 
-                def land(t=t):
+                ready = [0]
+
+                def land(t=t, ready=ready):          # the bytes and the producer's arrival behind the scales
+                    ready[0] += 1
+                    if ready[0] == 2:
+                        k_full[t % ring_k].arrive()
+
+                def bytes_there(t=t, land=land):
                     k_slot[t % ring_k] = t
-                    k_full[t % ring_k].arrive()
-                run.later(300, 1500, land)
-                yield run.delay(5, 400)
+                    land()
+                run.later(300, 1500, bytes_there)
+                yield run.delay(5, 2000)
                 info[t % infos] = t
-                info_bar[t % infos].arrive()
+                land()
                 for x in range(per):
                     c = t * per + x
                     yield from run.wait(c_empty[c % 2], ((c // 2) & 1) ^ 1, "producer V", c // 2 - 1)
@@ -288,71 +296,92 @@ def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, 
     def issuer():
         t, np = 0, [0, 0]
 
-        def scores(seg, buf, g, t, last):
-            yield from run.wait(k_full[t % ring_k], (t // ring_k) & 1, f"S {t}", t // ring_k)
+        def scores(seg, buf, g, t):
             pipe.append(("S", seg, buf, g, t, False))
             pipe.append(("commit", s_full[buf]))
-            if last:
-                pipe.append(("commit", k_empty[t % ring_k]))
             yield run.delay(20, 300)
 
-        def product(seg, buf, g, t, acc, last):
+        def k_there(t):
+            yield from run.wait(k_full[t % ring_k], (t // ring_k) & 1, f"S {t}", t // ring_k)
+
+        def p_there(buf):
             yield from run.wait(p_ready[buf], np[buf] & 1, f"P ready {buf}", np[buf])
             np[buf] += 1
-            for x in range(per):
-                c = t * per + x
-                yield from run.wait(v_full[c % 2], (c // 2) & 1, f"V {c}", c // 2)
-            pipe.append(("PV", seg, buf, g, t, not acc))
-            if last:
-                for x in range(per):
-                    pipe.append(("commit", v_empty[(t * per + x) % 2]))
-            yield run.delay(20, 300)
         for seg, (split, n0, n) in enumerate(segments):
             yield from run.wait(q_full, seg & 1, "issuer Q", seg)
             if groups == 1:
-                yield from scores(seg, t & 1, 0, t, True)
-                for j in range(n):
+                for j in range(-1, n):
                     if j + 1 < n:
-                        yield from scores(seg, (t + j + 1) & 1, 0, t + j + 1, True)
+                        at = t + j + 1
+                        yield from k_there(at)
+                        yield from scores(seg, at & 1, 0, at)
+                        pipe.append(("commit", k_empty[at % ring_k]))
                     else:
                         pipe.append(("commit", q_empty))
-                    yield from product(seg, (t + j) & 1, 0, t + j, j > 0, True)
+                    if j >= 0:
+                        yield from p_there((t + j) & 1)
+                        for x in range(per):
+                            c = (t + j) * per + x
+                            yield from run.wait(v_full[c % 2], (c // 2) & 1, f"V {c}", c // 2)
+                        pipe.append(("PV", seg, (t + j) & 1, 0, t + j, j == 0))
+                        for x in range(per):
+                            pipe.append(("commit", v_empty[((t + j) * per + x) % 2]))
                 pipe.append(("commit", o_final[0]))
-            elif split:
-                for x in range(min(n, 2)):
-                    yield from scores(seg, x, x, t + x, True)
-                if n <= 2:
-                    pipe.append(("commit", q_empty))
-                for x in range(n):
-                    g = x & 1
-                    yield from product(seg, g, g, t + x, x > 1, True)
-                    if x + 2 < n:
-                        yield from scores(seg, g, g, t + x + 2, True)
-                    else:
-                        pipe.append(("commit", o_final[g]))
-                    if x + 3 == n:
-                        pipe.append(("commit", q_empty))
             else:
-                if n0 > 0:
-                    yield from scores(seg, 0, 0, t, False)
-                yield from scores(seg, 1, 1, t, True)
-                if n == 1:
-                    pipe.append(("commit", q_empty))
-                for j in range(n):
-                    if j < n0:
-                        yield from product(seg, 0, 0, t + j, j > 0, False)
-                        if j + 1 < n0:
-                            yield from scores(seg, 0, 0, t + j + 1, False)
-                        else:
-                            pipe.append(("commit", o_final[0]))
-                    yield from product(seg, 1, 1, t + j, j > 0, True)
-                    if j + 1 < n:
-                        yield from scores(seg, 1, 1, t + j + 1, True)
-                    else:
-                        pipe.append(("commit", o_final[1]))
-                    if j + 2 == n:
+                k_next = t
+                for i in range(-2, n if split else 2 * n):
+                    gr, j = i & 1, i if split else i >> 1
+                    mine, next_j, last = (n if split or gr else n0), (i + 2 if split else j + 1), split or gr
+                    if j >= mine:
+                        continue
+                    if i >= 0:
+                        yield from p_there(gr)
+                        pipe.append(("PV", seg, gr, gr, t + j, i <= 1 if split else j == 0))
+                        yield run.delay(20, 300)
+                    elif next_j < mine and (split or not gr or n0 <= 0):
+                        yield from k_there(k_next)
+                    if next_j < mine:
+                        assert k_next == t + next_j
+                        yield from scores(seg, gr, gr, t + next_j)
+                        k_next += bool(last)
+                    elif i >= 0:
+                        pipe.append(("commit", o_final[gr]))
+                    if last and next_j + 1 == n:
                         pipe.append(("commit", q_empty))
             t += n
+
+    def watcher():
+        t0, k_seen, v_back, ns, np = 0, 0, 0, [0, 0], [0, 0]
+
+        def hand(g):
+            if np[g] > 0:
+                yield from run.wait(p_ready[g], (np[g] - 1) & 1, f"watcher P {g}", np[g] - 1)
+            p_ready[g].arrive()
+            np[g] += 1
+        for split, n0, n in segments:
+            for x in range(n):
+                t, g = t0 + x, x & 1 if split else 1
+                if not s_first:
+                    yield from run.wait(v_full[t & 1], (t >> 1) & 1, f"watcher V {t}", t >> 1)
+                yield from run.wait(s_full[g], ns[g] & 1, f"watcher S {t}", ns[g])
+                ns[g] += 1
+                k_empty[t % ring_k].arrive()
+                while v_back <= (t - v_late if split and x > 0 else t - 1):
+                    v_empty[v_back & 1].arrive()
+                    v_back += 1
+                if s_first:
+                    yield from run.wait(v_full[t & 1], (t >> 1) & 1, f"watcher V {t}", t >> 1)
+                k_last = t0 + min(n - 1, x + 2 if split else x + 1)
+                while k_seen <= k_last:
+                    yield from run.wait(k_full[k_seen % ring_k], (k_seen // ring_k) & 1, f"watcher K {k_seen}", k_seen // ring_k)
+                    k_seen += 1
+                if not split and x < n0:
+                    yield from hand(0)
+                yield from hand(g)
+                yield run.delay(20, 500)
+            if not split:
+                ns[0] += n0
+            t0 += n
 
     def converter(w):
         t = 0
@@ -365,15 +394,14 @@ def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, 
             scale_now[0].add((seg, w))
             q_full.arrive()
             for j in range(n):
-                yield from run.wait(info_bar[t % infos], (t // infos) & 1, "converter info", t // infos)
-                if info[t % infos] != t:
-                    errors.append(f"converter read info {info[t % infos]} for {t}")
                 for x in range(per):
                     c = t * per + x
                     yield from run.wait(c_full[c % 2], (c // 2) & 1, f"codes {c}", c // 2)
                     yield from run.wait(v_empty[c % 2], ((c // 2) & 1) ^ 1, f"V empty {c}", c // 2 - 1)
                     if c_slot[c % 2] != c:
                         errors.append(f"converted codes {c_slot[c % 2]} for {c}")
+                    if info[t % infos] != t:
+                        errors.append(f"converter read info {info[t % infos]} for {t}")
                     v_slot[c % 2] = {y for y in v_slot[c % 2] if y[0] == c}
                     yield run.delay(*convert)
                     if c_slot[c % 2] != c:
@@ -397,7 +425,6 @@ def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, 
             for x in range(x0, nx, dx):
                 at = t + x
                 buf = at & 1 if groups == 1 else g
-                yield from run.wait(info_bar[at % infos], (at // infos) & 1, f"softmax {g} info {at}", at // infos)
                 want = at >> 1 if groups == 1 else ns[0]
                 yield from run.wait(s_full[buf], want & 1, f"softmax {g} S {at}", want)
                 ns[0] += 1
@@ -444,7 +471,8 @@ def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, 
 
     roles = [producer(), issuer(), tensor_core()] + [converter(w) for w in range(WARPS)]
     roles += [softmax_warp(g, w) for g in range(groups) for w in range(WARPS)]
-    return run.go(roles, {2}, 2e6, lambda: not pipe)
+    roles += [watcher()] if watched else []
+    return run.go(roles, {2}, horizon, lambda: not pipe)
 
 
 def random_segments(rng, groups):
@@ -470,10 +498,10 @@ def test_hand_offs(groups):
         assert not errors, (segs, errors[:3])
 
 
-@pytest.mark.parametrize("planted", [dict(q_read=False), dict(other_empty=False), dict(infos=4)])
+@pytest.mark.parametrize("planted", [dict(q_read=False), dict(other_empty=False), dict(infos=2), dict(v_late=1), dict(s_first=False)])
 def test_planted_changes_are_found(planted):
     bad = 0
     for seed in range(60):
         segs = [(True, n, n) for n in random.Random(seed).choices([1, 2, 7, 12], k=10)]
-        bad += bool(chunk(segs, seed, softmax=(10, 6000), **planted))
+        bad += bool(chunk(segs, seed, softmax=(10, 6000), horizon=5e5, **planted))
     assert bad, planted
