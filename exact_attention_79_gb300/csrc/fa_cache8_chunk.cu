@@ -441,6 +441,7 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           const int slot = tile % C::kRingK;
           if (lane == 0) {
             ok = wait(bar_k_empty(slot), ((tile / C::kRingK) & 1) ^ 1, abort_flag, p.timeout_ns);
+            if (ok) mbar_expect_tx(bar_k_full(slot), ((za >= 0) + (zb >= 0)) * 8192 * C::kCh);
             for (int ch = 0; ch < C::kCh && ok; ++ch) {
               if (za >= 0) tma_load_3d(s_k(slot) + ch * 16384, &map_k, bar_k_full(slot), ch * 128, 0, za);
               if (zb >= 0) tma_load_3d(s_k(slot) + ch * 16384 + 8192, &map_k, bar_k_full(slot), ch * 128, 0, zb);
@@ -459,7 +460,7 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           }
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive_expect_tx(bar_k_full(slot), ((za >= 0) + (zb >= 0)) * 8192 * C::kCh);
+            mbar_arrive(bar_k_full(slot));
 #pragma unroll
             for (int x = 0; x < C::kPerTile && ok; ++x) {
               const int c = tile * C::kPerTile + x, cs = c % C::kRingV;
@@ -646,17 +647,21 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         const int n = s.t1 - s.t0;
         for (int x = 0; x < n && ok; ++x) {
           const int t = tile + x, g = s.split ? x & 1 : 1;
-          // (S first: V of this tile may wait for the slot that goes back here)
-          ok = wait(bar_s_full(g), (g ? ns1 : ns0) & 1, abort_flag, p.timeout_ns);
+          auto k_there = [&](int last) {
+            for (; k_seen <= last && ok; ++k_seen)
+              ok = wait(bar_k_full(k_seen % C::kRingK), (k_seen / C::kRingK) & 1, abort_flag, p.timeout_ns);
+          };
+          // (S before V: V of this tile may wait for the slot that goes back here. The segment's first K before that, as
+          // its slot goes back here too.)
+          k_there(t);
+          if (ok) ok = wait(bar_s_full(g), (g ? ns1 : ns0) & 1, abort_flag, p.timeout_ns);
           if (!ok) break;
           if (g) ++ns1;
           else ++ns0;
           mbar_arrive(bar_k_empty(t % C::kRingK));
           for (const int upto = s.split && x > 0 ? t - 2 : t - 1; v_back <= upto; ++v_back) mbar_arrive(bar_v_empty(v_back & 1));
           ok = wait(bar_v_full(t & 1), (t >> 1) & 1, abort_flag, p.timeout_ns);
-          const int k_last = tile + min(n - 1, s.split ? x + 2 : x + 1);
-          for (; k_seen <= k_last && ok; ++k_seen)
-            ok = wait(bar_k_full(k_seen % C::kRingK), (k_seen / C::kRingK) & 1, abort_flag, p.timeout_ns);
+          k_there(tile + min(n - 1, s.split ? x + 2 : x + 1));
           if (ok && !s.split && x < s.n0) hand(0);
           if (ok) hand(g);
         }

@@ -206,7 +206,7 @@ def test_every_key_tile_is_some_parts_once_and_joined(groups, causal):
 
 
 # ------------------------------------------------------------------ the hand-offs
-def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, infos=8, v_late=2, s_first=True, horizon=2e6, softmax=(300, 1500), convert=(200, 900)):
+def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, infos=8, v_late=2, s_first=True, k_first=True, land_in=(300, 1500), scales=2000, horizon=2e6, softmax=(300, 1500), convert=(200, 900)):
     """segments: (split, n0, n). WARPS stand for a softmax group's four, and for the converters'."""
     WARPS, RING_V = 2, 2
     per = 1 if groups == 2 else 2
@@ -279,8 +279,8 @@ def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, 
                 def bytes_there(t=t, land=land):
                     k_slot[t % ring_k] = t
                     land()
-                run.later(300, 1500, bytes_there)
-                yield run.delay(5, 2000)
+                run.later(*land_in, bytes_there)
+                yield run.delay(5, scales)
                 info[t % infos] = t
                 land()
                 for x in range(per):
@@ -290,7 +290,7 @@ def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, 
                     def land_v(c=c):
                         c_slot[c % 2] = c
                         c_full[c % 2].arrive()
-                    run.later(300, 1500, land_v)
+                    run.later(*land_in, land_v)
                 t += 1
 
     def issuer():
@@ -358,9 +358,17 @@ def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, 
                 yield from run.wait(p_ready[g], (np[g] - 1) & 1, f"watcher P {g}", np[g] - 1)
             p_ready[g].arrive()
             np[g] += 1
+
+        def k_there(last):
+            nonlocal k_seen
+            while k_seen <= last:
+                yield from run.wait(k_full[k_seen % ring_k], (k_seen // ring_k) & 1, f"watcher K {k_seen}", k_seen // ring_k)
+                k_seen += 1
         for split, n0, n in segments:
             for x in range(n):
                 t, g = t0 + x, x & 1 if split else 1
+                if k_first:
+                    yield from k_there(t)
                 if not s_first:
                     yield from run.wait(v_full[t & 1], (t >> 1) & 1, f"watcher V {t}", t >> 1)
                 yield from run.wait(s_full[g], ns[g] & 1, f"watcher S {t}", ns[g])
@@ -371,10 +379,7 @@ def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, 
                     v_back += 1
                 if s_first:
                     yield from run.wait(v_full[t & 1], (t >> 1) & 1, f"watcher V {t}", t >> 1)
-                k_last = t0 + min(n - 1, x + 2 if split else x + 1)
-                while k_seen <= k_last:
-                    yield from run.wait(k_full[k_seen % ring_k], (k_seen // ring_k) & 1, f"watcher K {k_seen}", k_seen // ring_k)
-                    k_seen += 1
+                yield from k_there(t0 + min(n - 1, x + 2 if split else x + 1))
                 if not split and x < n0:
                     yield from hand(0)
                 yield from hand(g)
@@ -491,17 +496,17 @@ def test_hand_offs(groups):
         segs = random_segments(random.Random(seed), groups)
         kw = {}
         if seed % 3 == 1:
-            kw = dict(softmax=(10, 6000))
+            kw = dict(softmax=(10, 6000), convert=(10, 6000))
         if seed % 3 == 2:
-            kw = dict(convert=(10, 5000))
+            kw = dict(convert=(10, 5000), land_in=(5, 50), scales=20)
         errors = chunk(segs, seed, groups=groups, ring_k=3 if groups == 2 else 2, **kw)
         assert not errors, (segs, errors[:3])
 
 
-@pytest.mark.parametrize("planted", [dict(q_read=False), dict(other_empty=False), dict(infos=2), dict(v_late=1), dict(s_first=False)])
+@pytest.mark.parametrize("planted", [dict(q_read=False), dict(other_empty=False), dict(infos=2), dict(v_late=1), dict(s_first=False), dict(k_first=False, land_in=(5, 50), scales=20)])
 def test_planted_changes_are_found(planted):
     bad = 0
     for seed in range(60):
         segs = [(True, n, n) for n in random.Random(seed).choices([1, 2, 7, 12], k=10)]
-        bad += bool(chunk(segs, seed, softmax=(10, 6000), horizon=5e5, **planted))
+        bad += bool(chunk(segs, seed, softmax=(10, 6000), convert=(10, 6000), horizon=5e5, **planted))
     assert bad, planted
