@@ -65,7 +65,7 @@ struct Cfg {
   static constexpr int kSmem = kLayout + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   // setmaxnreg, of the 512 x 128 launched: without spills, which L1 beside so much shared memory does not hold
-  static constexpr uint32_t kRegsSoftmax = D == 128 ? 192 : 184, kRegsOther = 256 - kRegsSoftmax;
+  static constexpr uint32_t kRegsSoftmax = D == 128 ? 192 : 168, kRegsOther = 256 - kRegsSoftmax;
   static __device__ __forceinline__ uint32_t col_s(int i) { return 128u * i; }
   static __device__ __forceinline__ uint32_t col_o(int i) { return 256u + 128u * i; }
 };
@@ -651,18 +651,26 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
             for (; k_seen <= last && ok; ++k_seen)
               ok = wait(bar_k_full(k_seen % C::kRingK), (k_seen / C::kRingK) & 1, abort_flag, p.timeout_ns);
           };
-          // (S before V: V of this tile may wait for the slot that goes back here. The segment's first K before that, as
-          // its slot goes back here too.)
-          k_there(t);
-          if (ok) ok = wait(bar_s_full(g), (g ? ns1 : ns0) & 1, abort_flag, p.timeout_ns);
-          if (!ok) break;
-          if (g) ++ns1;
-          else ++ns0;
-          mbar_arrive(bar_k_empty(t % C::kRingK));
-          for (const int upto = s.split && x > 0 ? t - 2 : t - 1; v_back <= upto; ++v_back) mbar_arrive(bar_v_empty(v_back & 1));
-          ok = wait(bar_v_full(t & 1), (t >> 1) & 1, abort_flag, p.timeout_ns);
+          auto s_done = [&]() {
+            if (ok) ok = wait(bar_s_full(g), (g ? ns1 : ns0) & 1, abort_flag, p.timeout_ns);
+            if (!ok) return;
+            if (g) ++ns1;
+            else ++ns0;
+            mbar_arrive(bar_k_empty(t % C::kRingK));
+            for (const int upto = s.split && x > 0 ? t - 2 : t - 1; v_back <= upto; ++v_back) mbar_arrive(bar_v_empty(v_back & 1));
+          };
+          // S before V where V of this tile may wait for the slot that goes back then: split, and at the segment's
+          // start (whose first K comes before that, as its slot goes back too). Otherwise group 0's P is ready long
+          // before this is: S of group 1 is done when P of group 0 nearly is, and each look costs 90 to 200 cycles.
+          const bool s_first = s.split || x == 0;
+          if (s_first) {
+            k_there(t);
+            s_done();
+          }
+          if (ok) ok = wait(bar_v_full(t & 1), (t >> 1) & 1, abort_flag, p.timeout_ns);
           k_there(tile + min(n - 1, s.split ? x + 2 : x + 1));
           if (ok && !s.split && x < s.n0) hand(0);
+          if (!s_first) s_done();
           if (ok) hand(g);
         }
         if (!s.split) ns0 += s.n0;
@@ -678,65 +686,72 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     int tile = 0;
     Segment s;
     for (int seg = 0; ok && walk.next<kGroups>(p, s); ++seg) {
-      // ---- Q: this warp's 32 rows of each row tile, four at a time
+      // ---- Q: 16 bytes a lane, eight loads of a warp under way together; this warp's 32 rows of each row tile. The
+      // rows are in L2 by now (below), as all other warps wait for this once the last S is done.
       ok = wait(bar_q_empty, (seg & 1) ^ 1, abort_flag, p.timeout_ns);
       if (!__all_sync(0xffffffffu, ok)) break;
+      constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes; // lanes of a row, rows of a load
+      const int piece_q = lane % kLanes, sub = lane / kLanes;
 #pragma unroll 1
-      for (int r0 = 0; r0 < (s.split ? 128 : C::kRows); r0 += 16) {
-        uint2 v[4][C::kCh];
-        const int tile_row = (r0 & 127) + 4 * cw, group = r0 >> 7;     // rows tile_row .. + 3 of the row tile
+      for (int r0 = 0; r0 < (s.split ? 128 : C::kRows); r0 += 32 * kAtOnce) {
+        uint4 v[8];
+        const int group = r0 >> 7, first_row = (r0 & 127) + 8 * kAtOnce * cw + sub;   // rows first_row + kAtOnce * e
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int row = tile_row + e, tok = row / p.G, token = s.tok0 + group * p.tt + tok;
-          const bool real = tok < p.tt && token < s.n;
-          const __nv_bfloat16* const src =
-              p.q + (s.h * p.G + (row - tok * p.G)) * p.q_sh + (static_cast<long long>(s.row0) + token) * p.q_st;
-#pragma unroll
-          for (int ch = 0; ch < C::kCh; ++ch) {
-            const int col = 128 * ch + 4 * lane;
-            v[e][ch] = real && col < p.c.d ? *reinterpret_cast<const uint2*>(src + col) : make_uint2(0, 0);
-          }
-        }
-        uint32_t amax[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t m = 0;                                  // both halves' largest magnitudes, as bits
-#pragma unroll
-          for (int ch = 0; ch < C::kCh; ++ch) {
-            const uint32_t w[2] = {v[e][ch].x & 0x7FFF7FFFu, v[e][ch].y & 0x7FFF7FFFu};
-#pragma unroll
-            for (int k = 0; k < 2; ++k) m = max(m, max(w[k] & 0xFFFFu, w[k] >> 16));
-          }
-          amax[e] = __reduce_max_sync(0xffffffffu, m);
+        for (int e = 0; e < 8; ++e) {
+          const int row = first_row + kAtOnce * e, tok = row / p.G, token = s.tok0 + group * p.tt + tok;
+          v[e] = make_uint4(0, 0, 0, 0);
+          if (tok < p.tt && token < s.n && 8 * piece_q < p.c.d)
+            v[e] = *reinterpret_cast<const uint4*>(p.q + (s.h * p.G + (row - tok * p.G)) * p.q_sh +
+                                                   (static_cast<long long>(s.row0) + token) * p.q_st + 8 * piece_q);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 8; ++e) {
+          const int row = first_row + kAtOnce * e;
+          const uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+          uint32_t m = 0;                                  // the largest magnitude, as bits
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m = max(m, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+          uint32_t amax = __reduce_max_sync(0xffffffffu, kAtOnce == 1 || sub == 0 ? m : 0u);
+          if (kAtOnce == 2) {
+            const uint32_t second = __reduce_max_sync(0xffffffffu, sub == 1 ? m : 0u);
+            if (sub == 1) amax = second;
+          }
           // exponent that brings the largest to [128, 256); bounded so that both powers are normal.
           // A row with an infinity or NaN becomes NaN, as its logits are.
-          const int e2 = amax[e] > 0 ? max(-100, min(100, static_cast<int>(amax[e] >> 7) - 127 - 7)) : 0;
-          const float down = amax[e] < 0x7F80u ? __uint_as_float(static_cast<uint32_t>(127 - e2) << 23) : NAN;
-          if (lane == 0) row_scale[group * 128 + tile_row + e] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+          const int e2 = amax > 0 ? max(-100, min(100, static_cast<int>(amax >> 7) - 127 - 7)) : 0;
+          const float down = amax < 0x7F80u ? __uint_as_float(static_cast<uint32_t>(127 - e2) << 23) : NAN;
+          if (piece_q == 0) row_scale[group * 128 + row] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+          uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
-          for (int ch = 0; ch < C::kCh; ++ch) {
-            const uint32_t w[2] = {v[e][ch].x, v[e][ch].y};
-            uint32_t hi = 0, lo = 0;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              // (eight significant bits and at most 256: f16 holds what the two terms can)
-              const uint32_t x = pack_f16x2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
-              const uint32_t c0 = f16x2_to_e4m3x2(x);
-              hi |= c0 << (16 * k);
-              lo |= f16x2_to_e4m3x2(sub_f16x2(x, e4m3x2_to_f16x2(c0))) << (16 * k);
-            }
-            const uint32_t at = swz128(ch * 16384, tile_row + e, lane >> 2) + (lane & 3) * 4;
-            asm volatile("st.shared.b32 [%0], %1;" :: "r"(s_q(group, 0) + at), "r"(hi) : "memory");
-            asm volatile("st.shared.b32 [%0], %1;" :: "r"(s_q(group, 1) + at), "r"(lo) : "memory");
+          for (int k = 0; k < 4; ++k) {
+            // (eight significant bits and at most 256: f16 holds what the two terms can)
+            const uint32_t x = pack_f16x2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
+            const uint32_t c0 = f16x2_to_e4m3x2(x);
+            hi[k >> 1] |= c0 << (16 * (k & 1));
+            lo[k >> 1] |= f16x2_to_e4m3x2(sub_f16x2(x, e4m3x2_to_f16x2(c0))) << (16 * (k & 1));
           }
+          const uint32_t at = swz128((piece_q >> 4) * 16384, row, (piece_q & 15) >> 1) + (piece_q & 1) * 8;
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" :: "r"(s_q(group, 0) + at), "r"(hi[0]), "r"(hi[1]) : "memory");
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" :: "r"(s_q(group, 1) + at), "r"(lo[0]), "r"(lo[1]) : "memory");
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_q_full);
+      {
+        // the next segment's rows of Q into L2 meanwhile
+        Segment t;
+        Walk w = walk;
+        if (w.next<kGroups>(p, t)) {
+          for (int r = tid; r < (t.split ? 128 : C::kRows); r += 128) {
+            const int row = r & 127, tok = row / p.G, token = t.tok0 + (r >> 7) * p.tt + tok;
+            if (tok >= p.tt || token >= t.n) continue;
+            const __nv_bfloat16* const src =
+                p.q + (t.h * p.G + (row - tok * p.G)) * p.q_sh + (static_cast<long long>(t.row0) + token) * p.q_st;
+            for (int c = 0; c < p.c.d; c += 64) asm volatile("prefetch.global.L2 [%0];" :: "l"(src + c));
+          }
+        }
+      }
       // ---- V: 16 codes of a key at a time
       constexpr int kPieces = D / 16;                      // of a key
       const int piece = tid % kPieces, key0 = tid / kPieces;
@@ -753,28 +768,33 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           const int valid = s.len - j * 128 - x * C::kKeysV;
           const bool here0 = there[C::kPerTile == 1 ? 2 : 4 * x + 2] != 0.f, here1 = there[6] != 0.f;
           const uint32_t src = s_codes(slot) + (piece >> 3) * 8192, dst = s_half(slot) + (piece >> 2) * C::kBoxV;
-          const int u0 = 2 * (piece & 3), flip = (piece >> 2) & 1;     // (every other box the second unit first: no bank twice)
+          const int u0 = 2 * (piece & 3);
           if (16 * piece < p.c.d) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int key = key0 + i * (128 / kPieces);
-              uint4 w = make_uint4(0, 0, 0, 0);
-              if (key < valid && (key < 64 ? here0 : here1))
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                             : "r"(swz128(src, key, piece & 7)) : "memory");
-              uint32_t f[8];
-              const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+            for (int i0 = 0; i0 < 8; i0 += 4) {
+              uint4 w[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                f[2 * e] = e4m3x2_to_f16x2(in[e] & 0xFFFFu);
-                f[2 * e + 1] = e4m3x2_to_f16x2(in[e] >> 16);
+              for (int i = 0; i < 4; ++i) {
+                const int key = key0 + (i0 + i) * (128 / kPieces);
+                w[i] = make_uint4(0, 0, 0, 0);
+                if (key < valid && (key < 64 ? here0 : here1))
+                  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                               : "r"(swz128(src, key, piece & 7)) : "memory");
               }
-              if (flip) {
-                store16(swz128(dst, key, u0 + 1), f[4], f[5], f[6], f[7]);
-                store16(swz128(dst, key, u0), f[0], f[1], f[2], f[3]);
-              } else {
-                store16(swz128(dst, key, u0), f[0], f[1], f[2], f[3]);
-                store16(swz128(dst, key, u0 + 1), f[4], f[5], f[6], f[7]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int key = key0 + (i0 + i) * (128 / kPieces);
+                uint32_t f[8];
+                const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  f[2 * e] = e4m3x2_to_f16x2(in[e] & 0xFFFFu);
+                  f[2 * e + 1] = e4m3x2_to_f16x2(in[e] >> 16);
+                }
+                // (every other box the second unit first: no bank twice)
+                const bool flip = (piece >> 2) & 1;
+                store16(swz128(dst, key, u0 + flip), flip ? f[4] : f[0], flip ? f[5] : f[1], flip ? f[6] : f[2], flip ? f[7] : f[3]);
+                store16(swz128(dst, key, u0 + !flip), flip ? f[0] : f[4], flip ? f[1] : f[5], flip ? f[2] : f[6], flip ? f[3] : f[7]);
               }
             }
           }

@@ -367,21 +367,26 @@ def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, 
         for split, n0, n in segments:
             for x in range(n):
                 t, g = t0 + x, x & 1 if split else 1
-                if k_first:
-                    yield from k_there(t)
-                if not s_first:
-                    yield from run.wait(v_full[t & 1], (t >> 1) & 1, f"watcher V {t}", t >> 1)
-                yield from run.wait(s_full[g], ns[g] & 1, f"watcher S {t}", ns[g])
-                ns[g] += 1
-                k_empty[t % ring_k].arrive()
-                while v_back <= (t - v_late if split and x > 0 else t - 1):
-                    v_empty[v_back & 1].arrive()
-                    v_back += 1
-                if s_first:
-                    yield from run.wait(v_full[t & 1], (t >> 1) & 1, f"watcher V {t}", t >> 1)
+                early = (split or x == 0) and s_first
+
+                def s_done():
+                    yield from run.wait(s_full[g], ns[g] & 1, f"watcher S {t}", ns[g])
+                    ns[g] += 1
+                    k_empty[t % ring_k].arrive()
+                    nonlocal v_back
+                    while v_back <= (t - v_late if split and x > 0 else t - 1):
+                        v_empty[v_back & 1].arrive()
+                        v_back += 1
+                if early:
+                    if k_first:
+                        yield from k_there(t)
+                    yield from s_done()
+                yield from run.wait(v_full[t & 1], (t >> 1) & 1, f"watcher V {t}", t >> 1)
                 yield from k_there(t0 + min(n - 1, x + 2 if split else x + 1))
                 if not split and x < n0:
                     yield from hand(0)
+                if not early:
+                    yield from s_done()
                 yield from hand(g)
                 yield run.delay(20, 500)
             if not split:
