@@ -27,7 +27,7 @@
 // gives its even key tiles to one softmax group and its odd ones to the other, joined in TMEM.
 //
 // Warps: 0-3 and 4-7 the softmax groups (one thread per row), 8 producer (block table, scales,
-// TMA), 9 tensor-core issuer, 10 ring watcher, 12-15 converters. At d > 128 (kGroups = 1) O takes half of TMEM, S is
+// TMA), 9 tensor-core issuer, 10 ring watcher, 11 scheduler, 12-15 converters. At d > 128 (kGroups = 1) O takes half of TMEM, S is
 // double-buffered and warps 4-7 rest.
 #include <type_traits>
 
@@ -41,7 +41,8 @@ constexpr float kTrailL = 8.f;            // log2 of how far the references may 
 constexpr float kTopO = 7.f, kTrailO = 15.f;   // P' of the row's largest is 2^7 where mo is set, at most 2^15
 constexpr float kNoKey = -1.f;            // factor of O for a row that sees no key
 constexpr int kInfo = 8;                  // tiles whose scales wait in shared memory
-constexpr int kStateInts = 20;            // a softmax warp's place on the line and its segment, kept in shared memory
+constexpr int kItems = 4;                 // segments that the scheduler may be ahead
+constexpr int kItemInts = 12;
 constexpr int kTurn = 1;                  // key tiles' time that a change of items costs
 
 template <int D>
@@ -49,6 +50,7 @@ struct Cfg {
   static constexpr int kGroups = D == 128 ? 2 : 1;
   static constexpr int kCh = D / 128;                      // 128-byte columns of codes
   static constexpr int kRows = 128 * kGroups;              // of an item
+  static constexpr int kReaders = 6 + (kGroups == 2 ? 1 : 0) + 4 * kGroups;   // warps that read a segment: producer, issuer, watcher, converters, softmax
   static constexpr int kKeysV = D == 128 ? 128 : 64;       // keys of a V stage
   static constexpr int kPerTile = 128 / kKeysV;            // V stages of a key tile
   static constexpr int kQTerm = 16384 * kCh;               // one term of a row tile
@@ -60,8 +62,8 @@ struct Cfg {
   static constexpr int kBoxV = kKeysV * 128;               // 64 columns of halves
   static constexpr int kOffK = kQBytes, kOffCodes = kOffK + kRingK * kTileK, kOffHalf = kOffCodes + kRingV * kCodesV;
   static constexpr int kOffStat = kOffHalf + kRingV * kHalfV;
-  static constexpr int kStat = kRows * 4 + (kGroups == 2 ? 128 * 12 : 0) + kInfo * 32 + (4 * kGroups + 1) * kStateInts * 4;
-  static constexpr int kLayout = kOffStat + kStat + 208;
+  static constexpr int kStat = kRows * 4 + (kGroups == 2 ? 128 * 12 : 0) + kInfo * 32 + kItems * kItemInts * 4;
+  static constexpr int kLayout = kOffStat + kStat + 272;
   static constexpr int kSmem = kLayout + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   // setmaxnreg, of the 512 x 128 launched: without spills, which L1 beside so much shared memory does not hold
@@ -177,10 +179,10 @@ struct Line {
 
 // A place of the line: `off` places into an item (its turn, then its units).
 struct Place {
-  int b, h, item, off;
-  long long start;                                         // places before the item
+  int b = 0, h = 0, item = 0, off = 0;
+  long long start = 0;                                     // places before the item
   // by a whole warp; u below the total
-  __device__ __forceinline__ Place(const ChunkParams& p, int turn, long long u, int lane) {
+  __device__ __forceinline__ void find(const ChunkParams& p, int turn, long long u, int lane) {
     long long before = 0, each = 0;
     b = p.B - 1;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
@@ -234,33 +236,8 @@ struct Walk {
   int b, h, item, off, turn;
   long long left;
   Sequence s;
-  __device__ __forceinline__ Walk(const ChunkParams& p, const volatile int* at)
-      : b(at[0]), h(at[1]), item(at[2]), off(at[3]), turn(at[4]),
-        left(static_cast<long long>(static_cast<unsigned>(at[5])) | static_cast<long long>(at[6]) << 32), s(p, at[0]) {}
-  // to and from ten ints of shared memory
-  __device__ __forceinline__ void save(volatile int* m) const {
-    m[0] = b;
-    m[1] = h;
-    m[2] = item;
-    m[3] = off;
-    m[4] = turn;
-    m[5] = static_cast<int>(left);
-    m[6] = static_cast<int>(left >> 32);
-    m[7] = s.row0;
-    m[8] = s.n;
-    m[9] = s.len;
-  }
-  __device__ __forceinline__ void restore(const volatile int* m) {
-    b = m[0];
-    h = m[1];
-    item = m[2];
-    off = m[3];
-    turn = m[4];
-    left = static_cast<long long>(static_cast<unsigned>(m[5])) | static_cast<long long>(m[6]) << 32;
-    s.row0 = m[7];
-    s.n = m[8];
-    s.len = m[9];
-  }
+  __device__ __forceinline__ Walk(const ChunkParams& p, const Place& at, int line_turn, long long length)
+      : b(at.b), h(at.h), item(at.item), off(at.off), turn(line_turn), left(length), s(p, at.b) {}
   template <int kGroups>
   __device__ __forceinline__ bool next(const ChunkParams& p, Segment& g) {
     if (left <= 0) return false;
@@ -291,6 +268,13 @@ struct Walk {
     }
     return g.t1 > g.t0;                                    // (false: the part ends in a turn)
   }
+};
+
+// A segment as the scheduler hands it on: the ints of its slot, and what most roles go by.
+enum { kB, kH, kRow0, kNew, kLen, kTok0, kT0, kN, kN0, kSplit, kWhole };
+struct Item {
+  int n, n0;                                               // key tiles; group 0's (not split)
+  bool split;
 };
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -335,7 +319,7 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   float* const row_scale = reinterpret_cast<float*>(gbase + C::kOffStat);           // [kRows] what Q's rows were divided by
   float* const other = row_scale + C::kRows;                                       // [3][128] group 1's ml, mo, l (split)
   volatile float* const info = reinterpret_cast<volatile float*>(other + (kGroups == 2 ? 3 * 128 : 0));   // [kInfo][8]: per half K scale, log2 of V's, there
-  volatile int* const states = reinterpret_cast<volatile int*>(gbase + C::kOffStat + C::kStat - (4 * kGroups + 1) * kStateInts * 4);
+  volatile int* const items = reinterpret_cast<volatile int*>(gbase + C::kOffStat + C::kStat - kItems * kItemInts * 4);
   const uint32_t bars = base + C::kOffStat + C::kStat;
   uint8_t* const gbars = gbase + (bars - base);
   auto bar_k_full = [&](int i) { return bars + 8u * i; };              // 3
@@ -349,10 +333,11 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   auto bar_o_final = [&](int i) { return bars + 144u + 8u * i; };
   const uint32_t bar_q_full = bars + 160u, bar_q_empty = bars + 168u;
   const uint32_t bar_other_full = bars + 176u, bar_other_empty = bars + 184u;
-  const uint32_t bar_stall = bars + 192u;                              // nothing arrives (timeout test)
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbars + 200);
-  volatile int* const abort_flag = reinterpret_cast<volatile int*>(gbars + 204);
-  volatile int* const first = reinterpret_cast<volatile int*>(row_scale);          // [7] the part's first place, until the roles begin
+  auto bar_item_full = [&](int i) { return bars + 192u + 8u * i; };    // kItems
+  auto bar_item_empty = [&](int i) { return bars + 224u + 8u * i; };
+  const uint32_t bar_stall = bars + 256u;                              // nothing arrives (timeout test)
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbars + 264);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(gbars + 268);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -374,6 +359,10 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     mbar_init(bar_q_empty, 1 + 4 * kGroups);               // its products done, its scales read by every softmax warp
     mbar_init(bar_other_full, 128);
     mbar_init(bar_other_empty, 128);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(bar_item_full(i), 1);
+      mbar_init(bar_item_empty(i), C::kReaders);
+    }
     mbar_init(bar_stall, 1);
     fence_mbar_init();
   }
@@ -381,30 +370,35 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     tmem_alloc(smem_addr(tmem_slot), 512);
     tmem_relinquish();
   }
-  if (warp == 2) {
-    const Line line(p, lane);
-    int at[7] = {0, 0, 0, 0, 0, 0, 0};
-    if (static_cast<int>(blockIdx.x) < line.parts) {
-      const long long u = line.begin(blockIdx.x), n = line.begin(blockIdx.x + 1) - u;
-      const Place place(p, line.turn, u, lane);
-      at[0] = place.b;
-      at[1] = place.h;
-      at[2] = place.item;
-      at[3] = place.off;
-      at[4] = line.turn;
-      at[5] = static_cast<int>(n);
-      at[6] = static_cast<int>(n >> 32);
-    }
-    if (lane == 0)
-#pragma unroll
-      for (int i = 0; i < 7; ++i) first[i] = at[i];
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  Walk walk(p, first);
-  __syncthreads();                                         // (row_scale is the converters' from here on)
+
+  // What the scheduler says of segment n of this part, as a thread or a warp reads it; false: there is none, or a wait ran
+  // out. `done` gives its slot back, once per warp.
+  auto take_one = [&](int n, Item& it) -> bool {
+    if (!wait(bar_item_full(n % kItems), (n / kItems) & 1, abort_flag, p.timeout_ns)) return false;
+    const volatile int* const m = items + (n % kItems) * kItemInts;
+    it.n = m[kN];
+    it.n0 = m[kN0];
+    it.split = m[kSplit];
+    return it.n > 0;
+  };
+  auto take = [&](int n, Item& it) -> bool {
+    const bool ok = wait(bar_item_full(n % kItems), (n / kItems) & 1, abort_flag, p.timeout_ns);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    const volatile int* const m = items + (n % kItems) * kItemInts;
+    it.n = m[kN];
+    it.n0 = m[kN0];
+    it.split = m[kSplit];
+    return it.n > 0;
+  };
+  auto field = [&](int n, int which) { return items[(n % kItems) * kItemInts + which]; };
+  auto done = [&](int n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_item_empty(n % kItems));
+  };
 
   if (warp == 8) {
     // ------------------------------------------------------------ producer
@@ -415,10 +409,12 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     }
     int tile = 0;                                          // tiles so far
     bool ok = true;
-    Segment s;
-    while (ok && walk.next<kGroups>(p, s)) {
-      const int* const table = p.table + static_cast<long long>(s.b) * p.max_blocks;
-      const int held = min(2 * s.t1, (s.len + kCacheBlock - 1) / kCacheBlock);
+    Item it;
+    for (int seg = 0; ok && take(seg, it); ++seg) {
+      const int blk0 = 2 * field(seg, kT0), blk1 = blk0 + 2 * it.n, h = field(seg, kH);
+      const int* const table = p.table + static_cast<long long>(field(seg, kB)) * p.max_blocks;
+      const int held = min(blk1, (field(seg, kLen) + kCacheBlock - 1) / kCacheBlock);
+      done(seg);
       // 32 blocks at a time, one per lane; the next 32 are looked up while these are loaded
       auto page_of = [&](int blk) {
         const int page = blk + lane < held ? table[blk + lane] : -1;
@@ -427,16 +423,16 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       float ks = 0.f, vs = 0.f;
       int z = -1;
       auto scales_of = [&](int page) {
-        const long long ph = page >= 0 ? static_cast<long long>(page) * p.c.Hkv + s.h : -1;
+        const long long ph = page >= 0 ? static_cast<long long>(page) * p.c.Hkv + h : -1;
         ks = page >= 0 ? p.c.k_scale[ph] : 0.f;
         vs = page >= 0 ? p.c.v_scale[ph] : 0.f;
         z = static_cast<int>(ph);
       };
-      scales_of(page_of(2 * s.t0));
-      for (int blk = 2 * s.t0; blk < 2 * s.t1 && ok; blk += 32) {
+      scales_of(page_of(blk0));
+      for (int blk = blk0; blk < blk1 && ok; blk += 32) {
         const float ks_now = ks, vs_now = vs;
         const int z_now = z, next_page = page_of(blk + 32);
-        for (int i = 0; i < 32 && blk + i < 2 * s.t1 && ok; i += 2, ++tile) {
+        for (int i = 0; i < 32 && blk + i < blk1 && ok; i += 2, ++tile) {
           const int za = __shfl_sync(0xffffffffu, z_now, i), zb = __shfl_sync(0xffffffffu, z_now, i + 1);
           const int slot = tile % C::kRingK;
           if (lane == 0) {
@@ -551,21 +547,12 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         np ^= 1u << buf;
         tc_fence_after();
       };
-      volatile int* const state = states + 4 * kGroups * kStateInts;
-      walk.save(state);
+      Item it;
       for (;; ++seg) {
-        int n, n0;
-        bool split;
-        {
-          Segment s;
-          Walk w = walk;
-          w.restore(state);
-          if (!ok || !w.next<kGroups>(p, s)) break;
-          w.save(state);
-          n = s.t1 - s.t0;
-          n0 = s.n0;
-          split = s.split;
-        }
+        if (!ok || !take_one(seg, it)) break;
+        mbar_arrive(bar_item_empty(seg % kItems));
+        const int n = it.n, n0 = it.n0;
+        const bool split = it.split;
         ok = wait(bar_q_full, seg & 1, abort_flag, p.timeout_ns);
         if (!ok) break;
         if (kGroups == 1) {
@@ -632,7 +619,7 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     // waits for every load in order, so no parity is taken for that of two phases earlier.
     setmaxnreg_dec<C::kRegsOther>();
     if (lane == 0) {
-      Segment s;
+      Item s;
       bool ok = true;
       int tile = 0, k_seen = 0, v_back = 0;                // tiles before the segment, K tiles waited for, V stages handed back
       uint32_t ns0 = 0, ns1 = 0, np0 = 0, np1 = 0;         // phases of S and of P-ready
@@ -643,8 +630,10 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         if (ok) mbar_arrive(bar_p_ready(g));
         ++np;
       };
-      while (ok && walk.next<kGroups>(p, s)) {
-        const int n = s.t1 - s.t0;
+      for (int seg = 0;; ++seg) {
+        if (!ok || !take_one(seg, s)) break;
+        mbar_arrive(bar_item_empty(seg % kItems));
+        const int n = s.n;
         for (int x = 0; x < n && ok; ++x) {
           const int t = tile + x, g = s.split ? x & 1 : 1;
           auto k_there = [&](int last) {
@@ -684,34 +673,45 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     const int cw = warp - 12, tid = threadIdx.x - 384;
     bool ok = true;
     int tile = 0;
-    Segment s;
-    for (int seg = 0; ok && walk.next<kGroups>(p, s); ++seg) {
-      // ---- Q: 16 bytes a lane, eight loads of a warp under way together; this warp's 32 rows of each row tile. The
-      // rows are in L2 by now (below), as all other warps wait for this once the last S is done.
+    Item it;
+    for (int seg = 0; ok && take(seg, it); ++seg) {
+      const int len = field(seg, kLen), t0 = field(seg, kT0);
+      // ---- Q: 16 bytes a lane, four loads of a warp under way; this warp's 32 rows of each row tile. The rows are in L2 by
+      // now (the scheduler). All wait for this once the last S is done, and its code comes from memory nearly every
+      // time: unrolled eightfold it took 45000 cycles, at about 230 for 128 bytes of it.
       ok = wait(bar_q_empty, (seg & 1) ^ 1, abort_flag, p.timeout_ns);
       if (!__all_sync(0xffffffffu, ok)) break;
       constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes; // lanes of a row, rows of a load
       const int piece_q = lane % kLanes, sub = lane / kLanes;
+      const int step_tok = kAtOnce / p.G, step_head = kAtOnce - step_tok * p.G;
 #pragma unroll 1
-      for (int r0 = 0; r0 < (s.split ? 128 : C::kRows); r0 += 32 * kAtOnce) {
-        uint4 v[8];
-        const int group = r0 >> 7, first_row = (r0 & 127) + 8 * kAtOnce * cw + sub;   // rows first_row + kAtOnce * e
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int row = first_row + kAtOnce * e, tok = row / p.G, token = s.tok0 + group * p.tt + tok;
-          v[e] = make_uint4(0, 0, 0, 0);
-          if (tok < p.tt && token < s.n && 8 * piece_q < p.c.d)
-            v[e] = *reinterpret_cast<const uint4*>(p.q + (s.h * p.G + (row - tok * p.G)) * p.q_sh +
-                                                   (static_cast<long long>(s.row0) + token) * p.q_st + 8 * piece_q);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int row = first_row + kAtOnce * e;
-          const uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+      for (int group = 0; group < (it.split ? 1 : kGroups); ++group) {
+        int tok = (32 * cw + sub) / p.G, head = 32 * cw + sub - tok * p.G;   // of the next load
+        const int first_token = field(seg, kTok0) + group * p.tt, left = min(p.tt, field(seg, kNew) - first_token);
+        const __nv_bfloat16* const src = p.q + static_cast<long long>(field(seg, kH) * p.G) * p.q_sh +
+                                         (static_cast<long long>(field(seg, kRow0)) + first_token) * p.q_st + 8 * piece_q;
+        uint4 v[4];
+#pragma unroll 1
+        for (int i = -4; i < 32 / kAtOnce; ++i) {
+          const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+          v[0] = v[1];
+          v[1] = v[2];
+          v[2] = v[3];
+          v[3] = make_uint4(0, 0, 0, 0);
+          if (i + 4 < 32 / kAtOnce && tok < left && 8 * piece_q < p.c.d)
+            v[3] = *reinterpret_cast<const uint4*>(src + head * p.q_sh + tok * p.q_st);
+          tok += step_tok;
+          head += step_head;
+          if (head >= p.G) {
+            head -= p.G;
+            ++tok;
+          }
+          if (i < 0) continue;
+          const int row = 32 * cw + sub + kAtOnce * i;
           uint32_t m = 0;                                  // the largest magnitude, as bits
 #pragma unroll
           for (int k = 0; k < 4; ++k) m = max(m, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-          uint32_t amax = __reduce_max_sync(0xffffffffu, kAtOnce == 1 || sub == 0 ? m : 0u);
+          uint32_t amax = __reduce_max_sync(0xffffffffu, sub == 0 ? m : 0u);
           if (kAtOnce == 2) {
             const uint32_t second = __reduce_max_sync(0xffffffffu, sub == 1 ? m : 0u);
             if (sub == 1) amax = second;
@@ -738,24 +738,11 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_q_full);
-      {
-        // the next segment's rows of Q into L2 meanwhile
-        Segment t;
-        Walk w = walk;
-        if (w.next<kGroups>(p, t)) {
-          for (int r = tid; r < (t.split ? 128 : C::kRows); r += 128) {
-            const int row = r & 127, tok = row / p.G, token = t.tok0 + (r >> 7) * p.tt + tok;
-            if (tok >= p.tt || token >= t.n) continue;
-            const __nv_bfloat16* const src =
-                p.q + (t.h * p.G + (row - tok * p.G)) * p.q_sh + (static_cast<long long>(t.row0) + token) * p.q_st;
-            for (int c = 0; c < p.c.d; c += 64) asm volatile("prefetch.global.L2 [%0];" :: "l"(src + c));
-          }
-        }
-      }
+      done(seg);
       // ---- V: 16 codes of a key at a time
       constexpr int kPieces = D / 16;                      // of a key
       const int piece = tid % kPieces, key0 = tid / kPieces;
-      for (int j = s.t0; j < s.t1 && ok; ++j, ++tile) {
+      for (int j = t0; j < t0 + it.n && ok; ++j, ++tile) {
         const volatile float* const there = info + (tile % kInfo) * 8;
 #pragma unroll
         for (int x = 0; x < C::kPerTile; ++x) {
@@ -765,12 +752,12 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           // keys of the stage that there are, in each of its blocks
-          const int valid = s.len - j * 128 - x * C::kKeysV;
+          const int valid = len - j * 128 - x * C::kKeysV;
           const bool here0 = there[C::kPerTile == 1 ? 2 : 4 * x + 2] != 0.f, here1 = there[6] != 0.f;
           const uint32_t src = s_codes(slot) + (piece >> 3) * 8192, dst = s_half(slot) + (piece >> 2) * C::kBoxV;
           const int u0 = 2 * (piece & 3);
           if (16 * piece < p.c.d) {
-#pragma unroll
+#pragma unroll 1
             for (int i0 = 0; i0 < 8; i0 += 4) {
               uint4 w[4];
 #pragma unroll
@@ -808,6 +795,52 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       }
     }
     __syncwarp();
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ scheduler
+    // Finds this part's segments ahead of time: one warp's look-up instead of all roles', whose code for it would come
+    // from memory at every change. And brings the segment's rows of Q into L2.
+    setmaxnreg_dec<C::kRegsOther>();
+    const Line line(p, lane);
+    bool ok = true;
+    long long u = 0, length = 0;
+    Place place;
+    if (static_cast<int>(blockIdx.x) < line.parts) {
+      u = line.begin(blockIdx.x);
+      length = line.begin(blockIdx.x + 1) - u;
+      place.find(p, line.turn, u, lane);
+    }
+    Walk walk(p, place, line.turn, length);
+    Segment s;
+    for (int n = 0; ok; ++n) {
+      const bool more = walk.next<kGroups>(p, s);
+      if (n >= kItems) ok = wait(bar_item_empty(n % kItems), ((n / kItems) & 1) ^ 1, abort_flag, p.timeout_ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) {
+        volatile int* const m = items + (n % kItems) * kItemInts;
+        m[kB] = s.b;
+        m[kH] = s.h;
+        m[kRow0] = s.row0;
+        m[kNew] = s.n;
+        m[kLen] = s.len;
+        m[kTok0] = s.tok0;
+        m[kT0] = s.t0;
+        m[kN] = more ? s.t1 - s.t0 : 0;
+        m[kN0] = s.n0;
+        m[kSplit] = s.split;
+        m[kWhole] = s.t0 == 0 && s.t1 == s.tiles;
+        mbar_arrive(bar_item_full(n % kItems));
+      }
+      __syncwarp();
+      if (!more) break;
+      for (int r = lane; r < (s.split ? 128 : C::kRows); r += 32) {
+        const int row = r & 127, tok = row / p.G, token = s.tok0 + (r >> 7) * p.tt + tok;
+        if (tok >= p.tt || token >= s.n) continue;
+        const __nv_bfloat16* const src =
+            p.q + (s.h * p.G + (row - tok * p.G)) * p.q_sh + (static_cast<long long>(s.row0) + token) * p.q_st;
+        for (int c = 0; c < p.c.d; c += 64) asm volatile("prefetch.global.L2 [%0];" :: "l"(src + c));
+      }
+    }
+    __syncwarp();
   } else if (warp >= 8) {
     setmaxnreg_dec<C::kRegsOther>();
   } else {
@@ -817,38 +850,21 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     const int quarter = warp & 3;                          // TMEM lane quarter this warp may access
     const int row = quarter * 32 + lane;                   // of the row tile
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    volatile int* const state = states + (warp & (4 * kGroups - 1)) * kStateInts;   // (registers hold a tile of S)
-    uint32_t par = 0;                                      // parities: bit 0 S, 1 O final, 2 group 1's results, 3 Q; 4: not the first segment
+    uint32_t tile = 0;                                     // tiles before the segment
+    uint32_t par = 0;                                      // parities: bit 0 S, 1 O final, 2 group 1's results, 3 Q
     bool ok = g < kGroups;
-    if (ok) {
-      walk.save(state);
-      state[17] = 0;                                       // tiles before the segment
-    }
-    while (ok) {
+    for (int seg = 0; ok; ++seg) {
       uint32_t at, end;                                    // this group's tiles at, at + dx, ... below end, counted from the kernel's start
       int dx, lim;                                         // lim: keys that this row sees from the tile on
       {
-        Segment s;
-        Walk w = walk;
-        __syncwarp();
-        w.restore(state);
-        if (!w.next<kGroups>(p, s)) break;
-        __syncwarp();
-        w.save(state);
-        state[10] = s.h;
-        state[11] = s.row0;
-        state[12] = s.n;
-        state[13] = s.tok0;
-        state[16] = s.t0 == 0 && s.t1 == s.tiles;
-        const uint32_t tile = state[17];
-        __syncwarp();
-        state[17] = tile + s.t1 - s.t0;
-        const int x = s.split ? g : 0;
-        dx = s.split ? 2 : 1;
-        at = tile + x;
-        end = tile + (s.split || g == 1 || kGroups == 1 ? s.t1 - s.t0 : s.n0);
-        const int last = s.tok0 + (s.split ? 0 : g * p.tt) + row / p.G + 1;   // tokens up to this row's
-        lim = (p.causal ? min(s.len, s.len - s.n + last) : s.len) - (s.t0 + x) * 128;
+        Item it;
+        if (!take(seg, it)) break;
+        at = tile + (it.split ? g : 0);
+        dx = it.split ? 2 : 1;
+        end = tile + (it.split || g == 1 || kGroups == 1 ? it.n : it.n0);
+        tile += it.n;
+        const int len = field(seg, kLen), last = field(seg, kTok0) + (it.split ? 0 : g * p.tt) + row / p.G + 1;   // tokens up to this row's
+        lim = (p.causal ? min(len, len - field(seg, kNew) + last) : len) - (field(seg, kT0) + (it.split ? g : 0)) * 128;
       }
       const bool any = at < end, split = dx == 2;
       ok = wait(bar_q_full, par >> 3 & 1u, abort_flag, p.timeout_ns);
@@ -886,11 +902,14 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #pragma unroll
         for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(sr[i >> 5][i & 31]);
         if (lim < 128 || !here_a || !here_b) {
-          const int la = here_a ? lim : 0, lb = here_b ? lim : 0;
+          // (by bits: fewer instructions, and these come from memory each time)
 #pragma unroll
-          for (int i = 0; i < 64; ++i) v[i] = i < la ? v[i] : -INFINITY;
+          for (int q4 = 0; q4 < 4; ++q4) {
+            const int n = (q4 < 2 ? here_a : here_b) ? lim - 32 * q4 : 0;
+            const uint32_t seen = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
 #pragma unroll
-          for (int i = 64; i < 128; ++i) v[i] = i < lb ? v[i] : -INFINITY;
+            for (int i = 0; i < 32; ++i) v[32 * q4 + i] = (seen >> i & 1u) ? v[32 * q4 + i] : -INFINITY;
+          }
         }
         float mk[4];
 #pragma unroll
@@ -944,6 +963,7 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #pragma unroll
           for (int c0 = 0; c0 < D; c0 += 32) {
             if (c0 >= p.c.d) continue;
+
             uint32_t o[32];
             tmem_ld_32x32b_x32(t_o + c0, o);
             tmem_wait_ld();
@@ -978,7 +998,7 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         ok = __all_sync(0xffffffffu, ok);
         par ^= 4u;
         tc_fence_after();
-        par |= 16u;
+        done(seg);
         continue;
       }
       float f0 = 1.f, f1 = kNoKey;                         // factors of this group's O and of the other's
@@ -1000,11 +1020,11 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           mo = mm;
         }
       }
-      const bool whole = state[16];
-      const int tok = row / p.G, token = state[13] + (split ? 0 : g * p.tt) + tok;   // counted from the sequence's first new one
-      const bool real = tok < p.tt && token < state[12];
-      const int head = state[10] * p.G + (row - tok * p.G);
-      const long long at_row = static_cast<long long>(state[11]) + token;
+      const bool whole = field(seg, kWhole);
+      const int tok = row / p.G, token = field(seg, kTok0) + (split ? 0 : g * p.tt) + tok;   // counted from the sequence's first new one
+      const bool real = tok < p.tt && token < field(seg, kNew);
+      const int head = field(seg, kH) * p.G + (row - tok * p.G);
+      const long long at_row = static_cast<long long>(field(seg, kRow0)) + token;
       const int slot_row = (split ? 0 : g * 128) + row;
       float* part = nullptr;
       if (whole) {
@@ -1013,7 +1033,7 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         f1 = f1 == kNoKey ? kNoKey : f1 * factor;
         if (real) p.lse[static_cast<long long>(head) * p.T + at_row] = l == 0.f ? -INFINITY : (ml + log2f(l)) * kLn2;
       } else {
-        const int slot = 2 * blockIdx.x + (par >> 4);
+        const int slot = 2 * blockIdx.x + (seg > 0);
         part = p.part_o + static_cast<long long>(slot) * C::kRows * D;
         float* const st = p.part_s + static_cast<long long>(slot) * C::kRows * 3;
         if (real) {
@@ -1022,10 +1042,10 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           st[2 * C::kRows + slot_row] = l;
         }
       }
+      done(seg);
       __nv_bfloat16* const dst = p.o + head * p.o_sh + at_row * p.o_st;
-#pragma unroll
-      for (int c0 = 0; c0 < D; c0 += 32) {
-        if (c0 >= p.c.d) continue;
+#pragma unroll 1
+      for (int c0 = 0; c0 < p.c.d; c0 += 32) {
         uint32_t o[32], o1[32];
         tmem_ld_32x32b_x32(tbase + lane_off + C::col_o(g) + c0, o);
         if (kGroups == 2 && split) tmem_ld_32x32b_x32(tbase + lane_off + C::col_o(1) + c0, o1);
@@ -1055,7 +1075,6 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       }
       tc_fence_before();
       if (kGroups == 2 && split) mbar_arrive(bar_other_empty);
-      par |= 16u;
     }
   }
 
@@ -1085,7 +1104,8 @@ __global__ void __launch_bounds__(kJoinThreads) cache8_chunk_join_kernel(const C
     int c0 = 0, c1 = -1, second = 0;
     int b = 0, h = 0, item = 0;
     if (i < line.parts) {
-      const Place place(p, line.turn, line.begin(i), lane);
+      Place place;
+      place.find(p, line.turn, line.begin(i), lane);
       if (place.off > line.turn) {
         const Sequence s(p, place.b);
         c0 = line.part_of(place.start + line.turn);

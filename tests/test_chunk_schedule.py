@@ -220,6 +220,26 @@ def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, 
     q_full, q_empty = Barrier(WARPS), Barrier(1 + (WARPS * groups if q_read else 0))
     other_full, other_emptied = Barrier(WARPS), Barrier(WARPS)
     info = [None] * infos
+    item_full, item_empty = [Barrier(1) for _ in range(4)], [Barrier(2 + WARPS + (1 if watched else 0) + WARPS * groups) for _ in range(4)]
+    ring = [None] * 4
+
+    def take(seg, who):
+        yield from run.wait(item_full[seg % 4], (seg // 4) & 1, who + " item", seg // 4)
+        if ring[seg % 4] != seg:
+            errors.append(f"{who} took {ring[seg % 4]} for {seg}")
+
+    def done(seg, who):
+        if ring[seg % 4] != seg:
+            errors.append(f"{who}: item {seg} was overwritten")
+        item_empty[seg % 4].arrive()
+
+    def scheduler():
+        for seg in range(len(segments)):
+            if seg >= 4:
+                yield from run.wait(item_empty[seg % 4], ((seg // 4) & 1) ^ 1, "scheduler", seg // 4 - 1)
+            ring[seg % 4] = seg
+            item_full[seg % 4].arrive()
+            yield run.delay(50, 3000)
     k_slot, c_slot, v_slot = [None] * ring_k, [None] * 2, [set() for _ in range(2)]
     q_now, scale_now = [set()], [set()]
     tmem_s, o_owner = [None, None], [None, None]
@@ -265,7 +285,9 @@ def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, 
 
     def producer():
         t = 0
-        for split, n0, n in segments:
+        for seg, (split, n0, n) in enumerate(segments):
+            yield from take(seg, "producer")
+            done(seg, "producer")
             for _ in range(n):
                 yield from run.wait(k_empty[t % ring_k], ((t // ring_k) & 1) ^ 1, "producer K", t // ring_k - 1)
 
@@ -308,6 +330,8 @@ def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, 
             yield from run.wait(p_ready[buf], np[buf] & 1, f"P ready {buf}", np[buf])
             np[buf] += 1
         for seg, (split, n0, n) in enumerate(segments):
+            yield from take(seg, "issuer")
+            done(seg, "issuer")
             yield from run.wait(q_full, seg & 1, "issuer Q", seg)
             if groups == 1:
                 for j in range(-1, n):
@@ -364,7 +388,9 @@ def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, 
             while k_seen <= last:
                 yield from run.wait(k_full[k_seen % ring_k], (k_seen // ring_k) & 1, f"watcher K {k_seen}", k_seen // ring_k)
                 k_seen += 1
-        for split, n0, n in segments:
+        for seg, (split, n0, n) in enumerate(segments):
+            yield from take(seg, "watcher")
+            done(seg, "watcher")
             for x in range(n):
                 t, g = t0 + x, x & 1 if split else 1
                 early = (split or x == 0) and s_first
@@ -396,6 +422,7 @@ def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, 
     def converter(w):
         t = 0
         for seg, (split, n0, n) in enumerate(segments):
+            yield from take(seg, "converter")
             yield from run.wait(q_empty, (seg & 1) ^ 1, "converter Q", seg - 1)
             q_now[0] = {x for x in q_now[0] if x[0] == seg}
             scale_now[0] = {x for x in scale_now[0] if x[0] == seg}
@@ -403,6 +430,7 @@ def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, 
             q_now[0].add((seg, w))
             scale_now[0].add((seg, w))
             q_full.arrive()
+            done(seg, "converter")
             for j in range(n):
                 for x in range(per):
                     c = t * per + x
@@ -426,6 +454,7 @@ def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, 
         for seg, (split, n0, n) in enumerate(segments):
             x0, dx = (g, 2) if split else (0, 1)
             nx = n if split or g == 1 or groups == 1 else n0
+            yield from take(seg, f"softmax {g}")
             yield from run.wait(q_full, seg & 1, f"softmax {g} Q", seg)
             yield run.delay(5, 300)
             if scale_now[0] != {(seg, x) for x in range(WARPS)} and nx > x0:
@@ -460,11 +489,13 @@ def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, 
                 if other_empty:
                     yield from run.wait(other_emptied, nm & 1, "group 1 waits for the join", nm)
                 nm += 1
+                done(seg, "softmax 1")
                 continue
             both = groups == 2 and split
             if both:
                 yield from run.wait(other_full, nm & 1, "group 0 waits for group 1", nm)
                 nm += 1
+            done(seg, f"softmax {g}")
             mine = [g] if nx > x0 else []
             mine += [1] if both and n > 1 else []
             for i in mine:
@@ -481,7 +512,7 @@ def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, 
 
     roles = [producer(), issuer(), tensor_core()] + [converter(w) for w in range(WARPS)]
     roles += [softmax_warp(g, w) for g in range(groups) for w in range(WARPS)]
-    roles += [watcher()] if watched else []
+    roles += [scheduler()] + ([watcher()] if watched else [])
     return run.go(roles, {2}, horizon, lambda: not pipe)
 
 
