@@ -301,6 +301,12 @@ __device__ __forceinline__ void mul2_b(float& d0, float& d1, float a0, float a1,
 __device__ __forceinline__ void store16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+// The lower half of an operand's descriptor (start address and leading offset), and the whole: eight-row groups 1024 bytes
+// apart, 128-byte swizzle.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+  return static_cast<uint32_t>(smem_desc_sw128(saddr, lbo_bytes, 1024));
+}
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) { return static_cast<uint64_t>(1024u >> 4 | 1u << 14 | 2u << 29) << 32 | lo; }
 __device__ __forceinline__ float times_factor(float o, float factor) { return factor == kNoKey ? 0.f : o * factor; }
 
 template <int D>
@@ -486,60 +492,38 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     if (lane == 0) {
       const uint32_t id_s = make_idesc(0, 128, 128, 0, 0);             // e4m3, both K-major
       const uint32_t id_o = make_idesc(0, 128, p.c.d, 0, 1);           // f16, V MN-major
-      // The issuing thread paces the kernel (a product takes 64 cycles, a look at a barrier 90 to 200, a commit 46):
-      // descriptors are stepped, slots and parities counted along, and a step's products stand in a row. With two
-      // groups P-ready stands for V and the next K too (the watcher's arrival), and the watcher hands the rings back.
+      // The issuing thread paces the kernel: a product takes 64 cycles, and every other instruction of this one thread
+      // about eight. So a step's products stand in a row with constant offsets, the steps between a segment's first and
+      // last ones run in a loop of their own, and with two groups P-ready stands for V and the next K too (the
+      // watcher's arrival) and the watcher hands the rings back.
       const int steps = (p.c.d + 31) / 32;                             // products over d that are not all zeros
-      const uint64_t kd0 = smem_desc_sw128(s_k(0), 16, 1024), qd0 = smem_desc_sw128(s_q(0, 0), 16, 1024);
-      const uint64_t vd0 = smem_desc_sw128(s_half(0), C::kBoxV, 1024);
+      // Descriptors by their lower halves; the upper ones are the same for all.
+      uint32_t tb = tbase;
+      const uint32_t kd0 = desc_lo(s_k(0), 16), qd0 = desc_lo(s_q(0, 0), 16), vd0 = desc_lo(s_half(0), C::kBoxV);
+      constexpr uint32_t kStepK = C::kTileK >> 4, kStepV = C::kHalfV >> 4;
       bool ok = !p.test_stall || wait(bar_stall, 0, abort_flag, p.timeout_ns);   // runs out by design
-      int seg = 0;
       uint32_t np = 0;                                                 // parities of the buffers' P-ready
-      [[maybe_unused]] int buf = 1;                                    // one group: S's buffer of the last tile
-      int k_slot = 0, v_slot = 0;                                      // of the next tile for S, of the next V stage
-      uint32_t k_par = 0, v_par = 0;
-      auto step_k = [&]() {
-        if (++k_slot == C::kRingK) {
-          k_slot = 0;
-          k_par ^= 1;
-        }
-      };
-      // S of rows `group` with K of k_slot into buffer `buf`
-      auto scores = [&](int buf, int group) {
-        const uint64_t kd = kd0 + static_cast<uint32_t>(k_slot * (C::kTileK >> 4));
-        const uint64_t qd = qd0 + static_cast<uint32_t>(group * (2 * C::kQTerm >> 4));
-        const uint32_t dst = tbase + C::col_s(buf);
-        auto row = [&](auto count) {
-          constexpr int n = decltype(count)::value;
+      int tile = 0;                                                    // tiles before the segment
+      // S of the rows behind descriptor qd with the K behind kd into buffer `buf`, d = 32 count at most
+      auto scores = [&](auto count, int buf, uint32_t qd, uint32_t kd) {
+        constexpr int n = decltype(count)::value;
+        const uint32_t dst = tb + C::col_s(buf);
 #pragma unroll
-          for (int i = 0; i < 2 * n; ++i) {
-            const int term = i / n, k = i % n, off = (k >> 2) * 16384 + (k & 3) * 32;
-            mma_fp8_ss(dst, desc_add(qd, term * C::kQTerm + off), desc_add(kd, off), id_s, i > 0);
-          }
-        };
-        constexpr int most = 4 * C::kCh;
-        if (steps == most) row(std::integral_constant<int, most>());
-        else if (steps == most - 2) row(std::integral_constant<int, most - 2>());
-        else if (steps == most - 1) row(std::integral_constant<int, most - 1>());
-        else row(std::integral_constant<int, most - 3>());
+        for (int i = 0; i < 2 * n; ++i) {
+          const int term = i / n, k = i % n, off = (k >> 2) * 16384 + (k & 3) * 32;
+          mma_fp8_ss(dst, desc_of(qd + ((term * C::kQTerm + off) >> 4)), desc_of(kd + (off >> 4)), id_s, i > 0);
+        }
         mma_commit(bar_s_full(buf));
       };
-      // O of `group` += P in buffer `buf` times a V stage
-      auto product = [&](int buf, int group, int x, bool acc) {
-        const uint64_t vd = vd0 + static_cast<uint32_t>(v_slot * (C::kHalfV >> 4));
-        const uint32_t src = tbase + C::col_s(buf) + x * (C::kKeysV / 2);
+      // O of `group` += P in buffer `buf` times the V stage behind vd, the x-th of its tile
+      auto product = [&](int buf, int group, int x, uint32_t vd, bool acc) {
+        const uint32_t src = tb + C::col_s(buf) + x * (C::kKeysV / 2);
 #pragma unroll
         for (int k = 0; k < C::kKeysV / 16; ++k)
-          mma_bf16_ts(tbase + C::col_o(group), src + k * 8, desc_add(vd, k * 2048), id_o, acc || k > 0);
+          mma_bf16_ts(tb + C::col_o(group), src + k * 8, desc_of(vd + (k * 2048 >> 4)), id_o, acc || k > 0);
       };
-      auto step_v = [&]() {
-        if (++v_slot == C::kRingV) {
-          v_slot = 0;
-          v_par ^= 1;
-        }
-      };
-      auto k_there = [&]() {
-        ok = wait(bar_k_full(k_slot), k_par, abort_flag, p.timeout_ns);
+      auto k_there = [&](int t) {
+        ok = wait(bar_k_full(t % C::kRingK), (t / C::kRingK) & 1, abort_flag, p.timeout_ns);
         tc_fence_after();
       };
       auto p_there = [&](int buf) {
@@ -547,69 +531,109 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         np ^= 1u << buf;
         tc_fence_after();
       };
-      Item it;
-      for (;; ++seg) {
-        if (!ok || !take_one(seg, it)) break;
-        mbar_arrive(bar_item_empty(seg % kItems));
-        const int n = it.n, n0 = it.n0;
-        const bool split = it.split;
-        ok = wait(bar_q_full, seg & 1, abort_flag, p.timeout_ns);
-        if (!ok) break;
-        if (kGroups == 1) {
-          // S of the next tile is out before this one's P V
-          for (int j = -1; j < n && ok; ++j) {
-            if (j + 1 < n) {
-              k_there();
-              if (!ok) break;
-              scores(buf ^ 1, 0);
-              mma_commit(bar_k_empty(k_slot));
-              step_k();
-            } else {
-              mma_commit(bar_q_empty);
-            }
-            if (j >= 0) {
-              p_there(buf);
+      auto kd_of = [&](int t) { return kd0 + static_cast<uint32_t>(t % C::kRingK) * kStepK; };
+      auto segments = [&](auto count) {
+        Item it;
+        for (int seg = 0; ok && take_one(seg, it); ++seg) {
+          mbar_arrive(bar_item_empty(seg % kItems));
+          const int n = it.n, n0 = it.n0;
+          const bool split = it.split;
+          ok = wait(bar_q_full, seg & 1, abort_flag, p.timeout_ns);
+          if (!ok) break;
+          if (kGroups == 1) {
+            // S of the next tile is out before this one's P V
+            for (int j = -1; j < n && ok; ++j) {
+              const int t = tile + j;
+              if (j + 1 < n) {
+                k_there(t + 1);
+                if (!ok) break;
+                scores(count, (t + 1) & 1, qd0, kd_of(t + 1));
+                mma_commit(bar_k_empty((t + 1) % C::kRingK));
+              } else {
+                mma_commit(bar_q_empty);
+              }
+              if (j < 0) continue;
+              p_there(t & 1);
 #pragma unroll
               for (int x = 0; x < C::kPerTile && ok; ++x) {
-                ok = wait(bar_v_full(v_slot), v_par, abort_flag, p.timeout_ns);
+                const int c = t * C::kPerTile + x, slot = c % C::kRingV;
+                ok = wait(bar_v_full(slot), (c / C::kRingV) & 1, abort_flag, p.timeout_ns);
                 if (!ok) break;
                 tc_fence_after();
-                product(buf, 0, x, j > 0 || x > 0);
-                mma_commit(bar_v_empty(v_slot));
-                step_v();
+                product(t & 1, 0, x, vd0 + slot * kStepV, j > 0 || x > 0);
+                mma_commit(bar_v_empty(slot));
               }
             }
-            if (j + 1 < n) buf ^= 1;
-          }
-          if (ok) mma_commit(bar_o_final(0));
-        } else {
-          // Step i is group i & 1's P V of a tile and its S of the next one: split, tile i, then i + 2; else tile
-          // i / 2 of either group, then the one behind it. The first two steps have no P V yet.
-          const int all = split ? n : 2 * n;
-          for (int i = -2; i < all; ++i) {
-            const int gr = i & 1, j = split ? i : i >> 1;
-            const int mine = split || gr ? n : n0, next_j = split ? i + 2 : j + 1;
-            const bool last = split || gr;
-            if (j >= mine) continue;
-            if (i >= 0) {
-              p_there(gr);
-              if (!ok) break;
-              product(gr, gr, 0, split ? i > 1 : j > 0);
-              if (last) step_v();
-            } else if (next_j < mine && (split || !gr || n0 <= 0)) {
-              k_there();
-              if (!ok) break;
+            if (ok) mma_commit(bar_o_final(0));
+          } else {
+            // Step i is group i & 1's P V of a tile and its S of the next one: split, tile i, then i + 2; else tile
+            // i / 2 of either group, then the one behind it. The first two steps have no P V yet.
+            const uint32_t qd1 = qd0 + (split ? 0 : 2 * C::kQTerm >> 4);
+            const int all = split ? n : 2 * n;
+            for (int i = -2; i < all; ++i) {
+              if (i == 0) {
+                // the steps that have a next one but not the last, two at a time: V and next K of group 0, of group 1
+                const int pairs = split ? (n - 3) / 2 : n0 - 2;
+                uint32_t va = vd0 + (tile & 1) * kStepV, vb = vd0 + ((tile + split) & 1) * kStepV;
+                const uint32_t turn_v = split ? 0u : vd0 ^ (vd0 + kStepV);
+                int ka = (tile + (split ? 2 : 1)) % C::kRingK, kb = split ? (ka + 1) % C::kRingK : ka;
+                uint32_t kda = kd0 + ka * kStepK, kdb = kd0 + kb * kStepK;
+                const uint32_t kd_end = kd0 + C::kRingK * kStepK;
+                auto step = [&](uint32_t kd) {
+                  kd += kStepK;
+                  return kd == kd_end ? kd0 : kd;
+                };
+                uint32_t par = np & 1u, par1 = np >> 1, qa = qd0, qb = qd1;
+                for (int j = 0; j < pairs; ++j) {
+                  asm volatile("" : "+r"(qa), "+r"(qb), "+r"(tb));     // (or every product's offsets get registers of their own)
+                  ok = wait(bar_p_ready(0), par, abort_flag, p.timeout_ns);
+                  if (!ok) break;
+                  tc_fence_after();
+                  product(0, 0, 0, va, j > 0);
+                  scores(count, 0, qa, kda);
+                  ok = wait(bar_p_ready(1), par1, abort_flag, p.timeout_ns);
+                  if (!ok) break;
+                  tc_fence_after();
+                  product(1, 1, 0, vb, j > 0);
+                  scores(count, 1, qb, kdb);
+                  par ^= 1u;
+                  par1 ^= 1u;
+                  va ^= turn_v;
+                  vb ^= turn_v;
+                  kda = step(kdb);
+                  kdb = split ? step(kda) : kda;
+                }
+                if (!ok) break;
+                if (pairs > 0) {
+                  np = par | par1 << 1;
+                  i = 2 * pairs;
+                }
+              }
+              const int gr = i & 1, j = split ? i : i >> 1;
+              const int mine = split || gr ? n : n0, next_j = split ? i + 2 : j + 1;
+              const bool last = split || gr;
+              if (j >= mine) continue;
+              if (i >= 0) {
+                p_there(gr);
+                if (!ok) break;
+                product(gr, gr, 0, vd0 + ((tile + j) & 1) * kStepV, split ? i > 1 : j > 0);
+              } else if (next_j < mine && (split || !gr || n0 <= 0)) {
+                k_there(tile + next_j);
+                if (!ok) break;
+              }
+              if (next_j < mine) scores(count, gr, gr ? qd1 : qd0, kd_of(tile + next_j));
+              else if (i >= 0) mma_commit(bar_o_final(gr));
+              if (last && next_j + 1 == n) mma_commit(bar_q_empty);    // every S is out
             }
-            if (next_j < mine) {
-              scores(gr, split ? 0 : gr);
-              if (last) step_k();
-            } else if (i >= 0) {
-              mma_commit(bar_o_final(gr));
-            }
-            if (last && next_j + 1 == n) mma_commit(bar_q_empty);      // every S is out
           }
+          tile += n;
         }
-      }
+      };
+      constexpr int most = 4 * C::kCh;
+      if (steps == most) segments(std::integral_constant<int, most>());
+      else if (steps == most - 2) segments(std::integral_constant<int, most - 2>());
+      else if (steps == most - 1) segments(std::integral_constant<int, most - 1>());
+      else segments(std::integral_constant<int, most - 3>());
     }
     __syncwarp();
   } else if (kGroups == 2 && warp == 10) {
@@ -670,7 +694,7 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   } else if (warp >= 12) {
     // ------------------------------------------------------------ converters
     setmaxnreg_dec<C::kRegsOther>();
-    const int cw = warp - 12, tid = threadIdx.x - 384;
+    const int cw = warp - 12;
     bool ok = true;
     int tile = 0;
     Item it;
@@ -739,9 +763,12 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_q_full);
       done(seg);
-      // ---- V: 16 codes of a key at a time
-      constexpr int kPieces = D / 16;                      // of a key
-      const int piece = tid % kPieces, key0 = tid / kPieces;
+      // ---- V: 16 codes of a key at a time, from the codes' swizzled rows to two units of the halves' rows. Eight lanes, whose
+      // 16 bytes go together, take four pieces of one box (64 columns) of keys k and k ^ 5: no bank twice, in the load
+      // or in either store. A thread's keys are 32 apart, so one address each serves with constant offsets.
+      constexpr int kBoxes = D / 64;
+      const int quad = lane & 3, key0 = 2 * ((lane >> 3) + 4 * cw) ^ (lane & 4 ? 5 : 0);
+      const uint32_t from = swz128(0, key0, quad), to = swz128(0, key0, 2 * quad);
       for (int j = t0; j < t0 + it.n && ok; ++j, ++tile) {
         const volatile float* const there = info + (tile % kInfo) * 8;
 #pragma unroll
@@ -751,38 +778,38 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           if (ok) ok = wait(bar_v_empty(slot), ((c / C::kRingV) & 1) ^ 1, abort_flag, p.timeout_ns);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          // keys of the stage that there are, in each of its blocks
+          // keys of the stage that there are, in each of its blocks; the others become 0
           const int valid = len - j * 128 - x * C::kKeysV;
           const bool here0 = there[C::kPerTile == 1 ? 2 : 4 * x + 2] != 0.f, here1 = there[6] != 0.f;
-          const uint32_t src = s_codes(slot) + (piece >> 3) * 8192, dst = s_half(slot) + (piece >> 2) * C::kBoxV;
-          const int u0 = 2 * (piece & 3);
-          if (16 * piece < p.c.d) {
+          const uint32_t src = s_codes(slot) + from, dst = s_half(slot) + to;
+          const bool all = valid >= C::kKeysV && here0 && (C::kPerTile == 2 || here1);
 #pragma unroll 1
-            for (int i0 = 0; i0 < 8; i0 += 4) {
-              uint4 w[4];
+          for (int half = 0; half < 2; ++half) {           // of the rows, four pieces each
+            const int down = half * (4 / kBoxes) * 32;
+            uint4 w[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int key = key0 + (i0 + i) * (128 / kPieces);
-                w[i] = make_uint4(0, 0, 0, 0);
-                if (key < valid && (key < 64 ? here0 : here1))
-                  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
-                               : "r"(swz128(src, key, piece & 7)) : "memory");
+            for (int e = 0; e < 4; ++e) {
+              const int box = e % kBoxes, step = 32 * (e / kBoxes);
+              if (64 * box >= p.c.d) continue;
+              const uint32_t at = (src ^ ((box & 1) * 64)) + (box >> 1) * 8192 + (down + step) * 128;
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[e].x), "=r"(w[e].y), "=r"(w[e].z), "=r"(w[e].w) : "r"(at) : "memory");
+            }
+            if (!all) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int key = key0 + down + 32 * (e / kBoxes);
+                if (!(key < valid && (key < 64 ? here0 : here1))) w[e] = make_uint4(0, 0, 0, 0);
               }
+            }
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int key = key0 + (i0 + i) * (128 / kPieces);
-                uint32_t f[8];
-                const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  f[2 * e] = e4m3x2_to_f16x2(in[e] & 0xFFFFu);
-                  f[2 * e + 1] = e4m3x2_to_f16x2(in[e] >> 16);
-                }
-                // (every other box the second unit first: no bank twice)
-                const bool flip = (piece >> 2) & 1;
-                store16(swz128(dst, key, u0 + flip), flip ? f[4] : f[0], flip ? f[5] : f[1], flip ? f[6] : f[2], flip ? f[7] : f[3]);
-                store16(swz128(dst, key, u0 + !flip), flip ? f[0] : f[4], flip ? f[1] : f[5], flip ? f[2] : f[6], flip ? f[3] : f[7]);
-              }
+            for (int e = 0; e < 4; ++e) {
+              const int box = e % kBoxes, step = 32 * (e / kBoxes);
+              if (64 * box >= p.c.d) continue;
+              const uint32_t at = box * C::kBoxV + (down + step) * 128;
+              store16(dst + at, e4m3x2_to_f16x2(w[e].x & 0xFFFFu), e4m3x2_to_f16x2(w[e].x >> 16), e4m3x2_to_f16x2(w[e].y & 0xFFFFu),
+                      e4m3x2_to_f16x2(w[e].y >> 16));
+              store16((dst ^ 16) + at, e4m3x2_to_f16x2(w[e].z & 0xFFFFu), e4m3x2_to_f16x2(w[e].z >> 16), e4m3x2_to_f16x2(w[e].w & 0xFFFFu),
+                      e4m3x2_to_f16x2(w[e].w >> 16));
             }
           }
           fence_proxy_async_smem();
