@@ -406,471 +406,7 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     if (lane == 0) mbar_arrive(bar_item_empty(n % kItems));
   };
 
-  if (warp == 8) {
-    // ------------------------------------------------------------ producer
-    setmaxnreg_dec<C::kRegsOther>();
-    if (lane == 0) {
-      tma_prefetch_map(&map_k);
-      tma_prefetch_map(&map_v);
-    }
-    int tile = 0;                                          // tiles so far
-    bool ok = true;
-    Item it;
-    for (int seg = 0; ok && take(seg, it); ++seg) {
-      const int blk0 = 2 * field(seg, kT0), blk1 = blk0 + 2 * it.n, h = field(seg, kH);
-      const int* const table = p.table + static_cast<long long>(field(seg, kB)) * p.max_blocks;
-      const int held = min(blk1, (field(seg, kLen) + kCacheBlock - 1) / kCacheBlock);
-      done(seg);
-      // 32 blocks at a time, one per lane; the next 32 are looked up while these are loaded
-      auto page_of = [&](int blk) {
-        const int page = blk + lane < held ? table[blk + lane] : -1;
-        return page < p.c.num_blocks ? page : -1;
-      };
-      float ks = 0.f, vs = 0.f;
-      int z = -1;
-      auto scales_of = [&](int page) {
-        const long long ph = page >= 0 ? static_cast<long long>(page) * p.c.Hkv + h : -1;
-        ks = page >= 0 ? p.c.k_scale[ph] : 0.f;
-        vs = page >= 0 ? p.c.v_scale[ph] : 0.f;
-        z = static_cast<int>(ph);
-      };
-      scales_of(page_of(blk0));
-      for (int blk = blk0; blk < blk1 && ok; blk += 32) {
-        const float ks_now = ks, vs_now = vs;
-        const int z_now = z, next_page = page_of(blk + 32);
-        for (int i = 0; i < 32 && blk + i < blk1 && ok; i += 2, ++tile) {
-          const int za = __shfl_sync(0xffffffffu, z_now, i), zb = __shfl_sync(0xffffffffu, z_now, i + 1);
-          const int slot = tile % C::kRingK;
-          if (lane == 0) {
-            ok = wait(bar_k_empty(slot), ((tile / C::kRingK) & 1) ^ 1, abort_flag, p.timeout_ns);
-            if (ok) mbar_expect_tx(bar_k_full(slot), ((za >= 0) + (zb >= 0)) * 8192 * C::kCh);
-            for (int ch = 0; ch < C::kCh && ok; ++ch) {
-              if (za >= 0) tma_load_3d(s_k(slot) + ch * 16384, &map_k, bar_k_full(slot), ch * 128, 0, za);
-              if (zb >= 0) tma_load_3d(s_k(slot) + ch * 16384 + 8192, &map_k, bar_k_full(slot), ch * 128, 0, zb);
-            }
-          }
-          ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
-          if (!ok) break;
-          // The scales, ahead of the one arrival that K's barrier waits for beside its bytes: who sees K's product sees
-          // them. Their slot is free: K's slot was, so S of tile - kRingK is done, which was issued behind the
-          // product of the tile before it, or two before it: the softmax of that one and of all before is done.
-          if (lane == i || lane == i + 1) {
-            volatile float* const dst = info + (tile % kInfo) * 8 + (lane - i) * 4;
-            dst[0] = ks_now;
-            dst[1] = log2f(vs_now);
-            dst[2] = z_now >= 0 ? 1.f : 0.f;
-          }
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar_k_full(slot));
-#pragma unroll
-            for (int x = 0; x < C::kPerTile && ok; ++x) {
-              const int c = tile * C::kPerTile + x, cs = c % C::kRingV;
-              ok = wait(bar_c_empty(cs), ((c / C::kRingV) & 1) ^ 1, abort_flag, p.timeout_ns);
-              if (!ok) break;
-              if (C::kPerTile == 1) {
-                mbar_arrive_expect_tx(bar_c_full(cs), ((za >= 0) + (zb >= 0)) * 8192);
-                if (za >= 0) tma_load_3d(s_codes(cs), &map_v, bar_c_full(cs), 0, 0, za);
-                if (zb >= 0) tma_load_3d(s_codes(cs) + 8192, &map_v, bar_c_full(cs), 0, 0, zb);
-              } else {
-                const int zx = x ? zb : za;
-                mbar_arrive_expect_tx(bar_c_full(cs), zx >= 0 ? 8192 * C::kCh : 0);
-                for (int ch = 0; ch < C::kCh; ++ch)
-                  if (zx >= 0) tma_load_3d(s_codes(cs) + ch * 8192, &map_v, bar_c_full(cs), ch * 128, 0, zx);
-              }
-            }
-          }
-          ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
-          if (i == 16) scales_of(next_page);
-        }
-      }
-    }
-    __syncwarp();
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ tensor-core issuer
-    setmaxnreg_dec<C::kRegsOther>();
-    if (lane == 0) {
-      const uint32_t id_s = make_idesc(0, 128, 128, 0, 0);             // e4m3, both K-major
-      const uint32_t id_o = make_idesc(0, 128, p.c.d, 0, 1);           // f16, V MN-major
-      // The issuing thread paces the kernel: a product takes 64 cycles, and every other instruction of this one thread
-      // about eight. So a step's products stand in a row with constant offsets, the steps between a segment's first and
-      // last ones run in a loop of their own, and with two groups P-ready stands for V and the next K too (the
-      // watcher's arrival) and the watcher hands the rings back.
-      const int steps = (p.c.d + 31) / 32;                             // products over d that are not all zeros
-      // Descriptors by their lower halves; the upper ones are the same for all.
-      uint32_t tb = tbase;
-      const uint32_t kd0 = desc_lo(s_k(0), 16), qd0 = desc_lo(s_q(0, 0), 16), vd0 = desc_lo(s_half(0), C::kBoxV);
-      constexpr uint32_t kStepK = C::kTileK >> 4, kStepV = C::kHalfV >> 4;
-      bool ok = !p.test_stall || wait(bar_stall, 0, abort_flag, p.timeout_ns);   // runs out by design
-      uint32_t np = 0;                                                 // parities of the buffers' P-ready
-      int tile = 0;                                                    // tiles before the segment
-      // S of the rows behind descriptor qd with the K behind kd into buffer `buf`, d = 32 count at most
-      auto scores = [&](auto count, int buf, uint32_t qd, uint32_t kd) {
-        constexpr int n = decltype(count)::value;
-        const uint32_t dst = tb + C::col_s(buf);
-#pragma unroll
-        for (int i = 0; i < 2 * n; ++i) {
-          const int term = i / n, k = i % n, off = (k >> 2) * 16384 + (k & 3) * 32;
-          mma_fp8_ss(dst, desc_of(qd + ((term * C::kQTerm + off) >> 4)), desc_of(kd + (off >> 4)), id_s, i > 0);
-        }
-        mma_commit(bar_s_full(buf));
-      };
-      // O of `group` += P in buffer `buf` times the V stage behind vd, the x-th of its tile
-      auto product = [&](int buf, int group, int x, uint32_t vd, bool acc) {
-        const uint32_t src = tb + C::col_s(buf) + x * (C::kKeysV / 2);
-#pragma unroll
-        for (int k = 0; k < C::kKeysV / 16; ++k)
-          mma_bf16_ts(tb + C::col_o(group), src + k * 8, desc_of(vd + (k * 2048 >> 4)), id_o, acc || k > 0);
-      };
-      auto k_there = [&](int t) {
-        ok = wait(bar_k_full(t % C::kRingK), (t / C::kRingK) & 1, abort_flag, p.timeout_ns);
-        tc_fence_after();
-      };
-      auto p_there = [&](int buf) {
-        ok = wait(bar_p_ready(buf), np >> buf & 1u, abort_flag, p.timeout_ns);
-        np ^= 1u << buf;
-        tc_fence_after();
-      };
-      auto kd_of = [&](int t) { return kd0 + static_cast<uint32_t>(t % C::kRingK) * kStepK; };
-      auto segments = [&](auto count) {
-        Item it;
-        for (int seg = 0; ok && take_one(seg, it); ++seg) {
-          mbar_arrive(bar_item_empty(seg % kItems));
-          const int n = it.n, n0 = it.n0;
-          const bool split = it.split;
-          ok = wait(bar_q_full, seg & 1, abort_flag, p.timeout_ns);
-          if (!ok) break;
-          if (kGroups == 1) {
-            // S of the next tile is out before this one's P V
-            for (int j = -1; j < n && ok; ++j) {
-              const int t = tile + j;
-              if (j + 1 < n) {
-                k_there(t + 1);
-                if (!ok) break;
-                scores(count, (t + 1) & 1, qd0, kd_of(t + 1));
-                mma_commit(bar_k_empty((t + 1) % C::kRingK));
-              } else {
-                mma_commit(bar_q_empty);
-              }
-              if (j < 0) continue;
-              p_there(t & 1);
-#pragma unroll
-              for (int x = 0; x < C::kPerTile && ok; ++x) {
-                const int c = t * C::kPerTile + x, slot = c % C::kRingV;
-                ok = wait(bar_v_full(slot), (c / C::kRingV) & 1, abort_flag, p.timeout_ns);
-                if (!ok) break;
-                tc_fence_after();
-                product(t & 1, 0, x, vd0 + slot * kStepV, j > 0 || x > 0);
-                mma_commit(bar_v_empty(slot));
-              }
-            }
-            if (ok) mma_commit(bar_o_final(0));
-          } else {
-            // Step i is group i & 1's P V of a tile and its S of the next one: split, tile i, then i + 2; else tile
-            // i / 2 of either group, then the one behind it. The first two steps have no P V yet.
-            const uint32_t qd1 = qd0 + (split ? 0 : 2 * C::kQTerm >> 4);
-            const int all = split ? n : 2 * n;
-            for (int i = -2; i < all; ++i) {
-              if (i == 0) {
-                // the steps that have a next one but not the last, two at a time: V and next K of group 0, of group 1
-                const int pairs = split ? (n - 3) / 2 : n0 - 2;
-                uint32_t va = vd0 + (tile & 1) * kStepV, vb = vd0 + ((tile + split) & 1) * kStepV;
-                const uint32_t turn_v = split ? 0u : vd0 ^ (vd0 + kStepV);
-                int ka = (tile + (split ? 2 : 1)) % C::kRingK, kb = split ? (ka + 1) % C::kRingK : ka;
-                uint32_t kda = kd0 + ka * kStepK, kdb = kd0 + kb * kStepK;
-                const uint32_t kd_end = kd0 + C::kRingK * kStepK;
-                auto step = [&](uint32_t kd) {
-                  kd += kStepK;
-                  return kd == kd_end ? kd0 : kd;
-                };
-                uint32_t par = np & 1u, par1 = np >> 1, qa = qd0, qb = qd1;
-                for (int j = 0; j < pairs; ++j) {
-                  asm volatile("" : "+r"(qa), "+r"(qb), "+r"(tb));     // (or every product's offsets get registers of their own)
-                  ok = wait(bar_p_ready(0), par, abort_flag, p.timeout_ns);
-                  if (!ok) break;
-                  tc_fence_after();
-                  product(0, 0, 0, va, j > 0);
-                  scores(count, 0, qa, kda);
-                  ok = wait(bar_p_ready(1), par1, abort_flag, p.timeout_ns);
-                  if (!ok) break;
-                  tc_fence_after();
-                  product(1, 1, 0, vb, j > 0);
-                  scores(count, 1, qb, kdb);
-                  par ^= 1u;
-                  par1 ^= 1u;
-                  va ^= turn_v;
-                  vb ^= turn_v;
-                  kda = step(kdb);
-                  kdb = split ? step(kda) : kda;
-                }
-                if (!ok) break;
-                if (pairs > 0) {
-                  np = par | par1 << 1;
-                  i = 2 * pairs;
-                }
-              }
-              const int gr = i & 1, j = split ? i : i >> 1;
-              const int mine = split || gr ? n : n0, next_j = split ? i + 2 : j + 1;
-              const bool last = split || gr;
-              if (j >= mine) continue;
-              if (i >= 0) {
-                p_there(gr);
-                if (!ok) break;
-                product(gr, gr, 0, vd0 + ((tile + j) & 1) * kStepV, split ? i > 1 : j > 0);
-              } else if (next_j < mine && (split || !gr || n0 <= 0)) {
-                k_there(tile + next_j);
-                if (!ok) break;
-              }
-              if (next_j < mine) scores(count, gr, gr ? qd1 : qd0, kd_of(tile + next_j));
-              else if (i >= 0) mma_commit(bar_o_final(gr));
-              if (last && next_j + 1 == n) mma_commit(bar_q_empty);    // every S is out
-            }
-          }
-          tile += n;
-        }
-      };
-      constexpr int most = 4 * C::kCh;
-      if (steps == most) segments(std::integral_constant<int, most>());
-      else if (steps == most - 2) segments(std::integral_constant<int, most - 2>());
-      else if (steps == most - 1) segments(std::integral_constant<int, most - 1>());
-      else segments(std::integral_constant<int, most - 3>());
-    }
-    __syncwarp();
-  } else if (kGroups == 2 && warp == 10) {
-    // ------------------------------------------------------------ ring watcher
-    // One arrival on P-ready when V of its tile and K of the next S behind it have landed, and the rings' slots back when
-    // the S that shows them read is done: K of that S, and V up to the tile whose product was issued before it. It
-    // waits for every load in order, so no parity is taken for that of two phases earlier.
-    setmaxnreg_dec<C::kRegsOther>();
-    if (lane == 0) {
-      Item s;
-      bool ok = true;
-      int tile = 0, k_seen = 0, v_back = 0;                // tiles before the segment, K tiles waited for, V stages handed back
-      uint32_t ns0 = 0, ns1 = 0, np0 = 0, np1 = 0;         // phases of S and of P-ready
-      auto hand = [&](int g) {
-        uint32_t& np = g ? np1 : np0;
-        // arrive for a phase only once the one before it has completed
-        if (np > 0) ok = wait(bar_p_ready(g), (np - 1) & 1, abort_flag, p.timeout_ns);
-        if (ok) mbar_arrive(bar_p_ready(g));
-        ++np;
-      };
-      for (int seg = 0;; ++seg) {
-        if (!ok || !take_one(seg, s)) break;
-        mbar_arrive(bar_item_empty(seg % kItems));
-        const int n = s.n;
-        for (int x = 0; x < n && ok; ++x) {
-          const int t = tile + x, g = s.split ? x & 1 : 1;
-          auto k_there = [&](int last) {
-            for (; k_seen <= last && ok; ++k_seen)
-              ok = wait(bar_k_full(k_seen % C::kRingK), (k_seen / C::kRingK) & 1, abort_flag, p.timeout_ns);
-          };
-          auto s_done = [&]() {
-            if (ok) ok = wait(bar_s_full(g), (g ? ns1 : ns0) & 1, abort_flag, p.timeout_ns);
-            if (!ok) return;
-            if (g) ++ns1;
-            else ++ns0;
-            mbar_arrive(bar_k_empty(t % C::kRingK));
-            for (const int upto = s.split && x > 0 ? t - 2 : t - 1; v_back <= upto; ++v_back) mbar_arrive(bar_v_empty(v_back & 1));
-          };
-          // S before V where V of this tile may wait for the slot that goes back then: split, and at the segment's
-          // start (whose first K comes before that, as its slot goes back too). Otherwise group 0's P is ready long
-          // before this is: S of group 1 is done when P of group 0 nearly is, and each look costs 90 to 200 cycles.
-          const bool s_first = s.split || x == 0;
-          if (s_first) {
-            k_there(t);
-            s_done();
-          }
-          if (ok) ok = wait(bar_v_full(t & 1), (t >> 1) & 1, abort_flag, p.timeout_ns);
-          k_there(tile + min(n - 1, s.split ? x + 2 : x + 1));
-          if (ok && !s.split && x < s.n0) hand(0);
-          if (!s_first) s_done();
-          if (ok) hand(g);
-        }
-        if (!s.split) ns0 += s.n0;
-        tile += n;
-      }
-    }
-    __syncwarp();
-  } else if (warp >= 12) {
-    // ------------------------------------------------------------ converters
-    setmaxnreg_dec<C::kRegsOther>();
-    const int cw = warp - 12;
-    bool ok = true;
-    int tile = 0;
-    Item it;
-    for (int seg = 0; ok && take(seg, it); ++seg) {
-      const int len = field(seg, kLen), t0 = field(seg, kT0);
-      // ---- Q: 16 bytes a lane, four loads of a warp under way; this warp's 32 rows of each row tile. The rows are in L2 by
-      // now (the scheduler). All wait for this once the last S is done, and its code comes from memory nearly every
-      // time: unrolled eightfold it took 45000 cycles, at about 230 for 128 bytes of it.
-      ok = wait(bar_q_empty, (seg & 1) ^ 1, abort_flag, p.timeout_ns);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes; // lanes of a row, rows of a load
-      const int piece_q = lane % kLanes, sub = lane / kLanes;
-      const int step_tok = kAtOnce / p.G, step_head = kAtOnce - step_tok * p.G;
-#pragma unroll 1
-      for (int group = 0; group < (it.split ? 1 : kGroups); ++group) {
-        int tok = (32 * cw + sub) / p.G, head = 32 * cw + sub - tok * p.G;   // of the next load
-        const int first_token = field(seg, kTok0) + group * p.tt, left = min(p.tt, field(seg, kNew) - first_token);
-        const __nv_bfloat16* const src = p.q + static_cast<long long>(field(seg, kH) * p.G) * p.q_sh +
-                                         (static_cast<long long>(field(seg, kRow0)) + first_token) * p.q_st + 8 * piece_q;
-        uint4 v[4];
-#pragma unroll 1
-        for (int i = -4; i < 32 / kAtOnce; ++i) {
-          const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-          v[0] = v[1];
-          v[1] = v[2];
-          v[2] = v[3];
-          v[3] = make_uint4(0, 0, 0, 0);
-          if (i + 4 < 32 / kAtOnce && tok < left && 8 * piece_q < p.c.d)
-            v[3] = *reinterpret_cast<const uint4*>(src + head * p.q_sh + tok * p.q_st);
-          tok += step_tok;
-          head += step_head;
-          if (head >= p.G) {
-            head -= p.G;
-            ++tok;
-          }
-          if (i < 0) continue;
-          const int row = 32 * cw + sub + kAtOnce * i;
-          uint32_t m = 0;                                  // the largest magnitude, as bits
-#pragma unroll
-          for (int k = 0; k < 4; ++k) m = max(m, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-          uint32_t amax = __reduce_max_sync(0xffffffffu, sub == 0 ? m : 0u);
-          if (kAtOnce == 2) {
-            const uint32_t second = __reduce_max_sync(0xffffffffu, sub == 1 ? m : 0u);
-            if (sub == 1) amax = second;
-          }
-          // exponent that brings the largest to [128, 256); bounded so that both powers are normal.
-          // A row with an infinity or NaN becomes NaN, as its logits are.
-          const int e2 = amax > 0 ? max(-100, min(100, static_cast<int>(amax >> 7) - 127 - 7)) : 0;
-          const float down = amax < 0x7F80u ? __uint_as_float(static_cast<uint32_t>(127 - e2) << 23) : NAN;
-          if (piece_q == 0) row_scale[group * 128 + row] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
-          uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            // (eight significant bits and at most 256: f16 holds what the two terms can)
-            const uint32_t x = pack_f16x2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
-            const uint32_t c0 = f16x2_to_e4m3x2(x);
-            hi[k >> 1] |= c0 << (16 * (k & 1));
-            lo[k >> 1] |= f16x2_to_e4m3x2(sub_f16x2(x, e4m3x2_to_f16x2(c0))) << (16 * (k & 1));
-          }
-          const uint32_t at = swz128((piece_q >> 4) * 16384, row, (piece_q & 15) >> 1) + (piece_q & 1) * 8;
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" :: "r"(s_q(group, 0) + at), "r"(hi[0]), "r"(hi[1]) : "memory");
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" :: "r"(s_q(group, 1) + at), "r"(lo[0]), "r"(lo[1]) : "memory");
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_q_full);
-      done(seg);
-      // ---- V: 16 codes of a key at a time, from the codes' swizzled rows to two units of the halves' rows. Eight lanes, whose
-      // 16 bytes go together, take four pieces of one box (64 columns) of keys k and k ^ 5: no bank twice, in the load
-      // or in either store. A thread's keys are 32 apart, so one address each serves with constant offsets.
-      constexpr int kBoxes = D / 64;
-      const int quad = lane & 3, key0 = 2 * ((lane >> 3) + 4 * cw) ^ (lane & 4 ? 5 : 0);
-      const uint32_t from = swz128(0, key0, quad), to = swz128(0, key0, 2 * quad);
-      for (int j = t0; j < t0 + it.n && ok; ++j, ++tile) {
-        const volatile float* const there = info + (tile % kInfo) * 8;
-#pragma unroll
-        for (int x = 0; x < C::kPerTile; ++x) {
-          const int c = tile * C::kPerTile + x, slot = c % C::kRingV;
-          if (ok) ok = wait(bar_c_full(slot), (c / C::kRingV) & 1, abort_flag, p.timeout_ns);
-          if (ok) ok = wait(bar_v_empty(slot), ((c / C::kRingV) & 1) ^ 1, abort_flag, p.timeout_ns);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          // keys of the stage that there are, in each of its blocks; the others become 0
-          const int valid = len - j * 128 - x * C::kKeysV;
-          const bool here0 = there[C::kPerTile == 1 ? 2 : 4 * x + 2] != 0.f, here1 = there[6] != 0.f;
-          const uint32_t src = s_codes(slot) + from, dst = s_half(slot) + to;
-          const bool all = valid >= C::kKeysV && here0 && (C::kPerTile == 2 || here1);
-#pragma unroll 1
-          for (int half = 0; half < 2; ++half) {           // of the rows, four pieces each
-            const int down = half * (4 / kBoxes) * 32;
-            uint4 w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int box = e % kBoxes, step = 32 * (e / kBoxes);
-              if (64 * box >= p.c.d) continue;
-              const uint32_t at = (src ^ ((box & 1) * 64)) + (box >> 1) * 8192 + (down + step) * 128;
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[e].x), "=r"(w[e].y), "=r"(w[e].z), "=r"(w[e].w) : "r"(at) : "memory");
-            }
-            if (!all) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int key = key0 + down + 32 * (e / kBoxes);
-                if (!(key < valid && (key < 64 ? here0 : here1))) w[e] = make_uint4(0, 0, 0, 0);
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int box = e % kBoxes, step = 32 * (e / kBoxes);
-              if (64 * box >= p.c.d) continue;
-              const uint32_t at = box * C::kBoxV + (down + step) * 128;
-              store16(dst + at, e4m3x2_to_f16x2(w[e].x & 0xFFFFu), e4m3x2_to_f16x2(w[e].x >> 16), e4m3x2_to_f16x2(w[e].y & 0xFFFFu),
-                      e4m3x2_to_f16x2(w[e].y >> 16));
-              store16((dst ^ 16) + at, e4m3x2_to_f16x2(w[e].z & 0xFFFFu), e4m3x2_to_f16x2(w[e].z >> 16), e4m3x2_to_f16x2(w[e].w & 0xFFFFu),
-                      e4m3x2_to_f16x2(w[e].w >> 16));
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar_c_empty(slot));
-            mbar_arrive(bar_v_full(slot));
-          }
-        }
-      }
-    }
-    __syncwarp();
-  } else if (warp == 11) {
-    // ------------------------------------------------------------ scheduler
-    // Finds this part's segments ahead of time: one warp's look-up instead of all roles', whose code for it would come
-    // from memory at every change. And brings the segment's rows of Q into L2.
-    setmaxnreg_dec<C::kRegsOther>();
-    const Line line(p, lane);
-    bool ok = true;
-    long long u = 0, length = 0;
-    Place place;
-    if (static_cast<int>(blockIdx.x) < line.parts) {
-      u = line.begin(blockIdx.x);
-      length = line.begin(blockIdx.x + 1) - u;
-      place.find(p, line.turn, u, lane);
-    }
-    Walk walk(p, place, line.turn, length);
-    Segment s;
-    for (int n = 0; ok; ++n) {
-      const bool more = walk.next<kGroups>(p, s);
-      if (n >= kItems) ok = wait(bar_item_empty(n % kItems), ((n / kItems) & 1) ^ 1, abort_flag, p.timeout_ns);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      if (lane == 0) {
-        volatile int* const m = items + (n % kItems) * kItemInts;
-        m[kB] = s.b;
-        m[kH] = s.h;
-        m[kRow0] = s.row0;
-        m[kNew] = s.n;
-        m[kLen] = s.len;
-        m[kTok0] = s.tok0;
-        m[kT0] = s.t0;
-        m[kN] = more ? s.t1 - s.t0 : 0;
-        m[kN0] = s.n0;
-        m[kSplit] = s.split;
-        m[kWhole] = s.t0 == 0 && s.t1 == s.tiles;
-        mbar_arrive(bar_item_full(n % kItems));
-      }
-      __syncwarp();
-      if (!more) break;
-      for (int r = lane; r < (s.split ? 128 : C::kRows); r += 32) {
-        const int row = r & 127, tok = row / p.G, token = s.tok0 + (r >> 7) * p.tt + tok;
-        if (tok >= p.tt || token >= s.n) continue;
-        const __nv_bfloat16* const src =
-            p.q + (s.h * p.G + (row - tok * p.G)) * p.q_sh + (static_cast<long long>(s.row0) + token) * p.q_st;
-        for (int c = 0; c < p.c.d; c += 64) asm volatile("prefetch.global.L2 [%0];" :: "l"(src + c));
-      }
-    }
-    __syncwarp();
-  } else if (warp >= 8) {
-    setmaxnreg_dec<C::kRegsOther>();
-  } else {
+  if (warp < 8) {
     // ------------------------------------------------------------ softmax groups
     setmaxnreg_inc<C::kRegsSoftmax>();
     const int g = warp >> 2;
@@ -929,13 +465,11 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #pragma unroll
         for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(sr[i >> 5][i & 31]);
         if (lim < 128 || !here_a || !here_b) {
-          // (by bits: fewer instructions, and these come from memory each time)
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) {
             const int n = (q4 < 2 ? here_a : here_b) ? lim - 32 * q4 : 0;
-            const uint32_t seen = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[32 * q4 + i] = (seen >> i & 1u) ? v[32 * q4 + i] : -INFINITY;
+            for (int i = 0; i < 32; ++i) v[32 * q4 + i] = i < n ? v[32 * q4 + i] : -INFINITY;
           }
         }
         float mk[4];
@@ -1103,6 +637,469 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       tc_fence_before();
       if (kGroups == 2 && split) mbar_arrive(bar_other_empty);
     }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ tensor-core issuer
+    setmaxnreg_dec<C::kRegsOther>();
+    if (lane == 0) {
+      const uint32_t id_s = make_idesc(0, 128, 128, 0, 0);             // e4m3, both K-major
+      const uint32_t id_o = make_idesc(0, 128, p.c.d, 0, 1);           // f16, V MN-major
+      // The issuing thread paces the kernel: a product takes 64 cycles, and every other instruction of this one thread
+      // about eight. So a step's products stand in a row with constant offsets, the steps between a segment's first and
+      // last ones run in a loop of their own, and with two groups P-ready stands for V and the next K too (the
+      // watcher's arrival) and the watcher hands the rings back.
+      const int steps = (p.c.d + 31) / 32;                             // products over d that are not all zeros
+      // Descriptors by their lower halves; the upper ones are the same for all.
+      uint32_t tb = tbase;
+      const uint32_t kd0 = desc_lo(s_k(0), 16), qd0 = desc_lo(s_q(0, 0), 16), vd0 = desc_lo(s_half(0), C::kBoxV);
+      constexpr uint32_t kStepK = C::kTileK >> 4, kStepV = C::kHalfV >> 4;
+      bool ok = !p.test_stall || wait(bar_stall, 0, abort_flag, p.timeout_ns);   // runs out by design
+      uint32_t np = 0;                                                 // parities of the buffers' P-ready
+      int tile = 0;                                                    // tiles before the segment
+      // S of the rows behind descriptor qd with the K behind kd into buffer `buf`, d = 32 count at most
+      auto scores = [&](auto count, int buf, uint32_t qd, uint32_t kd) {
+        constexpr int n = decltype(count)::value;
+        const uint32_t dst = tb + C::col_s(buf);
+#pragma unroll
+        for (int i = 0; i < 2 * n; ++i) {
+          const int term = i / n, k = i % n, off = (k >> 2) * 16384 + (k & 3) * 32;
+          mma_fp8_ss(dst, desc_of(qd + ((term * C::kQTerm + off) >> 4)), desc_of(kd + (off >> 4)), id_s, i > 0);
+        }
+        mma_commit(bar_s_full(buf));
+      };
+      // O of `group` += P in buffer `buf` times the V stage behind vd, the x-th of its tile
+      auto product = [&](int buf, int group, int x, uint32_t vd, bool acc) {
+        const uint32_t src = tb + C::col_s(buf) + x * (C::kKeysV / 2);
+#pragma unroll
+        for (int k = 0; k < C::kKeysV / 16; ++k)
+          mma_bf16_ts(tb + C::col_o(group), src + k * 8, desc_of(vd + (k * 2048 >> 4)), id_o, acc || k > 0);
+      };
+      auto k_there = [&](int t) {
+        ok = wait(bar_k_full(t % C::kRingK), (t / C::kRingK) & 1, abort_flag, p.timeout_ns);
+        tc_fence_after();
+      };
+      auto p_there = [&](int buf) {
+        ok = wait(bar_p_ready(buf), np >> buf & 1u, abort_flag, p.timeout_ns);
+        np ^= 1u << buf;
+        tc_fence_after();
+      };
+      auto kd_of = [&](int t) { return kd0 + static_cast<uint32_t>(t % C::kRingK) * kStepK; };
+      auto segments = [&](auto count) {
+        Item it;
+        for (int seg = 0; ok && take_one(seg, it); ++seg) {
+          mbar_arrive(bar_item_empty(seg % kItems));
+          const int n = it.n, n0 = it.n0;
+          const bool split = it.split;
+          ok = wait(bar_q_full, seg & 1, abort_flag, p.timeout_ns);
+          if (!ok) break;
+          if (kGroups == 1) {
+            // S of the next tile is out before this one's P V
+            for (int j = -1; j < n && ok; ++j) {
+              const int t = tile + j;
+              if (j + 1 < n) {
+                k_there(t + 1);
+                if (!ok) break;
+                scores(count, (t + 1) & 1, qd0, kd_of(t + 1));
+                mma_commit(bar_k_empty((t + 1) % C::kRingK));
+              } else {
+                mma_commit(bar_q_empty);
+              }
+              if (j < 0) continue;
+              p_there(t & 1);
+#pragma unroll
+              for (int x = 0; x < C::kPerTile && ok; ++x) {
+                const int c = t * C::kPerTile + x, slot = c % C::kRingV;
+                ok = wait(bar_v_full(slot), (c / C::kRingV) & 1, abort_flag, p.timeout_ns);
+                if (!ok) break;
+                tc_fence_after();
+                product(t & 1, 0, x, vd0 + slot * kStepV, j > 0 || x > 0);
+                mma_commit(bar_v_empty(slot));
+              }
+            }
+            if (ok) mma_commit(bar_o_final(0));
+          } else {
+            // Step i is group i & 1's P V of a tile and its S of the next one: split, tile i, then i + 2; else tile
+            // i / 2 of either group, then the one behind it. The first two steps have no P V yet.
+            const uint32_t qd1 = qd0 + (split ? 0 : 2 * C::kQTerm >> 4);
+            const int all = split ? n : 2 * n;
+            for (int i = -2; i < all; ++i) {
+              if (i == 0) {
+                // the steps that have a next one but not the last, two at a time: V and next K of group 0, of group 1
+                const int pairs = split ? (n - 3) / 2 : n0 - 2;
+                uint32_t va = vd0 + (tile & 1) * kStepV, vb = vd0 + ((tile + split) & 1) * kStepV;
+                const uint32_t turn_v = split ? 0u : vd0 ^ (vd0 + kStepV);
+                int ka = (tile + (split ? 2 : 1)) % C::kRingK, kb = split ? (ka + 1) % C::kRingK : ka;
+                uint32_t kda = kd0 + ka * kStepK, kdb = kd0 + kb * kStepK;
+                const uint32_t kd_end = kd0 + C::kRingK * kStepK;
+                auto step = [&](uint32_t kd) {
+                  kd += kStepK;
+                  return kd == kd_end ? kd0 : kd;
+                };
+                uint32_t par = np & 1u, par1 = np >> 1, qa = qd0, qb = qd1;
+                for (int j = 0; j < pairs; ++j) {
+                  asm volatile("" : "+r"(qa), "+r"(qb), "+r"(tb));     // (or every product's offsets get registers of their own)
+                  ok = wait(bar_p_ready(0), par, abort_flag, p.timeout_ns);
+                  if (!ok) break;
+                  tc_fence_after();
+                  product(0, 0, 0, va, j > 0);
+                  scores(count, 0, qa, kda);
+                  ok = wait(bar_p_ready(1), par1, abort_flag, p.timeout_ns);
+                  if (!ok) break;
+                  tc_fence_after();
+                  product(1, 1, 0, vb, j > 0);
+                  scores(count, 1, qb, kdb);
+                  par ^= 1u;
+                  par1 ^= 1u;
+                  va ^= turn_v;
+                  vb ^= turn_v;
+                  kda = step(kdb);
+                  kdb = split ? step(kda) : kda;
+                }
+                if (!ok) break;
+                if (pairs > 0) {
+                  np = par | par1 << 1;
+                  i = 2 * pairs;
+                }
+              }
+              const int gr = i & 1, j = split ? i : i >> 1;
+              const int mine = split || gr ? n : n0, next_j = split ? i + 2 : j + 1;
+              const bool last = split || gr;
+              if (j >= mine) continue;
+              if (i >= 0) {
+                p_there(gr);
+                if (!ok) break;
+                product(gr, gr, 0, vd0 + ((tile + j) & 1) * kStepV, split ? i > 1 : j > 0);
+              } else if (next_j < mine && (split || !gr || n0 <= 0)) {
+                k_there(tile + next_j);
+                if (!ok) break;
+              }
+              if (next_j < mine) scores(count, gr, gr ? qd1 : qd0, kd_of(tile + next_j));
+              else if (i >= 0) mma_commit(bar_o_final(gr));
+              if (last && next_j + 1 == n) mma_commit(bar_q_empty);    // every S is out
+            }
+          }
+          tile += n;
+        }
+      };
+      // Two widths of code: d up to 64 and 128, up to 192 and 256. A d between runs in the next, over zeros of K and Q.
+      constexpr int most = 4 * C::kCh;
+      if (steps > most - 2) segments(std::integral_constant<int, most>());
+      else segments(std::integral_constant<int, most - 2>());
+    }
+    __syncwarp();
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------ converters
+    setmaxnreg_dec<C::kRegsOther>();
+    const int cw = warp - 12;
+    bool ok = true;
+    int tile = 0;
+    Item it;
+    for (int seg = 0; ok && take(seg, it); ++seg) {
+      const int len = field(seg, kLen), t0 = field(seg, kT0);
+      // ---- Q: 16 bytes a lane, four loads of a warp under way; this warp's 32 rows of each row tile. The rows are in L2 by
+      // now (the scheduler). All wait for this once the last S is done, and its code comes from memory nearly every
+      // time: unrolled eightfold it took 45000 cycles, at about 230 for 128 bytes of it.
+      ok = wait(bar_q_empty, (seg & 1) ^ 1, abort_flag, p.timeout_ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes; // lanes of a row, rows of a load
+      const int piece_q = lane % kLanes, sub = lane / kLanes;
+      const int step_tok = kAtOnce / p.G, step_head = kAtOnce - step_tok * p.G;
+#pragma unroll 1
+      for (int group = 0; group < (it.split ? 1 : kGroups); ++group) {
+        int tok = (32 * cw + sub) / p.G, head = 32 * cw + sub - tok * p.G;   // of the next load
+        const int first_token = field(seg, kTok0) + group * p.tt, left = min(p.tt, field(seg, kNew) - first_token);
+        const __nv_bfloat16* const src = p.q + static_cast<long long>(field(seg, kH) * p.G) * p.q_sh +
+                                         (static_cast<long long>(field(seg, kRow0)) + first_token) * p.q_st + 8 * piece_q;
+        uint4 v[4];
+#pragma unroll 1
+        for (int i = -4; i < 32 / kAtOnce; ++i) {
+          const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+          v[0] = v[1];
+          v[1] = v[2];
+          v[2] = v[3];
+          v[3] = make_uint4(0, 0, 0, 0);
+          if (i + 4 < 32 / kAtOnce && tok < left && 8 * piece_q < p.c.d)
+            v[3] = *reinterpret_cast<const uint4*>(src + head * p.q_sh + tok * p.q_st);
+          tok += step_tok;
+          head += step_head;
+          if (head >= p.G) {
+            head -= p.G;
+            ++tok;
+          }
+          if (i < 0) continue;
+          const int row = 32 * cw + sub + kAtOnce * i;
+          uint32_t m = 0;                                  // the largest magnitude, as bits
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m = max(m, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+          uint32_t amax = __reduce_max_sync(0xffffffffu, sub == 0 ? m : 0u);
+          if (kAtOnce == 2) {
+            const uint32_t second = __reduce_max_sync(0xffffffffu, sub == 1 ? m : 0u);
+            if (sub == 1) amax = second;
+          }
+          // exponent that brings the largest to [128, 256); bounded so that both powers are normal.
+          // A row with an infinity or NaN becomes NaN, as its logits are.
+          const int e2 = amax > 0 ? max(-100, min(100, static_cast<int>(amax >> 7) - 127 - 7)) : 0;
+          const float down = amax < 0x7F80u ? __uint_as_float(static_cast<uint32_t>(127 - e2) << 23) : NAN;
+          if (piece_q == 0) row_scale[group * 128 + row] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+          uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            // (eight significant bits and at most 256: f16 holds what the two terms can)
+            const uint32_t x = pack_f16x2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
+            const uint32_t c0 = f16x2_to_e4m3x2(x);
+            hi[k >> 1] |= c0 << (16 * (k & 1));
+            lo[k >> 1] |= f16x2_to_e4m3x2(sub_f16x2(x, e4m3x2_to_f16x2(c0))) << (16 * (k & 1));
+          }
+          const uint32_t at = swz128((piece_q >> 4) * 16384, row, (piece_q & 15) >> 1) + (piece_q & 1) * 8;
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" :: "r"(s_q(group, 0) + at), "r"(hi[0]), "r"(hi[1]) : "memory");
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" :: "r"(s_q(group, 1) + at), "r"(lo[0]), "r"(lo[1]) : "memory");
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_q_full);
+      done(seg);
+      // ---- V: 16 codes of a key at a time, from the codes' swizzled rows to two units of the halves' rows. Eight lanes, whose
+      // 16 bytes go together, take four pieces of one box (64 columns) of keys k and k ^ 5: no bank twice, in the load
+      // or in either store. A thread's keys are 32 apart, so one address each serves with constant offsets.
+      constexpr int kBoxes = D / 64;
+      const int quad = lane & 3, key0 = 2 * ((lane >> 3) + 4 * cw) ^ (lane & 4 ? 5 : 0);
+      const uint32_t from = swz128(0, key0, quad), to = swz128(0, key0, 2 * quad);
+      for (int j = t0; j < t0 + it.n && ok; ++j, ++tile) {
+        const volatile float* const there = info + (tile % kInfo) * 8;
+#pragma unroll
+        for (int x = 0; x < C::kPerTile; ++x) {
+          const int c = tile * C::kPerTile + x, slot = c % C::kRingV;
+          if (ok) ok = wait(bar_c_full(slot), (c / C::kRingV) & 1, abort_flag, p.timeout_ns);
+          if (ok) ok = wait(bar_v_empty(slot), ((c / C::kRingV) & 1) ^ 1, abort_flag, p.timeout_ns);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          // keys of the stage that there are, in each of its blocks; the others become 0
+          const int valid = len - j * 128 - x * C::kKeysV;
+          const bool here0 = there[C::kPerTile == 1 ? 2 : 4 * x + 2] != 0.f, here1 = there[6] != 0.f;
+          const uint32_t src = s_codes(slot) + from, dst = s_half(slot) + to;
+          const bool all = valid >= C::kKeysV && here0 && (C::kPerTile == 2 || here1);
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {           // of the rows, four pieces each
+            const int down = half * (4 / kBoxes) * 32;
+            uint4 w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int box = e % kBoxes, step = 32 * (e / kBoxes);
+              if (64 * box >= p.c.d) continue;
+              const uint32_t at = (src ^ ((box & 1) * 64)) + (box >> 1) * 8192 + (down + step) * 128;
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[e].x), "=r"(w[e].y), "=r"(w[e].z), "=r"(w[e].w) : "r"(at) : "memory");
+            }
+            if (!all) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int key = key0 + down + 32 * (e / kBoxes);
+                if (!(key < valid && (key < 64 ? here0 : here1))) w[e] = make_uint4(0, 0, 0, 0);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int box = e % kBoxes, step = 32 * (e / kBoxes);
+              if (64 * box >= p.c.d) continue;
+              const uint32_t at = box * C::kBoxV + (down + step) * 128;
+              store16(dst + at, e4m3x2_to_f16x2(w[e].x & 0xFFFFu), e4m3x2_to_f16x2(w[e].x >> 16), e4m3x2_to_f16x2(w[e].y & 0xFFFFu),
+                      e4m3x2_to_f16x2(w[e].y >> 16));
+              store16((dst ^ 16) + at, e4m3x2_to_f16x2(w[e].z & 0xFFFFu), e4m3x2_to_f16x2(w[e].z >> 16), e4m3x2_to_f16x2(w[e].w & 0xFFFFu),
+                      e4m3x2_to_f16x2(w[e].w >> 16));
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar_c_empty(slot));
+            mbar_arrive(bar_v_full(slot));
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (kGroups == 2 && warp == 10) {
+    // ------------------------------------------------------------ ring watcher
+    // One arrival on P-ready when V of its tile and K of the next S behind it have landed, and the rings' slots back when
+    // the S that shows them read is done: K of that S, and V up to the tile whose product was issued before it. It
+    // waits for every load in order, so no parity is taken for that of two phases earlier.
+    setmaxnreg_dec<C::kRegsOther>();
+    if (lane == 0) {
+      Item s;
+      bool ok = true;
+      int tile = 0, k_seen = 0, v_back = 0;                // tiles before the segment, K tiles waited for, V stages handed back
+      uint32_t ns0 = 0, ns1 = 0, np0 = 0, np1 = 0;         // phases of S and of P-ready
+      auto hand = [&](int g) {
+        uint32_t& np = g ? np1 : np0;
+        // arrive for a phase only once the one before it has completed
+        if (np > 0) ok = wait(bar_p_ready(g), (np - 1) & 1, abort_flag, p.timeout_ns);
+        if (ok) mbar_arrive(bar_p_ready(g));
+        ++np;
+      };
+      for (int seg = 0;; ++seg) {
+        if (!ok || !take_one(seg, s)) break;
+        mbar_arrive(bar_item_empty(seg % kItems));
+        const int n = s.n;
+        for (int x = 0; x < n && ok; ++x) {
+          const int t = tile + x, g = s.split ? x & 1 : 1;
+          auto k_there = [&](int last) {
+            for (; k_seen <= last && ok; ++k_seen)
+              ok = wait(bar_k_full(k_seen % C::kRingK), (k_seen / C::kRingK) & 1, abort_flag, p.timeout_ns);
+          };
+          auto s_done = [&]() {
+            if (ok) ok = wait(bar_s_full(g), (g ? ns1 : ns0) & 1, abort_flag, p.timeout_ns);
+            if (!ok) return;
+            if (g) ++ns1;
+            else ++ns0;
+            mbar_arrive(bar_k_empty(t % C::kRingK));
+            for (const int upto = s.split && x > 0 ? t - 2 : t - 1; v_back <= upto; ++v_back) mbar_arrive(bar_v_empty(v_back & 1));
+          };
+          // S before V where V of this tile may wait for the slot that goes back then: split, and at the segment's
+          // start (whose first K comes before that, as its slot goes back too). Otherwise group 0's P is ready long
+          // before this is: S of group 1 is done when P of group 0 nearly is, and each look costs 90 to 200 cycles.
+          const bool s_first = s.split || x == 0;
+          if (s_first) {
+            k_there(t);
+            s_done();
+          }
+          if (ok) ok = wait(bar_v_full(t & 1), (t >> 1) & 1, abort_flag, p.timeout_ns);
+          k_there(tile + min(n - 1, s.split ? x + 2 : x + 1));
+          if (ok && !s.split && x < s.n0) hand(0);
+          if (!s_first) s_done();
+          if (ok) hand(g);
+        }
+        if (!s.split) ns0 += s.n0;
+        tile += n;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ producer
+    setmaxnreg_dec<C::kRegsOther>();
+    if (lane == 0) {
+      tma_prefetch_map(&map_k);
+      tma_prefetch_map(&map_v);
+    }
+    int tile = 0;                                          // tiles so far
+    bool ok = true;
+    Item it;
+    for (int seg = 0; ok && take(seg, it); ++seg) {
+      const int blk0 = 2 * field(seg, kT0), blk1 = blk0 + 2 * it.n, h = field(seg, kH);
+      const int* const table = p.table + static_cast<long long>(field(seg, kB)) * p.max_blocks;
+      const int held = min(blk1, (field(seg, kLen) + kCacheBlock - 1) / kCacheBlock);
+      done(seg);
+      // 32 blocks at a time, one per lane; the next 32 are looked up while these are loaded
+      auto page_of = [&](int blk) {
+        const int page = blk + lane < held ? table[blk + lane] : -1;
+        return page < p.c.num_blocks ? page : -1;
+      };
+      float ks = 0.f, vs = 0.f;
+      int z = -1;
+      auto scales_of = [&](int page) {
+        const long long ph = page >= 0 ? static_cast<long long>(page) * p.c.Hkv + h : -1;
+        ks = page >= 0 ? p.c.k_scale[ph] : 0.f;
+        vs = page >= 0 ? p.c.v_scale[ph] : 0.f;
+        z = static_cast<int>(ph);
+      };
+      scales_of(page_of(blk0));
+      for (int blk = blk0; blk < blk1 && ok; blk += 32) {
+        const float ks_now = ks, vs_now = vs;
+        const int z_now = z, next_page = page_of(blk + 32);
+        for (int i = 0; i < 32 && blk + i < blk1 && ok; i += 2, ++tile) {
+          const int za = __shfl_sync(0xffffffffu, z_now, i), zb = __shfl_sync(0xffffffffu, z_now, i + 1);
+          const int slot = tile % C::kRingK;
+          if (lane == 0) {
+            ok = wait(bar_k_empty(slot), ((tile / C::kRingK) & 1) ^ 1, abort_flag, p.timeout_ns);
+            if (ok) mbar_expect_tx(bar_k_full(slot), ((za >= 0) + (zb >= 0)) * 8192 * C::kCh);
+            for (int ch = 0; ch < C::kCh && ok; ++ch) {
+              if (za >= 0) tma_load_3d(s_k(slot) + ch * 16384, &map_k, bar_k_full(slot), ch * 128, 0, za);
+              if (zb >= 0) tma_load_3d(s_k(slot) + ch * 16384 + 8192, &map_k, bar_k_full(slot), ch * 128, 0, zb);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
+          if (!ok) break;
+          // The scales, ahead of the one arrival that K's barrier waits for beside its bytes: who sees K's product sees
+          // them. Their slot is free: K's slot was, so S of tile - kRingK is done, which was issued behind the
+          // product of the tile before it, or two before it: the softmax of that one and of all before is done.
+          if (lane == i || lane == i + 1) {
+            volatile float* const dst = info + (tile % kInfo) * 8 + (lane - i) * 4;
+            dst[0] = ks_now;
+            dst[1] = log2f(vs_now);
+            dst[2] = z_now >= 0 ? 1.f : 0.f;
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar_k_full(slot));
+#pragma unroll
+            for (int x = 0; x < C::kPerTile && ok; ++x) {
+              const int c = tile * C::kPerTile + x, cs = c % C::kRingV;
+              ok = wait(bar_c_empty(cs), ((c / C::kRingV) & 1) ^ 1, abort_flag, p.timeout_ns);
+              if (!ok) break;
+              if (C::kPerTile == 1) {
+                mbar_arrive_expect_tx(bar_c_full(cs), ((za >= 0) + (zb >= 0)) * 8192);
+                if (za >= 0) tma_load_3d(s_codes(cs), &map_v, bar_c_full(cs), 0, 0, za);
+                if (zb >= 0) tma_load_3d(s_codes(cs) + 8192, &map_v, bar_c_full(cs), 0, 0, zb);
+              } else {
+                const int zx = x ? zb : za;
+                mbar_arrive_expect_tx(bar_c_full(cs), zx >= 0 ? 8192 * C::kCh : 0);
+                for (int ch = 0; ch < C::kCh; ++ch)
+                  if (zx >= 0) tma_load_3d(s_codes(cs) + ch * 8192, &map_v, bar_c_full(cs), ch * 128, 0, zx);
+              }
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
+          if (i == 16) scales_of(next_page);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ scheduler
+    // Finds this part's segments ahead of time: one warp's look-up instead of all roles', whose code for it would come
+    // from memory at every change. And brings the segment's rows of Q into L2.
+    setmaxnreg_dec<C::kRegsOther>();
+    const Line line(p, lane);
+    bool ok = true;
+    long long u = 0, length = 0;
+    Place place;
+    if (static_cast<int>(blockIdx.x) < line.parts) {
+      u = line.begin(blockIdx.x);
+      length = line.begin(blockIdx.x + 1) - u;
+      place.find(p, line.turn, u, lane);
+    }
+    Walk walk(p, place, line.turn, length);
+    Segment s;
+    for (int n = 0; ok; ++n) {
+      const bool more = walk.next<kGroups>(p, s);
+      if (n >= kItems) ok = wait(bar_item_empty(n % kItems), ((n / kItems) & 1) ^ 1, abort_flag, p.timeout_ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) {
+        volatile int* const m = items + (n % kItems) * kItemInts;
+        m[kB] = s.b;
+        m[kH] = s.h;
+        m[kRow0] = s.row0;
+        m[kNew] = s.n;
+        m[kLen] = s.len;
+        m[kTok0] = s.tok0;
+        m[kT0] = s.t0;
+        m[kN] = more ? s.t1 - s.t0 : 0;
+        m[kN0] = s.n0;
+        m[kSplit] = s.split;
+        m[kWhole] = s.t0 == 0 && s.t1 == s.tiles;
+        mbar_arrive(bar_item_full(n % kItems));
+      }
+      __syncwarp();
+      if (!more) break;
+      for (int r = lane; r < (s.split ? 128 : C::kRows); r += 32) {
+        const int row = r & 127, tok = row / p.G, token = s.tok0 + (r >> 7) * p.tt + tok;
+        if (tok >= p.tt || token >= s.n) continue;
+        const __nv_bfloat16* const src =
+            p.q + (s.h * p.G + (row - tok * p.G)) * p.q_sh + (static_cast<long long>(s.row0) + token) * p.q_st;
+        for (int c = 0; c < p.c.d; c += 64) asm volatile("prefetch.global.L2 [%0];" :: "l"(src + c));
+      }
+    }
+    __syncwarp();
+  } else {
+    setmaxnreg_dec<C::kRegsOther>();
   }
 
   // ---------------------------------------------------------------- teardown
