@@ -50,7 +50,8 @@ struct Cfg {
   static constexpr int kGroups = D == 128 ? 2 : 1;
   static constexpr int kCh = D / 128;                      // 128-byte columns of codes
   static constexpr int kRows = 128 * kGroups;              // of an item
-  static constexpr int kReaders = 6 + (kGroups == 2 ? 1 : 0) + 4 * kGroups;   // warps that read a segment: producer, issuer, watcher, converters, softmax
+  static constexpr int kConv = kGroups == 2 ? 4 : 8;       // converting warps: 12-15, with one group 4-7 too
+  static constexpr int kReaders = 2 + (kGroups == 2 ? 1 : 0) + kConv + 4 * kGroups;   // warps that read a segment: producer, issuer, watcher, converters, softmax
   static constexpr int kKeysV = D == 128 ? 128 : 64;       // keys of a V stage
   static constexpr int kPerTile = 128 / kKeysV;            // V stages of a key tile
   static constexpr int kQTerm = 16384 * kCh;               // one term of a row tile
@@ -67,7 +68,8 @@ struct Cfg {
   static constexpr int kSmem = kLayout + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   // setmaxnreg, of the 512 x 128 launched: without spills, which L1 beside so much shared memory does not hold
-  static constexpr uint32_t kRegsSoftmax = D == 128 ? 192 : 168, kRegsOther = 256 - kRegsSoftmax;
+  static constexpr uint32_t kRegsSoftmax = D == 128 ? 192 : 168, kRegsOther = D == 128 ? 64 : 112;
+  static_assert(kGroups * kRegsSoftmax + (4 - kGroups) * kRegsOther <= 512, "register split");
   static __device__ __forceinline__ uint32_t col_s(int i) { return 128u * i; }
   static __device__ __forceinline__ uint32_t col_o(int i) { return 256u + 128u * i; }
 };
@@ -354,14 +356,14 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar_c_full(i), 1);
-      mbar_init(bar_c_empty(i), 4);
-      mbar_init(bar_v_full(i), 4);
+      mbar_init(bar_c_empty(i), C::kConv);
+      mbar_init(bar_v_full(i), C::kConv);
       mbar_init(bar_v_empty(i), 1);
       mbar_init(bar_s_full(i), 1);
       mbar_init(bar_p_ready(i), kGroups == 2 ? 129 : 128);   // + the watcher
       mbar_init(bar_o_final(i), 1);
     }
-    mbar_init(bar_q_full, 4);
+    mbar_init(bar_q_full, C::kConv);
     mbar_init(bar_q_empty, 1 + 4 * kGroups);               // its products done, its scales read by every softmax warp
     mbar_init(bar_other_full, 128);
     mbar_init(bar_other_empty, 128);
@@ -406,7 +408,7 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     if (lane == 0) mbar_arrive(bar_item_empty(n % kItems));
   };
 
-  if (warp < 8) {
+  if (warp < 4 * kGroups) {
     // ------------------------------------------------------------ softmax groups
     setmaxnreg_inc<C::kRegsSoftmax>();
     const int g = warp >> 2;
@@ -415,7 +417,7 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     uint32_t tile = 0;                                     // tiles before the segment
     uint32_t par = 0;                                      // parities: bit 0 S, 1 O final, 2 group 1's results, 3 Q
-    bool ok = g < kGroups;
+    bool ok = true;
     for (int seg = 0; ok; ++seg) {
       uint32_t at, end;                                    // this group's tiles at, at + dx, ... below end, counted from the kernel's start
       int dx, lim;                                         // lim: keys that this row sees from the tile on
@@ -786,73 +788,80 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       else segments(std::integral_constant<int, most - 2>());
     }
     __syncwarp();
-  } else if (warp >= 12) {
+  } else if (warp >= 12 || warp < 8) {
     // ------------------------------------------------------------ converters
     setmaxnreg_dec<C::kRegsOther>();
-    const int cw = warp - 12;
+    const int cw = warp >= 12 ? warp - 12 : warp;          // (with one group warps 4-7 are the converters 4-7)
     bool ok = true;
     int tile = 0;
     Item it;
     for (int seg = 0; ok && take(seg, it); ++seg) {
       const int len = field(seg, kLen), t0 = field(seg, kT0);
-      // ---- Q: 16 bytes a lane, four loads of a warp under way; this warp's 32 rows of each row tile. The rows are in L2 by
-      // now (the scheduler). All wait for this once the last S is done, and its code comes from memory nearly every
-      // time: unrolled eightfold it took 45000 cycles, at about 230 for 128 bytes of it.
+      // ---- Q, this warp's rows of each row tile. A row's bf16 values take as many bytes as its two terms: all rows come
+      // at once by asynchronous copies (from L2: the scheduler) to where their terms will be, and are converted in place,
+      // 16 bytes a lane. All wait for this once the last S is done, and its code comes from memory nearly every time, at about
+      // 230 cycles for 128 bytes of it: so it is rolled up (unrolled eightfold it took 45000 cycles).
       ok = wait(bar_q_empty, (seg & 1) ^ 1, abort_flag, p.timeout_ns);
       if (!__all_sync(0xffffffffu, ok)) break;
       constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes; // lanes of a row, rows of a load
+      constexpr int kMine = 128 / C::kConv;                // rows of a warp
       const int piece_q = lane % kLanes, sub = lane / kLanes;
+      // where piece x of a row's bf16 values lands: the first half in the first term's row, the second in the second's
+      const uint32_t raw_at = (piece_q / (kLanes / 2)) * C::kQTerm + (piece_q % (kLanes / 2) >> 3) * 16384;
       const int step_tok = kAtOnce / p.G, step_head = kAtOnce - step_tok * p.G;
 #pragma unroll 1
       for (int group = 0; group < (it.split ? 1 : kGroups); ++group) {
-        int tok = (32 * cw + sub) / p.G, head = 32 * cw + sub - tok * p.G;   // of the next load
+        int tok = (kMine * cw + sub) / p.G, head = kMine * cw + sub - tok * p.G;
         const int first_token = field(seg, kTok0) + group * p.tt, left = min(p.tt, field(seg, kNew) - first_token);
         const __nv_bfloat16* const src = p.q + static_cast<long long>(field(seg, kH) * p.G) * p.q_sh +
                                          (static_cast<long long>(field(seg, kRow0)) + first_token) * p.q_st + 8 * piece_q;
-        uint4 v[4];
 #pragma unroll 1
-        for (int i = -4; i < 32 / kAtOnce; ++i) {
-          const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-          v[0] = v[1];
-          v[1] = v[2];
-          v[2] = v[3];
-          v[3] = make_uint4(0, 0, 0, 0);
-          if (i + 4 < 32 / kAtOnce && tok < left && 8 * piece_q < p.c.d)
-            v[3] = *reinterpret_cast<const uint4*>(src + head * p.q_sh + tok * p.q_st);
+        for (int row = kMine * cw + sub; row < kMine * cw + kMine; row += kAtOnce) {
+          const bool real = tok < left && 8 * piece_q < p.c.d;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(swz128(s_q(group, 0) + raw_at, row, piece_q & 7)),
+                       "l"(real ? src + head * p.q_sh + tok * p.q_st : p.q), "r"(real ? 16 : 0) : "memory");
           tok += step_tok;
           head += step_head;
           if (head >= p.G) {
             head -= p.G;
             ++tok;
           }
-          if (i < 0) continue;
-          const int row = 32 * cw + sub + kAtOnce * i;
-          uint32_t m = 0;                                  // the largest magnitude, as bits
-#pragma unroll
-          for (int k = 0; k < 4; ++k) m = max(m, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-          uint32_t amax = __reduce_max_sync(0xffffffffu, sub == 0 ? m : 0u);
-          if (kAtOnce == 2) {
-            const uint32_t second = __reduce_max_sync(0xffffffffu, sub == 1 ? m : 0u);
-            if (sub == 1) amax = second;
-          }
-          // exponent that brings the largest to [128, 256); bounded so that both powers are normal.
-          // A row with an infinity or NaN becomes NaN, as its logits are.
-          const int e2 = amax > 0 ? max(-100, min(100, static_cast<int>(amax >> 7) - 127 - 7)) : 0;
-          const float down = amax < 0x7F80u ? __uint_as_float(static_cast<uint32_t>(127 - e2) << 23) : NAN;
-          if (piece_q == 0) row_scale[group * 128 + row] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
-          uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            // (eight significant bits and at most 256: f16 holds what the two terms can)
-            const uint32_t x = pack_f16x2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
-            const uint32_t c0 = f16x2_to_e4m3x2(x);
-            hi[k >> 1] |= c0 << (16 * (k & 1));
-            lo[k >> 1] |= f16x2_to_e4m3x2(sub_f16x2(x, e4m3x2_to_f16x2(c0))) << (16 * (k & 1));
-          }
-          const uint32_t at = swz128((piece_q >> 4) * 16384, row, (piece_q & 15) >> 1) + (piece_q & 1) * 8;
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" :: "r"(s_q(group, 0) + at), "r"(hi[0]), "r"(hi[1]) : "memory");
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" :: "r"(s_q(group, 1) + at), "r"(lo[0]), "r"(lo[1]) : "memory");
         }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+#pragma unroll 1
+      for (int r = 0; r < (it.split ? 1 : kGroups) * kMine; r += kAtOnce) {
+        const int group = r / kMine, row = kMine * cw + sub + r % kMine;
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(swz128(s_q(group, 0) + raw_at, row, piece_q & 7)) : "memory");
+        uint32_t m = 0;                                    // the largest magnitude, as bits
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m = max(m, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+        uint32_t amax = __reduce_max_sync(0xffffffffu, sub == 0 ? m : 0u);   // (all have read the rows when it returns)
+        if (kAtOnce == 2) {
+          const uint32_t second = __reduce_max_sync(0xffffffffu, sub == 1 ? m : 0u);
+          if (sub == 1) amax = second;
+        }
+        // exponent that brings the largest to [128, 256); bounded so that both powers are normal.
+        // A row with an infinity or NaN becomes NaN, as its logits are.
+        const int e2 = amax > 0 ? max(-100, min(100, static_cast<int>(amax >> 7) - 127 - 7)) : 0;
+        const float down = amax < 0x7F80u ? __uint_as_float(static_cast<uint32_t>(127 - e2) << 23) : NAN;
+        if (piece_q == 0) row_scale[group * 128 + row] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+        uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          // (eight significant bits and at most 256: f16 holds what the two terms can)
+          const uint32_t x = pack_f16x2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
+          const uint32_t c0 = f16x2_to_e4m3x2(x);
+          hi[k >> 1] |= c0 << (16 * (k & 1));
+          lo[k >> 1] |= f16x2_to_e4m3x2(sub_f16x2(x, e4m3x2_to_f16x2(c0))) << (16 * (k & 1));
+        }
+        const uint32_t at = swz128((piece_q >> 4) * 16384, row, (piece_q & 15) >> 1) + (piece_q & 1) * 8;
+        __syncwarp();
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" :: "r"(s_q(group, 0) + at), "r"(hi[0]), "r"(hi[1]) : "memory");
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" :: "r"(s_q(group, 1) + at), "r"(lo[0]), "r"(lo[1]) : "memory");
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -860,8 +869,9 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       done(seg);
       // ---- V: 16 codes of a key at a time, from the codes' swizzled rows to two units of the halves' rows. Eight lanes, whose
       // 16 bytes go together, take four pieces of one box (64 columns) of keys k and k ^ 5: no bank twice, in the load
-      // or in either store. A thread's keys are 32 apart, so one address each serves with constant offsets.
-      constexpr int kBoxes = D / 64;
+      // or in either store. A thread's keys are kApart apart, so one address each serves with constant offsets.
+      constexpr int kBoxes = D / 64, kPieces = C::kKeysV * D / 16 / (32 * C::kConv);   // of a thread
+      constexpr int kApart = 8 * C::kConv;
       const int quad = lane & 3, key0 = 2 * ((lane >> 3) + 4 * cw) ^ (lane & 4 ? 5 : 0);
       const uint32_t from = swz128(0, key0, quad), to = swz128(0, key0, 2 * quad);
       for (int j = t0; j < t0 + it.n && ok; ++j, ++tile) {
@@ -879,12 +889,12 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           const uint32_t src = s_codes(slot) + from, dst = s_half(slot) + to;
           const bool all = valid >= C::kKeysV && here0 && (C::kPerTile == 2 || here1);
 #pragma unroll 1
-          for (int half = 0; half < 2; ++half) {           // of the rows, four pieces each
-            const int down = half * (4 / kBoxes) * 32;
+          for (int four = 0; four < kPieces / 4; ++four) {
+            const int down = four * (4 / kBoxes) * kApart;
             uint4 w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int box = e % kBoxes, step = 32 * (e / kBoxes);
+              const int box = e % kBoxes, step = kApart * (e / kBoxes);
               if (64 * box >= p.c.d) continue;
               const uint32_t at = (src ^ ((box & 1) * 64)) + (box >> 1) * 8192 + (down + step) * 128;
               asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[e].x), "=r"(w[e].y), "=r"(w[e].z), "=r"(w[e].w) : "r"(at) : "memory");
@@ -892,13 +902,13 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
             if (!all) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const int key = key0 + down + 32 * (e / kBoxes);
+                const int key = key0 + down + kApart * (e / kBoxes);
                 if (!(key < valid && (key < 64 ? here0 : here1))) w[e] = make_uint4(0, 0, 0, 0);
               }
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int box = e % kBoxes, step = 32 * (e / kBoxes);
+              const int box = e % kBoxes, step = kApart * (e / kBoxes);
               if (64 * box >= p.c.d) continue;
               const uint32_t at = box * C::kBoxV + (down + step) * 128;
               store16(dst + at, e4m3x2_to_f16x2(w[e].x & 0xFFFFu), e4m3x2_to_f16x2(w[e].x >> 16), e4m3x2_to_f16x2(w[e].y & 0xFFFFu),
@@ -1001,6 +1011,20 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         z = static_cast<int>(ph);
       };
       scales_of(page_of(blk0));
+      int va = -1, vb = -1;                                // the last tile's blocks, whose V is still to come
+      auto load_v = [&](int t, int a, int b) {
+#pragma unroll 1
+        for (int x = 0; x < C::kPerTile && ok; ++x) {
+          const int c = t * C::kPerTile + x, cs = c % C::kRingV, za = C::kPerTile == 1 || x == 0 ? a : b;
+          ok = wait(bar_c_empty(cs), ((c / C::kRingV) & 1) ^ 1, abort_flag, p.timeout_ns);
+          if (!ok) break;
+          // a stage is two boxes: both blocks (d up to 128), or both halves of one block's columns
+          const bool two = C::kPerTile == 1 ? b >= 0 : za >= 0;
+          mbar_arrive_expect_tx(bar_c_full(cs), ((za >= 0) + two) * 8192);
+          if (za >= 0) tma_load_3d(s_codes(cs), &map_v, bar_c_full(cs), 0, 0, za);
+          if (two) tma_load_3d(s_codes(cs) + 8192, &map_v, bar_c_full(cs), C::kPerTile == 1 ? 0 : 128, 0, C::kPerTile == 1 ? b : za);
+        }
+      };
       for (int blk = blk0; blk < blk1 && ok; blk += 32) {
         const float ks_now = ks, vs_now = vs;
         const int z_now = z, next_page = page_of(blk + 32);
@@ -1029,27 +1053,17 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(bar_k_full(slot));
-#pragma unroll
-            for (int x = 0; x < C::kPerTile && ok; ++x) {
-              const int c = tile * C::kPerTile + x, cs = c % C::kRingV;
-              ok = wait(bar_c_empty(cs), ((c / C::kRingV) & 1) ^ 1, abort_flag, p.timeout_ns);
-              if (!ok) break;
-              if (C::kPerTile == 1) {
-                mbar_arrive_expect_tx(bar_c_full(cs), ((za >= 0) + (zb >= 0)) * 8192);
-                if (za >= 0) tma_load_3d(s_codes(cs), &map_v, bar_c_full(cs), 0, 0, za);
-                if (zb >= 0) tma_load_3d(s_codes(cs) + 8192, &map_v, bar_c_full(cs), 0, 0, zb);
-              } else {
-                const int zx = x ? zb : za;
-                mbar_arrive_expect_tx(bar_c_full(cs), zx >= 0 ? 8192 * C::kCh : 0);
-                for (int ch = 0; ch < C::kCh; ++ch)
-                  if (zx >= 0) tma_load_3d(s_codes(cs) + ch * 8192, &map_v, bar_c_full(cs), ch * 128, 0, zx);
-              }
-            }
+            // V a tile behind K: S of the next tile comes before this one's product
+            if (blk + i > blk0) load_v(tile - 1, va, vb);
           }
+          va = za;
+          vb = zb;
           ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
           if (i == 16) scales_of(next_page);
         }
       }
+      if (lane == 0 && ok) load_v(tile - 1, va, vb);
+      ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
     }
     __syncwarp();
   } else if (warp == 11) {

@@ -288,32 +288,32 @@ def chunk(segments, seed, *, groups=2, ring_k=3, q_read=True, other_empty=True, 
         for seg, (split, n0, n) in enumerate(segments):
             yield from take(seg, "producer")
             done(seg, "producer")
-            for _ in range(n):
-                yield from run.wait(k_empty[t % ring_k], ((t // ring_k) & 1) ^ 1, "producer K", t // ring_k - 1)
+            for i in range(n + 1):                       # K a tile ahead of V
+                if i < n:
+                    yield from run.wait(k_empty[t % ring_k], ((t // ring_k) & 1) ^ 1, "producer K", t // ring_k - 1)
+                    ready = [0]
 
-                ready = [0]
+                    def land(t=t, ready=ready):          # the bytes and the producer's arrival behind the scales
+                        ready[0] += 1
+                        if ready[0] == 2:
+                            k_full[t % ring_k].arrive()
 
-                def land(t=t, ready=ready):          # the bytes and the producer's arrival behind the scales
-                    ready[0] += 1
-                    if ready[0] == 2:
-                        k_full[t % ring_k].arrive()
-
-                def bytes_there(t=t, land=land):
-                    k_slot[t % ring_k] = t
+                    def bytes_there(t=t, land=land):
+                        k_slot[t % ring_k] = t
+                        land()
+                    run.later(*land_in, bytes_there)
+                    yield run.delay(5, scales)
+                    info[t % infos] = t
                     land()
-                run.later(*land_in, bytes_there)
-                yield run.delay(5, scales)
-                info[t % infos] = t
-                land()
-                for x in range(per):
-                    c = t * per + x
+                    t += 1
+                for x in range(per if i > 0 else 0):
+                    c = (t - 2 if i < n else t - 1) * per + x
                     yield from run.wait(c_empty[c % 2], ((c // 2) & 1) ^ 1, "producer V", c // 2 - 1)
 
                     def land_v(c=c):
                         c_slot[c % 2] = c
                         c_full[c % 2].arrive()
                     run.later(*land_in, land_v)
-                t += 1
 
     def issuer():
         t, np = 0, [0, 0]
