@@ -831,37 +831,45 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       asm volatile("cp.async.wait_all;" ::: "memory");
       __syncwarp();
 #pragma unroll 1
-      for (int r = 0; r < (it.split ? 1 : kGroups) * kMine; r += kAtOnce) {
-        const int group = r / kMine, row = kMine * cw + sub + r % kMine;
-        uint32_t w[4];
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(swz128(s_q(group, 0) + raw_at, row, piece_q & 7)) : "memory");
-        uint32_t m = 0;                                    // the largest magnitude, as bits
+      for (int r = 0; r < (it.split ? 1 : kGroups) * kMine; r += 2 * kAtOnce) {
+        const int group = r / kMine, row0 = kMine * cw + sub + r % kMine;   // and row0 + kAtOnce beside it
+        uint32_t w[2][4], hi[2][2], lo[2][2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) m = max(m, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-        uint32_t amax = __reduce_max_sync(0xffffffffu, sub == 0 ? m : 0u);   // (all have read the rows when it returns)
-        if (kAtOnce == 2) {
-          const uint32_t second = __reduce_max_sync(0xffffffffu, sub == 1 ? m : 0u);
-          if (sub == 1) amax = second;
-        }
-        // exponent that brings the largest to [128, 256); bounded so that both powers are normal.
-        // A row with an infinity or NaN becomes NaN, as its logits are.
-        const int e2 = amax > 0 ? max(-100, min(100, static_cast<int>(amax >> 7) - 127 - 7)) : 0;
-        const float down = amax < 0x7F80u ? __uint_as_float(static_cast<uint32_t>(127 - e2) << 23) : NAN;
-        if (piece_q == 0) row_scale[group * 128 + row] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
-        uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+        for (int e = 0; e < 2; ++e)
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[e][0]), "=r"(w[e][1]), "=r"(w[e][2]), "=r"(w[e][3])
+                       : "r"(swz128(s_q(group, 0) + raw_at, row0 + e * kAtOnce, piece_q & 7)) : "memory");
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          // (eight significant bits and at most 256: f16 holds what the two terms can)
-          const uint32_t x = pack_f16x2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
-          const uint32_t c0 = f16x2_to_e4m3x2(x);
-          hi[k >> 1] |= c0 << (16 * (k & 1));
-          lo[k >> 1] |= f16x2_to_e4m3x2(sub_f16x2(x, e4m3x2_to_f16x2(c0))) << (16 * (k & 1));
+        for (int e = 0; e < 2; ++e) {
+          uint32_t m = 0;                                  // the largest magnitude, as bits
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m = max(m, max(w[e][k] & 0x7FFFu, (w[e][k] >> 16) & 0x7FFFu));
+          uint32_t amax = __reduce_max_sync(0xffffffffu, sub == 0 ? m : 0u);
+          if (kAtOnce == 2) {
+            const uint32_t second = __reduce_max_sync(0xffffffffu, sub == 1 ? m : 0u);
+            if (sub == 1) amax = second;
+          }
+          // exponent that brings the largest to [128, 256); bounded so that both powers are normal.
+          // A row with an infinity or NaN becomes NaN, as its logits are.
+          const int e2 = amax > 0 ? max(-100, min(100, static_cast<int>(amax >> 7) - 127 - 7)) : 0;
+          const float down = amax < 0x7F80u ? __uint_as_float(static_cast<uint32_t>(127 - e2) << 23) : NAN;
+          if (piece_q == 0) row_scale[group * 128 + row0 + e * kAtOnce] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+          hi[e][0] = hi[e][1] = lo[e][0] = lo[e][1] = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            // (eight significant bits and at most 256: f16 holds what the two terms can)
+            const float x0 = __uint_as_float(w[e][k] << 16) * down, x1 = __uint_as_float(w[e][k] & 0xFFFF0000u) * down;
+            const uint32_t c0 = pack_e4m3x2(x0, x1);
+            hi[e][k >> 1] |= c0 << (16 * (k & 1));
+            lo[e][k >> 1] |= f16x2_to_e4m3x2(sub_f16x2(pack_f16x2(x0, x1), e4m3x2_to_f16x2(c0))) << (16 * (k & 1));
+          }
         }
-        const uint32_t at = swz128((piece_q >> 4) * 16384, row, (piece_q & 15) >> 1) + (piece_q & 1) * 8;
-        __syncwarp();
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" :: "r"(s_q(group, 0) + at), "r"(hi[0]), "r"(hi[1]) : "memory");
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" :: "r"(s_q(group, 1) + at), "r"(lo[0]), "r"(lo[1]) : "memory");
+        __syncwarp();                                      // all have read the rows
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t at = swz128((piece_q >> 4) * 16384, row0 + e * kAtOnce, (piece_q & 15) >> 1) + (piece_q & 1) * 8;
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" :: "r"(s_q(group, 0) + at), "r"(hi[e][0]), "r"(hi[e][1]) : "memory");
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" :: "r"(s_q(group, 1) + at), "r"(lo[e][0]), "r"(lo[e][1]) : "memory");
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
