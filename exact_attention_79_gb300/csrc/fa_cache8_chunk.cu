@@ -809,23 +809,24 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       // where piece x of a row's bf16 values lands: the first half in the first term's row, the second in the second's
       const uint32_t raw_at = (piece_q / (kLanes / 2)) * C::kQTerm + (piece_q % (kLanes / 2) >> 3) * 16384;
       const int step_tok = kAtOnce / p.G, step_head = kAtOnce - step_tok * p.G;
+      const long long step_plain = step_tok * p.q_st + step_head * p.q_sh, step_wrapped = step_plain + p.q_st - p.G * p.q_sh;
 #pragma unroll 1
       for (int group = 0; group < (it.split ? 1 : kGroups); ++group) {
         int tok = (kMine * cw + sub) / p.G, head = kMine * cw + sub - tok * p.G;
         const int first_token = field(seg, kTok0) + group * p.tt, left = min(p.tt, field(seg, kNew) - first_token);
-        const __nv_bfloat16* const src = p.q + static_cast<long long>(field(seg, kH) * p.G) * p.q_sh +
-                                         (static_cast<long long>(field(seg, kRow0)) + first_token) * p.q_st + 8 * piece_q;
-#pragma unroll 1
+        const __nv_bfloat16* src = p.q + (static_cast<long long>(field(seg, kH)) * p.G + head) * p.q_sh +
+                                   (static_cast<long long>(field(seg, kRow0)) + first_token + tok) * p.q_st + 8 * piece_q;
+        const uint32_t dst = s_q(group, 0) + raw_at;
+        if (8 * piece_q >= p.c.d) tok = p.tt;              // (columns behind d: zeros)
+#pragma unroll 2
         for (int row = kMine * cw + sub; row < kMine * cw + kMine; row += kAtOnce) {
-          const bool real = tok < left && 8 * piece_q < p.c.d;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(swz128(s_q(group, 0) + raw_at, row, piece_q & 7)),
-                       "l"(real ? src + head * p.q_sh + tok * p.q_st : p.q), "r"(real ? 16 : 0) : "memory");
-          tok += step_tok;
-          head += step_head;
-          if (head >= p.G) {
-            head -= p.G;
-            ++tok;
-          }
+          const bool real = tok < left;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(swz128(dst, row, piece_q & 7)),
+                       "l"(real ? src : p.q), "r"(real ? 16 : 0) : "memory");
+          const bool wrap = head + step_head >= p.G;
+          tok += step_tok + wrap;
+          head += step_head - (wrap ? p.G : 0);
+          src += wrap ? step_wrapped : step_plain;
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
