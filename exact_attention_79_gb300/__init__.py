@@ -342,26 +342,49 @@ def new_rope(freqs, axis=None, interleaved=False, device="cuda"):
 def _rope_specs(rope, axes):
     """The plan's tensors as _require takes them and its C form."""
     import torch
-    pairs = rope.turns.numel()
-    specs = [(rope.turns, "rope.turns", torch.int64, (pairs,))]
-    if rope.axis is not None:
-        specs.append((rope.axis, "rope.axis", torch.int32, (pairs,)))
-    return specs, _Rope(rope.turns.data_ptr(), None if rope.axis is None else rope.axis.data_ptr(), pairs, axes,
-                        int(bool(rope.interleaved)))
+    turns, axis, interleaved = rope
+    pairs = turns.numel()
+    specs = [(turns, "rope.turns", torch.int64, (pairs,))]
+    if axis is not None:
+        specs.append((axis, "rope.axis", torch.int32, (pairs,)))
+    return specs, _Rope(turns.data_ptr(), None if axis is None else axis.data_ptr(), pairs, axes, 1 if interleaved else 0)
 
 
 def _rope_strides(x, name, shape, dtype):
     """Batch, head and token strides of a [B, H, T, d] (or [H, T, d]) tensor whose rows of d values are contiguous and
     16-byte aligned. A dimension of size 1 gets a stride that nothing reads through."""
-    if x.dtype != dtype or x.shape != shape:
+    if x.dtype is not dtype or x.shape != shape:
         raise ValueError(f"{name}: expected {dtype} of shape {tuple(shape)}, got {x.dtype} of shape {tuple(x.shape)}")
-    d, unit = shape[-1], 16 // dtype.itemsize
-    if d > 1 and x.stride(-1) != 1:
+    *outer, H, T, d = shape
+    *sb, sh, st, sd = x.stride()
+    sb = sb[0] if outer and outer[0] > 1 else 0
+    sh, st = (sh if H > 1 else d), (st if T > 1 else d)
+    if sd != 1 and d > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    strides = [s if n > 1 else d for n, s in zip(shape[:-1], x.stride()[:-1])]
-    if any(s % unit for s in strides):
+    unit = 16 // dtype.itemsize
+    if sb % unit or sh % unit or st % unit:
         raise ValueError(f"{name}: strides other than the last must be multiples of {unit}")
-    return strides if len(strides) == 3 else [0, *strides]
+    return sb, sh, st
+
+
+def _rope_positions(positions, B, T, batched, one_axis):
+    """Axes and the strides between them and between batches of int32 positions [axes, B, T], with the batch's dimension
+    or without it, with the axes' or (one axis) without it."""
+    import torch
+    shape = positions.shape
+    n = len(shape)
+    if positions.dtype is not torch.int32 or not 1 <= n <= (3 if batched else 2) or shape[-1] != T or \
+            (T > 1 and positions.stride(-1) != 1):
+        raise ValueError("positions must be int32 [axes, B, T], [axes, T] or [T], the last dimension contiguous")
+    if n == 1:
+        return 1, 0, 0
+    if n == 3:
+        if shape[1] != B:
+            raise ValueError("positions must be [axes, B, T]")
+        return shape[0], positions.stride(0), positions.stride(1)
+    if batched and shape[0] == B and one_axis:
+        return 1, 0, positions.stride(0)                            # [B, T]
+    return shape[0], positions.stride(0), 0
 
 
 def rope(q, k, rope, positions, inverse=False, q_out=None, k_out=None):
@@ -370,59 +393,53 @@ def rope(q, k, rope, positions, inverse=False, q_out=None, k_out=None):
 
     q: [B, Hq, T, d] or [Hq, T, d], bf16 or fp32, any strides that are multiples of 16 bytes (a projection's
     [B, T, H, d].transpose(1, 2) too); k: the same with its own heads, or None. positions: int32, [axes, B, T] (3-D q:
-    [axes, T]); the batch may be left out where all share them, and the axes where there is one. q_out, k_out: where the
-    results go, in any such layout (q and k themselves too); otherwise tensors laid out like q and k. Returns (q_out,
+    [axes, T]); the batch may be left out where all share them, and the axes where the Rope names none. q_out, k_out: where
+    the results go, in any such layout (q and k themselves too); otherwise tensors laid out like q and k. Returns (q_out,
     k_out), k_out None without k."""
     import torch
-    if q.dim() not in (3, 4):
+    shape, dtype, dev = q.shape, q.dtype, q.device
+    batched = len(shape) == 4
+    if not batched and len(shape) != 3:
         raise ValueError("q must be [B, H, T, d] or [H, T, d]")
-    dtype, dev, batched = q.dtype, q.device, q.dim() == 4
-    if dtype not in (torch.bfloat16, torch.float32):
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise ValueError("q and k must be bf16 or fp32")
-    B, (Hq, T, d) = q.shape[0] if batched else 1, q.shape[-3:]
-    qs = _rope_strides(q, "q", q.shape, dtype)
-    placed, Hkv, ks, kos = [], 0, [0, 0, 0], [0, 0, 0]
+    B, (Hq, T, d) = shape[0] if batched else 1, shape[-3:]
+    axes, sa, sb = _rope_positions(positions, B, T, batched, rope.axis is None)
+    specs, plan = _rope_specs(rope, axes)
+    placed = [(positions, "positions")]
+    qs = _rope_strides(q, "q", shape, dtype)
+    q_os, ks, k_os = qs, (0, 0, 0), (0, 0, 0)
     if q_out is not None:
+        q_os = _rope_strides(q_out, "q_out", shape, dtype)
         placed.append((q_out, "q_out"))
+    Hkv = 0
     if k is not None:
-        if k.dim() != q.dim():
+        if len(k.shape) != len(shape):
             raise ValueError("k must have as many dimensions as q")
         Hkv = k.shape[-3]
-        shape = (*k.shape[:-3], Hkv, T, d) if not batched else (B, Hkv, T, d)
-        ks = _rope_strides(k, "k", shape, dtype)
+        k_shape = (B, Hkv, T, d) if batched else (Hkv, T, d)
+        ks = k_os = _rope_strides(k, "k", k_shape, dtype)
         placed.append((k, "k"))
         if k_out is not None:
-            kos = _rope_strides(k_out, "k_out", shape, dtype)
+            k_os = _rope_strides(k_out, "k_out", k_shape, dtype)
             placed.append((k_out, "k_out"))
     elif k_out is not None:
         raise ValueError("k_out without k")
-    if q_out is not None:
-        _rope_strides(q_out, "q_out", q.shape, dtype)
-    # positions to [axes, B, T]: with the batch's dimension or without it
-    n = positions.dim()
-    if positions.dtype != torch.int32 or n < 1 or positions.shape[-1] != T or n > (3 if batched else 2) or \
-            (T > 1 and positions.stride(-1) != 1):
-        raise ValueError("positions must be int32 [axes, B, T], [axes, T] or [T], the last dimension contiguous")
-    if batched and n == 2 and positions.shape[0] == B and rope.axis is None:
-        axes, sa, sb = 1, 0, positions.stride(0)                    # [B, T], one axis
-    elif n == 3:
-        if positions.shape[1] != B:
-            raise ValueError("positions must be [axes, B, T]")
-        axes, sa, sb = positions.shape[0], positions.stride(0), positions.stride(1)
-    else:
-        axes, sa, sb = (positions.shape[0], positions.stride(0), 0) if n == 2 else (1, 0, 0)
-    specs, plan = _rope_specs(rope, axes)
     _require(dev, *specs)
-    _placed(dev, (positions, "positions"), *placed)
-    q_out = torch.empty_like(q) if q_out is None else q_out
+    _placed(dev, *placed)
+    if q_out is None:
+        q_out = torch.empty_like(q)
+        if q_out.stride() != q.stride():                # (a cut out of something wider is laid out anew)
+            q_os = _rope_strides(q_out, "q_out", shape, dtype)
     if k is not None and k_out is None:
         k_out = torch.empty_like(k)
-        kos = _rope_strides(k_out, "k_out", k.shape, dtype)
+        if k_out.stride() != k.stride():
+            k_os = _rope_strides(k_out, "k_out", k_shape, dtype)
     if q.numel() == 0:
         return q_out, k_out
-    _call_on(dev, "fa_rope", q.data_ptr(), *qs, q_out.data_ptr(), *_rope_strides(q_out, "q_out", q.shape, dtype), Hq,
-             None if k is None else k.data_ptr(), *ks, None if k is None else k_out.data_ptr(), *kos, Hkv, B, T, d,
-             dtype.itemsize, ctypes.byref(plan), positions.data_ptr(), sa, sb, int(bool(inverse)))
+    _call_on(dev, "fa_rope", q.data_ptr(), *qs, q_out.data_ptr(), *q_os, Hq, None if k is None else k.data_ptr(), *ks,
+             None if k is None else k_out.data_ptr(), *k_os, Hkv, B, T, d, dtype.itemsize, ctypes.byref(plan),
+             positions.data_ptr(), sa, sb, 1 if inverse else 0)
     return q_out, k_out
 
 
