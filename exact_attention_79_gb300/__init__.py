@@ -435,7 +435,7 @@ def rope(q, k, rope, positions, inverse=False, q_out=None, k_out=None):
         k_out = torch.empty_like(k)
         if k_out.stride() != k.stride():
             k_os = _rope_strides(k_out, "k_out", k_shape, dtype)
-    if q.numel() == 0:
+    if T == 0 or B == 0:
         return q_out, k_out
     _call_on(dev, "fa_rope", q.data_ptr(), *qs, q_out.data_ptr(), *q_os, Hq, None if k is None else k.data_ptr(), *ks,
              None if k is None else k_out.data_ptr(), *k_os, Hkv, B, T, d, dtype.itemsize, ctypes.byref(plan),

@@ -10,6 +10,10 @@
 // instructions on finding their block (35 us). 30011 tokens of 8 heads, d 128: 31 us, 6.0 TB/s;
 // one token each for 64 sequences 5.3 us, which is the launch and two rounds of loads. Every CTA looks through
 // the sequences 32 at a time: 256 sequences take 21 us, 1024 131, 4096 1475.
+//
+// With rotation K's pairs of columns are turned by their positions on the way, in fp32, and the block's scale is that of the
+// rotated values, so K is rounded once. The angles are the same for all heads of a token: a CTA computes them once for
+// several. Issue-bound then (about 14 instructions per value of K).
 #include "fa_cache8.cuh"
 #include "fa_rope.cuh"
 
@@ -71,11 +75,12 @@ struct NewTokens {
   int lo, hi, tok0, pos0, page;
 };
 
-// K of one block for heads [h0, h1), each pair of columns turned by its angle on the way. A thread has
-// four pairs (eight columns) of up to kUnits tokens; their cosines and sines are computed once and serve
-// all its heads. The rotated values stay in fp32 until they are codes.
-template <int D, int N>
-__device__ __forceinline__ void append_rotated(const Cache8AppendParams& p, const NewTokens& n, int h0, int h1, float (*warp_max)[N / 32]) {
+// K, and with kBoth V, of one block for heads [h0, h1), each pair of K's columns turned by its angle on the way. A thread has
+// four pairs (eight columns) of up to kUnits tokens; their cosines and sines are computed once, kept in shared
+// memory where it has only this thread's, and serve all its heads. The rotated values stay in fp32 until they are codes. The
+// next head's loads are under way meanwhile.
+template <int D, int N, bool kBoth>
+__device__ __forceinline__ void append_rotated(const Cache8AppendParams& p, const NewTokens& n, int h0, int h1, float2 (*warp_max)[N / 32], float4* table) {
   constexpr int kUnits = kCacheBlock * D / 8 / N;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int upt = p.c.d / 8, slots = N / upt;               // units of a token, tokens at a time
@@ -87,100 +92,159 @@ __device__ __forceinline__ void append_rotated(const Cache8AppendParams& p, cons
   auto row_of = [&](int i) { return slot + i * slots; };
   auto mine = [&](int i) { return slot < slots && row_of(i) < count; };
   uint2 raw[kUnits][2];
+  uint4 raw_v[kBoth ? kUnits : 1];
   auto load = [&](int h) {
     const __nv_bfloat16* const x = static_cast<const __nv_bfloat16*>(p.k) + h * p.k_sh;
+    const __nv_bfloat16* const y = static_cast<const __nv_bfloat16*>(p.v) + h * p.v_sh;
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       raw[i][0] = raw[i][1] = make_uint2(0, 0);
+      if (kBoth) raw_v[kBoth ? i : 0] = make_uint4(0, 0, 0, 0);
       if (mine(i)) {
         const __nv_bfloat16* const row = x + (n.tok0 + row_of(i)) * p.k_st;
         raw[i][0] = *reinterpret_cast<const uint2*>(row + ca);
         raw[i][1] = *reinterpret_cast<const uint2*>(row + cb);
+        if (kBoth) raw_v[kBoth ? i : 0] = *reinterpret_cast<const uint4*>(y + (n.tok0 + row_of(i)) * p.v_st + 8 * c);
       }
     }
   };
   load(h0);
-  float2 cs[kUnits][4];
+  unsigned long long turns[4] = {0, 0, 0, 0};
+  const int* at[4] = {nullptr, nullptr, nullptr, nullptr};
+  if (turned) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    unsigned long long turns = 0;
-    const int* at = nullptr;
-    if (turned) {
-      turns = static_cast<unsigned long long>(p.rope.turns[4 * c + e]);
+    for (int e = 0; e < 4; ++e) {
+      turns[e] = static_cast<unsigned long long>(p.rope.turns[4 * c + e]);
       const int axis = p.rope.axis == nullptr ? 0 : max(0, min(p.rope.axis[4 * c + e], p.rope.axes - 1));
-      if (p.rope.positions != nullptr) at = p.rope.positions + axis * p.rope.pos_sa + n.tok0;
+      if (p.rope.positions != nullptr) at[e] = p.rope.positions + axis * p.rope.pos_sa + n.tok0;
     }
+  }
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
+  for (int i = 0; i < kUnits; ++i) {
+    float2 cs[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
       int pos = n.pos0 + row_of(i);
-      if (at != nullptr && mine(i)) pos = at[row_of(i)];
-      cs[i][e] = cos_sin_turns(turns, pos);
+      if (at[e] != nullptr && mine(i)) pos = at[e][row_of(i)];
+      cs[e] = cos_sin_turns(turns[e], pos);
     }
+    table[(2 * i) * N + tid] = make_float4(cs[0].x, cs[1].x, cs[2].x, cs[3].x);
+    table[(2 * i + 1) * N + tid] = make_float4(cs[0].y, cs[1].y, cs[2].y, cs[3].y);
   }
   if (n.page < 0 || n.page >= p.c.num_blocks) return;
   for (int h = h0; h < h1; ++h) {
     const size_t ph = static_cast<size_t>(n.page) * p.c.Hkv + h;
     uint8_t* const codes = p.c.k + ph * kCacheBlock * p.c.d;
-    float* const scale = p.c.k_scale + ph;
-    const float old = n.lo > 0 ? *scale : 0.f;              // read before the barrier, written after it
-    float f[kUnits][8];
-    float amax = 0.f;
+    uint8_t* const codes_v = p.c.v + ph * kCacheBlock * p.c.d;
+    // read before the barrier, written after it
+    const float old = n.lo > 0 ? p.c.k_scale[ph] : 0.f, old_v = kBoth && n.lo > 0 ? p.c.v_scale[ph] : 0.f;
+    float fa[kUnits][4], fb[kUnits][4];                     // the first and the second columns of the four pairs
+    uint4 v[kBoth ? kUnits : 1];
+    float2 amax = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       const uint32_t w[4] = {raw[i][0].x, raw[i][0].y, raw[i][1].x, raw[i][1].y};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        f[i][2 * e] = __uint_as_float(w[e] << 16);
-        f[i][2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+        const float lower = __uint_as_float(w[e] << 16), upper = __uint_as_float(w[e] & 0xFFFF0000u);
+        if (apart) {
+          (e < 2 ? fa : fb)[i][2 * (e & 1)] = lower;
+          (e < 2 ? fa : fb)[i][2 * (e & 1) + 1] = upper;
+        } else {
+          fa[i][e] = lower;
+          fb[i][e] = upper;
+        }
       }
-      if (apart) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) rotate(f[i][e], f[i][4 + e], cs[i][e]);
-      } else if (turned) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) rotate(f[i][2 * e], f[i][2 * e + 1], cs[i][e]);
+      if (turned) {
+        const float4 co = table[(2 * i) * N + tid], si = table[(2 * i + 1) * N + tid];
+        rotate2(fa[i][0], fa[i][1], fb[i][0], fb[i][1], co.x, co.y, si.x, si.y);
+        rotate2(fa[i][2], fa[i][3], fb[i][2], fb[i][3], co.z, co.w, si.z, si.w);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float a = fabsf(f[i][e]);
-        amax = fmaxf(amax, a < INFINITY ? a : 0.f);         // infinities and NaN are left out
-      }
+      for (int e = 0; e < 4; ++e) amax.x = fmaxf(amax.x, fmaxf(fabsf(fa[i][e]), fabsf(fb[i][e])));   // (NaN are left out)
+      if (kBoth) v[kBoth ? i : 0] = raw_v[kBoth ? i : 0];
+    }
+    if (!(amax.x < INFINITY)) {                             // an infinity: the largest of the others
+      amax.x = 0.f;
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = fabsf(fa[i][e]), y = fabsf(fb[i][e]);
+          amax.x = fmaxf(amax.x, fmaxf(x < INFINITY ? x : 0.f, y < INFINITY ? y : 0.f));
+        }
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < (kBoth ? kUnits : 0); ++i) top = max2(top, v[i]);
+    top = max(top & 0xFFFFu, top >> 16);
+    if (kBoth && top >= 0x7F80u) {
+      top = 0;
+      for (int i = 0; i < (kBoth ? kUnits : 0); ++i) top = finite_max(finite_max(finite_max(finite_max(top, v[i].x), v[i].y), v[i].z), v[i].w);
     }
     if (h + 1 < h1) load(h + 1);
-    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));   // (non-negative floats order like their bits)
-    float* const maxima = warp_max[(h - h0) & 1];           // (the other buffer may still be read for the head before)
+    // (non-negative floats order like their bits)
+    amax.x = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax.x)));
+    if (kBoth) amax.y = __uint_as_float(__reduce_max_sync(0xffffffffu, top << 16));
+    float2* const maxima = warp_max[(h - h0) & 1];          // (the other buffer may still be read for the head before)
     if (lane == 0) maxima[warp] = amax;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < N / 32; ++w) amax = fmaxf(amax, maxima[w]);
-    float now = fmaxf(old, power_scale(amax));
-    if (!(now > 0.f)) now = 1.f;
+    for (int w = 0; w < N / 32; ++w) {
+      amax.x = fmaxf(amax.x, maxima[w].x);
+      amax.y = fmaxf(amax.y, maxima[w].y);
+    }
+    auto grown = [&](float before, float most) {
+      const float s = fmaxf(before, power_scale(most));
+      return s > 0.f ? s : 1.f;
+    };
+    const float now = grown(old, amax.x), now_v = grown(old_v, amax.y);
     if (n.lo > 0 && now != old) rescale_codes(codes, n.lo * upt, __fdiv_rn(old, now), tid, N);
-    if (tid == 0) *scale = now;
-    const bool power = (__float_as_uint(now) & 0x7FFFFFu) == 0;   // as all made here are: 1 / now is exact
-    const float inv = __fdiv_rn(1.f, now);
+    if (kBoth && n.lo > 0 && now_v != old_v) rescale_codes(codes_v, n.lo * upt, __fdiv_rn(old_v, now_v), tid, N);
+    if (tid == 0) {
+      p.c.k_scale[ph] = now;
+      if (kBoth) p.c.v_scale[ph] = now_v;
+    }
+    // powers of two, as all made here are: 1 / now is exact
+    const bool power = (__float_as_uint(now) & 0x7FFFFFu) == 0, power_v = (__float_as_uint(now_v) & 0x7FFFFFu) == 0;
+    const float inv = __fdiv_rn(1.f, now), inv_v = __fdiv_rn(1.f, now_v);
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       if (!mine(i)) continue;
       if (power) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[i][e] *= inv;
+        for (int e = 0; e < 4; e += 2) {
+          mul2_bc(fa[i][e], fa[i][e + 1], inv);
+          mul2_bc(fb[i][e], fb[i][e + 1], inv);
+        }
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[i][e] = __fdiv_rn(f[i][e], now);
+        for (int e = 0; e < 4; ++e) {
+          fa[i][e] = __fdiv_rn(fa[i][e], now);
+          fb[i][e] = __fdiv_rn(fb[i][e], now);
+        }
       }
-      uint8_t* const dst = codes + (n.lo + row_of(i)) * p.c.d;
-      *reinterpret_cast<uint32_t*>(dst + ca) = pack_e4m3x2(f[i][0], f[i][1]) | pack_e4m3x2(f[i][2], f[i][3]) << 16;
-      *reinterpret_cast<uint32_t*>(dst + cb) = pack_e4m3x2(f[i][4], f[i][5]) | pack_e4m3x2(f[i][6], f[i][7]) << 16;
+      const int at = (n.lo + row_of(i)) * p.c.d;
+      uint32_t first, second;
+      if (apart) {
+        first = pack_e4m3x2(fa[i][0], fa[i][1]) | pack_e4m3x2(fa[i][2], fa[i][3]) << 16;
+        second = pack_e4m3x2(fb[i][0], fb[i][1]) | pack_e4m3x2(fb[i][2], fb[i][3]) << 16;
+      } else {
+        first = pack_e4m3x2(fa[i][0], fb[i][0]) | pack_e4m3x2(fa[i][1], fb[i][1]) << 16;
+        second = pack_e4m3x2(fa[i][2], fb[i][2]) | pack_e4m3x2(fa[i][3], fb[i][3]) << 16;
+      }
+      *reinterpret_cast<uint32_t*>(codes + at + ca) = first;
+      *reinterpret_cast<uint32_t*>(codes + at + cb) = second;
+      if (kBoth) *reinterpret_cast<uint2*>(codes_v + at + 8 * c) = power_v ? encode8(v[kBoth ? i : 0], inv_v) : divide8(v[kBoth ? i : 0], now_v);
     }
     if (p.c.weight != nullptr && tid < count) p.c.weight[ph * kCacheBlock + n.lo + tid] = 0.f;
   }
 }
 
-// D: 128 or 256, d at most that. Without rotation one CTA of kThreads per (touched block, KV head, K or V). With it (kRope, N threads) one per
-// (block, KV head) for V, and behind them one per (block, k_heads KV heads) for K.
-template <int D, bool kRope, int N>
-__global__ void __launch_bounds__(N, kRope ? 512 / N : D == 128 ? 8 : 4) cache8_append_kernel(const Cache8AppendParams p) {
+// D: 128 or 256, d at most that. kRotate 0: one CTA of kThreads per (touched block, KV head, K or V; V alone where K is
+// rotated). 1: K rotated, one CTA of N threads per block and `heads` KV heads. 2: V too, as it is.
+template <int D, int kRotate, int N>
+__global__ void __launch_bounds__(N, kRotate == 1 ? (D == 128 ? 3 : 1) : kRotate ? 512 / N : D == 128 ? 8 : 4) cache8_append_kernel(const Cache8AppendParams p) {
   constexpr int kThreads = N;
   constexpr int kMaxChunks = kCacheBlock * D / 8 / kThreads;   // 16-byte chunks of one block per thread
   __shared__ float warp_max[kThreads / 32];
@@ -223,16 +287,15 @@ __global__ void __launch_bounds__(N, kRope ? 512 / N : D == 128 ? 8 : 4) cache8_
   const int lo = max(0, s - blk * kCacheBlock);
   const int hi = min(kCacheBlock, s + (e - a) - blk * kCacheBlock);
   const int tok0 = a + (blk * kCacheBlock + lo - s);
-  if constexpr (kRope) {
-    if (static_cast<int>(blockIdx.y) >= p.c.Hkv) {
-      __shared__ float maxima[2][N / 32];
-      const int h0 = (static_cast<int>(blockIdx.y) - p.c.Hkv) * p.k_heads;
-      const NewTokens n{lo, hi, tok0, blk * kCacheBlock + lo, p.table[static_cast<long long>(b) * p.max_blocks + blk]};
-      append_rotated<D, N>(p, n, h0, min(h0 + p.k_heads, p.c.Hkv), maxima);
-      return;
-    }
+  if constexpr (kRotate > 0) {
+    __shared__ float2 maxima[2][N / 32];
+    const int h0 = static_cast<int>(blockIdx.y) * p.heads;
+    const NewTokens n{lo, hi, tok0, blk * kCacheBlock + lo, p.table[static_cast<long long>(b) * p.max_blocks + blk]};
+    extern __shared__ float4 table[];
+    append_rotated<D, N, kRotate == 2>(p, n, h0, min(h0 + p.heads, p.c.Hkv), maxima, table);
+    return;
   }
-  const int h = blockIdx.y, which = kRope ? 1 : blockIdx.z;
+  const int h = blockIdx.y, which = p.rope.pairs > 0 ? 1 : blockIdx.z;
   const int cpr = p.c.d / 8;                                  // chunks of eight values per token
   const int chunks = (hi - lo) * cpr;
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(which ? p.v : p.k) +
@@ -300,21 +363,40 @@ __global__ void __launch_bounds__(N, kRope ? 512 / N : D == 128 ? 8 : 4) cache8_
 
 }  // namespace
 
+template <int D, int kRotate, int N>
+static cudaError_t rotating(const Cache8AppendParams& p, unsigned items, cudaStream_t stream) {
+  constexpr int kTable = 2 * ((kCacheBlock * D / 8 + N - 1) / N) * N * static_cast<int>(sizeof(float4));
+  static PerDeviceOnce attr;
+  const cudaError_t e = attr.run([] {
+    return cudaFuncSetAttribute(cache8_append_kernel<D, kRotate, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTable);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_early(cache8_append_kernel<D, kRotate, N>, dim3(items, (p.c.Hkv + p.heads - 1) / p.heads), dim3(N), kTable, stream, p);
+}
+
 cudaError_t launch_cache8_append(const Cache8AppendParams& p, cudaStream_t stream) {
   // n tokens touch at most (n + 126) / 64 blocks of a sequence, and no more than n
   const long long most = (static_cast<long long>(p.T) + 126LL * p.B) / kCacheBlock;
   const unsigned items = static_cast<unsigned>(most < p.T ? most : p.T);
-  if (p.rope.pairs > 0) {
-    // Heads per CTA that rotates K: one where there are few blocks (a decoding step), all where there are many, whose
-    // angles are then computed once.
-    Cache8AppendParams r = p;
-    r.k_heads = static_cast<long long>(items) * p.c.Hkv <= 1216 ? 1 : p.c.Hkv < 8 ? p.c.Hkv : 8;
-    const dim3 grid(items, p.c.Hkv + (p.c.Hkv + r.k_heads - 1) / r.k_heads);
-    return p.c.d > 128 ? launch_early(cache8_append_kernel<256, true, 512>, grid, dim3(512), 0, stream, r)
-                       : launch_early(cache8_append_kernel<128, true, 256>, grid, dim3(256), 0, stream, r);
+  const bool wide = p.c.d > 128;
+  auto plain = [&](int z) {
+    return launch_early(wide ? cache8_append_kernel<256, 0, kThreads> : cache8_append_kernel<128, 0, kThreads>, dim3(items, p.c.Hkv, z),
+                        dim3(kThreads), 0, stream, p);
+  };
+  if (p.rope.pairs == 0) return plain(2);
+  Cache8AppendParams r = p;
+  if (static_cast<long long>(items) * p.c.Hkv <= 1216) {
+    // few blocks (a decoding step): K and V of a head together, in one launch
+    r.heads = 1;
+    return wide ? rotating<256, 2, 512>(r, items, stream) : rotating<128, 2, 256>(r, items, stream);
   }
-  return launch_early(p.c.d > 128 ? cache8_append_kernel<256, false, kThreads> : cache8_append_kernel<128, false, kThreads>,
-                      dim3(items, p.c.Hkv, 2), dim3(kThreads), 0, stream, p);
+  // Many: V by the kernel that has nothing else to do, eight CTAs per SM, and K by one whose registers are few enough for
+  // three, four heads to a CTA, for which the angles are computed once. (30011 tokens of 8 heads, d 128: 55 us, with two
+  // heads to a CTA 57, with eight 60; K and V together at two CTAs per SM 64.)
+  const cudaError_t e = plain(1);
+  if (e != cudaSuccess) return e;
+  r.heads = 4;
+  return wide ? rotating<256, 1, 512>(r, items, stream) : rotating<128, 1, 256>(r, items, stream);
 }
 
 }  // namespace fa

@@ -176,7 +176,7 @@ struct Cache8AppendParams {
   const int* table;                // [B, max_blocks]
   int B, T, max_blocks;
   RopePlan rope;                   // pairs = 0: K as it is
-  int k_heads;                     // heads of a CTA that rotates K (set at the launch)
+  int heads;                       // KV heads of a CTA that rotates (set at the launch)
 };
 struct Cache8Params {
   Cache8Pools c;

@@ -47,4 +47,21 @@ __device__ __forceinline__ void rotate(float& a, float& b, float2 cs) {
   a = x;
 }
 
+// The same for two pairs (a0, b0) and (a1, b1), each step rounded as there.
+__device__ __forceinline__ void rotate2(float& a0, float& a1, float& b0, float& b1, float c0, float c1, float s0, float s1) {
+  asm("{\n\t.reg .b64 a, b, c, s, t, u;\n\t"
+      "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tmov.b64 c, {%4, %5};\n\tmov.b64 s, {%6, %7};\n\t"
+      "mul.rn.f32x2 t, b, s;\n\tmul.rn.f32x2 u, b, c;\n\t"
+      "xor.b64 t, t, 0x8000000080000000;\n\t"
+      "fma.rn.f32x2 t, a, c, t;\n\tfma.rn.f32x2 u, a, s, u;\n\t"
+      "mov.b64 {%0, %1}, t;\n\tmov.b64 {%2, %3}, u;\n\t}"
+      : "+f"(a0), "+f"(a1), "+f"(b0), "+f"(b1) : "f"(c0), "f"(c1), "f"(s0), "f"(s1));
+}
+// (a0, a1) *= m
+__device__ __forceinline__ void mul2_bc(float& a0, float& a1, float m) {
+  asm("{\n\t.reg .b64 a, m;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 m, {%2, %2};\n\t"
+      "mul.rn.f32x2 a, a, m;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1) : "f"(m));
+}
+
 }  // namespace fa

@@ -401,7 +401,8 @@ fa_status fa_cache8_append(const void* k, long long k_stride_h, long long k_stri
                            void* stream);
 
 /* fa_cache8_append with K turned by its positions on the way: the scale and the
- * codes are of the rotated values, in fp32, so K is rounded once. positions:
+ * codes are of the rotated values, in fp32, so K is rounded once (a value within
+ * 2^-21 of the middle between two codes may take either). positions:
  * device int32, positions[a * pos_stride_axis + t] for token t of T on axis a; NULL:
  * the position that the token gets in the cache, start[b] + i, on every axis. V as
  * fa_cache8_append takes it. */
@@ -458,7 +459,7 @@ fa_status fa_fwd_cache8(const void* q, const fa_cache8* cache, const int* block_
  * workspace: fa_fwd_cache8_packed_workspace_bytes(B, T, Hq, Hkv, d, max_blocks)
  * bytes (40 MB; 256 says that a table of one or two blocks needs none, NULL will do), 256-byte aligned,
  * contents before and after of no meaning; calls that may overlap on the GPU need
- * one each. 0 for sizes that it refuses. Two launches. Every call gives the same
+ * one each. 0 for sizes that it refuses. Two launches (one where none is needed). Every call gives the same
  * bits. fa_fwd_cache8 is the call for single tokens, and the one that adds up weights. */
 size_t fa_fwd_cache8_packed_workspace_bytes(int B, int T, int Hq, int Hkv, int d, int max_blocks);
 fa_status fa_fwd_cache8_packed(const void* q, long long q_stride_h, long long q_stride_t, const fa_cache8* cache,

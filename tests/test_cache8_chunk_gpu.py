@@ -276,6 +276,26 @@ def test_graph_streams_and_workspaces(fa):
             assert torch.equal(a, want[0]) and torch.equal(b, want[1])
 
 
+def test_the_same_bits_many_times(fa):
+    """Hand-offs under many timings: short items one behind the other, long ones over several CTAs, wide heads, with nothing
+    between the calls."""
+    rng = np.random.default_rng(43)
+    for d, news, past in ((128, [40] * 30 + [300, 1, 1, 1], [0, 90, 200] * 10 + [2500, 5000, 10, 4000]), (64, [700, 33, 1], [3000, 50, 9000]),
+                          (256, [130, 20, 1, 64], [100, 2000, 5000, 0])):
+        lens = [a + b for a, b in zip(news, past)]
+        c, table = make(43 + d, lens, 4, d)
+        g, q = to_gpu(fa, c), bf16(rng, 16, sum(news), d).to(DEV)
+        cu, tb, ln = ints(np.concatenate([[0], np.cumsum(news)])), ints(table), ints(lens)
+        o, lse = fa.fwd_cache8_packed(q, g, cu, tb, ln)
+        bad = torch.zeros((), dtype=torch.int64, device=DEV)
+        for _ in range(150):
+            o2, l2 = fa.fwd_cache8_packed(q, g, cu, tb, ln)
+            bad += (o2 != o).any() | (l2 != lse).any()
+        fa.check_device_status()
+        assert int(bad) == 0
+        check(c, q, table, news, lens, True, d ** -0.5, o, lse, rows=2)
+
+
 def test_stall_is_reported(fa):
     news, lens = [30], [700]
     c, table = make(41, lens, 1, 128)
