@@ -698,15 +698,16 @@ fa_status cache8_rows(int B, int Hq, int Hkv, int Nq, int d, int max_blocks) {
   return FA_OK;
 }
 
-// Bytes of fa_fwd_cache8_packed's workspace: two partial results per CTA and their statistics (off_s).
+// Bytes of fa_fwd_cache8_packed's workspace: two partial results per CTA, their statistics (off_s) and what is to be
+// joined (off_j).
 struct ChunkWorkspace {
-  size_t off_s, total;
+  size_t off_s, off_j, total;
 };
 ChunkWorkspace chunk_workspace(int d, int max_blocks) {
-  if (max_blocks <= 2) return {0, kNoWorkspace};       // one key tile: nothing is split
+  if (max_blocks <= 2) return {0, 0, kNoWorkspace};    // one key tile: nothing is split
   const size_t D = d <= 128 ? 128 : 256, rows = 2 * static_cast<size_t>(fa::kCache8Sms) * fa::chunk_rows(d);
-  const size_t off = align256(rows * D * 4);
-  return {off, off + align256(rows * 3 * 4)};
+  const size_t off_s = align256(rows * D * 4), off_j = off_s + align256(rows * 3 * 4);
+  return {off_s, off_j, off_j + align256(fa::kCache8Sms * 8 * 4)};
 }
 fa_status chunk_sizes(int B, int T, int Hq, int Hkv, int d, int max_blocks) {
   if (B < 1 || B > 65535 || T < 1 || Hq < 1 || Hkv < 1 || Hkv > 65535 || Hq % Hkv != 0 || d < 1 || max_blocks < 1 ||
@@ -923,8 +924,9 @@ fa_status fa_fwd_cache8_packed(const void* q, long long q_stride_h, long long q_
   p.status = status;
   p.timeout_ns = wait_limit_ns();
   p.test_stall = test_stall();
-  p.part_o = static_cast<float*>(workspace);
+  p.part_o = static_cast<float*>(workspace);               // (offsets into nothing where none is needed: never read)
   p.part_s = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.off_s);
+  p.joins = w.total > kNoWorkspace ? reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + w.off_j) : nullptr;
   CUtensorMap mk, mv;
   const long long rows = static_cast<long long>(p.c.num_blocks) * p.c.Hkv;
   if (!make_map(&mk, p.c.k, 1, p.c.d, FA_CACHE8_BLOCK, rows, 64) || !make_map(&mv, p.c.v, 1, p.c.d, FA_CACHE8_BLOCK, rows, 64))

@@ -1090,6 +1090,21 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       place.find(p, line.turn, u, lane);
     }
     Walk walk(p, place, line.turn, length);
+    if (p.joins != nullptr) {
+      // for the second kernel: the item that this part is the second one of
+      int c0 = 0, c1 = -1, slot = 0;
+      if (length > 0 && place.off > line.turn) {
+        c0 = line.part_of(place.start + line.turn);
+        if (c0 == static_cast<int>(blockIdx.x) - 1)
+          c1 = line.part_of(place.start + line.turn + walk.s.tiles(p, walk.s.end_of(p, place.item)) - 1);
+        slot = line.begin(c0) >= place.start ? 0 : 1;      // the item is that part's first or not
+      }
+      if (lane == 0) {
+        int4* const join = reinterpret_cast<int4*>(p.joins) + 2 * blockIdx.x;
+        join[0] = make_int4(c0, c1, slot, place.h);
+        join[1] = make_int4(walk.s.row0, walk.s.n, place.item * p.span, 0);
+      }
+    }
     Segment s;
     for (int n = 0; ok; ++n) {
       const bool more = walk.next<kGroups>(p, s);
@@ -1138,49 +1153,23 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 }
 
 // ------------------------------------------------------------------ second kernel
-// Joins the items whose key tiles went to several parts: CTA (i, rows) those whose second part is i.
+// Joins the items whose key tiles went to several parts: CTA (i, rows) the one whose second part is i + 1, by what that part's
+// scheduler wrote down.
 constexpr int kJoinRows = 32;
 constexpr int kJoinThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) cache8_chunk_join_kernel(const ChunkParams p) {
   using C = Cfg<D>;
-  __shared__ int shared[8];
-  const int lane = threadIdx.x & 31, i = blockIdx.x + 1;
-  if (threadIdx.x < 32) {
-    const Line line(p, lane);
-    int c0 = 0, c1 = -1, second = 0;
-    int b = 0, h = 0, item = 0;
-    if (i < line.parts) {
-      Place place;
-      place.find(p, line.turn, line.begin(i), lane);
-      if (place.off > line.turn) {
-        const Sequence s(p, place.b);
-        c0 = line.part_of(place.start + line.turn);
-        c1 = c0 == i - 1 ? line.part_of(place.start + line.turn + s.tiles(p, s.end_of(p, place.item)) - 1) : -1;
-        second = line.begin(c0) >= place.start ? 0 : 1;    // the item is that part's first or not
-        b = place.b;
-        h = place.h;
-        item = place.item;
-      }
-    }
-    if (lane == 0) {
-      shared[0] = c0;
-      shared[1] = c1;
-      shared[2] = second;
-      shared[3] = b;
-      shared[4] = h;
-      shared[5] = item;
-    }
-  }
-  __syncthreads();
-  const int c0 = shared[0], c1 = shared[1];
+  const int4* const join = reinterpret_cast<const int4*>(p.joins) + 2 * (blockIdx.x + 1);
+  const int4 parts = join[0], at = join[1];                // (c0, c1, first slot, head), (row0, new tokens, first token)
+  const int c0 = parts.x, c1 = parts.y;
   if (c1 < c0) return;
-  const Sequence s(p, shared[3]);
+  const int lane = threadIdx.x & 31;
   const int r = blockIdx.y * kJoinRows + lane;             // row of the item
   const int group = r >> 7, tok = (r & 127) / p.G;
-  const int token = shared[5] * p.span + group * p.tt + tok;
-  if (tok >= p.tt || token >= s.n) return;
-  auto slot = [&](int c) { return 2LL * c + (c == c0 ? shared[2] : 0); };
+  const int token = at.z + group * p.tt + tok;
+  if (tok >= p.tt || token >= at.y) return;
+  auto slot = [&](int c) { return 2LL * c + (c == c0 ? parts.z : 0); };
   float ml = -INFINITY, mo = -INFINITY;
   for (int c = c0; c <= c1; ++c) {
     const float* const st = p.part_s + slot(c) * C::kRows * 3 + r;
@@ -1215,11 +1204,11 @@ __global__ void __launch_bounds__(kJoinThreads) cache8_chunk_join_kernel(const C
         }
     }
   }
-  const int head = shared[4] * p.G + ((r & 127) - tok * p.G);
-  const long long at = static_cast<long long>(s.row0) + token;
+  const int head = parts.w * p.G + ((r & 127) - tok * p.G);
+  const long long at_row = static_cast<long long>(at.x) + token;
   const float factor = l == 0.f ? 0.f : ex2_approx(mo - ml) / l;
-  if (threadIdx.x < 32) p.lse[static_cast<long long>(head) * p.T + at] = l == 0.f ? -INFINITY : (ml + log2f(l)) * kLn2;
-  __nv_bfloat16* const dst = p.o + head * p.o_sh + at * p.o_st;
+  if (threadIdx.x < 32) p.lse[static_cast<long long>(head) * p.T + at_row] = l == 0.f ? -INFINITY : (ml + log2f(l)) * kLn2;
+  __nv_bfloat16* const dst = p.o + head * p.o_sh + at_row * p.o_st;
 #pragma unroll
   for (int x = 0; x < kWide; ++x) {
     const int col = 8 * ((threadIdx.x >> 5) + x * (kJoinThreads / 32));

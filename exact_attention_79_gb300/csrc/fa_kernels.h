@@ -219,6 +219,7 @@ struct ChunkParams {
   int test_stall;                  // 1: the issuer first waits on a barrier nothing arrives on (timeout test)
   float* part_o;                   // partial results: [2 ctas][D / 4][rows of an item][4] and [2 ctas][3][rows]
   float* part_s;
+  int* joins;                      // [ctas][8] which item a part is the second one of; nullptr: nothing is split
 };
 struct Cache8EvictParams {
   Cache8Pools c;

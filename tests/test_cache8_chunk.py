@@ -42,9 +42,9 @@ def test_c_refusals(lib):
 
 def test_workspace_bytes(lib):
     f = lib.fa_fwd_cache8_packed_workspace_bytes
-    # two partial results per CTA (152): rows of an item x D floats, and three statistics per row
-    assert f(2, 100, 8, 2, 64, 8) == 2 * 152 * 256 * (128 + 3) * 4
-    assert f(2, 100, 8, 2, 256, 8) == 2 * 152 * 128 * (256 + 3) * 4
+    # two partial results per CTA (152): rows of an item x D floats, three statistics per row, and eight ints per CTA
+    assert f(2, 100, 8, 2, 64, 8) == 2 * 152 * 256 * (128 + 3) * 4 + 152 * 8 * 4
+    assert f(2, 100, 8, 2, 256, 8) == 2 * 152 * 128 * (256 + 3) * 4 + 152 * 8 * 4
     assert f(2, 100, 8, 2, 64, 2) == 256
     for bad in ((0, 100, 8, 2, 64, 8), (2, 0, 8, 2, 64, 8), (2, 100, 7, 2, 64, 8), (2, 100, 8, 2, 72, 8), (2, 100, 258, 2, 64, 8), (2, 100, 8, 2, 64, 0)):
         assert f(*bad) == 0, bad
