@@ -408,7 +408,68 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     if (lane == 0) mbar_arrive(bar_item_empty(n % kItems));
   };
 
-  if (warp < 4 * kGroups) {
+  if (warp == 11) {
+    // ------------------------------------------------------------ scheduler
+    // Finds this part's segments ahead of time: one warp's look-up instead of all roles', whose code for it would come
+    // from memory at every change. And brings the segment's rows of Q into L2.
+    setmaxnreg_dec<C::kRegsOther>();
+    const Line line(p, lane);
+    bool ok = true;
+    long long u = 0, length = 0;
+    Place place;
+    if (static_cast<int>(blockIdx.x) < line.parts) {
+      u = line.begin(blockIdx.x);
+      length = line.begin(blockIdx.x + 1) - u;
+      place.find(p, line.turn, u, lane);
+    }
+    Walk walk(p, place, line.turn, length);
+    if (p.joins != nullptr) {
+      // for the second kernel: the item that this part is the second one of
+      int c0 = 0, c1 = -1, slot = 0;
+      if (length > 0 && place.off > line.turn) {
+        c0 = line.part_of(place.start + line.turn);
+        if (c0 == static_cast<int>(blockIdx.x) - 1)
+          c1 = line.part_of(place.start + line.turn + walk.s.tiles(p, walk.s.end_of(p, place.item)) - 1);
+        slot = line.begin(c0) >= place.start ? 0 : 1;      // the item is that part's first or not
+      }
+      if (lane == 0) {
+        int4* const join = reinterpret_cast<int4*>(p.joins) + 2 * blockIdx.x;
+        join[0] = make_int4(c0, c1, slot, place.h);
+        join[1] = make_int4(walk.s.row0, walk.s.n, place.item * p.span, 0);
+      }
+    }
+    Segment s;
+    for (int n = 0; ok; ++n) {
+      const bool more = walk.next<kGroups>(p, s);
+      if (n >= kItems) ok = wait(bar_item_empty(n % kItems), ((n / kItems) & 1) ^ 1, abort_flag, p.timeout_ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) {
+        volatile int* const m = items + (n % kItems) * kItemInts;
+        m[kB] = s.b;
+        m[kH] = s.h;
+        m[kRow0] = s.row0;
+        m[kNew] = s.n;
+        m[kLen] = s.len;
+        m[kTok0] = s.tok0;
+        m[kT0] = s.t0;
+        m[kN] = more ? s.t1 - s.t0 : 0;
+        m[kN0] = s.n0;
+        m[kSplit] = s.split;
+        m[kWhole] = s.t0 == 0 && s.t1 == s.tiles;
+        mbar_arrive(bar_item_full(n % kItems));
+      }
+      __syncwarp();
+      if (!more) break;
+      for (int r = lane; r < (s.split ? 128 : C::kRows); r += 32) {
+        const int row = r & 127, tok = row / p.G, token = s.tok0 + (r >> 7) * p.tt + tok;
+        if (tok >= p.tt || token >= s.n) continue;
+        const __nv_bfloat16* const src =
+            p.q + (s.h * p.G + (row - tok * p.G)) * p.q_sh + (static_cast<long long>(s.row0) + token) * p.q_st;
+        for (int c = 0; c < p.c.d; c += 64) asm volatile("prefetch.global.L2 [%0];" :: "l"(src + c));
+      }
+    }
+    __syncwarp();
+  } else if (warp < 4 * kGroups) {
     // ------------------------------------------------------------ softmax groups
     setmaxnreg_inc<C::kRegsSoftmax>();
     const int g = warp >> 2;
@@ -788,7 +849,7 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       else segments(std::integral_constant<int, most - 2>());
     }
     __syncwarp();
-  } else if (warp >= 12 || warp < 8) {
+  } else if (warp >= 12 || (kGroups == 1 && warp >= 4 && warp < 8)) {
     // ------------------------------------------------------------ converters
     setmaxnreg_dec<C::kRegsOther>();
     const int cw = warp >= 12 ? warp - 12 : warp;          // (with one group warps 4-7 are the converters 4-7)
@@ -1073,67 +1134,6 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       }
       if (lane == 0 && ok) load_v(tile - 1, va, vb);
       ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
-    }
-    __syncwarp();
-  } else if (warp == 11) {
-    // ------------------------------------------------------------ scheduler
-    // Finds this part's segments ahead of time: one warp's look-up instead of all roles', whose code for it would come
-    // from memory at every change. And brings the segment's rows of Q into L2.
-    setmaxnreg_dec<C::kRegsOther>();
-    const Line line(p, lane);
-    bool ok = true;
-    long long u = 0, length = 0;
-    Place place;
-    if (static_cast<int>(blockIdx.x) < line.parts) {
-      u = line.begin(blockIdx.x);
-      length = line.begin(blockIdx.x + 1) - u;
-      place.find(p, line.turn, u, lane);
-    }
-    Walk walk(p, place, line.turn, length);
-    if (p.joins != nullptr) {
-      // for the second kernel: the item that this part is the second one of
-      int c0 = 0, c1 = -1, slot = 0;
-      if (length > 0 && place.off > line.turn) {
-        c0 = line.part_of(place.start + line.turn);
-        if (c0 == static_cast<int>(blockIdx.x) - 1)
-          c1 = line.part_of(place.start + line.turn + walk.s.tiles(p, walk.s.end_of(p, place.item)) - 1);
-        slot = line.begin(c0) >= place.start ? 0 : 1;      // the item is that part's first or not
-      }
-      if (lane == 0) {
-        int4* const join = reinterpret_cast<int4*>(p.joins) + 2 * blockIdx.x;
-        join[0] = make_int4(c0, c1, slot, place.h);
-        join[1] = make_int4(walk.s.row0, walk.s.n, place.item * p.span, 0);
-      }
-    }
-    Segment s;
-    for (int n = 0; ok; ++n) {
-      const bool more = walk.next<kGroups>(p, s);
-      if (n >= kItems) ok = wait(bar_item_empty(n % kItems), ((n / kItems) & 1) ^ 1, abort_flag, p.timeout_ns);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      if (lane == 0) {
-        volatile int* const m = items + (n % kItems) * kItemInts;
-        m[kB] = s.b;
-        m[kH] = s.h;
-        m[kRow0] = s.row0;
-        m[kNew] = s.n;
-        m[kLen] = s.len;
-        m[kTok0] = s.tok0;
-        m[kT0] = s.t0;
-        m[kN] = more ? s.t1 - s.t0 : 0;
-        m[kN0] = s.n0;
-        m[kSplit] = s.split;
-        m[kWhole] = s.t0 == 0 && s.t1 == s.tiles;
-        mbar_arrive(bar_item_full(n % kItems));
-      }
-      __syncwarp();
-      if (!more) break;
-      for (int r = lane; r < (s.split ? 128 : C::kRows); r += 32) {
-        const int row = r & 127, tok = row / p.G, token = s.tok0 + (r >> 7) * p.tt + tok;
-        if (tok >= p.tt || token >= s.n) continue;
-        const __nv_bfloat16* const src =
-            p.q + (s.h * p.G + (row - tok * p.G)) * p.q_sh + (static_cast<long long>(s.row0) + token) * p.q_st;
-        for (int c = 0; c < p.c.d; c += 64) asm volatile("prefetch.global.L2 [%0];" :: "l"(src + c));
-      }
     }
     __syncwarp();
   } else {

@@ -13,7 +13,7 @@
 //
 // With rotation K's pairs of columns are turned by their positions on the way, in fp32, and the block's scale is that of the
 // rotated values, so K is rounded once. The angles are the same for all heads of a token: a CTA computes them once for
-// several. Issue-bound then (about 14 instructions per value of K).
+// several. K's kernel then has half of the issue slots busy (about 20 instructions per value) and 2.1 waves of CTAs.
 #include "fa_cache8.cuh"
 #include "fa_rope.cuh"
 
@@ -79,36 +79,38 @@ struct NewTokens {
 // four pairs (eight columns) of up to kUnits tokens; their cosines and sines are computed once, kept in shared
 // memory where it has only this thread's, and serve all its heads. The rotated values stay in fp32 until they are codes. The
 // next head's loads are under way meanwhile.
-template <int D, int N, bool kBoth>
+template <int D, int N, bool kBoth, bool kApart>
 __device__ __forceinline__ void append_rotated(const Cache8AppendParams& p, const NewTokens& n, int h0, int h1, float2 (*warp_max)[N / 32], float4* table) {
   constexpr int kUnits = kCacheBlock * D / 8 / N;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int upt = p.c.d / 8, slots = N / upt;               // units of a token, tokens at a time
   const int slot = tid / upt, c = tid - slot * upt;
   const bool turned = 4 * c < p.rope.pairs;
-  const bool apart = turned && !p.rope.interleaved;
-  const int ca = apart ? 4 * c : 8 * c, cb = apart ? ca + p.rope.pairs : ca + 4;
+  // kApart: a pair's columns lie p.rope.pairs apart; otherwise, and behind the pairs, the thread's eight side by side
+  const int ca = kApart && turned ? 4 * c : 8 * c, cb = kApart && turned ? ca + p.rope.pairs : ca + 4;
   const int count = n.hi - n.lo;
   auto row_of = [&](int i) { return slot + i * slots; };
   auto mine = [&](int i) { return slot < slots && row_of(i) < count; };
   uint2 raw[kUnits][2];
   uint4 raw_v[kBoth ? kUnits : 1];
-  auto load = [&](int h) {
-    const __nv_bfloat16* const x = static_cast<const __nv_bfloat16*>(p.k) + h * p.k_sh;
-    const __nv_bfloat16* const y = static_cast<const __nv_bfloat16*>(p.v) + h * p.v_sh;
+  const __nv_bfloat16* next_k = static_cast<const __nv_bfloat16*>(p.k) + h0 * p.k_sh + static_cast<long long>(n.tok0 + slot) * p.k_st;
+  const __nv_bfloat16* next_v = static_cast<const __nv_bfloat16*>(p.v) + h0 * p.v_sh + static_cast<long long>(n.tok0 + slot) * p.v_st + 8 * c;
+  const long long step_k = slots * p.k_st, step_v = slots * p.v_st;
+  auto load = [&]() {                                        // the next head's
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       raw[i][0] = raw[i][1] = make_uint2(0, 0);
       if (kBoth) raw_v[kBoth ? i : 0] = make_uint4(0, 0, 0, 0);
       if (mine(i)) {
-        const __nv_bfloat16* const row = x + (n.tok0 + row_of(i)) * p.k_st;
-        raw[i][0] = *reinterpret_cast<const uint2*>(row + ca);
-        raw[i][1] = *reinterpret_cast<const uint2*>(row + cb);
-        if (kBoth) raw_v[kBoth ? i : 0] = *reinterpret_cast<const uint4*>(y + (n.tok0 + row_of(i)) * p.v_st + 8 * c);
+        raw[i][0] = *reinterpret_cast<const uint2*>(next_k + i * step_k + ca);
+        raw[i][1] = *reinterpret_cast<const uint2*>(next_k + i * step_k + cb);
+        if (kBoth) raw_v[kBoth ? i : 0] = *reinterpret_cast<const uint4*>(next_v + i * step_v);
       }
     }
+    next_k += p.k_sh;
+    next_v += p.v_sh;
   };
-  load(h0);
+  load();
   unsigned long long turns[4] = {0, 0, 0, 0};
   const int* at[4] = {nullptr, nullptr, nullptr, nullptr};
   if (turned) {
@@ -147,7 +149,7 @@ __device__ __forceinline__ void append_rotated(const Cache8AppendParams& p, cons
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float lower = __uint_as_float(w[e] << 16), upper = __uint_as_float(w[e] & 0xFFFF0000u);
-        if (apart) {
+        if (kApart) {
           (e < 2 ? fa : fb)[i][2 * (e & 1)] = lower;
           (e < 2 ? fa : fb)[i][2 * (e & 1) + 1] = upper;
         } else {
@@ -182,7 +184,7 @@ __device__ __forceinline__ void append_rotated(const Cache8AppendParams& p, cons
       top = 0;
       for (int i = 0; i < (kBoth ? kUnits : 0); ++i) top = finite_max(finite_max(finite_max(finite_max(top, v[i].x), v[i].y), v[i].z), v[i].w);
     }
-    if (h + 1 < h1) load(h + 1);
+    if (h + 1 < h1) load();
     // (non-negative floats order like their bits)
     amax.x = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax.x)));
     if (kBoth) amax.y = __uint_as_float(__reduce_max_sync(0xffffffffu, top << 16));
@@ -205,9 +207,10 @@ __device__ __forceinline__ void append_rotated(const Cache8AppendParams& p, cons
       p.c.k_scale[ph] = now;
       if (kBoth) p.c.v_scale[ph] = now_v;
     }
-    // powers of two, as all made here are: 1 / now is exact
-    const bool power = (__float_as_uint(now) & 0x7FFFFFu) == 0, power_v = (__float_as_uint(now_v) & 0x7FFFFFu) == 0;
-    const float inv = __fdiv_rn(1.f, now), inv_v = __fdiv_rn(1.f, now_v);
+    // powers of two, as all made here are (2^126 at most): 1 / now is exact, and its exponent the other's opposite
+    auto is_power = [](float s) { return (__float_as_uint(s) & 0x7FFFFFu) == 0 && s < 1.7014118e38f; };
+    const bool power = is_power(now), power_v = is_power(now_v);
+    const float inv = __uint_as_float(0x7F000000u - __float_as_uint(now)), inv_v = __uint_as_float(0x7F000000u - __float_as_uint(now_v));
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       if (!mine(i)) continue;
@@ -226,7 +229,7 @@ __device__ __forceinline__ void append_rotated(const Cache8AppendParams& p, cons
       }
       const int at = (n.lo + row_of(i)) * p.c.d;
       uint32_t first, second;
-      if (apart) {
+      if (kApart) {
         first = pack_e4m3x2(fa[i][0], fa[i][1]) | pack_e4m3x2(fa[i][2], fa[i][3]) << 16;
         second = pack_e4m3x2(fb[i][0], fb[i][1]) | pack_e4m3x2(fb[i][2], fb[i][3]) << 16;
       } else {
@@ -242,9 +245,10 @@ __device__ __forceinline__ void append_rotated(const Cache8AppendParams& p, cons
 }
 
 // D: 128 or 256, d at most that. kRotate 0: one CTA of kThreads per (touched block, KV head, K or V; V alone where K is
-// rotated). 1: K rotated, one CTA of N threads per block and `heads` KV heads. 2: V too, as it is.
+// rotated). 1: K rotated, one CTA of N threads per block and `heads` KV heads. 2: V too, as it is. 5 and 6: the same for pairs
+// side by side.
 template <int D, int kRotate, int N>
-__global__ void __launch_bounds__(N, kRotate == 1 ? (D == 128 ? 3 : 1) : kRotate ? 512 / N : D == 128 ? 8 : 4) cache8_append_kernel(const Cache8AppendParams p) {
+__global__ void __launch_bounds__(N, kRotate == 0 ? (D == 128 ? 8 : 4) : (kRotate & 1) && D == 128 ? 3 : 512 / N) cache8_append_kernel(const Cache8AppendParams p) {
   constexpr int kThreads = N;
   constexpr int kMaxChunks = kCacheBlock * D / 8 / kThreads;   // 16-byte chunks of one block per thread
   __shared__ float warp_max[kThreads / 32];
@@ -292,7 +296,7 @@ __global__ void __launch_bounds__(N, kRotate == 1 ? (D == 128 ? 3 : 1) : kRotate
     const int h0 = static_cast<int>(blockIdx.y) * p.heads;
     const NewTokens n{lo, hi, tok0, blk * kCacheBlock + lo, p.table[static_cast<long long>(b) * p.max_blocks + blk]};
     extern __shared__ float4 table[];
-    append_rotated<D, N, kRotate == 2>(p, n, h0, min(h0 + p.heads, p.c.Hkv), maxima, table);
+    append_rotated<D, N, (kRotate & 2) != 0, kRotate < 4>(p, n, h0, min(h0 + p.heads, p.c.Hkv), maxima, table);
     return;
   }
   const int h = blockIdx.y, which = p.rope.pairs > 0 ? 1 : blockIdx.z;
@@ -364,7 +368,7 @@ __global__ void __launch_bounds__(N, kRotate == 1 ? (D == 128 ? 3 : 1) : kRotate
 }  // namespace
 
 template <int D, int kRotate, int N>
-static cudaError_t rotating(const Cache8AppendParams& p, unsigned items, cudaStream_t stream) {
+static cudaError_t rotate_as(const Cache8AppendParams& p, unsigned items, cudaStream_t stream) {
   constexpr int kTable = 2 * ((kCacheBlock * D / 8 + N - 1) / N) * N * static_cast<int>(sizeof(float4));
   static PerDeviceOnce attr;
   const cudaError_t e = attr.run([] {
@@ -372,6 +376,12 @@ static cudaError_t rotating(const Cache8AppendParams& p, unsigned items, cudaStr
   });
   if (e != cudaSuccess) return e;
   return launch_early(cache8_append_kernel<D, kRotate, N>, dim3(items, (p.c.Hkv + p.heads - 1) / p.heads), dim3(N), kTable, stream, p);
+}
+
+// kRotate 1 or 2
+template <int D, int kRotate, int N>
+static cudaError_t rotating(const Cache8AppendParams& p, unsigned items, cudaStream_t stream) {
+  return p.rope.interleaved ? rotate_as<D, kRotate + 4, N>(p, items, stream) : rotate_as<D, kRotate, N>(p, items, stream);
 }
 
 cudaError_t launch_cache8_append(const Cache8AppendParams& p, cudaStream_t stream) {
@@ -391,8 +401,8 @@ cudaError_t launch_cache8_append(const Cache8AppendParams& p, cudaStream_t strea
     return wide ? rotating<256, 2, 512>(r, items, stream) : rotating<128, 2, 256>(r, items, stream);
   }
   // Many: V by the kernel that has nothing else to do, eight CTAs per SM, and K by one whose registers are few enough for
-  // three, four heads to a CTA, for which the angles are computed once. (30011 tokens of 8 heads, d 128: 55 us, with two
-  // heads to a CTA 57, with eight 60; K and V together at two CTAs per SM 64.)
+  // three, four heads to a CTA, for which the angles are computed once. (30011 tokens of 8 heads, d 128: 49 us, with two
+  // heads to a CTA 51, with eight 53; K and V together at two CTAs per SM 64.)
   const cudaError_t e = plain(1);
   if (e != cudaSuccess) return e;
   r.heads = 4;
