@@ -17,7 +17,7 @@
 // P' within 2^-11 of itself or 2^-31 of the row's largest. O's error against 64 bits is then its own rounding to bf16.
 // (P in two e4m3 terms would save V's conversion but is 2^-8, and three cost half as much again.)
 //
-// K goes from memory into the product untouched (TMA). V passes through four converting
+// K goes from memory into the product untouched (TMA). V passes through converting
 // warps: 16 codes a thread at a time from the landing buffer to the MN-major f16 tile; they
 // clear keys that are not there (P is 0, but 0 x NaN is not) and also lay out Q.
 //
@@ -27,8 +27,14 @@
 // gives its even key tiles to one softmax group and its odd ones to the other, joined in TMEM.
 //
 // Warps: 0-3 and 4-7 the softmax groups (one thread per row), 8 producer (block table, scales,
-// TMA), 9 tensor-core issuer, 10 ring watcher, 11 scheduler, 12-15 converters. At d > 128 (kGroups = 1) O takes half of TMEM, S is
-// double-buffered and warps 4-7 rest.
+// TMA), 9 tensor-core issuer, 10 ring watcher, 11 scheduler, 12-15 converters. At d > 128 (kGroups = 1) O takes half of
+// TMEM, S is double-buffered, warps 4-7 convert too and there is no watcher. The loops of all roles are about 20 KB of
+// code, more than the instruction cache holds: each line that has gone costs some 230 cycles, and the order of
+// the roles below is the best of ten (4096 tokens at the end of 32768, 32 heads on 8, d 128: 1434 to 1812 us).
+//
+// What bounds it. There (1.44 PFLOP/s, 75% of the bf16 rate) a step of two row tiles takes 3300 cycles, 2100 of them products:
+// each group's S, softmax (1600), P V and the hand-offs between follow one another, and two groups do not cover it all. At
+// d 64 a step takes 2900. A change of items costs some 15000 (Q's terms, the diagonal's mask, O's way out).
 #include <type_traits>
 
 #include "fa_cache8.cuh"
@@ -587,7 +593,6 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #pragma unroll
           for (int c0 = 0; c0 < D; c0 += 32) {
             if (c0 >= p.c.d) continue;
-
             uint32_t o[32];
             tmem_ld_32x32b_x32(t_o + c0, o);
             tmem_wait_ld();
