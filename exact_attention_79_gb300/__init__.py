@@ -350,18 +350,22 @@ def _rope_specs(rope, axes):
     return specs, _Rope(turns.data_ptr(), None if axis is None else axis.data_ptr(), pairs, axes, 1 if interleaved else 0)
 
 
-def _rope_strides(x, name, shape, dtype):
+def _rope_strides(x, name, shape, dtype, unit):
     """Batch, head and token strides of a [B, H, T, d] (or [H, T, d]) tensor whose rows of d values are contiguous and
-    16-byte aligned. A dimension of size 1 gets a stride that nothing reads through."""
+    16-byte (`unit` values) aligned. A dimension of size 1 gets a stride that nothing reads through."""
     if x.dtype is not dtype or x.shape != shape:
         raise ValueError(f"{name}: expected {dtype} of shape {tuple(shape)}, got {x.dtype} of shape {tuple(x.shape)}")
+    if len(shape) == 4:
+        sb, sh, st, sd = x.stride()
+    else:
+        sb, (sh, st, sd) = 0, x.stride()
+    if sd == 1 and not (sb | sh | st) & (unit - 1):
+        return sb, sh, st
     *outer, H, T, d = shape
-    *sb, sh, st, sd = x.stride()
-    sb = sb[0] if outer and outer[0] > 1 else 0
+    sb = sb if outer and outer[0] > 1 else 0
     sh, st = (sh if H > 1 else d), (st if T > 1 else d)
     if sd != 1 and d > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    unit = 16 // dtype.itemsize
     if sb % unit or sh % unit or st % unit:
         raise ValueError(f"{name}: strides other than the last must be multiples of {unit}")
     return sb, sh, st
@@ -399,29 +403,36 @@ def rope(q, k, rope, positions, inverse=False, q_out=None, k_out=None):
     import torch
     shape, dtype, dev = q.shape, q.dtype, q.device
     batched = len(shape) == 4
-    if not batched and len(shape) != 3:
+    if batched:
+        B, Hq, T, d = shape
+    elif len(shape) == 3:
+        B, (Hq, T, d) = 1, shape
+    else:
         raise ValueError("q must be [B, H, T, d] or [H, T, d]")
-    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+    if dtype is torch.bfloat16:
+        size, unit = 2, 8
+    elif dtype is torch.float32:
+        size, unit = 4, 4
+    else:
         raise ValueError("q and k must be bf16 or fp32")
-    B, (Hq, T, d) = shape[0] if batched else 1, shape[-3:]
     axes, sa, sb = _rope_positions(positions, B, T, batched, rope.axis is None)
     specs, plan = _rope_specs(rope, axes)
     placed = [(positions, "positions")]
-    qs = _rope_strides(q, "q", shape, dtype)
-    q_os, ks, k_os = qs, (0, 0, 0), (0, 0, 0)
+    q_os = qs = _rope_strides(q, "q", shape, dtype, unit)
     if q_out is not None:
-        q_os = _rope_strides(q_out, "q_out", shape, dtype)
+        q_os = _rope_strides(q_out, "q_out", shape, dtype, unit)
         placed.append((q_out, "q_out"))
-    Hkv = 0
     if k is not None:
-        if len(k.shape) != len(shape):
+        k_shape = k.shape
+        if len(k_shape) != len(shape):
             raise ValueError("k must have as many dimensions as q")
-        Hkv = k.shape[-3]
-        k_shape = (B, Hkv, T, d) if batched else (Hkv, T, d)
-        ks = k_os = _rope_strides(k, "k", k_shape, dtype)
+        Hkv = k_shape[-3]
+        if k_shape[-1] != d or k_shape[-2] != T or k_shape[0] != (B if batched else Hkv):
+            raise ValueError(f"k: expected {(B, Hkv, T, d) if batched else (Hkv, T, d)}, got {tuple(k_shape)}")
+        k_os = ks = _rope_strides(k, "k", k_shape, dtype, unit)
         placed.append((k, "k"))
         if k_out is not None:
-            k_os = _rope_strides(k_out, "k_out", k_shape, dtype)
+            k_os = _rope_strides(k_out, "k_out", k_shape, dtype, unit)
             placed.append((k_out, "k_out"))
     elif k_out is not None:
         raise ValueError("k_out without k")
@@ -429,16 +440,16 @@ def rope(q, k, rope, positions, inverse=False, q_out=None, k_out=None):
     _placed(dev, *placed)
     if q_out is None:
         q_out = torch.empty_like(q)
-        if q_out.stride() != q.stride():                # (a cut out of something wider is laid out anew)
-            q_os = _rope_strides(q_out, "q_out", shape, dtype)
+        if q_out.stride() != q.stride():                # (what is cut out of something wider is laid out anew)
+            q_os = _rope_strides(q_out, "q_out", shape, dtype, unit)
     if k is not None and k_out is None:
         k_out = torch.empty_like(k)
         if k_out.stride() != k.stride():
-            k_os = _rope_strides(k_out, "k_out", k_shape, dtype)
+            k_os = _rope_strides(k_out, "k_out", k_shape, dtype, unit)
     if T == 0 or B == 0:
         return q_out, k_out
-    _call_on(dev, "fa_rope", q.data_ptr(), *qs, q_out.data_ptr(), *q_os, Hq, None if k is None else k.data_ptr(), *ks,
-             None if k is None else k_out.data_ptr(), *k_os, Hkv, B, T, d, dtype.itemsize, ctypes.byref(plan),
+    k_args = (None, 0, 0, 0, None, 0, 0, 0, 0) if k is None else (k.data_ptr(), *ks, k_out.data_ptr(), *k_os, Hkv)
+    _call_on(dev, "fa_rope", q.data_ptr(), *qs, q_out.data_ptr(), *q_os, Hq, *k_args, B, T, d, size, ctypes.byref(plan),
              positions.data_ptr(), sa, sb, 1 if inverse else 0)
     return q_out, k_out
 
@@ -671,8 +682,9 @@ def fwd_cache8_packed(q, cache, cu_seqlens, block_table, lengths, causal=True, s
     qs = _heads_strides(q, "q", Hq, T, d)
     i32 = torch.int32
     specs += [_table_spec(block_table), (cu_seqlens, "cu_seqlens", i32, (B + 1,)), (lengths, "lengths", i32, (B,))]
+    os = qs
     if out is not None:
-        _heads_strides(out, "out", Hq, T, d)
+        os = _heads_strides(out, "out", Hq, T, d)
     if lse is not None:
         specs.append((lse, "lse", torch.float32, (Hq, T)))
     if workspace is not None:
@@ -682,6 +694,8 @@ def fwd_cache8_packed(q, cache, cu_seqlens, block_table, lengths, causal=True, s
         _placed(dev, (out, "out"))
     else:
         out = torch.empty_like(q)
+        if out.stride() != q.stride():                  # (what is cut out of something wider is laid out anew)
+            os = _heads_strides(out, "out", Hq, T, d)
     if lse is None:
         lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
     if T == 0 or B == 0:
@@ -691,7 +705,7 @@ def fwd_cache8_packed(q, cache, cu_seqlens, block_table, lengths, causal=True, s
     if workspace is None and n > 256:                   # 256: none is needed
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
     _call_on(dev, "fa_fwd_cache8_packed", q.data_ptr(), *qs, ctypes.byref(c), block_table.data_ptr(), max_blocks,
-             cu_seqlens.data_ptr(), lengths.data_ptr(), out.data_ptr(), *_heads_strides(out, "out", Hq, T, d), lse.data_ptr(),
+             cu_seqlens.data_ptr(), lengths.data_ptr(), out.data_ptr(), *os, lse.data_ptr(),
              None if workspace is None else workspace.data_ptr(), n, B, T, Hq, int(bool(causal)), float(scale))
     return out, lse
 
