@@ -920,7 +920,9 @@ fa_status fa_fwd_cache8_packed(const void* q, long long q_stride_h, long long q_
   p.tt = 128 / p.G;
   p.causal = causal ? 1 : 0;
   p.ctas = num_sms < fa::kCache8Sms ? num_sms : fa::kCache8Sms;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  int power = 0;
+  p.scale_digits = 2.f * std::frexp(scale * 1.4426950408889634f, &power);
+  p.scale_power = std::ldexp(1.f, power - 1);
   p.status = status;
   p.timeout_ns = wait_limit_ns();
   p.test_stall = test_stall();

@@ -332,7 +332,7 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   auto s_half = [&](int i) { return base + C::kOffHalf + i * C::kHalfV; };
   float* const row_scale = reinterpret_cast<float*>(gbase + C::kOffStat);           // [kRows] what Q's rows were divided by
   float* const other = row_scale + C::kRows;                                       // [3][128] group 1's ml, mo, l (split)
-  volatile float* const info = reinterpret_cast<volatile float*>(other + (kGroups == 2 ? 3 * 128 : 0));   // [kInfo][8]: per half K scale, log2 of V's, there
+  volatile float* const info = reinterpret_cast<volatile float*>(other + (kGroups == 2 ? 3 * 128 : 0));   // [kInfo][8]: per half K scale times scale_digits, log2 of V's, there
   volatile int* const items = reinterpret_cast<volatile int*>(gbase + C::kOffStat + C::kStat - kItems * kItemInts * 4);
   const uint32_t bars = base + C::kOffStat + C::kStat;
   uint8_t* const gbars = gbase + (bars - base);
@@ -503,7 +503,7 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       par ^= 8u;
-      const float sl2 = p.scale_log2 * row_scale[(split ? 0 : g * 128) + row];
+      const float rs = p.scale_power * row_scale[(split ? 0 : g * 128) + row];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_q_empty);
       bool rescale = false;                                // O holds something
@@ -519,7 +519,7 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         const volatile float* const sc = info + (at % kInfo) * 8;
         // (at least the smallest normal number: a K scale of 0 makes 0 of every logit, but would make NaN of the -inf of
         // keys that are not there)
-        const float ka = fmaxf(sc[0] * sl2, 1.17549435e-38f), kb = fmaxf(sc[4] * sl2, 1.17549435e-38f);
+        const float ka = fmaxf(sc[0] * rs, 1.17549435e-38f), kb = fmaxf(sc[4] * rs, 1.17549435e-38f);
         const float lva = sc[1], lvb = sc[5];
         const bool here_a = sc[2] != 0.f, here_b = sc[6] != 0.f;
         const uint32_t t_s = tbase + lane_off + C::col_s(buf);
@@ -915,9 +915,11 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
             const uint32_t second = __reduce_max_sync(0xffffffffu, sub == 1 ? m : 0u);
             if (sub == 1) amax = second;
           }
-          // exponent that brings the largest to [128, 256); bounded so that both powers are normal.
+          // exponent that brings the largest to [128, 256); at least -126, so that both powers are normal: what is below 2^-119
+          // comes to less than 128, down to 2^-7, and keeps all its bits (bf16's smallest is 2^-133). 120 is a finite row's largest
+          // (without the min seven prompts' pieces take 326 us instead of 318: the code behind it lies otherwise).
           // A row with an infinity or NaN becomes NaN, as its logits are.
-          const int e2 = amax > 0 ? max(-100, min(100, static_cast<int>(amax >> 7) - 127 - 7)) : 0;
+          const int e2 = amax > 0 ? max(-126, min(120, static_cast<int>(amax >> 7) - 127 - 7)) : 0;
           const float down = amax < 0x7F80u ? __uint_as_float(static_cast<uint32_t>(127 - e2) << 23) : NAN;
           if (piece_q == 0) row_scale[group * 128 + row0 + e * kAtOnce] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
           hi[e][0] = hi[e][1] = lo[e][0] = lo[e][1] = 0;
@@ -1121,7 +1123,7 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           // product of the tile before it, or two before it: the softmax of that one and of all before is done.
           if (lane == i || lane == i + 1) {
             volatile float* const dst = info + (tile % kInfo) * 8 + (lane - i) * 4;
-            dst[0] = ks_now;
+            dst[0] = ks_now * p.scale_digits;
             dst[1] = log2f(vs_now);
             dst[2] = z_now >= 0 ? 1.f : 0.f;
           }

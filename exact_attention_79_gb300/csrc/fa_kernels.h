@@ -213,7 +213,9 @@ struct ChunkParams {
   int G, tt;                       // query heads per KV head; tokens of a row tile, 128 / G
   int span;                        // tokens of an item (set at the launch)
   int causal, ctas;
-  float scale_log2;
+  // scale log2(e) as 1 to 2 and a power of two: K's scales are multiplied by the one and the rows' powers by the other, so that
+  // neither loses bits next to the smallest normal number
+  float scale_digits, scale_power;
   unsigned* status;                // device status word
   unsigned long long timeout_ns;   // bound on every wait inside the kernel
   int test_stall;                  // 1: the issuer first waits on a barrier nothing arrives on (timeout test)

@@ -1,0 +1,43 @@
+"""Attention over the 8-bit cache at the ends of what bf16 queries and the cache's scales can be, on the GPU against 64 bits.
+
+The bounds are those of test_cache8_chunk_gpu.check, which are relative to the row's own values.
+"""
+import numpy as np
+import pytest
+import torch
+
+from test_cache8_chunk_gpu import check, run
+from test_cache8_gpu import DEV, bf16, make
+
+pytestmark = pytest.mark.gpu
+
+# new tokens and cached ones before them, Hq, Hkv, d: an item of one row tile, whole and over many CTAs; of two row tiles; wide
+CASES = [
+    ([20], [200], 4, 2, 128),
+    ([300, 3], [70, 9000], 4, 2, 128),
+    ([130, 3], [100, 3000], 2, 2, 256),
+]
+
+
+def spread_rows(x, exponents):
+    """x, row after row (tokens; the dimension before the last) times 2 to one of the exponents, as bf16."""
+    e = torch.tensor([exponents[i % len(exponents)] for i in range(x.shape[-2])], dtype=torch.float64)
+    return (x.double() * torch.exp2(e)[:, None]).to(torch.bfloat16)
+
+
+# exponents of the rows' values and of K's scales: logits of up to some tens in the rows that count most
+ENDS = [(list(range(100, 126)), -126), (list(range(-117, -103)), 104), (list(range(-133, -113)), 115)]
+
+
+@pytest.mark.parametrize("rows,k_scale", ENDS)
+@pytest.mark.parametrize("news,past,Hq,Hkv,d", CASES)
+def test_queries_of_any_size(fa, news, past, Hq, Hkv, d, rows, k_scale):
+    """Rows of the largest finite values down to subnormal ones, against K scales that make moderate logits of them."""
+    lens = [a + b for a, b in zip(news, past)]
+    c, table = make(d + k_scale % 97, lens, Hkv, d)
+    c["k_scale"][:] = 2.0 ** k_scale
+    q = spread_rows(bf16(np.random.default_rng(7), Hq, sum(news), d), rows)
+    assert torch.isfinite(q).all()
+    q = q.to(DEV)
+    o, lse = run(fa, c, q, table, news, lens, scale=0.01)
+    check(c, q, table, news, lens, True, 0.01, o, lse, rows=30)
