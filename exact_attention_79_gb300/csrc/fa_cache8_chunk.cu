@@ -631,6 +631,7 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         continue;
       }
       float f0 = 1.f, f1 = kNoKey;                         // factors of this group's O and of the other's
+      float root = 1.f;                                    // of both: V's scale itself may be below the normal numbers
       if (l == 0.f) f0 = kNoKey;
       if (kGroups == 2 && split) {
         ok = wait(bar_other_full, par >> 2 & 1u, abort_flag, p.timeout_ns);
@@ -657,7 +658,8 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       const int slot_row = (split ? 0 : g * 128) + row;
       float* part = nullptr;
       if (whole) {
-        const float factor = l == 0.f ? 0.f : ex2_approx(mo - ml) / l;   // (0 where mo is not set)
+        root = l == 0.f ? 0.f : ex2_approx(0.5f * (mo - ml));   // (0 where mo is not set)
+        const float factor = l == 0.f ? 0.f : root / l;
         f0 = f0 == kNoKey ? kNoKey : f0 * factor;
         f1 = f1 == kNoKey ? kNoKey : f1 * factor;
         if (real) p.lse[static_cast<long long>(head) * p.T + at_row] = l == 0.f ? -INFINITY : (ml + log2f(l)) * kLn2;
@@ -688,6 +690,8 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #pragma unroll
           for (int i = 0; i < 32; ++i) y[i] += times_factor(__uint_as_float(o1[i]), f1);
         }
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) mul2_b(y[i], y[i + 1], y[i], y[i + 1], root);
         if (!real) continue;
         if (whole) {
 #pragma unroll
@@ -1213,7 +1217,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache8_chunk_join_kernel(const C
   }
   const int head = parts.w * p.G + ((r & 127) - tok * p.G);
   const long long at_row = static_cast<long long>(at.x) + token;
-  const float factor = l == 0.f ? 0.f : ex2_approx(mo - ml) / l;
+  const float root = l == 0.f ? 0.f : ex2_approx(0.5f * (mo - ml)), factor = l == 0.f ? 0.f : root / l;   // (V's scale itself may be below the normal numbers)
   if (threadIdx.x < 32) p.lse[static_cast<long long>(head) * p.T + at_row] = l == 0.f ? -INFINITY : (ml + log2f(l)) * kLn2;
   __nv_bfloat16* const dst = p.o + head * p.o_sh + at_row * p.o_st;
 #pragma unroll
@@ -1221,8 +1225,8 @@ __global__ void __launch_bounds__(kJoinThreads) cache8_chunk_join_kernel(const C
     const int col = 8 * ((threadIdx.x >> 5) + x * (kJoinThreads / 32));
     if (col < p.c.d)
       *reinterpret_cast<uint4*>(dst + col) =
-          make_uint4(pack_bf16x2(a[x][0].x * factor, a[x][0].y * factor), pack_bf16x2(a[x][0].z * factor, a[x][0].w * factor),
-                     pack_bf16x2(a[x][1].x * factor, a[x][1].y * factor), pack_bf16x2(a[x][1].z * factor, a[x][1].w * factor));
+          make_uint4(pack_bf16x2(a[x][0].x * factor * root, a[x][0].y * factor * root), pack_bf16x2(a[x][0].z * factor * root, a[x][0].w * factor * root),
+                     pack_bf16x2(a[x][1].x * factor * root, a[x][1].y * factor * root), pack_bf16x2(a[x][1].z * factor * root, a[x][1].w * factor * root));
   }
 }
 

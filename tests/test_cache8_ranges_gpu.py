@@ -1,6 +1,9 @@
 """Attention over the 8-bit cache at the ends of what bf16 queries and the cache's scales can be, on the GPU against 64 bits.
 
-The bounds are those of test_cache8_chunk_gpu.check, which are relative to the row's own values.
+The bounds are those of test_cache8_chunk_gpu.check, which are relative to the row's own values but for 1e-30. O is linear in
+V's scales, so results near that are compared times a power of two, taken in 64 bits: V's scales and O both, which changes no
+relative bound. A bf16 below 2^-126 is off by at most 2^-134; with V scales of 2^-126 the bound is 2^-11 sum p |code| 2^-126,
+which is more as soon as the mean magnitude of the codes is 2^3, and here it is about 38.
 """
 import numpy as np
 import pytest
@@ -41,3 +44,24 @@ def test_queries_of_any_size(fa, news, past, Hq, Hkv, d, rows, k_scale):
     q = q.to(DEV)
     o, lse = run(fa, c, q, table, news, lens, scale=0.01)
     check(c, q, table, news, lens, True, 0.01, o, lse, rows=30)
+
+
+def scaled(c, o, power):
+    """The cache with V's scales, and O, times 2^power, in 64 bits."""
+    return dict(c, v_scale=c["v_scale"].astype(np.float64) * 2.0 ** power), o.double() * 2.0 ** power
+
+
+V_ENDS = [(-126, -117, 100), (-126, -60, 80), (108, 117, -100)]
+
+
+@pytest.mark.parametrize("low,high,power", V_ENDS)
+@pytest.mark.parametrize("news,past,Hq,Hkv,d", CASES)
+def test_values_of_any_size(fa, news, past, Hq, Hkv, d, low, high, power):
+    lens = [a + b for a, b in zip(news, past)]
+    c, table = make(d + low % 97, lens, Hkv, d)
+    rng = np.random.default_rng(3)
+    c["v_scale"] = np.exp2(rng.integers(low, high + 1, c["v_scale"].shape)).astype(np.float32)
+    q = bf16(np.random.default_rng(8), Hq, sum(news), d).to(DEV)
+    o, lse = run(fa, c, q, table, news, lens)
+    c, o = scaled(c, o, power)
+    check(c, q, table, news, lens, True, d ** -0.5, o, lse, rows=30)
