@@ -709,6 +709,12 @@ ChunkWorkspace chunk_workspace(int d, int max_blocks) {
   const size_t off_s = align256(rows * D * 4), off_j = off_s + align256(rows * 3 * 4);
   return {off_s, off_j, off_j + align256(fa::kCache8Sms * 8 * 4)};
 }
+// scale log2(e) = digits power, digits from 1 to 2.
+void split_scale(float scale, float* digits, float* power) {
+  int e = 0;
+  *digits = 2.f * std::frexp(scale * 1.4426950408889634f, &e);
+  *power = std::ldexp(1.f, e - 1);
+}
 fa_status chunk_sizes(int B, int T, int Hq, int Hkv, int d, int max_blocks) {
   if (B < 1 || B > 65535 || T < 1 || Hq < 1 || Hkv < 1 || Hkv > 65535 || Hq % Hkv != 0 || d < 1 || max_blocks < 1 ||
       max_blocks > (1 << 24))
@@ -860,7 +866,7 @@ fa_status fa_fwd_cache8(const void* q, const fa_cache8* cache, const int* block_
   p.Nq = Nq;
   p.causal = causal ? 1 : 0;
   p.add_weights = add_weights ? 1 : 0;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  split_scale(scale, &p.scale_digits, &p.scale_power);
   p.decay = weight_decay;
   p.part_o = static_cast<float*>(workspace);
   p.part_s = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.off_s);
@@ -920,9 +926,7 @@ fa_status fa_fwd_cache8_packed(const void* q, long long q_stride_h, long long q_
   p.tt = 128 / p.G;
   p.causal = causal ? 1 : 0;
   p.ctas = num_sms < fa::kCache8Sms ? num_sms : fa::kCache8Sms;
-  int power = 0;
-  p.scale_digits = 2.f * std::frexp(scale * 1.4426950408889634f, &power);
-  p.scale_power = std::ldexp(1.f, power - 1);
+  split_scale(scale, &p.scale_digits, &p.scale_power);
   p.status = status;
   p.timeout_ns = wait_limit_ns();
   p.test_stall = test_stall();

@@ -299,7 +299,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   float* const change_o = change_l + R;
   float* const warp_l = change_o + R;                                  // [4][R] maxima of the warps (ml, mo); sums
   float* const warp_o = warp_l + 4 * R;
-  float* const q_scale = warp_o + 4 * R;                               // [2][R] power of two the row was divided by
+  float* const q_scale = warp_o + 4 * R;                               // [2][R] power of two the row was divided by, times scale_power
   volatile float* const info = reinterpret_cast<volatile float*>(q_scale + 2 * R);   // [kInfo][8]: per half K scale, V scale, there
   const uint32_t bars = base + kOffStat + C::kStatFloats * 4 + kInfo * 32;
   uint8_t* const gbars = gbase + (bars - base);
@@ -495,11 +495,12 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
         for (int e = 0; e < C::kE; ++e) {
           const int q = q0 + e;
-          // exponent that brings the largest to [128, 256); bounded so that both powers are normal.
-          // An infinity among them becomes NaN, as its logits are.
-          const int e2 = amax[e] > 0.f ? max(-100, min(100, static_cast<int>(__float_as_uint(amax[e]) >> 23) - 127 - 7)) : 0;
+          // exponent that brings the largest to [128, 256), 120 at most for a finite one; at least -126, so that both powers
+          // are normal: what is below 2^-119 comes to less than 128, down to 2^-7, and keeps all its bits (bf16's smallest is
+          // 2^-133). An infinity among them becomes NaN, as its logits are.
+          const int e2 = amax[e] > 0.f ? max(-126, min(120, static_cast<int>(__float_as_uint(amax[e]) >> 23) - 127 - 7)) : 0;
           const float down = amax[e] < INFINITY ? __uint_as_float(static_cast<uint32_t>(127 - e2) << 23) : NAN;
-          if (lane == 0) q_scale[buf * R + q] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+          if (lane == 0) q_scale[buf * R + q] = p.scale_power * __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
 #pragma unroll
           for (int ch = 0; ch < C::kChunks; ++ch) {
             const uint32_t w[2] = {v[e][ch].x, v[e][ch].y};
@@ -567,7 +568,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
           for (int q = 0; q < R; ++q) sq[kKeep ? q : 0] = qs[q];
         }
-        const float ks = info[(tile % kInfo) * 8 + half * 4] * p.scale_log2;
+        const float ks = info[(tile % kInfo) * 8 + half * 4] * p.scale_digits;
         const float vs = info[(tile % kInfo) * 8 + half * 4 + 1];
         const int blk = s.blk0 + 2 * j + half;
         const int key = blk * kCacheBlock + (row & 63);

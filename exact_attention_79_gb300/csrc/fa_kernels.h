@@ -190,7 +190,10 @@ struct Cache8Params {
   int chunks;                      // row chunks of cache8_columns() rows
   int whole;                       // 1: one row group per CTA, nothing to join (set at the launch)
   int causal, add_weights;
-  float scale_log2, decay;
+  // scale log2(e) as 1 to 2 and a power of two: K's scales are multiplied by the one and the rows' powers by the other, so that
+  // neither loses bits next to the smallest normal number
+  float scale_digits, scale_power;
+  float decay;
   unsigned* status;                // device status word
   unsigned long long timeout_ns;   // bound on every wait inside the kernel
   int test_stall;                  // 1: the issuer first waits on a barrier nothing arrives on (timeout test)
@@ -213,9 +216,7 @@ struct ChunkParams {
   int G, tt;                       // query heads per KV head; tokens of a row tile, 128 / G
   int span;                        // tokens of an item (set at the launch)
   int causal, ctas;
-  // scale log2(e) as 1 to 2 and a power of two: K's scales are multiplied by the one and the rows' powers by the other, so that
-  // neither loses bits next to the smallest normal number
-  float scale_digits, scale_power;
+  float scale_digits, scale_power; // as Cache8Params
   unsigned* status;                // device status word
   unsigned long long timeout_ns;   // bound on every wait inside the kernel
   int test_stall;                  // 1: the issuer first waits on a barrier nothing arrives on (timeout test)

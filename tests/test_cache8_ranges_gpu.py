@@ -1,16 +1,16 @@
 """Attention over the 8-bit cache at the ends of what bf16 queries and the cache's scales can be, on the GPU against 64 bits.
 
-The bounds are those of test_cache8_chunk_gpu.check, which are relative to the row's own values but for 1e-30. O is linear in
-V's scales, so results near that are compared times a power of two, taken in 64 bits: V's scales and O both, which changes no
-relative bound. A bf16 below 2^-126 is off by at most 2^-134; with V scales of 2^-126 the bound is 2^-11 sum p |code| 2^-126,
-which is more as soon as the mean magnitude of the codes is 2^3, and here it is about 38.
+The bounds are those of test_cache8_chunk_gpu.check and test_cache8_gpu.check_attention, which are relative to the row's own
+values but for 1e-30. O is linear in V's scales, so results near that are compared times a power of two, taken in 64 bits:
+V's scales and O both, which changes no relative bound. A bf16 below 2^-126 is off by at most 2^-134; with V scales of 2^-126
+the bound is 2^-11 sum p |code| 2^-126, which is more as soon as the mean magnitude of the codes is 2^3, and here it is about 38.
 """
 import numpy as np
 import pytest
 import torch
 
 from test_cache8_chunk_gpu import check, run
-from test_cache8_gpu import DEV, bf16, make
+from test_cache8_gpu import DEV, bf16, check_attention, ints, make, to_gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +65,21 @@ def test_values_of_any_size(fa, news, past, Hq, Hkv, d, low, high, power):
     o, lse = run(fa, c, q, table, news, lens)
     c, o = scaled(c, o, power)
     check(c, q, table, news, lens, True, d ** -0.5, o, lse, rows=30)
+
+
+# lengths, Hq, Hkv, Nq, d of the single tokens' call: row groups that stay whole, that are split and joined, wide heads
+SINGLE = [([300, 40], 8, 2, 1, 128), ([9000], 16, 2, 2, 64), ([5000, 700], 4, 4, 4, 256)]
+
+
+@pytest.mark.parametrize("rows,k_scale", ENDS)
+@pytest.mark.parametrize("lens,Hq,Hkv,Nq,d", SINGLE)
+def test_single_tokens_queries_of_any_size(fa, lens, Hq, Hkv, Nq, d, rows, k_scale):
+    c, table = make(d + k_scale % 97, lens, Hkv, d)
+    c["k_scale"][:] = 2.0 ** k_scale
+    x = bf16(np.random.default_rng(7), len(lens) * Hq * Nq, d)
+    q = spread_rows(x, rows).view(len(lens), Hq, Nq, d)
+    assert torch.isfinite(q).all()
+    q = q.to(DEV)
+    o, lse = fa.fwd_cache8(q, to_gpu(fa, c), ints(table), ints(lens), scale=0.01)
+    fa.check_device_status()
+    check_attention(c, q, table, lens, True, 0.01, o, lse, None)
