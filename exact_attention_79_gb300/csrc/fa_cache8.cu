@@ -78,6 +78,11 @@ __device__ __forceinline__ void store_byte(uint32_t addr, uint32_t x) {
 // O of a row that sees no key is 0 whatever V holds: its P is 0, but 0 x NaN is not. (By a mark of its own: the
 // factor of V scales of 0 is 0 as well.)
 __device__ __forceinline__ float times_factor(float o, float factor) { return factor == kNoKey ? 0.f : o * factor; }
+// 2^x / sum in two factors, the second a power of two: with V's scales next to the smallest normal number it is below it itself.
+__device__ __forceinline__ float2 two_factors(float x, float sum) {
+  const bool low = x < -64.f;
+  return make_float2(ex2_approx(low ? x + 64.f : x) / sum, low ? 5.421010862427522e-20f : 1.f);   // 2^-64
+}
 // Bounded wait whose limit starts at its own first look at the timer.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned long long limit_ns) {
   uint32_t polls = 0;
@@ -731,12 +736,15 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       const long long slot0 = (2LL * blockIdx.x + (u == u0 ? 0 : 1)) * R;
       const size_t qrow = (static_cast<size_t>(s.b) * p.Hq + static_cast<size_t>(s.h) * p.G) * p.Nq + row0;
       const int rows = min(R, p.R - row0);
-      float* const factor = change_l;                    // of O, per row
+      float* const factor = change_l;                    // of O, per row, and a second one
+      float* const second = change_o;
       if (row < R) {
         const float sum = warp_l[row] + warp_l[R + row] + warp_l[2 * R + row] + warp_l[3 * R + row];
         const float ml = ref_l[row], mo = ref_o[row] - kShift;
         if (whole) {
-          factor[row] = sum == 0.f ? kNoKey : ex2_approx(mo - ml) / sum;
+          const float2 f = two_factors(mo - ml, sum);
+          factor[row] = sum == 0.f ? kNoKey : f.x;
+          second[row] = f.y;
           if (row < rows) p.lse[qrow + row] = sum == 0.f ? -INFINITY : (ml + log2f(sum)) * kLn2;
         } else {
           float* const s3 = p.part_s + (slot0 + row) * 3;
@@ -776,7 +784,7 @@ cache8_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             if (col < p.c.d) {
 #pragma unroll
               for (int e = 0; e < C::kE; ++e)
-                if (q0 + e < rows) dst[e * p.c.d] = __float2bfloat16_rn(times_factor(v[e], factor[q0 + e]));
+                if (q0 + e < rows) dst[e * p.c.d] = __float2bfloat16_rn(times_factor(v[e], factor[q0 + e]) * second[q0 + e]);
             }
           } else {
             float* const dst = p.part_o + (slot0 + q0) * D + col;
@@ -940,13 +948,14 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 8) cache8_finish_kernel(con
       }
     }
     const size_t at = (static_cast<size_t>(b) * p.Hq + static_cast<size_t>(h) * p.G) * p.Nq + r;
-    const float f = sum == 0.f ? kNoKey : ex2_approx(mo - ml) / sum;
+    const float2 two = two_factors(mo - ml, sum);
+    const float f = sum == 0.f ? kNoKey : two.x;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (128 * i + 4 * lane < p.c.d)
         *reinterpret_cast<uint2*>(p.o + at * p.c.d + 128 * i + 4 * lane) =
-            make_uint2(pack_bf16x2(times_factor(a[i].x, f), times_factor(a[i].y, f)),
-                       pack_bf16x2(times_factor(a[i].z, f), times_factor(a[i].w, f)));
+            make_uint2(pack_bf16x2(times_factor(a[i].x, f) * two.y, times_factor(a[i].y, f) * two.y),
+                       pack_bf16x2(times_factor(a[i].z, f) * two.y, times_factor(a[i].w, f) * two.y));
     if (lane == 0) p.lse[at] = sum == 0.f ? -INFINITY : (ml + log2f(sum)) * kLn2;
     return;
   }

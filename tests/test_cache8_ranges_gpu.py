@@ -83,3 +83,16 @@ def test_single_tokens_queries_of_any_size(fa, lens, Hq, Hkv, Nq, d, rows, k_sca
     o, lse = fa.fwd_cache8(q, to_gpu(fa, c), ints(table), ints(lens), scale=0.01)
     fa.check_device_status()
     check_attention(c, q, table, lens, True, 0.01, o, lse, None)
+
+
+@pytest.mark.parametrize("low,high,power", V_ENDS)
+@pytest.mark.parametrize("lens,Hq,Hkv,Nq,d", SINGLE)
+def test_single_tokens_values_of_any_size(fa, lens, Hq, Hkv, Nq, d, low, high, power):
+    c, table = make(d + low % 97, lens, Hkv, d)
+    rng = np.random.default_rng(3)
+    c["v_scale"] = np.exp2(rng.integers(low, high + 1, c["v_scale"].shape)).astype(np.float32)
+    q = bf16(np.random.default_rng(8), len(lens), Hq, Nq, d).to(DEV)
+    o, lse = fa.fwd_cache8(q, to_gpu(fa, c), ints(table), ints(lens))
+    fa.check_device_status()
+    c, o = scaled(c, o, power)
+    check_attention(c, q, table, lens, True, d ** -0.5, o, lse, None)
