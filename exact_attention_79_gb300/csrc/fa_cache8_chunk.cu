@@ -8,9 +8,11 @@
 // K and V.
 //
 // Products, per tile of 128 keys (two cache blocks), on the tensor cores:
-//   S [128 x 128 keys] = Q K^T   e4m3 (kind::f8f6f4): K's codes as they are, Q in two e4m3 terms
-//      q = q0 + q1 of the row scaled by a power of two to [128, 256): exact down to 2^-9 of the row's largest value,
-//      2^-17 of it below that. Two terms at the e4m3 rate cost what one bf16 product does.
+//   S [128 x 128 keys] = Q K^T   8-bit (kind::f8f6f4): K's codes as they are, Q in two terms, e4m3 and e5m2,
+//      q = q0 + q1 of the row scaled by a power of two to [128, 256). From 2^-6 on q0 has four of bf16's eight
+//      significant bits, and what it leaves is at most eight units of the last, which three bits hold (e5m2, down to
+//      2^-16): exact down to 2^-13 of the row's largest value. Below that 2^-10 at most is left, off by 2^-14: 2^-21 of the
+//      row's largest. Two terms at the 8-bit rate cost what one bf16 product does.
 //   O [128 x d] += P V           f16 (kind::f16): V's codes as halves (exact), P in f16.
 // A block's K scale multiplies its logits, its V scale its P, by a factor that keeps them within f16:
 // hence two references per row, ml for the sum of probabilities and mo for O, P' = 2^(x - ml) 2^(ml - mo) vs <= 2^15, each
@@ -290,9 +292,9 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t x) {
+__device__ __forceinline__ uint32_t f16x2_to_e5m2x2(uint32_t x) {
   uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
   return r;
 }
 __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
@@ -714,6 +716,7 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     setmaxnreg_dec<C::kRegsOther>();
     if (lane == 0) {
       const uint32_t id_s = make_idesc(0, 128, 128, 0, 0);             // e4m3, both K-major
+      const uint32_t id_s1 = id_s | 1u << 7;                           // A e5m2: Q's second term
       const uint32_t id_o = make_idesc(0, 128, p.c.d, 0, 1);           // f16, V MN-major
       // The issuing thread paces the kernel: a product takes 64 cycles, and every other instruction of this one thread
       // about eight. So a step's products stand in a row with constant offsets, the steps between a segment's first and
@@ -734,7 +737,7 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #pragma unroll
         for (int i = 0; i < 2 * n; ++i) {
           const int term = i / n, k = i % n, off = (k >> 2) * 16384 + (k & 3) * 32;
-          mma_fp8_ss(dst, desc_of(qd + ((term * C::kQTerm + off) >> 4)), desc_of(kd + (off >> 4)), id_s, i > 0);
+          mma_fp8_ss(dst, desc_of(qd + ((term * C::kQTerm + off) >> 4)), desc_of(kd + (off >> 4)), term ? id_s1 : id_s, i > 0);
         }
         mma_commit(bar_s_full(buf));
       };
@@ -929,11 +932,11 @@ cache8_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           hi[e][0] = hi[e][1] = lo[e][0] = lo[e][1] = 0;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            // (eight significant bits and at most 256: f16 holds what the two terms can)
+            // (eight significant bits and at most 256: f16, down to 2^-24, holds what the two terms can)
             const float x0 = __uint_as_float(w[e][k] << 16) * down, x1 = __uint_as_float(w[e][k] & 0xFFFF0000u) * down;
             const uint32_t c0 = pack_e4m3x2(x0, x1);
             hi[e][k >> 1] |= c0 << (16 * (k & 1));
-            lo[e][k >> 1] |= f16x2_to_e4m3x2(sub_f16x2(pack_f16x2(x0, x1), e4m3x2_to_f16x2(c0))) << (16 * (k & 1));
+            lo[e][k >> 1] |= f16x2_to_e5m2x2(sub_f16x2(pack_f16x2(x0, x1), e4m3x2_to_f16x2(c0))) << (16 * (k & 1));
           }
         }
         __syncwarp();                                      // all have read the rows

@@ -451,8 +451,8 @@ fa_status fa_fwd_cache8(const void* q, const fa_cache8* cache, const int* block_
  * causal, j <= i + lengths[b] - n; a row that sees none gets O = 0, lse = -inf. lse
  * fp32 [Hq, T]. Rows of no sequence are left as they were, in o and in lse; a sequence
  * may have no new tokens. Hq / Hkv <= 128 and T <= 2^30 (FA_ERR_UNSUPPORTED above). K's
- * codes enter the products as they are; Q to the bit down to 2^-9 of a row's largest
- * value (smaller ones are off by at most 2^-17 of it); each P (times its block's V scale)
+ * codes enter the products as they are; Q to the bit down to 2^-13 of a row's largest
+ * value (smaller ones are off by at most 2^-21 of it); each P (times its block's V scale)
  * within 2^-11 of itself plus 2^-31 of the row's largest; probabilities below
  * 2^-126 of the largest count as 0; sums are fp32. A NaN among the V
  * values of a tile of 128 keys that a row tile looks at reaches all its rows.

@@ -9,8 +9,9 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import cache8 as oc
 from test_cache8_chunk_gpu import check, run
-from test_cache8_gpu import DEV, bf16, check_attention, ints, make, to_gpu
+from test_cache8_gpu import DEV, bf16, check_attention, f64, ints, make, to_gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +97,35 @@ def test_single_tokens_values_of_any_size(fa, lens, Hq, Hkv, Nq, d, low, high, p
     fa.check_device_status()
     c, o = scaled(c, o, power)
     check_attention(c, q, table, lens, True, d ** -0.5, o, lse, None)
+
+
+@pytest.mark.parametrize("d", [64, 256])
+def test_small_columns_beside_a_large_one(fa, d):
+    """A row's columns of 2^-6 to 2^-13 of its largest count to the bit, smaller ones to 2^-21 of it. K is 0 where Q is large, so
+    that the logits are the small columns' alone: off by (2 d + 8) 2^-23 of sum |q k| over those (two terms of d products
+    added in fp32) and by 2^-21 of the row's largest times sum |k| over the ones below 2^-13. (A second
+    term that is off by 2^-17 of the largest in each column, as in e4m3, fails at d 64.)"""
+    n, scale = 7, d ** -0.5
+    c, table = make(d, [n], 1, d)
+    c["k"][table[0, 0], :, :n, 0] = 0
+    e = np.concatenate([[0], -(6.0 + 12.0 * np.arange(d - 1) / d)])
+    rng = np.random.default_rng(5)
+    for low in (-13, -18):
+        x = np.exp2(np.maximum(e, low)) * rng.uniform(1, 2, (2, n, d)) * rng.choice([-1, 1], (2, n, d))
+        x[..., 0] = 1.5
+        q = torch.from_numpy(x * 1024).to(torch.bfloat16).to(DEV)
+        o, lse = run(fa, c, q, table, [n], [n], causal=False, scale=scale)
+        K, V, _ = oc.gather(c, table[0], 0, n)
+        qd = f64(q)
+        for j in range(2):
+            for r in range(n):
+                y, top = qd[j, r], np.abs(qd[j, r]).max()
+                s = scale * (K @ y)
+                rl = s.max() + np.log(np.exp(s - s.max()).sum())
+                p = np.exp(s - rl)
+                ds = (2 * d + 8) * 2.0 ** -23 * scale * (np.abs(K) @ np.abs(y)).max() + \
+                    2.0 ** -21 * top * scale * np.abs(K)[:, np.abs(y) < 2.0 ** -13 * top].sum(1).max()
+                assert abs(f64(lse)[j, r] - rl) <= ds + 2.0 ** -20 + n * 2.0 ** -23 + abs(rl) * 2.0 ** -22
+                rel = 2.0 ** -11 + 2.0 ** -20 + 2 * ds + 2 * n * 2.0 ** -23
+                tol = 2.0 ** -8 * np.abs(p @ V) + rel * (p @ np.abs(V)) + 2.0 ** -31 * np.abs(V).max(0)
+                assert (np.abs(f64(o)[j, r] - p @ V) <= tol).all()
