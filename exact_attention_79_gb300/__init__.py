@@ -398,8 +398,8 @@ def rope(q, k, rope, positions, inverse=False, q_out=None, k_out=None):
     q: [B, Hq, T, d] or [Hq, T, d], bf16 or fp32, any strides that are multiples of 16 bytes (a projection's
     [B, T, H, d].transpose(1, 2) too); k: the same with its own heads, or None. positions: int32, [axes, B, T] (3-D q:
     [axes, T]); the batch may be left out where all share them, and the axes where the Rope names none. q_out, k_out: where
-    the results go, in any such layout (q and k themselves too); otherwise tensors laid out like q and k. Returns (q_out,
-    k_out), k_out None without k."""
+    the results go, in any such layout (q_out may be q itself and k_out k itself, and they are otherwise apart from both);
+    without them tensors laid out like q and k. Returns (q_out, k_out), k_out None without k."""
     import torch
     shape, dtype, dev = q.shape, q.dtype, q.device
     batched = len(shape) == 4

@@ -816,6 +816,17 @@ fa_status fa_rope(const void* q, long long q_stride_b, long long q_stride_h, lon
     if ((B > 1 && x.out_sb < d) || (x.H > 1 && x.out_sh < d) || (T > 1 && x.out_st < d)) return FA_ERR_INVALID_ARG;
   }
   if (static_cast<long long>(B) * T >= (1LL << 31) || static_cast<long long>(Hq) + Hkv > 65535) return FA_ERR_UNSUPPORTED;
+  // An output where an input begins is that tensor's own, row for row: threads that read other rows than they write
+  // would race.
+  for (int i = 0; i < 2; ++i) {
+    const fa::RopeTensor& x = p.x[i];
+    if (x.H == 0) continue;
+    if (i == 1 && x.out == p.x[0].out) return FA_ERR_INVALID_ARG;
+    if (p.x[1 - i].H > 0 && x.out == p.x[1 - i].in) return FA_ERR_INVALID_ARG;
+    if (x.out == x.in &&
+        ((B > 1 && x.out_sb != x.in_sb) || (x.H > 1 && x.out_sh != x.in_sh) || (T > 1 && x.out_st != x.in_st)))
+      return FA_ERR_INVALID_ARG;
+  }
   unsigned* status = nullptr;
   const fa_status dev = device_state(stream, &status);
   if (dev != FA_OK) return dev;

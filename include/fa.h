@@ -337,8 +337,9 @@ typedef struct {
  * (elt_bytes 2) or fp32 (4); computed in fp32 and rounded once. Strides in
  * elements, multiples of 16 bytes, the d values of a row contiguous, inputs and
  * outputs each with their own: a [B, T, H, d] projection can go to the
- * [B, H, T, d] of fa_fwd. An output may be its input (same pointer and strides) and
- * otherwise lies apart from the inputs and the other output. positions: device int32,
+ * [B, H, T, d] of fa_fwd. An output may be its own input (same pointer and strides) and
+ * otherwise lies apart from the inputs and the other output (FA_ERR_INVALID_ARG where it begins
+ * at one of them, or at its input with other strides). positions: device int32,
  * positions[a * pos_stride_axis + b * pos_stride_b + t], pos_stride_b 0 where batches
  * share them. d a multiple of 8 from 8 to 256; pointers 16-byte aligned. */
 fa_status fa_rope(const void* q, long long q_stride_b, long long q_stride_h, long long q_stride_t, void* q_out,
