@@ -669,7 +669,8 @@ def fwd_cache8_packed(q, cache, cu_seqlens, block_table, lengths, causal=True, s
     q: bf16 [Hq, T, d] or a [T, Hq, d] tensor's .transpose(0, 1), the chunks one behind the other; sequence b's are rows
     cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32 [B + 1]) and the last of its lengths[b] tokens (int32 [B]). Returns (o with
     q's layout, lse fp32 [Hq, T]); rows of no sequence are left as they were (unset in new tensors). workspace: uint8, of
-    fa_fwd_cache8_packed_workspace_bytes (about 40 MB); made by the call otherwise."""
+    fa_fwd_cache8_packed_workspace_bytes (about 40 MB); made by the call otherwise. Adds no attention weights: cache8_evict
+    ranks tokens that only this call has looked at as equals."""
     import torch
     lib = load()
     if q.dim() != 3:

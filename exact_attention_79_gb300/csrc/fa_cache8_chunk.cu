@@ -24,9 +24,11 @@
 // clear keys that are not there (P is 0, but 0 x NaN is not) and also lay out Q.
 //
 // The work is a line of units, one per (item, key tile), cut into equal parts for a
-// persistent grid of one CTA per SM, whatever the lengths; an item whose units fall to several
-// CTAs is joined from partial results by a second kernel. An item of no more than one row tile
-// gives its even key tiles to one softmax group and its odd ones to the other, joined in TMEM.
+// persistent grid of one CTA per SM, whatever the lengths (a unit is a unit, of one row tile or of two: by a model of
+// the line the longest part is 16% above the mean for a piece beside single tokens, 8% for several prompts' pieces,
+// nothing for one prompt); an item whose units fall to several CTAs is joined from partial results by a second
+// kernel. An item of no more than one row tile gives its even key tiles to one softmax group and its odd ones to
+// the other, joined in TMEM.
 //
 // Warps: 0-3 and 4-7 the softmax groups (one thread per row), 8 producer (block table, scales,
 // TMA), 9 tensor-core issuer, 10 ring watcher, 11 scheduler, 12-15 converters. At d > 128 (kGroups = 1) O takes half of
@@ -34,9 +36,9 @@
 // code, more than the instruction cache holds: each line that has gone costs some 230 cycles, and the order of
 // the roles below is the best of ten (4096 tokens at the end of 32768, 32 heads on 8, d 128: 1434 to 1812 us).
 //
-// What bounds it. There (1.44 PFLOP/s, 75% of the bf16 rate) a step of two row tiles takes 3300 cycles, 2100 of them products:
-// each group's S, softmax (1600), P V and the hand-offs between follow one another, and two groups do not cover it all. At
-// d 64 a step takes 2900. A change of items costs some 15000 (Q's terms, the diagonal's mask, O's way out).
+// What bounds it. There (1463 to 1526 us from one GPU to the next, 1.35 to 1.41 PFLOP/s, 70 to 73% of the bf16
+// rate) a step of two row tiles takes 3300 cycles, 2100 of them products: each group's S, softmax (1600), P V and the
+// hand-offs between follow one another, and two groups do not cover it all. At d 64 a step takes 2900. A change of items costs some 15000 (Q's terms, the diagonal's mask, O's way out).
 #include <type_traits>
 
 #include "fa_cache8.cuh"
@@ -51,7 +53,10 @@ constexpr float kNoKey = -1.f;            // factor of O for a row that sees no 
 constexpr int kInfo = 8;                  // tiles whose scales wait in shared memory
 constexpr int kItems = 4;                 // segments that the scheduler may be ahead
 constexpr int kItemInts = 12;
-constexpr int kTurn = 1;                  // key tiles' time that a change of items costs
+// Places that a change of items takes up on the line, so that parts of many items have fewer key tiles. (Not what it costs,
+// four to five key tiles' time: the line does not weigh items of one row tile less either, and both go together. With 1, 4 and
+// 9: 7 prompts' pieces 315, 308, 305 us; a piece and 24 single tokens 348, 345, 352; wide heads 280, 281, 286.)
+constexpr int kTurn = 1;
 
 template <int D>
 struct Cfg {
@@ -118,7 +123,7 @@ struct Sequence {
     return static_cast<int>(min(static_cast<long long>(n), (item + 1LL) * p.span));
   }
 };
-// sum over j < n of floor((a j + b) / m), by Euclid's steps on (a, m)
+// sum over j < n of floor((a j + b) / m), by the well-known steps of Euclid's algorithm on (a, m)
 __device__ __forceinline__ long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
   long long sum = 0;
   while (n > 0) {

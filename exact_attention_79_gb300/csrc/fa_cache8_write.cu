@@ -13,7 +13,7 @@
 //
 // With rotation K's pairs of columns are turned by their positions on the way, in fp32, and the block's scale is that of the
 // rotated values, so K is rounded once. The angles are the same for all heads of a token: a CTA computes them once for
-// several. K's kernel then has half of the issue slots busy (about 20 instructions per value) and 2.1 waves of CTAs.
+// several. K's kernel then has 60% of the issue slots busy (about 20 instructions per value) and 2.1 waves of CTAs.
 #include "fa_cache8.cuh"
 #include "fa_rope.cuh"
 

@@ -63,7 +63,7 @@ struct Vec {
   }
 };
 
-// kPairs: 0 columns i and i + pairs, 1 columns 2 i and 2 i + 1. threadIdx.x: unit of a row (rotated
+// kAdjacent: 0 pairs are columns i and i + pairs, 1 columns 2 i and 2 i + 1. threadIdx.x: unit of a row (rotated
 // vectors, or pairs of them, then the vectors behind them); threadIdx.y: row.
 template <typename T, int E, int kAdjacent>
 __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {

@@ -455,13 +455,16 @@ fa_status fa_fwd_cache8(const void* q, const fa_cache8* cache, const int* block_
  * codes enter the products as they are; Q to the bit down to 2^-13 of a row's largest
  * value (smaller ones are off by at most 2^-21 of it); each P (times its block's V scale)
  * within 2^-11 of itself plus 2^-31 of the row's largest; probabilities below
- * 2^-126 of the largest count as 0; sums are fp32. A NaN among the V
+ * 2^-111 of the largest may count for less in O, below 2^-126 for nothing; sums are fp32. A NaN among the V
  * values of a tile of 128 keys that a row tile looks at reaches all its rows.
  * workspace: fa_fwd_cache8_packed_workspace_bytes(B, T, Hq, Hkv, d, max_blocks)
  * bytes (40 MB; 256 says that a table of one or two blocks needs none, NULL will do), 256-byte aligned,
  * contents before and after of no meaning; calls that may overlap on the GPU need
  * one each. 0 for sizes that it refuses. Two launches (one where none is needed). Every call gives the same
- * bits. fa_fwd_cache8 is the call for single tokens, and the one that adds up weights. */
+ * bits. fa_fwd_cache8 is the call for single tokens, and the one that adds up weights: this one
+ * leaves cache->weight as it is, and tokens appended with weight 0 stay there until a
+ * fa_fwd_cache8 with add_weights has seen them. fa_cache8_evict before that ranks them as
+ * equals, the earlier ones first. */
 size_t fa_fwd_cache8_packed_workspace_bytes(int B, int T, int Hq, int Hkv, int d, int max_blocks);
 fa_status fa_fwd_cache8_packed(const void* q, long long q_stride_h, long long q_stride_t, const fa_cache8* cache,
                                const int* block_table, int max_blocks, const int* cu_seqlens, const int* lengths, void* o,
