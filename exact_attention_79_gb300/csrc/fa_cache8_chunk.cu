@@ -38,7 +38,8 @@
 //
 // What bounds it. There (1463 to 1526 us from one GPU to the next, 1.35 to 1.41 PFLOP/s, 70 to 73% of the bf16
 // rate) a step of two row tiles takes 3300 cycles, 2100 of them products: each group's S, softmax (1600), P V and the
-// hand-offs between follow one another, and two groups do not cover it all. At d 64 a step takes 2900. A change of items costs some 15000 (Q's terms, the diagonal's mask, O's way out).
+// hand-offs between follow one another, and two groups do not cover it all. At d 64 a step takes 2900. A change of
+// items costs some 15000 (Q's terms, the diagonal's mask, O's way out).
 #include <type_traits>
 
 #include "fa_cache8.cuh"
